@@ -570,6 +570,147 @@ KLA_API kla_status kla_chunk_bwd_noalloc(
     kla_stream_t stream);
 
 /*
+ * Layer norm over the last axis of a [rows, D] tensor, with an optional
+ * residual add in front:
+ *
+ *     s = x + residual            (s = x without a residual)
+ *     mean = sum(s) / D,  rstd = 1 / sqrt(sum((s - mean)^2) / D + eps)
+ *     y = (s - mean) * rstd * weight + bias
+ *
+ * kla_layernorm_fwd -- x, residual, sum [rows, D] and y [rows, D] of type
+ * `dtype`; weight, bias [D] of type `wdtype`; mean, rstd [rows] fp32.
+ * x_stride and residual_stride are the distances between rows in elements
+ * (each row's D elements are adjacent; any value >= 0, 0 repeats one row);
+ * y and sum are contiguous.  May be null: residual (then sum must be null
+ * too), weight (ones), bias (zeros), sum, mean, rstd.  Every row is held and
+ * reduced in fp32; y and the statistics come from the unrounded s, and sum is
+ * s rounded to `dtype`.  y and sum may not overlap any input, nor each other.
+ * rows = 0 launches nothing.
+ * Errors: KLA_ERR_INVALID_ARG (rows < 0, D < 1, eps negative or not finite,
+ * a negative stride, a null or misaligned pointer, overlapping buffers),
+ * KLA_ERR_CUDA.  Any D is supported.  No workspace.
+ */
+KLA_API kla_status kla_layernorm_fwd(
+    const void* x, long long x_stride, const void* residual,
+    long long residual_stride, const void* weight, const void* bias,
+    float eps, void* y, void* sum, float* mean, float* rstd, int rows, int D,
+    kla_dtype dtype, kla_dtype wdtype, kla_stream_t stream);
+
+/*
+ * kla_layernorm_bwd -- gradients of a loss, given y_grad = dL/dy and
+ * optionally sum_grad = dL/dsum (the gradient that reaches s past the norm,
+ * along the residual stream); x is the normalised tensor (the forward's
+ * `sum`, or its x without a residual), mean and rstd the forward's:
+ *
+ *     xh = (x - mean) rstd
+ *     c1 = sum(w y_grad xh) / D,  c2 = sum(w y_grad) / D
+ *     x_grad      = rstd (w y_grad - c2 - xh c1) + sum_grad    (per row)
+ *     weight_grad = sum over rows of y_grad xh
+ *     bias_grad   = sum over rows of y_grad
+ *
+ * x_grad [rows, D] (contiguous, of type `dtype`) is the gradient of x and of
+ * the residual alike; weight_grad, bias_grad [D] are of type `wdtype`, summed
+ * in fp32 in a fixed order (the same bits on every run on one GPU model) and
+ * rounded once.  May be null: weight (ones), sum_grad, weight_grad,
+ * bias_grad.  x_grad may not overlap any input (not sum_grad either).  With
+ * rows = 0 the weight and bias gradients are zeroed.
+ * workspace: kla_layernorm_bwd_workspace_size bytes, 16-byte aligned, fp32
+ * partial sums; not needed (may be null) when weight_grad and bias_grad are
+ * both null.
+ * Errors: as kla_layernorm_fwd; KLA_ERR_INVALID_ARG for a workspace that is
+ * missing, too small, misaligned or overlapping.
+ */
+KLA_API kla_status kla_layernorm_bwd_workspace_size(int rows, int D,
+                                                    kla_dtype dtype,
+                                                    size_t* bytes);
+KLA_API kla_status kla_layernorm_bwd(
+    const void* y_grad, long long y_grad_stride, const void* x,
+    long long x_stride, const void* weight, const float* mean,
+    const float* rstd, const void* sum_grad, long long sum_grad_stride,
+    void* x_grad, void* weight_grad, void* bias_grad, int rows, int D,
+    kla_dtype dtype, kla_dtype wdtype, void* workspace,
+    size_t workspace_bytes, kla_stream_t stream);
+
+/*
+ * Gated linear recurrence: an elementwise recurrence with one decay per token
+ * and channel, the diagonal sibling of the recurrence above.  Per sequence
+ * and channel, from h_0:
+ *
+ *     h_t = exp(log_alpha_t) h_{t-1} + x_t,     o_t = h_t
+ *
+ * kla_glr_fwd -- two forms:
+ *   cu_seqlens null: B sequences of T tokens.  x, log_alpha [B, T, D] with
+ *     strides (elements) *_sb between sequences and *_st between tokens (a
+ *     token's D elements are adjacent; strides >= 0, 0 repeats); o [B, T, D]
+ *     contiguous.
+ *   cu_seqlens given: B sequences packed back to back into T tokens in all.
+ *     cu_seqlens [B + 1] (device, int32, 0 = cu[0] <= ... <= cu[B] = T):
+ *     sequence n holds the tokens cu[n] .. cu[n+1] - 1 and may be empty.
+ *     x, log_alpha, o [T, D]; the *_sb are not looked at.  The offsets are
+ *     on the device and not checked; bad ones give wrong results, but no
+ *     access outside the tensors.
+ * x, o of type `dtype`, log_alpha of type `gate_dtype`; h0, hT [B, D] fp32.
+ * The state is held in fp32, rounded only on its way to o.  log_alpha is
+ * meant to be <= 0 (-inf forgets: h_t = x_t for finite h_{t-1}); positive
+ * values are computed as written.  h0 null: zeros; hT null: not written; hT
+ * may be h0 itself (else it may not overlap any input).  The hT of an empty
+ * sequence is its h0.
+ * workspace: kla_glr_workspace_size bytes, 16-byte aligned, the states handed
+ * from one block of tokens to the next; may be null when that size is 0.
+ * Every call initialises what it reads of it.
+ * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, D < 1, a null or
+ * misaligned pointer, overlapping buffers, a workspace that is missing or too
+ * small), KLA_ERR_CUDA.
+ */
+KLA_API kla_status kla_glr_workspace_size(int B, int T, int D, int packed,
+                                          kla_dtype dtype,
+                                          kla_dtype gate_dtype,
+                                          size_t* bytes);
+KLA_API kla_status kla_glr_fwd(
+    const void* x, long long x_sb, long long x_st, const void* log_alpha,
+    long long a_sb, long long a_st, const float* h0, void* o, float* hT,
+    const int* cu_seqlens, int B, int T, int D, kla_dtype dtype,
+    kla_dtype gate_dtype, void* workspace, size_t workspace_bytes,
+    kla_stream_t stream);
+
+/*
+ * kla_glr_bwd -- gradients given o_grad = dL/do and optionally hT_grad =
+ * dL/dhT (null: zeros), from the forward's o, log_alpha and h0:
+ *
+ *     g_t = o_grad_t + exp(log_alpha_{t+1}) g_{t+1}  (last token: + hT_grad)
+ *     x_grad_t = g_t
+ *     log_alpha_grad_t = exp(log_alpha_t) g_t h_{t-1}  (h from o and h0)
+ *     h0_grad = exp(log_alpha_1) g_1                   (empty: hT_grad)
+ *
+ * g is held in fp32.  h_{t-1} is the o that the forward rounded to `dtype`:
+ * with bf16 it carries that one rounding (at most 2^-8) into log_alpha_grad.
+ * Shapes, strides, packing and workspace as kla_glr_fwd; x_grad (`dtype`) and
+ * log_alpha_grad (`gate_dtype`) contiguous like o; h0_grad [B, D] fp32 or
+ * null.  The outputs may not overlap any input nor each other.
+ * Errors: as kla_glr_fwd.
+ */
+KLA_API kla_status kla_glr_bwd(
+    const void* o, long long o_sb, long long o_st, const void* log_alpha,
+    long long a_sb, long long a_st, const float* h0, const void* o_grad,
+    long long g_sb, long long g_st, const float* hT_grad, void* x_grad,
+    void* log_alpha_grad, float* h0_grad, const int* cu_seqlens, int B, int T,
+    int D, kla_dtype dtype, kla_dtype gate_dtype, void* workspace,
+    size_t workspace_bytes, kla_stream_t stream);
+
+/*
+ * kla_glr_step -- one token for N sequences: S [N, D] fp32 (contiguous) is
+ * updated in place, S = exp(log_alpha) S + x, and o [N, D] (contiguous) is
+ * the new S rounded to `dtype`.  x, log_alpha [N, D] with row strides in
+ * elements.  o may not overlap any other buffer, nor S an input.
+ * Errors: as kla_glr_fwd.
+ */
+KLA_API kla_status kla_glr_step(const void* x, long long x_stride,
+                                const void* log_alpha, long long a_stride,
+                                float* S, void* o, int N, int D,
+                                kla_dtype dtype, kla_dtype gate_dtype,
+                                kla_stream_t stream);
+
+/*
  * kla_device_status -- synchronises `stream`, then reads and clears the
  * library's device-side fault word.  Returns KLA_ERR_TIMEOUT if a bounded
  * wait inside a kernel gave up since the last call (the kernel then skipped

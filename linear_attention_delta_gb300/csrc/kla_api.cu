@@ -4,47 +4,15 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.cuh"
 #include "kla_internal.cuh"
+
+using namespace kla::api;
 
 namespace {
 
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-
-bool aligned(const void* p, size_t n) {
-    return (reinterpret_cast<uintptr_t>(p) % n) == 0;
-}
-
-kla_status from_cuda(cudaError_t e) {
-    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
-}
-
-// A buffer of the call: start and length in bytes (null or empty: none).
-struct Span {
-    const void* p;
-    size_t n;
-};
-
-// True when the byte ranges of a and b share at least one byte.
-bool overlap(Span a, Span b) {
-    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p);
-    const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-// True when any written span overlaps any read span, or two written spans
-// overlap each other.
-template <size_t NI, size_t NO>
-bool any_overlap(const Span (&ins)[NI], const Span (&outs)[NO]) {
-    for (size_t i = 0; i < NO; ++i) {
-        for (size_t j = 0; j < NI; ++j)
-            if (overlap(outs[i], ins[j])) return true;
-        for (size_t j = i + 1; j < NO; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-    }
-    return false;
-}
 
 }  // namespace
 

@@ -111,6 +111,59 @@ struct DecodeArgs {
     const void* kw = nullptr;   // separate write keys [N, H, dk] or null
 };
 
+struct LayerNormArgs {
+    const void* x;
+    long long x_stride;          // elements between rows
+    const void* residual;        // may be null
+    long long residual_stride;
+    const void* weight;          // may be null (ones)
+    const void* bias;            // may be null (zeros)
+    float eps;
+    void* y;                     // [rows, D] contiguous
+    void* sum;                   // may be null
+    float* mean;                 // may be null
+    float* rstd;                 // may be null
+    int rows, D;
+    kla_dtype dtype, wdtype;
+};
+
+struct LayerNormBwdArgs {
+    const void* dy;
+    long long dy_stride;
+    const void* x;
+    long long x_stride;
+    const void* weight;          // may be null (ones)
+    const float* mean;
+    const float* rstd;
+    const void* dsum;            // may be null
+    long long dsum_stride;
+    void* dx;                    // [rows, D] contiguous
+    void* dw;                    // [D], may be null
+    void* db;                    // [D], may be null
+    int rows, D;
+    kla_dtype dtype, wdtype;
+};
+
+// A [B, T, D] tensor read through strides (elements).
+struct Strided {
+    const void* p;
+    long long sb, st;
+};
+
+struct GlrArgs {
+    Strided x;                   // backward: o
+    Strided la;                  // log_alpha
+    Strided g;                   // backward: o_grad
+    const float* h0;             // [B, D] or null
+    const float* dhT;            // backward: [B, D] or null
+    void* o;                     // forward: o; backward: x_grad
+    void* dla;                   // backward: log_alpha_grad
+    float* hT;                   // forward: hT; backward: h0_grad; or null
+    const int* cu;               // [B + 1] or null
+    int B, T, D;
+    kla_dtype dtype, gdtype;
+};
+
 // Each returns cudaSuccess or the launch error.  Shapes are validated by the
 // caller (kla_api.cu); a launcher returning cudaErrorInvalidValue means the
 // shape has no instantiation.
@@ -174,6 +227,21 @@ size_t chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int C);
 // Every argument check of kla_chunk_bwd except those on the workspace and
 // the step rule (a.ckpt, a.dsck are not looked at).
 kla_status check_chunk_bwd_args(const BwdArgs& a);
+// Layer norm (rows > 0); workspace: layernorm_bwd_workspace_bytes bytes for
+// the partial weight and bias gradients (unused when both are null).
+cudaError_t launch_layernorm(const LayerNormArgs& a, cudaStream_t stream);
+size_t layernorm_bwd_workspace_bytes(int rows, int D, kla_dtype dtype);
+cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, void* workspace,
+                                 cudaStream_t stream);
+// Gated linear recurrence (B > 0).
+size_t glr_workspace_bytes(int B, int T, int D, bool packed, kla_dtype dtype,
+                           kla_dtype gdtype);
+cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
+                       cudaStream_t stream);
+cudaError_t launch_glr_step(const void* x, long long x_stride,
+                            const void* la, long long la_stride, float* S,
+                            void* o, int N, int D, kla_dtype dtype,
+                            kla_dtype gdtype, cudaStream_t stream);
 // SM count of the current device (cached per device).
 int device_sm_count();
 

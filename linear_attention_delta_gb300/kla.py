@@ -26,6 +26,7 @@ RULES = {"kaczmarz": 0, "given": 1}
 # name -> (restype, argtypes) of every symbol include/kla.h declares
 _VP, _FP, _F, _I = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, \
     ctypes.c_int
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "kla_chunk_fwd": (_I, [_VP, _VP, _VP, _FP, _FP, _F, _FP, _VP, _FP,
                            _I, _I, _I, _I, _I, _I, _I, _VP]),
@@ -74,6 +75,22 @@ SIGNATURES = {
     "kla_chunk_fwd_host": (_I, [_VP, _VP, _VP, _FP, _FP, _F, _FP, _VP, _FP,
                                 _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                 _VP, ctypes.c_size_t, _VP]),
+    "kla_layernorm_fwd": (_I, [_VP, _LL, _VP, _LL, _VP, _VP, _F, _VP, _VP,
+                               _FP, _FP, _I, _I, _I, _I, _VP]),
+    "kla_layernorm_bwd_workspace_size": (
+        _I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "kla_layernorm_bwd": (_I, [_VP, _LL, _VP, _LL, _VP, _FP, _FP, _VP, _LL,
+                               _VP, _VP, _VP, _I, _I, _I, _I,
+                               _VP, ctypes.c_size_t, _VP]),
+    "kla_glr_workspace_size": (
+        _I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "kla_glr_fwd": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _FP, _VP, _FP, _VP,
+                         _I, _I, _I, _I, _I, _VP, ctypes.c_size_t, _VP]),
+    "kla_glr_bwd": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _FP, _VP, _LL, _LL,
+                         _FP, _VP, _VP, _FP, _VP, _I, _I, _I, _I, _I,
+                         _VP, ctypes.c_size_t, _VP]),
+    "kla_glr_step": (_I, [_VP, _LL, _VP, _LL, _FP, _VP, _I, _I, _I, _I,
+                          _VP]),
     "kla_device_status": (_I, [_VP]),
     "kla_selftest_wait_timeout": (_I, [_VP]),
     "kla_status_string": (ctypes.c_char_p, [_I]),
@@ -534,6 +551,325 @@ def decode_step_kw(q, k, k_write, v, log_alpha, eta, S, eps: float = 1e-6,
         RULES[rule], _stream(stream))
     if st != KLA_OK:
         raise KlaError("kla_decode_step_kw", st)
+    return o
+
+
+# --- layer norm and the gated linear recurrence ----------------------------
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tensor(name, t, device, dtypes, shape=None, packed_last=True):
+    """Checks a tensor of the call: on ``device``, of one of ``dtypes``, of
+    ``shape`` (when given), its last axis adjacent; contiguous unless
+    ``packed_last`` says that the last axis is enough."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (no CPU fallback)")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on device {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has the unsupported dtype {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if not t.is_contiguous() and not (
+            packed_last and (t.shape[-1] == 1 or t.stride(-1) == 1)):
+        raise ValueError(f"{name} must be contiguous"
+                         + (" along its last axis" if packed_last else ""))
+
+
+_F32, _IO = (torch.float32,), tuple(DTYPES)
+
+
+def _device_of(name, t):
+    """The CUDA device of the call, which has to be the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (no CPU fallback)")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current "
+                         f"device")
+    return dev
+
+
+def _row_stride(name, t):
+    """Elements between the rows of t seen as [rows, D]."""
+    D = t.shape[-1]
+    if t.is_contiguous():
+        return D
+    stride = step = None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != step:
+            raise ValueError(f"the rows of {name} must be evenly spaced")
+        step = st * n
+    return D if stride is None else stride
+
+
+def _workspace(workspace, nbytes, device):
+    """(the buffer, its bytes): the caller's, or one of torch's when None."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    _tensor("workspace", workspace, device, (torch.uint8,),
+            packed_last=False)
+    return workspace, workspace.numel()
+
+
+def _output(name, t, shape, dtype, device):
+    """A preallocated contiguous output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(name, t, device, (dtype,), shape, packed_last=False)
+    return t
+
+
+def _call(name, *args):
+    st = getattr(load_library(), name)(
+        *args, torch.cuda.current_stream().cuda_stream)
+    if st != KLA_OK:
+        raise KlaError(name, st)
+
+
+def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
+                  residual=None, y=None, sum=None, want_stats: bool = True,
+                  stream=None):
+    """Layer norm over the last axis (``kla_layernorm_fwd``), of x or, with a
+    ``residual``, of s = x + residual.
+
+    x, residual [..., D] (fp32 or bf16; rows evenly spaced, so a slice of a
+    wider tensor will do); weight, bias [D] (fp32 or bf16, one dtype) or None.
+    Returns (y, sum, mean, rstd): ``sum`` is s, rounded to x's dtype (None
+    without a residual); mean, rstd [...] fp32 are what ``layernorm_bwd``
+    takes (None unless ``want_stats``).  ``y`` and ``sum`` may be passed
+    preallocated."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_fwd(x, weight, bias, eps, residual, y, sum,
+                                 want_stats)
+    dev = _device_of("x", x)
+    _tensor("x", x, dev, _IO)
+    shape, dt = x.shape, x.dtype
+    if x.ndim < 1 or shape[-1] < 1:
+        raise ValueError("x must have a last axis of at least one element")
+    D = shape[-1]
+    rows = x.numel() // D
+    wt = dt
+    if weight is not None or bias is not None:
+        wt = (bias if weight is None else weight).dtype
+        if weight is not None:
+            _tensor("weight", weight, dev, _IO, (D,), packed_last=False)
+        if bias is not None:
+            _tensor("bias", bias, dev, _IO if weight is None else (wt,), (D,),
+                    packed_last=False)
+    rs = 0
+    if residual is not None:
+        _tensor("residual", residual, dev, (dt,), shape)
+        rs = _row_stride("residual", residual)
+        sum = _output("sum", sum, shape, dt, dev)
+    elif sum is not None:
+        raise ValueError("sum is written only with a residual")
+    y = _output("y", y, shape, dt, dev)
+    mean = rstd = None
+    if want_stats:
+        mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32,
+                                 device=dev).unbind(0)
+    _call("kla_layernorm_fwd", x.data_ptr(), _row_stride("x", x),
+          _addr(residual), rs, _addr(weight), _addr(bias), eps, y.data_ptr(),
+          _addr(sum), _addr(mean), _addr(rstd), rows, D, DTYPES[dt],
+          DTYPES[wt])
+    return y, sum, mean, rstd
+
+
+def layernorm_bwd_workspace_size(rows: int, D: int, dtype) -> int:
+    """Bytes of device workspace ``layernorm_bwd`` needs."""
+    n = ctypes.c_size_t(0)
+    st = load_library().kla_layernorm_bwd_workspace_size(
+        rows, D, DTYPES[dtype], ctypes.byref(n))
+    if st != KLA_OK:
+        raise KlaError("kla_layernorm_bwd_workspace_size", st)
+    return n.value
+
+
+def layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad=None,
+                  want_weight_grads: bool = True, workspace=None,
+                  stream=None):
+    """Backward pass of ``layernorm_fwd`` (``kla_layernorm_bwd``).
+
+    x is the tensor that was normalised (the forward's ``sum``, or its x
+    without a residual), mean and rstd what the forward returned; weight [D]
+    or None (ones); ``sum_grad``: dL/dsum, the gradient that reaches the sum
+    past the norm, or None.  Returns a dict with x_grad (the gradient of x
+    and of the residual alike, x's dtype) and weight_grad, bias_grad (weight's
+    dtype, x's without a weight; None unless ``want_weight_grads``).
+    ``workspace``: a device uint8 tensor of at least
+    ``layernorm_bwd_workspace_size`` bytes, allocated here when None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad,
+                                 want_weight_grads, workspace)
+    dev = _device_of("x", x)
+    _tensor("x", x, dev, _IO)
+    shape, dt = x.shape, x.dtype
+    if x.ndim < 1 or shape[-1] < 1:
+        raise ValueError("x must have a last axis of at least one element")
+    D = shape[-1]
+    rows = x.numel() // D
+    _tensor("y_grad", y_grad, dev, (dt,), shape)
+    _tensor("mean", mean, dev, _F32, shape[:-1], packed_last=False)
+    _tensor("rstd", rstd, dev, _F32, shape[:-1], packed_last=False)
+    wt, ss = dt, 0
+    if weight is not None:
+        _tensor("weight", weight, dev, _IO, (D,), packed_last=False)
+        wt = weight.dtype
+    if sum_grad is not None:
+        _tensor("sum_grad", sum_grad, dev, (dt,), shape)
+        ss = _row_stride("sum_grad", sum_grad)
+    dx = torch.empty(shape, dtype=dt, device=dev)
+    dw = db = None
+    nbytes = 0
+    if want_weight_grads:
+        dw = torch.empty(D, dtype=wt, device=dev)
+        db = torch.empty(D, dtype=wt, device=dev)
+        workspace, nbytes = _workspace(
+            workspace, layernorm_bwd_workspace_size(rows, D, dt), dev)
+    _call("kla_layernorm_bwd", y_grad.data_ptr(),
+          _row_stride("y_grad", y_grad), x.data_ptr(), _row_stride("x", x),
+          _addr(weight), mean.data_ptr(), rstd.data_ptr(), _addr(sum_grad),
+          ss, dx.data_ptr(), _addr(dw), _addr(db), rows, D, DTYPES[dt],
+          DTYPES[wt], _addr(workspace), nbytes)
+    return dict(x_grad=dx, weight_grad=dw, bias_grad=db)
+
+
+def glr_workspace_size(B: int, T: int, D: int, dtype, gate_dtype,
+                       packed: bool = False) -> int:
+    """Bytes of device workspace ``glr_fwd`` and ``glr_bwd`` need: B sequences
+    of T tokens, or B sequences ``packed`` into T tokens in all."""
+    n = ctypes.c_size_t(0)
+    st = load_library().kla_glr_workspace_size(
+        B, T, D, int(packed), DTYPES[dtype], DTYPES[gate_dtype],
+        ctypes.byref(n))
+    if st != KLA_OK:
+        raise KlaError("kla_glr_workspace_size", st)
+    return n.value
+
+
+def _glr_shape(name, x, cu_seqlens):
+    """(device, B, T, D) of a recurrence call."""
+    dev = _device_of(name, x)
+    _tensor(name, x, dev, _IO)
+    if cu_seqlens is None:
+        if x.ndim != 3:
+            raise ValueError(f"{name} must be [B, T, D]")
+        B, T, D = x.shape
+    else:
+        if x.ndim != 2:
+            raise ValueError(f"{name} must be [T, D] with cu_seqlens")
+        _tensor("cu_seqlens", cu_seqlens, dev, (torch.int32,),
+                packed_last=False)
+        if cu_seqlens.ndim != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [B + 1]")
+        B = cu_seqlens.numel() - 1
+        T, D = x.shape
+    if D < 1:
+        raise ValueError(f"{name} must have at least one channel")
+    return dev, B, T, D
+
+
+def _glr_strides(t):
+    return (t.data_ptr(), 0 if t.ndim == 2 else t.stride(0), t.stride(-2))
+
+
+def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
+            want_state: bool = True, workspace=None, stream=None):
+    """Gated linear recurrence (``kla_glr_fwd``), per sequence and channel
+    h_t = exp(log_alpha_t) h_{t-1} + x_t, o_t = h_t.
+
+    x, log_alpha [B, T, D] (fp32 or bf16 each; any strides with the last axis
+    adjacent) with h0 [B, D] fp32 or None (zeros); or, with ``cu_seqlens``
+    [B + 1] (device, int32), [T, D]: B sequences packed back to back, the
+    n-th holding the tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1.  Returns
+    (o, hT): o contiguous of x's dtype, hT [B, D] fp32 the last states (None
+    unless ``want_state``).  ``o`` / ``hT`` may be passed preallocated (``hT``
+    may be ``h0``); ``workspace``: a device uint8 tensor of at least
+    ``glr_workspace_size`` bytes, allocated here when None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return glr_fwd(x, log_alpha, h0, cu_seqlens, o, hT, want_state,
+                           workspace)
+    dev, B, T, D = _glr_shape("x", x, cu_seqlens)
+    dt = x.dtype
+    _tensor("log_alpha", log_alpha, dev, _IO, x.shape)
+    if h0 is not None:
+        _tensor("h0", h0, dev, _F32, (B, D), packed_last=False)
+    o = _output("o", o, x.shape, dt, dev)
+    if hT is not None or want_state:
+        hT = _output("hT", hT, (B, D), torch.float32, dev)
+    workspace, nbytes = _workspace(
+        workspace, glr_workspace_size(B, T, D, dt, log_alpha.dtype,
+                                      cu_seqlens is not None), dev)
+    _call("kla_glr_fwd", *_glr_strides(x), *_glr_strides(log_alpha),
+          _addr(h0), o.data_ptr(), _addr(hT), _addr(cu_seqlens), B, T, D,
+          DTYPES[dt], DTYPES[log_alpha.dtype], _addr(workspace), nbytes)
+    return o, hT
+
+
+def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
+            want_h0_grad: bool = True, workspace=None, stream=None):
+    """Backward pass of ``glr_fwd`` (``kla_glr_bwd``): gradients given dL/do
+    (``o_grad``, like o) and dL/dhT (``hT_grad``, [B, D] fp32 or None).  o is
+    what the forward returned, the other arguments what it took.  Returns a
+    dict with x_grad (o's dtype), log_alpha_grad (log_alpha's dtype) and
+    h0_grad ([B, D] fp32; None unless ``want_h0_grad``)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return glr_bwd(o, log_alpha, o_grad, hT_grad, h0, cu_seqlens,
+                           want_h0_grad, workspace)
+    dev, B, T, D = _glr_shape("o", o, cu_seqlens)
+    dt, gt = o.dtype, log_alpha.dtype
+    _tensor("log_alpha", log_alpha, dev, _IO, o.shape)
+    _tensor("o_grad", o_grad, dev, (dt,), o.shape)
+    for name, t in (("h0", h0), ("hT_grad", hT_grad)):
+        if t is not None:
+            _tensor(name, t, dev, _F32, (B, D), packed_last=False)
+    dx = torch.empty(o.shape, dtype=dt, device=dev)
+    dla = torch.empty(o.shape, dtype=gt, device=dev)
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) \
+        if want_h0_grad else None
+    workspace, nbytes = _workspace(
+        workspace, glr_workspace_size(B, T, D, dt, gt,
+                                      cu_seqlens is not None), dev)
+    _call("kla_glr_bwd", *_glr_strides(o), *_glr_strides(log_alpha),
+          _addr(h0), *_glr_strides(o_grad), _addr(hT_grad), dx.data_ptr(),
+          dla.data_ptr(), _addr(dh0), _addr(cu_seqlens), B, T, D, DTYPES[dt],
+          DTYPES[gt], _addr(workspace), nbytes)
+    return dict(x_grad=dx, log_alpha_grad=dla, h0_grad=dh0)
+
+
+def glr_step(x, log_alpha, S, o=None, stream=None):
+    """One token of the gated linear recurrence for N sequences
+    (``kla_glr_step``): S [N, D] fp32 becomes exp(log_alpha) S + x in place;
+    x, log_alpha [N, D] (fp32 or bf16 each, rows evenly spaced).  Returns the
+    new states rounded to x's dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return glr_step(x, log_alpha, S, o)
+    dev = _device_of("x", x)
+    _tensor("x", x, dev, _IO)
+    if x.ndim != 2 or x.shape[1] < 1:
+        raise ValueError("x must be [N, D]")
+    shape, dt = x.shape, x.dtype
+    _tensor("log_alpha", log_alpha, dev, _IO, shape)
+    _tensor("S", S, dev, _F32, shape, packed_last=False)
+    o = _output("o", o, shape, dt, dev)
+    _call("kla_glr_step", x.data_ptr(), x.stride(0), log_alpha.data_ptr(),
+          log_alpha.stride(0), S.data_ptr(), o.data_ptr(), shape[0], shape[1],
+          DTYPES[dt], DTYPES[log_alpha.dtype])
     return o
 
 

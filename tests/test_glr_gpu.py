@@ -1,0 +1,432 @@
+"""Gated linear recurrence (kla_glr_fwd / _bwd / _step) against the fp64
+oracle.  Bounds per element: the running error bound of a 32-bit evaluation
+(oracle.mixer.glr_fwd_bound, glr_bwd_bound), plus half a unit of the output's
+type."""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_delta_gb300 import kla
+from oracle import mixer
+from oracle.mixer import U16, U32
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+TYPES = [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    kla.load_library()
+    yield
+    assert kla.device_status() == 0
+
+
+def normal(shape, dtype, seed):
+    r = np.random.default_rng(seed)
+    return torch.from_numpy(
+        r.standard_normal(shape).astype(np.float32)).cuda().to(dtype)
+
+
+def gates(shape, dtype, seed, lo=1e-4, hi=3.0):
+    """Log decays from almost none to almost all, mixed over channels and
+    tokens."""
+    r = np.random.default_rng(seed)
+    rate = np.exp(r.uniform(np.log(lo), np.log(hi), shape[-1:]))
+    g = -(rate * 2 * r.random(shape)).astype(np.float32)
+    return torch.from_numpy(g).cuda().to(dtype)
+
+
+def assert_within(name, got, ref, bound, dtype):
+    got = mixer.f64(got)
+    assert got.shape == ref.shape, name
+    bound = bound + (U16 * 1.01 if dtype == BF16 else U32) * np.abs(ref)
+    bad = ~(np.abs(got - ref) <= bound)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(
+            f"{name}: {bad.sum()} of {bad.size} outside, first at {i}: got "
+            f"{got[i]}, expected {ref[i]} +- {bound[i]}")
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+
+
+def check_fwd(x, la, h0=None, cu=None):
+    o, hT = kla.glr_fwd(x, la, h0, None if cu is None else cu.cuda())
+    ro, rh = mixer.glr_fwd(x, la, h0, cu)
+    bo, bh = mixer.glr_fwd_bound(x, la, h0, cu)
+    assert_within("o", o, ro, bo, x.dtype)
+    assert_within("hT", hT, rh, bh, F32)
+    assert o.dtype == x.dtype and hT.dtype == F32
+    return o, hT
+
+
+def check_bwd(o, la, do, dhT=None, h0=None, cu=None):
+    g = kla.glr_bwd(o, la, do, dhT, h0, None if cu is None else cu.cuda())
+    ref = mixer.glr_bwd(o, la, do, dhT, h0, cu)
+    bound = mixer.glr_bwd_bound(o, la, do, dhT, h0, cu)
+    for name, r, b, dt in zip(("x_grad", "log_alpha_grad", "h0_grad"), ref,
+                              bound, (o.dtype, la.dtype, F32)):
+        assert_within(name, g[name], r, b, dt)
+        assert g[name].dtype == dt
+    return g
+
+
+SHAPES = [(1, 1, 1), (2, 1, 7), (1, 2, 64), (5, 3, 33), (3, 17, 130),
+          (2, 128, 64), (2, 129, 256), (1, 1000, 33), (1, 5000, 8),
+          (2, 257, 2048), (40, 65, 96), (1, 1025, 1001)]
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("B,T,D", SHAPES)
+def test_sizes_and_types(B, T, D, dtype, gtype):
+    seed = B * 1000 + T + D
+    x, la = normal((B, T, D), dtype, seed), gates((B, T, D), gtype, seed + 1)
+    h0, dhT = normal((B, D), F32, seed + 2), normal((B, D), F32, seed + 3)
+    do = normal((B, T, D), dtype, seed + 4)
+    check_fwd(x, la)
+    o, _ = check_fwd(x, la, h0)
+    check_bwd(o, la, do)
+    check_bwd(o, la, do, dhT, h0)
+
+
+LENGTHS = [[5], [0], [0, 0], [0, 1, 0], [1] * 40, [3, 0, 0, 130, 1, 0],
+           [0, 0, 127, 1, 128, 129, 2], [300, 1, 0, 511, 64, 64, 64, 1, 1],
+           [0, 2000, 0, 0, 1, 700, 0], [16] * 30 + [15, 17, 1]]
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("k", range(len(LENGTHS)))
+def test_packed(k, dtype, gtype):
+    lens = LENGTHS[k]
+    cu, T, N = offsets(lens), sum(lens), len(lens)
+    for D in (1, 64, 131):
+        seed = 100 * k + D
+        x, la = normal((T, D), dtype, seed), gates((T, D), gtype, seed + 1)
+        h0, dhT = normal((N, D), F32, seed + 2), normal((N, D), F32, seed + 3)
+        do = normal((T, D), dtype, seed + 4)
+        check_fwd(x, la, None, cu)
+        o, _ = check_fwd(x, la, h0, cu)
+        check_bwd(o, la, do, None, None, cu)
+        check_bwd(o, la, do, dhT, h0, cu)
+
+
+def test_packed_many_empty_sequences():
+    r = np.random.default_rng(0)
+    lens = [int(v) if r.random() < 0.02 else 0
+            for v in r.integers(1, 400, 3000)]
+    cu, T = offsets(lens), sum(lens)
+    x, la = normal((T, 70), BF16, 1), gates((T, 70), F32, 2)
+    h0 = normal((3000, 70), F32, 3)
+    o, _ = check_fwd(x, la, h0, cu)
+    check_bwd(o, la, x, h0, h0, cu)
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+def test_strided_views(dtype, gtype):
+    """Slices of wider tensors (odd offsets among them), sequences and tokens
+    in swapped order, a gate repeated over the batch."""
+    B, T, D = 3, 150, 96
+    wide, wide_a = normal((B, T, 2 * D + 1), dtype, 5), \
+        gates((B, T, 2 * D + 1), gtype, 6)
+    h0 = normal((B, D), F32, 7)
+    for off in (0, 1, 2, D):
+        x, la = wide[..., off:off + D], wide_a[..., off:off + D]
+        o, _ = check_fwd(x, la, h0)
+        check_bwd(x, la, wide[..., D:2 * D], h0, h0)
+    x, la = (v[..., :D].transpose(0, 1).contiguous().transpose(0, 1)
+             for v in (wide, wide_a))
+    assert not x.is_contiguous()
+    check_fwd(x, la, h0)
+    check_bwd(x, la, x, h0, h0)
+    la = wide_a[:1, :, :D].expand(B, T, D)
+    check_fwd(x, la, h0)
+    check_bwd(x, la, x, h0, h0)
+    la = wide_a[:, :1, :D].expand(B, T, D)       # one gate for all tokens
+    check_fwd(x, la, h0)
+    cut = wide[:, 5:, :D], wide_a[:, 5:, :D]
+    check_fwd(*cut, h0)
+    cu = offsets([40, 0, 110])
+    check_fwd(wide[0, :, 3:3 + D], wide_a[0, :, 3:3 + D], h0, cu)
+
+
+@pytest.mark.parametrize("T", [5, 128, 700])
+def test_extreme_gates(T):
+    D = 64
+    x, h0 = normal((2, T, D), F32, 8), normal((2, D), F32, 9)
+    la = gates((2, T, D), F32, 10)
+    la[:, ::7] = -float("inf")                   # forget
+    la[:, 3::11] = torch.finfo(F32).min
+    la[:, 1::5] = 0.0                            # keep everything
+    la[:, 2::13] = -1e-30
+    o, hT = check_fwd(x, la, h0)
+    check_bwd(o, la, x, h0, h0)
+    check_fwd(x, torch.zeros_like(la), h0)
+    check_fwd(x, torch.full_like(la, 1e-3), h0)   # growth
+    check_fwd(x, torch.full_like(la, -100.0), h0)
+
+
+def test_growth_past_the_range_starts_from_zero():
+    """exp(log_alpha) whose product over many tokens overflows, on a state
+    that stays zero: 0, not 0 * inf."""
+    x = torch.zeros(1, 600, 64, device="cuda")
+    la = torch.ones_like(x)
+    o, hT = kla.glr_fwd(x, la)
+    assert (o == 0).all() and (hT == 0).all()
+    g = kla.glr_bwd(x, la, x)
+    assert (g["x_grad"] == 0).all() and (g["log_alpha_grad"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+def test_bad_sequences_stay_their_own(dtype, gtype):
+    """NaN and infinities of one packed sequence, in x, in the gates or in
+    its initial state, reach no other sequence."""
+    lens = [100, 33, 0, 260, 1, 90]
+    cu, T, D = offsets(lens), sum(lens), 66
+    x, la = normal((T, D), dtype, 11), gates((T, D), gtype, 12)
+    h0, do = normal((6, D), F32, 13), normal((T, D), dtype, 14)
+    o, hT = kla.glr_fwd(x, la, h0, cu.cuda())
+    g = kla.glr_bwd(o, la, do, h0, h0, cu.cuda())
+    x2, la2, h2, do2, o2 = x.clone(), la.clone(), h0.clone(), do.clone(), \
+        o.clone()
+    x2[40] = float("nan")                        # sequence 0
+    x2[150, ::2] = float("inf")                  # sequence 3
+    do2[60], do2[300] = float("inf"), float("nan")
+    o2[99] = float("nan")
+    h2[1] = float("inf")
+    la2[110] = float("nan")                      # sequence 1
+    oo, hh = kla.glr_fwd(x2, la2, h2, cu.cuda())
+    gg = kla.glr_bwd(o2, la2, do2, h2, h2, cu.cuda())
+    for n in (2, 4, 5):
+        q = slice(int(cu[n]), int(cu[n + 1]))
+        assert torch.equal(oo[q], o[q]) and torch.equal(hh[n], hT[n])
+        assert torch.equal(gg["x_grad"][q], g["x_grad"][q])
+        assert torch.equal(gg["log_alpha_grad"][q], g["log_alpha_grad"][q])
+        assert torch.equal(gg["h0_grad"][n], g["h0_grad"][n])
+    assert oo[40:100].isnan().all()
+
+
+def test_bad_offsets_stay_inside():
+    """Offsets that run backwards or past the tokens: whatever the result,
+    every access stays inside the tensors (the guard rows keep their value)
+    and the call returns."""
+    T, D = 300, 64
+    buf = torch.full((T + 512, D), 3.0, device="cuda")
+    o = buf[256:256 + T]
+    x, la = normal((T, D), F32, 15), gates((T, D), F32, 16)
+    for cu in ([0, 500, 20, 300], [5, 2, 1, 0], [-7, 90, 10 ** 9, 300],
+               [300, 300, 300, 300], [0, 0, 0, 0], [200, 300, 400, 500]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        kla.glr_fwd(x, la, normal((3, D), F32, 17), c, o=o)
+        kla.glr_bwd(x, la, x, normal((3, D), F32, 17), None, c)
+        assert (buf[:256] == 3).all() and (buf[256 + T:] == 3).all()
+    assert kla.device_status() == 0
+
+
+def test_zero_tokens_and_zero_sequences():
+    h0 = normal((3, 50), F32, 18)
+    x = torch.empty(3, 0, 50, device="cuda")
+    o, hT = kla.glr_fwd(x, x, h0)
+    assert o.shape == x.shape and torch.equal(hT, h0)
+    assert (kla.glr_fwd(x, x)[1] == 0).all()
+    assert torch.equal(kla.glr_bwd(x, x, x, h0)["h0_grad"], h0)
+    e = torch.empty(0, 7, 50, device="cuda")
+    o, hT = kla.glr_fwd(e, e)
+    assert o.shape == e.shape and hT.shape == (0, 50)
+
+
+def test_state_in_place_and_carried_over():
+    """hT written over h0; a sequence in two calls equals one call within
+    rounding; tokens one by one through glr_step equal the scan."""
+    B, T, D = 3, 200, 320
+    x, la = normal((B, T, D), BF16, 19), gates((B, T, D), F32, 20)
+    h0 = normal((B, D), F32, 21)
+    o, hT = check_fwd(x, la, h0)
+    s = h0.clone()
+    o2, s2 = kla.glr_fwd(x, la, s, hT=s)
+    assert s2 is s and torch.equal(s, hT) and torch.equal(o2, o)
+    _, mid = kla.glr_fwd(x[:, :77], la[:, :77], h0)
+    _, end = kla.glr_fwd(x[:, 77:], la[:, 77:], mid)
+    ref, bound = mixer.glr_fwd(x, la, h0)[1], \
+        mixer.glr_fwd_bound(x, la, h0)[1]
+    assert_within("hT in two calls", end, ref, bound, F32)
+    S = h0.clone()
+    out = torch.stack([kla.glr_step(x[:, t], la[:, t], S) for t in range(T)],
+                      1)
+    ro, bo = mixer.glr_fwd(x, la, h0)[0], mixer.glr_fwd_bound(x, la, h0)[0]
+    assert_within("steps", out, ro, bo, BF16)
+    assert_within("S", S, ref, bound, F32)
+    cu = offsets([150, 0, 50])
+    p, pa = x[0], la[0]
+    ref = kla.glr_fwd(p, pa, h0, cu.cuda())
+    s = h0.clone()
+    got = kla.glr_fwd(p, pa, s, cu.cuda(), hT=s)
+    assert torch.equal(got[0], ref[0]) and torch.equal(s, ref[1])
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("N,D", [(1, 1), (1, 2048), (7, 33), (300, 130),
+                                 (256, 2048), (70000, 3)])
+def test_step(N, D, dtype, gtype):
+    x, la = normal((N, D + 5), dtype, 22), gates((N, D + 5), gtype, 23)
+    for off in (0, 3):
+        xs, as_ = x[:, off:off + D], la[:, off:off + D]
+        if off == 0:
+            xs, as_ = xs.contiguous(), as_.contiguous()
+        S = normal((N, D), F32, 24)
+        a, s0 = np.exp(mixer.f64(as_)), mixer.f64(S)
+        ref = a * s0 + mixer.f64(xs)
+        bound = 8 * U32 * (np.abs(a * s0) + np.abs(ref)) + 1e-30
+        o = kla.glr_step(xs, as_, S)
+        assert_within("S", S, ref, bound, F32)
+        assert_within("o", o, ref, bound, dtype)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_are_the_differences(packed):
+    """fp32 gradients against central differences of the fp64 forward."""
+    r = np.random.default_rng(25)
+    lens = [60, 0, 1, 199] if packed else None
+    cu = offsets(lens) if packed else None
+    shape, N = ((260, 5), 4) if packed else ((2, 130, 5), 2)
+    x, la = normal(shape, F32, 26), gates(shape, F32, 27, 1e-2)
+    h0, dhT = normal((N, 5), F32, 28), normal((N, 5), F32, 29)
+    do = normal(shape, F32, 30)
+    dcu = cu.cuda() if packed else None
+    o, _ = kla.glr_fwd(x, la, h0, dcu)
+    g = kla.glr_bwd(o, la, do, dhT, h0, dcu)
+    args = [mixer.f64(v) for v in (x, la, h0)]
+    fdo, fdh = mixer.f64(do), mixer.f64(dhT)
+
+    def loss(x, la, h0):
+        o, hT = mixer.glr_fwd(x, la, h0, cu)
+        return (o * fdo).sum() + (hT * fdh).sum()
+
+    for k, name in enumerate(("x_grad", "log_alpha_grad", "h0_grad")):
+        got = mixer.f64(g[name])
+        v, h = r.standard_normal(got.shape), 1e-6
+        up, dn = list(args), list(args)
+        up[k], dn[k] = args[k] + h * v, args[k] - h * v
+        slope = (loss(*up) - loss(*dn)) / (2 * h)
+        # fp32: some 1e-6 of the terms; the differences: 1e-9
+        assert abs((got * v).sum() - slope) <= 1e-5 * (
+            np.abs(got * v).sum() + 1), name
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 20000, 64), (2, 4096, 512)])
+def test_same_bits_every_call_and_on_another_stream(B, T, D):
+    x, la = normal((B, T, D), BF16, 31), gates((B, T, D), F32, 32)
+    h0, do = normal((B, D), F32, 33), normal((B, T, D), BF16, 34)
+    o, hT = kla.glr_fwd(x, la, h0)
+    g = kla.glr_bwd(o, la, do, h0, h0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(10):
+        s = side if i % 2 else None
+        o2, h2 = kla.glr_fwd(x, la, h0, stream=s)
+        g2 = kla.glr_bwd(o, la, do, h0, h0, stream=s)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(o, o2) and torch.equal(hT, h2)
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_long_sequence_with_long_memory():
+    """65536 tokens, decays down to 1e-4 a token."""
+    x, la = normal((1, 65536, 16), F32, 35), gates((1, 65536, 16), F32, 36)
+    o, _ = check_fwd(x, la, normal((1, 16), F32, 37))
+    check_bwd(o, la, x)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own workspace."""
+    x, la = normal((1, 30000, 256), BF16, 38), gates((1, 30000, 256), F32, 39)
+    ref, _ = kla.glr_fwd(x, la)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [kla.glr_fwd(x, la, stream=streams[i % 2])[0] for i in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_graph_replay_equals_eager():
+    x, la = normal((2, 3000, 128), BF16, 40), gates((2, 3000, 128), F32, 41)
+    S0 = normal((2, 128), F32, 42)
+    ref, hT = kla.glr_fwd(x, la, S0)
+    gref = kla.glr_bwd(ref, la, x, S0, S0)
+    S = S0.clone()
+    sref = kla.glr_step(x[:, 0], la[:, 0], S)
+    S.copy_(S0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, h = kla.glr_fwd(x, la, S0)
+        g = kla.glr_bwd(o, la, x, S0, S0)
+        so = kla.glr_step(x[:, 0], la[:, 0], S)
+    for _ in range(3):
+        S.copy_(S0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, ref) and torch.equal(h, hT)
+        assert all(torch.equal(g[k], gref[k]) for k in g)
+        assert torch.equal(so, sref)
+
+
+def test_offsets_past_32_bits():
+    T, D = 1100000, 2048               # 2.25e9 elements
+    x = torch.zeros(T, D, dtype=BF16, device="cuda")
+    la = torch.zeros(T, D, dtype=BF16, device="cuda")
+    x[0] = 1.0                         # carried unchanged to the last block
+    x[-300:], la[-300:] = normal((300, D), BF16, 43), gates((300, D), BF16,
+                                                            44)
+    o, hT = kla.glr_fwd(x[None], la[None])
+    one = torch.ones(1, D, device="cuda")
+    ro, rh = mixer.glr_fwd(x[None, -300:], la[None, -300:], one)
+    bo, bh = mixer.glr_fwd_bound(x[None, -300:], la[None, -300:], one)
+    assert (o[0, 1000000] == 1).all()
+    assert_within("o", o[:, -300:], ro, bo, BF16)
+    assert_within("hT", hT, rh, bh, F32)
+    g = kla.glr_bwd(o, la[None], x[None])
+    ref = mixer.glr_bwd(o[None, 0, -300:], la[None, -300:], x[None, -300:],
+                        None, one)
+    b = mixer.glr_bwd_bound(o[None, 0, -300:], la[None, -300:],
+                            x[None, -300:], None, one)
+    assert_within("x_grad", g["x_grad"][:, -300:], ref[0], b[0], BF16)
+    assert_within("log_alpha_grad", g["log_alpha_grad"][:, -300:], ref[1],
+                  b[1], BF16)
+
+
+def test_refusals():
+    x, la = normal((2, 9, 64), BF16, 45), gates((2, 9, 64), F32, 46)
+    h0 = normal((2, 64), F32, 47)
+    o, _ = kla.glr_fwd(x, la, h0)
+    cu = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
+    for bad in (lambda: kla.glr_fwd(x.half(), la),
+                lambda: kla.glr_fwd(x, la.double()),
+                lambda: kla.glr_fwd(x, la, h0.bfloat16()),
+                lambda: kla.glr_fwd(x.cpu(), la),
+                lambda: kla.glr_fwd(x[0], la[0], None, cu.long()),
+                lambda: kla.glr_bwd(o, la, o.float()),
+                lambda: kla.glr_step(x[:, 0], la[:, 0], h0.bfloat16())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: kla.glr_fwd(x[0], la[0]),
+                lambda: kla.glr_fwd(x, la, None, cu),
+                lambda: kla.glr_fwd(x, la[:, :8]),
+                lambda: kla.glr_fwd(x, la, h0[:1]),
+                lambda: kla.glr_fwd(x.transpose(1, 2), la.transpose(1, 2)),
+                lambda: kla.glr_fwd(x, la, hT=h0.t()),
+                lambda: kla.glr_bwd(o, la, o[:1]),
+                lambda: kla.glr_step(x, la, h0)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(kla.KlaError):
+        kla.glr_fwd(x, la, h0, o=x)              # over its own input
+    empty = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(kla.KlaError):            # tokens of no sequence
+        kla.glr_fwd(x[0], la[0], None, empty)
+    f = torch.zeros(4, 8, device="cuda")
+    with pytest.raises(kla.KlaError):
+        kla.glr_step(f, f, f)

@@ -1,0 +1,324 @@
+"""Layer norm (kla_layernorm_fwd / _bwd) against the fp64 oracle.
+
+Bounds per element, from the arithmetic: a sum of D terms is made of chains of
+at most D / 32 additions and a tree, and rounding errors of a chain are at
+most its length in units u = 2^-24 of the sum of magnitudes; K = 32 + D / 32
+units cover it with the few roundings around it.  A bf16 result adds its own
+rounding, at most 2^-8 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_delta_gb300 import kla
+from oracle import mixer
+from oracle.mixer import U16, U32
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    kla.load_library()
+    yield
+    assert kla.device_status() == 0
+
+
+def normal(shape, dtype, seed, scale=1.0, shift=0.0):
+    r = np.random.default_rng(seed)
+    v = r.standard_normal(shape) * scale + shift
+    return torch.from_numpy(v.astype(np.float32)).cuda().to(dtype)
+
+
+def rounding(ref, dtype):
+    """The output's own rounding, with the fp32 value's behind it."""
+    return (U16 * 1.01 if dtype == BF16 else U32) * np.abs(ref)
+
+
+def assert_within(name, got, ref, bound):
+    got = mixer.f64(got)
+    assert got.shape == ref.shape, name
+    bad = ~(np.abs(got - ref) <= bound)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(
+            f"{name}: {bad.sum()} of {bad.size} outside, first at {i}: got "
+            f"{got[i]}, expected {ref[i]} +- {bound[i]}")
+
+
+def check_fwd(x, w, b, eps=1e-5, residual=None):
+    y, s, mean, rstd = kla.layernorm_fwd(x, w, b, eps=eps, residual=residual)
+    ry, rs, rm, rr = mixer.ln_fwd(x, w, b, eps, residual)
+    D = x.shape[-1]
+    K = (32 + D / 32) * U32
+    top = np.abs(rs).max(-1)
+    aw = 1.0 if w is None else np.abs(mixer.f64(w))
+    # relative error of rstd: the variance's, from s - mean and its squares
+    drel = K * (1 + top * rr)
+    assert_within("mean", mean, rm, K * top)
+    assert_within("rstd", rstd, rr, rr * drel)
+    xh = np.abs(rs - rm[..., None]) * rr[..., None]
+    ab = 0.0 if b is None else np.abs(mixer.f64(b))
+    # xh's own error and the last addition's roundings, relative to its terms
+    err = aw * ((K * top * rr)[..., None] + xh * drel[..., None]) \
+        + 4 * U32 * (aw * xh + ab)
+    assert_within("y", y, ry, err + rounding(ry, x.dtype))
+    assert y.dtype == x.dtype and mean.dtype == rstd.dtype == F32
+    if residual is None:
+        assert s is None
+    else:
+        assert_within("sum", s, rs, U32 * top[..., None] +
+                      rounding(rs, x.dtype))
+    return y, s, mean, rstd
+
+
+def check_bwd(dy, x, w, ds=None, eps=1e-5):
+    s = mixer.f64(x)
+    m = s.mean(-1)
+    r = 1 / np.sqrt(((s - m[..., None]) ** 2).mean(-1) + eps)
+    mean, rstd = (torch.from_numpy(np.asarray(v, np.float32)).cuda()
+                  for v in (m, r))
+    got = kla.layernorm_bwd(dy, x, w, mean, rstd, sum_grad=ds)
+    dx, dw, db = mixer.ln_bwd(dy, x, w, mean, rstd, ds)
+    D, rows = x.shape[-1], x.numel() // x.shape[-1]
+    K = (32 + D / 32) * U32
+    f = mixer.f64
+    r = f(rstd)[..., None]
+    xh = np.abs(s - f(mean)[..., None]) * r
+    g = np.abs(f(dy)) * (1.0 if w is None else np.abs(f(w)))
+    c1, c2 = (g * xh).mean(-1, keepdims=True), g.mean(-1, keepdims=True)
+    err = K * r * (g + c2 + xh * c1) + \
+        (0 if ds is None else U32 * np.abs(f(ds)))
+    assert_within("x_grad", got["x_grad"], dx, err + rounding(dx, x.dtype))
+    # the rows' sum: chains of rows and slices, at most rows + 64 additions
+    wt = dy.dtype if w is None else w.dtype
+    axes = tuple(range(dy.ndim - 1))
+    n = (rows + 64) * U32
+    aw = (np.abs(f(dy)) * xh).sum(axes)
+    ab = np.abs(f(dy)).sum(axes)
+    assert_within("weight_grad", got["weight_grad"], dw,
+                  n * aw + 4 * U32 * aw + rounding(dw, wt))
+    assert_within("bias_grad", got["bias_grad"], db,
+                  n * ab + rounding(db, wt))
+    assert got["weight_grad"].dtype == got["bias_grad"].dtype == wt
+    return got
+
+
+ROWS = [1, 3, 130]
+WIDTHS = [1, 2, 7, 31, 64, 128, 200, 1000, 1001, 1024, 2048, 4100, 8192,
+          8200, 20000, 40001]
+
+
+@pytest.mark.parametrize("dtype,wtype", [(F32, F32), (BF16, BF16),
+                                         (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_sizes_and_types(D, dtype, wtype):
+    for rows in ROWS:
+        seed = D * 7 + rows
+        x = normal((rows, D), dtype, seed, 2.0, 0.5)
+        w = normal((D,), wtype, seed + 1, 0.2, 1.0)
+        b = normal((D,), wtype, seed + 2)
+        res = normal((rows, D), dtype, seed + 3)
+        check_fwd(x, w, b)
+        check_fwd(x, w, b, residual=res)
+        check_bwd(normal((rows, D), dtype, seed + 4), x, w)
+        check_bwd(normal((rows, D), dtype, seed + 4), x, w, ds=res)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_rows(dtype):
+    x, dy = normal((5001, 384), dtype, 1), normal((5001, 384), dtype, 2)
+    w = normal((384,), F32, 3, 0.2, 1.0)
+    check_fwd(x, w, None)
+    check_bwd(dy, x, w, ds=x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [128, 1001, 2048])
+def test_without_weight_or_bias(D, dtype):
+    x, dy = normal((9, D), dtype, 4), normal((9, D), dtype, 5)
+    w, b = normal((D,), F32, 6), normal((D,), F32, 7)
+    check_fwd(x, None, None)
+    check_fwd(x, w, None)
+    check_fwd(x, None, b)
+    check_bwd(dy, x, None)
+    y, s, mean, rstd = kla.layernorm_fwd(x, w, b, want_stats=False)
+    assert s is None and mean is None and rstd is None
+    _, _, mean, rstd = kla.layernorm_fwd(x)
+    g = kla.layernorm_bwd(dy, x, w, mean, rstd, want_weight_grads=False)
+    assert g["weight_grad"] is None and g["bias_grad"] is None
+    full = kla.layernorm_bwd(dy, x, w, mean, rstd)
+    assert torch.equal(g["x_grad"], full["x_grad"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layouts_give_the_same_bits(dtype):
+    """Slices, odd offsets, repeated rows and more axes against contiguous
+    copies, when the same vector width applies; else within bounds."""
+    D = 640
+    big = normal((12, 3 * D + 1), dtype, 8)
+    w, b = normal((D,), dtype, 9), normal((D,), dtype, 10)
+    dy = normal((12, 3 * D + 1), dtype, 11)
+    for off in (0, 1, 3, D, D + 1):
+        x, g = big[:, off:off + D], dy[:, off:off + D]
+        check_fwd(x, w, b, residual=g)
+        check_bwd(g, x, w, ds=x)
+    x = normal((5, D), dtype, 12)
+    y0 = kla.layernorm_fwd(x, w, b)[0]
+    y1 = kla.layernorm_fwd(x.view(5, 1, D), w, b)[0]
+    assert y1.shape == (5, 1, D) and torch.equal(y1[:, 0], y0)
+    y2, _, m, _ = kla.layernorm_fwd(x[0], w, b)
+    assert y2.shape == (D,) and m.shape == () and torch.equal(y2, y0[0])
+    rep = x[:1].expand(6, D)
+    y3 = kla.layernorm_fwd(rep, w, b)[0]
+    assert all(torch.equal(r, y0[0]) for r in y3)
+    odd = torch.empty(5 * D + 1, dtype=dtype, device="cuda")[1:].view(5, D)
+    res = normal((5, D), dtype, 13)
+    _, s, _, _ = kla.layernorm_fwd(x, w, b, residual=res, y=odd)
+    ref, *_ = kla.layernorm_fwd(x, w, b, residual=res)
+    assert torch.allclose(odd.float(), ref.float(), rtol=1e-2, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [256, 1001, 40001])
+def test_offset_rows_keep_their_variance(D, dtype):
+    # mean 1000 times the spread: E[s^2] - m^2 would lose it
+    check_fwd(normal((4, D), dtype, 14, 0.05, 50.0), None, None)
+
+
+def test_constant_rows():
+    x = torch.full((3, 512), 7.0, device="cuda")
+    y, _, mean, rstd = kla.layernorm_fwd(x, None, None, eps=1e-5)
+    assert (y == 0).all() and (mean == 7).all()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
+
+
+@pytest.mark.parametrize("D", [96, 512, 1001, 8192, 40001])
+def test_bad_rows_stay_their_own(D):
+    """A row with a NaN or an infinity is NaN; its neighbours are not."""
+    x = normal((8, D), BF16, 15)
+    clean = kla.layernorm_fwd(x)[0].clone()
+    x[2, D // 2] = float("nan")
+    x[5, D - 1] = float("inf")
+    y = kla.layernorm_fwd(x)[0]
+    assert y[2].isnan().all() and y[5].isnan().any()
+    for i in (0, 1, 3, 4, 6, 7):
+        assert torch.equal(y[i], clean[i])
+
+
+def test_no_rows():
+    w = normal((64,), F32, 16)
+    x = torch.empty(0, 64, device="cuda")
+    y, _, mean, _ = kla.layernorm_fwd(x, w, w)
+    assert y.shape == (0, 64) and mean.shape == (0,)
+    g = kla.layernorm_bwd(x, x, w, mean, mean)
+    assert (g["weight_grad"] == 0).all() and (g["bias_grad"] == 0).all()
+
+
+@pytest.mark.parametrize("rows,D", [(6, 48), (3, 1001), (5, 512)])
+def test_gradients_are_the_differences(rows, D):
+    """fp32 gradients against central differences of the fp64 forward: the
+    kernel's error is some 1e-6 of the terms' magnitude, the differences'
+    1e-8."""
+    r = np.random.default_rng(D)
+    x, w = r.standard_normal((rows, D)), r.standard_normal(D)
+    dy, ds = r.standard_normal((rows, D)), r.standard_normal((rows, D))
+    t = [torch.from_numpy(v.astype(np.float32)).cuda()
+         for v in (x, w, dy, ds)]
+    x, w, dy, ds = (mixer.f64(v) for v in t)
+    _, _, mean, rstd = kla.layernorm_fwd(t[0], t[1], t[1])
+    g = kla.layernorm_bwd(t[2], t[0], t[1], mean, rstd, sum_grad=t[3])
+
+    def loss(x, w, b):
+        y, s, _, _ = mixer.ln_fwd(x, w, b)
+        return (y * dy).sum() + (s * ds).sum()
+
+    args, h = (x, w, w), 1e-5
+    for k, name in enumerate(("x_grad", "weight_grad", "bias_grad")):
+        got = mixer.f64(g[name])
+        v = r.standard_normal(got.shape)
+        up, dn = list(args), list(args)
+        up[k], dn[k] = args[k] + h * v, args[k] - h * v
+        slope = (loss(*up) - loss(*dn)) / (2 * h)
+        scale = np.abs(got * v).sum() + np.abs(dy).sum()
+        assert abs((got * v).sum() - slope) <= 1e-5 * scale, name
+
+
+def test_same_bits_every_call_and_on_another_stream():
+    x, dy = normal((777, 2048), BF16, 17), normal((777, 2048), BF16, 18)
+    w = normal((2048,), BF16, 19)
+    y, _, mean, rstd = kla.layernorm_fwd(x, w, w)
+    g = kla.layernorm_bwd(dy, x, w, mean, rstd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2, _, mean2, rstd2 = kla.layernorm_fwd(x, w, w, stream=side)
+    g2 = kla.layernorm_bwd(dy, x, w, mean2, rstd2, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, y2) and torch.equal(rstd, rstd2)
+    assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_graph_replay_equals_eager():
+    x, res = normal((4, 2048), BF16, 20), normal((4, 2048), BF16, 21)
+    w = normal((2048,), BF16, 22)
+    ref = kla.layernorm_fwd(x, w, w, residual=res)
+    gref = kla.layernorm_bwd(res, x, w, ref[2], ref[3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = kla.layernorm_fwd(x, w, w, residual=res)
+        g = kla.layernorm_bwd(res, x, w, out[2], out[3])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert all(torch.equal(g[k], gref[k]) for k in g)
+
+
+def test_offsets_past_32_bits():
+    rows, D = 1100000, 2048            # 2.25e9 elements
+    x = torch.empty(rows, D, dtype=BF16, device="cuda")
+    x.fill_(1.0)
+    x[-3:] = normal((3, D), BF16, 23)
+    w = normal((D,), BF16, 24)
+    y, _, mean, rstd = kla.layernorm_fwd(x, w, w)
+    ref = kla.layernorm_fwd(x[-3:].clone(), w, w)
+    assert torch.equal(y[-3:], ref[0]) and torch.equal(rstd[-3:], ref[3])
+    assert (y[:4].float() == w.float()).all()
+    g = kla.layernorm_bwd(x, x, w, mean, rstd, want_weight_grads=False)
+    gref = kla.layernorm_bwd(x[-3:].clone(), x[-3:].clone(), w, ref[2],
+                             ref[3], want_weight_grads=False)
+    assert torch.equal(g["x_grad"][-3:], gref["x_grad"])
+
+
+def test_refusals():
+    x, w = normal((4, 64), BF16, 25), normal((64,), BF16, 26)
+    _, _, mean, rstd = kla.layernorm_fwd(x, w, w)
+    with pytest.raises(TypeError):
+        kla.layernorm_fwd(x.half(), w, w)
+    with pytest.raises(TypeError):
+        kla.layernorm_fwd(x, w.cpu(), w)
+    with pytest.raises(TypeError):
+        kla.layernorm_fwd(x, w, w.float())
+    with pytest.raises(ValueError):
+        kla.layernorm_fwd(x, w[:63], w[:63])
+    with pytest.raises(ValueError):
+        kla.layernorm_fwd(x.t(), None, None)
+    with pytest.raises(ValueError):
+        kla.layernorm_fwd(x.view(2, 2, 64).transpose(0, 1), w, w)
+    with pytest.raises(ValueError):
+        kla.layernorm_fwd(x, w, w, residual=x[:2])
+    with pytest.raises(ValueError):
+        kla.layernorm_fwd(x, w, w, sum=x)
+    with pytest.raises(kla.KlaError):
+        kla.layernorm_fwd(x, w, w, eps=-1.0)
+    with pytest.raises(kla.KlaError):
+        kla.layernorm_fwd(x, w, w, y=x)
+    with pytest.raises(TypeError):
+        kla.layernorm_bwd(x.float(), x, w, mean, rstd)
+    with pytest.raises(ValueError):
+        kla.layernorm_bwd(x, x, w, mean[:2], rstd)
+    with pytest.raises(kla.KlaError):
+        kla.layernorm_bwd(x, x, w, mean, rstd, workspace=torch.empty(
+            16, dtype=torch.uint8, device="cuda"))
