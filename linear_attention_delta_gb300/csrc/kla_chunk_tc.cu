@@ -1144,6 +1144,9 @@ cudaError_t read_and_clear_fault(cudaStream_t stream, unsigned int* word) {
     unsigned int w2 = 0;
     e = read_and_clear_fault2(&w2);
     *word |= w2;
+    if (e != cudaSuccess) return e;
+    e = read_and_clear_fault_glr(&w2);
+    *word |= w2;
     return e;
 }
 
