@@ -660,7 +660,7 @@ KLA_API kla_status kla_layernorm_bwd(
  * Every call initialises what it reads of it.
  * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, D < 1, a null or
  * misaligned pointer, overlapping buffers, a workspace that is missing or too
- * small), KLA_ERR_CUDA.
+ * small), KLA_ERR_UNSUPPORTED_SHAPE (T > 2^31 - 4097), KLA_ERR_CUDA.
  */
 KLA_API kla_status kla_glr_workspace_size(int B, int T, int D, int packed,
                                           kla_dtype dtype,

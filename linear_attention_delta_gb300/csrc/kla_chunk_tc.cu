@@ -1065,6 +1065,8 @@ bool get_encoder() {
     return g_encode != nullptr;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tile_map_encoder() { return g_encode; }
+
 // [B, T, H, 128] bf16, box = 64 features x 1 head x 64 tokens x 1 batch.
 bool make_map(CUtensorMap* m, const void* base, int B, int T, int H) {
     cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)T,

@@ -5,6 +5,9 @@
 // and its reverse: g_t = do_t + alpha_{t+1} g_{t+1}, dx_t = g_t,
 // dlog_alpha_t = alpha_t g_t h_{t-1}, dh0 = alpha_1 g_1.  Bound by HBM: three
 // to five operations per element of each tensor it reads.
+#include <algorithm>
+#include <type_traits>
+
 #include "kla_internal.cuh"
 #include "tc_primitives.cuh"
 
@@ -14,35 +17,47 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // ---------------------------------------------------------------------------
-// The scan.  A tile is L = W * S consecutive tokens (in scan order: backwards
-// in the backward pass) of 32 * VEC channels; warp w of its block holds S of
-// the tokens in registers, a lane VEC channels.  Tiles of one run of tokens
-// and one group of channels form a chain.  A block
-//   1. loads its tile (each input element is read once),
+// The scan.  A tile is kTile = W * S consecutive tokens (in scan order:
+// backwards in the backward pass) of CH = 64 channels; warp w of its block
+// holds S of the tokens, a lane two of the channels.  All tiles of one run of
+// tokens (a batch entry, or all packed tokens) and one group of channels form
+// a chain.  A chain is walked by the G blocks of a team, which take every
+// G-th tile each, in order; a block
+//   1. waits for its tile's inputs, which were copied into shared memory
+//      while it worked on the tile before (two stages), takes them into
+//      registers and hands the stage over to the copy of a later tile,
 //   2. reduces each warp's S steps to the affine map c -> P c + H of the
-//      state, and the warps' maps to the tile's,
-//   3. publishes the map, and finds the state before the tile: it polls the W
-//      tiles before it (a warp each) until one has published its last state
-//      and all between that one and this have published their maps,
-//   4. publishes its own last state, and runs its steps again from the
-//      now known state, writing the outputs.
-// The state before a tile is always formed as P_{k-1} c_{k-1} + H_{k-1} from
-// left to right, wherever the nearest published state was found, so the
-// result has the same bits on every run.  Blocks take their tile from a
-// counter, in token order, so that a block only waits for blocks that run
-// already.
+//      state, and the warps' maps to the tile's map,
+//   3. publishes the tile's map in global memory and collects those of the
+//      G - 1 other tiles of this step (G > 1 only),
+//   4. applies the maps before its own tokens to the state before the step's
+//      first tile, and all G to carry that state on: every block of the team
+//      carries it by itself, so that no state is handed from block to block
+//      and a step costs one exchange, not G,
+//   5. runs its steps again from the now known state and writes the outputs.
+// Every input element is read from HBM once.  Maps are applied in token
+// order, so the result has the same bits on every run.  The blocks of a team
+// wait for one another: they are launched together (cooperative launch), and
+// every wait is bounded.
 //
 // A state that a sequence starts from replaces c (it is not multiplied by
-// zero), so nothing of one packed sequence, not even a NaN, reaches the next.
+// zero), so nothing of one packed sequence, not even a NaN, reaches the next:
+// a map that does not depend on the state before it has P = -0, which no
+// product of decays is.
 
-// Workspace of the scan: the tile counter, then per tile and channel the map
-// (P, H) and the last state.  Everything starts as all ones, which no
-// published value is (see `publishable`).
+constexpr int W = 8;             // warps of a block
+constexpr int S = 8;             // tokens of a warp
+constexpr int kTile = W * S;
+constexpr int CH = 64;           // channels of a tile
+constexpr int kThreads = 32 * W;
+constexpr int kMaxTeam = 32;     // blocks of a team
+constexpr int kMaxBlocks = 1024; // blocks that walk chains at the same time
+
 struct ScanPlan {
-    int tiles, groups, chains;   // tiles of a chain; channel groups; chains
-    unsigned int* counter;
-    unsigned long long* map;
-    unsigned int* last;
+    int tiles, groups;           // tiles of a chain; channel groups
+    int rounds;                  // chains that each block walks alone, then
+    int rest, team;              // `rest` chains walked by a team each
+    uint2* map;                  // [rest][tiles][CH] (P, H); all ones: none
 };
 
 constexpr unsigned int kEmpty = 0xffffffffu;
@@ -50,49 +65,172 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_fault_glr = 0;
 
-// The bits of x; a NaN with all bits set becomes another NaN.
-__device__ __forceinline__ unsigned int publishable(float x) {
-    const unsigned int b = __float_as_uint(x);
-    return b == kEmpty ? 0x7fffffffu : b;
+// Arithmetic on a lane's two channels at once (one instruction each).
+__device__ __forceinline__ uint64_t bits(float2 x) {
+    return (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+}
+__device__ __forceinline__ float2 floats(uint64_t b) {
+    return make_float2(__uint_as_float((unsigned int)b),
+                       __uint_as_float((unsigned int)(b >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return floats(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return floats(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return floats(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// exp of two log decays.  Near 0, where a state remembers 1 / -l tokens and
+// a decay's error is multiplied by as much, the Taylor polynomial of degree
+// 5 rounds correctly nearly always (|l| <= 1/8: at most 0.73 units of 2^-24
+// measured, mean 0; expf: 1.8, mean up to 0.26).  Elsewhere 2^(l log2 e) by
+// the hardware's approximation (2.6 units at l = -1, 8 at l = -8).
+__device__ __forceinline__ float2 decay(float2 l) {
+    float2 p = fma2(l, both(1.f / 120), both(1.f / 24));
+    p = fma2(l, p, both(1.f / 6));
+    p = fma2(l, p, both(0.5f));
+    p = fma2(l, p, both(1.f));
+    p = fma2(l, p, both(1.f));
+    const float2 t = mul2(l, both(1.44269504f));
+    const float ex = tc::ex2(t.x), ey = tc::ex2(t.y);
+    return make_float2(fabsf(l.x) <= 0.125f ? p.x : ex,
+                       fabsf(l.y) <= 0.125f ? p.y : ey);
 }
 
-__device__ __forceinline__ void st_relaxed(unsigned long long* p,
-                                           unsigned long long v) {
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v)
-                 : "memory");
+// Maps of two channels as (P.x, P.y, H.x, H.y).
+__device__ __forceinline__ bool fresh(float P) {
+    return __float_as_uint(P) == 0x80000000u;
 }
-__device__ __forceinline__ void st_relaxed(unsigned int* p, unsigned int v) {
-    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v)
-                 : "memory");
-}
-__device__ __forceinline__ unsigned long long ld_relaxed(
-    const unsigned long long* p) {
-    unsigned long long v;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];"
-                 : "=l"(v)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ unsigned int ld_relaxed(const unsigned int* p) {
-    unsigned int v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];"
-                 : "=r"(v)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
-// P c + H; a zero state stays zero however large P grew.
+// A zero state stays zero however large P grew.
 __device__ __forceinline__ float apply(float P, float H, float c) {
-    return c == 0.f ? H : fmaf(P, c, H);
+    return c == 0.f || fresh(P) ? H : fmaf(P, c, H);
+}
+__device__ __forceinline__ float2 apply(float4 m, float2 c) {
+    return make_float2(apply(m.x, m.z, c.x), apply(m.y, m.w, c.y));
+}
+// The map of `first`, then `then`.
+__device__ __forceinline__ float4 compose(float4 first, float4 then) {
+    const float2 h = apply(then, make_float2(first.z, first.w));
+    return make_float4(fresh(then.x) ? then.x : first.x * then.x,
+                       fresh(then.y) ? then.y : first.y * then.y, h.x, h.y);
 }
 
-// VEC adjacent elements as they lie in memory.
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
+// A published map is one 64-bit memory operation per channel, so a reader
+// sees it whole or not at all; a NaN with all bits set becomes another NaN.
+__device__ __forceinline__ uint64_t map_bits(float P, float H) {
+    const unsigned int h = __float_as_uint(H);
+    return (uint64_t)(h == kEmpty ? 0x7fffffffu : h) << 32 |
+           __float_as_uint(P);
+}
+__device__ __forceinline__ void publish(uint2* p, float4 m) {
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p),
+                 "l"(map_bits(m.x, m.z)), "l"(map_bits(m.y, m.w))
+                 : "memory");
+}
+__device__ __forceinline__ bool collect(const uint2* p, float4& m) {
+    uint64_t a, b;
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                 : "=l"(a), "=l"(b)
+                 : "l"(p)
+                 : "memory");
+    const float2 u = floats(a), v = floats(b);
+    m = make_float4(u.x, v.x, u.y, v.y);
+    return a != ~0ull && b != ~0ull;
+}
+
+// How the inputs' rows line up: on 16 bytes, so that whole tiles can be
+// copied (TMA); on pairs of channels; on elements only.
+enum Align { kWide, kPair, kElement };
+
+// The two channels of a lane: adjacent where pairs are aligned, else 32
+// apart, so that a warp's single elements are adjacent.
+template <Align A>
+__device__ __forceinline__ int channel(int lane, int v) {
+    return A == kElement ? lane + 32 * v : 2 * lane + v;
+}
+
+// Two channels as they lie in memory.
+template <typename T>
+struct alignas(2 * sizeof(T)) Two {
+    T x, y;
 };
+__device__ __forceinline__ float2 values(Two<float> t) {
+    return make_float2(t.x, t.y);
+}
+__device__ __forceinline__ float2 values(Two<bf16> t) {
+    return make_float2(__bfloat162float(t.x), __bfloat162float(t.y));
+}
+
+template <Align A, typename T>
+__device__ __forceinline__ Two<T> read2(const T* row, int lane) {
+    if constexpr (A == kElement) return {row[lane], row[lane + 32]};
+    else return reinterpret_cast<const Two<T>*>(row)[lane];
+}
+
+// To the lane's channels of an output row (`row`: the lane's own place).
+template <Align A, typename T>
+__device__ __forceinline__ void write2(T* row, bool l0, bool l1, float2 c) {
+    if constexpr (A == kElement) {
+        if (l0) row[0] = from_f32<T>(c.x);
+        if (l1) row[32] = from_f32<T>(c.y);
+    } else if (l0) {
+        *reinterpret_cast<Two<T>*>(row) =
+            Two<T>{from_f32<T>(c.x), from_f32<T>(c.y)};
+    }
+}
+
+// Copies tokens t .. t + kTile - 1 (rows `stride` elements apart) of `room`
+// channels into dst [kTile][CH]; what lies outside the tokens 0 .. T - 1 or
+// the channels becomes zero.  Asynchronous where pairs or elements have 4
+// bytes at least; the caller commits.
+template <Align A, typename T>
+__device__ __forceinline__ void copy_tile(T* dst, const T* src,
+                                          long long stride, long long t,
+                                          int T_, int room) {
+    constexpr int E = A == kElement ? 1 : 2;     // elements of a copy
+    constexpr int BYTES = E * sizeof(T);
+    constexpr int PER = CH / E;                  // copies of a row
+    const int col = (threadIdx.x % PER) * E;
+#pragma unroll 4
+    for (int r = threadIdx.x / PER; r < kTile; r += kThreads / PER) {
+        const bool in = t + r >= 0 && t + r < T_ && col < room;
+        const T* from = in ? src + (t + r) * stride + col : src;
+        T* to = dst + r * CH + col;
+        if constexpr (BYTES >= 4) {
+            asm volatile(
+                "cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(
+                    tc::smem_u32(to)),
+                "l"(from), "r"(in ? BYTES : 0), "n"(BYTES)
+                : "memory");
+        } else {
+            *to = in ? *from : T(0.f);
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
+                                            uint64_t* bar, int c0, int c1,
+                                            int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::"
+        "complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)),
+        "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 
 // Where sequences begin and end among S tokens of one warp, and which.  In
 // scan order: bit i of `mask` says that a sequence begins at step i, which is
@@ -107,7 +245,7 @@ struct Bounds {
 // downwards with BACK).  A warp works together: a 32-way search for the
 // sequence of t, then 32 offsets at a time.  Any content of cu gives
 // 0 <= n < B.
-template <int S, bool BACK>
+template <bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
                                               long long t) {
     const int lane = threadIdx.x % 32;
@@ -138,312 +276,323 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
     return {mask, lo};
 }
 
-template <typename T, typename G, int VEC, int S, int W, bool BWD,
-          bool PACKED>
-__global__ void __launch_bounds__(32 * W)
-glr_scan_kernel(GlrArgs a, ScanPlan plan) {
-    constexpr int CH = 32 * VEC;
-    using PT = Pack<T, VEC>;
-    using PG = Pack<G, VEC>;
-    __shared__ float sP[W][CH], sH[W][CH];     // the warps' maps
-    __shared__ float vP[W][CH], vH[W][CH];     // the tiles before
-    __shared__ unsigned int s_ticket, s_begins[W];
-    __shared__ int s_seen[W];
-
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-    unsigned int ticket = blockIdx.x;
-    if (plan.tiles > 1) {
-        if (threadIdx.x == 0) s_ticket = atomicAdd(plan.counter, 1u) + 1u;
-        __syncthreads();
-        ticket = s_ticket;
-    }
-    const int k = ticket / plan.chains;        // tile of the chain
-    const int chain = ticket % plan.chains;
-    const int group = chain % plan.groups;
-    const int b = chain / plan.groups;         // 0 when packed
-    const int d = group * CH + lane * VEC;
-    const bool live = d < a.D;
-
-    // scan position p <-> token t
-    const long long p0 = (long long)k * (W * S) + w * S;
-    const long long t0 = BWD ? a.T - 1 - p0 : p0;
-    const int steps = (int)max(0ll, min((long long)S, a.T - p0));
-    constexpr int DT = BWD ? -1 : 1;
-
-    const T* xp = static_cast<const T*>(a.x.p) + b * a.x.sb + d;
-    const G* lp = static_cast<const G*>(a.la.p) + b * a.la.sb + d;
-    const T* gp = static_cast<const T*>(a.g.p) + b * a.g.sb + d;
-    PT rx[S];                    // forward: x; backward: o of the token before
-    PT rg[BWD ? S : 1];          // backward: o_grad
-    PG rl[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        rl[i] = PG{};
-        rx[i] = PT{};
-        if (BWD) rg[BWD ? i : 0] = PT{};
-        if (live && i < steps) {
-            const long long t = t0 + i * DT;
-            rl[i] = *reinterpret_cast<const PG*>(lp + t * a.la.st);
-            if (BWD) {
-                rg[BWD ? i : 0] =
-                    *reinterpret_cast<const PT*>(gp + t * a.g.st);
-                if (t > 0)
-                    rx[i] =
-                        *reinterpret_cast<const PT*>(xp + (t - 1) * a.x.st);
-            } else {
-                rx[i] = *reinterpret_cast<const PT*>(xp + t * a.x.st);
-            }
+// The tiles of a block, in its order.
+struct Cursor {
+    int round, chain, k, step;
+    __device__ Cursor(const ScanPlan& p) : round(-1) { open(p); }
+    __device__ void open(const ScanPlan& p) {    // the next chain
+        ++round;
+        k = 0;
+        step = 1;
+        const int b = blockIdx.x;
+        if (round < p.rounds) {
+            chain = round * (int)gridDim.x + b;
+        } else if (round == p.rounds && b < p.rest * p.team) {
+            chain = p.rounds * (int)gridDim.x + b / p.team;
+            k = b % p.team;
+            step = p.team;
+        } else {
+            chain = -1;                          // no more
         }
     }
-
-    Bounds bd{0u, b};
-    if (PACKED) {
-        if (steps > 0) bd = find_bounds<S, BWD>(a.cu, a.B, t0);
-    } else {
-        if (p0 == 0) bd.mask = 1u;
-        if (steps > 0 && a.T - p0 <= S) bd.mask |= 1u << (a.T - p0);
+    __device__ void move(const ScanPlan& p) {
+        if (chain < 0) return;
+        k += step;
+        if (k >= p.tiles) open(p);
     }
-    const unsigned int begins = bd.mask & ((1u << S) - 1);
+};
+
+template <typename T, typename G, bool BWD>
+struct Stage {
+    T x[kTile][CH];
+    G la[kTile][CH];
+};
+template <typename T, typename G>
+struct Stage<T, G, true> {
+    T x[kTile][CH];              // o of the token before
+    G la[kTile][CH];
+    T g[kTile][CH];              // o_grad
+};
+template <typename T, typename G, bool BWD>
+struct Shared {
+    Stage<T, G, BWD> stage[2];
+    float4 own[2][W][32];        // the warps' maps, of this tile and the next
+    uint64_t full[2];
+};
+
+// Shared memory of a block whose team collects `team` maps (1: none), and how
+// many such blocks an SM holds (228 KB, 1 KB of it per block the system's),
+// at most 4: 64 registers a thread.
+template <typename T, typename G, bool BWD>
+constexpr int shared_bytes(int team) {
+    return (int)sizeof(Shared<T, G, BWD>) + (team > 1 ? team * 512 : 0);
+}
+template <typename T, typename G, bool BWD>
+constexpr int resident(int team) {
+    return std::min(4, 228 * 1024 / (shared_bytes<T, G, BWD>(team) + 1024));
+}
+
+template <typename T, typename G, Align A, bool BWD>
+__global__ void __launch_bounds__(kThreads, (resident<T, G, BWD>(1)))
+glr_scan_kernel(const __grid_constant__ GlrArgs a,
+                const __grid_constant__ ScanPlan plan,
+                const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ CUtensorMap map_la,
+                const __grid_constant__ CUtensorMap map_g) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    auto& sh = *reinterpret_cast<Shared<T, G, BWD>*>(smem);
+    // the team's maps of this step
+    auto* team = reinterpret_cast<float4(*)[32]>(&sh + 1);
+    constexpr int DT = BWD ? -1 : 1;             // token step of the scan
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     const float* init = BWD ? a.dhT : a.h0;
 
-    // Moves n on to the sequence that begins at step i.
-    auto next = [&](int i, int& n) {
-        if (!PACKED || i == 0) return;
-        const long long t = t0 + i * DT;
-        if (BWD) {
-            n = max(n - 1, 0);
-            while (n > 0 && a.cu[n] > t) --n;
+    if (A == kWide) {
+        if (threadIdx.x == 0) {
+            tc::mbar_init(&sh.full[0], 1);
+            tc::mbar_init(&sh.full[1], 1);
+            tc::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    // Starts the copy of a tile's inputs into a stage: row r of it is token
+    // lo + r, lo the tile's lowest token.
+    auto fetch = [&](const Cursor& at, int s) {
+        Stage<T, G, BWD>& st = sh.stage[s];
+        if (at.chain >= 0 && (A != kWide || threadIdx.x == 0)) {
+            const int b = at.chain / plan.groups;
+            const int d = at.chain % plan.groups * CH;
+            const int p = at.k * kTile;
+            const int lo = BWD ? a.T - kTile - p : p;
+            if (A == kWide) {
+                tc::mbar_arrive_expect_tx(&sh.full[s], sizeof(st));
+                tma_load_3d(&st.la[0][0], &map_la, &sh.full[s], d, lo, b);
+                tma_load_3d(&st.x[0][0], &map_x, &sh.full[s], d,
+                            BWD ? lo - 1 : lo, b);
+                if constexpr (BWD)
+                    tma_load_3d(&st.g[0][0], &map_g, &sh.full[s], d, lo, b);
+            } else {
+                const int room = a.D - d;
+                copy_tile<A>(&st.la[0][0],
+                             static_cast<const G*>(a.la.p) + b * a.la.sb + d,
+                             a.la.st, lo, a.T, room);
+                copy_tile<A>(&st.x[0][0],
+                             static_cast<const T*>(a.x.p) + b * a.x.sb + d,
+                             a.x.st, BWD ? lo - 1ll : lo, a.T, room);
+                if constexpr (BWD)
+                    copy_tile<A>(&st.g[0][0],
+                                 static_cast<const T*>(a.g.p) + b * a.g.sb +
+                                     d,
+                                 a.g.st, lo, a.T, room);
+            }
+        }
+        if (A != kWide) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    Cursor here(plan), ahead = here;
+    fetch(ahead, 0);
+    ahead.move(plan);
+    fetch(ahead, 1);
+
+    float2 carry = both(0.f);        // the state before the team's tiles
+    bool fault = false;
+    unsigned int turn = 0, issued = 2;           // copies started
+    for (; here.chain >= 0; ++turn) {
+        const int s = turn & 1;
+        const Stage<T, G, BWD>& st = sh.stage[s];
+        const int b = a.cu ? 0 : here.chain / plan.groups;
+        const int d0 = here.chain % plan.groups * CH;
+        const int da = d0 + channel<A>(lane, 0), db = d0 + channel<A>(lane, 1);
+        const bool la = da < a.D, lb = db < a.D;
+        // scan position p <-> token t
+        const int p0 = here.k * kTile + w * S;
+        const int t0 = BWD ? a.T - 1 - p0 : p0;
+        const int steps = max(0, min(S, a.T - p0));
+        if (here.k < here.step) carry = both(0.f);       // a chain begins
+
+        Bounds bd{0u, b};
+        if (a.cu) {
+            if (steps > 0) bd = find_bounds<BWD>(a.cu, a.B, t0);
         } else {
-            n = min(n + 1, a.B - 1);
-            while (n < a.B - 1 && a.cu[n + 1] <= t) ++n;
+            if (p0 == 0) bd.mask = 1u;
+            if (steps > 0 && a.T - p0 <= S) bd.mask |= 1u << (a.T - p0);
         }
-    };
-    auto start_of = [&](int n, float (&c)[VEC]) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-            c[v] = init && live ? init[(size_t)n * a.D + d + v] : 0.f;
-    };
+        const unsigned int begins = bd.mask & ((1u << S) - 1);
+        // nothing begins, ends or is missing here
+        const bool plain = bd.mask == 0 && steps == S;
 
-    float al[S][VEC];            // alpha
-    float P[VEC], H[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        P[v] = 1.f;
-        H[v] = 0.f;
-    }
-    int n = bd.n;
-    // the start of the last sequence that begins here: whoever ends it may
-    // write its last state in the place of this start (hT == h0) before the
-    // second pass
-    float kept[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) kept[v] = 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        if (begins >> i & 1) {
-            next(i, n);
-            start_of(n, kept);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) H[v] = kept[v];
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            al[i][v] = expf(to_f32(rl[i].v[v]));
-            P[v] *= al[i][v];
-            H[v] = BWD ? al[i][v] * (H[v] + to_f32(rg[BWD ? i : 0].v[v]))
-                       : fmaf(al[i][v], H[v], to_f32(rx[i].v[v]));
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        sP[w][lane * VEC + v] = P[v];
-        sH[w][lane * VEC + v] = H[v];
-    }
-    if (lane == 0) s_begins[w] = begins;
-    __syncthreads();
-
-    // the tile's map, and whether its last state is known already
-    bool known = (s_begins[0] & 1) || k == 0;
-    const bool wait = !known;
-    const size_t at = ((size_t)chain * plan.tiles + k) * CH + lane * VEC;
-    const bool share = plan.tiles > 1 && k + 1 < plan.tiles;
-    if (w == 0 && plan.tiles > 1) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            P[v] = 1.f;
-            H[v] = 0.f;
-        }
-        for (int u = 0; u < W; ++u) {
-            const bool fresh = s_begins[u] != 0;
-            known |= fresh;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float pu = sP[u][lane * VEC + v];
-                const float hu = sH[u][lane * VEC + v];
-                H[v] = fresh ? hu : apply(pu, hu, H[v]);
-                P[v] *= pu;
+        // Moves n on to the sequence that begins at step i.
+        auto next = [&](int i, int& n) {
+            if (!a.cu || i == 0) return;
+            const int t = t0 + i * DT;
+            if (BWD) {
+                n = max(n - 1, 0);
+                while (n > 0 && a.cu[n] > t) --n;
+            } else {
+                n = min(n + 1, a.B - 1);
+                while (n < a.B - 1 && a.cu[n + 1] <= t) ++n;
             }
-        }
-        if (share) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if (known)
-                    st_relaxed(plan.last + at + v, publishable(H[v]));
-                else
-                    st_relaxed(plan.map + at + v,
-                               (unsigned long long)publishable(H[v]) << 32 |
-                                   publishable(P[v]));
-            }
-        }
-    }
+        };
+        auto state_of = [&](const float* p, int n) {
+            float2 c = both(0.f);
+            if (p && la) c.x = p[(size_t)n * a.D + da];
+            if (p && lb) c.y = p[(size_t)n * a.D + db];
+            return c;
+        };
+        auto keep_state = [&](int n, float2 c) {
+            if (a.hT && la) a.hT[(size_t)n * a.D + da] = c.x;
+            if (a.hT && lb) a.hT[(size_t)n * a.D + db] = c.y;
+        };
 
-    // the state before the tile
-    float c[VEC];
+        if (A == kWide)
+            fault |= !tc::mbar_wait(&sh.full[s], (turn >> 1) & 1);
+        else
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (A != kWide) __syncthreads();
+
+        float2 al[S];                // decays
+        Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
+        float2 P = both(1.f), H = both(0.f);
+        // the start of the last sequence that begins here: whoever ends it
+        // may write its last state in the place of this start (hT == h0)
+        // before the second pass
+        float2 kept = both(0.f);
+        int n = bd.n;
+        auto reduce = [&](auto events) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) c[v] = 0.f;
-    if (wait) {                  // the same in all threads
-        int seen = 0;            // 1: the map, 2: the last state
-        const size_t from = at - (size_t)(w + 1) * CH;
-        const uint64_t begun = tc::globaltimer_ns();
-        int r;
-        while (true) {
-            if (k - 1 - w >= 0 && seen < 2) {
-                bool got = true;
-                float h[VEC], q[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const unsigned int x = ld_relaxed(plan.last + from + v);
-                    h[v] = __uint_as_float(x);
-                    q[v] = 0.f;
-                    got &= x != kEmpty;
+            for (int i = 0; i < S; ++i) {
+                if (decltype(events)::value && begins >> i & 1) {
+                    next(i, n);
+                    kept = H = state_of(init, n);
+                    P = both(-0.f);
                 }
-                if (__all_sync(0xffffffffu, got)) {
-                    seen = 2;
-                } else if (seen == 0) {
-                    got = true;
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const unsigned long long x =
-                            ld_relaxed(plan.map + from + v);
-                        q[v] = __uint_as_float((unsigned int)x);
-                        h[v] = __uint_as_float((unsigned int)(x >> 32));
-                        got &= x != ~0ull;
-                    }
-                    if (__all_sync(0xffffffffu, got)) seen = 1;
-                    else got = false;
+                const int r = BWD ? kTile - 1 - (w * S + i) : w * S + i;
+                al[i] = decay(values(read2<A>(st.la[r], lane)));
+                x[i] = read2<A>(st.x[r], lane);
+                P = mul2(P, al[i]);
+                if constexpr (BWD) {
+                    g[i] = read2<A>(st.g[r], lane);
+                    H = mul2(al[i], add2(H, values(g[i])));
                 } else {
-                    got = false;
-                }
-                if (__all_sync(0xffffffffu, got)) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        vP[w][lane * VEC + v] = q[v];
-                        vH[w][lane * VEC + v] = h[v];
-                    }
+                    H = fma2(al[i], H, values(x[i]));
                 }
             }
-            if (lane == 0) s_seen[w] = seen;
-            const bool late = tc::globaltimer_ns() - begun > kWaitLimitNs;
-            if (__syncthreads_or(late)) {
-                r = -1;
+        };
+        if (plain) reduce(std::false_type());
+        else reduce(std::true_type());
+        sh.own[s][w][lane] = make_float4(P.x, P.y, H.x, H.y);
+        // the stage is free, the maps are there
+        if (__syncthreads_or(fault)) {
+            fault = true;
+            break;
+        }
+        ahead.move(plan);
+        fetch(ahead, s);
+        ++issued;
+
+        float2 c = carry;            // the state before the tile
+        if (here.step > 1) {
+            const int G_ = here.step, m = here.k % G_;
+            // in the last step of the chain only those before
+            const int want = here.k + G_ < plan.tiles ? G_ : m;
+            const size_t at =
+                ((size_t)(here.chain - plan.rounds * (int)gridDim.x) *
+                     plan.tiles + (here.k - m)) * CH + 2 * lane;
+            if (w == 0) {
+                float4 t = sh.own[s][0][lane];
+#pragma unroll
+                for (int u = 1; u < W; ++u)
+                    t = compose(t, sh.own[s][u][lane]);
+                if (here.k + 1 < plan.tiles)
+                    publish(plan.map + at + (size_t)m * CH, t);
+                team[m][lane] = t;
+            }
+            // the others' maps: a warp takes every W-th, from the last warp
+            for (int j = W - 1 - w; j < want; j += W) {
+                if (j == m) continue;
+                float4 t;
+                uint64_t begun = 0;
+                while (!__all_sync(0xffffffffu,
+                                   collect(plan.map + at + (size_t)j * CH,
+                                           t))) {
+                    const uint64_t now = tc::globaltimer_ns();
+                    if (begun == 0) begun = now;
+                    if (__any_sync(0xffffffffu, now > begun + kWaitLimitNs)) {
+                        fault = true;
+                        break;
+                    }
+                }
+                if (fault) break;
+                team[j][lane] = t;
+            }
+            if (__syncthreads_or(fault)) {
+                fault = true;
                 break;
             }
-            r = 0;
-            while (r < W && s_seen[r] == 1) ++r;
-            if (r < W && s_seen[r] == 2) break;
-            __syncthreads();
+            for (int j = 0; j < m; ++j) c = apply(team[j][lane], c);
+            carry = c;
+            for (int j = m; j < want; ++j) carry = apply(team[j][lane], carry);
         }
-        if (r < 0) {             // gave up: the tiles after this one go on
-            if (threadIdx.x == 0) atomicOr(&g_fault_glr, 1u);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) c[v] = __uint_as_float(0x7fffffffu);
-        } else {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) c[v] = vH[r][lane * VEC + v];
-            for (int u = r - 1; u >= 0; --u)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    c[v] = apply(vP[u][lane * VEC + v],
-                                 vH[u][lane * VEC + v], c[v]);
+        for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
+        if (here.step == 1) {
+            carry = c;
+            for (int u = w; u < W; ++u)
+                carry = apply(sh.own[s][u][lane], carry);
         }
-        if (w == 0 && share && !known) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                st_relaxed(plan.last + at + v,
-                           publishable(apply(P[v], H[v], c[v])));
-        }
-    }
-    // and before this warp's tokens
-    for (int u = 0; u < w; ++u) {
-        const bool fresh = s_begins[u] != 0;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float hu = sH[u][lane * VEC + v];
-            c[v] = fresh ? hu : apply(sP[u][lane * VEC + v], hu, c[v]);
-        }
-    }
 
-    if (live && steps > 0) {
-        const size_t out = (PACKED ? 0 : (size_t)b * a.T * a.D) + d;
+        const size_t out = ((size_t)b * a.T + t0) * a.D + da;
         T* op = static_cast<T*>(a.o) + out;
         G* dp = static_cast<G*>(a.dla) + out;
         n = bd.n;
+        auto write = [&](auto events) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            if (i < steps) {
-                const long long t = t0 + i * DT;
-                if (begins >> i & 1) {
-                    next(i, n);
-                    if (begins >> (i + 1)) {
-                        start_of(n, c);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) c[v] = kept[v];
+            for (int i = 0; i < S; ++i) {
+                if (decltype(events)::value) {
+                    if (i >= steps) break;
+                    if (begins >> i & 1) {
+                        next(i, n);
+                        c = begins >> (i + 1) ? state_of(init, n) : kept;
                     }
                 }
-                const bool ends = bd.mask >> (i + 1) & 1;
-                PT ro;
-                if (BWD) {
-                    PG rd;
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const float g =
-                            to_f32(rg[BWD ? i : 0].v[v]) + c[v];
-                        ro.v[v] = from_f32<T>(g);
-                        c[v] = al[i][v] * g;
-                        float h = to_f32(rx[i].v[v]);
-                        if (ends)
-                            h = a.h0 ? a.h0[(size_t)n * a.D + d + v] : 0.f;
-                        rd.v[v] = from_f32<G>(c[v] * h);
-                    }
-                    *reinterpret_cast<PG*>(dp + t * a.D) = rd;
+                const bool ends =
+                    decltype(events)::value && (bd.mask >> (i + 1) & 1);
+                if constexpr (BWD) {
+                    float2 h = values(x[i]);
+                    if (ends) h = state_of(a.h0, n);
+                    c = add2(c, values(g[i]));
+                    write2<A>(op, la, lb, c);
+                    c = mul2(al[i], c);
+                    write2<A>(dp, la, lb, mul2(c, h));
+                    dp -= a.D;
+                    op -= a.D;
                 } else {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        c[v] = fmaf(al[i][v], c[v], to_f32(rx[i].v[v]));
-                        ro.v[v] = from_f32<T>(c[v]);
-                    }
+                    c = fma2(al[i], c, values(x[i]));
+                    write2<A>(op, la, lb, c);
+                    op += a.D;
                 }
-                *reinterpret_cast<PT*>(op + t * a.D) = ro;
-                if (ends && a.hT) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v)
-                        a.hT[(size_t)n * a.D + d + v] = c[v];
-                }
+                if (ends) keep_state(n, c);
             }
-        }
-    }
+        };
+        if (plain) write(std::false_type());
+        else write(std::true_type());
 
-    // empty sequences, shared out over the tiles
-    if (PACKED && a.hT && a.hT != init && live) {
-        for (long long e = (long long)k * W + w; e < a.B;
-             e += (long long)plan.tiles * W)
-            if (a.cu[e] == a.cu[e + 1])
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    a.hT[e * a.D + d + v] =
-                        init ? init[e * a.D + d + v] : 0.f;
+        // empty sequences, shared out over the tiles
+        if (a.cu && a.hT && a.hT != init) {
+            for (long long e = (long long)here.k * W + w; e < a.B;
+                 e += (long long)plan.tiles * W)
+                if (a.cu[e] == a.cu[e + 1])
+                    keep_state((int)e, state_of(init, (int)e));
+        }
+        here.move(plan);
     }
+    if (A != kWide) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (fault && threadIdx.x == 0) {
+        atomicOr(&g_fault_glr, 1u);
+        // copies that may be on their way yet
+        for (++turn; A == kWide && turn < issued; ++turn)
+            tc::mbar_wait(&sh.full[turn & 1], (turn >> 1) & 1, 1000000);
+    }
+    if (fault) __syncthreads();
 }
 
 template <typename T, typename G>
@@ -476,75 +625,117 @@ cudaError_t by_type(kla_dtype t, kla_dtype g, F f) {
 
 namespace {
 
-// Steps of a warp and warps of a block, by the bytes of one step.
-constexpr int kWarps = 8;
-template <typename T, typename G>
-constexpr int steps_of() {
-    return 8;
+long long chains_of(int B, int D, bool packed) {
+    return (long long)((D + CH - 1) / CH) * (packed ? 1 : B);
 }
-constexpr int kTile = kWarps * 8;
 
-template <int VEC>
-ScanPlan plan_of(int B, int T, int D, bool packed, void* ws) {
+// How `chains` chains of `tiles` tiles share the blocks that the SMs hold:
+// whole rounds of a chain per block, then the rest by teams as large as fit.
+template <typename T, typename G, bool BWD>
+ScanPlan plan_of(long long chains, int tiles, int D, void* ws, int* blocks) {
     ScanPlan p;
-    p.tiles = (T + kTile - 1) / kTile;
-    p.groups = (D + 32 * VEC - 1) / (32 * VEC);
-    p.chains = p.groups * (packed ? 1 : B);
-    const size_t n = (size_t)p.tiles * p.chains * 32 * VEC;
-    p.counter = static_cast<unsigned int*>(ws);
-    p.map = reinterpret_cast<unsigned long long*>(p.counter + 4);
-    p.last = reinterpret_cast<unsigned int*>(p.map + n);
+    p.tiles = tiles;
+    p.groups = (D + CH - 1) / CH;
+    p.map = static_cast<uint2*>(ws);
+    for (int per = resident<T, G, BWD>(1); per > 0; --per) {
+        const int slots = std::min(per * device_sm_count(), kMaxBlocks);
+        if (slots <= 0) break;
+        p.rounds = (int)(chains / slots);
+        p.rest = (int)(chains % slots);
+        p.team = 1;
+        if (p.rest)
+            p.team = std::max(
+                1, std::min({slots / p.rest, kMaxTeam, tiles}));
+        *blocks = p.rounds ? slots : p.rest * p.team;
+        // the maps of a large team may take the room of a block
+        if (resident<T, G, BWD>(p.team) >= per) return p;
+    }
+    *blocks = 0;
     return p;
 }
 
-template <int VEC>
-size_t plan_bytes(int B, int T, int D, bool packed) {
-    const ScanPlan p = plan_of<VEC>(B, T, D, packed, nullptr);
-    return p.tiles <= 1 ? 0
-                        : 16 + (size_t)p.tiles * p.chains * 32 * VEC * 12;
+// The element's tensor map over [B, T, D] with boxes of kTile tokens x CH
+// channels (zeros outside).
+template <typename T>
+bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a) {
+    const bool packed = a.cu != nullptr;
+    cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.T,
+                          (cuuint64_t)(packed ? 1 : a.B)};
+    // a stride that no row is taken with still has to be a valid one
+    const cuuint64_t row = ((cuuint64_t)a.D * sizeof(T) + 15) / 16 * 16;
+    cuuint64_t strides[2] = {
+        a.T > 1 ? (cuuint64_t)x.st * sizeof(T) : row,
+        !packed && a.B > 1 ? (cuuint64_t)x.sb * sizeof(T) : row * a.T};
+    cuuint32_t box[3] = {CH, kTile, 1}, es[3] = {1, 1, 1};
+    return tile_map_encoder()(
+               m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+               3, const_cast<void*>(x.p), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether VEC adjacent channels of a strided input can be read at once.
-bool packs(const Strided& x, size_t elt, int vec, bool batched) {
-    return reinterpret_cast<uintptr_t>(x.p) % (elt * vec) == 0 &&
-           x.st % vec == 0 && (!batched || x.sb % vec == 0);
-}
-bool packs(const void* p, size_t elt, int vec) {
-    return reinterpret_cast<uintptr_t>(p) % (elt * vec) == 0;
-}
-
-template <typename T, typename G, int VEC, bool BWD, bool PACKED>
+template <typename T, typename G, Align A, bool BWD>
 cudaError_t launch_scan(const GlrArgs& a, void* ws, cudaStream_t s) {
-    const ScanPlan p = plan_of<VEC>(a.B, a.T, a.D, PACKED, ws);
-    const long long blocks = (long long)p.tiles * p.chains;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (p.tiles > 1) {
-        const cudaError_t e = cudaMemsetAsync(
-            ws, 0xff, plan_bytes<VEC>(a.B, a.T, a.D, PACKED), s);
+    const long long chains = chains_of(a.B, a.D, a.cu != nullptr);
+    const int tiles = (a.T + kTile - 1) / kTile;
+    if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
+    int blocks = 0;
+    const ScanPlan p = plan_of<T, G, BWD>(chains, tiles, a.D, ws, &blocks);
+    if (blocks <= 0) return cudaErrorInvalidValue;
+    CUtensorMap mx{}, ml{}, mg{};
+    if (A == kWide &&
+        (!make_tile_map<T>(&mx, a.x, a) || !make_tile_map<G>(&ml, a.la, a) ||
+         (BWD && !make_tile_map<T>(&mg, a.g, a))))
+        return cudaErrorInvalidValue;
+    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
+    cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        shared_bytes<T, G, BWD>(kMaxTeam));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared_bytes<T, G, BWD>(p.team);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.team > 1 ? 1 : 0;
+    if (p.team > 1) {
+        e = cudaMemsetAsync(ws, 0xff, (size_t)p.rest * tiles * CH * 8, s);
         if (e != cudaSuccess) return e;
     }
-    glr_scan_kernel<T, G, VEC, steps_of<T, G>(), kWarps, BWD, PACKED>
-        <<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, p);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, a, p, mx, ml, mg);
 }
 
-template <typename T, typename G, int VEC>
-cudaError_t launch_vec(const GlrArgs& a, bool bwd, void* ws, cudaStream_t s) {
-    if (a.cu)
-        return bwd ? launch_scan<T, G, VEC, true, true>(a, ws, s)
-                   : launch_scan<T, G, VEC, false, true>(a, ws, s);
-    return bwd ? launch_scan<T, G, VEC, true, false>(a, ws, s)
-               : launch_scan<T, G, VEC, false, false>(a, ws, s);
+// Whether all rows of a strided input start on a multiple of `bytes`.
+bool lines_up(const Strided& x, const GlrArgs& a, size_t elt, size_t bytes) {
+    return reinterpret_cast<uintptr_t>(x.p) % bytes == 0 &&
+           (a.T == 1 || x.st * elt % bytes == 0) &&
+           (a.cu || a.B == 1 || x.sb * elt % bytes == 0);
+}
+// Whether a tensor map can describe it: no repeated rows.
+bool maps(const Strided& x, const GlrArgs& a) {
+    return (a.T == 1 || x.st > 0) && (a.cu || a.B == 1 || x.sb > 0);
+}
+
+template <typename T, typename G, Align A>
+cudaError_t launch_way(const GlrArgs& a, bool bwd, void* ws, cudaStream_t s) {
+    return bwd ? launch_scan<T, G, A, true>(a, ws, s)
+               : launch_scan<T, G, A, false>(a, ws, s);
 }
 
 }  // namespace
 
 size_t glr_workspace_bytes(int B, int T, int D, bool packed, kla_dtype,
                            kla_dtype) {
-    if (B <= 0) return 0;
-    const size_t n1 = plan_bytes<1>(B, T, D, packed);
-    const size_t n2 = plan_bytes<2>(B, T, D, packed);
-    return n1 > n2 ? n1 : n2;
+    if (B <= 0 || T <= kTile) return 0;
+    const long long tiles = (T + kTile - 1) / kTile;
+    return std::min<long long>(chains_of(B, D, packed), kMaxBlocks) * tiles *
+           CH * 8;
 }
 
 cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
@@ -560,13 +751,22 @@ cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
     return by_type(a.dtype, a.gdtype, [&](auto t, auto g) {
         using T = decltype(t);
         using G = decltype(g);
-        const bool batched = !a.cu && a.B > 1;
-        const bool two = a.D % 2 == 0 && packs(a.x, sizeof(T), 2, batched) &&
-                         packs(a.la, sizeof(G), 2, batched) &&
-                         packs(a.g, sizeof(T), 2, batched) &&
-                         packs(a.o, sizeof(T), 2) && packs(a.dla, sizeof(G), 2);
-        return two ? launch_vec<T, G, 2>(a, bwd, workspace, stream)
-                   : launch_vec<T, G, 1>(a, bwd, workspace, stream);
+        auto in = [&](size_t tb, size_t gb) {
+            return lines_up(a.x, a, sizeof(T), tb) &&
+                   lines_up(a.la, a, sizeof(G), gb) &&
+                   (!bwd || lines_up(a.g, a, sizeof(T), tb));
+        };
+        // pairs: the outputs' rows (of D) too
+        const bool pairs =
+            a.D % 2 == 0 && in(2 * sizeof(T), 2 * sizeof(G)) &&
+            reinterpret_cast<uintptr_t>(a.o) % (2 * sizeof(T)) == 0 &&
+            reinterpret_cast<uintptr_t>(a.dla) % (2 * sizeof(G)) == 0;
+        const bool wide = pairs && in(16, 16) && maps(a.x, a) &&
+                          maps(a.la, a) && (!bwd || maps(a.g, a)) &&
+                          get_encoder();
+        return wide    ? launch_way<T, G, kWide>(a, bwd, workspace, stream)
+               : pairs ? launch_way<T, G, kPair>(a, bwd, workspace, stream)
+                       : launch_way<T, G, kElement>(a, bwd, workspace, stream);
     });
 }
 

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
 #include <cstdint>
 
 #include "kla.h"
@@ -248,6 +249,8 @@ int device_sm_count();
 
 // cuTensorMapEncodeTiled from the driver (looked up once); false if absent.
 bool get_encoder();
+// The function itself (after get_encoder() has returned true).
+PFN_cuTensorMapEncodeTiled_v12000 tile_map_encoder();
 // Tensor map of a [B, T, H, 128] bf16 tensor with 128-byte swizzle and boxes
 // of 64 features x 1 head x 64 tokens x 1 batch (zero fill out of range).
 bool make_map(CUtensorMap* m, const void* base, int B, int T, int H);

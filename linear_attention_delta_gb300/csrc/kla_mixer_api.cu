@@ -126,6 +126,9 @@ extern "C" kla_status kla_glr_workspace_size(int B, int T, int D, int packed,
 
 namespace {
 
+// Token positions are counted in 32 bits, with room for a partial tile.
+constexpr int kMaxTokens = 0x7fffffff - 4096;
+
 // Bytes spanned by a strided [B, T, D] input of the recurrence.
 size_t span_bytes(const kla::GlrArgs& a, const kla::Strided& x, size_t elt) {
     const long long t = a.T ? (long long)(a.T - 1) * x.st : 0;
@@ -142,6 +145,7 @@ kla_status glr_impl(kla::GlrArgs& a, bool bwd, void* workspace,
     if (!ok_or_null(a.h0, 4) || !ok_or_null(a.dhT, 4) ||
         !ok_or_null(a.hT, 4) || !ok_or_null(a.cu, 4))
         return KLA_ERR_INVALID_ARG;
+    if (a.T > kMaxTokens) return KLA_ERR_UNSUPPORTED_SHAPE;
     // packed tokens belong to some sequence
     if (a.B == 0) return a.cu && a.T > 0 ? KLA_ERR_INVALID_ARG : KLA_OK;
     const size_t e = size_of(a.dtype), ge = size_of(a.gdtype);

@@ -341,6 +341,26 @@ def test_long_sequence_with_long_memory():
     check_bwd(o, la, x)
 
 
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("D", [64, 66, 131, 1024])
+def test_few_channels_and_many_tokens(D, dtype, gtype):
+    """Few channels for the whole GPU: many blocks share a run of tokens."""
+    T = 20000
+    x, la = normal((1, T, D), dtype, 48), gates((1, T, D), gtype, 49)
+    h0 = normal((1, D), F32, 50)
+    o, _ = check_fwd(x, la, h0)
+    check_bwd(o, la, x, h0, h0)
+
+
+@pytest.mark.parametrize("B,T,D", [(500, 70, 64), (30, 130, 2048),
+                                   (700, 66, 70)])
+def test_more_channels_than_blocks(B, T, D):
+    x, la = normal((B, T, D), BF16, 51), gates((B, T, D), F32, 52)
+    h0 = normal((B, D), F32, 53)
+    o, _ = check_fwd(x, la, h0)
+    check_bwd(o, la, x, h0, h0)
+
+
 def test_two_streams_at_once():
     """Calls that overlap on two streams, each with its own workspace."""
     x, la = normal((1, 30000, 256), BF16, 38), gates((1, 30000, 256), F32, 39)
