@@ -45,8 +45,8 @@ using bf16 = __nv_bfloat16;
 // a map that does not depend on the state before it has P = -0, which no
 // product of decays is.
 
-constexpr int W = 8;             // warps of a block
-constexpr int S = 8;             // tokens of a warp
+constexpr int W = 4;             // warps of a block
+constexpr int S = 16;            // tokens of a warp
 constexpr int kTile = W * S;
 constexpr int CH = 64;           // channels of a tile
 constexpr int kThreads = 32 * W;
