@@ -655,23 +655,17 @@ KLA_API kla_status kla_layernorm_bwd(
  * values are computed as written.  h0 null: zeros; hT null: not written; hT
  * may be h0 itself (else it may not overlap any input).  The hT of an empty
  * sequence is its h0.
- * workspace: kla_glr_workspace_size bytes, 16-byte aligned, the states handed
- * from one block of tokens to the next; may be null when that size is 0.
- * Every call initialises what it reads of it.
+ * No workspace.  One kernel; blocks that share a sequence exchange their
+ * parts on chip (thread-block clusters).
  * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, D < 1, a null or
- * misaligned pointer, overlapping buffers, a workspace that is missing or too
- * small), KLA_ERR_UNSUPPORTED_SHAPE (T > 2^31 - 4097), KLA_ERR_CUDA.
+ * misaligned pointer, overlapping buffers), KLA_ERR_UNSUPPORTED_SHAPE
+ * (T > 2^31 - 4097), KLA_ERR_CUDA.
  */
-KLA_API kla_status kla_glr_workspace_size(int B, int T, int D, int packed,
-                                          kla_dtype dtype,
-                                          kla_dtype gate_dtype,
-                                          size_t* bytes);
 KLA_API kla_status kla_glr_fwd(
     const void* x, long long x_sb, long long x_st, const void* log_alpha,
     long long a_sb, long long a_st, const float* h0, void* o, float* hT,
     const int* cu_seqlens, int B, int T, int D, kla_dtype dtype,
-    kla_dtype gate_dtype, void* workspace, size_t workspace_bytes,
-    kla_stream_t stream);
+    kla_dtype gate_dtype, kla_stream_t stream);
 
 /*
  * kla_glr_bwd -- gradients given o_grad = dL/do and optionally hT_grad =
@@ -684,7 +678,7 @@ KLA_API kla_status kla_glr_fwd(
  *
  * g is held in fp32.  h_{t-1} is the o that the forward rounded to `dtype`:
  * with bf16 it carries that one rounding (at most 2^-8) into log_alpha_grad.
- * Shapes, strides, packing and workspace as kla_glr_fwd; x_grad (`dtype`) and
+ * Shapes, strides and packing as kla_glr_fwd; x_grad (`dtype`) and
  * log_alpha_grad (`gate_dtype`) contiguous like o; h0_grad [B, D] fp32 or
  * null.  The outputs may not overlap any input nor each other.
  * Errors: as kla_glr_fwd.
@@ -694,8 +688,7 @@ KLA_API kla_status kla_glr_bwd(
     long long a_sb, long long a_st, const float* h0, const void* o_grad,
     long long g_sb, long long g_st, const float* hT_grad, void* x_grad,
     void* log_alpha_grad, float* h0_grad, const int* cu_seqlens, int B, int T,
-    int D, kla_dtype dtype, kla_dtype gate_dtype, void* workspace,
-    size_t workspace_bytes, kla_stream_t stream);
+    int D, kla_dtype dtype, kla_dtype gate_dtype, kla_stream_t stream);
 
 /*
  * kla_glr_step -- one token for N sequences: S [N, D] fp32 (contiguous) is

@@ -21,24 +21,22 @@ using bf16 = __nv_bfloat16;
 // backwards in the backward pass) of CH = 64 channels; warp w of its block
 // holds S of the tokens, a lane two of the channels.  All tiles of one run of
 // tokens (a batch entry, or all packed tokens) and one group of channels form
-// a chain.  A chain is walked by the G blocks of a team, which take every
-// G-th tile each, in order; a block
+// a chain.  A chain is walked by a team of G blocks, a thread-block cluster,
+// which take every G-th tile each, in order; a block
 //   1. waits for its tile's inputs, which were copied into shared memory
 //      while it worked on the tile before (two stages), takes them into
 //      registers and hands the stage over to the copy of a later tile,
 //   2. reduces each warp's S steps to the affine map c -> P c + H of the
 //      state, and the warps' maps to the tile's map,
-//   3. publishes the tile's map in global memory and collects those of the
-//      G - 1 other tiles of this step (G > 1 only),
+//   3. sends the tile's map to all blocks of the team (st.async into their
+//      shared memory) and waits for the G maps of this step,
 //   4. applies the maps before its own tokens to the state before the step's
 //      first tile, and all G to carry that state on: every block of the team
 //      carries it by itself, so that no state is handed from block to block
 //      and a step costs one exchange, not G,
 //   5. runs its steps again from the now known state and writes the outputs.
 // Every input element is read from HBM once.  Maps are applied in token
-// order, so the result has the same bits on every run.  The blocks of a team
-// wait for one another: they are launched together (cooperative launch), and
-// every wait is bounded.
+// order, so the result has the same bits on every run.
 //
 // A state that a sequence starts from replaces c (it is not multiplied by
 // zero), so nothing of one packed sequence, not even a NaN, reaches the next:
@@ -50,18 +48,13 @@ constexpr int S = 16;            // tokens of a warp
 constexpr int kTile = W * S;
 constexpr int CH = 64;           // channels of a tile
 constexpr int kThreads = 32 * W;
-constexpr int kMaxTeam = 32;     // blocks of a team
-constexpr int kMaxBlocks = 1024; // blocks that walk chains at the same time
+constexpr int kMaxTeam = 16;     // blocks of a team: the largest cluster
 
 struct ScanPlan {
     int tiles, groups;           // tiles of a chain; channel groups
     int rounds;                  // chains that each block walks alone, then
     int rest, team;              // `rest` chains walked by a team each
-    uint2* map;                  // [rest][tiles][CH] (P, H); all ones: none
 };
-
-constexpr unsigned int kEmpty = 0xffffffffu;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_fault_glr = 0;
 
@@ -109,45 +102,61 @@ __device__ __forceinline__ float2 decay(float2 l) {
                        fabsf(l.y) <= 0.125f ? p.y : ey);
 }
 
-// Maps of two channels as (P.x, P.y, H.x, H.y).
-__device__ __forceinline__ bool fresh(float P) {
-    return __float_as_uint(P) == 0x80000000u;
+// Maps of two channels as (P.x, P.y, H.x, H.y).  P is finite (see `bounded`),
+// so that a zero state stays zero however large the decays' product grew.
+__device__ __forceinline__ float2 plain_apply(float4 m, float2 c) {
+    return fma2(make_float2(m.x, m.y), c, make_float2(m.z, m.w));
 }
-// A zero state stays zero however large P grew.
-__device__ __forceinline__ float apply(float P, float H, float c) {
-    return c == 0.f || fresh(P) ? H : fmaf(P, c, H);
+// Whether a map does not depend on the state before it.  That goes by the
+// tokens, so it is the same in all channels.
+__device__ __forceinline__ bool fresh(float4 m) {
+    return __float_as_uint(m.x) == 0x80000000u;
 }
 __device__ __forceinline__ float2 apply(float4 m, float2 c) {
-    return make_float2(apply(m.x, m.z, c.x), apply(m.y, m.w, c.y));
+    return fresh(m) ? make_float2(m.z, m.w) : plain_apply(m, c);
 }
-// The map of `first`, then `then`.
-__device__ __forceinline__ float4 compose(float4 first, float4 then) {
-    const float2 h = apply(then, make_float2(first.z, first.w));
-    return make_float4(fresh(then.x) ? then.x : first.x * then.x,
-                       fresh(then.y) ? then.y : first.y * then.y, h.x, h.y);
-}
+// A product past the range (decays above 1) or NaN (then H is, too) becomes
+// the largest number; -0 stays.
+__device__ __forceinline__ float bounded(float P) { return fminf(P, 3e38f); }
 
-// A published map is one 64-bit memory operation per channel, so a reader
-// sees it whole or not at all; a NaN with all bits set becomes another NaN.
-__device__ __forceinline__ uint64_t map_bits(float P, float H) {
-    const unsigned int h = __float_as_uint(H);
-    return (uint64_t)(h == kEmpty ? 0x7fffffffu : h) << 32 |
-           __float_as_uint(P);
+// A map to the same place in the shared memory of block `rank` of the
+// cluster, counted by that block's mbarrier.
+__device__ __forceinline__ void send(float4* to, uint64_t* bar, int rank,
+                                     float4 m) {
+    asm volatile(
+        "{\n\t.reg .b32 a, b;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 "
+        "[a], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(tc::smem_u32(to)),
+        "r"(tc::smem_u32(bar)), "r"(rank), "r"(__float_as_uint(m.x)),
+        "r"(__float_as_uint(m.y)), "r"(__float_as_uint(m.z)),
+        "r"(__float_as_uint(m.w))
+        : "memory");
 }
-__device__ __forceinline__ void publish(uint2* p, float4 m) {
-    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p),
-                 "l"(map_bits(m.x, m.z)), "l"(map_bits(m.y, m.w))
-                 : "memory");
+// Waits (2 s at most) until the maps of a step have arrived.
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
+    uint64_t begun = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, "
+            "[%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(tc::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        const uint64_t now = tc::globaltimer_ns();
+        if (begun == 0) begun = now;
+        if (now - begun > 2000000000ull) return false;
+    }
 }
-__device__ __forceinline__ bool collect(const uint2* p, float4& m) {
-    uint64_t a, b;
-    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
-                 : "=l"(a), "=l"(b)
-                 : "l"(p)
-                 : "memory");
-    const float2 u = floats(a), v = floats(b);
-    m = make_float4(u.x, v.x, u.y, v.y);
-    return a != ~0ull && b != ~0ull;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
 }
 
 // How the inputs' rows line up: on 16 bytes, so that whole tiles can be
@@ -276,29 +285,30 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
     return {mask, lo};
 }
 
-// The tiles of a block, in its order.
+// The tiles of a block, in its order: tile k of the run of tokens b, channels
+// from d on.
 struct Cursor {
-    int round, chain, k, step;
+    int round, b, d, k, step;
+    bool more;
     __device__ Cursor(const ScanPlan& p) : round(-1) { open(p); }
     __device__ void open(const ScanPlan& p) {    // the next chain
         ++round;
+        int chain = round * (int)gridDim.x + blockIdx.x;
+        more = round < p.rounds;
         k = 0;
         step = 1;
-        const int b = blockIdx.x;
-        if (round < p.rounds) {
-            chain = round * (int)gridDim.x + b;
-        } else if (round == p.rounds && b < p.rest * p.team) {
-            chain = p.rounds * (int)gridDim.x + b / p.team;
-            k = b % p.team;
+        if (round == p.rounds) {
+            chain = round * (int)gridDim.x + blockIdx.x / p.team;
+            more = blockIdx.x < p.rest * p.team;
+            k = blockIdx.x % p.team;
             step = p.team;
-        } else {
-            chain = -1;                          // no more
         }
+        b = chain / p.groups;
+        d = chain % p.groups * CH;
     }
     __device__ void move(const ScanPlan& p) {
-        if (chain < 0) return;
         k += step;
-        if (k >= p.tiles) open(p);
+        if (k >= p.tiles && more) open(p);
     }
 };
 
@@ -317,15 +327,15 @@ template <typename T, typename G, bool BWD>
 struct Shared {
     Stage<T, G, BWD> stage[2];
     float4 own[2][W][32];        // the warps' maps, of this tile and the next
-    uint64_t full[2];
+    uint64_t full[2], got[2];    // a stage has its tile; a step has its maps
 };
 
 // Shared memory of a block whose team collects `team` maps (1: none), and how
 // many such blocks an SM holds (228 KB, 1 KB of it per block the system's),
-// at most 4: 64 registers a thread.
+// at most 4: 128 registers a thread.
 template <typename T, typename G, bool BWD>
 constexpr int shared_bytes(int team) {
-    return (int)sizeof(Shared<T, G, BWD>) + (team > 1 ? team * 512 : 0);
+    return (int)sizeof(Shared<T, G, BWD>) + (team > 1 ? 2 * team * 512 : 0);
 }
 template <typename T, typename G, bool BWD>
 constexpr int resident(int team) {
@@ -341,27 +351,27 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 const __grid_constant__ CUtensorMap map_g) {
     extern __shared__ __align__(128) unsigned char smem[];
     auto& sh = *reinterpret_cast<Shared<T, G, BWD>*>(smem);
-    // the team's maps of this step
-    auto* team = reinterpret_cast<float4(*)[32]>(&sh + 1);
+    // the team's maps of this step and the next: [2][team][32]
+    auto* maps = reinterpret_cast<float4(*)[32]>(&sh + 1);
     constexpr int DT = BWD ? -1 : 1;             // token step of the scan
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     const float* init = BWD ? a.dhT : a.h0;
 
-    if (A == kWide) {
-        if (threadIdx.x == 0) {
-            tc::mbar_init(&sh.full[0], 1);
-            tc::mbar_init(&sh.full[1], 1);
-            tc::fence_mbar_init();
-        }
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint64_t* bar : {&sh.full[0], &sh.full[1], &sh.got[0],
+                              &sh.got[1]})
+            tc::mbar_init(bar, 1);
+        tc::fence_mbar_init();
     }
+    if (plan.team > 1) cluster_sync();
+    else __syncthreads();
     // Starts the copy of a tile's inputs into a stage: row r of it is token
     // lo + r, lo the tile's lowest token.
     auto fetch = [&](const Cursor& at, int s) {
         Stage<T, G, BWD>& st = sh.stage[s];
-        if (at.chain >= 0 && (A != kWide || threadIdx.x == 0)) {
-            const int b = at.chain / plan.groups;
-            const int d = at.chain % plan.groups * CH;
+        // (the first warp has the tile's map to form meanwhile)
+        if (at.more && (A != kWide || threadIdx.x == kThreads - 1)) {
+            const int b = at.b, d = at.d;
             const int p = at.k * kTile;
             const int lo = BWD ? a.T - kTile - p : p;
             if (A == kWide) {
@@ -397,12 +407,12 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     float2 carry = both(0.f);        // the state before the team's tiles
     bool fault = false;
     unsigned int turn = 0, issued = 2;           // copies started
-    for (; here.chain >= 0; ++turn) {
+    for (unsigned int hops = 0; here.more; ++turn) {
         const int s = turn & 1;
         const Stage<T, G, BWD>& st = sh.stage[s];
-        const int b = a.cu ? 0 : here.chain / plan.groups;
-        const int d0 = here.chain % plan.groups * CH;
-        const int da = d0 + channel<A>(lane, 0), db = d0 + channel<A>(lane, 1);
+        const int b = here.b;
+        const int da = here.d + channel<A>(lane, 0);
+        const int db = here.d + channel<A>(lane, 1);
         const bool la = da < a.D, lb = db < a.D;
         // scan position p <-> token t
         const int p0 = here.k * kTile + w * S;
@@ -480,7 +490,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         };
         if (plain) reduce(std::false_type());
         else reduce(std::true_type());
-        sh.own[s][w][lane] = make_float4(P.x, P.y, H.x, H.y);
+        sh.own[s][w][lane] =
+            make_float4(bounded(P.x), bounded(P.y), H.x, H.y);
         // the stage is free, the maps are there
         if (__syncthreads_or(fault)) {
             fault = true;
@@ -490,50 +501,57 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         fetch(ahead, s);
         ++issued;
 
+        // which of the warps' maps start anew
+        const unsigned int cut = __ballot_sync(
+            0xffffffffu, lane < W && fresh(sh.own[s][lane % W][0]));
         float2 c = carry;            // the state before the tile
         if (here.step > 1) {
-            const int G_ = here.step, m = here.k % G_;
-            // in the last step of the chain only those before
-            const int want = here.k + G_ < plan.tiles ? G_ : m;
-            const size_t at =
-                ((size_t)(here.chain - plan.rounds * (int)gridDim.x) *
-                     plan.tiles + (here.k - m)) * CH + 2 * lane;
+            const int m = here.k % here.step, h = hops & 1;
+            const int there = min(here.step, plan.tiles - (here.k - m));
+            float4(*team)[32] = maps + h * here.step;
             if (w == 0) {
                 float4 t = sh.own[s][0][lane];
 #pragma unroll
-                for (int u = 1; u < W; ++u)
-                    t = compose(t, sh.own[s][u][lane]);
-                if (here.k + 1 < plan.tiles)
-                    publish(plan.map + at + (size_t)m * CH, t);
-                team[m][lane] = t;
-            }
-            // the others' maps: a warp takes every W-th, from the last warp
-            for (int j = W - 1 - w; j < want; j += W) {
-                if (j == m) continue;
-                float4 t;
-                uint64_t begun = 0;
-                while (!__all_sync(0xffffffffu,
-                                   collect(plan.map + at + (size_t)j * CH,
-                                           t))) {
-                    const uint64_t now = tc::globaltimer_ns();
-                    if (begun == 0) begun = now;
-                    if (__any_sync(0xffffffffu, now > begun + kWaitLimitNs)) {
-                        fault = true;
-                        break;
-                    }
+                for (int u = 1; u < W; ++u) {
+                    const float4 q = sh.own[s][u][lane];
+                    const float2 v = cut >> u & 1
+                                         ? make_float2(q.z, q.w)
+                                         : plain_apply(q, make_float2(t.z,
+                                                                      t.w));
+                    t = make_float4(bounded(t.x * q.x), bounded(t.y * q.y),
+                                    v.x, v.y);
                 }
-                if (fault) break;
-                team[j][lane] = t;
+                if (cut) t.x = t.y = -0.f;
+                if (lane == 0)
+                    tc::mbar_arrive_expect_tx(&sh.got[h], there * 512);
+                __syncwarp();
+                for (int r = 0; r < there; ++r)
+                    send(&team[m][lane], &sh.got[h], r, t);
             }
-            if (__syncthreads_or(fault)) {
-                fault = true;
-                break;
+            fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
+            ++hops;
+            const unsigned int anew = __ballot_sync(
+                0xffffffffu, lane < there && fresh(team[lane % there][0]));
+            if (anew == 0) {
+#pragma unroll 4
+                for (int j = 0; j < there; ++j) {
+                    if (j == m) c = carry;
+                    carry = plain_apply(team[j][lane], carry);
+                }
+            } else {
+                for (int j = 0; j < there; ++j) {
+                    if (j == m) c = carry;
+                    carry = apply(team[j][lane], carry);
+                }
             }
-            for (int j = 0; j < m; ++j) c = apply(team[j][lane], c);
-            carry = c;
-            for (int j = m; j < want; ++j) carry = apply(team[j][lane], carry);
         }
-        for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
+        if (cut == 0) {
+#pragma unroll
+            for (int u = 0; u < W - 1; ++u)
+                if (u < w) c = plain_apply(sh.own[s][u][lane], c);
+        } else {
+            for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
+        }
         if (here.step == 1) {
             carry = c;
             for (int u = w; u < W; ++u)
@@ -592,7 +610,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         for (++turn; A == kWide && turn < issued; ++turn)
             tc::mbar_wait(&sh.full[turn & 1], (turn >> 1) & 1, 1000000);
     }
-    if (fault) __syncthreads();
+    if (plan.team > 1) cluster_sync();           // nobody sends here any more
+    else if (fault) __syncthreads();
 }
 
 template <typename T, typename G>
@@ -625,32 +644,27 @@ cudaError_t by_type(kla_dtype t, kla_dtype g, F f) {
 
 namespace {
 
-long long chains_of(int B, int D, bool packed) {
-    return (long long)((D + CH - 1) / CH) * (packed ? 1 : B);
-}
-
 // How `chains` chains of `tiles` tiles share the blocks that the SMs hold:
-// whole rounds of a chain per block, then the rest by teams as large as fit.
+// whole rounds of a chain per block, then the rest by teams as large as fit
+// (powers of two, which fill a GPC's SMs best).
 template <typename T, typename G, bool BWD>
-ScanPlan plan_of(long long chains, int tiles, int D, void* ws, int* blocks) {
-    ScanPlan p;
-    p.tiles = tiles;
-    p.groups = (D + CH - 1) / CH;
-    p.map = static_cast<uint2*>(ws);
+ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
+    ScanPlan p{tiles, (D + CH - 1) / CH, 0, 0, 1};
+    *blocks = 0;
     for (int per = resident<T, G, BWD>(1); per > 0; --per) {
-        const int slots = std::min(per * device_sm_count(), kMaxBlocks);
+        const int slots = per * device_sm_count() / kMaxTeam * kMaxTeam;
         if (slots <= 0) break;
         p.rounds = (int)(chains / slots);
         p.rest = (int)(chains % slots);
         p.team = 1;
-        if (p.rest)
-            p.team = std::max(
-                1, std::min({slots / p.rest, kMaxTeam, tiles}));
-        *blocks = p.rounds ? slots : p.rest * p.team;
+        while (p.rest && 2 * p.team <= kMaxTeam && 2 * p.team <= tiles &&
+               2 * p.team * p.rest <= slots)
+            p.team *= 2;
         // the maps of a large team may take the room of a block
-        if (resident<T, G, BWD>(p.team) >= per) return p;
+        if (resident<T, G, BWD>(p.team) < per) continue;
+        *blocks = p.rounds ? slots : p.rest * p.team;
+        break;
     }
-    *blocks = 0;
     return p;
 }
 
@@ -677,12 +691,13 @@ bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a) {
 }
 
 template <typename T, typename G, Align A, bool BWD>
-cudaError_t launch_scan(const GlrArgs& a, void* ws, cudaStream_t s) {
-    const long long chains = chains_of(a.B, a.D, a.cu != nullptr);
-    const int tiles = (a.T + kTile - 1) / kTile;
+cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
+    const long long chains =
+        (long long)((a.D + CH - 1) / CH) * (a.cu ? 1 : a.B);
     if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
     int blocks = 0;
-    const ScanPlan p = plan_of<T, G, BWD>(chains, tiles, a.D, ws, &blocks);
+    const ScanPlan p = plan_of<T, G, BWD>(
+        chains, (int)((a.T + (long long)kTile - 1) / kTile), a.D, &blocks);
     if (blocks <= 0) return cudaErrorInvalidValue;
     CUtensorMap mx{}, ml{}, mg{};
     if (A == kWide &&
@@ -700,12 +715,14 @@ cudaError_t launch_scan(const GlrArgs& a, void* ws, cudaStream_t s) {
     cfg.dynamicSmemBytes = shared_bytes<T, G, BWD>(p.team);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.team;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.team > 1 ? 1 : 0;
-    if (p.team > 1) {
-        e = cudaMemsetAsync(ws, 0xff, (size_t)p.rest * tiles * CH * 8, s);
+    if (p.team > 8) {
+        e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     return cudaLaunchKernelEx(&cfg, kernel, a, p, mx, ml, mg);
@@ -723,23 +740,14 @@ bool maps(const Strided& x, const GlrArgs& a) {
 }
 
 template <typename T, typename G, Align A>
-cudaError_t launch_way(const GlrArgs& a, bool bwd, void* ws, cudaStream_t s) {
-    return bwd ? launch_scan<T, G, A, true>(a, ws, s)
-               : launch_scan<T, G, A, false>(a, ws, s);
+cudaError_t launch_way(const GlrArgs& a, bool bwd, cudaStream_t s) {
+    return bwd ? launch_scan<T, G, A, true>(a, s)
+               : launch_scan<T, G, A, false>(a, s);
 }
 
 }  // namespace
 
-size_t glr_workspace_bytes(int B, int T, int D, bool packed, kla_dtype,
-                           kla_dtype) {
-    if (B <= 0 || T <= kTile) return 0;
-    const long long tiles = (T + kTile - 1) / kTile;
-    return std::min<long long>(chains_of(B, D, packed), kMaxBlocks) * tiles *
-           CH * 8;
-}
-
-cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
-                       cudaStream_t stream) {
+cudaError_t launch_glr(const GlrArgs& a, bool bwd, cudaStream_t stream) {
     if (a.T == 0) {              // every sequence is empty
         const float* init = bwd ? a.dhT : a.h0;
         const size_t n = sizeof(float) * (size_t)a.B * a.D;
@@ -764,9 +772,9 @@ cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
         const bool wide = pairs && in(16, 16) && maps(a.x, a) &&
                           maps(a.la, a) && (!bwd || maps(a.g, a)) &&
                           get_encoder();
-        return wide    ? launch_way<T, G, kWide>(a, bwd, workspace, stream)
-               : pairs ? launch_way<T, G, kPair>(a, bwd, workspace, stream)
-                       : launch_way<T, G, kElement>(a, bwd, workspace, stream);
+        return wide    ? launch_way<T, G, kWide>(a, bwd, stream)
+               : pairs ? launch_way<T, G, kPair>(a, bwd, stream)
+                       : launch_way<T, G, kElement>(a, bwd, stream);
     });
 }
 

@@ -236,10 +236,7 @@ size_t layernorm_bwd_workspace_bytes(int rows, int D, kla_dtype dtype);
 cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, void* workspace,
                                  cudaStream_t stream);
 // Gated linear recurrence (B > 0).
-size_t glr_workspace_bytes(int B, int T, int D, bool packed, kla_dtype dtype,
-                           kla_dtype gdtype);
-cudaError_t launch_glr(const GlrArgs& a, bool bwd, void* workspace,
-                       cudaStream_t stream);
+cudaError_t launch_glr(const GlrArgs& a, bool bwd, cudaStream_t stream);
 cudaError_t launch_glr_step(const void* x, long long x_stride,
                             const void* la, long long la_stride, float* S,
                             void* o, int N, int D, kla_dtype dtype,

@@ -112,18 +112,6 @@ extern "C" kla_status kla_layernorm_bwd(
     return from_cuda(kla::launch_layernorm_bwd(a, workspace, s));
 }
 
-extern "C" kla_status kla_glr_workspace_size(int B, int T, int D, int packed,
-                                             kla_dtype dtype,
-                                             kla_dtype gate_dtype,
-                                             size_t* bytes) {
-    if (!bytes || B < 0 || T < 0 || D < 1 || !valid(dtype) ||
-        !valid(gate_dtype))
-        return KLA_ERR_INVALID_ARG;
-    *bytes = kla::glr_workspace_bytes(B, T, D, packed != 0, dtype,
-                                      gate_dtype);
-    return KLA_OK;
-}
-
 namespace {
 
 // Token positions are counted in 32 bits, with room for a partial tile.
@@ -136,8 +124,7 @@ size_t span_bytes(const kla::GlrArgs& a, const kla::Strided& x, size_t elt) {
     return a.T ? (size_t)(b + t + a.D) * elt : 0;
 }
 
-kla_status glr_impl(kla::GlrArgs& a, bool bwd, void* workspace,
-                    size_t workspace_bytes, kla_stream_t stream) {
+kla_status glr_impl(const kla::GlrArgs& a, bool bwd, kla_stream_t stream) {
     if (a.B < 0 || a.T < 0 || a.D < 1 || a.x.sb < 0 || a.x.st < 0 ||
         a.la.sb < 0 || a.la.st < 0 || a.g.sb < 0 || a.g.st < 0 ||
         !valid(a.dtype) || !valid(a.gdtype))
@@ -153,11 +140,6 @@ kla_status glr_impl(kla::GlrArgs& a, bool bwd, void* workspace,
         (!given(a.x.p, e) || !given(a.la.p, ge) || !given(a.o, e) ||
          (bwd && (!given(a.g.p, e) || !given(a.dla, ge)))))
         return KLA_ERR_INVALID_ARG;
-    const size_t need = kla::glr_workspace_bytes(a.B, a.T, a.D,
-                                                 a.cu != nullptr, a.dtype,
-                                                 a.gdtype);
-    if (need && (!given(workspace, 16) || workspace_bytes < need))
-        return KLA_ERR_INVALID_ARG;
     const size_t n = (size_t)a.T * (a.cu ? 1 : a.B) * a.D;
     const size_t st = (size_t)a.B * a.D * 4;
     // hT in the place of h0 is allowed in the forward: each state is read
@@ -170,10 +152,10 @@ kla_status glr_impl(kla::GlrArgs& a, bool bwd, void* workspace,
                         span(a.dhT, st),
                         span(a.cu, ((size_t)a.B + 1) * 4)};
     const Span outs[] = {span(a.o, n * e), span(a.dla, n * ge),
-                         span(a.hT, st), span(workspace, need)};
+                         span(a.hT, st)};
     if (any_overlap(ins, outs)) return KLA_ERR_INVALID_ARG;
-    return from_cuda(kla::launch_glr(
-        a, bwd, workspace, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(
+        kla::launch_glr(a, bwd, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -182,12 +164,11 @@ extern "C" kla_status kla_glr_fwd(
     const void* x, long long x_sb, long long x_st, const void* log_alpha,
     long long a_sb, long long a_st, const float* h0, void* o, float* hT,
     const int* cu_seqlens, int B, int T, int D, kla_dtype dtype,
-    kla_dtype gate_dtype, void* workspace, size_t workspace_bytes,
-    kla_stream_t stream) {
-    kla::GlrArgs a{{x, x_sb, x_st}, {log_alpha, a_sb, a_st}, {nullptr, 0, 0},
+    kla_dtype gate_dtype, kla_stream_t stream) {
+    const kla::GlrArgs a{{x, x_sb, x_st}, {log_alpha, a_sb, a_st}, {nullptr, 0, 0},
                    h0, nullptr, o, nullptr, hT, cu_seqlens, B, T, D, dtype,
                    gate_dtype};
-    return glr_impl(a, false, workspace, workspace_bytes, stream);
+    return glr_impl(a, false, stream);
 }
 
 extern "C" kla_status kla_glr_bwd(
@@ -195,12 +176,11 @@ extern "C" kla_status kla_glr_bwd(
     long long a_sb, long long a_st, const float* h0, const void* o_grad,
     long long g_sb, long long g_st, const float* hT_grad, void* x_grad,
     void* log_alpha_grad, float* h0_grad, const int* cu_seqlens, int B, int T,
-    int D, kla_dtype dtype, kla_dtype gate_dtype, void* workspace,
-    size_t workspace_bytes, kla_stream_t stream) {
-    kla::GlrArgs a{{o, o_sb, o_st}, {log_alpha, a_sb, a_st},
+    int D, kla_dtype dtype, kla_dtype gate_dtype, kla_stream_t stream) {
+    const kla::GlrArgs a{{o, o_sb, o_st}, {log_alpha, a_sb, a_st},
                    {o_grad, g_sb, g_st}, h0, hT_grad, x_grad, log_alpha_grad,
                    h0_grad, cu_seqlens, B, T, D, dtype, gate_dtype};
-    return glr_impl(a, true, workspace, workspace_bytes, stream);
+    return glr_impl(a, true, stream);
 }
 
 extern "C" kla_status kla_glr_step(const void* x, long long x_stride,

@@ -82,13 +82,10 @@ SIGNATURES = {
     "kla_layernorm_bwd": (_I, [_VP, _LL, _VP, _LL, _VP, _FP, _FP, _VP, _LL,
                                _VP, _VP, _VP, _I, _I, _I, _I,
                                _VP, ctypes.c_size_t, _VP]),
-    "kla_glr_workspace_size": (
-        _I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "kla_glr_fwd": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _FP, _VP, _FP, _VP,
-                         _I, _I, _I, _I, _I, _VP, ctypes.c_size_t, _VP]),
+                         _I, _I, _I, _I, _I, _VP]),
     "kla_glr_bwd": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _FP, _VP, _LL, _LL,
-                         _FP, _VP, _VP, _FP, _VP, _I, _I, _I, _I, _I,
-                         _VP, ctypes.c_size_t, _VP]),
+                         _FP, _VP, _VP, _FP, _VP, _I, _I, _I, _I, _I, _VP]),
     "kla_glr_step": (_I, [_VP, _LL, _VP, _LL, _FP, _VP, _I, _I, _I, _I,
                           _VP]),
     "kla_device_status": (_I, [_VP]),
@@ -746,19 +743,6 @@ def layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad=None,
     return dict(x_grad=dx, weight_grad=dw, bias_grad=db)
 
 
-def glr_workspace_size(B: int, T: int, D: int, dtype, gate_dtype,
-                       packed: bool = False) -> int:
-    """Bytes of device workspace ``glr_fwd`` and ``glr_bwd`` need: B sequences
-    of T tokens, or B sequences ``packed`` into T tokens in all."""
-    n = ctypes.c_size_t(0)
-    st = load_library().kla_glr_workspace_size(
-        B, T, D, int(packed), DTYPES[dtype], DTYPES[gate_dtype],
-        ctypes.byref(n))
-    if st != KLA_OK:
-        raise KlaError("kla_glr_workspace_size", st)
-    return n.value
-
-
 def _glr_shape(name, x, cu_seqlens):
     """(device, B, T, D) of a recurrence call."""
     dev = _device_of(name, x)
@@ -786,7 +770,7 @@ def _glr_strides(t):
 
 
 def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
-            want_state: bool = True, workspace=None, stream=None):
+            want_state: bool = True, stream=None):
     """Gated linear recurrence (``kla_glr_fwd``), per sequence and channel
     h_t = exp(log_alpha_t) h_{t-1} + x_t, o_t = h_t.
 
@@ -796,12 +780,10 @@ def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
     n-th holding the tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1.  Returns
     (o, hT): o contiguous of x's dtype, hT [B, D] fp32 the last states (None
     unless ``want_state``).  ``o`` / ``hT`` may be passed preallocated (``hT``
-    may be ``h0``); ``workspace``: a device uint8 tensor of at least
-    ``glr_workspace_size`` bytes, allocated here when None."""
+    may be ``h0``)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return glr_fwd(x, log_alpha, h0, cu_seqlens, o, hT, want_state,
-                           workspace)
+            return glr_fwd(x, log_alpha, h0, cu_seqlens, o, hT, want_state)
     dev, B, T, D = _glr_shape("x", x, cu_seqlens)
     dt = x.dtype
     _tensor("log_alpha", log_alpha, dev, _IO, x.shape)
@@ -810,17 +792,14 @@ def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
     o = _output("o", o, x.shape, dt, dev)
     if hT is not None or want_state:
         hT = _output("hT", hT, (B, D), torch.float32, dev)
-    workspace, nbytes = _workspace(
-        workspace, glr_workspace_size(B, T, D, dt, log_alpha.dtype,
-                                      cu_seqlens is not None), dev)
     _call("kla_glr_fwd", *_glr_strides(x), *_glr_strides(log_alpha),
           _addr(h0), o.data_ptr(), _addr(hT), _addr(cu_seqlens), B, T, D,
-          DTYPES[dt], DTYPES[log_alpha.dtype], _addr(workspace), nbytes)
+          DTYPES[dt], DTYPES[log_alpha.dtype])
     return o, hT
 
 
 def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
-            want_h0_grad: bool = True, workspace=None, stream=None):
+            want_h0_grad: bool = True, stream=None):
     """Backward pass of ``glr_fwd`` (``kla_glr_bwd``): gradients given dL/do
     (``o_grad``, like o) and dL/dhT (``hT_grad``, [B, D] fp32 or None).  o is
     what the forward returned, the other arguments what it took.  Returns a
@@ -829,7 +808,7 @@ def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
     if stream is not None:
         with torch.cuda.stream(stream):
             return glr_bwd(o, log_alpha, o_grad, hT_grad, h0, cu_seqlens,
-                           want_h0_grad, workspace)
+                           want_h0_grad)
     dev, B, T, D = _glr_shape("o", o, cu_seqlens)
     dt, gt = o.dtype, log_alpha.dtype
     _tensor("log_alpha", log_alpha, dev, _IO, o.shape)
@@ -841,13 +820,10 @@ def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
     dla = torch.empty(o.shape, dtype=gt, device=dev)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) \
         if want_h0_grad else None
-    workspace, nbytes = _workspace(
-        workspace, glr_workspace_size(B, T, D, dt, gt,
-                                      cu_seqlens is not None), dev)
     _call("kla_glr_bwd", *_glr_strides(o), *_glr_strides(log_alpha),
           _addr(h0), *_glr_strides(o_grad), _addr(hT_grad), dx.data_ptr(),
           dla.data_ptr(), _addr(dh0), _addr(cu_seqlens), B, T, D, DTYPES[dt],
-          DTYPES[gt], _addr(workspace), nbytes)
+          DTYPES[gt])
     return dict(x_grad=dx, log_alpha_grad=dla, h0_grad=dh0)
 
 

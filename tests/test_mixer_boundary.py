@@ -7,7 +7,7 @@ import torch
 
 from linear_attention_delta_gb300 import kla
 
-INVALID, OK = -1, 0
+INVALID, UNSUPPORTED, OK = -1, -2, 0
 F32, BF16 = 0, 1
 
 
@@ -42,7 +42,7 @@ def ln_bwd(lib, **kw):
 def glr_fwd(lib, **kw):
     a = dict(x=at(1), xsb=640, xst=64, la=at(2), asb=640, ast=64, h0=None,
              o=at(4), hT=at(5), cu=None, B=2, T=10, D=64, dtype=BF16,
-             gdtype=F32, ws=at(6), ws_bytes=1 << 22)
+             gdtype=F32)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.kla_glr_fwd(*a.values(), None)
@@ -51,8 +51,7 @@ def glr_fwd(lib, **kw):
 def glr_bwd(lib, **kw):
     a = dict(o=at(1), osb=640, ost=64, la=at(2), asb=640, ast=64, h0=at(3),
              do=at(4), gsb=640, gst=64, dhT=None, dx=at(5), dla=at(6),
-             dh0=at(7), cu=None, B=2, T=10, D=64, dtype=BF16, gdtype=F32,
-             ws=at(8), ws_bytes=1 << 22)
+             dh0=at(7), cu=None, B=2, T=10, D=64, dtype=BF16, gdtype=F32)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.kla_glr_bwd(*a.values(), None)
@@ -104,17 +103,8 @@ def test_layernorm_bwd_refuses(lib, bad):
     dict(x=ctypes.c_void_p(0x1000001)), dict(la=ctypes.c_void_p(0x2000002)),
     dict(h0=ctypes.c_void_p(0x3000002)), dict(cu=ctypes.c_void_p(0x9000002)),
     dict(cu=at(9), B=0), dict(cu=at(4)),
-    dict(T=100000, ws=None), dict(T=100000, ws_bytes=4),
 ])
 def test_glr_fwd_refuses(lib, bad):
-    if bad.get("T") == 100000:
-        n = ctypes.c_size_t(0)
-        assert lib.kla_glr_workspace_size(2, 100000, 64, 0, BF16, F32,
-                                          ctypes.byref(n)) == OK
-        if n.value == 0:
-            pytest.skip("no workspace at this size")
-        bad = dict(bad, o=at(40), hT=at(60), xsb=6400000, asb=6400000,
-                   x=at(1), la=at(100))
     assert glr_fwd(lib, **bad) == INVALID
 
 
@@ -151,18 +141,18 @@ def test_empty_problems_are_no_ops(lib):
 
 def test_workspace_sizes(lib):
     n = ctypes.c_size_t(0)
-    f, g = lib.kla_layernorm_bwd_workspace_size, lib.kla_glr_workspace_size
+    f = lib.kla_layernorm_bwd_workspace_size
     assert f(1000, 64, BF16, ctypes.byref(n)) == OK
     assert n.value >= 2 * 64 * 4
     assert f(-1, 64, BF16, ctypes.byref(n)) == INVALID
     assert f(1, 0, BF16, ctypes.byref(n)) == INVALID
     assert f(1, 64, 9, ctypes.byref(n)) == INVALID
     assert f(1, 64, BF16, None) == INVALID
-    assert g(1, 1, 64, 0, BF16, F32, ctypes.byref(n)) == OK and n.value == 0
-    assert g(1, -1, 64, 0, BF16, F32, ctypes.byref(n)) == INVALID
-    assert g(1, 1, 0, 0, BF16, F32, ctypes.byref(n)) == INVALID
-    assert g(1, 1, 1, 0, 9, F32, ctypes.byref(n)) == INVALID
-    assert g(1, 1, 1, 0, BF16, F32, None) == INVALID
+
+
+def test_glr_refuses_more_tokens_than_it_counts(lib):
+    assert glr_fwd(lib, T=0x7fffffff) == UNSUPPORTED
+    assert glr_bwd(lib, T=0x7fffffff) == UNSUPPORTED
 
 
 def test_binding_refuses_cpu_tensors():
