@@ -6,6 +6,7 @@
 // dlog_alpha_t = alpha_t g_t h_{t-1}, dh0 = alpha_1 g_1.  Bound by HBM: three
 // to five operations per element of each tensor it reads.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kla_internal.cuh"
@@ -160,8 +161,12 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // How the inputs' rows line up: on 16 bytes, so that whole tiles can be
-// copied (TMA); on pairs of channels; on elements only.
+// copied (TMA); on pairs of channels; on elements only.  In the last two
+// cases a row is copied with the 16-byte pieces that it touches and keeps its
+// place within the first of them.
 enum Align { kWide, kPair, kElement };
+template <Align A, typename T>
+constexpr int kPitch = CH + (A == kWide ? 0 : 16 / (int)sizeof(T));
 
 // The two channels of a lane: adjacent where pairs are aligned, else 32
 // apart, so that a warp's single elements are adjacent.
@@ -200,34 +205,44 @@ __device__ __forceinline__ void write2(T* row, bool l0, bool l1, float2 c) {
     }
 }
 
-// Copies tokens t .. t + kTile - 1 (rows `stride` elements apart) of `room`
-// channels into dst [kTile][CH]; what lies outside the tokens 0 .. T - 1 or
-// the channels becomes zero.  Asynchronous where pairs or elements have 4
-// bytes at least; the caller commits.
+// Copies rows t .. t + kTile - 1 (`stride` elements apart) of `room`
+// channels into dst [kTile][kPitch]; what lies outside the rows 0 .. n - 1 or
+// the channels becomes zero.  A piece of 16 aligned bytes is read from its
+// start to the row's end only; the bytes that it may hold before the row
+// belong to the same allocation, which starts on 16 bytes.
 template <Align A, typename T>
-__device__ __forceinline__ void copy_tile(T* dst, const T* src,
+__device__ __forceinline__ void copy_rows(T* dst, const T* src,
                                           long long stride, long long t,
-                                          int T_, int room) {
-    constexpr int E = A == kElement ? 1 : 2;     // elements of a copy
-    constexpr int BYTES = E * sizeof(T);
-    constexpr int PER = CH / E;                  // copies of a row
-    const int col = (threadIdx.x % PER) * E;
-#pragma unroll 4
-    for (int r = threadIdx.x / PER; r < kTile; r += kThreads / PER) {
-        const bool in = t + r >= 0 && t + r < T_ && col < room;
-        const T* from = in ? src + (t + r) * stride + col : src;
-        T* to = dst + r * CH + col;
-        if constexpr (BYTES >= 4) {
-            asm volatile(
-                "cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(
-                    tc::smem_u32(to)),
-                "l"(from), "r"(in ? BYTES : 0), "n"(BYTES)
-                : "memory");
-        } else {
-            *to = in ? *from : T(0.f);
-        }
+                                          int n, int room) {
+    constexpr int P = kPitch<A, T> * sizeof(T) / 16;   // pieces of a row
+    const int bytes = min(room, CH) * (int)sizeof(T);
+    for (int q = threadIdx.x; q < kTile * P; q += kThreads) {
+        const int r = q / P, piece = q % P;
+        const uintptr_t row =
+            reinterpret_cast<uintptr_t>(src + (t + r) * stride);
+        const uintptr_t from = (row & ~(uintptr_t)15) + piece * 16;
+        const long long left = (long long)(row + bytes) - (long long)from;
+        const bool in = t + r >= 0 && t + r < n && left > 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         tc::smem_u32(dst) + q * 16),
+                     "l"(in ? from : reinterpret_cast<uintptr_t>(src) &
+                                         ~(uintptr_t)15),
+                     "r"(in ? (int)min(left, 16ll) : 0)
+                     : "memory");
     }
 }
+// Where a row starts within its first piece (elements): of row t, and how
+// that moves from row to row.
+template <typename T>
+struct Shift {
+    unsigned int at, by;
+    __device__ Shift(const T* src, long long stride, long long t)
+        : at((unsigned int)reinterpret_cast<uintptr_t>(src + t * stride)),
+          by((unsigned int)(stride * (long long)sizeof(T))) {}
+    __device__ int operator()(int rows) const {
+        return ((at + rows * by) & 15) / sizeof(T);
+    }
+};
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
                                             uint64_t* bar, int c0, int c1,
@@ -312,45 +327,47 @@ struct Cursor {
     }
 };
 
-template <typename T, typename G, bool BWD>
+template <typename T, typename G, Align A, bool BWD>
 struct Stage {
-    T x[kTile][CH];
-    G la[kTile][CH];
+    T x[kTile][kPitch<A, T>];
+    G la[kTile][kPitch<A, G>];
 };
-template <typename T, typename G>
-struct Stage<T, G, true> {
-    T x[kTile][CH];              // o of the token before
-    G la[kTile][CH];
-    T g[kTile][CH];              // o_grad
+template <typename T, typename G, Align A>
+struct Stage<T, G, A, true> {
+    T x[kTile][kPitch<A, T>];    // o of the token before
+    G la[kTile][kPitch<A, G>];
+    T g[kTile][kPitch<A, T>];    // o_grad
 };
-template <typename T, typename G, bool BWD>
+template <typename T, typename G, Align A, bool BWD>
 struct Shared {
-    Stage<T, G, BWD> stage[2];
-    float4 own[2][W][32];        // the warps' maps, of this tile and the next
+    Stage<T, G, A, BWD> stage[2];
+    // the maps of all warps but the last, of this tile and the next
+    float4 own[2][W - 1][32];
     uint64_t full[2], got[2];    // a stage has its tile; a step has its maps
 };
 
-// Shared memory of a block whose team collects `team` maps (1: none), and how
-// many such blocks an SM holds (228 KB, 1 KB of it per block the system's),
-// at most 4: 128 registers a thread.
-template <typename T, typename G, bool BWD>
+// Shared memory of a block of a team, and how many such blocks an SM holds
+// (228 KB, 1 KB of it per block the system's), at most 4: 128 registers a
+// thread.
+template <typename T, typename G, Align A, bool BWD>
 constexpr int shared_bytes(int team) {
-    return (int)sizeof(Shared<T, G, BWD>) + (team > 1 ? 2 * team * 512 : 0);
+    return (int)sizeof(Shared<T, G, A, BWD>) + 2 * team * 512;
 }
-template <typename T, typename G, bool BWD>
-constexpr int resident(int team) {
-    return std::min(4, 228 * 1024 / (shared_bytes<T, G, BWD>(team) + 1024));
+template <typename T, typename G, Align A, bool BWD>
+constexpr int resident() {
+    return std::min(4,
+                    228 * 1024 / (shared_bytes<T, G, A, BWD>(1) + 1024));
 }
 
 template <typename T, typename G, Align A, bool BWD>
-__global__ void __launch_bounds__(kThreads, (resident<T, G, BWD>(1)))
+__global__ void __launch_bounds__(kThreads, (resident<T, G, A, BWD>()))
 glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 const __grid_constant__ ScanPlan plan,
                 const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_la,
                 const __grid_constant__ CUtensorMap map_g) {
     extern __shared__ __align__(128) unsigned char smem[];
-    auto& sh = *reinterpret_cast<Shared<T, G, BWD>*>(smem);
+    auto& sh = *reinterpret_cast<Shared<T, G, A, BWD>*>(smem);
     // the team's maps of this step and the next: [2][team][32]
     auto* maps = reinterpret_cast<float4(*)[32]>(&sh + 1);
     constexpr int DT = BWD ? -1 : 1;             // token step of the scan
@@ -368,9 +385,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     // Starts the copy of a tile's inputs into a stage: row r of it is token
     // lo + r, lo the tile's lowest token.
     auto fetch = [&](const Cursor& at, int s) {
-        Stage<T, G, BWD>& st = sh.stage[s];
-        // (the first warp has the tile's map to form meanwhile)
-        if (at.more && (A != kWide || threadIdx.x == kThreads - 1)) {
+        Stage<T, G, A, BWD>& st = sh.stage[s];
+        // (the last warp has the tile's map to form meanwhile)
+        if (at.more && (A != kWide || threadIdx.x == 0)) {
             const int b = at.b, d = at.d;
             const int p = at.k * kTile;
             const int lo = BWD ? a.T - kTile - p : p;
@@ -383,14 +400,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     tma_load_3d(&st.g[0][0], &map_g, &sh.full[s], d, lo, b);
             } else {
                 const int room = a.D - d;
-                copy_tile<A>(&st.la[0][0],
+                copy_rows<A>(&st.la[0][0],
                              static_cast<const G*>(a.la.p) + b * a.la.sb + d,
                              a.la.st, lo, a.T, room);
-                copy_tile<A>(&st.x[0][0],
+                copy_rows<A>(&st.x[0][0],
                              static_cast<const T*>(a.x.p) + b * a.x.sb + d,
                              a.x.st, BWD ? lo - 1ll : lo, a.T, room);
                 if constexpr (BWD)
-                    copy_tile<A>(&st.g[0][0],
+                    copy_rows<A>(&st.g[0][0],
                                  static_cast<const T*>(a.g.p) + b * a.g.sb +
                                      d,
                                  a.g.st, lo, a.T, room);
@@ -399,17 +416,29 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (A != kWide) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    // The boundaries among the warp's tokens of a tile.
+    auto bounds_of = [&](const Cursor& at) {
+        Bounds bd{0u, at.b};
+        const int p = at.k * kTile + w * S;
+        if (!at.more || p >= a.T) return bd;
+        if (a.cu) return find_bounds<BWD>(a.cu, a.B, BWD ? a.T - 1 - p : p);
+        if (p == 0) bd.mask = 1u;
+        if (a.T - p <= S) bd.mask |= 1u << (a.T - p);
+        return bd;
+    };
+
     Cursor here(plan), ahead = here;
     fetch(ahead, 0);
     ahead.move(plan);
     fetch(ahead, 1);
+    Bounds soon = bounds_of(here);
 
     float2 carry = both(0.f);        // the state before the team's tiles
     bool fault = false;
     unsigned int turn = 0, issued = 2;           // copies started
     for (unsigned int hops = 0; here.more; ++turn) {
         const int s = turn & 1;
-        const Stage<T, G, BWD>& st = sh.stage[s];
+        const Stage<T, G, A, BWD>& st = sh.stage[s];
         const int b = here.b;
         const int da = here.d + channel<A>(lane, 0);
         const int db = here.d + channel<A>(lane, 1);
@@ -420,13 +449,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         const int steps = max(0, min(S, a.T - p0));
         if (here.k < here.step) carry = both(0.f);       // a chain begins
 
-        Bounds bd{0u, b};
-        if (a.cu) {
-            if (steps > 0) bd = find_bounds<BWD>(a.cu, a.B, t0);
-        } else {
-            if (p0 == 0) bd.mask = 1u;
-            if (steps > 0 && a.T - p0 <= S) bd.mask |= 1u << (a.T - p0);
-        }
+        const Bounds bd = soon;
         const unsigned int begins = bd.mask & ((1u << S) - 1);
         // nothing begins, ends or is missing here
         const bool plain = bd.mask == 0 && steps == S;
@@ -468,6 +491,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         // before the second pass
         float2 kept = both(0.f);
         int n = bd.n;
+        // rows that do not line up on 16 bytes: where each starts
+        const int lo = BWD ? a.T - kTile - here.k * kTile : here.k * kTile;
+        const Shift<G> sl(static_cast<const G*>(a.la.p) + b * a.la.sb +
+                              here.d, a.la.st, lo);
+        const Shift<T> sx(static_cast<const T*>(a.x.p) + b * a.x.sb + here.d,
+                          a.x.st, BWD ? lo - 1ll : lo);
+        const Shift<T> sg(static_cast<const T*>(a.g.p) + b * a.g.sb + here.d,
+                          a.g.st, lo);
         auto reduce = [&](auto events) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
@@ -477,11 +508,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     P = both(-0.f);
                 }
                 const int r = BWD ? kTile - 1 - (w * S + i) : w * S + i;
-                al[i] = decay(values(read2<A>(st.la[r], lane)));
-                x[i] = read2<A>(st.x[r], lane);
+                const int ol = A == kWide ? 0 : sl(r);
+                const int ox = A == kWide ? 0 : sx(r);
+                al[i] = decay(values(read2<A>(st.la[r] + ol, lane)));
+                x[i] = read2<A>(st.x[r] + ox, lane);
                 P = mul2(P, al[i]);
                 if constexpr (BWD) {
-                    g[i] = read2<A>(st.g[r], lane);
+                    const int og = A == kWide ? 0 : sg(r);
+                    g[i] = read2<A>(st.g[r] + og, lane);
                     H = mul2(al[i], add2(H, values(g[i])));
                 } else {
                     H = fma2(al[i], H, values(x[i]));
@@ -490,8 +524,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         };
         if (plain) reduce(std::false_type());
         else reduce(std::true_type());
-        sh.own[s][w][lane] =
+        const float4 mine =
             make_float4(bounded(P.x), bounded(P.y), H.x, H.y);
+        if (w < W - 1) sh.own[s][w][lane] = mine;
         // the stage is free, the maps are there
         if (__syncthreads_or(fault)) {
             fault = true;
@@ -501,62 +536,53 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         fetch(ahead, s);
         ++issued;
 
-        // which of the warps' maps start anew
-        const unsigned int cut = __ballot_sync(
-            0xffffffffu, lane < W && fresh(sh.own[s][lane % W][0]));
+        const int m = here.k % here.step, h = hops & 1;
+        const int there = min(here.step, plan.tiles - (here.k - m));
+        float4(*team)[32] = maps + h * here.step;
+        if (w == W - 1) {            // the tile's map, to all of the team
+            float4 t = sh.own[s][0][lane];
+            bool cut = fresh(t);
+#pragma unroll
+            for (int u = 1; u < W; ++u) {
+                const float4 q = u < W - 1 ? sh.own[s][u][lane] : mine;
+                const bool f = fresh(q);
+                const float2 v = f ? make_float2(q.z, q.w)
+                                   : plain_apply(q, make_float2(t.z, t.w));
+                t = make_float4(bounded(t.x * q.x), bounded(t.y * q.y), v.x,
+                                v.y);
+                cut |= f;
+            }
+            if (cut) t.x = t.y = -0.f;
+            if (lane == 0)
+                tc::mbar_arrive_expect_tx(&sh.got[h], there * 512);
+            __syncwarp();
+            // a block that walks alone is its own team of one
+            const int first = here.step > 1 ? 0 : blockIdx.x % plan.team;
+            for (int r = 0; r < there; ++r)
+                send(&team[m][lane], &sh.got[h], first + r, t);
+        }
+        // meanwhile: what the next tile will need to know
+        Cursor then = here;
+        then.move(plan);
+        soon = bounds_of(then);
+        fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
+        ++hops;
+
         float2 c = carry;            // the state before the tile
-        if (here.step > 1) {
-            const int m = here.k % here.step, h = hops & 1;
-            const int there = min(here.step, plan.tiles - (here.k - m));
-            float4(*team)[32] = maps + h * here.step;
-            if (w == 0) {
-                float4 t = sh.own[s][0][lane];
+        for (int j0 = 0; j0 < there; j0 += 4) {
+            float4 q[4];
 #pragma unroll
-                for (int u = 1; u < W; ++u) {
-                    const float4 q = sh.own[s][u][lane];
-                    const float2 v = cut >> u & 1
-                                         ? make_float2(q.z, q.w)
-                                         : plain_apply(q, make_float2(t.z,
-                                                                      t.w));
-                    t = make_float4(bounded(t.x * q.x), bounded(t.y * q.y),
-                                    v.x, v.y);
-                }
-                if (cut) t.x = t.y = -0.f;
-                if (lane == 0)
-                    tc::mbar_arrive_expect_tx(&sh.got[h], there * 512);
-                __syncwarp();
-                for (int r = 0; r < there; ++r)
-                    send(&team[m][lane], &sh.got[h], r, t);
-            }
-            fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
-            ++hops;
-            const unsigned int anew = __ballot_sync(
-                0xffffffffu, lane < there && fresh(team[lane % there][0]));
-            if (anew == 0) {
-#pragma unroll 4
-                for (int j = 0; j < there; ++j) {
-                    if (j == m) c = carry;
-                    carry = plain_apply(team[j][lane], carry);
-                }
-            } else {
-                for (int j = 0; j < there; ++j) {
-                    if (j == m) c = carry;
-                    carry = apply(team[j][lane], carry);
-                }
+            for (int i = 0; i < 4; ++i)
+                q[i] = team[min(j0 + i, there - 1)][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (j0 + i == m) c = carry;
+                if (j0 + i < there) carry = apply(q[i], carry);
             }
         }
-        if (cut == 0) {
 #pragma unroll
-            for (int u = 0; u < W - 1; ++u)
-                if (u < w) c = plain_apply(sh.own[s][u][lane], c);
-        } else {
-            for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
-        }
-        if (here.step == 1) {
-            carry = c;
-            for (int u = w; u < W; ++u)
-                carry = apply(sh.own[s][u][lane], carry);
-        }
+        for (int u = 0; u < W - 1; ++u)
+            if (u < w) c = apply(sh.own[s][u][lane], c);
 
         const size_t out = ((size_t)b * a.T + t0) * a.D + da;
         T* op = static_cast<T*>(a.o) + out;
@@ -601,7 +627,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 if (a.cu[e] == a.cu[e + 1])
                     keep_state((int)e, state_of(init, (int)e));
         }
-        here.move(plan);
+        here = then;
     }
     if (A != kWide) asm volatile("cp.async.wait_all;" ::: "memory");
     if (fault && threadIdx.x == 0) {
@@ -644,28 +670,62 @@ cudaError_t by_type(kla_dtype t, kla_dtype g, F f) {
 
 namespace {
 
-// How `chains` chains of `tiles` tiles share the blocks that the SMs hold:
-// whole rounds of a chain per block, then the rest by teams as large as fit
-// (powers of two, which fill a GPC's SMs best).
-template <typename T, typename G, bool BWD>
+template <typename T, typename G, Align A, bool BWD>
+void team_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
+                 int blocks, int team) {
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared_bytes<T, G, A, BWD>(team);
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = team;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+}
+
+// Blocks in teams of 2^i that the current GPU holds at the same time (looked
+// up once per device).
+template <typename T, typename G, Align A, bool BWD>
+int capacity(int i) {
+    static std::atomic<int> found[64][5];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = found[dev][i].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    team_config<T, G, A, BWD>(cfg, attr, 1 << i, 1 << i);
+    if (cudaOccupancyMaxActiveClusters(&n, glr_scan_kernel<T, G, A, BWD>,
+                                       &cfg) != cudaSuccess)
+        return 0;
+    n <<= i;
+    found[dev][i].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// How `chains` chains of `tiles` tiles share the blocks that the GPU holds:
+// whole rounds of a chain per block, then the rest by a team each.  A round
+// counts as 1, a team of t as 1 / t.
+template <typename T, typename G, Align A, bool BWD>
 ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
-    ScanPlan p{tiles, (D + CH - 1) / CH, 0, 0, 1};
+    ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1};
     *blocks = 0;
-    for (int per = resident<T, G, BWD>(1); per > 0; --per) {
-        const int slots = per * device_sm_count() / kMaxTeam * kMaxTeam;
+    double cost = 0;
+    for (int i = 0; i < 5 && (1 << i) <= tiles; ++i) {
+        const int team = 1 << i;
+        const int slots = capacity<T, G, A, BWD>(i);
         if (slots <= 0) break;
-        p.rounds = (int)(chains / slots);
-        p.rest = (int)(chains % slots);
-        p.team = 1;
-        while (p.rest && 2 * p.team <= kMaxTeam && 2 * p.team <= tiles &&
-               2 * p.team * p.rest <= slots)
-            p.team *= 2;
-        // the maps of a large team may take the room of a block
-        if (resident<T, G, BWD>(p.team) < per) continue;
-        *blocks = p.rounds ? slots : p.rest * p.team;
-        break;
+        const int rounds = (int)(chains / slots), rest = (int)(chains % slots);
+        if ((long long)rest * team > slots) break;
+        const double c = rounds + (rest ? 1.0 / team : 0.0);
+        if (*blocks && c >= cost) continue;
+        cost = c;
+        best.rounds = rounds;
+        best.rest = rest;
+        best.team = team;
+        *blocks = rounds ? slots : rest * team;
     }
-    return p;
+    return best;
 }
 
 // The element's tensor map over [B, T, D] with boxes of kTile tokens x CH
@@ -695,8 +755,16 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
     const long long chains =
         (long long)((a.D + CH - 1) / CH) * (a.cu ? 1 : a.B);
     if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
+    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
+    cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        shared_bytes<T, G, A, BWD>(kMaxTeam));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     int blocks = 0;
-    const ScanPlan p = plan_of<T, G, BWD>(
+    const ScanPlan p = plan_of<T, G, A, BWD>(
         chains, (int)((a.T + (long long)kTile - 1) / kTile), a.D, &blocks);
     if (blocks <= 0) return cudaErrorInvalidValue;
     CUtensorMap mx{}, ml{}, mg{};
@@ -704,27 +772,10 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
         (!make_tile_map<T>(&mx, a.x, a) || !make_tile_map<G>(&ml, a.la, a) ||
          (BWD && !make_tile_map<T>(&mg, a.g, a))))
         return cudaErrorInvalidValue;
-    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
-    cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        shared_bytes<T, G, BWD>(kMaxTeam));
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = shared_bytes<T, G, BWD>(p.team);
-    cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.team;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.team > 1 ? 1 : 0;
-    if (p.team > 8) {
-        e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    team_config<T, G, A, BWD>(cfg, attr, blocks, p.team);
+    cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kernel, a, p, mx, ml, mg);
 }
 
