@@ -60,47 +60,49 @@ struct ScanPlan {
 __device__ unsigned int g_fault_glr = 0;
 
 // Arithmetic on a lane's two channels at once (one instruction each).
-__device__ __forceinline__ uint64_t bits(float2 x) {
-    return (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
-}
-__device__ __forceinline__ float2 floats(uint64_t b) {
-    return make_float2(__uint_as_float((unsigned int)b),
-                       __uint_as_float((unsigned int)(b >> 32)));
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(d)
-        : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return floats(d);
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return floats(d);
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return floats(d);
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // exp of two log decays.  Near 0, where a state remembers 1 / -l tokens and
-// a decay's error is multiplied by as much, the Taylor polynomial of degree
-// 5 rounds correctly nearly always (|l| <= 1/8: at most 0.73 units of 2^-24
-// measured, mean 0; expf: 1.8, mean up to 0.26).  Elsewhere 2^(l log2 e) by
-// the hardware's approximation (2.6 units at l = -1, 8 at l = -8).
+// a decay's error is multiplied by as much, 1 + l + l^2 / 2 + l^3 / 6 (|l| <=
+// 1/64: the rest of the series is below 2^-28, so that the last addition
+// rounds correctly nearly always).  Elsewhere 2^(l log2 e) by the hardware's
+// approximation (about 2 units of 2^-24 up to l = -1, 8 at l = -8).
 __device__ __forceinline__ float2 decay(float2 l) {
-    float2 p = fma2(l, both(1.f / 120), both(1.f / 24));
-    p = fma2(l, p, both(1.f / 6));
-    p = fma2(l, p, both(0.5f));
+    float2 p = fma2(l, both(1.f / 6), both(0.5f));
     p = fma2(l, p, both(1.f));
     p = fma2(l, p, both(1.f));
     const float2 t = mul2(l, both(1.44269504f));
     const float ex = tc::ex2(t.x), ey = tc::ex2(t.y);
-    return make_float2(fabsf(l.x) <= 0.125f ? p.x : ex,
-                       fabsf(l.y) <= 0.125f ? p.y : ey);
+    return make_float2(fabsf(l.x) <= 0x1p-6f ? p.x : ex,
+                       fabsf(l.y) <= 0x1p-6f ? p.y : ey);
 }
 
 // Maps of two channels as (P.x, P.y, H.x, H.y).  P is finite (see `bounded`),
@@ -215,21 +217,30 @@ __device__ __forceinline__ void copy_rows(T* dst, const T* src,
                                           long long stride, long long t,
                                           int n, int room) {
     constexpr int P = kPitch<A, T> * sizeof(T) / 16;   // pieces of a row
+    static_assert(kThreads % (P - 1) == 0 && kThreads >= kTile, "");
+    const uintptr_t none =
+        reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15;
     const int bytes = min(room, CH) * (int)sizeof(T);
-    for (int q = threadIdx.x; q < kTile * P; q += kThreads) {
-        const int r = q / P, piece = q % P;
-        const uintptr_t row =
-            reinterpret_cast<uintptr_t>(src + (t + r) * stride);
-        const uintptr_t from = (row & ~(uintptr_t)15) + piece * 16;
-        const long long left = (long long)(row + bytes) - (long long)from;
+    const unsigned int to = tc::smem_u32(dst);
+    auto piece = [&](int r, int p, uintptr_t row) {
+        const uintptr_t from = (row & ~(uintptr_t)15) + p * 16;
+        const int left = (int)(row - from) + bytes;
         const bool in = t + r >= 0 && t + r < n && left > 0;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         tc::smem_u32(dst) + q * 16),
-                     "l"(in ? from : reinterpret_cast<uintptr_t>(src) &
-                                         ~(uintptr_t)15),
-                     "r"(in ? (int)min(left, 16ll) : 0)
+                         to + (r * P + p) * 16),
+                     "l"(in ? from : none), "r"(in ? min(left, 16) : 0)
                      : "memory");
-    }
+    };
+    // all pieces but the last: a thread keeps its place in the row
+    constexpr int R = kThreads / (P - 1);
+    const int r0 = threadIdx.x / (P - 1), p0 = threadIdx.x % (P - 1);
+    uintptr_t row = reinterpret_cast<uintptr_t>(src + (t + r0) * stride);
+    const long long by = R * stride * (long long)sizeof(T);
+#pragma unroll 4
+    for (int r = r0; r < kTile; r += R, row += by) piece(r, p0, row);
+    if (threadIdx.x < kTile)
+        piece(threadIdx.x, P - 1,
+              reinterpret_cast<uintptr_t>(src + (t + threadIdx.x) * stride));
 }
 // Where a row starts within its first piece (elements): of row t, and how
 // that moves from row to row.
@@ -259,16 +270,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
 // Where sequences begin and end among S tokens of one warp, and which.  In
 // scan order: bit i of `mask` says that a sequence begins at step i, which is
 // also the end of the one before it, after step i - 1; n is the sequence of
-// step 0.
+// step 0, last the one that begins last (if any does).
 struct Bounds {
     unsigned int mask;
-    int n;
+    int n, last;
 };
 
 // Packed sequences: the boundaries among the S tokens from t on (upwards, or
 // downwards with BACK).  A warp works together: a 32-way search for the
 // sequence of t, then 32 offsets at a time.  Any content of cu gives
-// 0 <= n < B.
+// 0 <= n, last < B.
 template <bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
                                               long long t) {
@@ -284,6 +295,7 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
         len = min(step, len - skip);
     }
     unsigned int mask = 0;
+    int last = lo;                   // the outermost boundary before step S
     for (int j0 = BACK ? lo + 1 : lo;;) {
         const int j = BACK ? j0 - lane : j0 + lane;
         long long pos = -1;          // step at which the boundary lies
@@ -292,12 +304,17 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
             pos = BACK ? t + 1 - cu[j] : cu[j] - t;
             beyond = pos > S;
         }
-        mask |= __reduce_or_sync(0xffffffffu,
-                                 pos >= 0 && pos <= S ? 1u << pos : 0u);
+        const bool in = pos >= 0 && pos <= S;
+        mask |= __reduce_or_sync(0xffffffffu, in ? 1u << pos : 0u);
+        // upwards the sequence from the last such offset on, downwards the
+        // one up to the first
+        const int at = in && pos < S ? (BACK ? j - 1 : j) : last;
+        last = BACK ? __reduce_min_sync(0xffffffffu, at)
+                    : __reduce_max_sync(0xffffffffu, at);
         if (__any_sync(0xffffffffu, beyond)) break;
         j0 += BACK ? -32 : 32;
     }
-    return {mask, lo};
+    return {mask, lo, min(max(last, 0), B - 1)};
 }
 
 // The tiles of a block, in its order: tile k of the run of tokens b, channels
@@ -343,6 +360,7 @@ struct Shared {
     Stage<T, G, A, BWD> stage[2];
     // the maps of all warps but the last, of this tile and the next
     float4 own[2][W - 1][32];
+    float2 start[32];            // the state before the tile
     uint64_t full[2], got[2];    // a stage has its tile; a step has its maps
 };
 
@@ -391,7 +409,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             const int b = at.b, d = at.d;
             const int p = at.k * kTile;
             const int lo = BWD ? a.T - kTile - p : p;
-            if (A == kWide) {
+            if constexpr (A == kWide) {
                 tc::mbar_arrive_expect_tx(&sh.full[s], sizeof(st));
                 tma_load_3d(&st.la[0][0], &map_la, &sh.full[s], d, lo, b);
                 tma_load_3d(&st.x[0][0], &map_x, &sh.full[s], d,
@@ -416,27 +434,54 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (A != kWide) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    // The boundaries among the warp's tokens of a tile.
-    auto bounds_of = [&](const Cursor& at) {
-        Bounds bd{0u, at.b};
-        const int p = at.k * kTile + w * S;
-        if (!at.more || p >= a.T) return bd;
-        if (a.cu) return find_bounds<BWD>(a.cu, a.B, BWD ? a.T - 1 - p : p);
-        if (p == 0) bd.mask = 1u;
-        if (a.T - p <= S) bd.mask |= 1u << (a.T - p);
-        return bd;
-    };
-
     Cursor here(plan), ahead = here;
     fetch(ahead, 0);
     ahead.move(plan);
     fetch(ahead, 1);
-    Bounds soon = bounds_of(here);
+    // What a warp needs to know of its tokens: the boundaries; the start of
+    // the sequence that begins last (whoever ends it may write its last state
+    // in the place of this start, hT == h0, once the team has this tile's
+    // map); backwards, the state before the sequence that ends first.  Looked
+    // up a tile ahead, except that without packing most tiles have none.
+    Bounds soon{0u, here.b, here.b};
+    float2 soon_start = both(0.f), soon_prev = both(0.f);
+    auto look = [&](const Cursor& at) {
+        const int p = at.k * kTile + w * S;
+        soon = Bounds{0u, at.b, at.b};
+        if (a.cu) {
+            if (!at.more || p >= a.T) return;
+            soon = find_bounds<BWD>(a.cu, a.B, BWD ? a.T - 1 - p : p);
+        } else {
+            if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
+            if (p == 0) soon.mask = 1u;
+            if (a.T - p <= S) soon.mask |= 1u << (a.T - p);
+        }
+        const int da = at.d + channel<A>(lane, 0);
+        const int db = at.d + channel<A>(lane, 1);
+        if (init && (soon.mask & ((1u << S) - 1))) {
+            const float* q = init + (size_t)soon.last * a.D;
+            if (da < a.D) soon_start.x = q[da];
+            if (db < a.D) soon_start.y = q[db];
+        }
+        if (BWD && a.h0 && soon.mask >> 1) {
+            const float* q = a.h0 + (size_t)soon.n * a.D;
+            if (da < a.D) soon_prev.x = q[da];
+            if (db < a.D) soon_prev.y = q[db];
+        }
+    };
+    look(here);
 
+    // blocks that walked chains alone meet before they work as a team: no map
+    // may come while its buffer and barrier are in use otherwise
+    bool apart = plan.rounds > 0 && plan.team > 1;
     float2 carry = both(0.f);        // the state before the team's tiles
     bool fault = false;
     unsigned int turn = 0, issued = 2;           // copies started
     for (unsigned int hops = 0; here.more; ++turn) {
+        if (apart && here.step > 1) {
+            cluster_sync();
+            apart = false;
+        }
         const int s = turn & 1;
         const Stage<T, G, A, BWD>& st = sh.stage[s];
         const int b = here.b;
@@ -450,6 +495,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (here.k < here.step) carry = both(0.f);       // a chain begins
 
         const Bounds bd = soon;
+        const float2 start = soon_start, prev = soon_prev;
+        // whether some map of this step may start anew
+        const bool anew = a.cu || here.k < here.step;
         const unsigned int begins = bd.mask & ((1u << S) - 1);
         // nothing begins, ends or is missing here
         const bool plain = bd.mask == 0 && steps == S;
@@ -486,10 +534,6 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         float2 al[S];                // decays
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
         float2 P = both(1.f), H = both(0.f);
-        // the start of the last sequence that begins here: whoever ends it
-        // may write its last state in the place of this start (hT == h0)
-        // before the second pass
-        float2 kept = both(0.f);
         int n = bd.n;
         // rows that do not line up on 16 bytes: where each starts
         const int lo = BWD ? a.T - kTile - here.k * kTile : here.k * kTile;
@@ -503,8 +547,12 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (decltype(events)::value && begins >> i & 1) {
-                    next(i, n);
-                    kept = H = state_of(init, n);
+                    if (begins >> (i + 1)) {
+                        next(i, n);
+                        H = state_of(init, n);
+                    } else {
+                        H = start;
+                    }
                     P = both(-0.f);
                 }
                 const int r = BWD ? kTile - 1 - (w * S + i) : w * S + i;
@@ -545,12 +593,15 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
 #pragma unroll
             for (int u = 1; u < W; ++u) {
                 const float4 q = u < W - 1 ? sh.own[s][u][lane] : mine;
-                const bool f = fresh(q);
-                const float2 v = f ? make_float2(q.z, q.w)
-                                   : plain_apply(q, make_float2(t.z, t.w));
-                t = make_float4(bounded(t.x * q.x), bounded(t.y * q.y), v.x,
-                                v.y);
-                cut |= f;
+                const float2 v = plain_apply(q, make_float2(t.z, t.w));
+                const float2 pq =
+                    mul2(make_float2(t.x, t.y), make_float2(q.x, q.y));
+                t = make_float4(bounded(pq.x), bounded(pq.y), v.x, v.y);
+                if (anew && fresh(q)) {
+                    t.z = q.z;
+                    t.w = q.w;
+                    cut = true;
+                }
             }
             if (cut) t.x = t.y = -0.f;
             if (lane == 0)
@@ -558,31 +609,41 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             __syncwarp();
             // a block that walks alone is its own team of one
             const int first = here.step > 1 ? 0 : blockIdx.x % plan.team;
+#pragma unroll 4
             for (int r = 0; r < there; ++r)
                 send(&team[m][lane], &sh.got[h], first + r, t);
         }
-        // meanwhile: what the next tile will need to know
+        // meanwhile
         Cursor then = here;
         then.move(plan);
-        soon = bounds_of(then);
-        fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
-        ++hops;
-
-        float2 c = carry;            // the state before the tile
-        for (int j0 = 0; j0 < there; j0 += 4) {
-            float4 q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                q[i] = team[min(j0 + i, there - 1)][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (j0 + i == m) c = carry;
-                if (j0 + i < there) carry = apply(q[i], carry);
+        look(then);
+        if (w == 0) {                // the state before the tile, and after
+            fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
+            if (anew) {
+                for (int j = 0; j < there; ++j) {
+                    if (j == m) sh.start[lane] = carry;
+                    carry = apply(team[j][lane], carry);
+                }
+            } else {
+                int j = 0;
+#pragma unroll 4
+                for (; j < m; ++j) carry = plain_apply(team[j][lane], carry);
+                sh.start[lane] = carry;
+#pragma unroll 4
+                for (; j < there; ++j)
+                    carry = plain_apply(team[j][lane], carry);
             }
         }
+        ++hops;
+        __syncthreads();
+        float2 c = sh.start[lane];
+        if (anew) {
+            for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
+        } else {
 #pragma unroll
-        for (int u = 0; u < W - 1; ++u)
-            if (u < w) c = apply(sh.own[s][u][lane], c);
+            for (int u = 0; u < W - 1; ++u)
+                if (u < w) c = plain_apply(sh.own[s][u][lane], c);
+        }
 
         const size_t out = ((size_t)b * a.T + t0) * a.D + da;
         T* op = static_cast<T*>(a.o) + out;
@@ -594,15 +655,20 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 if (decltype(events)::value) {
                     if (i >= steps) break;
                     if (begins >> i & 1) {
-                        next(i, n);
-                        c = begins >> (i + 1) ? state_of(init, n) : kept;
+                        if (begins >> (i + 1)) {
+                            next(i, n);
+                            c = state_of(init, n);
+                        } else {
+                            n = bd.last;
+                            c = start;
+                        }
                     }
                 }
                 const bool ends =
                     decltype(events)::value && (bd.mask >> (i + 1) & 1);
                 if constexpr (BWD) {
                     float2 h = values(x[i]);
-                    if (ends) h = state_of(a.h0, n);
+                    if (ends) h = n == bd.n ? prev : state_of(a.h0, n);
                     c = add2(c, values(g[i]));
                     write2<A>(op, la, lb, c);
                     c = mul2(al[i], c);
@@ -636,6 +702,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         for (++turn; A == kWide && turn < issued; ++turn)
             tc::mbar_wait(&sh.full[turn & 1], (turn >> 1) & 1, 1000000);
     }
+    if (apart) cluster_sync();
     if (plan.team > 1) cluster_sync();           // nobody sends here any more
     else if (fault) __syncthreads();
 }
