@@ -24,9 +24,8 @@ using bf16 = __nv_bfloat16;
 // tokens (a batch entry, or all packed tokens) and one group of channels form
 // a chain.  A chain is walked by a team of G blocks, a thread-block cluster,
 // which take every G-th tile each, in order; a block
-//   1. waits for its tile's inputs, which were copied into shared memory
-//      while it worked on the tile before (two stages), takes them into
-//      registers and hands the stage over to the copy of a later tile,
+//   1. waits for its tile's inputs in shared memory, takes them into
+//      registers, and starts the copy of its next tile,
 //   2. reduces each warp's S steps to the affine map c -> P c + H of the
 //      state, and the warps' maps to the tile's map,
 //   3. sends the tile's map to all blocks of the team (st.async into their
@@ -49,6 +48,7 @@ constexpr int S = 16;            // tokens of a warp
 constexpr int kTile = W * S;
 constexpr int CH = 64;           // channels of a tile
 constexpr int kThreads = 32 * W;
+constexpr int kMaxKept = 512;    // offsets of sequences kept on chip
 constexpr int kMaxTeam = 16;     // blocks of a team: the largest cluster
 
 struct ScanPlan {
@@ -357,28 +357,28 @@ struct Stage<T, G, A, true> {
 };
 template <typename T, typename G, Align A, bool BWD>
 struct Shared {
-    Stage<T, G, A, BWD> stage[2];
+    Stage<T, G, A, BWD> stage;
     // the maps of all warps but the last, of this tile and the next
     float4 own[2][W - 1][32];
     float2 start[32];            // the state before the tile
-    uint64_t full[2], got[2];    // a stage has its tile; a step has its maps
+    int cu[kMaxKept];            // packed sequences: their offsets, if few
+    uint64_t full, got[2];       // the tile is there; the step's maps are
 };
 
-// Shared memory of a block of a team, and how many such blocks an SM holds
-// (228 KB, 1 KB of it per block the system's), at most 4: 128 registers a
-// thread.
 template <typename T, typename G, Align A, bool BWD>
 constexpr int shared_bytes(int team) {
     return (int)sizeof(Shared<T, G, A, BWD>) + 2 * team * 512;
 }
-template <typename T, typename G, Align A, bool BWD>
+// Blocks that an SM is to hold: as many as leave the registers that a thread
+// needs (128 with 4 blocks, 168 with 3; with one block more each, the kernel
+// spills and the 2048-wide layer takes 63 instead of 51 us).
+template <typename T, bool BWD>
 constexpr int resident() {
-    return std::min(4,
-                    228 * 1024 / (shared_bytes<T, G, A, BWD>(1) + 1024));
+    return sizeof(T) == 2 && !BWD ? 4 : 3;
 }
 
 template <typename T, typename G, Align A, bool BWD>
-__global__ void __launch_bounds__(kThreads, (resident<T, G, A, BWD>()))
+__global__ void __launch_bounds__(kThreads, (resident<T, BWD>()))
 glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 const __grid_constant__ ScanPlan plan,
                 const __grid_constant__ CUtensorMap map_x,
@@ -393,29 +393,33 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     const float* init = BWD ? a.dhT : a.h0;
 
     if (threadIdx.x == 0) {
-        for (uint64_t* bar : {&sh.full[0], &sh.full[1], &sh.got[0],
-                              &sh.got[1]})
+        for (uint64_t* bar : {&sh.full, &sh.got[0], &sh.got[1]})
             tc::mbar_init(bar, 1);
         tc::fence_mbar_init();
     }
+    const int* cu = a.cu;
+    if (a.cu && a.B < kMaxKept) {
+        for (int i = threadIdx.x; i <= a.B; i += kThreads) sh.cu[i] = a.cu[i];
+        cu = sh.cu;
+    }
     if (plan.team > 1) cluster_sync();
     else __syncthreads();
-    // Starts the copy of a tile's inputs into a stage: row r of it is token
-    // lo + r, lo the tile's lowest token.
-    auto fetch = [&](const Cursor& at, int s) {
-        Stage<T, G, A, BWD>& st = sh.stage[s];
+    // Starts the copy of a tile's inputs: row r is token lo + r, lo the tile's
+    // lowest token.
+    Stage<T, G, A, BWD>& st = sh.stage;
+    auto fetch = [&](const Cursor& at) {
         // (the last warp has the tile's map to form meanwhile)
         if (at.more && (A != kWide || threadIdx.x == 0)) {
             const int b = at.b, d = at.d;
             const int p = at.k * kTile;
             const int lo = BWD ? a.T - kTile - p : p;
             if constexpr (A == kWide) {
-                tc::mbar_arrive_expect_tx(&sh.full[s], sizeof(st));
-                tma_load_3d(&st.la[0][0], &map_la, &sh.full[s], d, lo, b);
-                tma_load_3d(&st.x[0][0], &map_x, &sh.full[s], d,
+                tc::mbar_arrive_expect_tx(&sh.full, sizeof(st));
+                tma_load_3d(&st.la[0][0], &map_la, &sh.full, d, lo, b);
+                tma_load_3d(&st.x[0][0], &map_x, &sh.full, d,
                             BWD ? lo - 1 : lo, b);
                 if constexpr (BWD)
-                    tma_load_3d(&st.g[0][0], &map_g, &sh.full[s], d, lo, b);
+                    tma_load_3d(&st.g[0][0], &map_g, &sh.full, d, lo, b);
             } else {
                 const int room = a.D - d;
                 copy_rows<A>(&st.la[0][0],
@@ -434,10 +438,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (A != kWide) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    Cursor here(plan), ahead = here;
-    fetch(ahead, 0);
-    ahead.move(plan);
-    fetch(ahead, 1);
+    Cursor here(plan);
+    fetch(here);
     // What a warp needs to know of its tokens: the boundaries; the start of
     // the sequence that begins last (whoever ends it may write its last state
     // in the place of this start, hT == h0, once the team has this tile's
@@ -450,7 +452,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         soon = Bounds{0u, at.b, at.b};
         if (a.cu) {
             if (!at.more || p >= a.T) return;
-            soon = find_bounds<BWD>(a.cu, a.B, BWD ? a.T - 1 - p : p);
+            soon = find_bounds<BWD>(cu, a.B, BWD ? a.T - 1 - p : p);
         } else {
             if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
             if (p == 0) soon.mask = 1u;
@@ -476,14 +478,13 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     bool apart = plan.rounds > 0 && plan.team > 1;
     float2 carry = both(0.f);        // the state before the team's tiles
     bool fault = false;
-    unsigned int turn = 0, issued = 2;           // copies started
-    for (unsigned int hops = 0; here.more; ++turn) {
+    unsigned int turn = 0;
+    for (; here.more; ++turn) {
         if (apart && here.step > 1) {
             cluster_sync();
             apart = false;
         }
-        const int s = turn & 1;
-        const Stage<T, G, A, BWD>& st = sh.stage[s];
+        const int h = turn & 1;
         const int b = here.b;
         const int da = here.d + channel<A>(lane, 0);
         const int db = here.d + channel<A>(lane, 1);
@@ -508,10 +509,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             const int t = t0 + i * DT;
             if (BWD) {
                 n = max(n - 1, 0);
-                while (n > 0 && a.cu[n] > t) --n;
+                while (n > 0 && cu[n] > t) --n;
             } else {
                 n = min(n + 1, a.B - 1);
-                while (n < a.B - 1 && a.cu[n + 1] <= t) ++n;
+                while (n < a.B - 1 && cu[n + 1] <= t) ++n;
             }
         };
         auto state_of = [&](const float* p, int n) {
@@ -525,11 +526,12 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             if (a.hT && lb) a.hT[(size_t)n * a.D + db] = c.y;
         };
 
-        if (A == kWide)
-            fault |= !tc::mbar_wait(&sh.full[s], (turn >> 1) & 1);
-        else
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        if (A != kWide) __syncthreads();
+        if (A == kWide) {
+            fault |= !tc::mbar_wait(&sh.full, h);
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+        }
 
         float2 al[S];                // decays
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
@@ -574,25 +576,25 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         else reduce(std::true_type());
         const float4 mine =
             make_float4(bounded(P.x), bounded(P.y), H.x, H.y);
-        if (w < W - 1) sh.own[s][w][lane] = mine;
-        // the stage is free, the maps are there
+        if (w < W - 1) sh.own[h][w][lane] = mine;
+        // the tile's place is free, the maps are there
         if (__syncthreads_or(fault)) {
             fault = true;
             break;
         }
-        ahead.move(plan);
-        fetch(ahead, s);
-        ++issued;
+        Cursor then = here;
+        then.move(plan);
+        fetch(then);
 
-        const int m = here.k % here.step, h = hops & 1;
+        const int m = here.k % here.step;
         const int there = min(here.step, plan.tiles - (here.k - m));
         float4(*team)[32] = maps + h * here.step;
         if (w == W - 1) {            // the tile's map, to all of the team
-            float4 t = sh.own[s][0][lane];
+            float4 t = sh.own[h][0][lane];
             bool cut = fresh(t);
 #pragma unroll
             for (int u = 1; u < W; ++u) {
-                const float4 q = u < W - 1 ? sh.own[s][u][lane] : mine;
+                const float4 q = u < W - 1 ? sh.own[h][u][lane] : mine;
                 const float2 v = plain_apply(q, make_float2(t.z, t.w));
                 const float2 pq =
                     mul2(make_float2(t.x, t.y), make_float2(q.x, q.y));
@@ -613,12 +615,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             for (int r = 0; r < there; ++r)
                 send(&team[m][lane], &sh.got[h], first + r, t);
         }
-        // meanwhile
-        Cursor then = here;
-        then.move(plan);
-        look(then);
+        look(then);                  // meanwhile
         if (w == 0) {                // the state before the tile, and after
-            fault |= !wait_maps(&sh.got[h], hops >> 1 & 1);
+            fault |= !wait_maps(&sh.got[h], turn >> 1 & 1);
             if (anew) {
                 for (int j = 0; j < there; ++j) {
                     if (j == m) sh.start[lane] = carry;
@@ -634,15 +633,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     carry = plain_apply(team[j][lane], carry);
             }
         }
-        ++hops;
         __syncthreads();
         float2 c = sh.start[lane];
         if (anew) {
-            for (int u = 0; u < w; ++u) c = apply(sh.own[s][u][lane], c);
+            for (int u = 0; u < w; ++u) c = apply(sh.own[h][u][lane], c);
         } else {
 #pragma unroll
             for (int u = 0; u < W - 1; ++u)
-                if (u < w) c = plain_apply(sh.own[s][u][lane], c);
+                if (u < w) c = plain_apply(sh.own[h][u][lane], c);
         }
 
         const size_t out = ((size_t)b * a.T + t0) * a.D + da;
@@ -690,7 +688,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (a.cu && a.hT && a.hT != init) {
             for (long long e = (long long)here.k * W + w; e < a.B;
                  e += (long long)plan.tiles * W)
-                if (a.cu[e] == a.cu[e + 1])
+                if (cu[e] == cu[e + 1])
                     keep_state((int)e, state_of(init, (int)e));
         }
         here = then;
@@ -698,9 +696,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     if (A != kWide) asm volatile("cp.async.wait_all;" ::: "memory");
     if (fault && threadIdx.x == 0) {
         atomicOr(&g_fault_glr, 1u);
-        // copies that may be on their way yet
-        for (++turn; A == kWide && turn < issued; ++turn)
-            tc::mbar_wait(&sh.full[turn & 1], (turn >> 1) & 1, 1000000);
+        // a copy that may be on its way yet
+        if (A == kWide) tc::mbar_wait(&sh.full, ~turn & 1, 1000000);
     }
     if (apart) cluster_sync();
     if (plan.team > 1) cluster_sync();           // nobody sends here any more
@@ -750,23 +747,23 @@ void team_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
     cfg.numAttrs = 1;
 }
 
-// Blocks in teams of 2^i that the current GPU holds at the same time (looked
+// Blocks in teams of `team` that the current GPU holds at the same time (looked
 // up once per device).
 template <typename T, typename G, Align A, bool BWD>
-int capacity(int i) {
-    static std::atomic<int> found[64][5];
+int capacity(int team) {
+    static std::atomic<int> found[64][kMaxTeam + 1];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = found[dev][i].load(std::memory_order_relaxed);
+    int n = found[dev][team].load(std::memory_order_relaxed);
     if (n > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    team_config<T, G, A, BWD>(cfg, attr, 1 << i, 1 << i);
+    team_config<T, G, A, BWD>(cfg, attr, team, team);
     if (cudaOccupancyMaxActiveClusters(&n, glr_scan_kernel<T, G, A, BWD>,
                                        &cfg) != cudaSuccess)
         return 0;
-    n <<= i;
-    found[dev][i].store(n, std::memory_order_relaxed);
+    n *= team;
+    found[dev][team].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -778,12 +775,11 @@ ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
     ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1};
     *blocks = 0;
     double cost = 0;
-    for (int i = 0; i < 5 && (1 << i) <= tiles; ++i) {
-        const int team = 1 << i;
-        const int slots = capacity<T, G, A, BWD>(i);
+    for (int team = 1; team <= std::min(kMaxTeam, tiles); ++team) {
+        const int slots = capacity<T, G, A, BWD>(team);
         if (slots <= 0) break;
         const int rounds = (int)(chains / slots), rest = (int)(chains % slots);
-        if ((long long)rest * team > slots) break;
+        if ((long long)rest * team > slots) continue;
         const double c = rounds + (rest ? 1.0 / team : 0.0);
         if (*blocks && c >= cost) continue;
         cost = c;
