@@ -552,15 +552,22 @@ def decode_step_kw(q, k, k_write, v, log_alpha, eta, S, eps: float = 1e-6,
 
 
 # --- layer norm and the gated linear recurrence ----------------------------
+# These calls are short on the GPU, so the checks take the quick way out for
+# the ordinary tensor (contiguous, of the right type and shape) and go through
+# the details only for others.
+
+_F32, _IO = (torch.float32,), tuple(DTYPES)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _tensor(name, t, device, dtypes, shape=None, packed_last=True):
-    """Checks a tensor of the call: on ``device``, of one of ``dtypes``, of
-    ``shape`` (when given), its last axis adjacent; contiguous unless
-    ``packed_last`` says that the last axis is enough."""
+def _check(name, t, device, dtypes, shape=None, packed_last=True):
+    """Raises unless t is a tensor on ``device`` of one of ``dtypes`` and of
+    ``shape`` (when given), contiguous or, with ``packed_last``, at least with
+    its last axis adjacent."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (no CPU fallback)")
     if t.get_device() != device:
@@ -576,7 +583,11 @@ def _tensor(name, t, device, dtypes, shape=None, packed_last=True):
                          + (" along its last axis" if packed_last else ""))
 
 
-_F32, _IO = (torch.float32,), tuple(DTYPES)
+def _plain(t, device, dtype, shape):
+    """Whether t is the ordinary tensor that needs no further check."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device)
 
 
 def _device_of(name, t):
@@ -587,6 +598,8 @@ def _device_of(name, t):
     if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current "
                          f"device")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} has the unsupported dtype {t.dtype}")
     return dev
 
 
@@ -607,30 +620,32 @@ def _row_stride(name, t):
     return D if stride is None else stride
 
 
-def _workspace(workspace, nbytes, device):
-    """(the buffer, its bytes): the caller's, or one of torch's when None."""
-    if workspace is None:
-        if nbytes == 0:
-            return None, 0
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
-    _tensor("workspace", workspace, device, (torch.uint8,),
-            packed_last=False)
-    return workspace, workspace.numel()
+def _input_rows(name, t, device, dtype, shape):
+    """Elements between the rows of an input, checked."""
+    if _plain(t, device, dtype, shape):
+        return shape[-1]
+    _check(name, t, device, (dtype,), shape)
+    return _row_stride(name, t)
 
 
-def _output(name, t, shape, dtype, device):
-    """A preallocated contiguous output, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(name, t, device, (dtype,), shape, packed_last=False)
+def _exact(name, t, device, dtype, shape):
+    """Checks a contiguous tensor of one type and shape."""
+    if not _plain(t, device, dtype, shape):
+        _check(name, t, device, (dtype,), shape, packed_last=False)
     return t
 
 
-def _call(name, *args):
-    st = getattr(load_library(), name)(
-        *args, torch.cuda.current_stream().cuda_stream)
-    if st != KLA_OK:
-        raise KlaError(name, st)
+def _workspace(workspace, nbytes, device):
+    """(the buffer, its bytes): the caller's, or one of torch's when None."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    _check("workspace", workspace, device, (torch.uint8,), packed_last=False)
+    return workspace, workspace.numel()
+
+
+def _done(name, status):
+    if status != KLA_OK:
+        raise KlaError(name, status)
 
 
 def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
@@ -650,36 +665,39 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
             return layernorm_fwd(x, weight, bias, eps, residual, y, sum,
                                  want_stats)
     dev = _device_of("x", x)
-    _tensor("x", x, dev, _IO)
     shape, dt = x.shape, x.dtype
-    if x.ndim < 1 or shape[-1] < 1:
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must have a last axis of at least one element")
+    xs = _input_rows("x", x, dev, dt, shape)
     D = shape[-1]
-    rows = x.numel() // D
-    wt = dt
+    wt, rs = dt, 0
     if weight is not None or bias is not None:
-        wt = (bias if weight is None else weight).dtype
-        if weight is not None:
-            _tensor("weight", weight, dev, _IO, (D,), packed_last=False)
-        if bias is not None:
-            _tensor("bias", bias, dev, _IO if weight is None else (wt,), (D,),
-                    packed_last=False)
-    rs = 0
+        wt = getattr(bias if weight is None else weight, "dtype", dt)
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None:
+                _exact(name, t, dev, wt, (D,))
+        if wt not in DTYPES:
+            raise TypeError(f"unsupported weight or bias dtype {wt}")
     if residual is not None:
-        _tensor("residual", residual, dev, (dt,), shape)
-        rs = _row_stride("residual", residual)
-        sum = _output("sum", sum, shape, dt, dev)
+        rs = _input_rows("residual", residual, dev, dt, shape)
+        if sum is None:
+            sum = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _exact("sum", sum, dev, dt, shape)
     elif sum is not None:
         raise ValueError("sum is written only with a residual")
-    y = _output("y", y, shape, dt, dev)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _exact("y", y, dev, dt, shape)
     mean = rstd = None
     if want_stats:
-        mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32,
-                                 device=dev).unbind(0)
-    _call("kla_layernorm_fwd", x.data_ptr(), _row_stride("x", x),
-          _addr(residual), rs, _addr(weight), _addr(bias), eps, y.data_ptr(),
-          _addr(sum), _addr(mean), _addr(rstd), rows, D, DTYPES[dt],
-          DTYPES[wt])
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
+    _done("kla_layernorm_fwd", load_library().kla_layernorm_fwd(
+        x.data_ptr(), xs, _addr(residual), rs, _addr(weight), _addr(bias),
+        eps, y.data_ptr(), _addr(sum), _addr(mean), _addr(rstd),
+        x.numel() // D, D, DTYPES[dt], DTYPES[wt], _raw_stream(dev)))
     return y, sum, mean, rstd
 
 
@@ -711,62 +729,74 @@ def layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad=None,
             return layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad,
                                  want_weight_grads, workspace)
     dev = _device_of("x", x)
-    _tensor("x", x, dev, _IO)
     shape, dt = x.shape, x.dtype
-    if x.ndim < 1 or shape[-1] < 1:
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must have a last axis of at least one element")
+    xs = _input_rows("x", x, dev, dt, shape)
+    ys = _input_rows("y_grad", y_grad, dev, dt, shape)
+    _exact("mean", mean, dev, torch.float32, shape[:-1])
+    _exact("rstd", rstd, dev, torch.float32, shape[:-1])
     D = shape[-1]
     rows = x.numel() // D
-    _tensor("y_grad", y_grad, dev, (dt,), shape)
-    _tensor("mean", mean, dev, _F32, shape[:-1], packed_last=False)
-    _tensor("rstd", rstd, dev, _F32, shape[:-1], packed_last=False)
     wt, ss = dt, 0
     if weight is not None:
-        _tensor("weight", weight, dev, _IO, (D,), packed_last=False)
-        wt = weight.dtype
+        wt = getattr(weight, "dtype", dt)
+        _exact("weight", weight, dev, wt, (D,))
+        if wt not in DTYPES:
+            raise TypeError(f"unsupported weight dtype {wt}")
     if sum_grad is not None:
-        _tensor("sum_grad", sum_grad, dev, (dt,), shape)
-        ss = _row_stride("sum_grad", sum_grad)
+        ss = _input_rows("sum_grad", sum_grad, dev, dt, shape)
     dx = torch.empty(shape, dtype=dt, device=dev)
     dw = db = None
     nbytes = 0
     if want_weight_grads:
         dw = torch.empty(D, dtype=wt, device=dev)
-        db = torch.empty(D, dtype=wt, device=dev)
+        db = torch.empty_like(dw)
         workspace, nbytes = _workspace(
             workspace, layernorm_bwd_workspace_size(rows, D, dt), dev)
-    _call("kla_layernorm_bwd", y_grad.data_ptr(),
-          _row_stride("y_grad", y_grad), x.data_ptr(), _row_stride("x", x),
-          _addr(weight), mean.data_ptr(), rstd.data_ptr(), _addr(sum_grad),
-          ss, dx.data_ptr(), _addr(dw), _addr(db), rows, D, DTYPES[dt],
-          DTYPES[wt], _addr(workspace), nbytes)
+    _done("kla_layernorm_bwd", load_library().kla_layernorm_bwd(
+        y_grad.data_ptr(), ys, x.data_ptr(), xs, _addr(weight),
+        mean.data_ptr(), rstd.data_ptr(), _addr(sum_grad), ss, dx.data_ptr(),
+        _addr(dw), _addr(db), rows, D, DTYPES[dt], DTYPES[wt],
+        _addr(workspace), nbytes, _raw_stream(dev)))
     return dict(x_grad=dx, weight_grad=dw, bias_grad=db)
 
 
 def _glr_shape(name, x, cu_seqlens):
-    """(device, B, T, D) of a recurrence call."""
+    """(device, sequences, tokens, channels) of a recurrence call."""
     dev = _device_of(name, x)
-    _tensor(name, x, dev, _IO)
+    if not x.is_contiguous():
+        _check(name, x, dev, _IO)
+    shape = x.shape
     if cu_seqlens is None:
-        if x.ndim != 3:
+        if len(shape) != 3:
             raise ValueError(f"{name} must be [B, T, D]")
-        B, T, D = x.shape
+        B = shape[0]
     else:
-        if x.ndim != 2:
+        if len(shape) != 2:
             raise ValueError(f"{name} must be [T, D] with cu_seqlens")
-        _tensor("cu_seqlens", cu_seqlens, dev, (torch.int32,),
-                packed_last=False)
+        _check("cu_seqlens", cu_seqlens, dev, (torch.int32,),
+               packed_last=False)
         if cu_seqlens.ndim != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [B + 1]")
         B = cu_seqlens.numel() - 1
-        T, D = x.shape
-    if D < 1:
+    if shape[-1] < 1:
         raise ValueError(f"{name} must have at least one channel")
-    return dev, B, T, D
+    return dev, B, shape[-2], shape[-1]
 
 
-def _glr_strides(t):
-    return (t.data_ptr(), 0 if t.ndim == 2 else t.stride(0), t.stride(-2))
+def _glr_gate(log_alpha, device, shape):
+    """The gates' dtype, checked."""
+    gt = getattr(log_alpha, "dtype", None)
+    if gt not in DTYPES or not _plain(log_alpha, device, gt, shape):
+        _check("log_alpha", log_alpha, device, _IO, shape)
+    return gt
+
+
+def _strides(t):
+    """(between sequences, between tokens) of [B, T, D] or [T, D]."""
+    st = t.stride()
+    return (0, st[0]) if len(st) == 2 else (st[0], st[1])
 
 
 def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
@@ -785,16 +815,23 @@ def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
         with torch.cuda.stream(stream):
             return glr_fwd(x, log_alpha, h0, cu_seqlens, o, hT, want_state)
     dev, B, T, D = _glr_shape("x", x, cu_seqlens)
-    dt = x.dtype
-    _tensor("log_alpha", log_alpha, dev, _IO, x.shape)
+    shape, dt = x.shape, x.dtype
+    gt = _glr_gate(log_alpha, dev, shape)
     if h0 is not None:
-        _tensor("h0", h0, dev, _F32, (B, D), packed_last=False)
-    o = _output("o", o, x.shape, dt, dev)
-    if hT is not None or want_state:
-        hT = _output("hT", hT, (B, D), torch.float32, dev)
-    _call("kla_glr_fwd", *_glr_strides(x), *_glr_strides(log_alpha),
-          _addr(h0), o.data_ptr(), _addr(hT), _addr(cu_seqlens), B, T, D,
-          DTYPES[dt], DTYPES[log_alpha.dtype])
+        _exact("h0", h0, dev, torch.float32, (B, D))
+    if o is None:
+        o = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _exact("o", o, dev, dt, shape)
+    if hT is not None:
+        _exact("hT", hT, dev, torch.float32, (B, D))
+    elif want_state:
+        hT = torch.empty((B, D), dtype=torch.float32, device=dev)
+    _done("kla_glr_fwd", load_library().kla_glr_fwd(
+        x.data_ptr(), *_strides(x), log_alpha.data_ptr(),
+        *_strides(log_alpha), _addr(h0), o.data_ptr(), _addr(hT),
+        _addr(cu_seqlens), B, T, D, DTYPES[dt], DTYPES[gt],
+        _raw_stream(dev)))
     return o, hT
 
 
@@ -810,20 +847,23 @@ def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
             return glr_bwd(o, log_alpha, o_grad, hT_grad, h0, cu_seqlens,
                            want_h0_grad)
     dev, B, T, D = _glr_shape("o", o, cu_seqlens)
-    dt, gt = o.dtype, log_alpha.dtype
-    _tensor("log_alpha", log_alpha, dev, _IO, o.shape)
-    _tensor("o_grad", o_grad, dev, (dt,), o.shape)
+    shape, dt = o.shape, o.dtype
+    gt = _glr_gate(log_alpha, dev, shape)
+    if not _plain(o_grad, dev, dt, shape):
+        _check("o_grad", o_grad, dev, (dt,), shape)
     for name, t in (("h0", h0), ("hT_grad", hT_grad)):
         if t is not None:
-            _tensor(name, t, dev, _F32, (B, D), packed_last=False)
-    dx = torch.empty(o.shape, dtype=dt, device=dev)
-    dla = torch.empty(o.shape, dtype=gt, device=dev)
+            _exact(name, t, dev, torch.float32, (B, D))
+    dx = torch.empty(shape, dtype=dt, device=dev)
+    dla = torch.empty(shape, dtype=gt, device=dev)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) \
         if want_h0_grad else None
-    _call("kla_glr_bwd", *_glr_strides(o), *_glr_strides(log_alpha),
-          _addr(h0), *_glr_strides(o_grad), _addr(hT_grad), dx.data_ptr(),
-          dla.data_ptr(), _addr(dh0), _addr(cu_seqlens), B, T, D, DTYPES[dt],
-          DTYPES[gt])
+    _done("kla_glr_bwd", load_library().kla_glr_bwd(
+        o.data_ptr(), *_strides(o), log_alpha.data_ptr(),
+        *_strides(log_alpha), _addr(h0), o_grad.data_ptr(),
+        *_strides(o_grad), _addr(hT_grad), dx.data_ptr(), dla.data_ptr(),
+        _addr(dh0), _addr(cu_seqlens), B, T, D, DTYPES[dt], DTYPES[gt],
+        _raw_stream(dev)))
     return dict(x_grad=dx, log_alpha_grad=dla, h0_grad=dh0)
 
 
@@ -836,16 +876,21 @@ def glr_step(x, log_alpha, S, o=None, stream=None):
         with torch.cuda.stream(stream):
             return glr_step(x, log_alpha, S, o)
     dev = _device_of("x", x)
-    _tensor("x", x, dev, _IO)
-    if x.ndim != 2 or x.shape[1] < 1:
-        raise ValueError("x must be [N, D]")
     shape, dt = x.shape, x.dtype
-    _tensor("log_alpha", log_alpha, dev, _IO, shape)
-    _tensor("S", S, dev, _F32, shape, packed_last=False)
-    o = _output("o", o, shape, dt, dev)
-    _call("kla_glr_step", x.data_ptr(), x.stride(0), log_alpha.data_ptr(),
-          log_alpha.stride(0), S.data_ptr(), o.data_ptr(), shape[0], shape[1],
-          DTYPES[dt], DTYPES[log_alpha.dtype])
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError("x must be [N, D]")
+    if not x.is_contiguous():
+        _check("x", x, dev, _IO)
+    gt = _glr_gate(log_alpha, dev, shape)
+    _exact("S", S, dev, torch.float32, shape)
+    if o is None:
+        o = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _exact("o", o, dev, dt, shape)
+    _done("kla_glr_step", load_library().kla_glr_step(
+        x.data_ptr(), x.stride(0), log_alpha.data_ptr(), log_alpha.stride(0),
+        S.data_ptr(), o.data_ptr(), shape[0], shape[1], DTYPES[dt],
+        DTYPES[gt], _raw_stream(dev)))
     return o
 
 
