@@ -1149,6 +1149,9 @@ cudaError_t read_and_clear_fault(cudaStream_t stream, unsigned int* word) {
     if (e != cudaSuccess) return e;
     e = read_and_clear_fault_glr(&w2);
     *word |= w2;
+    if (e != cudaSuccess) return e;
+    e = read_and_clear_fault_ln(&w2);
+    *word |= w2;
     return e;
 }
 

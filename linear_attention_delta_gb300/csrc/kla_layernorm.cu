@@ -11,13 +11,17 @@
 // the squared differences from the row's mean (not E[s^2] - m^2, which loses
 // every digit on rows with a large offset).
 //
-// A row is held in the registers of a group of threads, which read it once:
-// a warp, or a block.  V elements of a thread lie side by side (16 bytes), or
-// one (rows that do not line up on 16 bytes).  Rows wider than a block's
-// registers take the loop kernels at the end, which read them again.
+// A row is the work of a group of threads, a warp to a block, which read it
+// once.  Where there are many rows, a group walks through some of them, with
+// the copies of its next rows into shared memory on their way meanwhile (a
+// ring of rows per group): with loads into registers alone, as many as fit,
+// the 2048-wide layer's forward took 48 and its backward 92 us.  Where there
+// are few, a block per row loads it straight into registers.  Rows wider than
+// a block can hold take the loop kernels at the end, which read them again.
 #include <algorithm>
 
 #include "kla_internal.cuh"
+#include "tc_primitives.cuh"
 
 namespace kla {
 namespace {
@@ -63,27 +67,36 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Sum over a group of TPR threads (a warp, or the TPR threads that share the
-// named barrier `bar`) of two values at once; every thread gets both.  `red`:
-// TPR / 32 places, free when the call begins and not reused until the next
-// but one.
+// named barrier `bar`); every thread gets it.  `red`: TPR / 32 places, free
+// when the call begins and not written again until the next call but one.
 template <int TPR>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2* red,
-                                            int bar) {
+__device__ __forceinline__ float group_sum(float a, float* red, int bar) {
     a = warp_sum(a);
-    b = warp_sum(b);
     if constexpr (TPR == 32) {
-        return make_float2(a, b);
+        return a;
     } else {
-        constexpr int NW = TPR / 32;
-        const int warp = threadIdx.x % TPR / 32;
-        if (threadIdx.x % 32 == 0) red[warp] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TPR) : "memory");
+        if (threadIdx.x % 32 == 0) red[threadIdx.x % TPR / 32] = a;
+        tc::named_bar_sync(bar, TPR);
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) t += red[w];
+        return t;
+    }
+}
+template <int TPR>
+__device__ __forceinline__ float2 group_sum(float2 a, float2* red, int bar) {
+    a.x = warp_sum(a.x);
+    a.y = warp_sum(a.y);
+    if constexpr (TPR == 32) {
+        return a;
+    } else {
+        if (threadIdx.x % 32 == 0) red[threadIdx.x % TPR / 32] = a;
+        tc::named_bar_sync(bar, TPR);
         float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float2 r = red[w];
-            t.x += r.x;
-            t.y += r.y;
+        for (int w = 0; w < TPR / 32; ++w) {
+            t.x += red[w].x;
+            t.y += red[w].y;
         }
         return t;
     }
@@ -96,7 +109,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
     using P = Pack<T, V>;
     constexpr int ROWS = TPR < 128 ? 128 / TPR : 1;
-    __shared__ float2 red[2][ROWS * TPR / 32];
+    __shared__ float red[2][ROWS * TPR / 32];
     const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * ROWS + sub;
     if (row >= a.rows) return;
@@ -126,7 +139,7 @@ ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
         }
     }
     const float mean =
-        group_sum<TPR>(sum, 0.f, red[0] + sub * (TPR / 32), 1 + sub).x / a.D;
+        group_sum<TPR>(sum, red[0] + sub * (TPR / 32), 1 + sub) / a.D;
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -138,8 +151,8 @@ ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
         }
     }
     const float rstd =
-        1.f / sqrtf(group_sum<TPR>(sq, 0.f, red[1] + sub * (TPR / 32),
-                                   1 + sub).x / a.D + a.eps);
+        1.f / sqrtf(group_sum<TPR>(sq, red[1] + sub * (TPR / 32), 1 + sub) /
+                        a.D + a.eps);
     T* y = static_cast<T*>(a.y) + row * a.D;
     T* so = a.sum ? static_cast<T*>(a.sum) + row * a.D : nullptr;
 #pragma unroll
@@ -170,121 +183,412 @@ ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
     }
 }
 
-// Backward, the row in registers: a block of GROUPS groups of TPR threads
-// walks the rows group by group (rows g, g + all groups, ...), a thread
-// keeping its N * V columns, whose dw and db it adds up in registers; the
-// next row's loads are issued before the present row is reduced.  At the end
-// the block's groups are added up in shared memory, in order, and the block's
-// partial sums go to part [gridDim.x][2][D].
-template <typename T, int V, int TPR, int N, int GROUPS>
+// The rows of a group on their way into shared memory: IN inputs a row, K
+// rows.  Rows that line up on 16 bytes (WIDE) are copied whole by one thread
+// (bulk copies, an mbarrier per place); others by all threads with the
+// 16-byte pieces that they touch, each row keeping its place within the first
+// of them (read from the piece's start to the row's end only: the bytes that
+// it may hold before the row belong to the same allocation, which starts on
+// 16 bytes).
+constexpr int kMaxDepth = 8;
+
+template <bool WIDE, typename T, int TPR, int IN>
+struct Ring {
+    unsigned char* at;           // the group's place in shared memory
+    uint64_t* full;              // its mbarriers
+    int depth, pitch, bytes;     // rows; bytes between and in inputs
+    int t, bar;                  // thread and barrier of the group
+    const T* src[IN];
+    long long stride[IN];
+    long long rows, step;        // rows in all; between those of the group
+    int in;                      // inputs that there are
+
+    __device__ const T* place(int slot, int i) const {
+        return reinterpret_cast<const T*>(at + (slot * in + i) * pitch);
+    }
+    // Input i of a row in a slot: its first element.
+    __device__ const T* row_of(int slot, int i, long long row) const {
+        const T* p = place(slot, i);
+        if (WIDE) return p;
+        return p + (reinterpret_cast<uintptr_t>(src[i] + row * stride[i]) &
+                    15) / sizeof(T);
+    }
+    __device__ void fetch(int slot, long long row) const {
+        if (WIDE) {
+            if (t != 0 || row >= rows) return;
+            tc::mbar_arrive_expect_tx(full + slot, in * bytes);
+#pragma unroll
+            for (int i = 0; i < IN; ++i)
+                if (i < in)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::"
+                        "complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            tc::smem_u32(place(slot, i))),
+                        "l"(src[i] + row * stride[i]), "r"(bytes),
+                        "r"(tc::smem_u32(full + slot))
+                        : "memory");
+        } else {
+            if (row < rows) {
+#pragma unroll
+                for (int i = 0; i < IN; ++i) {
+                    if (i >= in) break;
+                    const uintptr_t p =
+                        reinterpret_cast<uintptr_t>(src[i] + row * stride[i]);
+                    const uintptr_t from = p & ~(uintptr_t)15;
+                    const int len = (int)(p - from) + bytes;
+                    const unsigned int to = tc::smem_u32(place(slot, i));
+                    for (int c = t * 16; c < len; c += TPR * 16)
+                        asm volatile(
+                            "cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                            ::"r"(to + c), "l"(from + c),
+                            "r"(min(16, len - c))
+                            : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    // Until the copy of the turn-th row is there; false: it never came.
+    __device__ bool wait(int slot, int phase) const {
+        if (WIDE) return tc::mbar_wait(full + slot, phase);
+        // the pieces on their way: those of the kDepth - 2 rows after it
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLooseDepth - 2)
+                     : "memory");
+        if (TPR == 32) __syncwarp();
+        else tc::named_bar_sync(bar, TPR);
+        return true;
+    }
+    static constexpr int kLooseDepth = 4;
+
+    // After a copy that never came: waits (1 ms each) for those that may be
+    // on their way yet.
+    __device__ void give_up() const {
+        if (!WIDE || t != 0) return;
+        for (int k = 0; k < depth; ++k)
+            for (int p = 0; p < 2; ++p) tc::mbar_wait(full + k, p, 1000000);
+    }
+};
+
+// Whether some thread of the group gave up waiting for this row: known to all
+// of them after the group's next barrier.  `dead` has two places per group,
+// used in turns, so that a thread that is ahead does not disturb the answer.
+template <int TPR>
+__device__ __forceinline__ bool group_dead(bool fault, volatile int* dead) {
+    if constexpr (TPR == 32) return __any_sync(0xffffffffu, fault);
+    else return *dead != 0;
+}
+
+__device__ unsigned int g_fault_ln = 0;
+
+// Where thread t's i-th run of V columns begins.
+template <int V, int TPR>
+__device__ __forceinline__ int column(int i, int t) {
+    return (i * TPR + t) * V;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void read_v(const T* p, float (&out)[V]) {
+    const auto q = *reinterpret_cast<const Pack<T, V>*>(p);
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = to_f32(q.v[v]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void write_v(T* p, const float (&x)[V]) {
+    Pack<T, V> q;
+#pragma unroll
+    for (int v = 0; v < V; ++v) q.v[v] = from_f32<T>(x[v]);
+    *reinterpret_cast<Pack<T, V>*>(p) = q;
+}
+
+// Sets up the ring of this thread's group; true once its first rows are on
+// their way.
+template <bool WIDE, typename T, int TPR, int GROUPS, int IN>
+__device__ __forceinline__ void open_ring(Ring<WIDE, T, TPR, IN>& ring,
+                                          unsigned char* smem, uint64_t* full,
+                                          int* dead, long long rows, int D, int depth) {
+    const int g = threadIdx.x / TPR;
+    if (threadIdx.x < 2 * GROUPS) dead[threadIdx.x] = 0;
+    ring.t = threadIdx.x % TPR;
+    ring.bar = 1 + g;
+    ring.depth = depth;
+    ring.bytes = D * (int)sizeof(T);
+    ring.pitch = (ring.bytes + (WIDE ? 0 : 15) + 15) / 16 * 16;
+    ring.at = smem + (size_t)g * depth * ring.in * ring.pitch;
+    ring.full = full + g * kMaxDepth;
+    ring.rows = rows;
+    ring.step = (long long)gridDim.x * GROUPS;
+    if (WIDE) {
+        if (ring.t == 0) {
+            for (int k = 0; k < depth; ++k) tc::mbar_init(ring.full + k, 1);
+            tc::fence_mbar_init();
+        }
+    }
+    __syncthreads();
+    const long long row = (long long)blockIdx.x * GROUPS + g;
+    for (int k = 0; k < depth - 1; ++k) ring.fetch(k, row + k * ring.step);
+}
+
+template <typename T, bool WIDE>
+constexpr int kV = WIDE ? 16 / (int)sizeof(T) : 1;
+
+// Forward over many rows: a thread holds N runs of V elements of its row.
+template <typename T, bool WIDE, int TPR, int N, int GROUPS>
 __global__ void __launch_bounds__(TPR * GROUPS)
-ln_bwd_kernel(const __grid_constant__ LayerNormBwdArgs a, float* part) {
-    using P = Pack<T, V>;
-    __shared__ float2 red[2][GROUPS * TPR / 32];
-    extern __shared__ float2 total[];            // [TPR * N * V] (dw, db)
+ln_fwd_ring_kernel(const __grid_constant__ LayerNormArgs a, int depth) {
+    constexpr int V = kV<T, WIDE>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[GROUPS * kMaxDepth];
+    __shared__ int dead[2][GROUPS];
+    __shared__ float red[2][GROUPS * TPR / 32];
     const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    float w[N][V], dw[N][V], db[N][V];
+    Ring<WIDE, T, TPR, 2> ring;
+    ring.src[0] = static_cast<const T*>(a.x);
+    ring.src[1] = static_cast<const T*>(a.residual);
+    ring.stride[0] = a.x_stride;
+    ring.stride[1] = a.residual_stride;
+    ring.in = a.residual ? 2 : 1;
+    open_ring<WIDE, T, TPR, GROUPS>(ring, smem, full, dead[0], a.rows, a.D,
+                                      depth);
+
+    float w[N][V], b[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (i * TPR + t) * V;
+        const int c = column<V, TPR>(i, t);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             w[i][v] = 1.f;
-            dw[i][v] = db[i][v] = 0.f;
+            b[i][v] = 0.f;
         }
         if (a.weight && c < a.D) load_v<V>(a.weight, c, a.wdtype, w[i]);
+        if (a.bias && c < a.D) load_v<V>(a.bias, c, a.wdtype, b[i]);
     }
-    const long long step = (long long)gridDim.x * GROUPS;
-    long long row = (long long)blockIdx.x * GROUPS + g;
-    P nx[N], ny[N], nd[N];
-    float nm = 0.f, nr = 0.f;
-    auto fetch = [&](long long row) {
-        if (row >= a.rows) return;
-        const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-        const T* y = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        const T* d = static_cast<const T*>(a.dsum) + row * a.dsum_stride;
+    const float over = 1.f / a.D;
+    bool fault = false;
+    int slot = 0, phase = 0, turn = 0;
+    for (long long row = (long long)blockIdx.x * GROUPS + g; row < a.rows;
+         row += ring.step, turn ^= 1) {
+        if (!ring.wait(slot, phase)) fault = dead[turn][g] = true;
+        const T* x = ring.row_of(slot, 0, row);
+        const T* r = a.residual ? ring.row_of(slot, 1, row) : nullptr;
+        float s[N][V];
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (i * TPR + t) * V;
+            const int c = column<V, TPR>(i, t);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[i][v] = 0.f;
             if (c < a.D) {
-                nx[i] = *reinterpret_cast<const P*>(x + c);
-                ny[i] = *reinterpret_cast<const P*>(y + c);
-                if (a.dsum) nd[i] = *reinterpret_cast<const P*>(d + c);
+                read_v<T, V>(x + c, s[i]);
+                if (r) {
+                    float q[V];
+                    read_v<T, V>(r + c, q);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[i][v] += q[v];
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += s[i][v];
+        }
+        const float mean =
+            group_sum<TPR>(sum, red[0] + g * (TPR / 32), 1 + g) * over;
+        if (group_dead<TPR>(fault, &dead[turn][g])) {
+            fault = true;
+            break;
+        }
+        // all of the group are done with the row before: its place is free
+        ring.fetch(slot == 0 ? depth - 1 : slot - 1,
+                   row + (depth - 1) * ring.step);
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (column<V, TPR>(i, t) < a.D) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float d = s[i][v] - mean;
+                    sq = fmaf(d, d, sq);
+                }
             }
         }
-        nm = a.mean[row];
-        nr = a.rstd[row];
-    };
-    fetch(row);
-    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-        P px[N], py[N], pd[N];
+        const float rstd = 1.f / sqrtf(
+            group_sum<TPR>(sq, red[1] + g * (TPR / 32), 1 + g) * over +
+            a.eps);
+        T* y = static_cast<T*>(a.y) + row * a.D;
+        T* so = a.sum ? static_cast<T*>(a.sum) + row * a.D : nullptr;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            px[i] = nx[i];
-            py[i] = ny[i];
-            pd[i] = nd[i];
+            const int c = column<V, TPR>(i, t);
+            if (c >= a.D) break;
+            if (so) write_v<T, V>(so + c, s[i]);
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                o[v] = fmaf((s[i][v] - mean) * rstd, w[i][v], b[i][v]);
+            write_v<T, V>(y + c, o);
         }
-        const float mean = nm, rstd = nr;
-        fetch(row + step);
-        float s1 = 0.f, s2 = 0.f;
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+    if (!WIDE) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (fault) {
+        if (t == 0) atomicOr(&g_fault_ln, 1u);
+        ring.give_up();
+    }
+}
+
+// Backward over the rows of a group, a thread keeping its N * V columns,
+// whose dw and db it adds up in registers.  At the end the block's groups are
+// added up in shared memory, in order, and the block's partial sums go to
+// part [gridDim.x][2][D].  HOLD: w, xh and w dy stay in registers from the
+// sums to the result (else they are formed again: very wide rows).
+template <typename T, bool WIDE, int TPR, int N, int GROUPS, bool HOLD>
+__global__ void __launch_bounds__(TPR * GROUPS)
+ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
+                   float* part) {
+    constexpr int V = kV<T, WIDE>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[GROUPS * kMaxDepth];
+    __shared__ int dead[2][GROUPS];
+    __shared__ float2 red[2][GROUPS * TPR / 32];
+    const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    Ring<WIDE, T, TPR, 3> ring;
+    ring.src[0] = static_cast<const T*>(a.x);
+    ring.src[1] = static_cast<const T*>(a.dy);
+    ring.src[2] = static_cast<const T*>(a.dsum);
+    ring.stride[0] = a.x_stride;
+    ring.stride[1] = a.dy_stride;
+    ring.stride[2] = a.dsum_stride;
+    ring.in = a.dsum ? 3 : 2;
+    open_ring<WIDE, T, TPR, GROUPS>(ring, smem, full, dead[0], a.rows, a.D,
+                                      depth);
+
+    float dw[N][V], db[N][V], wr[HOLD ? N : 1][V];
+    auto weight = [&](int c, float (&w)[V]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if ((i * TPR + t) * V >= a.D) break;
+        for (int v = 0; v < V; ++v) w[v] = 1.f;
+        if (a.weight && c < a.D) load_v<V>(a.weight, c, a.wdtype, w);
+    };
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
+        if (HOLD) weight(column<V, TPR>(i, t), wr[HOLD ? i : 0]);
+    }
+    const float over = 1.f / a.D;
+    bool fault = false;
+    int slot = 0, phase = 0, turn = 0;
+    long long row = (long long)blockIdx.x * GROUPS + g;
+    float mean = 0.f, rstd = 0.f;
+    if (row < a.rows) {
+        mean = a.mean[row];
+        rstd = a.rstd[row];
+    }
+    for (; row < a.rows; row += ring.step, turn ^= 1) {
+        if (!ring.wait(slot, phase)) fault = dead[turn][g] = true;
+        const T* x = ring.row_of(slot, 0, row);
+        const T* y = ring.row_of(slot, 1, row);
+        const T* d = a.dsum ? ring.row_of(slot, 2, row) : nullptr;
+        float xh[N][V], wy[N][V];
+        float2 sum = make_float2(0.f, 0.f);
+        // xh and w dy of a run; first: the sums, too
+        auto run = [&](int i, float (&xh)[V], float (&wy)[V], bool first) {
+            const int c = column<V, TPR>(i, t);
+            float w[V];
+            if (!HOLD) weight(c, w);
+            read_v<T, V>(x + c, xh);
+            read_v<T, V>(y + c, wy);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float xh = (to_f32(px[i].v[v]) - mean) * rstd;
-                const float dy = to_f32(py[i].v[v]);
-                const float wy = w[i][v] * dy;
-                s1 = fmaf(wy, xh, s1);
-                s2 += wy;
-                dw[i][v] = fmaf(dy, xh, dw[i][v]);
-                db[i][v] += dy;
+                xh[v] = (xh[v] - mean) * rstd;
+                if (first) {
+                    dw[i][v] = fmaf(wy[v], xh[v], dw[i][v]);
+                    db[i][v] += wy[v];
+                }
+                wy[v] *= HOLD ? wr[HOLD ? i : 0][v] : w[v];
+                if (first) {
+                    sum.x = fmaf(wy[v], xh[v], sum.x);
+                    sum.y += wy[v];
+                }
             }
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (column<V, TPR>(i, t) < a.D)
+                run(i, xh[HOLD ? i : 0], wy[HOLD ? i : 0], true);
+        float next_mean = 0.f, next_rstd = 0.f;
+        if (row + ring.step < a.rows) {
+            next_mean = a.mean[row + ring.step];
+            next_rstd = a.rstd[row + ring.step];
         }
-        const float2 c = group_sum<TPR>(s1, s2, red[turn] + g * (TPR / 32),
-                                        1 + g);
-        const float c1 = c.x / a.D, c2 = c.y / a.D;
+        const float2 c =
+            group_sum<TPR>(sum, red[turn] + g * (TPR / 32), 1 + g);
+        if (group_dead<TPR>(fault, &dead[turn][g])) {
+            fault = true;
+            break;
+        }
+        // all of the group are done with the row before: its place is free
+        ring.fetch(slot == 0 ? depth - 1 : slot - 1,
+                   row + (depth - 1) * ring.step);
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+        const float c1 = c.x * over, c2 = c.y * over;
         T* dx = static_cast<T*>(a.dx) + row * a.D;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int col = (i * TPR + t) * V;
+            const int col = column<V, TPR>(i, t);
             if (col >= a.D) break;
-            P out;
+            if (!HOLD) run(i, xh[0], wy[0], false);
+            float o[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float xh = (to_f32(px[i].v[v]) - mean) * rstd;
-                const float wy = w[i][v] * to_f32(py[i].v[v]);
-                const float d = rstd * (wy - c2 - xh * c1);
-                out.v[v] = from_f32<T>(
-                    a.dsum ? d + to_f32(pd[i].v[v]) : d);
+            for (int v = 0; v < V; ++v)
+                o[v] = rstd * (wy[HOLD ? i : 0][v] - c2 -
+                               xh[HOLD ? i : 0][v] * c1);
+            if (d) {
+                float q[V];
+                read_v<T, V>(d + col, q);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] += q[v];
             }
-            *reinterpret_cast<P*>(dx + col) = out;
+            write_v<T, V>(dx + col, o);
         }
+        mean = next_mean;
+        rstd = next_rstd;
+    }
+    if (!WIDE) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (fault) {
+        if (t == 0) atomicOr(&g_fault_ln, 1u);
+        ring.give_up();
     }
     if (!part) return;
+    // every copy has been waited for: the rings' place is free
+    float2* total = reinterpret_cast<float2*>(smem);     // [N * V][TPR]
     for (int q = 0; q < GROUPS; ++q) {
-        if (g == q) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float2& s = total[(i * V + v) * TPR + t];
-                    const float2 old =
-                        q ? s : make_float2(0.f, 0.f);
-                    s = make_float2(old.x + dw[i][v], old.y + db[i][v]);
-                }
-        }
         __syncthreads();
+        if (g != q) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float2& s = total[(i * V + v) * TPR + t];
+                const float2 old = q ? s : make_float2(0.f, 0.f);
+                s = make_float2(old.x + dw[i][v], old.y + db[i][v]);
+            }
     }
+    __syncthreads();
     float* p = part + (size_t)blockIdx.x * 2 * a.D;
-    for (int e = threadIdx.x; e < N * V * TPR; e += TPR * GROUPS) {
-        // column e of the row: pack e / V, thread (e / V) % TPR
+    for (int e = threadIdx.x; e < a.D; e += TPR * GROUPS) {
+        // column e: run e / V, thread (e / V) % TPR
         const int i = e / (V * TPR), u = e / V % TPR, v = e % V;
-        if (e < a.D) {
-            const float2 s = total[(i * V + v) * TPR + u];
-            p[e] = s.x;
-            p[a.D + e] = s.y;
-        }
+        const float2 s = total[(i * V + v) * TPR + u];
+        p[e] = s.x;
+        p[a.D + e] = s.y;
     }
 }
 
@@ -293,7 +597,7 @@ constexpr int kLoopThreads = 512;
 // Sum over a block of kLoopThreads of two values at once.
 __device__ __forceinline__ float2 block_sum(float a, float b, float2* red) {
     __syncthreads();             // red is free again
-    return group_sum<kLoopThreads>(a, b, red, 0);
+    return group_sum<kLoopThreads>(make_float2(a, b), red, 0);
 }
 
 // Any D, strides and alignment: one block per row, which it reads three
@@ -429,6 +733,36 @@ bool lines_up(const void* p, size_t elt, long long stride, int vec) {
            stride % vec == 0;
 }
 
+// Blocks of a ring kernel, and its ring: as many rows as fit into about 200
+// KB for 1024 threads on an SM, 2 at least and 4 for rows copied in pieces
+// (0 blocks: they do not fit).
+struct RingPlan {
+    int blocks, depth, bytes;
+};
+template <typename K>
+RingPlan ring_plan(K* kernel, int threads, int groups, bool wide, int in,
+                   int elt, int D, int rows, int least) {
+    RingPlan p{0, 0, 0};
+    const int pitch = (D * elt + (wide ? 0 : 15) + 15) / 16 * 16;
+    const int row = groups * in * pitch;         // of all groups of a block
+    const int want = std::max(1, 1024 / threads);
+    p.depth = wide ? std::max(2, std::min(kMaxDepth,
+                                          200 * 1024 / want / row))
+                   : 4;
+    p.bytes = std::max(p.depth * row, least);
+    if (p.bytes > 220 * 1024) return p;
+    int per = 0;
+    if (cudaFuncSetAttribute(kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             220 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &per, kernel, threads, p.bytes) != cudaSuccess)
+        return p;
+    p.blocks = (int)std::min<long long>(((long long)rows + groups - 1) / groups,
+                                        (long long)per * device_sm_count());
+    return p;
+}
+
 template <typename T, int V, int TPR, int N>
 cudaError_t fwd_rows(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int threads = TPR < 128 ? 128 : TPR, rows = threads / TPR;
@@ -437,21 +771,39 @@ cudaError_t fwd_rows(const LayerNormArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, bool WIDE, int TPR, int N>
+cudaError_t fwd_ring(const LayerNormArgs& a, cudaStream_t s) {
+    constexpr int GROUPS = TPR < 256 ? 256 / TPR : 1;
+    auto* kernel = ln_fwd_ring_kernel<T, WIDE, TPR, N, GROUPS>;
+    const RingPlan p = ring_plan(kernel, TPR * GROUPS, GROUPS, WIDE,
+                                 a.residual ? 2 : 1, sizeof(T), a.D, a.rows,
+                                 0);
+    if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
+    kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth);
+    return cudaGetLastError();
+}
+
 template <typename T, int V>
 cudaError_t fwd_width(const LayerNormArgs& a, cudaStream_t s) {
+    constexpr bool WIDE = V > 1;
+    constexpr int M = WIDE ? 1 : 4;              // runs are 1 element then
     const int packs = (a.D + V - 1) / V;
-    // enough rows to fill the GPU with a warp per row
-    const bool many = a.rows >= 16 * device_sm_count();
+    // a few rows for each group of threads that the GPU holds
+    if ((long long)a.rows * packs >= 152 * 1024 * 4 * M) {
+        if (packs <= 32 * M) return fwd_ring<T, WIDE, 32, M>(a, s);
+        if (packs <= 64 * M) return fwd_ring<T, WIDE, 32, 2 * M>(a, s);
+        if (packs <= 128 * M) return fwd_ring<T, WIDE, 64, 2 * M>(a, s);
+        if (packs <= 256 * M) return fwd_ring<T, WIDE, 128, 2 * M>(a, s);
+        if (packs <= 512 * M) return fwd_ring<T, WIDE, 256, 2 * M>(a, s);
+        if (packs <= 1024 * M) return fwd_ring<T, WIDE, 512, 2 * M>(a, s);
+        if (WIDE && packs <= 2048) return fwd_ring<T, WIDE, 1024, 2 * M>(a, s);
+    }
     if (packs <= 32) return fwd_rows<T, V, 32, 1>(a, s);
     if (packs <= 64) return fwd_rows<T, V, 32, 2>(a, s);
-    if (packs <= 128 && many) return fwd_rows<T, V, 32, 4>(a, s);
-    if (packs <= 256 && many) return fwd_rows<T, V, 32, 8>(a, s);
     if (packs <= 128) return fwd_rows<T, V, 128, 1>(a, s);
     if (packs <= 256) return fwd_rows<T, V, 256, 1>(a, s);
-    if (packs <= 512 && many) return fwd_rows<T, V, 128, 4>(a, s);
     if (packs <= 512) return fwd_rows<T, V, 512, 1>(a, s);
-    if (packs <= 1024) return fwd_rows<T, V, 256, 4>(a, s);
-    if (packs <= 2048) return fwd_rows<T, V, 512, 4>(a, s);
+    if (packs <= 1024) return fwd_rows<T, V, 1024, 1>(a, s);
     if (packs <= 4096) return fwd_rows<T, V, 1024, 4>(a, s);
     ln_fwd_loop_kernel<T><<<a.rows, kLoopThreads, 0, s>>>(a);
     return cudaGetLastError();
@@ -486,26 +838,20 @@ cudaError_t join(const LayerNormBwdArgs& a, const float* part, int slices,
                               a.dw, a.db, (int)a.wdtype);
 }
 
-template <typename T, int V, int TPR, int N, int GROUPS>
-cudaError_t bwd_rows(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
-    auto* kernel = ln_bwd_kernel<T, V, TPR, N, GROUPS>;
-    constexpr int bytes = TPR * N * V * (int)sizeof(float2);
-    if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
-    int per = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per, kernel, TPR * GROUPS, bytes);
-    if (e != cudaSuccess) return e;
-    const long long want = ((long long)a.rows + GROUPS - 1) / GROUPS;
-    const int blocks = (int)std::min<long long>(
-        want, std::min(std::max(per, 1) * device_sm_count(), kMaxSlices));
+template <typename T, bool WIDE, int TPR, int N, bool HOLD = true>
+cudaError_t bwd_ring(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
+    constexpr int GROUPS = TPR < 256 ? 256 / TPR : 1;
+    auto* kernel = ln_bwd_ring_kernel<T, WIDE, TPR, N, GROUPS, HOLD>;
     const bool grads = a.dw || a.db;
-    kernel<<<blocks, TPR * GROUPS, bytes, s>>>(a, grads ? part : nullptr);
-    e = cudaGetLastError();
-    return e != cudaSuccess || !grads ? e : join(a, part, blocks, s);
+    RingPlan p = ring_plan(kernel, TPR * GROUPS, GROUPS, WIDE,
+                           a.dsum ? 3 : 2, sizeof(T), a.D, a.rows,
+                           TPR * N * kV<T, WIDE> * (int)sizeof(float2));
+    if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
+    p.blocks = std::min(p.blocks, kMaxSlices);
+    kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth,
+                                                   grads ? part : nullptr);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess || !grads ? e : join(a, part, p.blocks, s);
 }
 
 template <typename T>
@@ -522,14 +868,17 @@ cudaError_t bwd_loop(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
 template <typename T, int V>
 cudaError_t bwd_width(const LayerNormBwdArgs& a, float* part,
                       cudaStream_t s) {
+    constexpr bool WIDE = V > 1;
+    constexpr int M = WIDE ? 1 : 4;              // runs are 1 element then
     const int packs = (a.D + V - 1) / V;
-    if (packs <= 32) return bwd_rows<T, V, 32, 1, 8>(a, part, s);
-    if (packs <= 64) return bwd_rows<T, V, 64, 1, 8>(a, part, s);
-    if (packs <= 128) return bwd_rows<T, V, 128, 1, 4>(a, part, s);
-    if (packs <= 256) return bwd_rows<T, V, 256, 1, 2>(a, part, s);
-    if (packs <= 512) return bwd_rows<T, V, 512, 1, 1>(a, part, s);
-    if (packs <= 1024) return bwd_rows<T, V, 512, 2, 1>(a, part, s);
-    if (packs <= 2048) return bwd_rows<T, V, 1024, 2, 1>(a, part, s);
+    if (packs <= 32 * M) return bwd_ring<T, WIDE, 32, M>(a, part, s);
+    if (packs <= 64 * M) return bwd_ring<T, WIDE, 64, M>(a, part, s);
+    if (packs <= 128 * M) return bwd_ring<T, WIDE, 128, M>(a, part, s);
+    if (packs <= 256 * M) return bwd_ring<T, WIDE, 256, M>(a, part, s);
+    if (packs <= 512 * M) return bwd_ring<T, WIDE, 512, M>(a, part, s);
+    if (packs <= 1024 * M) return bwd_ring<T, WIDE, 1024, M>(a, part, s);
+    if (WIDE && packs <= 2048)
+        return bwd_ring<T, WIDE, 512, 4, false>(a, part, s);
     return bwd_loop<T>(a, part, s);
 }
 
@@ -547,6 +896,14 @@ cudaError_t launch_bwd(const LayerNormBwdArgs& a, float* part,
 }
 
 }  // namespace
+
+cudaError_t read_and_clear_fault_ln(unsigned int* word) {
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_fault_ln,
+                                         sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_fault_ln, &zero, sizeof(unsigned int));
+}
 
 cudaError_t launch_layernorm(const LayerNormArgs& a, cudaStream_t stream) {
     return a.dtype == KLA_BF16 ? launch_fwd<bf16>(a, stream)
