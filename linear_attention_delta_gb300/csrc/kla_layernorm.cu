@@ -20,6 +20,7 @@
 // a block can hold take the loop kernels at the end, which read them again.
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "kla_internal.cuh"
 #include "tc_primitives.cuh"
 
@@ -83,21 +84,26 @@ __device__ __forceinline__ float group_sum(float a, float* red, int bar) {
         return t;
     }
 }
+// The same of two values, each in half of a warp's lanes after the first
+// step.
 template <int TPR>
 __device__ __forceinline__ float2 group_sum(float2 a, float2* red, int bar) {
-    a.x = warp_sum(a.x);
-    a.y = warp_sum(a.y);
+    const bool low = threadIdx.x % 32 < 16;
+    float v = low ? a.x : a.y;
+    v += __shfl_xor_sync(0xffffffffu, low ? a.y : a.x, 16);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
     if constexpr (TPR == 32) {
-        return a;
+        return make_float2(__shfl_sync(0xffffffffu, v, 0),
+                           __shfl_sync(0xffffffffu, v, 16));
     } else {
-        if (threadIdx.x % 32 == 0) red[threadIdx.x % TPR / 32] = a;
+        if (threadIdx.x % 16 == 0)
+            reinterpret_cast<float*>(red)[threadIdx.x % TPR / 16] = v;
         tc::named_bar_sync(bar, TPR);
         float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) {
-            t.x += red[w].x;
-            t.y += red[w].y;
-        }
+        for (int w = 0; w < TPR / 32; ++w) t = add2(t, red[w]);
         return t;
     }
 }
@@ -150,9 +156,9 @@ ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
             sq = in ? fmaf(d, d, sq) : sq;
         }
     }
-    const float rstd =
-        1.f / sqrtf(group_sum<TPR>(sq, red[1] + sub * (TPR / 32), 1 + sub) /
-                        a.D + a.eps);
+    const float rstd = rsqrtf(
+        group_sum<TPR>(sq, red[1] + sub * (TPR / 32), 1 + sub) / a.D +
+        a.eps);
     T* y = static_cast<T*>(a.y) + row * a.D;
     T* so = a.sum ? static_cast<T*>(a.sum) + row * a.D : nullptr;
 #pragma unroll
@@ -280,25 +286,121 @@ __device__ __forceinline__ bool group_dead(bool fault, volatile int* dead) {
 
 __device__ unsigned int g_fault_ln = 0;
 
-// Where thread t's i-th run of V columns begins.
-template <int V, int TPR>
-__device__ __forceinline__ int column(int i, int t) {
-    return (i * TPR + t) * V;
+// A thread's part of a row: N runs of V adjacent elements, run i from column
+// (i * TPR + t) * V on, as pairs of fp32 (adjacent elements, or elements of
+// runs 2 i and 2 i + 1 where V = 1).
+template <typename T, bool WIDE>
+constexpr int kV = WIDE ? 16 / (int)sizeof(T) : 1;
+
+template <typename T>
+__device__ __forceinline__ float2 pair_of(T x, T y) {
+    return make_float2(to_f32(x), to_f32(y));
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void read_v(const T* p, float (&out)[V]) {
-    const auto q = *reinterpret_cast<const Pack<T, V>*>(p);
+template <typename T, int V, int TPR, int N>
+struct Part {
+    static constexpr int E = N * V / 2;          // pairs
+    float2 v[E];
+
+    // Whether column (i * TPR + t) * V + ... of run i is in a row of D; runs
+    // that lie inside for all threads need no test.
+    __device__ static int column(int i, int t) { return (i * TPR + t) * V; }
+    __device__ static bool inside(int i, int t, int D) {
+        return (i + 1) * TPR * V <= D || column(i, t) < D;
+    }
+    // f(pair index, both elements in the row, the first, run) for all pairs
+    // of which some element is in the row.
+    template <typename F>
+    __device__ static void each(int t, int D, F f) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = to_f32(q.v[v]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void write_v(T* p, const float (&x)[V]) {
-    Pack<T, V> q;
+        for (int e = 0; e < E; ++e) {
+            const int i = V == 1 ? 2 * e : 2 * e / V;
+            const bool a = inside(i, t, D);
+            const bool b = V == 1 ? inside(i + 1, t, D) : a;
+            f(e, a, b);
+        }
+    }
+    // From a row in memory (any type); zeros outside.
+    template <typename U>
+    __device__ void read(const U* p, int t, int D, float fill = 0.f) {
+        if constexpr (V == 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) q.v[v] = from_f32<T>(x[v]);
-    *reinterpret_cast<Pack<T, V>*>(p) = q;
-}
+            for (int e = 0; e < E; ++e) {
+                v[e] = both(fill);
+                if (inside(2 * e, t, D)) v[e].x = to_f32(p[column(2 * e, t)]);
+                if (inside(2 * e + 1, t, D))
+                    v[e].y = to_f32(p[column(2 * e + 1, t)]);
+            }
+        } else {
+            constexpr int M = 16 / sizeof(U) < V ? 16 / sizeof(U) : V;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+#pragma unroll
+                for (int u = 0; u < V; u += M) {
+                    Pack<U, M> q;
+                    const bool in = inside(i, t, D);
+                    if (in)
+                        q = *reinterpret_cast<const Pack<U, M>*>(
+                            p + column(i, t) + u);
+#pragma unroll
+                    for (int w = 0; w < M; w += 2)
+                        v[(i * V + u + w) / 2] =
+                            in ? pair_of(q.v[w], q.v[w + 1]) : both(fill);
+                }
+            }
+        }
+    }
+    // To a row in memory, rounded to T.
+    __device__ void write(T* p, int t, int D) const {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (inside(2 * e, t, D))
+                    p[column(2 * e, t)] = from_f32<T>(v[e].x);
+                if (inside(2 * e + 1, t, D))
+                    p[column(2 * e + 1, t)] = from_f32<T>(v[e].y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!inside(i, t, D)) continue;
+                if constexpr (sizeof(T) == 2) {
+                    uint4 q;
+                    q.x = bf16x2(v[i * 4]);
+                    q.y = bf16x2(v[i * 4 + 1]);
+                    q.z = bf16x2(v[i * 4 + 2]);
+                    q.w = bf16x2(v[i * 4 + 3]);
+                    *reinterpret_cast<uint4*>(p + column(i, t)) = q;
+                } else {
+                    *reinterpret_cast<float4*>(p + column(i, t)) =
+                        make_float4(v[i * 2].x, v[i * 2].y, v[i * 2 + 1].x,
+                                    v[i * 2 + 1].y);
+                }
+            }
+        }
+    }
+    __device__ static unsigned int bf16x2(float2 x) {
+        return tc::pack_bf16x2(x.x, x.y);
+    }
+    // A weight or bias of either type (null: `fill` everywhere).
+    __device__ void read_weight(const void* p, int dt, int t, int D,
+                                float fill) {
+        if (!p) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = both(fill);
+        } else if (dt == KLA_BF16) {
+            read(static_cast<const bf16*>(p), t, D, 0.f);
+        } else {
+            read(static_cast<const float*>(p), t, D, 0.f);
+        }
+    }
+    __device__ float sum() const {
+        float2 s = v[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) s = add2(s, v[e]);
+        return s.x + s.y;
+    }
+};
 
 // Sets up the ring of this thread's group; true once its first rows are on
 // their way.
@@ -328,9 +430,6 @@ __device__ __forceinline__ void open_ring(Ring<WIDE, T, TPR, IN>& ring,
     for (int k = 0; k < depth - 1; ++k) ring.fetch(k, row + k * ring.step);
 }
 
-template <typename T, bool WIDE>
-constexpr int kV = WIDE ? 16 / (int)sizeof(T) : 1;
-
 // Forward over many rows: a thread holds N runs of V elements of its row.
 template <typename T, bool WIDE, int TPR, int N, int GROUPS>
 __global__ void __launch_bounds__(TPR * GROUPS)
@@ -350,47 +449,26 @@ ln_fwd_ring_kernel(const __grid_constant__ LayerNormArgs a, int depth) {
     open_ring<WIDE, T, TPR, GROUPS>(ring, smem, full, dead[0], a.rows, a.D,
                                       depth);
 
-    float w[N][V], b[N][V];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = column<V, TPR>(i, t);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            w[i][v] = 1.f;
-            b[i][v] = 0.f;
-        }
-        if (a.weight && c < a.D) load_v<V>(a.weight, c, a.wdtype, w[i]);
-        if (a.bias && c < a.D) load_v<V>(a.bias, c, a.wdtype, b[i]);
-    }
+    using Row = Part<T, V, TPR, N>;
+    Row w, b;
+    w.read_weight(a.weight, a.wdtype, t, a.D, 1.f);
+    b.read_weight(a.bias, a.wdtype, t, a.D, 0.f);
     const float over = 1.f / a.D;
     bool fault = false;
     int slot = 0, phase = 0, turn = 0;
     for (long long row = (long long)blockIdx.x * GROUPS + g; row < a.rows;
          row += ring.step, turn ^= 1) {
         if (!ring.wait(slot, phase)) fault = dead[turn][g] = true;
-        const T* x = ring.row_of(slot, 0, row);
-        const T* r = a.residual ? ring.row_of(slot, 1, row) : nullptr;
-        float s[N][V];
-        float sum = 0.f;
+        Row s;
+        s.read(ring.row_of(slot, 0, row), t, a.D);
+        if (a.residual) {
+            Row r;
+            r.read(ring.row_of(slot, 1, row), t, a.D);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = column<V, TPR>(i, t);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[i][v] = 0.f;
-            if (c < a.D) {
-                read_v<T, V>(x + c, s[i]);
-                if (r) {
-                    float q[V];
-                    read_v<T, V>(r + c, q);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) s[i][v] += q[v];
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum += s[i][v];
+            for (int e = 0; e < Row::E; ++e) s.v[e] = add2(s.v[e], r.v[e]);
         }
         const float mean =
-            group_sum<TPR>(sum, red[0] + g * (TPR / 32), 1 + g) * over;
+            group_sum<TPR>(s.sum(), red[0] + g * (TPR / 32), 1 + g) * over;
         if (group_dead<TPR>(fault, &dead[turn][g])) {
             fault = true;
             break;
@@ -402,33 +480,22 @@ ln_fwd_ring_kernel(const __grid_constant__ LayerNormArgs a, int depth) {
             slot = 0;
             phase ^= 1;
         }
-        float sq = 0.f;
+        if (a.sum)
+            s.write(static_cast<T*>(a.sum) + row * a.D, t, a.D);
+        float2 sq = both(0.f);
+        Row::each(t, a.D, [&](int e, bool p, bool q) {
+            s.v[e] = add2(s.v[e], both(-mean));
+            if (!p) s.v[e].x = 0.f;
+            if (!q) s.v[e].y = 0.f;
+            sq = fma2(s.v[e], s.v[e], sq);
+        });
+        const float rstd = rsqrtf(
+            group_sum<TPR>(sq.x + sq.y, red[1] + g * (TPR / 32), 1 + g) *
+                over + a.eps);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (column<V, TPR>(i, t) < a.D) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float d = s[i][v] - mean;
-                    sq = fmaf(d, d, sq);
-                }
-            }
-        }
-        const float rstd = 1.f / sqrtf(
-            group_sum<TPR>(sq, red[1] + g * (TPR / 32), 1 + g) * over +
-            a.eps);
-        T* y = static_cast<T*>(a.y) + row * a.D;
-        T* so = a.sum ? static_cast<T*>(a.sum) + row * a.D : nullptr;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = column<V, TPR>(i, t);
-            if (c >= a.D) break;
-            if (so) write_v<T, V>(so + c, s[i]);
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                o[v] = fmaf((s[i][v] - mean) * rstd, w[i][v], b[i][v]);
-            write_v<T, V>(y + c, o);
-        }
+        for (int e = 0; e < Row::E; ++e)
+            s.v[e] = fma2(mul2(s.v[e], both(rstd)), w.v[e], b.v[e]);
+        s.write(static_cast<T*>(a.y) + row * a.D, t, a.D);
         if (t == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -467,18 +534,11 @@ ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
     open_ring<WIDE, T, TPR, GROUPS>(ring, smem, full, dead[0], a.rows, a.D,
                                       depth);
 
-    float dw[N][V], db[N][V], wr[HOLD ? N : 1][V];
-    auto weight = [&](int c, float (&w)[V]) {
+    using Row = Part<T, V, TPR, N>;
+    Row dw, db, w;
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[v] = 1.f;
-        if (a.weight && c < a.D) load_v<V>(a.weight, c, a.wdtype, w);
-    };
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
-        if (HOLD) weight(column<V, TPR>(i, t), wr[HOLD ? i : 0]);
-    }
+    for (int e = 0; e < Row::E; ++e) dw.v[e] = db.v[e] = both(0.f);
+    if (HOLD) w.read_weight(a.weight, a.wdtype, t, a.D, 1.f);
     const float over = 1.f / a.D;
     bool fault = false;
     int slot = 0, phase = 0, turn = 0;
@@ -493,33 +553,30 @@ ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
         const T* x = ring.row_of(slot, 0, row);
         const T* y = ring.row_of(slot, 1, row);
         const T* d = a.dsum ? ring.row_of(slot, 2, row) : nullptr;
-        float xh[N][V], wy[N][V];
-        float2 sum = make_float2(0.f, 0.f);
-        // xh and w dy of a run; first: the sums, too
-        auto run = [&](int i, float (&xh)[V], float (&wy)[V], bool first) {
-            const int c = column<V, TPR>(i, t);
-            float w[V];
-            if (!HOLD) weight(c, w);
-            read_v<T, V>(x + c, xh);
-            read_v<T, V>(y + c, wy);
+        // xh and w dy (zeros outside the row); dw and db, too
+        Row xh, wy;
+        auto form = [&](bool add) {
+            if (!HOLD) w.read_weight(a.weight, a.wdtype, t, a.D, 1.f);
+            xh.read(x, t, a.D, mean);
+            wy.read(y, t, a.D);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                xh[v] = (xh[v] - mean) * rstd;
-                if (first) {
-                    dw[i][v] = fmaf(wy[v], xh[v], dw[i][v]);
-                    db[i][v] += wy[v];
+            for (int e = 0; e < Row::E; ++e) {
+                xh.v[e] = mul2(add2(xh.v[e], both(-mean)), both(rstd));
+                if (add) {
+                    dw.v[e] = fma2(wy.v[e], xh.v[e], dw.v[e]);
+                    db.v[e] = add2(db.v[e], wy.v[e]);
                 }
-                wy[v] *= HOLD ? wr[HOLD ? i : 0][v] : w[v];
-                if (first) {
-                    sum.x = fmaf(wy[v], xh[v], sum.x);
-                    sum.y += wy[v];
-                }
+                wy.v[e] = mul2(wy.v[e], w.v[e]);
             }
         };
+        form(true);
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (column<V, TPR>(i, t) < a.D)
-                run(i, xh[HOLD ? i : 0], wy[HOLD ? i : 0], true);
+        for (int e = 0; e < Row::E; ++e) {
+            s1 = fma2(wy.v[e], xh.v[e], s1);
+            s2 = add2(s2, wy.v[e]);
+        }
+        const float2 sum = make_float2(s1.x + s1.y, s2.x + s2.y);
         float next_mean = 0.f, next_rstd = 0.f;
         if (row + ring.step < a.rows) {
             next_mean = a.mean[row + ring.step];
@@ -539,25 +596,22 @@ ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
             phase ^= 1;
         }
         const float c1 = c.x * over, c2 = c.y * over;
-        T* dx = static_cast<T*>(a.dx) + row * a.D;
+        if (!HOLD) form(false);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int col = column<V, TPR>(i, t);
-            if (col >= a.D) break;
-            if (!HOLD) run(i, xh[0], wy[0], false);
-            float o[V];
+        for (int e = 0; e < Row::E; ++e)
+            wy.v[e] = add2(fma2(xh.v[e], both(-c1), wy.v[e]), both(-c2));
+        if (d) {
+            Row ds;
+            ds.read(d, t, a.D);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                o[v] = rstd * (wy[HOLD ? i : 0][v] - c2 -
-                               xh[HOLD ? i : 0][v] * c1);
-            if (d) {
-                float q[V];
-                read_v<T, V>(d + col, q);
+            for (int e = 0; e < Row::E; ++e)
+                wy.v[e] = fma2(wy.v[e], both(rstd), ds.v[e]);
+        } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[v] += q[v];
-            }
-            write_v<T, V>(dx + col, o);
+            for (int e = 0; e < Row::E; ++e)
+                wy.v[e] = mul2(wy.v[e], both(rstd));
         }
+        wy.write(static_cast<T*>(a.dx) + row * a.D, t, a.D);
         mean = next_mean;
         rstd = next_rstd;
     }
@@ -573,22 +627,22 @@ ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
         __syncthreads();
         if (g != q) continue;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float2& s = total[(i * V + v) * TPR + t];
-                const float2 old = q ? s : make_float2(0.f, 0.f);
-                s = make_float2(old.x + dw[i][v], old.y + db[i][v]);
-            }
+        for (int e = 0; e < 2 * Row::E; ++e) {
+            float2& s = total[e * TPR + t];
+            const float2 old = q ? s : both(0.f);
+            const float x = e % 2 ? dw.v[e / 2].y : dw.v[e / 2].x;
+            const float y = e % 2 ? db.v[e / 2].y : db.v[e / 2].x;
+            s = make_float2(old.x + x, old.y + y);
+        }
     }
     __syncthreads();
     float* p = part + (size_t)blockIdx.x * 2 * a.D;
-    for (int e = threadIdx.x; e < a.D; e += TPR * GROUPS) {
-        // column e: run e / V, thread (e / V) % TPR
-        const int i = e / (V * TPR), u = e / V % TPR, v = e % V;
-        const float2 s = total[(i * V + v) * TPR + u];
-        p[e] = s.x;
-        p[a.D + e] = s.y;
+    for (int c = threadIdx.x; c < a.D; c += TPR * GROUPS) {
+        // column c: run c / (V TPR), thread c / V % TPR, element c % V
+        const float2 s =
+            total[(c / (V * TPR) * V + c % V) * TPR + c / V % TPR];
+        p[c] = s.x;
+        p[a.D + c] = s.y;
     }
 }
 
@@ -622,7 +676,7 @@ ln_fwd_loop_kernel(LayerNormArgs a) {
         const float d = s(i) - mean;
         t = fmaf(d, d, t);
     }
-    const float rstd = 1.f / sqrtf(block_sum(t, 0.f, red).x / a.D + a.eps);
+    const float rstd = rsqrtf(block_sum(t, 0.f, red).x / a.D + a.eps);
     T* y = static_cast<T*>(a.y) + row * a.D;
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.D : nullptr;
     for (int i = threadIdx.x; i < a.D; i += kLoopThreads) {
