@@ -33,4 +33,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// Two bf16 as they lie in memory (a bf16 is the upper half of its fp32; taken
+// apart as 16-bit numbers they would cost two instructions each).
+__device__ __forceinline__ float2 from_bf16x2(unsigned int b) {
+    return make_float2(__uint_as_float(b << 16),
+                       __uint_as_float(b & 0xffff0000u));
+}
+
 }  // namespace kla

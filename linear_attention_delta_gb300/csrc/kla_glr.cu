@@ -149,20 +149,28 @@ __device__ __forceinline__ int channel(int lane, int v) {
 
 // Two channels as they lie in memory.
 template <typename T>
-struct alignas(2 * sizeof(T)) Two {
-    T x, y;
+struct Two {
+    float2 b;
 };
-__device__ __forceinline__ float2 values(Two<float> t) {
-    return make_float2(t.x, t.y);
-}
+template <>
+struct Two<bf16> {
+    unsigned int b;
+};
+__device__ __forceinline__ float2 values(Two<float> t) { return t.b; }
 __device__ __forceinline__ float2 values(Two<bf16> t) {
-    return make_float2(__bfloat162float(t.x), __bfloat162float(t.y));
+    return from_bf16x2(t.b);
 }
 
 template <Align A, typename T>
 __device__ __forceinline__ Two<T> read2(const T* row, int lane) {
-    if constexpr (A == kElement) return {row[lane], row[lane + 32]};
-    else return reinterpret_cast<const Two<T>*>(row)[lane];
+    if constexpr (A != kElement) {
+        return reinterpret_cast<const Two<T>*>(row)[lane];
+    } else if constexpr (sizeof(T) == 4) {
+        return {make_float2(row[lane], row[lane + 32])};
+    } else {
+        const auto* r = reinterpret_cast<const unsigned short*>(row);
+        return {r[lane] | (unsigned int)r[lane + 32] << 16};
+    }
 }
 
 // To the lane's channels of an output row (`row`: the lane's own place).
@@ -172,8 +180,11 @@ __device__ __forceinline__ void write2(T* row, bool l0, bool l1, float2 c) {
         if (l0) row[0] = from_f32<T>(c.x);
         if (l1) row[32] = from_f32<T>(c.y);
     } else if (l0) {
-        *reinterpret_cast<Two<T>*>(row) =
-            Two<T>{from_f32<T>(c.x), from_f32<T>(c.y)};
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float2*>(row) = c;
+        else
+            *reinterpret_cast<unsigned int*>(row) =
+                tc::pack_bf16x2(c.x, c.y);
     }
 }
 

@@ -19,6 +19,7 @@
 // are few, a block per row loads it straight into registers.  Rows wider than
 // a block can hold take the loop kernels at the end, which read them again.
 #include <algorithm>
+#include <atomic>
 
 #include "f32x2.cuh"
 #include "kla_internal.cuh"
@@ -292,9 +293,19 @@ __device__ unsigned int g_fault_ln = 0;
 template <typename T, bool WIDE>
 constexpr int kV = WIDE ? 16 / (int)sizeof(T) : 1;
 
-template <typename T>
-__device__ __forceinline__ float2 pair_of(T x, T y) {
-    return make_float2(to_f32(x), to_f32(y));
+__device__ __forceinline__ void load_words(unsigned int (&q)[4],
+                                           const void* p) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    q[0] = v.x;
+    q[1] = v.y;
+    q[2] = v.z;
+    q[3] = v.w;
+}
+__device__ __forceinline__ void load_words(unsigned int (&q)[2],
+                                           const void* p) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    q[0] = v.x;
+    q[1] = v.y;
 }
 
 template <typename T, int V, int TPR, int N>
@@ -337,15 +348,20 @@ struct Part {
             for (int i = 0; i < N; ++i) {
 #pragma unroll
                 for (int u = 0; u < V; u += M) {
-                    Pack<U, M> q;
                     const bool in = inside(i, t, D);
+                    unsigned int q[M * sizeof(U) / 4];
                     if (in)
-                        q = *reinterpret_cast<const Pack<U, M>*>(
-                            p + column(i, t) + u);
+                        load_words(q, p + column(i, t) + u);
 #pragma unroll
-                    for (int w = 0; w < M; w += 2)
-                        v[(i * V + u + w) / 2] =
-                            in ? pair_of(q.v[w], q.v[w + 1]) : both(fill);
+                    for (int w = 0; w < M; w += 2) {
+                        float2 x;
+                        if constexpr (sizeof(U) == 2)
+                            x = from_bf16x2(q[w / 2]);
+                        else
+                            x = make_float2(__uint_as_float(q[w]),
+                                            __uint_as_float(q[w + 1]));
+                        v[(i * V + u + w) / 2] = in ? x : both(fill);
+                    }
                 }
             }
         }
@@ -514,7 +530,7 @@ ln_fwd_ring_kernel(const __grid_constant__ LayerNormArgs a, int depth) {
 // part [gridDim.x][2][D].  HOLD: w, xh and w dy stay in registers from the
 // sums to the result (else they are formed again: very wide rows).
 template <typename T, bool WIDE, int TPR, int N, int GROUPS, bool HOLD>
-__global__ void __launch_bounds__(TPR * GROUPS)
+__global__ void __launch_bounds__(TPR * GROUPS, TPR * GROUPS <= 256 ? 2 : 1)
 ln_bwd_ring_kernel(const __grid_constant__ LayerNormBwdArgs a, int depth,
                    float* part) {
     constexpr int V = kV<T, WIDE>;
@@ -787,33 +803,42 @@ bool lines_up(const void* p, size_t elt, long long stride, int vec) {
            stride % vec == 0;
 }
 
-// Blocks of a ring kernel, and its ring: as many rows as fit into about 200
-// KB for 1024 threads on an SM, 2 at least and 4 for rows copied in pieces
-// (0 blocks: they do not fit).
+// Blocks of a ring kernel, and its ring: as many rows as fit beside the other
+// blocks that an SM's registers hold, at most kMaxDepth and 2 at least; 4 for
+// rows copied in pieces (0 blocks: they do not fit).
 struct RingPlan {
     int blocks, depth, bytes;
 };
-template <typename K>
-RingPlan ring_plan(K* kernel, int threads, int groups, bool wide, int in,
-                   int elt, int D, int rows, int least) {
+constexpr int kSmBytes = 228 * 1024, kBlockBytes = 1024 + 1024;  // own, fixed
+
+template <auto K>
+RingPlan ring_plan(int threads, int groups, bool wide, int in, int elt, int D,
+                   int rows, int least) {
+    // blocks that an SM's registers and threads allow (looked up once)
+    static std::atomic<int> found[64];
     RingPlan p{0, 0, 0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return p;
+    int per = found[dev].load(std::memory_order_relaxed);
+    if (per == 0) {
+        if (cudaFuncSetAttribute(K,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 220 * 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &per, K, threads, 0) != cudaSuccess || per < 1)
+            return p;
+        found[dev].store(per, std::memory_order_relaxed);
+    }
     const int pitch = (D * elt + (wide ? 0 : 15) + 15) / 16 * 16;
     const int row = groups * in * pitch;         // of all groups of a block
-    const int want = std::max(1, 1024 / threads);
-    p.depth = wide ? std::max(2, std::min(kMaxDepth,
-                                          200 * 1024 / want / row))
-                   : 4;
+    const int share = std::min(kSmBytes / per - kBlockBytes, 220 * 1024);
+    p.depth = wide ? std::max(2, std::min(kMaxDepth, share / row)) : 4;
     p.bytes = std::max(p.depth * row, least);
     if (p.bytes > 220 * 1024) return p;
-    int per = 0;
-    if (cudaFuncSetAttribute(kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             220 * 1024) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &per, kernel, threads, p.bytes) != cudaSuccess)
-        return p;
-    p.blocks = (int)std::min<long long>(((long long)rows + groups - 1) / groups,
-                                        (long long)per * device_sm_count());
+    per = std::min(per, kSmBytes / (p.bytes + kBlockBytes));
+    p.blocks = (int)std::min<long long>(
+        ((long long)rows + groups - 1) / groups,
+        (long long)std::max(1, per) * device_sm_count());
     return p;
 }
 
@@ -827,11 +852,12 @@ cudaError_t fwd_rows(const LayerNormArgs& a, cudaStream_t s) {
 
 template <typename T, bool WIDE, int TPR, int N>
 cudaError_t fwd_ring(const LayerNormArgs& a, cudaStream_t s) {
-    constexpr int GROUPS = TPR < 256 ? 256 / TPR : 1;
-    auto* kernel = ln_fwd_ring_kernel<T, WIDE, TPR, N, GROUPS>;
-    const RingPlan p = ring_plan(kernel, TPR * GROUPS, GROUPS, WIDE,
-                                 a.residual ? 2 : 1, sizeof(T), a.D, a.rows,
-                                 0);
+    constexpr int LEAST = WIDE ? 128 : 256;      // threads of a block
+    constexpr int GROUPS = TPR < LEAST ? LEAST / TPR : 1;
+    constexpr auto* kernel = ln_fwd_ring_kernel<T, WIDE, TPR, N, GROUPS>;
+    const RingPlan p = ring_plan<kernel>(TPR * GROUPS, GROUPS, WIDE,
+                                         a.residual ? 2 : 1, sizeof(T), a.D,
+                                         a.rows, 0);
     if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
     kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth);
     return cudaGetLastError();
@@ -895,11 +921,12 @@ cudaError_t join(const LayerNormBwdArgs& a, const float* part, int slices,
 template <typename T, bool WIDE, int TPR, int N, bool HOLD = true>
 cudaError_t bwd_ring(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
     constexpr int GROUPS = TPR < 256 ? 256 / TPR : 1;
-    auto* kernel = ln_bwd_ring_kernel<T, WIDE, TPR, N, GROUPS, HOLD>;
+    constexpr auto* kernel =
+        ln_bwd_ring_kernel<T, WIDE, TPR, N, GROUPS, HOLD>;
     const bool grads = a.dw || a.db;
-    RingPlan p = ring_plan(kernel, TPR * GROUPS, GROUPS, WIDE,
-                           a.dsum ? 3 : 2, sizeof(T), a.D, a.rows,
-                           TPR * N * kV<T, WIDE> * (int)sizeof(float2));
+    RingPlan p = ring_plan<kernel>(
+        TPR * GROUPS, GROUPS, WIDE, a.dsum ? 3 : 2, sizeof(T), a.D, a.rows,
+        TPR * N * kV<T, WIDE> * (int)sizeof(float2));
     if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
     p.blocks = std::min(p.blocks, kMaxSlices);
     kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth,
@@ -926,11 +953,11 @@ cudaError_t bwd_width(const LayerNormBwdArgs& a, float* part,
     constexpr int M = WIDE ? 1 : 4;              // runs are 1 element then
     const int packs = (a.D + V - 1) / V;
     if (packs <= 32 * M) return bwd_ring<T, WIDE, 32, M>(a, part, s);
-    if (packs <= 64 * M) return bwd_ring<T, WIDE, 64, M>(a, part, s);
-    if (packs <= 128 * M) return bwd_ring<T, WIDE, 128, M>(a, part, s);
-    if (packs <= 256 * M) return bwd_ring<T, WIDE, 256, M>(a, part, s);
-    if (packs <= 512 * M) return bwd_ring<T, WIDE, 512, M>(a, part, s);
-    if (packs <= 1024 * M) return bwd_ring<T, WIDE, 1024, M>(a, part, s);
+    if (packs <= 64 * M) return bwd_ring<T, WIDE, 32, 2 * M>(a, part, s);
+    if (packs <= 128 * M) return bwd_ring<T, WIDE, 64, 2 * M>(a, part, s);
+    if (packs <= 256 * M) return bwd_ring<T, WIDE, 128, 2 * M>(a, part, s);
+    if (packs <= 512 * M) return bwd_ring<T, WIDE, 256, 2 * M>(a, part, s);
+    if (packs <= 1024 * M) return bwd_ring<T, WIDE, 512, 2 * M>(a, part, s);
     if (WIDE && packs <= 2048)
         return bwd_ring<T, WIDE, 512, 4, false>(a, part, s);
     return bwd_loop<T>(a, part, s);
