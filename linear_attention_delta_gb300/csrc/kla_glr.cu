@@ -19,7 +19,7 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // ---------------------------------------------------------------------------
-// The scan.  A tile is kTile = W * S consecutive tokens (in scan order:
+// The scan.  A tile is W * S consecutive tokens (in scan order:
 // backwards in the backward pass) of CH = 64 channels; warp w of its block
 // holds S of the tokens, a lane two of the channels.  All tiles of one run of
 // tokens (a batch entry, or all packed tokens) and one group of channels form
@@ -45,8 +45,13 @@ using bf16 = __nv_bfloat16;
 // product of decays is.
 
 constexpr int W = 4;             // warps of a block
-constexpr int S = 16;            // tokens of a warp
-constexpr int kTile = W * S;
+// Tokens of a warp, S.  With 20 rather than 16, the forward in bf16 takes
+// 65536 tokens in 150 instead of 166 us; the other kernels then spill or hold
+// fewer blocks (2048-wide backward 90 instead of 84 us).
+template <typename T, bool BWD>
+constexpr int kSteps = sizeof(T) == 2 && !BWD ? 20 : 16;
+template <typename T, bool BWD>
+constexpr int kTile = W * kSteps<T, BWD>;
 constexpr int CH = 64;           // channels of a tile
 constexpr int kThreads = 32 * W;
 constexpr int kMaxKept = 512;    // offsets of sequences kept on chip
@@ -188,40 +193,46 @@ __device__ __forceinline__ void write2(T* row, bool l0, bool l1, float2 c) {
     }
 }
 
-// Copies rows t .. t + kTile - 1 (`stride` elements apart) of `room`
-// channels into dst [kTile][kPitch]; what lies outside the rows 0 .. n - 1 or
+// Copies rows t .. t + ROWS - 1 (`stride` elements apart) of `room`
+// channels into dst [ROWS][kPitch]; what lies outside the rows 0 .. n - 1 or
 // the channels becomes zero.  A piece of 16 aligned bytes is read from its
 // start to the row's end only; the bytes that it may hold before the row
 // belong to the same allocation, which starts on 16 bytes.
-template <Align A, typename T>
+template <Align A, int ROWS, typename T>
 __device__ __forceinline__ void copy_rows(T* dst, const T* src,
                                           long long stride, long long t,
                                           int n, int room) {
     constexpr int P = kPitch<A, T> * sizeof(T) / 16;   // pieces of a row
-    static_assert(kThreads % (P - 1) == 0 && kThreads >= kTile, "");
+    static_assert(kThreads % (P - 1) == 0 && kThreads >= ROWS, "");
     const uintptr_t none =
         reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15;
     const int bytes = min(room, CH) * (int)sizeof(T);
-    const unsigned int to = tc::smem_u32(dst);
-    auto piece = [&](int r, int p, uintptr_t row) {
-        const uintptr_t from = (row & ~(uintptr_t)15) + p * 16;
-        const int left = (int)(row - from) + bytes;
-        const bool in = t + r >= 0 && t + r < n && left > 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         to + (r * P + p) * 16),
-                     "l"(in ? from : none), "r"(in ? min(left, 16) : 0)
+    const int first = (int)max(0ll, -t), last = (int)min((long long)ROWS, n - t);
+    auto piece = [&](int r, int p, uintptr_t row, unsigned int to) {
+        const int left = (int)(row & 15) + bytes - p * 16;
+        const bool in = r >= first && r < last && left > 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                     "l"(in ? (row & ~(uintptr_t)15) + p * 16 : none),
+                     "r"(in ? min(left, 16) : 0)
                      : "memory");
     };
     // all pieces but the last: a thread keeps its place in the row
     constexpr int R = kThreads / (P - 1);
     const int r0 = threadIdx.x / (P - 1), p0 = threadIdx.x % (P - 1);
     uintptr_t row = reinterpret_cast<uintptr_t>(src + (t + r0) * stride);
+    unsigned int to = tc::smem_u32(dst) + (r0 * P + p0) * 16;
     const long long by = R * stride * (long long)sizeof(T);
-#pragma unroll 4
-    for (int r = r0; r < kTile; r += R, row += by) piece(r, p0, row);
-    if (threadIdx.x < kTile)
+#pragma unroll
+    for (int r = 0; r < ROWS / R * R; r += R) {
+        piece(r0 + r, p0, row, to);
+        row += by;
+        to += R * P * 16;
+    }
+    if (ROWS % R && r0 < ROWS % R) piece(r0 + ROWS / R * R, p0, row, to);
+    if (threadIdx.x < ROWS)
         piece(threadIdx.x, P - 1,
-              reinterpret_cast<uintptr_t>(src + (t + threadIdx.x) * stride));
+              reinterpret_cast<uintptr_t>(src + (t + threadIdx.x) * stride),
+              tc::smem_u32(dst) + (threadIdx.x * P + P - 1) * 16);
 }
 // Where a row starts within its first piece (elements): of row t, and how
 // that moves from row to row.
@@ -261,7 +272,7 @@ struct Bounds {
 // downwards with BACK).  A warp works together: a 32-way search for the
 // sequence of t, then 32 offsets at a time.  Any content of cu gives
 // 0 <= n, last < B.
-template <bool BACK>
+template <int S, bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
                                               long long t) {
     const int lane = threadIdx.x % 32;
@@ -301,21 +312,22 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
 // The tiles of a block, in its order: tile k of the run of tokens b, channels
 // from d on.
 struct Cursor {
-    int round, b, d, k, step;
+    int round, b, d, k, step, member;            // member of the team
     bool more;
     __device__ Cursor(const ScanPlan& p) : round(-1) { open(p); }
     __device__ void open(const ScanPlan& p) {    // the next chain
         ++round;
         int chain = round * (int)gridDim.x + blockIdx.x;
         more = round < p.rounds;
-        k = 0;
+        member = 0;
         step = 1;
         if (round == p.rounds) {
             chain = round * (int)gridDim.x + blockIdx.x / p.team;
             more = blockIdx.x < p.rest * p.team;
-            k = blockIdx.x % p.team;
+            member = blockIdx.x % p.team;
             step = p.team;
         }
+        k = member;
         b = chain / p.groups;
         d = chain % p.groups * CH;
     }
@@ -327,14 +339,14 @@ struct Cursor {
 
 template <typename T, typename G, Align A, bool BWD>
 struct Stage {
-    T x[kTile][kPitch<A, T>];
-    G la[kTile][kPitch<A, G>];
+    T x[kTile<T, BWD>][kPitch<A, T>];
+    G la[kTile<T, BWD>][kPitch<A, G>];
 };
 template <typename T, typename G, Align A>
 struct Stage<T, G, A, true> {
-    T x[kTile][kPitch<A, T>];    // o of the token before
-    G la[kTile][kPitch<A, G>];
-    T g[kTile][kPitch<A, T>];    // o_grad
+    T x[kTile<T, true>][kPitch<A, T>];           // o of the token before
+    G la[kTile<T, true>][kPitch<A, G>];
+    T g[kTile<T, true>][kPitch<A, T>];           // o_grad
 };
 template <typename T, typename G, Align A, bool BWD>
 struct Shared {
@@ -370,6 +382,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     // the team's maps of this step and the next: [2][team][32]
     auto* maps = reinterpret_cast<float4(*)[32]>(&sh + 1);
     constexpr int DT = BWD ? -1 : 1;             // token step of the scan
+    constexpr int S = kSteps<T, BWD>, TILE = kTile<T, BWD>;
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     const float* init = BWD ? a.dhT : a.h0;
 
@@ -392,8 +405,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         // (the last warp has the tile's map to form meanwhile)
         if (at.more && (A != kWide || threadIdx.x == 0)) {
             const int b = at.b, d = at.d;
-            const int p = at.k * kTile;
-            const int lo = BWD ? a.T - kTile - p : p;
+            const int p = at.k * TILE;
+            const int lo = BWD ? a.T - TILE - p : p;
             if constexpr (A == kWide) {
                 tc::mbar_arrive_expect_tx(&sh.full, sizeof(st));
                 tma_load_3d(&st.la[0][0], &map_la, &sh.full, d, lo, b);
@@ -403,14 +416,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     tma_load_3d(&st.g[0][0], &map_g, &sh.full, d, lo, b);
             } else {
                 const int room = a.D - d;
-                copy_rows<A>(&st.la[0][0],
+                copy_rows<A, TILE>(&st.la[0][0],
                              static_cast<const G*>(a.la.p) + b * a.la.sb + d,
                              a.la.st, lo, a.T, room);
-                copy_rows<A>(&st.x[0][0],
+                copy_rows<A, TILE>(&st.x[0][0],
                              static_cast<const T*>(a.x.p) + b * a.x.sb + d,
                              a.x.st, BWD ? lo - 1ll : lo, a.T, room);
                 if constexpr (BWD)
-                    copy_rows<A>(&st.g[0][0],
+                    copy_rows<A, TILE>(&st.g[0][0],
                                  static_cast<const T*>(a.g.p) + b * a.g.sb +
                                      d,
                                  a.g.st, lo, a.T, room);
@@ -429,11 +442,11 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     Bounds soon{0u, here.b, here.b};
     float2 soon_start = both(0.f), soon_prev = both(0.f);
     auto look = [&](const Cursor& at) {
-        const int p = at.k * kTile + w * S;
+        const int p = at.k * TILE + w * S;
         soon = Bounds{0u, at.b, at.b};
         if (a.cu) {
             if (!at.more || p >= a.T) return;
-            soon = find_bounds<BWD>(cu, a.B, BWD ? a.T - 1 - p : p);
+            soon = find_bounds<S, BWD>(cu, a.B, BWD ? a.T - 1 - p : p);
         } else {
             if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
             if (p == 0) soon.mask = 1u;
@@ -471,7 +484,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         const int db = here.d + channel<A>(lane, 1);
         const bool la = da < a.D, lb = db < a.D;
         // scan position p <-> token t
-        const int p0 = here.k * kTile + w * S;
+        const int p0 = here.k * TILE + w * S;
         const int t0 = BWD ? a.T - 1 - p0 : p0;
         const int steps = max(0, min(S, a.T - p0));
         if (here.k < here.step) carry = both(0.f);       // a chain begins
@@ -484,18 +497,6 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         // nothing begins, ends or is missing here
         const bool plain = bd.mask == 0 && steps == S;
 
-        // Moves n on to the sequence that begins at step i.
-        auto next = [&](int i, int& n) {
-            if (!a.cu || i == 0) return;
-            const int t = t0 + i * DT;
-            if (BWD) {
-                n = max(n - 1, 0);
-                while (n > 0 && cu[n] > t) --n;
-            } else {
-                n = min(n + 1, a.B - 1);
-                while (n < a.B - 1 && cu[n + 1] <= t) ++n;
-            }
-        };
         auto state_of = [&](const float* p, int n) {
             float2 c = both(0.f);
             if (p && la) c.x = p[(size_t)n * a.D + da];
@@ -517,44 +518,43 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         float2 al[S];                // decays
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
         float2 P = both(1.f), H = both(0.f);
-        int n = bd.n;
         // rows that do not line up on 16 bytes: where each starts
-        const int lo = BWD ? a.T - kTile - here.k * kTile : here.k * kTile;
+        const int lo = BWD ? a.T - TILE - here.k * TILE : here.k * TILE;
         const Shift<G> sl(static_cast<const G*>(a.la.p) + b * a.la.sb +
                               here.d, a.la.st, lo);
         const Shift<T> sx(static_cast<const T*>(a.x.p) + b * a.x.sb + here.d,
                           a.x.st, BWD ? lo - 1ll : lo);
         const Shift<T> sg(static_cast<const T*>(a.g.p) + b * a.g.sb + here.d,
                           a.g.st, lo);
-        auto reduce = [&](auto events) {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (decltype(events)::value && begins >> i & 1) {
-                    if (begins >> (i + 1)) {
-                        next(i, n);
-                        H = state_of(init, n);
-                    } else {
-                        H = start;
-                    }
-                    P = both(-0.f);
-                }
-                const int r = BWD ? kTile - 1 - (w * S + i) : w * S + i;
-                const int ol = A == kWide ? 0 : sl(r);
-                const int ox = A == kWide ? 0 : sx(r);
-                al[i] = decay(values(read2<A>(st.la[r] + ol, lane)));
-                x[i] = read2<A>(st.x[r] + ox, lane);
-                P = mul2(P, al[i]);
-                if constexpr (BWD) {
-                    const int og = A == kWide ? 0 : sg(r);
-                    g[i] = read2<A>(st.g[r] + og, lane);
-                    H = mul2(al[i], add2(H, values(g[i])));
-                } else {
-                    H = fma2(al[i], H, values(x[i]));
-                }
+        for (int i = 0; i < S; ++i) {
+            const int r = BWD ? TILE - 1 - (w * S + i) : w * S + i;
+            const int ol = A == kWide ? 0 : sl(r);
+            const int ox = A == kWide ? 0 : sx(r);
+            al[i] = decay(values(read2<A>(st.la[r] + ol, lane)));
+            x[i] = read2<A>(st.x[r] + ox, lane);
+            P = mul2(P, al[i]);
+            if constexpr (BWD) {
+                const int og = A == kWide ? 0 : sg(r);
+                g[i] = read2<A>(st.g[r] + og, lane);
+                H = mul2(al[i], add2(H, values(g[i])));
+            } else {
+                H = fma2(al[i], H, values(x[i]));
             }
-        };
-        if (plain) reduce(std::false_type());
-        else reduce(std::true_type());
+        }
+        if (begins) {                // only the last sequence matters
+            const int from = 31 - __clz(begins);
+            P = both(-0.f);
+            H = start;
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+                if (i >= from) {
+                    if constexpr (BWD)
+                        H = mul2(al[i], add2(H, values(g[i])));
+                    else
+                        H = fma2(al[i], H, values(x[i]));
+                }
+        }
         const float4 mine =
             make_float4(bounded(P.x), bounded(P.y), H.x, H.y);
         if (w < W - 1) sh.own[h][w][lane] = mine;
@@ -567,7 +567,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         then.move(plan);
         fetch(then);
 
-        const int m = here.k % here.step;
+        const int m = here.member;
         const int there = min(here.step, plan.tiles - (here.k - m));
         float4(*team)[32] = maps + h * here.step;
         if (w == W - 1) {            // the tile's map, to all of the team
@@ -600,10 +600,13 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (w == 0) {                // the state before the tile, and after
             fault |= !wait_maps(&sh.got[h], turn >> 1 & 1);
             if (anew) {
-                for (int j = 0; j < there; ++j) {
-                    if (j == m) sh.start[lane] = carry;
+#pragma unroll 4
+                for (int j = 0; j < m; ++j)
                     carry = apply(team[j][lane], carry);
-                }
+                sh.start[lane] = carry;
+#pragma unroll 4
+                for (int j = m; j < there; ++j)
+                    carry = apply(team[j][lane], carry);
             } else {
                 int j = 0;
 #pragma unroll 4
@@ -627,31 +630,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         const size_t out = ((size_t)b * a.T + t0) * a.D + da;
         T* op = static_cast<T*>(a.o) + out;
         G* dp = static_cast<G*>(a.dla) + out;
-        n = bd.n;
-        auto write = [&](auto events) {
+        if (plain) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (decltype(events)::value) {
-                    if (i >= steps) break;
-                    if (begins >> i & 1) {
-                        if (begins >> (i + 1)) {
-                            next(i, n);
-                            c = state_of(init, n);
-                        } else {
-                            n = bd.last;
-                            c = start;
-                        }
-                    }
-                }
-                const bool ends =
-                    decltype(events)::value && (bd.mask >> (i + 1) & 1);
                 if constexpr (BWD) {
-                    float2 h = values(x[i]);
-                    if (ends) h = n == bd.n ? prev : state_of(a.h0, n);
                     c = add2(c, values(g[i]));
                     write2<A>(op, la, lb, c);
                     c = mul2(al[i], c);
-                    write2<A>(dp, la, lb, mul2(c, h));
+                    write2<A>(dp, la, lb, mul2(c, values(x[i])));
                     dp -= a.D;
                     op -= a.D;
                 } else {
@@ -659,11 +645,55 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     write2<A>(op, la, lb, c);
                     op += a.D;
                 }
-                if (ends) keep_state(n, c);
             }
-        };
-        if (plain) write(std::false_type());
-        else write(std::true_type());
+        } else if (steps > 0) {
+            // One sequence after the other, steps from .. to - 1 each: the
+            // code of all steps stands here once (unrolled with all that may
+            // happen at each, it was so long that warps with a boundary
+            // waited for its instructions).
+            int from = 0, n = bd.n;
+            if (begins & 1) c = begins == 1 ? start : state_of(init, n);
+            while (true) {
+                const unsigned int rest = bd.mask >> (from + 1);
+                const int to = min(rest ? from + __ffs(rest) : S, steps);
+                float2 before = both(0.f);
+                if (BWD && rest)
+                    before = n == bd.n ? prev : state_of(a.h0, n);
+#pragma unroll
+                for (int i = 0; i < S; ++i) {
+                    if (i < from || i >= to) continue;
+                    const long long at = (long long)(i * DT) * a.D;
+                    if constexpr (BWD) {
+                        float2 h = values(x[i]);
+                        if (rest && i == to - 1) h = before;
+                        c = add2(c, values(g[i]));
+                        write2<A>(op + at, la, lb, c);
+                        c = mul2(al[i], c);
+                        write2<A>(dp + at, la, lb, mul2(c, h));
+                    } else {
+                        c = fma2(al[i], c, values(x[i]));
+                        write2<A>(op + at, la, lb, c);
+                    }
+                }
+                if (rest) keep_state(n, c);
+                if (!rest || to >= steps) break;
+                from = to;
+                if (begins >> (from + 1)) {      // not the last that begins
+                    const int t = t0 + from * DT;
+                    if (BWD) {
+                        n = max(n - 1, 0);
+                        while (n > 0 && cu[n] > t) --n;
+                    } else {
+                        n = min(n + 1, a.B - 1);
+                        while (n < a.B - 1 && cu[n + 1] <= t) ++n;
+                    }
+                    c = state_of(init, n);
+                } else {
+                    n = bd.last;
+                    c = start;
+                }
+            }
+        }
 
         // empty sequences, shared out over the tiles
         if (a.cu && a.hT && a.hT != init) {
@@ -772,10 +802,11 @@ ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
     return best;
 }
 
-// The element's tensor map over [B, T, D] with boxes of kTile tokens x CH
-// channels (zeros outside).
+// The element's tensor map over [B, T, D] with boxes of `tokens` tokens x
+// CH channels (zeros outside).
 template <typename T>
-bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a) {
+bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a,
+                   int tokens) {
     const bool packed = a.cu != nullptr;
     cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.T,
                           (cuuint64_t)(packed ? 1 : a.B)};
@@ -784,7 +815,7 @@ bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a) {
     cuuint64_t strides[2] = {
         a.T > 1 ? (cuuint64_t)x.st * sizeof(T) : row,
         !packed && a.B > 1 ? (cuuint64_t)x.sb * sizeof(T) : row * a.T};
-    cuuint32_t box[3] = {CH, kTile, 1}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {CH, (cuuint32_t)tokens, 1}, es[3] = {1, 1, 1};
     return tile_map_encoder()(
                m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
@@ -799,6 +830,7 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
     const long long chains =
         (long long)((a.D + CH - 1) / CH) * (a.cu ? 1 : a.B);
     if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
+    constexpr int TILE = kTile<T, BWD>;
     auto* kernel = glr_scan_kernel<T, G, A, BWD>;
     cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -809,12 +841,13 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     int blocks = 0;
     const ScanPlan p = plan_of<T, G, A, BWD>(
-        chains, (int)((a.T + (long long)kTile - 1) / kTile), a.D, &blocks);
+        chains, (int)((a.T + (long long)TILE - 1) / TILE), a.D, &blocks);
     if (blocks <= 0) return cudaErrorInvalidValue;
     CUtensorMap mx{}, ml{}, mg{};
     if (A == kWide &&
-        (!make_tile_map<T>(&mx, a.x, a) || !make_tile_map<G>(&ml, a.la, a) ||
-         (BWD && !make_tile_map<T>(&mg, a.g, a))))
+        (!make_tile_map<T>(&mx, a.x, a, TILE) ||
+         !make_tile_map<G>(&ml, a.la, a, TILE) ||
+         (BWD && !make_tile_map<T>(&mg, a.g, a, TILE))))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
