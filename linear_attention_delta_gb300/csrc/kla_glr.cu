@@ -45,11 +45,18 @@ using bf16 = __nv_bfloat16;
 // product of decays is.
 
 constexpr int W = 4;             // warps of a block
-// Tokens of a warp, S.  With 20 rather than 16, the forward in bf16 takes
-// 65536 tokens in 150 instead of 166 us; the other kernels then spill or hold
-// fewer blocks (2048-wide backward 90 instead of 84 us).
+// Tokens of a warp, S, and blocks that an SM is to hold, which bounds a
+// thread's registers (3: 168, 2: 255; the decays take 2 per token, each input
+// 1 or 2).  More tokens mean fewer exchanges, more blocks hide them.  Measured
+// (us; 65536 tokens x 2048 forward, 4 x 4096 x 2048 forward with fp32 gates):
+// bf16 forward 24 and 3 blocks 145, 47.8; 16 and 4 158, 46.4; 28 and 3 140,
+// 48.0; 12 and 5 220, 48.5.  bf16 backward (the second) 16 and 3 blocks 79;
+// 20 and 3 87; 12 and 4 81.  fp32, 16384 x 1000 forward: 20 and 2 blocks 45;
+// 16 and 3 48; backward, 8191 x 1001 packed: 51 and 61.
 template <typename T, bool BWD>
-constexpr int kSteps = sizeof(T) == 2 && !BWD ? 20 : 16;
+constexpr int kSteps = sizeof(T) == 4 ? 20 : BWD ? 16 : 24;
+template <typename T>
+constexpr int kResident = sizeof(T) == 4 ? 2 : 3;
 template <typename T, bool BWD>
 constexpr int kTile = W * kSteps<T, BWD>;
 constexpr int CH = 64;           // channels of a tile
@@ -362,16 +369,8 @@ template <typename T, typename G, Align A, bool BWD>
 constexpr int shared_bytes(int team) {
     return (int)sizeof(Shared<T, G, A, BWD>) + 2 * team * 512;
 }
-// Blocks that an SM is to hold: as many as leave the registers that a thread
-// needs (128 with 4 blocks, 168 with 3; with one block more each, the kernel
-// spills and the 2048-wide layer takes 63 instead of 51 us).
-template <typename T, bool BWD>
-constexpr int resident() {
-    return sizeof(T) == 2 && !BWD ? 4 : 3;
-}
-
 template <typename T, typename G, Align A, bool BWD>
-__global__ void __launch_bounds__(kThreads, (resident<T, BWD>()))
+__global__ void __launch_bounds__(kThreads, kResident<T>)
 glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 const __grid_constant__ ScanPlan plan,
                 const __grid_constant__ CUtensorMap map_x,
@@ -767,11 +766,18 @@ int capacity(int team) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int n = found[dev][team].load(std::memory_order_relaxed);
     if (n > 0) return n;
+    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     team_config<T, G, A, BWD>(cfg, attr, team, team);
-    if (cudaOccupancyMaxActiveClusters(&n, glr_scan_kernel<T, G, A, BWD>,
-                                       &cfg) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             shared_bytes<T, G, A, BWD>(kMaxTeam)) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
         return 0;
     n *= team;
     found[dev][team].store(n, std::memory_order_relaxed);
@@ -832,13 +838,6 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
     if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
     constexpr int TILE = kTile<T, BWD>;
     auto* kernel = glr_scan_kernel<T, G, A, BWD>;
-    cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        shared_bytes<T, G, A, BWD>(kMaxTeam));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
     int blocks = 0;
     const ScanPlan p = plan_of<T, G, A, BWD>(
         chains, (int)((a.T + (long long)TILE - 1) / TILE), a.D, &blocks);
