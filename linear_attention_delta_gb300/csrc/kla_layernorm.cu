@@ -958,6 +958,10 @@ cudaError_t bwd_width(const LayerNormBwdArgs& a, float* part,
     if (packs <= 256 * M) return bwd_ring<T, WIDE, 128, 2 * M>(a, part, s);
     if (packs <= 512 * M) return bwd_ring<T, WIDE, 256, 2 * M>(a, part, s);
     if (packs <= 1024 * M) return bwd_ring<T, WIDE, 512, 2 * M>(a, part, s);
+    // (a thread has the registers for 2 runs up to about 640 threads; 4 runs
+    // formed twice take 38 instead of 28 us on 1023 rows of 8200)
+    if (WIDE && packs <= 1280) return bwd_ring<T, WIDE, 640, 2>(a, part, s);
+    if (WIDE && packs <= 1536) return bwd_ring<T, WIDE, 768, 2>(a, part, s);
     if (WIDE && packs <= 2048)
         return bwd_ring<T, WIDE, 512, 4, false>(a, part, s);
     return bwd_loop<T>(a, part, s);

@@ -9,6 +9,7 @@ without CUDA tensors these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -643,11 +644,6 @@ def _workspace(workspace, nbytes, device):
     return workspace, workspace.numel()
 
 
-def _done(name, status):
-    if status != KLA_OK:
-        raise KlaError(name, status)
-
-
 def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
                   residual=None, y=None, sum=None, want_stats: bool = True,
                   stream=None):
@@ -673,11 +669,12 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
     wt, rs = dt, 0
     if weight is not None or bias is not None:
         wt = getattr(bias if weight is None else weight, "dtype", dt)
-        for name, t in (("weight", weight), ("bias", bias)):
-            if t is not None:
-                _exact(name, t, dev, wt, (D,))
         if wt not in DTYPES:
             raise TypeError(f"unsupported weight or bias dtype {wt}")
+        if weight is not None:
+            _exact("weight", weight, dev, wt, (D,))
+        if bias is not None:
+            _exact("bias", bias, dev, wt, (D,))
     if residual is not None:
         rs = _input_rows("residual", residual, dev, dt, shape)
         if sum is None:
@@ -694,13 +691,16 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
     if want_stats:
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty_like(mean)
-    _done("kla_layernorm_fwd", load_library().kla_layernorm_fwd(
+    st = load_library().kla_layernorm_fwd(
         x.data_ptr(), xs, _addr(residual), rs, _addr(weight), _addr(bias),
         eps, y.data_ptr(), _addr(sum), _addr(mean), _addr(rstd),
-        x.numel() // D, D, DTYPES[dt], DTYPES[wt], _raw_stream(dev)))
+        x.numel() // D, D, DTYPES[dt], DTYPES[wt], _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_layernorm_fwd", st)
     return y, sum, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def layernorm_bwd_workspace_size(rows: int, D: int, dtype) -> int:
     """Bytes of device workspace ``layernorm_bwd`` needs."""
     n = ctypes.c_size_t(0)
@@ -754,11 +754,13 @@ def layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad=None,
         db = torch.empty_like(dw)
         workspace, nbytes = _workspace(
             workspace, layernorm_bwd_workspace_size(rows, D, dt), dev)
-    _done("kla_layernorm_bwd", load_library().kla_layernorm_bwd(
+    st = load_library().kla_layernorm_bwd(
         y_grad.data_ptr(), ys, x.data_ptr(), xs, _addr(weight),
         mean.data_ptr(), rstd.data_ptr(), _addr(sum_grad), ss, dx.data_ptr(),
         _addr(dw), _addr(db), rows, D, DTYPES[dt], DTYPES[wt],
-        _addr(workspace), nbytes, _raw_stream(dev)))
+        _addr(workspace), nbytes, _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_layernorm_bwd", st)
     return dict(x_grad=dx, weight_grad=dw, bias_grad=db)
 
 
@@ -827,11 +829,13 @@ def glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, o=None, hT=None,
         _exact("hT", hT, dev, torch.float32, (B, D))
     elif want_state:
         hT = torch.empty((B, D), dtype=torch.float32, device=dev)
-    _done("kla_glr_fwd", load_library().kla_glr_fwd(
+    st = load_library().kla_glr_fwd(
         x.data_ptr(), *_strides(x), log_alpha.data_ptr(),
         *_strides(log_alpha), _addr(h0), o.data_ptr(), _addr(hT),
         _addr(cu_seqlens), B, T, D, DTYPES[dt], DTYPES[gt],
-        _raw_stream(dev)))
+        _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_glr_fwd", st)
     return o, hT
 
 
@@ -858,12 +862,14 @@ def glr_bwd(o, log_alpha, o_grad, hT_grad=None, h0=None, cu_seqlens=None,
     dla = torch.empty(shape, dtype=gt, device=dev)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) \
         if want_h0_grad else None
-    _done("kla_glr_bwd", load_library().kla_glr_bwd(
+    st = load_library().kla_glr_bwd(
         o.data_ptr(), *_strides(o), log_alpha.data_ptr(),
         *_strides(log_alpha), _addr(h0), o_grad.data_ptr(),
         *_strides(o_grad), _addr(hT_grad), dx.data_ptr(), dla.data_ptr(),
         _addr(dh0), _addr(cu_seqlens), B, T, D, DTYPES[dt], DTYPES[gt],
-        _raw_stream(dev)))
+        _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_glr_bwd", st)
     return dict(x_grad=dx, log_alpha_grad=dla, h0_grad=dh0)
 
 
@@ -887,10 +893,12 @@ def glr_step(x, log_alpha, S, o=None, stream=None):
         o = torch.empty(shape, dtype=dt, device=dev)
     else:
         _exact("o", o, dev, dt, shape)
-    _done("kla_glr_step", load_library().kla_glr_step(
+    st = load_library().kla_glr_step(
         x.data_ptr(), x.stride(0), log_alpha.data_ptr(), log_alpha.stride(0),
         S.data_ptr(), o.data_ptr(), shape[0], shape[1], DTYPES[dt],
-        DTYPES[gt], _raw_stream(dev)))
+        DTYPES[gt], _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_glr_step", st)
     return o
 
 
