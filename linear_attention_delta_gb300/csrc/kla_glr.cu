@@ -714,22 +714,47 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     else if (fault) __syncthreads();
 }
 
-template <typename T, typename G>
-__global__ void glr_step_kernel(const T* x, long long xs, const G* la,
-                                long long ls, float* S, T* o, int N, int D) {
-    const int d = blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= D) return;
-    for (int n = blockIdx.y; n < N; n += gridDim.y) {
-        const size_t i = (size_t)n * D + d;
-        const float h =
-            fmaf(expf(to_f32(la[n * ls + d])), S[i], to_f32(x[n * xs + d]));
-        S[i] = h;
-        o[i] = from_f32<T>(h);
+// ---------------------------------------------------------------------------
+// One token: each state is read and written once.  A thread takes 4 channels
+// of a sequence, adjacent ones (V = 4) or, where they do not line up, single
+// ones 128 apart (V = 1), so that their loads are on their way together.
+template <typename T, typename G, int V>
+__global__ void __launch_bounds__(128)
+glr_step_kernel(const T* x, long long xs, const G* la, long long ls,
+                float* S, T* o, int N, int D) {
+    struct alignas(sizeof(T) * V) PT { T v[V]; };
+    struct alignas(sizeof(G) * V) PG { G v[V]; };
+    struct alignas(4 * V) PS { float v[V]; };
+    constexpr int U = 4 / V;
+    const int d0 = blockIdx.x * 512 + threadIdx.x * V;
+    for (long long n = blockIdx.y; n < N; n += gridDim.y) {
+        const size_t i = (size_t)n * D;
+        PT px[U];
+        PG pl[U];
+        PS ps[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int d = d0 + u * 128;
+            if (d >= D) continue;
+            px[u] = *reinterpret_cast<const PT*>(x + n * xs + d);
+            pl[u] = *reinterpret_cast<const PG*>(la + n * ls + d);
+            ps[u] = *reinterpret_cast<const PS*>(S + i + d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int d = d0 + u * 128;
+            if (d >= D) continue;
+            PT po;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                ps[u].v[v] = fmaf(expf(to_f32(pl[u].v[v])), ps[u].v[v],
+                                  to_f32(px[u].v[v]));
+                po.v[v] = from_f32<T>(ps[u].v[v]);
+            }
+            *reinterpret_cast<PS*>(S + i + d) = ps[u];
+            *reinterpret_cast<PT*>(o + i + d) = po;
+        }
     }
-}
-
-dim3 grid_of(int D, int N) {
-    return dim3((D + 127) / 128, N < 65535 ? N : 65535);
 }
 
 // f<T, G>() for the pair of element types.
@@ -920,7 +945,16 @@ cudaError_t launch_glr_step(const void* x, long long x_stride,
     return by_type(dtype, gdtype, [&](auto t, auto g) {
         using T = decltype(t);
         using G = decltype(g);
-        glr_step_kernel<T, G><<<grid_of(D, N), 128, 0, stream>>>(
+        auto aligned = [](const void* p, size_t n) {
+            return reinterpret_cast<uintptr_t>(p) % n == 0;
+        };
+        const bool four = D % 4 == 0 && x_stride % 4 == 0 &&
+                          la_stride % 4 == 0 && aligned(x, 4 * sizeof(T)) &&
+                          aligned(la, 4 * sizeof(G)) && aligned(S, 16) &&
+                          aligned(o, 4 * sizeof(T));
+        const dim3 grid((D + 511) / 512, std::min(N, 65535));
+        (four ? glr_step_kernel<T, G, 4>
+              : glr_step_kernel<T, G, 1>)<<<grid, 128, 0, stream>>>(
             static_cast<const T*>(x), x_stride, static_cast<const G*>(la),
             la_stride, S, static_cast<T*>(o), N, D);
         return cudaGetLastError();
