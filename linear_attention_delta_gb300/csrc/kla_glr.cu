@@ -276,12 +276,12 @@ struct Bounds {
 };
 
 // Packed sequences: the boundaries among the S tokens from t on (upwards, or
-// downwards with BACK).  A warp works together: a 32-way search for the
+// downwards with BACK), of which `steps` are there.  A warp works together: a 32-way search for the
 // sequence of t, then 32 offsets at a time.  Any content of cu gives
 // 0 <= n, last < B.
 template <int S, bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
-                                              long long t) {
+                                              long long t, int steps) {
     const int lane = threadIdx.x % 32;
     int lo = 0, len = B;
     while (len > 1) {
@@ -294,7 +294,7 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
         len = min(step, len - skip);
     }
     unsigned int mask = 0;
-    int last = lo;                   // the outermost boundary before step S
+    int last = lo;               // of the outermost boundary that begins one
     for (int j0 = BACK ? lo + 1 : lo;;) {
         const int j = BACK ? j0 - lane : j0 + lane;
         long long pos = -1;          // step at which the boundary lies
@@ -307,7 +307,7 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
         mask |= __reduce_or_sync(0xffffffffu, in ? 1u << pos : 0u);
         // upwards the sequence from the last such offset on, downwards the
         // one up to the first
-        const int at = in && pos < S ? (BACK ? j - 1 : j) : last;
+        const int at = in && pos < steps ? (BACK ? j - 1 : j) : last;
         last = BACK ? __reduce_min_sync(0xffffffffu, at)
                     : __reduce_max_sync(0xffffffffu, at);
         if (__any_sync(0xffffffffu, beyond)) break;
@@ -445,7 +445,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         soon = Bounds{0u, at.b, at.b};
         if (a.cu) {
             if (!at.more || p >= a.T) return;
-            soon = find_bounds<S, BWD>(cu, a.B, BWD ? a.T - 1 - p : p);
+            soon = find_bounds<S, BWD>(cu, a.B, BWD ? a.T - 1 - p : p,
+                                       min(S, a.T - p));
         } else {
             if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
             if (p == 0) soon.mask = 1u;
@@ -492,7 +493,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         const float2 start = soon_start, prev = soon_prev;
         // whether some map of this step may start anew
         const bool anew = a.cu || here.k < here.step;
-        const unsigned int begins = bd.mask & ((1u << S) - 1);
+        const unsigned int begins = bd.mask & ((1u << steps) - 1);
         // nothing begins, ends or is missing here
         const bool plain = bd.mask == 0 && steps == S;
 
@@ -564,7 +565,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         }
         Cursor then = here;
         then.move(plan);
-        fetch(then);
+        if (A == kWide) fetch(then);
 
         const int m = here.member;
         const int there = min(here.step, plan.tiles - (here.k - m));
@@ -595,7 +596,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             for (int r = 0; r < there; ++r)
                 send(&team[m][lane], &sh.got[h], first + r, t);
         }
-        look(then);                  // meanwhile
+        // meanwhile
+        if (A != kWide) fetch(then);
+        look(then);
         if (w == 0) {                // the state before the tile, and after
             fault |= !wait_maps(&sh.got[h], turn >> 1 & 1);
             if (anew) {
@@ -645,11 +648,43 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     op += a.D;
                 }
             }
+        } else if (steps > 0 && (begins & (begins - 1)) == 0) {
+            // At most one sequence begins here (at `turn_at`), where the one
+            // before it ends; another end may be after the last step.  (Code
+            // that warps with a boundary alone run costs them most by its
+            // length: its instructions have to be fetched.)
+            const int turn_at = begins ? __ffs(begins) - 1 : S;
+            const bool last_ends = bd.mask >> steps & 1;
+            float2 ended = both(0.f), before = prev;
+            if (BWD && last_ends && begins && turn_at > 0)
+                before = state_of(a.h0, bd.last);
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (i == turn_at) {
+                    ended = c;
+                    c = start;
+                }
+                const long long at = (long long)(i * DT) * a.D;
+                const bool l0 = la && i < steps, l1 = lb && i < steps;
+                if constexpr (BWD) {
+                    float2 h = values(x[i]);
+                    if (i == turn_at - 1) h = prev;
+                    if (last_ends && i == steps - 1) h = before;
+                    c = add2(c, values(g[i]));
+                    write2<A>(op + at, l0, l1, c);
+                    c = mul2(al[i], c);
+                    write2<A>(dp + at, l0, l1, mul2(c, h));
+                } else {
+                    c = fma2(al[i], c, values(x[i]));
+                    write2<A>(op + at, l0, l1, c);
+                }
+            }
+            if (begins > 1) keep_state(bd.n, ended);
+            // (steps that are missing leave c as it is)
+            if (last_ends)
+                keep_state(begins ? bd.last : bd.n, c);
         } else if (steps > 0) {
-            // One sequence after the other, steps from .. to - 1 each: the
-            // code of all steps stands here once (unrolled with all that may
-            // happen at each, it was so long that warps with a boundary
-            // waited for its instructions).
+            // One sequence after the other, steps from .. to - 1 each.
             int from = 0, n = bd.n;
             if (begins & 1) c = begins == 1 ? start : state_of(init, n);
             while (true) {
