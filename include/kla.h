@@ -33,7 +33,8 @@
  *     next synchronisation, as with any CUDA call; bounded device-side waits
  *     that give up are reported by kla_device_status().
  *   - No C++ exception crosses this interface.
- *   - Tensors are contiguous and row-major.  Pointers to bf16 data must be
+ *   - Tensors are contiguous and row-major (the layer norm and the gated
+ *     linear recurrence also take strided inputs, see there).  Pointers to bf16 data must be
  *     2-byte aligned and pointers to fp32 data 4-byte aligned; the tensor-core
  *     forward path additionally wants 16-byte aligned q, k, v, o (it falls
  *     back to the CUDA-core path otherwise, see kla_chunk_fwd_ex).

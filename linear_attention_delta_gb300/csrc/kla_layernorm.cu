@@ -14,10 +14,17 @@
 // A row is the work of a group of threads, a warp to a block, which read it
 // once.  Where there are many rows, a group walks through some of them, with
 // the copies of its next rows into shared memory on their way meanwhile (a
-// ring of rows per group): with loads into registers alone, as many as fit,
-// the 2048-wide layer's forward took 48 and its backward 92 us.  Where there
-// are few, a block per row loads it straight into registers.  Rows wider than
-// a block can hold take the loop kernels at the end, which read them again.
+// ring of rows per group).  Where there are few, a block per row loads it
+// straight into registers.  Rows wider than a block can hold take the loop
+// kernels at the end, which read them again.
+//
+// Measured on 16384 x 2048 bf16: forward with a residual 50 us (268 MB, 80 %
+// of the copy bandwidth), without 27 us (73 %); backward with the residual's
+// gradient 52 us (268 MB, 76 %), without 47 us.  (With the next row in
+// registers instead of rings: 92 us for the backward.)  What bounds them is
+// issue and the latency of the sums across threads: 16 instructions per
+// element forward (20 with a residual) and 24 backward, at 55 to 60 % of the
+// issue slots; fp32, with half the elements per byte, reaches 85 and 81 %.
 #include <algorithm>
 #include <atomic>
 
@@ -868,8 +875,12 @@ cudaError_t fwd_width(const LayerNormArgs& a, cudaStream_t s) {
     constexpr bool WIDE = V > 1;
     constexpr int M = WIDE ? 1 : 4;              // runs are 1 element then
     const int packs = (a.D + V - 1) / V;
-    // a few rows for each group of threads that the GPU holds
-    if ((long long)a.rows * packs >= 152 * 1024 * 4 * M) {
+    // Rings pay where a group gets more than a row or so.  Measured (ring /
+    // rows, us): bf16 4096 x 512 4.0 / 3.7, 8192 x 512 5.0 / 5.9; 512 x 2048
+    // 3.6 / 3.1, 1024 x 2048 4.1 / 4.5, 16384 x 2048 25 / 46; 64 x 8192 3.6 /
+    // 3.7, 256 x 8192 4.7 / 6.2; fp32 256 x 2048 2.9 / 2.8, 512 x 2048 3.5 /
+    // 3.7; 256 x 1001 2.6 / 3.8, 16384 x 1001 26 / 139.
+    if ((long long)a.rows * packs >= 196608) {
         if (packs <= 32 * M) return fwd_ring<T, WIDE, 32, M>(a, s);
         if (packs <= 64 * M) return fwd_ring<T, WIDE, 32, 2 * M>(a, s);
         if (packs <= 128 * M) return fwd_ring<T, WIDE, 64, 2 * M>(a, s);
