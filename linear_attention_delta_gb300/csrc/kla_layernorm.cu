@@ -324,7 +324,10 @@ struct Part {
     // that lie inside for all threads need no test.
     __device__ static int column(int i, int t) { return (i * TPR + t) * V; }
     __device__ static bool inside(int i, int t, int D) {
-        return (i + 1) * TPR * V <= D || column(i, t) < D;
+        // the launch takes the narrowest kernel, so that the first half of
+        // the runs lies inside; not so in the narrowest of all
+        constexpr int sure = N == 1 || (V == 1 && N == 4) ? 0 : N / 2;
+        return i < sure || (i + 1) * TPR * V <= D || column(i, t) < D;
     }
     // f(pair index, both elements in the row, the first, run) for all pairs
     // of which some element is in the row.
@@ -767,18 +770,20 @@ __global__ void ln_bwd_cols_kernel(LayerNormBwdArgs a, float* part) {
 }
 
 // dw, db = the partial sums added up in a fixed order: a block takes 32
-// columns, a warp every 8th slice, then the warps are added up.
-__global__ void __launch_bounds__(256)
+// columns, a warp every 32nd slice (304 slices of 2048 columns: 1.5 us less
+// than with 8 warps), then the warps are added up.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
 ln_bwd_join_kernel(const float* part, int slices, int D, void* dw, void* db,
                    int wdtype) {
-    __shared__ float2 red[8][32];
+    __shared__ float2 red[kJoinWarps][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int col = blockIdx.x * 32 + lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float w = 0.f, b = 0.f;
     if (col < D) {
 #pragma unroll 4
-        for (int i = warp; i < slices; i += 8) {
+        for (int i = warp; i < slices; i += kJoinWarps) {
             w += part[(size_t)i * 2 * D + col];
             b += part[((size_t)i * 2 + 1) * D + col];
         }
@@ -786,7 +791,7 @@ ln_bwd_join_kernel(const float* part, int slices, int D, void* dw, void* db,
     red[warp][lane] = make_float2(w, b);
     __syncthreads();
     if (warp != 0 || col >= D) return;
-    for (int u = 1; u < 8; ++u) {
+    for (int u = 1; u < kJoinWarps; ++u) {
         w += red[u][lane].x;
         b += red[u][lane].y;
     }
@@ -887,7 +892,10 @@ cudaError_t fwd_width(const LayerNormArgs& a, cudaStream_t s) {
         if (packs <= 256 * M) return fwd_ring<T, WIDE, 128, 2 * M>(a, s);
         if (packs <= 512 * M) return fwd_ring<T, WIDE, 256, 2 * M>(a, s);
         if (packs <= 1024 * M) return fwd_ring<T, WIDE, 512, 2 * M>(a, s);
-        if (WIDE && packs <= 2048) return fwd_ring<T, WIDE, 1024, 2 * M>(a, s);
+        // (1024 threads leave 64 registers: 8192 x 8200 94 instead of 62 us,
+        // 2048 x 16384 34 instead of 26)
+        if (WIDE && packs <= 1280) return fwd_ring<T, WIDE, 640, 2>(a, s);
+        if (WIDE && packs <= 2048) return fwd_ring<T, WIDE, 512, 4>(a, s);
     }
     if (packs <= 32) return fwd_rows<T, V, 32, 1>(a, s);
     if (packs <= 64) return fwd_rows<T, V, 32, 2>(a, s);
@@ -918,7 +926,7 @@ cudaError_t join(const LayerNormBwdArgs& a, const float* part, int slices,
                  cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.D + 31) / 32);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -939,7 +947,12 @@ cudaError_t bwd_ring(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
         TPR * GROUPS, GROUPS, WIDE, a.dsum ? 3 : 2, sizeof(T), a.D, a.rows,
         TPR * N * kV<T, WIDE> * (int)sizeof(float2));
     if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
-    p.blocks = std::min(p.blocks, kMaxSlices);
+    // every block's partial sums are written and read again: blocks beyond
+    // 128 have 4 rows a group at least (1024 x 2048 8.9 -> 7.9 us, 256 x 2048
+    // and 4096 x 2048 the same)
+    p.blocks = std::min({p.blocks, kMaxSlices,
+                         std::max(128, (int)(((long long)a.rows + 4 * GROUPS -
+                                              1) / (4 * GROUPS)))});
     kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth,
                                                    grads ? part : nullptr);
     const cudaError_t e = cudaGetLastError();
