@@ -237,11 +237,25 @@ __device__ __forceinline__ void copy_rows(T* dst, const T* src,
     uintptr_t row = reinterpret_cast<uintptr_t>(src + (t + r0) * stride);
     unsigned int to = tc::smem_u32(dst) + (r0 * P + p0) * 16;
     const long long by = R * stride * (long long)sizeof(T);
+    if (first == 0 && last == ROWS && room >= CH) {      // most tiles: whole
+        uintptr_t from = row + p0 * 16;
 #pragma unroll
-    for (int r = 0; r < ROWS / R * R; r += R) {
-        piece(r0 + r, p0, row, to);
-        row += by;
-        to += R * P * 16;
+        for (int r = 0; r < ROWS / R * R; r += R) {
+            asm volatile(
+                "cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+                "l"(from & ~(uintptr_t)15)
+                : "memory");
+            from += by;
+            to += R * P * 16;
+        }
+        row += by * (ROWS / R);
+    } else {
+#pragma unroll
+        for (int r = 0; r < ROWS / R * R; r += R) {
+            piece(r0 + r, p0, row, to);
+            row += by;
+            to += R * P * 16;
+        }
     }
     if (ROWS % R && r0 < ROWS % R) piece(r0 + ROWS / R * R, p0, row, to);
     if (threadIdx.x < ROWS)
