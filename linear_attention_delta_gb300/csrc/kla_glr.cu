@@ -154,11 +154,29 @@ __device__ __forceinline__ void cluster_sync() {
 
 // How the inputs' rows line up: on 16 bytes, so that whole tiles can be
 // copied (TMA); on pairs of channels; on elements only.  In the last two
-// cases a row is copied with the 16-byte pieces that it touches and keeps its
-// place within the first of them.
+// cases a row is copied with the 16-byte pieces that it touches, and rows lie
+// in shared memory as far apart, modulo 16 bytes, as in global memory, so
+// that pieces meet pieces (kPitch: elements between them at most).
 enum Align { kWide, kPair, kElement };
 template <Align A, typename T>
-constexpr int kPitch = CH + (A == kWide ? 0 : 16 / (int)sizeof(T));
+constexpr int kPitch = CH + (A == kWide ? 0 : 32 / (int)sizeof(T));
+
+// Where the rows of a tile lie: element 0 of row r at first + r * pitch.
+template <Align A, typename T>
+struct Rows {
+    int first, pitch;
+    __device__ Rows(const T* src, long long stride, long long t) {
+        if (A == kWide) {
+            first = 0;
+            pitch = CH;
+        } else {
+            first = (int)((reinterpret_cast<uintptr_t>(src + t * stride)) &
+                          15) / (int)sizeof(T);
+            pitch = CH + (16 + (int)(stride * (long long)sizeof(T) & 15)) /
+                             (int)sizeof(T);
+        }
+    }
+};
 
 // The two channels of a lane: adjacent where pairs are aligned, else 32
 // apart, so that a warp's single elements are adjacent.
@@ -208,73 +226,64 @@ __device__ __forceinline__ void write2(T* row, bool l0, bool l1, float2 c) {
     }
 }
 
-// Copies rows t .. t + ROWS - 1 (`stride` elements apart) of `room`
-// channels into dst [ROWS][kPitch]; what lies outside the rows 0 .. n - 1 or
-// the channels becomes zero.  A piece of 16 aligned bytes is read from its
-// start to the row's end only; the bytes that it may hold before the row
-// belong to the same allocation, which starts on 16 bytes.
+// Copies rows t .. t + ROWS - 1 (`stride` elements apart) of `room` channels
+// to their places (`Rows`) in dst; rows outside 0 .. n - 1 become zero.  A
+// piece of 16 aligned bytes is read from its start to the row's end only; the
+// bytes that it may hold before the row belong to the same allocation, which
+// starts on 16 bytes.
 template <Align A, int ROWS, typename T>
 __device__ __forceinline__ void copy_rows(T* dst, const T* src,
                                           long long stride, long long t,
                                           int n, int room) {
-    constexpr int P = kPitch<A, T> * sizeof(T) / 16;   // pieces of a row
+    constexpr int P = CH * sizeof(T) / 16 + 1;         // pieces of a row
+    constexpr int R = kThreads / (P - 1);              // rows at a time
     static_assert(kThreads % (P - 1) == 0 && kThreads >= ROWS, "");
     const uintptr_t none =
         reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15;
     const int bytes = min(room, CH) * (int)sizeof(T);
     const int first = (int)max(0ll, -t), last = (int)min((long long)ROWS, n - t);
-    auto piece = [&](int r, int p, uintptr_t row, unsigned int to) {
+    const Rows<A, T> place(src, stride, t);
+    const int pitch = place.pitch * (int)sizeof(T);
+    const unsigned int base = tc::smem_u32(dst);
+    auto piece = [&](int r, int p, uintptr_t row, int at) {
         const int left = (int)(row & 15) + bytes - p * 16;
         const bool in = r >= first && r < last && left > 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         base + (at & ~15) + p * 16),
                      "l"(in ? (row & ~(uintptr_t)15) + p * 16 : none),
                      "r"(in ? min(left, 16) : 0)
                      : "memory");
     };
     // all pieces but the last: a thread keeps its place in the row
-    constexpr int R = kThreads / (P - 1);
     const int r0 = threadIdx.x / (P - 1), p0 = threadIdx.x % (P - 1);
     uintptr_t row = reinterpret_cast<uintptr_t>(src + (t + r0) * stride);
-    unsigned int to = tc::smem_u32(dst) + (r0 * P + p0) * 16;
+    int at = place.first * (int)sizeof(T) + r0 * pitch;
     const long long by = R * stride * (long long)sizeof(T);
     if (first == 0 && last == ROWS && room >= CH) {      // most tiles: whole
-        uintptr_t from = row + p0 * 16;
 #pragma unroll
         for (int r = 0; r < ROWS / R * R; r += R) {
             asm volatile(
-                "cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
-                "l"(from & ~(uintptr_t)15)
+                "cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                    base + (at & ~15) + p0 * 16),
+                "l"((row & ~(uintptr_t)15) + p0 * 16)
                 : "memory");
-            from += by;
-            to += R * P * 16;
-        }
-        row += by * (ROWS / R);
-    } else {
-#pragma unroll
-        for (int r = 0; r < ROWS / R * R; r += R) {
-            piece(r0 + r, p0, row, to);
             row += by;
-            to += R * P * 16;
+            at += R * pitch;
+        }
+    } else {
+#pragma unroll 1
+        for (int r = 0; r < ROWS / R * R; r += R) {
+            piece(r0 + r, p0, row, at);
+            row += by;
+            at += R * pitch;
         }
     }
-    if (ROWS % R && r0 < ROWS % R) piece(r0 + ROWS / R * R, p0, row, to);
+    if (ROWS % R && r0 < ROWS % R) piece(r0 + ROWS / R * R, p0, row, at);
     if (threadIdx.x < ROWS)
         piece(threadIdx.x, P - 1,
               reinterpret_cast<uintptr_t>(src + (t + threadIdx.x) * stride),
-              tc::smem_u32(dst) + (threadIdx.x * P + P - 1) * 16);
+              place.first * (int)sizeof(T) + (int)threadIdx.x * pitch);
 }
-// Where a row starts within its first piece (elements): of row t, and how
-// that moves from row to row.
-template <typename T>
-struct Shift {
-    unsigned int at, by;
-    __device__ Shift(const T* src, long long stride, long long t)
-        : at((unsigned int)reinterpret_cast<uintptr_t>(src + t * stride)),
-          by((unsigned int)(stride * (long long)sizeof(T))) {}
-    __device__ int operator()(int rows) const {
-        return ((at + rows * by) & 15) / sizeof(T);
-    }
-};
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
                                             uint64_t* bar, int c0, int c1,
@@ -540,25 +549,26 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         float2 al[S];                // decays
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
         float2 P = both(1.f), H = both(0.f);
-        // rows that do not line up on 16 bytes: where each starts
+        // where the rows of this warp lie (backwards: from its last)
         const int lo = BWD ? a.T - TILE - here.k * TILE : here.k * TILE;
-        const Shift<G> sl(static_cast<const G*>(a.la.p) + b * a.la.sb +
-                              here.d, a.la.st, lo);
-        const Shift<T> sx(static_cast<const T*>(a.x.p) + b * a.x.sb + here.d,
-                          a.x.st, BWD ? lo - 1ll : lo);
-        const Shift<T> sg(static_cast<const T*>(a.g.p) + b * a.g.sb + here.d,
-                          a.g.st, lo);
+        const Rows<A, G> rl(static_cast<const G*>(a.la.p) + b * a.la.sb +
+                                here.d, a.la.st, lo);
+        const Rows<A, T> rx(static_cast<const T*>(a.x.p) + b * a.x.sb +
+                                here.d, a.x.st, BWD ? lo - 1ll : lo);
+        const Rows<A, T> rg(static_cast<const T*>(a.g.p) + b * a.g.sb +
+                                here.d, a.g.st, lo);
+        const int r0 = BWD ? TILE - 1 - w * S : w * S;
+        const G* at_l = &st.la[0][0] + rl.first + r0 * rl.pitch;
+        const T* at_x = &st.x[0][0] + rx.first + r0 * rx.pitch;
+        const T* at_g = nullptr;
+        if constexpr (BWD) at_g = &st.g[0][0] + rg.first + r0 * rg.pitch;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const int r = BWD ? TILE - 1 - (w * S + i) : w * S + i;
-            const int ol = A == kWide ? 0 : sl(r);
-            const int ox = A == kWide ? 0 : sx(r);
-            al[i] = decay(values(read2<A>(st.la[r] + ol, lane)));
-            x[i] = read2<A>(st.x[r] + ox, lane);
+            al[i] = decay(values(read2<A>(at_l + DT * i * rl.pitch, lane)));
+            x[i] = read2<A>(at_x + DT * i * rx.pitch, lane);
             P = mul2(P, al[i]);
             if constexpr (BWD) {
-                const int og = A == kWide ? 0 : sg(r);
-                g[i] = read2<A>(st.g[r] + og, lane);
+                g[i] = read2<A>(at_g + DT * i * rg.pitch, lane);
                 H = mul2(al[i], add2(H, values(g[i])));
             } else {
                 H = fma2(al[i], H, values(x[i]));
