@@ -782,7 +782,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
 }
 
 // ---------------------------------------------------------------------------
-// One token: each state is read and written once.  A thread takes 4 channels
+// One token, as a programmatic dependent of the kernel before it: each state
+// is read and written once.  A thread takes 4 channels
 // of a sequence, adjacent ones (V = 4) or, where they do not line up, single
 // ones 128 apart (V = 1), so that their loads are on their way together.
 template <typename T, typename G, int V>
@@ -794,6 +795,8 @@ glr_step_kernel(const T* x, long long xs, const G* la, long long ls,
     struct alignas(4 * V) PS { float v[V]; };
     constexpr int U = 4 / V;
     const int d0 = blockIdx.x * 512 + threadIdx.x * V;
+    await_grid_before();
+    release_grid_after();
     for (long long n = blockIdx.y; n < N; n += gridDim.y) {
         const size_t i = (size_t)n * D;
         PT px[U];
@@ -1020,11 +1023,11 @@ cudaError_t launch_glr_step(const void* x, long long x_stride,
                           aligned(la, 4 * sizeof(G)) && aligned(S, 16) &&
                           aligned(o, 4 * sizeof(T));
         const dim3 grid((D + 511) / 512, std::min(N, 65535));
-        (four ? glr_step_kernel<T, G, 4>
-              : glr_step_kernel<T, G, 1>)<<<grid, 128, 0, stream>>>(
-            static_cast<const T*>(x), x_stride, static_cast<const G*>(la),
-            la_stride, S, static_cast<T*>(o), N, D);
-        return cudaGetLastError();
+        return launch_dependent(
+            four ? glr_step_kernel<T, G, 4> : glr_step_kernel<T, G, 1>, grid,
+            128, stream, static_cast<const T*>(x), x_stride,
+            static_cast<const G*>(la), la_stride, S, static_cast<T*>(o), N,
+            D);
     });
 }
 

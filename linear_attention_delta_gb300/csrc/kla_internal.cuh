@@ -25,6 +25,31 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(
     return __float2bfloat16_rn(x);
 }
 
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// the grid may be scheduled while that one drains.  The kernel has to call
+// await_grid_before() before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads,
+                             cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void await_grid_before() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next kernel's grid be scheduled (it waits for this one's memory).
+__device__ __forceinline__ void release_grid_after() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct FwdArgs {
     const void* q;
     const void* k;

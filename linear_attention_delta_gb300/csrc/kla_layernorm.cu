@@ -116,7 +116,8 @@ __device__ __forceinline__ float2 group_sum(float2 a, float2* red, int bar) {
     }
 }
 
-// Forward, the row in registers: TPR threads per row, N packs of V elements
+// Forward, the row in registers (as a programmatic dependent of the kernel
+// before it): TPR threads per row, N packs of V elements
 // each; a block of max(TPR, 128) threads.
 template <typename T, int V, int TPR, int N>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
@@ -126,6 +127,8 @@ ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
     __shared__ float red[2][ROWS * TPR / 32];
     const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * ROWS + sub;
+    await_grid_before();
+    release_grid_after();
     if (row >= a.rows) return;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* r = a.residual
@@ -779,7 +782,7 @@ ln_bwd_join_kernel(const float* part, int slices, int D, void* dw, void* db,
     __shared__ float2 red[kJoinWarps][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int col = blockIdx.x * 32 + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    await_grid_before();
     float w = 0.f, b = 0.f;
     if (col < D) {
 #pragma unroll 4
@@ -858,8 +861,8 @@ template <typename T, int V, int TPR, int N>
 cudaError_t fwd_rows(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int threads = TPR < 128 ? 128 : TPR, rows = threads / TPR;
     const long long blocks = ((long long)a.rows + rows - 1) / rows;
-    ln_fwd_kernel<T, V, TPR, N><<<(unsigned)blocks, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(ln_fwd_kernel<T, V, TPR, N>,
+                            dim3((unsigned)blocks), threads, s, a);
 }
 
 template <typename T, bool WIDE, int TPR, int N>
@@ -924,17 +927,9 @@ cudaError_t launch_fwd(const LayerNormArgs& a, cudaStream_t s) {
 
 cudaError_t join(const LayerNormBwdArgs& a, const float* part, int slices,
                  cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.D + 31) / 32);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ln_bwd_join_kernel, part, slices, a.D,
-                              a.dw, a.db, (int)a.wdtype);
+    return launch_dependent(ln_bwd_join_kernel, dim3((a.D + 31) / 32),
+                            32 * kJoinWarps, s, part, slices, a.D, a.dw, a.db,
+                            (int)a.wdtype);
 }
 
 template <typename T, bool WIDE, int TPR, int N, bool HOLD = true>
