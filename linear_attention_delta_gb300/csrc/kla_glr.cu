@@ -421,6 +421,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             tc::mbar_init(bar, 1);
         tc::fence_mbar_init();
     }
+    await_grid_before();
+    release_grid_after();
     const int* cu = a.cu;
     if (a.cu && a.B < kMaxKept) {
         for (int i = threadIdx.x; i <= a.B; i += kThreads) sh.cu[i] = a.cu[i];
@@ -845,11 +847,13 @@ void team_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = shared_bytes<T, G, A, BWD>(team);
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = team;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = team;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
 }
 
 // Blocks in teams of `team` that the current GPU holds at the same time (looked
@@ -863,7 +867,7 @@ int capacity(int team) {
     if (n > 0) return n;
     auto* kernel = glr_scan_kernel<T, G, A, BWD>;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     team_config<T, G, A, BWD>(cfg, attr, team, team);
     if (cudaFuncSetAttribute(kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -944,7 +948,7 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
          (BWD && !make_tile_map<T>(&mg, a.g, a, TILE))))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     team_config<T, G, A, BWD>(cfg, attr, blocks, p.team);
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kernel, a, p, mx, ml, mg);
@@ -1025,7 +1029,7 @@ cudaError_t launch_glr_step(const void* x, long long x_stride,
         const dim3 grid((D + 511) / 512, std::min(N, 65535));
         return launch_dependent(
             four ? glr_step_kernel<T, G, 4> : glr_step_kernel<T, G, 1>, grid,
-            128, stream, static_cast<const T*>(x), x_stride,
+            128, stream, 0, static_cast<const T*>(x), x_stride,
             static_cast<const G*>(la), la_stride, S, static_cast<T*>(o), N,
             D);
     });

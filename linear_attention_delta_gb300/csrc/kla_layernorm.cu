@@ -431,13 +431,15 @@ struct Part {
     }
 };
 
-// Sets up the ring of this thread's group; true once its first rows are on
-// their way.
+// Waits for the grid before this one and starts the first rows of this
+// thread's group on their way.
 template <bool WIDE, typename T, int TPR, int GROUPS, int IN>
 __device__ __forceinline__ void open_ring(Ring<WIDE, T, TPR, IN>& ring,
                                           unsigned char* smem, uint64_t* full,
                                           int* dead, long long rows, int D, int depth) {
     const int g = threadIdx.x / TPR;
+    await_grid_before();
+    release_grid_after();
     if (threadIdx.x < 2 * GROUPS) dead[threadIdx.x] = 0;
     ring.t = threadIdx.x % TPR;
     ring.bar = 1 + g;
@@ -862,7 +864,7 @@ cudaError_t fwd_rows(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int threads = TPR < 128 ? 128 : TPR, rows = threads / TPR;
     const long long blocks = ((long long)a.rows + rows - 1) / rows;
     return launch_dependent(ln_fwd_kernel<T, V, TPR, N>,
-                            dim3((unsigned)blocks), threads, s, a);
+                            dim3((unsigned)blocks), threads, s, 0, a);
 }
 
 template <typename T, bool WIDE, int TPR, int N>
@@ -874,8 +876,8 @@ cudaError_t fwd_ring(const LayerNormArgs& a, cudaStream_t s) {
                                          a.residual ? 2 : 1, sizeof(T), a.D,
                                          a.rows, 0);
     if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
-    kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(p.blocks), TPR * GROUPS, s, p.bytes, a,
+                            p.depth);
 }
 
 template <typename T, int V>
@@ -928,7 +930,7 @@ cudaError_t launch_fwd(const LayerNormArgs& a, cudaStream_t s) {
 cudaError_t join(const LayerNormBwdArgs& a, const float* part, int slices,
                  cudaStream_t s) {
     return launch_dependent(ln_bwd_join_kernel, dim3((a.D + 31) / 32),
-                            32 * kJoinWarps, s, part, slices, a.D, a.dw, a.db,
+                            32 * kJoinWarps, s, 0, part, slices, a.D, a.dw, a.db,
                             (int)a.wdtype);
 }
 
@@ -948,9 +950,9 @@ cudaError_t bwd_ring(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
     p.blocks = std::min({p.blocks, kMaxSlices,
                          std::max(128, (int)(((long long)a.rows + 4 * GROUPS -
                                               1) / (4 * GROUPS)))});
-    kernel<<<p.blocks, TPR * GROUPS, p.bytes, s>>>(a, p.depth,
-                                                   grads ? part : nullptr);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(kernel, dim3(p.blocks), TPR * GROUPS, s, p.bytes, a,
+                         p.depth, grads ? part : nullptr);
     return e != cudaSuccess || !grads ? e : join(a, part, p.blocks, s);
 }
 
