@@ -7,12 +7,17 @@
 // to five operations per element of each tensor it reads.
 //
 // Measured (us, share of the copy bandwidth; bf16 with fp32 gates): 4 x 4096
-// x 2048 forward 47 (85 %), backward 78 (89 %); 65536 x 2048, bf16 gates,
-// forward 144 (83 %), where a step of a team of 12 blocks takes 2.5 us: 1.2 of
+// x 2048 forward 45 (89 %), backward 76 (91 %); 65536 x 2048, bf16 gates,
+// forward 141 (85 %), where a step of a team of 12 blocks takes 2.5 us: 1.2 of
 // work on its tile, the rest waiting for the slowest block's map and for the
-// next tile; 16411 x 1024 packed forward 36 (42 %): 16 chains fill 256 of the
-// 456 blocks that the GPU holds; 8191 x 1001 packed backward in fp32 50 (48
-// %): rows that line up on 4 bytes only, copied in pieces by all threads.
+// next tile; 16411 x 1024 packed forward 34 (44 %): 16 chains fill 256 of the
+// 456 blocks that the GPU holds; 8191 x 1001 packed backward in fp32 46 (53
+// %): rows that line up on 4 bytes only, copied in pieces by all threads
+// (4 x 4096 x 2047 bf16 forward 57 against 40 us for 2048 channels).
+//
+// The kernels launch as programmatic dependents: their blocks take their
+// places while the kernel before them on the stream drains, and wait for its
+// end before they touch memory.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

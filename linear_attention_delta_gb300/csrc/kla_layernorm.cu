@@ -18,13 +18,17 @@
 // straight into registers.  Rows wider than a block can hold take the loop
 // kernels at the end, which read them again.
 //
-// Measured on 16384 x 2048 bf16: forward with a residual 50 us (268 MB, 80 %
-// of the copy bandwidth), without 27 us (73 %); backward with the residual's
-// gradient 52 us (268 MB, 76 %), without 47 us.  (With the next row in
-// registers instead of rings: 92 us for the backward.)  What bounds them is
-// issue and the latency of the sums across threads: 16 instructions per
+// Measured on 16384 x 2048 bf16: forward with a residual 46 us (268 MB, 86 %
+// of the copy bandwidth), without 24 us (84 %); backward with the residual's
+// gradient 47.5 us (268 MB, 84 %), without 41 us (74 %).  (With the next row
+// in registers instead of rings: 92 us for the backward.)  What bounds them
+// is issue and the latency of the sums across threads: 16 instructions per
 // element forward (20 with a residual) and 24 backward, at 55 to 60 % of the
-// issue slots; fp32, with half the elements per byte, reaches 85 and 81 %.
+// issue slots; fp32, with half the elements per byte, reaches 89 and 90 %.
+//
+// All kernels launch as programmatic dependents: their blocks take their
+// places while the kernel before them on the stream drains, and wait for its
+// end before they touch memory (3 us of the 49 that the forward took).
 #include <algorithm>
 #include <atomic>
 
