@@ -727,6 +727,16 @@ KLA_API kla_status kla_device_status(kla_stream_t stream);
  */
 KLA_API kla_status kla_selftest_wait_timeout(kla_stream_t stream);
 
+/*
+ * kla_selftest_glr_timeout -- the same for the gated linear recurrence:
+ * launches one block of its scan on `stream` that sends no map and waits 1 ms
+ * for one (on memory of the library's own).  The wait runs out, the block
+ * leaves and sets the fault word, so that the next kla_device_status on
+ * `stream` returns KLA_ERR_TIMEOUT (and the one after that KLA_OK).
+ * Errors: KLA_ERR_CUDA.
+ */
+KLA_API kla_status kla_selftest_glr_timeout(kla_stream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 KLA_API const char* kla_status_string(kla_status status);
 

@@ -81,9 +81,12 @@ struct ScanPlan {
     int tiles, groups;           // tiles of a chain; channel groups
     int rounds;                  // chains that each block walks alone, then
     int rest, team;              // `rest` chains walked by a team each
+    unsigned int wait_ns;        // how long a block waits for maps at most
+    bool mute;                   // send none (the self-test of that wait)
 };
 
 __device__ unsigned int g_fault_glr = 0;
+__device__ float g_selftest_glr[3 * CH];         // the self-test's tensors
 
 // exp of two log decays.  Near 0, where a state remembers 1 / -l tokens and
 // a decay's error is multiplied by as much, 1 + l + l^2 / 2 + l^3 / 6 (|l| <=
@@ -132,8 +135,9 @@ __device__ __forceinline__ void send(float4* to, uint64_t* bar, int rank,
         "r"(__float_as_uint(m.w))
         : "memory");
 }
-// Waits (2 s at most) until the maps of a step have arrived.
-__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
+// Waits, `limit` ns at most, until the maps of a step have arrived.
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity,
+                                          uint64_t limit) {
     uint64_t begun = 0;
     while (true) {
         uint32_t ok;
@@ -147,7 +151,7 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
         if (ok) return true;
         const uint64_t now = tc::globaltimer_ns();
         if (begun == 0) begun = now;
-        if (now - begun > 2000000000ull) return false;
+        if (now - begun > limit) return false;
     }
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -312,9 +316,9 @@ struct Bounds {
 };
 
 // Packed sequences: the boundaries among the S tokens from t on (upwards, or
-// downwards with BACK), of which `steps` are there.  A warp works together: a 32-way search for the
-// sequence of t, then 32 offsets at a time.  Any content of cu gives
-// 0 <= n, last < B.
+// downwards with BACK), of which `steps` are there.  A warp works together: a
+// 32-way search for the sequence of t, then 32 offsets at a time.  Any content
+// of cu gives 0 <= n, last < B.
 template <int S, bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
                                               long long t, int steps) {
@@ -401,10 +405,12 @@ struct Shared {
     uint64_t full, got[2];       // the tile is there; the step's maps are
 };
 
+// Shared memory of a block of a team.
 template <typename T, typename G, Align A, bool BWD>
 constexpr int shared_bytes(int team) {
     return (int)sizeof(Shared<T, G, A, BWD>) + 2 * team * 512;
 }
+
 template <typename T, typename G, Align A, bool BWD>
 __global__ void __launch_bounds__(kThreads, kResident<T>)
 glr_scan_kernel(const __grid_constant__ GlrArgs a,
@@ -453,17 +459,19 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     tma_load_3d(&st.g[0][0], &map_g, &sh.full, d, lo, b);
             } else {
                 const int room = a.D - d;
-                copy_rows<A, TILE>(&st.la[0][0],
-                             static_cast<const G*>(a.la.p) + b * a.la.sb + d,
-                             a.la.st, lo, a.T, room);
-                copy_rows<A, TILE>(&st.x[0][0],
-                             static_cast<const T*>(a.x.p) + b * a.x.sb + d,
-                             a.x.st, BWD ? lo - 1ll : lo, a.T, room);
+                copy_rows<A, TILE>(
+                    &st.la[0][0],
+                    static_cast<const G*>(a.la.p) + b * a.la.sb + d, a.la.st,
+                    lo, a.T, room);
+                copy_rows<A, TILE>(
+                    &st.x[0][0],
+                    static_cast<const T*>(a.x.p) + b * a.x.sb + d, a.x.st,
+                    BWD ? lo - 1ll : lo, a.T, room);
                 if constexpr (BWD)
-                    copy_rows<A, TILE>(&st.g[0][0],
-                                 static_cast<const T*>(a.g.p) + b * a.g.sb +
-                                     d,
-                                 a.g.st, lo, a.T, room);
+                    copy_rows<A, TILE>(
+                        &st.g[0][0],
+                        static_cast<const T*>(a.g.p) + b * a.g.sb + d,
+                        a.g.st, lo, a.T, room);
             }
         }
         if (A != kWide) asm volatile("cp.async.commit_group;" ::: "memory");
@@ -632,14 +640,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             // a block that walks alone is its own team of one
             const int first = here.step > 1 ? 0 : blockIdx.x % plan.team;
 #pragma unroll 4
-            for (int r = 0; r < there; ++r)
+            for (int r = 0; r < there && !plan.mute; ++r)
                 send(&team[m][lane], &sh.got[h], first + r, t);
         }
         // meanwhile
         if (A != kWide) fetch(then);
         look(then);
         if (w == 0) {                // the state before the tile, and after
-            fault |= !wait_maps(&sh.got[h], turn >> 1 & 1);
+            fault |= !wait_maps(&sh.got[h], turn >> 1 & 1, plan.wait_ns);
             if (anew) {
 #pragma unroll 4
                 for (int j = 0; j < m; ++j)
@@ -790,9 +798,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
 
 // ---------------------------------------------------------------------------
 // One token, as a programmatic dependent of the kernel before it: each state
-// is read and written once.  A thread takes 4 channels
-// of a sequence, adjacent ones (V = 4) or, where they do not line up, single
-// ones 128 apart (V = 1), so that their loads are on their way together.
+// is read and written once.  A thread takes 4 channels of a sequence, adjacent
+// ones (V = 4) or, where they do not line up, single ones 128 apart (V = 1),
+// so that their loads are on their way together (1024 x 8191: 17 us, with one
+// channel a thread 44; 256 x 2048: 1.6 us in a graph).
 template <typename T, typename G, int V>
 __global__ void __launch_bounds__(128)
 glr_step_kernel(const T* x, long long xs, const G* la, long long ls,
@@ -842,10 +851,6 @@ cudaError_t by_type(kla_dtype t, kla_dtype g, F f) {
     return g == KLA_BF16 ? f(float(), bf16()) : f(float(), float());
 }
 
-}  // namespace
-
-namespace {
-
 template <typename T, typename G, Align A, bool BWD>
 void team_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
                  int blocks, int team) {
@@ -893,7 +898,7 @@ int capacity(int team) {
 // counts as 1, a team of t as 1 / t.
 template <typename T, typename G, Align A, bool BWD>
 ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
-    ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1};
+    ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1, 2000000000u, false};
     *blocks = 0;
     double cost = 0;
     for (int team = 1; team <= std::min(kMaxTeam, tiles); ++team) {
@@ -1007,6 +1012,30 @@ cudaError_t launch_glr(const GlrArgs& a, bool bwd, cudaStream_t stream) {
                : pairs ? launch_way<T, G, kPair>(a, bwd, stream)
                        : launch_way<T, G, kElement>(a, bwd, stream);
     });
+}
+
+cudaError_t launch_glr_selftest(cudaStream_t stream) {
+    // one tile of one token and CH channels in memory of its own
+    void* p = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&p, g_selftest_glr);
+    if (e != cudaSuccess) return e;
+    float* m = static_cast<float*>(p);
+    GlrArgs a{};
+    a.x = {m, CH, CH};
+    a.la = {m + CH, CH, CH};
+    a.o = m + 2 * CH;
+    a.B = a.T = 1;
+    a.D = CH;
+    if (capacity<float, float, kPair, false>(1) <= 0)
+        return cudaErrorInvalidValue;
+    const ScanPlan plan{1, 1, 0, 1, 1, 1000000u, true};
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    team_config<float, float, kPair, false>(cfg, attr, 1, 1);
+    cfg.stream = stream;
+    const CUtensorMap none{};
+    return cudaLaunchKernelEx(&cfg, glr_scan_kernel<float, float, kPair, false>,
+                              a, plan, none, none, none);
 }
 
 cudaError_t read_and_clear_fault_glr(unsigned int* word) {

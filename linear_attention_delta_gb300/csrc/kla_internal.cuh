@@ -231,6 +231,9 @@ const unsigned int* chunk_tc2_ready(const void* ws, int B, int T, int H);
 int chunk_tc2_state_ctas(int B, int H);
 cudaError_t read_and_clear_fault2(unsigned int* word);
 cudaError_t read_and_clear_fault_glr(unsigned int* word);
+// One block of the scan that sends no map and waits 1 ms for one: its wait
+// runs out and it sets the fault word.
+cudaError_t launch_glr_selftest(cudaStream_t stream);
 cudaError_t read_and_clear_fault_ln(unsigned int* word);
 // One CTA of the state-pass kernel whose producer issues no copy and whose
 // waits give up after 1 ms: it takes the kernel's abort path and sets the

@@ -440,7 +440,8 @@ struct Part {
 template <bool WIDE, typename T, int TPR, int GROUPS, int IN>
 __device__ __forceinline__ void open_ring(Ring<WIDE, T, TPR, IN>& ring,
                                           unsigned char* smem, uint64_t* full,
-                                          int* dead, long long rows, int D, int depth) {
+                                          int* dead, long long rows, int D,
+                                          int depth) {
     const int g = threadIdx.x / TPR;
     await_grid_before();
     release_grid_after();

@@ -165,9 +165,9 @@ extern "C" kla_status kla_glr_fwd(
     long long a_sb, long long a_st, const float* h0, void* o, float* hT,
     const int* cu_seqlens, int B, int T, int D, kla_dtype dtype,
     kla_dtype gate_dtype, kla_stream_t stream) {
-    const kla::GlrArgs a{{x, x_sb, x_st}, {log_alpha, a_sb, a_st}, {nullptr, 0, 0},
-                   h0, nullptr, o, nullptr, hT, cu_seqlens, B, T, D, dtype,
-                   gate_dtype};
+    const kla::GlrArgs a{{x, x_sb, x_st}, {log_alpha, a_sb, a_st},
+                         {nullptr, 0, 0}, h0, nullptr, o, nullptr, hT,
+                         cu_seqlens, B, T, D, dtype, gate_dtype};
     return glr_impl(a, false, stream);
 }
 
@@ -178,8 +178,9 @@ extern "C" kla_status kla_glr_bwd(
     void* log_alpha_grad, float* h0_grad, const int* cu_seqlens, int B, int T,
     int D, kla_dtype dtype, kla_dtype gate_dtype, kla_stream_t stream) {
     const kla::GlrArgs a{{o, o_sb, o_st}, {log_alpha, a_sb, a_st},
-                   {o_grad, g_sb, g_st}, h0, hT_grad, x_grad, log_alpha_grad,
-                   h0_grad, cu_seqlens, B, T, D, dtype, gate_dtype};
+                         {o_grad, g_sb, g_st}, h0, hT_grad, x_grad,
+                         log_alpha_grad, h0_grad, cu_seqlens, B, T, D, dtype,
+                         gate_dtype};
     return glr_impl(a, true, stream);
 }
 
@@ -202,5 +203,10 @@ extern "C" kla_status kla_glr_step(const void* x, long long x_stride,
     if (any_overlap(ins, outs)) return KLA_ERR_INVALID_ARG;
     return from_cuda(kla::launch_glr_step(
         x, x_stride, log_alpha, a_stride, S, o, N, D, dtype, gate_dtype,
+        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" kla_status kla_selftest_glr_timeout(kla_stream_t stream) {
+    return from_cuda(kla::launch_glr_selftest(
         reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -91,6 +91,7 @@ SIGNATURES = {
                           _VP]),
     "kla_device_status": (_I, [_VP]),
     "kla_selftest_wait_timeout": (_I, [_VP]),
+    "kla_selftest_glr_timeout": (_I, [_VP]),
     "kla_status_string": (ctypes.c_char_p, [_I]),
 }
 
@@ -911,3 +912,9 @@ def selftest_wait_timeout(stream=None) -> int:
     """``kla_selftest_wait_timeout``: one kernel whose device-side waits give
     up after 1 ms (nothing arrives on them); returns the launch status."""
     return int(load_library().kla_selftest_wait_timeout(_stream(stream)))
+
+
+def selftest_glr_timeout(stream=None) -> int:
+    """``kla_selftest_glr_timeout``: one block of the recurrence's scan whose
+    wait gives up after 1 ms; returns the launch status."""
+    return int(load_library().kla_selftest_glr_timeout(_stream(stream)))

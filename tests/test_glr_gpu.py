@@ -361,6 +361,17 @@ def test_more_channels_than_blocks(B, T, D):
     check_bwd(o, la, x, h0, h0)
 
 
+def test_a_wait_that_runs_out_is_reported_then_cleared():
+    """A block whose team's maps never come gives up, reports it once, and the
+    context and the next calls are as before."""
+    assert kla.device_status() == 0
+    assert kla.selftest_glr_timeout() == 0
+    assert kla.device_status() == -4
+    assert kla.device_status() == 0
+    x, la = normal((1, 300, 64), F32, 60), gates((1, 300, 64), F32, 61)
+    check_fwd(x, la)
+
+
 def test_two_streams_at_once():
     """Calls that overlap on two streams, each with its own workspace."""
     x, la = normal((1, 30000, 256), BF16, 38), gates((1, 30000, 256), F32, 39)
