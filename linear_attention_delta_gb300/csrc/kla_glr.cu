@@ -10,16 +10,17 @@
 // x 2048 forward 45 (89 %), backward 76 (91 %); 65536 x 2048, bf16 gates,
 // forward 141 (85 %), where a step of a team of 12 blocks takes 2.5 us: 1.2 of
 // work on its tile, the rest waiting for the slowest block's map and for the
-// next tile; 16411 x 1024 packed forward 34 (44 %): 16 chains fill 256 of the
-// 456 blocks that the GPU holds; 8191 x 1001 packed backward in fp32 46 (53
-// %): rows that line up on 4 bytes only, copied in pieces by all threads
-// (4 x 4096 x 2047 bf16 forward 57 against 40 us for 2048 channels).
+// next tile; 16411 x 1024 in 24 packed sequences, forward 28 (54 %); 8191 x
+// 1001 in 9, backward in fp32 43 (57 %): rows that line up on 4 bytes only,
+// copied in pieces by all threads (4 x 4096 x 2047 bf16 forward 56 against 40
+// us for 2048 channels).
 //
 // The kernels launch as programmatic dependents: their blocks take their
 // places while the kernel before them on the stream drains, and wait for its
 // end before they touch memory.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -35,8 +36,8 @@ using bf16 = __nv_bfloat16;
 // The scan.  A tile is W * S consecutive tokens (in scan order:
 // backwards in the backward pass) of CH = 64 channels; warp w of its block
 // holds S of the tokens, a lane two of the channels.  All tiles of one run of
-// tokens (a batch entry, or all packed tokens) and one group of channels form
-// a chain.  A chain is walked by a team of G blocks, a thread-block cluster,
+// tokens (a batch entry, or a part of the packed tokens) and one group of
+// channels form a chain.  A chain is walked by a team of G blocks, a thread-block cluster,
 // which take every G-th tile each, in order; a block
 //   1. waits for its tile's inputs in shared memory, takes them into
 //      registers, and starts the copy of its next tile,
@@ -49,6 +50,10 @@ using bf16 = __nv_bfloat16;
 //      carries it by itself, so that no state is handed from block to block
 //      and a step costs one exchange, not G,
 //   5. runs its steps again from the now known state and writes the outputs.
+// Packed tokens are cut into parts of similar length between two sequences
+// where that lets more blocks work; every block looks its part up in the
+// offsets.
+//
 // Every input element is read from HBM once.  Maps are applied in token
 // order, so the result has the same bits on every run.
 //
@@ -81,6 +86,7 @@ struct ScanPlan {
     int tiles, groups;           // tiles of a chain; channel groups
     int rounds;                  // chains that each block walks alone, then
     int rest, team;              // `rest` chains walked by a team each
+    int parts;                   // of the packed tokens (1: no rounds else)
     unsigned int wait_ns;        // how long a block waits for maps at most
     bool mute;                   // send none (the self-test of that wait)
 };
@@ -356,12 +362,36 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
     return {mask, lo, min(max(last, 0), B - 1)};
 }
 
+// Packed sequences: the boundary that lies nearest to token t, but not 0.  A
+// warp works together; 1 to T, whatever cu holds, rising with t where cu does.
+__device__ __forceinline__ int nearest_bound(const int* cu, int B, int T,
+                                             int t) {
+    const int lane = threadIdx.x % 32;
+    int lo = 0, len = B;         // the last one up to t (cu[0] = 0 is)
+    while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int i = lane * step;
+        const bool le = i < len && cu[lo + i] <= t;
+        const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+        const int skip = (cnt - 1) * step;
+        lo += skip;
+        len = min(step, len - skip);
+    }
+    const long long below = cu[lo], above = cu[lo + 1];
+    const long long u = below > 0 && t - below < above - t ? below : above;
+    return (int)min(max(u, 1ll), (long long)T);
+}
+
 // The tiles of a block, in its order: tile k of the run of tokens b, channels
 // from d on.
 struct Cursor {
     int round, b, d, k, step, member;            // member of the team
     bool more;
     __device__ Cursor(const ScanPlan& p) : round(-1) { open(p); }
+    // Of the packed tokens: the part of this block's chain.
+    static __device__ int part(const ScanPlan& p) {
+        return blockIdx.x / p.team / p.groups;
+    }
     __device__ void open(const ScanPlan& p) {    // the next chain
         ++round;
         int chain = round * (int)gridDim.x + blockIdx.x;
@@ -375,12 +405,12 @@ struct Cursor {
             step = p.team;
         }
         k = member;
-        b = chain / p.groups;
+        b = p.parts > 1 ? 0 : chain / p.groups;
         d = chain % p.groups * CH;
     }
-    __device__ void move(const ScanPlan& p) {
+    __device__ void move(const ScanPlan& p, int tiles) {
         k += step;
-        if (k >= p.tiles && more) open(p);
+        if (k >= tiles && more) open(p);
     }
 };
 
@@ -402,6 +432,7 @@ struct Shared {
     float4 own[2][W - 1][32];
     float2 start[32];            // the state before the tile
     int cu[kMaxKept];            // packed sequences: their offsets, if few
+    int begin, end, tiles;       // the part's tokens; tiles that they fill
     uint64_t full, got[2];       // the tile is there; the step's maps are
 };
 
@@ -411,7 +442,7 @@ constexpr int shared_bytes(int team) {
     return (int)sizeof(Shared<T, G, A, BWD>) + 2 * team * 512;
 }
 
-template <typename T, typename G, Align A, bool BWD>
+template <typename T, typename G, Align A, bool BWD, bool PACKED>
 __global__ void __launch_bounds__(kThreads, kResident<T>)
 glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 const __grid_constant__ ScanPlan plan,
@@ -431,16 +462,43 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         for (uint64_t* bar : {&sh.full, &sh.got[0], &sh.got[1]})
             tc::mbar_init(bar, 1);
         tc::fence_mbar_init();
+        sh.begin = 0;
+        sh.end = a.T;
+        sh.tiles = plan.tiles;
     }
     await_grid_before();
     release_grid_after();
     const int* cu = a.cu;
-    if (a.cu && a.B < kMaxKept) {
+    if (PACKED && a.B < kMaxKept) {
         for (int i = threadIdx.x; i <= a.B; i += kThreads) sh.cu[i] = a.cu[i];
         cu = sh.cu;
     }
     if (plan.team > 1) cluster_sync();
     else __syncthreads();
+    if (PACKED && plan.parts > 1) {
+        const int q = Cursor::part(plan);
+        auto bound = [&](int i) {
+            return i == 0            ? 0
+                   : i == plan.parts ? a.T
+                                     : nearest_bound(
+                                           cu, a.B, a.T,
+                                           (int)((long long)a.T * i /
+                                                 plan.parts));
+        };
+        if (w == 0) {
+            const int u = bound(q), v = max(u, bound(q + 1));
+            if (lane == 0) {
+                sh.begin = u;
+                sh.end = v;
+                sh.tiles = (v - u + TILE - 1) / TILE;
+            }
+        }
+        __syncthreads();
+    }
+    // The chain's tokens, and tiles that they fill.
+    auto begin = [&] { return PACKED ? sh.begin : 0; };
+    auto end = [&] { return PACKED ? sh.end : a.T; };
+    auto tiles = [&] { return PACKED ? sh.tiles : plan.tiles; };
     // Starts the copy of a tile's inputs: row r is token lo + r, lo the tile's
     // lowest token.
     Stage<T, G, A, BWD>& st = sh.stage;
@@ -449,7 +507,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if (at.more && (A != kWide || threadIdx.x == 0)) {
             const int b = at.b, d = at.d;
             const int p = at.k * TILE;
-            const int lo = BWD ? a.T - TILE - p : p;
+            const int lo = BWD ? end() - TILE - p : begin() + p;
             if constexpr (A == kWide) {
                 tc::mbar_arrive_expect_tx(&sh.full, sizeof(st));
                 tma_load_3d(&st.la[0][0], &map_la, &sh.full, d, lo, b);
@@ -478,6 +536,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     };
 
     Cursor here(plan);
+    if (PACKED) here.more &= here.k < tiles();
     fetch(here);
     // What a warp needs to know of its tokens: the boundaries; the start of
     // the sequence that begins last (whoever ends it may write its last state
@@ -489,10 +548,12 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     auto look = [&](const Cursor& at) {
         const int p = at.k * TILE + w * S;
         soon = Bounds{0u, at.b, at.b};
-        if (a.cu) {
-            if (!at.more || p >= a.T) return;
-            soon = find_bounds<S, BWD>(cu, a.B, BWD ? a.T - 1 - p : p,
-                                       min(S, a.T - p));
+        if (PACKED) {
+            const int all = end() - begin();
+            if (!at.more || p >= all) return;
+            soon = find_bounds<S, BWD>(cu, a.B,
+                                       BWD ? end() - 1 - p : begin() + p,
+                                       min(S, all - p));
         } else {
             if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
             if (p == 0) soon.mask = 1u;
@@ -531,14 +592,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         const bool la = da < a.D, lb = db < a.D;
         // scan position p <-> token t
         const int p0 = here.k * TILE + w * S;
-        const int t0 = BWD ? a.T - 1 - p0 : p0;
-        const int steps = max(0, min(S, a.T - p0));
+        const int t0 = BWD ? end() - 1 - p0 : begin() + p0;
+        const int steps = max(0, min(S, end() - begin() - p0));
         if (here.k < here.step) carry = both(0.f);       // a chain begins
 
         const Bounds bd = soon;
         const float2 start = soon_start, prev = soon_prev;
         // whether some map of this step may start anew
-        const bool anew = a.cu || here.k < here.step;
+        const bool anew = PACKED || here.k < here.step;
         const unsigned int begins = bd.mask & ((1u << steps) - 1);
         // nothing begins, ends or is missing here
         const bool plain = bd.mask == 0 && steps == S;
@@ -565,7 +626,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
         float2 P = both(1.f), H = both(0.f);
         // where the rows of this warp lie (backwards: from its last)
-        const int lo = BWD ? a.T - TILE - here.k * TILE : here.k * TILE;
+        const int lo = BWD ? end() - TILE - here.k * TILE
+                           : begin() + here.k * TILE;
         const Rows<A, G> rl(static_cast<const G*>(a.la.p) + b * a.la.sb +
                                 here.d, a.la.st, lo);
         const Rows<A, T> rx(static_cast<const T*>(a.x.p) + b * a.x.sb +
@@ -611,11 +673,11 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             break;
         }
         Cursor then = here;
-        then.move(plan);
+        then.move(plan, tiles());
         if (A == kWide) fetch(then);
 
         const int m = here.member;
-        const int there = min(here.step, plan.tiles - (here.k - m));
+        const int there = min(here.step, tiles() - (here.k - m));
         float4(*team)[32] = maps + h * here.step;
         if (w == W - 1) {            // the tile's map, to all of the team
             float4 t = sh.own[h][0][lane];
@@ -695,14 +757,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     op += a.D;
                 }
             }
-        } else if (steps > 0 && (begins & (begins - 1)) == 0) {
+        } else if (!PACKED || (steps > 0 && (begins & (begins - 1)) == 0)) {
             // At most one sequence begins here (at `turn_at`), where the one
             // before it ends; another end may be after the last step.  (Code
             // that warps with a boundary alone run costs them most by its
             // length: its instructions have to be fetched.)
             const int turn_at = begins ? __ffs(begins) - 1 : S;
             const bool last_ends = bd.mask >> steps & 1;
-            float2 ended = both(0.f), before = prev;
+            float2 ended = both(0.f), before = prev, tail = both(0.f);
             if (BWD && last_ends && begins && turn_at > 0)
                 before = state_of(a.h0, bd.last);
 #pragma unroll
@@ -725,11 +787,13 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                     c = fma2(al[i], c, values(x[i]));
                     write2<A>(op + at, l0, l1, c);
                 }
+                if (PACKED && i == steps - 1) tail = c;
             }
             if (begins > 1) keep_state(bd.n, ended);
-            // (steps that are missing leave c as it is)
+            // (steps that are missing leave c as it is; those of the next
+            // part do not)
             if (last_ends)
-                keep_state(begins ? bd.last : bd.n, c);
+                keep_state(begins ? bd.last : bd.n, PACKED ? tail : c);
         } else if (steps > 0) {
             // One sequence after the other, steps from .. to - 1 each.
             int from = 0, n = bd.n;
@@ -776,10 +840,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             }
         }
 
-        // empty sequences, shared out over the tiles
-        if (a.cu && a.hT && a.hT != init) {
+        // empty sequences, shared out over the tiles (of the first part)
+        if (PACKED && a.hT && a.hT != init && begin() == 0) {
             for (long long e = (long long)here.k * W + w; e < a.B;
-                 e += (long long)plan.tiles * W)
+                 e += (long long)tiles() * W)
                 if (cu[e] == cu[e + 1])
                     keep_state((int)e, state_of(init, (int)e));
         }
@@ -868,14 +932,14 @@ void team_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
 
 // Blocks in teams of `team` that the current GPU holds at the same time (looked
 // up once per device).
-template <typename T, typename G, Align A, bool BWD>
+template <typename T, typename G, Align A, bool BWD, bool PACKED>
 int capacity(int team) {
     static std::atomic<int> found[64][kMaxTeam + 1];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int n = found[dev][team].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
+    auto* kernel = glr_scan_kernel<T, G, A, BWD, PACKED>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     team_config<T, G, A, BWD>(cfg, attr, team, team);
@@ -896,13 +960,26 @@ int capacity(int team) {
 // How `chains` chains of `tiles` tiles share the blocks that the GPU holds:
 // whole rounds of a chain per block, then the rest by a team each.  A round
 // counts as 1, a team of t as 1 / t.
-template <typename T, typename G, Align A, bool BWD>
-ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
-    ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1, 2000000000u, false};
+//
+// Packed tokens can be cut between two of the `sequences`, into as many parts
+// as leave a team of the chosen size to each.  A part is longer than the
+// average by what the lengths are, which the host does not know: half a
+// sequence per doubling is expected.  A step costs a larger team more (1 +
+// 0.03 t as measured).  Measured (us, whole / in parts; random lengths): 24
+// sequences of 16411 tokens, 1024 channels, forward 34.6 / 27.5, backward 52 /
+// 39.6; 4 of them, forward 33.5 / 25.5; 600 of 32768 x 2048 175 / 154; 64 of
+// 65536 x 64 85 / 15; 1000 of 65536 x 256 225 / 50.  Where one sequence has
+// nearly all the tokens the parts leave it a smaller team, of half as many
+// blocks at least: 600 of 32768 x 2048 122 / 150, 1000 of 65536 x 256 125 /
+// 134, 24 of 16411 x 1024 55 / 55.
+template <typename T, typename G, Align A, bool BWD, bool PACKED>
+ScanPlan plan_of(long long chains, int tiles, int D, int sequences,
+                 int* blocks) {
+    ScanPlan best{tiles, (D + CH - 1) / CH, 0, 0, 1, 1, 2000000000u, false};
     *blocks = 0;
     double cost = 0;
     for (int team = 1; team <= std::min(kMaxTeam, tiles); ++team) {
-        const int slots = capacity<T, G, A, BWD>(team);
+        const int slots = capacity<T, G, A, BWD, PACKED>(team);
         if (slots <= 0) break;
         const int rounds = (int)(chains / slots), rest = (int)(chains % slots);
         if ((long long)rest * team > slots) continue;
@@ -913,6 +990,28 @@ ScanPlan plan_of(long long chains, int tiles, int D, int* blocks) {
         best.rest = rest;
         best.team = team;
         *blocks = rounds ? slots : rest * team;
+    }
+    if (sequences < 2 || *blocks == 0 || best.rounds) return best;
+    // the time of a team, in steps of one block
+    auto steps = [&](int team, int parts) {
+        const double uneven = std::log2((double)parts) / 2 / sequences;
+        return (1 + 0.03 * team) *
+               std::max(1.0, tiles * (1.0 / parts + uneven) / team);
+    };
+    const int whole = best.team;
+    double least = steps(whole, 1) - 1;
+    for (int team = (whole + 1) / 2; team <= std::min(kMaxTeam, tiles);
+         ++team) {
+        const int slots = capacity<T, G, A, BWD, PACKED>(team);
+        if (slots <= 0) break;
+        const int parts =
+            std::min(sequences, slots / (best.groups * team));
+        if (parts < 2 || steps(team, parts) >= least) continue;
+        least = steps(team, parts);
+        best.parts = parts;
+        best.rest = best.groups * parts;
+        best.team = team;
+        *blocks = best.rest * team;
     }
     return best;
 }
@@ -940,16 +1039,17 @@ bool make_tile_map(CUtensorMap* m, const Strided& x, const GlrArgs& a,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, typename G, Align A, bool BWD>
+template <typename T, typename G, Align A, bool BWD, bool PACKED>
 cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
     const long long chains =
         (long long)((a.D + CH - 1) / CH) * (a.cu ? 1 : a.B);
     if (chains > 0x7fffffffLL) return cudaErrorInvalidValue;
     constexpr int TILE = kTile<T, BWD>;
-    auto* kernel = glr_scan_kernel<T, G, A, BWD>;
+    auto* kernel = glr_scan_kernel<T, G, A, BWD, PACKED>;
     int blocks = 0;
-    const ScanPlan p = plan_of<T, G, A, BWD>(
-        chains, (int)((a.T + (long long)TILE - 1) / TILE), a.D, &blocks);
+    const ScanPlan p = plan_of<T, G, A, BWD, PACKED>(
+        chains, (int)((a.T + (long long)TILE - 1) / TILE), a.D,
+        a.cu ? a.B : 1, &blocks);
     if (blocks <= 0) return cudaErrorInvalidValue;
     CUtensorMap mx{}, ml{}, mg{};
     if (A == kWide &&
@@ -977,8 +1077,11 @@ bool maps(const Strided& x, const GlrArgs& a) {
 
 template <typename T, typename G, Align A>
 cudaError_t launch_way(const GlrArgs& a, bool bwd, cudaStream_t s) {
-    return bwd ? launch_scan<T, G, A, true>(a, s)
-               : launch_scan<T, G, A, false>(a, s);
+    if (a.cu)
+        return bwd ? launch_scan<T, G, A, true, true>(a, s)
+                   : launch_scan<T, G, A, false, true>(a, s);
+    return bwd ? launch_scan<T, G, A, true, false>(a, s)
+               : launch_scan<T, G, A, false, false>(a, s);
 }
 
 }  // namespace
@@ -1026,15 +1129,16 @@ cudaError_t launch_glr_selftest(cudaStream_t stream) {
     a.o = m + 2 * CH;
     a.B = a.T = 1;
     a.D = CH;
-    if (capacity<float, float, kPair, false>(1) <= 0)
+    if (capacity<float, float, kPair, false, false>(1) <= 0)
         return cudaErrorInvalidValue;
-    const ScanPlan plan{1, 1, 0, 1, 1, 1000000u, true};
+    const ScanPlan plan{1, 1, 0, 1, 1, 1, 1000000u, true};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     team_config<float, float, kPair, false>(cfg, attr, 1, 1);
     cfg.stream = stream;
     const CUtensorMap none{};
-    return cudaLaunchKernelEx(&cfg, glr_scan_kernel<float, float, kPair, false>,
+    return cudaLaunchKernelEx(&cfg, glr_scan_kernel<float, float, kPair, false,
+                                              false>,
                               a, plan, none, none, none);
 }
 

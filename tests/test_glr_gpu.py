@@ -352,6 +352,58 @@ def test_few_channels_and_many_tokens(D, dtype, gtype):
     check_bwd(o, la, x, h0, h0)
 
 
+def uneven_lengths(kind):
+    r = np.random.default_rng(54)
+    if kind == "random":
+        return [int(v) for v in r.integers(0, 700, 40)]
+    if kind == "one long":               # most parts of the tokens are empty
+        return [0, 0, 9000] + [1, 0] * 20 + [3]
+    if kind == "long last":
+        return [1, 0] * 20 + [9000]
+    return [0, 411, 0, 0] * 30 + [0]     # empty ones at every boundary
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("D", [64, 66, 1001])
+@pytest.mark.parametrize("kind", ["random", "one long", "long last",
+                                  "empty between"])
+def test_packed_tokens_in_parts(kind, D, dtype, gtype):
+    """Many tokens of few channels: the sequences are shared out among more
+    blocks than could share one."""
+    lens = uneven_lengths(kind)
+    cu, T, N = offsets(lens), sum(lens), len(lens)
+    x, la = normal((T, D), dtype, 55), gates((T, D), gtype, 56)
+    h0, dhT = normal((N, D), F32, 57), normal((N, D), F32, 58)
+    o, hT = check_fwd(x, la, h0, cu)
+    g = check_bwd(o, la, x, dhT, h0, cu)
+    s = h0.clone()
+    o2, _ = kla.glr_fwd(x, la, s, cu.cuda(), hT=s)
+    n = torch.tensor(lens).cuda() > 0            # an empty one keeps its state
+    assert torch.equal(s[n], hT[n]) and torch.equal(s[~n], h0[~n])
+    assert torch.equal(o2, o)
+    x[int(cu[N // 2]):int(cu[N // 2 + 1])] = float("nan")
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[int(cu[N // 2]):int(cu[N // 2 + 1])] = True
+    o2, _ = kla.glr_fwd(x, la, h0, cu.cuda())
+    assert torch.equal(o2[~bad], o[~bad]) and o2[bad].isnan().all()
+
+
+def test_bad_offsets_of_many_tokens_stay_inside():
+    T, D, N = 9000, 64, 30
+    buf = torch.full((T + 512, D), 3.0, device="cuda")
+    o = buf[256:256 + T]
+    x, la = normal((T, D), F32, 59), gates((T, D), F32, 60)
+    h = normal((N, D), F32, 61)
+    r = np.random.default_rng(62)
+    for cu in (r.integers(-100, 20000, N + 1), np.arange(N, -1, -1) * 300,
+               np.full(N + 1, T), np.zeros(N + 1), np.full(N + 1, -5)):
+        c = torch.tensor(cu.astype(np.int32), device="cuda")
+        kla.glr_fwd(x, la, h, c, o=o)
+        kla.glr_bwd(x, la, x, h, None, c)
+        assert (buf[:256] == 3).all() and (buf[256 + T:] == 3).all()
+    assert kla.device_status() == 0
+
+
 @pytest.mark.parametrize("B,T,D", [(500, 70, 64), (30, 130, 2048),
                                    (700, 66, 70)])
 def test_more_channels_than_blocks(B, T, D):
