@@ -10,8 +10,8 @@
 // x 2048 forward 45 (89 %), backward 76 (91 %); 65536 x 2048, bf16 gates,
 // forward 141 (85 %), where a step of a team of 12 blocks takes 2.5 us: 1.2 of
 // work on its tile, the rest waiting for the slowest block's map and for the
-// next tile; 16411 x 1024 in 24 packed sequences, forward 28 (54 %); 8191 x
-// 1001 in 9, backward in fp32 43 (57 %): rows that line up on 4 bytes only,
+// next tile; 16411 x 1024 in 24 packed sequences, forward 27 (55 %); 8191 x
+// 1001 in 9, backward in fp32 48 (51 %): rows that line up on 4 bytes only,
 // copied in pieces by all threads (4 x 4096 x 2047 bf16 forward 56 against 40
 // us for 2048 channels).
 //
@@ -324,10 +324,12 @@ struct Bounds {
 // Packed sequences: the boundaries among the S tokens from t on (upwards, or
 // downwards with BACK), of which `steps` are there.  A warp works together: a
 // 32-way search for the sequence of t, then 32 offsets at a time.  Any content
-// of cu gives 0 <= n, last < B.
+// of cu gives 0 <= n, last < B.  Upwards, seq [S]: the sequence that begins at
+// step i (any number, where cu is not sorted).
 template <int S, bool BACK>
 __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
-                                              long long t, int steps) {
+                                              long long t, int steps,
+                                              int* seq) {
     const int lane = threadIdx.x % 32;
     int lo = 0, len = B;
     while (len > 1) {
@@ -351,6 +353,8 @@ __device__ __forceinline__ Bounds find_bounds(const int* cu, int B,
         }
         const bool in = pos >= 0 && pos <= S;
         mask |= __reduce_or_sync(0xffffffffu, in ? 1u << pos : 0u);
+        if (!BACK && in && pos < S && j < B && cu[j] < cu[j + 1])
+            seq[pos] = j;
         // upwards the sequence from the last such offset on, downwards the
         // one up to the first
         const int at = in && pos < steps ? (BACK ? j - 1 : j) : last;
@@ -433,6 +437,8 @@ struct Shared {
     float2 start[32];            // the state before the tile
     int cu[kMaxKept];            // packed sequences: their offsets, if few
     int begin, end, tiles;       // the part's tokens; tiles that they fill
+    // the sequences that begin in a warp's tokens, of this tile and the next
+    int seq[2][W][kSteps<T, BWD>];
     uint64_t full, got[2];       // the tile is there; the step's maps are
 };
 
@@ -545,7 +551,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     // up a tile ahead, except that without packing most tiles have none.
     Bounds soon{0u, here.b, here.b};
     float2 soon_start = both(0.f), soon_prev = both(0.f);
-    auto look = [&](const Cursor& at) {
+    auto look = [&](const Cursor& at, unsigned int turn) {
         const int p = at.k * TILE + w * S;
         soon = Bounds{0u, at.b, at.b};
         if (PACKED) {
@@ -553,7 +559,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             if (!at.more || p >= all) return;
             soon = find_bounds<S, BWD>(cu, a.B,
                                        BWD ? end() - 1 - p : begin() + p,
-                                       min(S, all - p));
+                                       min(S, all - p), sh.seq[turn & 1][w]);
         } else {
             if (p > 0 && p < a.T - S || p >= a.T || !at.more) return;
             if (p == 0) soon.mask = 1u;
@@ -572,7 +578,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             if (db < a.D) soon_prev.y = q[db];
         }
     };
-    look(here);
+    look(here, 0);
 
     // blocks that walked chains alone meet before they work as a team: no map
     // may come while its buffer and barrier are in use otherwise
@@ -707,7 +713,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         }
         // meanwhile
         if (A != kWide) fetch(then);
-        look(then);
+        look(then, turn + 1);
         if (w == 0) {                // the state before the tile, and after
             fault |= !wait_maps(&sh.got[h], turn >> 1 & 1, plan.wait_ns);
             if (anew) {
@@ -794,44 +800,69 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             // part do not)
             if (last_ends)
                 keep_state(begins ? bd.last : bd.n, PACKED ? tail : c);
+        } else if (steps > 0 && !BWD) {
+            // Any number of sequences, the states of K steps on their way at
+            // a time.  (One state after the other: 256 sequences of a token,
+            // 1024 channels, 26 instead of 12 us.)
+            constexpr int K = 4;
+            static_assert(S % K == 0, "");
+            auto begins_at = [&](int i) {
+                return min(max(sh.seq[h][w][i], 0), a.B - 1);
+            };
+            int n = bd.n;
+#pragma unroll
+            for (int i0 = 0; i0 < S; i0 += K) {
+                float2 from[K];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    from[k] = start;
+                    if (begins >> (i0 + k) & 1 && begins >> (i0 + k + 1))
+                        from[k] = state_of(init, begins_at(i0 + k));
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int i = i0 + k;
+                    if (i >= steps) break;
+                    if (begins >> i & 1) {
+                        if (i > 0) keep_state(n, c);
+                        n = begins_at(i);
+                        c = from[k];
+                    }
+                    c = fma2(al[i], c, values(x[i]));
+                    write2<A>(op + (long long)i * a.D, la, lb, c);
+                }
+            }
+            if (bd.mask >> steps & 1) keep_state(n, c);
         } else if (steps > 0) {
-            // One sequence after the other, steps from .. to - 1 each.
+            // Backwards one sequence after the other, steps from .. to - 1
+            // each.  (As above, with the states before them on their way too,
+            // this took 56 instead of 49 us on 90 sequences of 8191 x 1001 in
+            // fp32, 22 instead of 23 on 256 of a token.)
             int from = 0, n = bd.n;
             if (begins & 1) c = begins == 1 ? start : state_of(init, n);
             while (true) {
                 const unsigned int rest = bd.mask >> (from + 1);
                 const int to = min(rest ? from + __ffs(rest) : S, steps);
                 float2 before = both(0.f);
-                if (BWD && rest)
-                    before = n == bd.n ? prev : state_of(a.h0, n);
+                if (rest) before = n == bd.n ? prev : state_of(a.h0, n);
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
                     if (i < from || i >= to) continue;
                     const long long at = (long long)(i * DT) * a.D;
-                    if constexpr (BWD) {
-                        float2 h = values(x[i]);
-                        if (rest && i == to - 1) h = before;
-                        c = add2(c, values(g[i]));
-                        write2<A>(op + at, la, lb, c);
-                        c = mul2(al[i], c);
-                        write2<A>(dp + at, la, lb, mul2(c, h));
-                    } else {
-                        c = fma2(al[i], c, values(x[i]));
-                        write2<A>(op + at, la, lb, c);
-                    }
+                    float2 hp = values(x[i]);
+                    if (rest && i == to - 1) hp = before;
+                    c = add2(c, values(g[BWD ? i : 0]));
+                    write2<A>(op + at, la, lb, c);
+                    c = mul2(al[i], c);
+                    write2<A>(dp + at, la, lb, mul2(c, hp));
                 }
                 if (rest) keep_state(n, c);
                 if (!rest || to >= steps) break;
                 from = to;
                 if (begins >> (from + 1)) {      // not the last that begins
-                    const int t = t0 + from * DT;
-                    if (BWD) {
-                        n = max(n - 1, 0);
-                        while (n > 0 && cu[n] > t) --n;
-                    } else {
-                        n = min(n + 1, a.B - 1);
-                        while (n < a.B - 1 && cu[n + 1] <= t) ++n;
-                    }
+                    const int t = t0 - from;
+                    n = max(n - 1, 0);
+                    while (n > 0 && cu[n] > t) --n;
                     c = state_of(init, n);
                 } else {
                     n = bd.last;
@@ -964,14 +995,14 @@ int capacity(int team) {
 // Packed tokens can be cut between two of the `sequences`, into as many parts
 // as leave a team of the chosen size to each.  A part is longer than the
 // average by what the lengths are, which the host does not know: half a
-// sequence per doubling is expected.  A step costs a larger team more (1 +
-// 0.03 t as measured).  Measured (us, whole / in parts; random lengths): 24
-// sequences of 16411 tokens, 1024 channels, forward 34.6 / 27.5, backward 52 /
-// 39.6; 4 of them, forward 33.5 / 25.5; 600 of 32768 x 2048 175 / 154; 64 of
-// 65536 x 64 85 / 15; 1000 of 65536 x 256 225 / 50.  Where one sequence has
-// nearly all the tokens the parts leave it a smaller team, of half as many
-// blocks at least: 600 of 32768 x 2048 122 / 150, 1000 of 65536 x 256 125 /
-// 134, 24 of 16411 x 1024 55 / 55.
+// sequence per doubling is expected, and, the less likely the more sequences
+// there are, one with nearly all of the tokens, where only one team has work.
+// A step costs a larger team more (1 + 0.03 t).  Measured (us, whole / in
+// parts; random lengths): 24 sequences of 16411 tokens, 1024 channels, forward
+// 35 / 27, backward 52 / 39; 4 of them, forward 34 / 26; 600 of 32768 x 2048
+// 171 / 155; 64 of 65536 x 64 87 / 14; 1000 of 65536 x 256 209 / 49.  With one
+// long sequence and short ones: 24 of 16411 x 1024 34 / 40 (52 in three parts
+// instead of two, which gain no more on random lengths).
 template <typename T, typename G, Align A, bool BWD, bool PACKED>
 ScanPlan plan_of(long long chains, int tiles, int D, int sequences,
                  int* blocks) {
@@ -993,21 +1024,25 @@ ScanPlan plan_of(long long chains, int tiles, int D, int sequences,
     }
     if (sequences < 2 || *blocks == 0 || best.rounds) return best;
     // the time of a team, in steps of one block
-    auto steps = [&](int team, int parts) {
-        const double uneven = std::log2((double)parts) / 2 / sequences;
-        return (1 + 0.03 * team) *
-               std::max(1.0, tiles * (1.0 / parts + uneven) / team);
+    auto steps = [&](int team, double share) {
+        return (1 + 0.03 * team) * std::max(1.0, tiles * share / team);
     };
-    const int whole = best.team;
-    double least = steps(whole, 1) - 1;
-    for (int team = (whole + 1) / 2; team <= std::min(kMaxTeam, tiles);
-         ++team) {
+    double least = steps(best.team, 1) - 1;
+    // how likely one sequence has nearly all tokens
+    const double one = std::min(0.25, 6.0 / sequences);
+    for (int team = (best.team + 1) / 2, most = std::min(kMaxTeam, tiles);
+         team <= most; ++team) {
         const int slots = capacity<T, G, A, BWD, PACKED>(team);
         if (slots <= 0) break;
         const int parts =
             std::min(sequences, slots / (best.groups * team));
-        if (parts < 2 || steps(team, parts) >= least) continue;
-        least = steps(team, parts);
+        if (parts < 2) continue;
+        const double share =
+            1.0 / parts + std::log2((double)parts) / 2 / sequences;
+        const double time =
+            (1 - one) * steps(team, share) + one * steps(team, 1);
+        if (time >= least) continue;
+        least = time;
         best.parts = parts;
         best.rest = best.groups * parts;
         best.team = team;

@@ -388,6 +388,22 @@ def test_packed_tokens_in_parts(kind, D, dtype, gtype):
     assert torch.equal(o2[~bad], o[~bad]) and o2[bad].isnan().all()
 
 
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("D", [64, 70, 131])
+def test_many_sequences_of_a_token_beside_a_long_one(D, dtype, gtype):
+    """Single tokens of many sequences and a prompt in one call, states in
+    place."""
+    lens = [1] * 200 + [0, 2, 0, 0, 3] * 10 + [500] + [1, 0] * 30
+    cu, T, N = offsets(lens), sum(lens), len(lens)
+    x, la = normal((T, D), dtype, 63), gates((T, D), gtype, 64)
+    h0 = normal((N, D), F32, 65)
+    o, hT = check_fwd(x, la, h0, cu)
+    check_bwd(o, la, x, h0, h0, cu)
+    s = h0.clone()
+    o2, _ = kla.glr_fwd(x, la, s, cu.cuda(), hT=s)
+    assert torch.equal(s, hT) and torch.equal(o2, o)
+
+
 def test_bad_offsets_of_many_tokens_stay_inside():
     T, D, N = 9000, 64, 30
     buf = torch.full((T + 512, D), 3.0, device="cuda")
