@@ -284,9 +284,11 @@ struct Ring {
     // After a copy that never came: waits (1 ms each) for those that may be
     // on their way yet.
     __device__ void give_up() const {
-        if (!WIDE || t != 0) return;
-        for (int k = 0; k < depth; ++k)
-            for (int p = 0; p < 2; ++p) tc::mbar_wait(full + k, p, 1000000);
+        if constexpr (WIDE) {
+            for (int k = 0; t == 0 && k < depth; ++k)
+                for (int p = 0; p < 2; ++p)
+                    tc::mbar_wait(full + k, p, 1000000);
+        }
     }
 };
 
