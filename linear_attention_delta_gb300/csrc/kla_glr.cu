@@ -1100,10 +1100,9 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t s) {
 }
 
 // Whether all rows of a strided input start on a multiple of `bytes`.
-bool lines_up(const Strided& x, const GlrArgs& a, size_t elt, size_t bytes) {
+bool lines_up(const Strided& x, size_t elt, size_t bytes) {
     return reinterpret_cast<uintptr_t>(x.p) % bytes == 0 &&
-           (a.T == 1 || x.st * elt % bytes == 0) &&
-           (a.cu || a.B == 1 || x.sb * elt % bytes == 0);
+           x.st * elt % bytes == 0 && x.sb * elt % bytes == 0;
 }
 // Whether a tensor map can describe it: no repeated rows.
 bool maps(const Strided& x, const GlrArgs& a) {
@@ -1121,7 +1120,14 @@ cudaError_t launch_way(const GlrArgs& a, bool bwd, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_glr(const GlrArgs& a, bool bwd, cudaStream_t stream) {
+cudaError_t launch_glr(const GlrArgs& args, bool bwd, cudaStream_t stream) {
+    // A stride that no step is taken with may be any number: how rows line up,
+    // in global and in shared memory, must not be derived from it.
+    GlrArgs a = args;
+    for (Strided* x : {&a.x, &a.la, &a.g}) {
+        if (a.T <= 1) x->st = 0;
+        if (a.cu || a.B <= 1) x->sb = 0;
+    }
     if (a.T == 0) {              // every sequence is empty
         const float* init = bwd ? a.dhT : a.h0;
         const size_t n = sizeof(float) * (size_t)a.B * a.D;
@@ -1134,9 +1140,9 @@ cudaError_t launch_glr(const GlrArgs& a, bool bwd, cudaStream_t stream) {
         using T = decltype(t);
         using G = decltype(g);
         auto in = [&](size_t tb, size_t gb) {
-            return lines_up(a.x, a, sizeof(T), tb) &&
-                   lines_up(a.la, a, sizeof(G), gb) &&
-                   (!bwd || lines_up(a.g, a, sizeof(T), tb));
+            return lines_up(a.x, sizeof(T), tb) &&
+                   lines_up(a.la, sizeof(G), gb) &&
+                   (!bwd || lines_up(a.g, sizeof(T), tb));
         };
         // pairs: the outputs' rows (of D) too
         const bool pairs =

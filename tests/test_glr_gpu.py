@@ -154,6 +154,32 @@ def test_strided_views(dtype, gtype):
     check_fwd(wide[0, :, 3:3 + D], wide_a[0, :, 3:3 + D], h0, cu)
 
 
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("width", [129, 133, 200])
+def test_one_token_of_a_strided_view(width, dtype, gtype):
+    """One token a sequence, cut out of rows of odd width: the distance
+    between tokens, which no step is taken with, says nothing about how the
+    token lines up."""
+    for B, T in ((1, 4), (2, 2), (2, 3)):
+        wide = normal((B, T, width), dtype, 5)
+        wide_a = gates((B, T, width), gtype, 6)
+        for D, at in ((64, 0), (66, 0), (64, 2), (66, 1), (34, 4), (63, 1)):
+            h0, dhT = normal((B, D), F32, 7), normal((B, D), F32, 8)
+            x, la = (v[:, 1:2, at:at + D] for v in (wide, wide_a))
+            dx, da = x.contiguous().clone(), la.contiguous().clone()
+            for v, g in ((x, la), (x, da), (dx, la)):
+                o, _ = check_fwd(v, g, h0)
+                check_bwd(v, g, dx, dhT, h0)
+                check_bwd(o, g, x, dhT, h0)
+            # the same tokens packed: one token in all
+            cu = offsets([0, 1])
+            h0, dhT = normal((2, D), F32, 9), normal((2, D), F32, 10)
+            for v, g in ((x[0], la[0]), (x[0], da[0]), (dx[0], la[0])):
+                o, _ = check_fwd(v, g, h0, cu)
+                check_bwd(v, g, dx[0], dhT, h0, cu)
+                check_bwd(o, g, x[0], dhT, h0, cu)
+
+
 @pytest.mark.parametrize("T", [5, 128, 700])
 def test_extreme_gates(T):
     D = 64
