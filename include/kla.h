@@ -589,7 +589,7 @@ KLA_API kla_status kla_chunk_bwd_noalloc(
  * rows = 0 launches nothing.
  * Errors: KLA_ERR_INVALID_ARG (rows < 0, D < 1, eps negative or not finite,
  * a negative stride, a null or misaligned pointer, overlapping buffers),
- * KLA_ERR_CUDA.  Any D is supported.  No workspace.
+ * KLA_ERR_UNSUPPORTED_SHAPE (D > 2^31 - 4097), KLA_ERR_CUDA.  No workspace.
  */
 KLA_API kla_status kla_layernorm_fwd(
     const void* x, long long x_stride, const void* residual,
@@ -660,7 +660,7 @@ KLA_API kla_status kla_layernorm_bwd(
  * parts on chip (thread-block clusters).
  * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, D < 1, a null or
  * misaligned pointer, overlapping buffers), KLA_ERR_UNSUPPORTED_SHAPE
- * (T > 2^31 - 4097), KLA_ERR_CUDA.
+ * (T, D or the number of packed sequences > 2^31 - 4097), KLA_ERR_CUDA.
  */
 KLA_API kla_status kla_glr_fwd(
     const void* x, long long x_sb, long long x_st, const void* log_alpha,

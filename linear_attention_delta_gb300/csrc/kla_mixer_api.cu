@@ -26,6 +26,10 @@ size_t row_bytes(int rows, int D, long long stride, size_t elt) {
 
 Span span(const void* p, size_t n) { return {p, p ? n : 0}; }
 
+// The kernels count columns, tokens and packed sequences in 32 bits; a thread
+// may step past the last one by a block's or a tile's worth.
+constexpr int kMaxCount = 0x7fffffff - 4096;
+
 }  // namespace
 
 extern "C" kla_status kla_layernorm_fwd(
@@ -37,6 +41,7 @@ extern "C" kla_status kla_layernorm_fwd(
         !valid(dtype) || !valid(wdtype) || !(eps >= 0.f) ||
         !std::isfinite(eps) || (sum && !residual))
         return KLA_ERR_INVALID_ARG;
+    if (D > kMaxCount) return KLA_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return KLA_OK;
     const size_t e = size_of(dtype), we = size_of(wdtype);
     if (!given(x, e) || !given(y, e) || !ok_or_null(residual, e) ||
@@ -63,6 +68,7 @@ extern "C" kla_status kla_layernorm_bwd_workspace_size(int rows, int D,
                                                        size_t* bytes) {
     if (!bytes || rows < 0 || D < 1 || !valid(dtype))
         return KLA_ERR_INVALID_ARG;
+    if (D > kMaxCount) return KLA_ERR_UNSUPPORTED_SHAPE;
     *bytes = kla::layernorm_bwd_workspace_bytes(rows, D, dtype);
     return KLA_OK;
 }
@@ -77,6 +83,7 @@ extern "C" kla_status kla_layernorm_bwd(
     if (rows < 0 || D < 1 || y_grad_stride < 0 || x_stride < 0 ||
         sum_grad_stride < 0 || !valid(dtype) || !valid(wdtype))
         return KLA_ERR_INVALID_ARG;
+    if (D > kMaxCount) return KLA_ERR_UNSUPPORTED_SHAPE;
     const size_t e = size_of(dtype), we = size_of(wdtype);
     if (!ok_or_null(weight_grad, we) || !ok_or_null(bias_grad, we) ||
         !ok_or_null(weight, we) || !ok_or_null(sum_grad, e))
@@ -114,9 +121,6 @@ extern "C" kla_status kla_layernorm_bwd(
 
 namespace {
 
-// Token positions are counted in 32 bits, with room for a partial tile.
-constexpr int kMaxTokens = 0x7fffffff - 4096;
-
 // Bytes spanned by a strided [B, T, D] input of the recurrence.
 size_t span_bytes(const kla::GlrArgs& a, const kla::Strided& x, size_t elt) {
     const long long t = a.T ? (long long)(a.T - 1) * x.st : 0;
@@ -132,7 +136,8 @@ kla_status glr_impl(const kla::GlrArgs& a, bool bwd, kla_stream_t stream) {
     if (!ok_or_null(a.h0, 4) || !ok_or_null(a.dhT, 4) ||
         !ok_or_null(a.hT, 4) || !ok_or_null(a.cu, 4))
         return KLA_ERR_INVALID_ARG;
-    if (a.T > kMaxTokens) return KLA_ERR_UNSUPPORTED_SHAPE;
+    if (a.T > kMaxCount || a.D > kMaxCount || (a.cu && a.B > kMaxCount))
+        return KLA_ERR_UNSUPPORTED_SHAPE;
     // packed tokens belong to some sequence
     if (a.B == 0) return a.cu && a.T > 0 ? KLA_ERR_INVALID_ARG : KLA_OK;
     const size_t e = size_of(a.dtype), ge = size_of(a.gdtype);
@@ -192,6 +197,7 @@ extern "C" kla_status kla_glr_step(const void* x, long long x_stride,
     if (N < 0 || D < 1 || x_stride < 0 || a_stride < 0 || !valid(dtype) ||
         !valid(gate_dtype))
         return KLA_ERR_INVALID_ARG;
+    if (D > kMaxCount) return KLA_ERR_UNSUPPORTED_SHAPE;
     if (N == 0) return KLA_OK;
     const size_t e = size_of(dtype), ge = size_of(gate_dtype);
     if (!given(x, e) || !given(log_alpha, ge) || !given(S, 4) || !given(o, e))

@@ -155,6 +155,24 @@ def test_glr_refuses_more_tokens_than_it_counts(lib):
     assert glr_bwd(lib, T=0x7fffffff) == UNSUPPORTED
 
 
+def test_refuses_more_channels_and_sequences_than_it_counts(lib):
+    """A thread's column would pass 2^31.  (At the limit itself the call gets
+    as far as the overlap of these buffers.)"""
+    n, most = ctypes.c_size_t(0), 0x7fffffff - 4096
+    size = lib.kla_layernorm_bwd_workspace_size
+    for D, want in ((most, INVALID), (most + 1, UNSUPPORTED),
+                    (0x7fffffff, UNSUPPORTED)):
+        assert ln_fwd(lib, rows=1, D=D) == want
+        assert ln_bwd(lib, rows=1, D=D, ws_bytes=1 << 40) == want
+        assert glr_fwd(lib, B=1, T=1, D=D) == want
+        assert glr_bwd(lib, B=1, T=1, D=D) == want
+        assert glr_step(lib, N=1, D=D) == want
+        assert glr_fwd(lib, cu=at(9), B=D) == want
+        assert glr_bwd(lib, cu=at(9), B=D) == want
+        assert size(1, D, BF16, ctypes.byref(n)) == (
+            OK if D == most else UNSUPPORTED)
+
+
 def test_binding_refuses_cpu_tensors():
     x, s = torch.zeros(1, 4, 16), torch.zeros(4, 16)
     for call in (lambda: kla.layernorm_fwd(x),
