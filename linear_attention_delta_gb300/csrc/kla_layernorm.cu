@@ -778,7 +778,7 @@ __global__ void ln_bwd_cols_kernel(LayerNormBwdArgs a, float* part) {
     }
     float* p = part + (size_t)blockIdx.y * 2 * a.D;
     p[col] = w;
-    p[a.D + col] = b;
+    p[(size_t)a.D + col] = b;
 }
 
 // dw, db = the partial sums added up in a fixed order: a block takes 32

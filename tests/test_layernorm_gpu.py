@@ -301,6 +301,26 @@ def test_offsets_past_32_bits():
               stats=(tail[2], tail[3]))
 
 
+def test_weight_gradients_of_more_than_2_30_columns():
+    """The partial sums' place of column c of the bias's gradient is D + c,
+    past 2^31.  With one row the gradients are dy xh and dy."""
+    D = 2 ** 30 + 1000
+    g = torch.Generator(device="cuda").manual_seed(27)
+    x = torch.randn(1, D, device="cuda", generator=g, dtype=BF16)
+    dy = torch.randn(1, D, device="cuda", generator=g, dtype=BF16)
+    mean = torch.full((1,), 0.25, device="cuda")
+    rstd = torch.full((1,), 0.75, device="cuda")
+    got = kla.layernorm_bwd(dy, x, None, mean, rstd)
+    assert torch.equal(got["bias_grad"], dy[0])
+    for i in range(0, D, 1 << 28):
+        q = slice(i, i + (1 << 28))
+        xh = (x[0, q].float() - 0.25) * 0.75
+        ref = dy[0, q].float() * xh
+        err = (got["weight_grad"][q].float() - ref).abs()
+        # the result's own rounding; xh's and the product's in fp32
+        assert (err <= (U16 * 1.01 + 4 * U32) * ref.abs()).all()
+
+
 def test_refusals():
     x, w = normal((4, 64), BF16, 25), normal((64,), BF16, 26)
     _, _, mean, rstd = kla.layernorm_fwd(x, w, w)
