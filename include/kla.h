@@ -653,7 +653,10 @@ KLA_API kla_status kla_layernorm_bwd(
  * x, o of type `dtype`, log_alpha of type `gate_dtype`; h0, hT [B, D] fp32.
  * The state is held in fp32, rounded only on its way to o.  log_alpha is
  * meant to be <= 0 (-inf forgets: h_t = x_t for finite h_{t-1}); positive
- * values are computed as written.  h0 null: zeros; hT null: not written; hT
+ * values up to 88 (where a decay leaves the range of fp32) are computed as
+ * written, whatever the products of the decays are, as long as the state stays
+ * in range.  A decay below 2^-126, and the product of up to 96 tokens' decays
+ * below 2^-252, counts as 0; an infinite state becomes NaN there.  h0 null: zeros; hT null: not written; hT
  * may be h0 itself (else it may not overlap any input).  The hT of an empty
  * sequence is its h0.
  * No workspace.  One kernel; blocks that share a sequence exchange their

@@ -41,7 +41,7 @@ using bf16 = __nv_bfloat16;
 // which take every G-th tile each, in order; a block
 //   1. waits for its tile's inputs in shared memory, takes them into
 //      registers, and starts the copy of its next tile,
-//   2. reduces each warp's S steps to the affine map c -> P c + H of the
+//   2. reduces each warp's S steps to the affine map c -> R^2 c + H of the
 //      state, and the warps' maps to the tile's map,
 //   3. sends the tile's map to all blocks of the team (st.async into their
 //      shared memory) and waits for the G maps of this step,
@@ -59,8 +59,8 @@ using bf16 = __nv_bfloat16;
 //
 // A state that a sequence starts from replaces c (it is not multiplied by
 // zero), so nothing of one packed sequence, not even a NaN, reaches the next:
-// a map that does not depend on the state before it has P = -0, which no
-// product of decays is.
+// a map that does not depend on the state before it has R = -0, which no
+// root of decays is.
 
 constexpr int W = 4;             // warps of a block
 // Tokens of a warp, S, and blocks that an SM is to hold, which bounds a
@@ -109,10 +109,15 @@ __device__ __forceinline__ float2 decay(float2 l) {
                        fabsf(l.y) <= 0x1p-6f ? p.y : ey);
 }
 
-// Maps of two channels as (P.x, P.y, H.x, H.y).  P is finite (see `bounded`),
-// so that a zero state stays zero however large the decays' product grew.
+// Maps c -> R R c + H of two channels as (R.x, R.y, H.x, H.y).  R is the square
+// root of the decays' product: the product of up to 96 decays may be far out of
+// the range of fp32 where it meets a state that it brings back into it, and R
+// has twice the range (a product of 2^-252 or 2^254 takes any state but
+// denormal ones out of range).  R is finite (see `bounded`), so that a zero
+// state stays zero however large the product grew.
 __device__ __forceinline__ float2 plain_apply(float4 m, float2 c) {
-    return fma2(make_float2(m.x, m.y), c, make_float2(m.z, m.w));
+    const float2 R = make_float2(m.x, m.y);
+    return fma2(mul2(c, R), R, make_float2(m.z, m.w));
 }
 // Whether a map does not depend on the state before it.  That goes by the
 // tokens, so it is the same in all channels.
@@ -122,9 +127,9 @@ __device__ __forceinline__ bool fresh(float4 m) {
 __device__ __forceinline__ float2 apply(float4 m, float2 c) {
     return fresh(m) ? make_float2(m.z, m.w) : plain_apply(m, c);
 }
-// A product past the range (decays above 1) or NaN (then H is, too) becomes
-// the largest number; -0 stays.
-__device__ __forceinline__ float bounded(float P) { return fminf(P, 3e38f); }
+// An R past the range (decays above 1) or NaN (then H is, too) becomes the
+// largest number; -0 stays.
+__device__ __forceinline__ float bounded(float R) { return fminf(R, 3e38f); }
 
 // A map to the same place in the shared memory of block `rank` of the
 // cluster, counted by that block's mbarrier.
@@ -630,7 +635,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
 
         float2 al[S];                // decays
         Two<T> x[S], g[BWD ? S : 1]; // x; backward: o of the token before, do
-        float2 P = both(1.f), H = both(0.f);
+        float2 L[2] = {both(0.f), both(0.f)};    // sums of their logs
+        float2 H = both(0.f);
         // where the rows of this warp lie (backwards: from its last)
         const int lo = BWD ? end() - TILE - here.k * TILE
                            : begin() + here.k * TILE;
@@ -647,9 +653,11 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         if constexpr (BWD) at_g = &st.g[0][0] + rg.first + r0 * rg.pitch;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            al[i] = decay(values(read2<A>(at_l + DT * i * rl.pitch, lane)));
+            const float2 l = values(read2<A>(at_l + DT * i * rl.pitch, lane));
+            al[i] = decay(l);
             x[i] = read2<A>(at_x + DT * i * rx.pitch, lane);
-            P = mul2(P, al[i]);
+            // (in two halves: smaller sums, smaller roundings)
+            L[2 * i / S] = add2(L[2 * i / S], l);
             if constexpr (BWD) {
                 g[i] = read2<A>(at_g + DT * i * rg.pitch, lane);
                 H = mul2(al[i], add2(H, values(g[i])));
@@ -657,9 +665,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 H = fma2(al[i], H, values(x[i]));
             }
         }
+        float2 R = decay(mul2(add2(L[0], L[1]), both(0.5f)));
         if (begins) {                // only the last sequence matters
             const int from = 31 - __clz(begins);
-            P = both(-0.f);
+            R = both(-0.f);
             H = start;
 #pragma unroll
             for (int i = 0; i < S; ++i)
@@ -671,7 +680,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
                 }
         }
         const float4 mine =
-            make_float4(bounded(P.x), bounded(P.y), H.x, H.y);
+            make_float4(bounded(R.x), bounded(R.y), H.x, H.y);
         if (w < W - 1) sh.own[h][w][lane] = mine;
         // the tile's place is free, the maps are there
         if (__syncthreads_or(fault)) {
@@ -692,9 +701,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
             for (int u = 1; u < W; ++u) {
                 const float4 q = u < W - 1 ? sh.own[h][u][lane] : mine;
                 const float2 v = plain_apply(q, make_float2(t.z, t.w));
-                const float2 pq =
+                const float2 r =
                     mul2(make_float2(t.x, t.y), make_float2(q.x, q.y));
-                t = make_float4(bounded(pq.x), bounded(pq.y), v.x, v.y);
+                t = make_float4(bounded(r.x), bounded(r.y), v.x, v.y);
                 if (anew && fresh(q)) {
                     t.z = q.z;
                     t.w = q.w;

@@ -207,6 +207,89 @@ def test_growth_past_the_range_starts_from_zero():
     assert (g["x_grad"] == 0).all() and (g["log_alpha_grad"] == 0).all()
 
 
+def check_growth(x, la, h0, do=None, dhT=None, cu=None):
+    """Forward (and backward, with do) where decays above 1 have products
+    past the range of fp32 and states stay inside it.  A decay's error is
+    that of l log2 e, two roundings of its size, besides the 8 units of the
+    other bounds; the smallest numbers are rounded to 2^-149, bf16's to
+    2^-133."""
+    small = {F32: 0.0, BF16: 2.0 ** -134}
+    dcu, f = None if cu is None else cu.cuda(), mixer.f64
+    k = (8 + 2 * np.abs(np.maximum(f(la), -88.0))) * U32
+    ab = lambda v: None if v is None else np.abs(f(v))  # noqa: E731
+    o, hT = kla.glr_fwd(x, la, h0, dcu)
+    mag, _ = mixer.glr_fwd(ab(x), la, ab(h0), cu)
+    bo, bh = mixer.glr_fwd(k * mag + 1e-44, la, None, cu)
+    ro, rh = mixer.glr_fwd(x, la, h0, cu)
+    assert np.abs(ro).max() < 3e38
+    assert_within("o", o, ro, bo + small[x.dtype], x.dtype)
+    assert_within("hT", hT, rh, bh, F32)
+    if do is None:
+        return
+    g = kla.glr_bwd(o, la, do, dhT, h0, dcu)
+    ref = mixer.glr_bwd(o, la, do, dhT, h0, cu)
+    mag, da, d0 = mixer.glr_bwd(ab(o), la, ab(do), ab(dhT), ab(h0), cu)
+    e, ea, e0 = mixer.glr_bwd(ab(o), la, k * mag + 1e-44, None, ab(h0), cu)
+    for name, r, b, dt in zip(
+            ("x_grad", "log_alpha_grad", "h0_grad"), ref,
+            (e, ea + k * da + 1e-44, e0 + k.max() * d0),
+            (o.dtype, la.dtype, F32)):
+        assert np.abs(r).max() < 3e38
+        assert_within(name, g[name], r, b + small[dt], dt)
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("B,T,D", [(2, 150, 64), (1, 1000, 66), (2, 700, 33),
+                                   (1, 9000, 128), (300, 160, 96)])
+def test_growth_of_a_small_state(B, T, D, dtype, gtype):
+    """Up by some e^150 and down again: the product of a tile's decays
+    overflows, the state does not."""
+    r = np.random.default_rng(66)
+    up = np.where(np.arange(T) // 150 % 2 == 0, 1.0, -1.0)
+    la = torch.from_numpy((up[:, None] * r.uniform(0.8, 1.1, D)).astype(
+        np.float32)).cuda().to(gtype).expand(B, T, D).contiguous()
+    x, do = normal((B, T, D), dtype, 67) * 1e-36, \
+        normal((B, T, D), dtype, 68) * 1e-36
+    h0, dhT = normal((B, D), F32, 69) * 1e-36, normal((B, D), F32, 70) * 1e-36
+    check_growth(x, la, h0, do, dhT)
+    check_growth(torch.zeros_like(x), la, h0, torch.zeros_like(x), dhT)
+    if B == 1:                           # sequences that begin on the way up
+        cu = offsets([T // 3, 0, 1, T - T // 3 - 41, 40])
+        h0, dhT = normal((5, D), F32, 71) * 1e-36, \
+            normal((5, D), F32, 72) * 1e-36
+        check_growth(x[0], la[0], h0, do[0], dhT, cu)
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("D", [64, 33])
+def test_growth_in_few_tokens(D, dtype, gtype):
+    T = 400
+    la = torch.zeros(1, T, D, device="cuda", dtype=gtype)
+    la[:, 5:9], la[:, 30:34] = 40.0, -40.0       # within a warp's tokens
+    la[:, 90:94], la[:, 310:314] = 42.0, -42.0   # and tiles apart
+    la[:, 200::50] += 0.5
+    h0, dhT = normal((1, D), F32, 73) * 1e-37, normal((1, D), F32, 74) * 1e-37
+    x = normal((1, T, D), dtype, 75) * 1e-38
+    check_growth(x, la, h0, torch.zeros_like(x), dhT)
+    # growth that is then forgotten, in one warp's tokens and in two tiles'
+    la = torch.zeros(1, T, D, device="cuda", dtype=gtype)
+    la[:, 2:14] = la[:, 60:200:12] = 10.0
+    la[:, 16] = la[:, 250] = -float("inf")
+    x = normal((1, T, D), dtype, 76)
+    x[:, :251] = 0.0
+    x[:, 17] = 1e-37
+    check_growth(x, la, h0)
+
+
+def test_growth_past_the_range_is_infinite():
+    x = torch.zeros(2, 500, 64, device="cuda")
+    la = torch.ones_like(x)
+    o, hT = kla.glr_fwd(x, la, torch.ones(2, 64, device="cuda"))
+    ref = np.exp(np.arange(1, 501.0))
+    assert (o[:, ref > 4e38] == float("inf")).all() and hT.isinf().all()
+    assert o[:, ref < 3e38].isfinite().all()
+
+
 @pytest.mark.parametrize("dtype,gtype", TYPES)
 def test_bad_sequences_stay_their_own(dtype, gtype):
     """NaN and infinities of one packed sequence, in x, in the gates or in
