@@ -589,7 +589,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     // may come while its buffer and barrier are in use otherwise
     bool apart = plan.rounds > 0 && plan.team > 1;
     float2 carry = both(0.f);        // the state before the team's tiles
-    bool fault = false;
+    bool fault = false, late = false;    // late: the tile has not come
     unsigned int turn = 0;
     for (; here.more; ++turn) {
         if (apart && here.step > 1) {
@@ -627,7 +627,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
         };
 
         if (A == kWide) {
-            fault |= !tc::mbar_wait(&sh.full, h);
+            late = !tc::mbar_wait(&sh.full, h);
+            fault |= late;
         } else {
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();
@@ -892,8 +893,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs a,
     if (A != kWide) asm volatile("cp.async.wait_all;" ::: "memory");
     if (fault && threadIdx.x == 0) {
         atomicOr(&g_fault_glr, 1u);
-        // a copy that may be on its way yet
-        if (A == kWide) tc::mbar_wait(&sh.full, ~turn & 1, 1000000);
+        // The late copy may be on its way yet.  (A block that gave up waiting
+        // for maps has still waited for its next tile before it left.)
+        if (A == kWide && late) tc::mbar_wait(&sh.full, turn & 1, 1000000);
     }
     if (apart) cluster_sync();
     if (plan.team > 1) cluster_sync();           // nobody sends here any more
