@@ -505,8 +505,14 @@ ln_fwd_ring_kernel(const __grid_constant__ LayerNormArgs a, int depth) {
 #pragma unroll
             for (int e = 0; e < Row::E; ++e) s.v[e] = add2(s.v[e], r.v[e]);
         }
-        const float mean =
-            group_sum<TPR>(s.sum(), red[0] + g * (TPR / 32), 1 + g) * over;
+        // The sum over D, as a division rounds it: a row of one value has that
+        // mean exactly, where the sum is exact, and y = bias.  (1 / D rounded
+        // alone left 6e-5 of 1000 at D = 1000, which eps = 1e-5 makes 0.02
+        // in y.)
+        const float sum =
+            group_sum<TPR>(s.sum(), red[0] + g * (TPR / 32), 1 + g);
+        const float first = sum * over, rest = fmaf(-first, (float)a.D, sum);
+        const float mean = rest == rest ? fmaf(rest, over, first) : first;
         if (group_dead<TPR>(fault, &dead[turn][g])) {
             fault = true;
             break;

@@ -204,6 +204,28 @@ def test_constant_rows():
     assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [3, 20000])
+@pytest.mark.parametrize("D", [96, 100, 250, 1000, 1001, 1025])
+def test_constant_rows_of_any_width(D, rows, dtype):
+    """Sums that are exact: the mean is the value and y the bias, however many
+    rows there are."""
+    v = torch.tensor([1.0, 3.0, 7.0, 10.0, 100.0, 1000.0, 0.5, -3.0],
+                     device="cuda").repeat(rows)[:rows]
+    x = v[:, None].to(dtype).expand(rows, D).contiguous()
+    b = normal((D,), dtype, 28)
+    y, _, mean, _ = kla.layernorm_fwd(x, None, b)
+    assert torch.equal(mean, x[:, 0].float())
+    assert torch.equal(y, b.expand(rows, D))
+
+
+def test_infinite_rows_keep_their_mean():
+    x = normal((20000, 384), BF16, 29)
+    x[::100, 7] = float("inf")
+    mean = kla.layernorm_fwd(x)[2]
+    assert mean[::100].isinf().all() and mean.isinf().sum() == 200
+
+
 @pytest.mark.parametrize("D", [96, 512, 1001, 8192, 40001])
 def test_bad_rows_stay_their_own(D):
     """A row with a NaN or an infinity is NaN; its neighbours are not."""
