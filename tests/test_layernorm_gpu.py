@@ -144,6 +144,97 @@ def test_many_rows(dtype):
     check_bwd(dy, x, w, ds=x)
 
 
+# Widths of each number of threads a row (in elements of bf16; half of it in
+# fp32), aligned rows first, and rows enough for a group of threads to take a
+# dozen even where an SM holds 2048 threads: the rings go round.
+RINGS = [(256, 32), (512, 32), (1000, 64), (2048, 128), (4096, 256),
+         (8192, 512), (8208, 640), (10240, 640), (12288, 512), (16384, 512)]
+LOOSE = [(127, 32), (255, 32), (511, 64), (1001, 128), (2047, 256),
+         (4095, 512)]
+
+
+def ring_rows(threads):
+    return 12 * 152 * (2048 // threads) + 5
+
+
+def assert_close(name, got, ref, bound):
+    """As assert_within, on the GPU; bound already has the rounding."""
+    bad = ~((got.double() - ref).abs() <= bound)
+    assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[0].tolist())
+
+
+def integers(g, lo, hi, shape, dtype):
+    return torch.randint(lo, hi + 1, shape, device="cuda",
+                         generator=g).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("k", range(len(RINGS) + 2 * len(LOOSE)))
+def test_rings_of_rows(k, dtype):
+    """Forward and backward over many rows of every width of the rings, all
+    different: a place that is read too early or twice, or a row left out of
+    the weight gradients, shows.  The loose widths also as slices at an odd
+    offset of wider rows.  In the backward, x, dy and the statistics are such
+    that the weight gradients' terms and sums are exact in fp32."""
+    if k < len(RINGS):
+        D, threads = RINGS[k]
+        D = D if dtype == BF16 else D // 2
+        wider = 0
+    else:
+        D, threads = LOOSE[(k - len(RINGS)) % len(LOOSE)]
+        wider = 0 if k - len(RINGS) < len(LOOSE) else 6
+    rows, g = ring_rows(threads), torch.Generator(device="cuda")
+    g.manual_seed(1000 * k + D)
+
+    def cut(t):
+        return t[:, wider // 2:wider // 2 + D]
+
+    u = U16 * 1.01 if dtype == BF16 else U32
+    x = cut(torch.randn(rows, D + wider, device="cuda", generator=g).to(dtype))
+    res = cut(torch.randn(rows, D + wider, device="cuda",
+                          generator=g).to(dtype))
+    w = 1 + 0.2 * torch.randn(D, device="cuda", generator=g)
+    b = torch.randn(D, device="cuda", generator=g)
+    K = (32 + D / 32) * U32
+    for r in (None, res):
+        y, s, mean, rstd = kla.layernorm_fwd(x, w, b, residual=r)
+        exact = x.double() if r is None else x.double() + r.double()
+        var, m = torch.var_mean(exact, 1, correction=0, keepdim=True)
+        rr = (var + 1e-5).rsqrt()
+        xh = (exact - m) * rr
+        top = exact.abs().amax(1, keepdim=True)
+        drel = K * (1 + top * rr)
+        assert_close("mean", mean[:, None], m, K * top)
+        assert_close("rstd", rstd[:, None], rr, rr * (drel + U32))
+        wd, bd = w.double(), b.double()
+        ref = xh * wd + bd
+        a = xh.abs() * wd.abs()
+        assert_close("y", y, ref, wd.abs() * (K * top * rr) + a * drel
+                     + 4 * U32 * (a + bd.abs()) + u * ref.abs())
+        if r is not None:
+            assert torch.equal(s, (x.float() + r.float()).to(dtype))
+        del exact, xh, ref, a
+    x = cut(integers(g, -8, 8, (rows, D + wider), dtype))
+    dy = cut(integers(g, -3, 3, (rows, D + wider), dtype))
+    mean = integers(g, -2, 2, (rows,), F32)
+    rstd = 2.0 ** integers(g, -1, 1, (rows,), F32)
+    xh = (x.double() - mean[:, None]) * rstd[:, None]
+    gd = dy.double() * w.double()
+    c1, c2 = (gd * xh).mean(1, keepdim=True), gd.mean(1, keepdim=True)
+    a1, a2 = (gd * xh).abs().mean(1, keepdim=True), \
+        gd.abs().mean(1, keepdim=True)
+    dx = rstd[:, None] * (gd - c2 - xh * c1)
+    err = K * rstd[:, None] * (gd.abs() + a2 + xh.abs() * a1)
+    for ds in (None, res):
+        got = kla.layernorm_bwd(dy, x, w, mean, rstd, sum_grad=ds)
+        ref = dx if ds is None else dx + ds.double()
+        assert_close("x_grad", got["x_grad"], ref, err + u * ref.abs() + (
+            0 if ds is None else U32 * ds.double().abs()))
+        assert torch.equal(got["weight_grad"].double(),
+                           (dy.double() * xh).sum(0))
+        assert torch.equal(got["bias_grad"].double(), dy.double().sum(0))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("D", [128, 1001, 2048])
 def test_without_weight_or_bias(D, dtype):
