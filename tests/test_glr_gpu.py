@@ -498,6 +498,47 @@ def test_packed_tokens_in_parts(kind, D, dtype, gtype):
 
 
 @pytest.mark.parametrize("dtype,gtype", TYPES)
+@pytest.mark.parametrize("D", [64, 66, 1001])
+@pytest.mark.parametrize("kind", ["random", "one long", "long last",
+                                  "empty between"])
+def test_bad_sequences_of_tokens_in_parts(kind, D, dtype, gtype):
+    """Every second sequence that holds tokens (then the others) is NaN in all
+    that it has: its neighbours, on both sides of every cut, keep their bits,
+    forward and backward."""
+    lens = uneven_lengths(kind)
+    cu, T, N = offsets(lens), sum(lens), len(lens)
+    x, la = normal((T, D), dtype, 77), gates((T, D), gtype, 78)
+    do = normal((T, D), dtype, 79)
+    h0, dhT = normal((N, D), F32, 80), normal((N, D), F32, 81)
+    dcu, nan = cu.cuda(), float("nan")
+    o, hT = kla.glr_fwd(x, la, h0, dcu)
+    g = kla.glr_bwd(o, la, do, dhT, h0, dcu)
+    held = [n for n in range(N) if lens[n]]
+    for first in (0, 1):
+        seqs = torch.zeros(N, dtype=torch.bool)
+        seqs[held[first::2]] = True
+        rows = seqs.repeat_interleave(torch.tensor(lens)).cuda()
+        seqs = seqs.cuda()
+        assert rows.any() and not rows.all()
+        x2, la2, do2, o2, h2, d2 = (v.clone() for v in (x, la, do, o, h0,
+                                                        dhT))
+        for v in (x2, do2, o2):
+            v[rows] = nan
+        h2[seqs], d2[seqs] = nan, nan
+        for gate in (la, la2):
+            oo, hh = kla.glr_fwd(x2, gate, h2, dcu)
+            gg = kla.glr_bwd(o2, gate, do2, d2, h2, dcu)
+            assert torch.equal(oo[~rows], o[~rows])
+            assert torch.equal(hh[~seqs], hT[~seqs])
+            for name in ("x_grad", "log_alpha_grad"):
+                assert torch.equal(gg[name][~rows], g[name][~rows]), name
+                assert gg[name][rows].isnan().all(), name
+            assert torch.equal(gg["h0_grad"][~seqs], g["h0_grad"][~seqs])
+            assert oo[rows].isnan().all() and hh[seqs].isnan().all()
+            la2[rows] = nan
+
+
+@pytest.mark.parametrize("dtype,gtype", TYPES)
 @pytest.mark.parametrize("D", [64, 70, 131])
 def test_many_sequences_of_a_token_beside_a_long_one(D, dtype, gtype):
     """Single tokens of many sequences and a prompt in one call, states in
