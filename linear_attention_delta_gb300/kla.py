@@ -637,6 +637,13 @@ def _exact(name, t, device, dtype, shape):
     return t
 
 
+def _counts(*sizes):
+    """Raises unless the sizes fit the library's 32-bit counts (a larger one
+    would be cut off silently)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size of {max(sizes)} is more than 2^31 - 1")
+
+
 def _workspace(workspace, nbytes, device):
     """(the buffer, its bytes): the caller's, or one of torch's when None."""
     if workspace is None:
@@ -667,6 +674,8 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
         raise ValueError("x must have a last axis of at least one element")
     xs = _input_rows("x", x, dev, dt, shape)
     D = shape[-1]
+    rows = x.numel() // D
+    _counts(rows, D)
     wt, rs = dt, 0
     if weight is not None or bias is not None:
         wt = getattr(bias if weight is None else weight, "dtype", dt)
@@ -695,7 +704,7 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
     st = load_library().kla_layernorm_fwd(
         x.data_ptr(), xs, _addr(residual), rs, _addr(weight), _addr(bias),
         eps, y.data_ptr(), _addr(sum), _addr(mean), _addr(rstd),
-        x.numel() // D, D, DTYPES[dt], DTYPES[wt], _raw_stream(dev))
+        rows, D, DTYPES[dt], DTYPES[wt], _raw_stream(dev))
     if st != KLA_OK:
         raise KlaError("kla_layernorm_fwd", st)
     return y, sum, mean, rstd
@@ -704,6 +713,7 @@ def layernorm_fwd(x, weight=None, bias=None, eps: float = 1e-5,
 @functools.lru_cache(maxsize=256)
 def layernorm_bwd_workspace_size(rows: int, D: int, dtype) -> int:
     """Bytes of device workspace ``layernorm_bwd`` needs."""
+    _counts(rows, D)
     n = ctypes.c_size_t(0)
     st = load_library().kla_layernorm_bwd_workspace_size(
         rows, D, DTYPES[dtype], ctypes.byref(n))
@@ -733,12 +743,13 @@ def layernorm_bwd(y_grad, x, weight, mean, rstd, sum_grad=None,
     shape, dt = x.shape, x.dtype
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must have a last axis of at least one element")
+    D = shape[-1]
+    rows = x.numel() // D
+    _counts(rows, D)
     xs = _input_rows("x", x, dev, dt, shape)
     ys = _input_rows("y_grad", y_grad, dev, dt, shape)
     _exact("mean", mean, dev, torch.float32, shape[:-1])
     _exact("rstd", rstd, dev, torch.float32, shape[:-1])
-    D = shape[-1]
-    rows = x.numel() // D
     wt, ss = dt, 0
     if weight is not None:
         wt = getattr(weight, "dtype", dt)
@@ -785,6 +796,7 @@ def _glr_shape(name, x, cu_seqlens):
         B = cu_seqlens.numel() - 1
     if shape[-1] < 1:
         raise ValueError(f"{name} must have at least one channel")
+    _counts(B, shape[-2], shape[-1])
     return dev, B, shape[-2], shape[-1]
 
 
@@ -886,6 +898,7 @@ def glr_step(x, log_alpha, S, o=None, stream=None):
     shape, dt = x.shape, x.dtype
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError("x must be [N, D]")
+    _counts(*shape)
     if not x.is_contiguous():
         _check("x", x, dev, _IO)
     gt = _glr_gate(log_alpha, dev, shape)

@@ -647,6 +647,20 @@ def test_offsets_past_32_bits():
                   b[1], BF16)
 
 
+def test_refuses_more_than_it_counts():
+    one, n = torch.zeros(1, 1, 1, device="cuda", dtype=BF16), 2 ** 31 + 5
+    for x in (one.expand(n, 1, 1), one.expand(1, n, 1)):
+        for call in (lambda: kla.glr_fwd(x, x), lambda: kla.glr_bwd(x, x, x)):
+            with pytest.raises(ValueError, match="2.31"):
+                call()
+    x = one[0].expand(n, 1)
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="2.31"):
+        kla.glr_fwd(x, x, cu_seqlens=cu)
+    with pytest.raises(ValueError, match="2.31"):
+        kla.glr_step(x, x, one[0].float().expand(n, 1))
+
+
 def test_refusals():
     x, la = normal((2, 9, 64), BF16, 45), gates((2, 9, 64), F32, 46)
     h0 = normal((2, 64), F32, 47)

@@ -434,6 +434,15 @@ def test_weight_gradients_of_more_than_2_30_columns():
         assert (err <= (U16 * 1.01 + 4 * U32) * ref.abs()).all()
 
 
+def test_refuses_more_rows_than_it_counts():
+    x = torch.zeros(1, 1, device="cuda", dtype=BF16).expand(2 ** 31 + 5, 1)
+    with pytest.raises(ValueError, match="2.31"):
+        kla.layernorm_fwd(x)
+    mean = torch.zeros(1, device="cuda").expand(2 ** 31 + 5)
+    with pytest.raises(ValueError, match="2.31"):
+        kla.layernorm_bwd(x, x, None, mean, mean)
+
+
 def test_refusals():
     x, w = normal((4, 64), BF16, 25), normal((64,), BF16, 26)
     _, _, mean, rstd = kla.layernorm_fwd(x, w, w)

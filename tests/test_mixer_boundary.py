@@ -173,6 +173,13 @@ def test_refuses_more_channels_and_sequences_than_it_counts(lib):
             OK if D == most else UNSUPPORTED)
 
 
+def test_binding_refuses_sizes_that_c_would_cut_off():
+    n = 2 ** 31 + 5
+    for rows, D in ((n, 1), (1, n)):
+        with pytest.raises(ValueError, match="2.31"):
+            kla.layernorm_bwd_workspace_size(rows, D, torch.float32)
+
+
 def test_binding_refuses_cpu_tensors():
     x, s = torch.zeros(1, 4, 16), torch.zeros(4, 16)
     for call in (lambda: kla.layernorm_fwd(x),
