@@ -824,9 +824,18 @@ ln_bwd_join_kernel(const float* part, int slices, int D, void* dw, void* db,
     put(db, b);
 }
 
-// Row groups of partial sums that a backward call may write (its workspace);
-// the number of blocks that it launches at most.
-constexpr int kMaxSlices = 608;
+// Rows of partial sums that a backward call may write (its workspace), which
+// is the number of blocks that it launches at most: four an SM of 152, one
+// where a row takes 512 threads or more (their registers leave no room for a
+// second).  Every block's sums are written and read again: blocks beyond 128
+// have 4 rows a group at least (1024 x 2048 8.9 -> 7.9 us, 256 x 2048 and 4096
+// x 2048 the same).
+int most_slices(int rows, int groups, int D, size_t elt) {
+    const int sms = (size_t)D * elt > 8192 ? 152 : 608;
+    const long long four = ((long long)rows + 4 * groups - 1) / (4 * groups);
+    return std::max(1, (int)std::min<long long>({sms, rows,
+                                                 std::max(128ll, four)}));
+}
 
 bool lines_up(const void* p, size_t elt, long long stride, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (elt * vec) == 0 &&
@@ -957,12 +966,8 @@ cudaError_t bwd_ring(const LayerNormBwdArgs& a, float* part, cudaStream_t s) {
         TPR * GROUPS, GROUPS, WIDE, a.dsum ? 3 : 2, sizeof(T), a.D, a.rows,
         TPR * N * kV<T, WIDE> * (int)sizeof(float2));
     if (p.blocks <= 0) return cudaErrorInvalidConfiguration;
-    // every block's partial sums are written and read again: blocks beyond
-    // 128 have 4 rows a group at least (1024 x 2048 8.9 -> 7.9 us, 256 x 2048
-    // and 4096 x 2048 the same)
-    p.blocks = std::min({p.blocks, kMaxSlices,
-                         std::max(128, (int)(((long long)a.rows + 4 * GROUPS -
-                                              1) / (4 * GROUPS)))});
+    p.blocks = std::min(p.blocks,
+                        most_slices(a.rows, GROUPS, a.D, sizeof(T)));
     const cudaError_t e =
         launch_dependent(kernel, dim3(p.blocks), TPR * GROUPS, s, p.bytes, a,
                          p.depth, grads ? part : nullptr);
@@ -1029,8 +1034,8 @@ cudaError_t launch_layernorm(const LayerNormArgs& a, cudaStream_t stream) {
                                : launch_fwd<float>(a, stream);
 }
 
-size_t layernorm_bwd_workspace_bytes(int rows, int D, kla_dtype) {
-    return (size_t)std::max(1, std::min(rows, kMaxSlices)) * 2 * D *
+size_t layernorm_bwd_workspace_bytes(int rows, int D, kla_dtype dtype) {
+    return (size_t)most_slices(rows, 1, D, dtype == KLA_BF16 ? 2 : 4) * 2 * D *
            sizeof(float);
 }
 

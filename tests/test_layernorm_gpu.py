@@ -236,6 +236,25 @@ def test_rings_of_rows(k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [1, 3, 129, 700, 5000])
+def test_workspace_of_the_stated_size_suffices(rows, dtype):
+    """Every width of the rings and of the loops: nothing is written past the
+    workspace, and more of it changes nothing."""
+    for D, _ in RINGS + LOOSE + [(4097, 0), (20001, 0)]:
+        g = torch.Generator(device="cuda").manual_seed(D)
+        x = torch.randn(rows, D, device="cuda", generator=g).to(dtype)
+        mean, rstd = torch.zeros(rows, device="cuda"), \
+            torch.ones(rows, device="cuda")
+        n = kla.layernorm_bwd_workspace_size(rows, D, dtype)
+        ws = torch.full((n + 65536,), 77, dtype=torch.uint8, device="cuda")
+        got = kla.layernorm_bwd(x, x, None, mean, rstd, workspace=ws[:n])
+        assert (ws[n:] == 77).all(), D
+        more = torch.empty(4 * n, dtype=torch.uint8, device="cuda")
+        ref = kla.layernorm_bwd(x, x, None, mean, rstd, workspace=more)
+        assert all(torch.equal(got[k], ref[k]) for k in got), D
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("D", [128, 1001, 2048])
 def test_without_weight_or_bias(D, dtype):
     x, dy = normal((9, D), dtype, 4), normal((9, D), dtype, 5)

@@ -150,6 +150,17 @@ def test_workspace_sizes(lib):
     assert f(1, 64, BF16, None) == INVALID
 
 
+@pytest.mark.parametrize("dtype,elt", [(BF16, 2), (F32, 4)])
+def test_workspace_of_wide_rows_is_a_row_of_sums_a_block(lib, dtype, elt):
+    """A row a block where one block fills an SM of the 152."""
+    n, f = ctypes.c_size_t(0), lib.kla_layernorm_bwd_workspace_size
+    for D in (8192 // elt + 1, 16384, 100000):
+        assert f(1 << 20, D, dtype, ctypes.byref(n)) == OK
+        assert n.value <= 152 * 2 * D * 4
+    assert f(400, 64, dtype, ctypes.byref(n)) == OK
+    assert n.value <= 128 * 2 * 64 * 4
+
+
 def test_glr_refuses_more_tokens_than_it_counts(lib):
     assert glr_fwd(lib, T=0x7fffffff) == UNSUPPORTED
     assert glr_bwd(lib, T=0x7fffffff) == UNSUPPORTED
