@@ -459,21 +459,6 @@ __global__ void __launch_bounds__(kPcThreads)
     }
 }
 
-template <typename K, typename... Args>
-cudaError_t launch_dependent(K kern, unsigned grid, unsigned block,
-                             cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <typename IO>
 cudaError_t launch_chunked_io(const PrecondArgs& a, float* ws,
                               cudaStream_t stream) {
@@ -493,13 +478,11 @@ cudaError_t launch_chunked_io(const PrecondArgs& a, float* ws,
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_dependent(kla_precond_scan_kernel,
-                                     (unsigned)((long)a.B * a.H), kPcDk,
-                                     stream, a, (const float*)sums, bases,
-                                     nchunks);
+                                     dim3((unsigned)((long)a.B * a.H)), kPcDk,
+                                     stream, 0, a, sums, bases, nchunks);
     if (e != cudaSuccess || !items) return e;
-    return launch_dependent(kla_precond_weigh_kernel<IO, false>, items,
-                            kPcThreads, stream, a, (const float*)bases,
-                            nchunks);
+    return launch_dependent(kla_precond_weigh_kernel<IO, false>, dim3(items),
+                            kPcThreads, stream, 0, a, bases, nchunks);
 }
 
 template <int DK>
