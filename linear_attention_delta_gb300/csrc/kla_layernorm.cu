@@ -921,8 +921,10 @@ cudaError_t fwd_width(const LayerNormArgs& a, cudaStream_t s) {
         if (packs <= 1024 * M) return fwd_ring<T, WIDE, 512, 2 * M>(a, s);
         // (1024 threads leave 64 registers: 8192 x 8200 94 instead of 62 us,
         // 2048 x 16384 34 instead of 26)
-        if (WIDE && packs <= 1280) return fwd_ring<T, WIDE, 640, 2>(a, s);
-        if (WIDE && packs <= 2048) return fwd_ring<T, WIDE, 512, 4>(a, s);
+        if constexpr (WIDE) {
+            if (packs <= 1280) return fwd_ring<T, WIDE, 640, 2>(a, s);
+            if (packs <= 2048) return fwd_ring<T, WIDE, 512, 4>(a, s);
+        }
     }
     if (packs <= 32) return fwd_rows<T, V, 32, 1>(a, s);
     if (packs <= 64) return fwd_rows<T, V, 32, 2>(a, s);
@@ -999,10 +1001,12 @@ cudaError_t bwd_width(const LayerNormBwdArgs& a, float* part,
     if (packs <= 1024 * M) return bwd_ring<T, WIDE, 512, 2 * M>(a, part, s);
     // (a thread has the registers for 2 runs up to about 640 threads; 4 runs
     // formed twice take 38 instead of 28 us on 1023 rows of 8200)
-    if (WIDE && packs <= 1280) return bwd_ring<T, WIDE, 640, 2>(a, part, s);
-    if (WIDE && packs <= 1536) return bwd_ring<T, WIDE, 768, 2>(a, part, s);
-    if (WIDE && packs <= 2048)
-        return bwd_ring<T, WIDE, 512, 4, false>(a, part, s);
+    if constexpr (WIDE) {
+        if (packs <= 1280) return bwd_ring<T, WIDE, 640, 2>(a, part, s);
+        if (packs <= 1536) return bwd_ring<T, WIDE, 768, 2>(a, part, s);
+        if (packs <= 2048)
+            return bwd_ring<T, WIDE, 512, 4, false>(a, part, s);
+    }
     return bwd_loop<T>(a, part, s);
 }
 
