@@ -7,13 +7,13 @@
 // to five operations per element of each tensor it reads.
 //
 // Measured (us, share of the copy bandwidth; bf16 with fp32 gates): 4 x 4096
-// x 2048 forward 45 (89 %), backward 76 (91 %); 65536 x 2048, bf16 gates,
+// x 2048 forward 45 (89 %), backward 76.5 (91 %); 65536 x 2048, bf16 gates,
 // forward 141 (85 %), where a step of a team of 12 blocks takes 2.5 us: 1.2 of
 // work on its tile, the rest waiting for the slowest block's map and for the
-// next tile; 16411 x 1024 in 24 packed sequences, forward 27 (55 %); 8191 x
-// 1001 in 9, backward in fp32 48 (51 %): rows that line up on 4 bytes only,
-// copied in pieces by all threads (4 x 4096 x 2047 bf16 forward 56 against 40
-// us for 2048 channels).
+// next tile; 16411 x 1024 in 24 packed sequences of random lengths, forward 30
+// (50 %); 8191 x 1001 in 9, backward in fp32 47.5 (51 %): rows that line up on
+// 4 bytes only, copied in pieces by all threads (4 x 4096 x 2047 with bf16
+// gates, forward, 55 against 38.5 us for 2048 channels).
 //
 // The kernels launch as programmatic dependents: their blocks take their
 // places while the kernel before them on the stream drains, and wait for its
@@ -66,7 +66,7 @@ constexpr int W = 4;             // warps of a block
 // Tokens of a warp, S, and blocks that an SM is to hold, which bounds a
 // thread's registers (3: 168, 2: 255; the decays take 2 per token, each input
 // 1 or 2).  More tokens mean fewer exchanges, more blocks hide them.  Measured
-// (us; 65536 tokens x 2048 forward, 4 x 4096 x 2048 forward with fp32 gates):
+// against each other, before the launches became dependent ones (us; 65536 tokens x 2048 forward, 4 x 4096 x 2048 forward with fp32 gates):
 // bf16 forward 24 and 3 blocks 145, 47.8; 16 and 4 158, 46.4; 28 and 3 140,
 // 48.0; 12 and 5 220, 48.5.  bf16 backward (the second) 16 and 3 blocks 79;
 // 20 and 3 87; 12 and 4 81.  fp32, 16384 x 1000 forward: 20 and 2 blocks 45;
@@ -1029,12 +1029,14 @@ int capacity(int team) {
 // average by what the lengths are, which the host does not know: half a
 // sequence per doubling is expected, and, the less likely the more sequences
 // there are, one with nearly all of the tokens, where only one team has work.
-// A step costs a larger team more (1 + 0.03 t).  Measured (us, whole / in
-// parts; random lengths): 24 sequences of 16411 tokens, 1024 channels, forward
-// 35 / 27, backward 52 / 39; 4 of them, forward 34 / 26; 600 of 32768 x 2048
-// 171 / 155; 64 of 65536 x 64 87 / 14; 1000 of 65536 x 256 209 / 49.  With one
-// long sequence and short ones: 24 of 16411 x 1024 34 / 40 (52 in three parts
-// instead of two, which gain no more on random lengths).
+// A step costs a larger team more (1 + 0.03 t).  How likely one long sequence
+// is, is an assumption, not a measurement.  Measured (GPU us, whole / in parts;
+// four draws of random lengths, one in six sequences empty and one a token): 24
+// sequences of 16411 tokens, 1024 channels, forward 37 to 41 / 28 to 30,
+// backward 52 to 57 / 39 to 42; 4 of them, forward 33 / 25 to 31; 600 of 32768
+// x 2048 162 to 174 / 151 to 163; 64 of 65536 x 64 101 to 108 / 13 to 15; 1000
+// of 65536 x 256 200 to 211 / 47 to 51.  Even lengths: 24 of 16411 x 1024 34 /
+// 25.  One long sequence and single tokens: 41 / 43, backward 68 / 68.
 template <typename T, typename G, Align A, bool BWD, bool PACKED>
 ScanPlan plan_of(long long chains, int tiles, int D, int sequences,
                  int* blocks) {

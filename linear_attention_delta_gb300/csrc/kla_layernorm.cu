@@ -19,11 +19,11 @@
 // kernels at the end, which read them again.
 //
 // Measured on 16384 x 2048 bf16: forward with a residual 46 us (268 MB, 86 %
-// of the copy bandwidth), without 24 us (84 %); backward with the residual's
-// gradient 47.5 us (268 MB, 84 %), without 41 us (74 %).  (With the next row
+// of the copy bandwidth), without 25 us (80 %); backward with the residual's
+// gradient 47.5 us (268 MB, 84 %), without 41 us (72 %).  (With the next row
 // in registers instead of rings: 92 us for the backward.)  What bounds them
 // is issue and the latency of the sums across threads: 16 instructions per
-// element forward (20 with a residual) and 24 backward, at 55 to 60 % of the
+// element forward (20 with a residual) and 22 backward, at 54 to 58 % of the
 // issue slots; fp32, with half the elements per byte, reaches 89 and 90 %.
 //
 // All kernels launch as programmatic dependents: their blocks take their
@@ -699,7 +699,9 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2* red) {
 }
 
 // Any D, strides and alignment: one block per row, which it reads three
-// times (from L1 or L2 after the first).
+// times (from L1 or L2 after the first), element by element.  For the rows
+// that no other kernel takes: 2048 x 8191 bf16 in 39 us (floor 9.9), in the
+// backward below 64 (floor 14.9).
 template <typename T>
 __global__ void __launch_bounds__(kLoopThreads)
 ln_fwd_loop_kernel(LayerNormArgs a) {
