@@ -98,7 +98,8 @@ __device__ float g_selftest_glr[3 * CH];         // the self-test's tensors
 // a decay's error is multiplied by as much, 1 + l + l^2 / 2 + l^3 / 6 (|l| <=
 // 1/64: the rest of the series is below 2^-28, so that the last addition
 // rounds correctly nearly always).  Elsewhere 2^(l log2 e) by the hardware's
-// approximation (about 2 units of 2^-24 up to l = -1, 8 at l = -8).
+// approximation (about 2 units of 2^-24 up to l = -1, 8 at l = -8, |l| further
+// out: the rounding of l log2 e).
 __device__ __forceinline__ float2 decay(float2 l) {
     float2 p = fma2(l, both(1.f / 6), both(0.5f));
     p = fma2(l, p, both(1.f));
