@@ -33,9 +33,10 @@
  *     next synchronisation, as with any CUDA call; bounded device-side waits
  *     that give up are reported by kla_device_status().
  *   - No C++ exception crosses this interface.
- *   - Tensors are contiguous and row-major (the layer norm and the gated
- *     linear recurrence also take strided inputs, see there).  Pointers to bf16 data must be
- *     2-byte aligned and pointers to fp32 data 4-byte aligned; the tensor-core
+ *   - Tensors are contiguous and row-major (the layer norm, the gated linear
+ *     recurrence, linear attention with a decay for each head and the log
+ *     probabilities also take strided inputs, see there).  Pointers to bf16
+ *     data must be 2-byte aligned and pointers to fp32 data 4-byte aligned; the tensor-core
  *     forward path additionally wants 16-byte aligned q, k, v, o (it falls
  *     back to the CUDA-core path otherwise, see kla_chunk_fwd_ex).
  */
@@ -706,6 +707,136 @@ KLA_API kla_status kla_glr_step(const void* x, long long x_stride,
                                 float* S, void* o, int N, int D,
                                 kla_dtype dtype, kla_dtype gate_dtype,
                                 kla_stream_t stream);
+
+/*
+ * Linear attention with a decay for each head: the recurrence above without
+ * its residual, written with a fixed decay.  Per sequence and head, from
+ * S_0 = h0:
+ *
+ *     S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t
+ *
+ * (no 1/sqrt(dk); a caller wanting a scale pre-scales q.)
+ *
+ * kla_linattn_fwd -- q, k [B, T, H, dk], v [B, T, H, dv] of type `dtype`,
+ * each with strides (elements, >= 0; 0 repeats) *_sb between sequences, *_st
+ * between tokens and *_sh between heads; a head's elements are adjacent.
+ * log_decay [H] fp32, shared by all sequences; o [B, T, H, dv] contiguous;
+ * h0 [B, H, dk, dv] fp32 or null (zeros); hT the same or null (not written).
+ * hT may be h0 itself (else it may not overlap any input).  T = 0: hT is h0.
+ * log_decay is meant to be <= 0; -inf forgets (o_t = (q_t k_t) v_t), 0 is
+ * linear attention without decay, positive values grow as written while
+ * they stay in range.  The decays are constants of the model: there is no
+ * gradient for them.  1 <= dk, dv <= 256.
+ * Sums and states are held in fp32.  A value that is not finite makes its own
+ * token's and later outputs not finite (which of inf and NaN is not fixed)
+ * and reaches no earlier token, sequence or head.
+ * workspace: kla_linattn_workspace_size bytes (0 for many sequences or short
+ * ones, then it may be null), 16-byte aligned: the states between the parts
+ * of long sequences.  Its contents on entry do not matter.  Results are the
+ * same bits on every run.
+ * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, a null or
+ * misaligned pointer, overlapping buffers, a workspace too small),
+ * KLA_ERR_UNSUPPORTED_SHAPE (dk or dv outside the range, T > 2^31 - 4097,
+ * B H > 2^24), KLA_ERR_CUDA.
+ */
+KLA_API kla_status kla_linattn_workspace_size(int B, int T, int H, int dk,
+                                              int dv, kla_dtype dtype,
+                                              int backward, size_t* bytes);
+KLA_API kla_status kla_linattn_fwd(
+    const void* q, long long q_sb, long long q_st, long long q_sh,
+    const void* k, long long k_sb, long long k_st, long long k_sh,
+    const void* v, long long v_sb, long long v_st, long long v_sh,
+    const float* log_decay, const float* h0, void* o, float* hT, int B, int T,
+    int H, int dk, int dv, kla_dtype dtype, void* workspace,
+    size_t workspace_bytes, kla_stream_t stream);
+
+/*
+ * kla_linattn_bwd -- gradients given o_grad = dL/do ([B, T, H, dv] with
+ * strides) and optionally hT_grad = dL/dhT (null: zeros).  With D_t the
+ * gradient of S_t:
+ *
+ *     D_t = exp(log_decay_h) D_{t+1} + q_t o_grad_t^T   (last: + hT_grad)
+ *     q_grad_t = S_t o_grad_t,  k_grad_t = D_t v_t,  v_grad_t = D_t^T k_t,
+ *     h0_grad = exp(log_decay_h) D_1                    (T = 0: hT_grad)
+ *
+ * The states are formed again from k, v and h0.  q_grad, k_grad, v_grad are
+ * contiguous and of type `dtype`; h0_grad [B, H, dk, dv] fp32 or null.  The
+ * outputs may not overlap any input nor each other.  workspace:
+ * kla_linattn_workspace_size bytes with backward = 1.
+ * Errors: as kla_linattn_fwd.
+ */
+KLA_API kla_status kla_linattn_bwd(
+    const void* q, long long q_sb, long long q_st, long long q_sh,
+    const void* k, long long k_sb, long long k_st, long long k_sh,
+    const void* v, long long v_sb, long long v_st, long long v_sh,
+    const float* log_decay, const float* h0, const void* o_grad,
+    long long g_sb, long long g_st, long long g_sh, const float* hT_grad,
+    void* q_grad, void* k_grad, void* v_grad, float* h0_grad, int B, int T,
+    int H, int dk, int dv, kla_dtype dtype, void* workspace,
+    size_t workspace_bytes, kla_stream_t stream);
+
+/*
+ * kla_linattn_step -- one token for N sequences: S [N, H, dk, dv] fp32
+ * (contiguous) is updated in place and read out.  q, k [N, H, dk], v
+ * [N, H, dv] with strides *_sn between sequences and *_sh between heads;
+ * o [N, H, dv] contiguous.  o may not overlap any other buffer, nor S an
+ * input.  Errors: as kla_linattn_fwd.  No workspace.
+ */
+KLA_API kla_status kla_linattn_step(
+    const void* q, long long q_sn, long long q_sh, const void* k,
+    long long k_sn, long long k_sh, const void* v, long long v_sn,
+    long long v_sh, const float* log_decay, float* S, void* o, int N, int H,
+    int dk, int dv, kla_dtype dtype, kla_stream_t stream);
+
+/*
+ * Log probabilities of given tokens.  Per row of logits x [V]:
+ *
+ *     z = scale x,  lse = log sum_j exp(z_j),  p_j = exp(z_j - lse)
+ *     logp = z_token - lse,   entropy = -sum_j p_j log p_j
+ *     top: the `top` largest logits' log probabilities and ids, from the
+ *     largest down, equal ones by rising id
+ *
+ * kla_logprob_fwd -- logits [N, V] of type `dtype`, `logits_stride` elements
+ * between rows (>= 0); tokens [N] int64 (device); logp [N] fp32; entropy,
+ * lse [N] fp32 or null; top_logp [N, top] fp32 and top_ids [N, top] int64
+ * (null with top = 0).  A token outside 0 .. V - 1 (padding, by custom -1 or
+ * -100) has logp 0.  scale (1 / temperature): finite and > 0.  -inf masks a
+ * logit (its p is 0); a row masked throughout has lse and logp -inf, entropy
+ * 0, and its top ids are 0, 1, ...  NaN or +inf in a row makes its lse, logp
+ * and entropy NaN (NaN ranks above +inf among the top).  All sums in fp32.
+ * The outputs may not overlap logits, tokens or each other.
+ * Errors: KLA_ERR_INVALID_ARG (N < 0, V < 1, top < 0 or > V, a negative
+ * stride, a bad scale, a null or misaligned pointer, overlapping buffers),
+ * KLA_ERR_UNSUPPORTED_SHAPE (top > 128, V > 2^31 - 4097), KLA_ERR_CUDA.
+ * No workspace.
+ */
+KLA_API kla_status kla_logprob_fwd(
+    const void* logits, long long logits_stride, const long long* tokens,
+    float scale, float* logp, float* entropy, float* lse, float* top_logp,
+    long long* top_ids, int N, int V, int top, kla_dtype dtype,
+    kla_stream_t stream);
+
+/*
+ * kla_logprob_bwd -- gradient of a loss with respect to the logits, given
+ * logp_grad = dL/dlogp and entropy_grad = dL/dentropy ([N] fp32 each, null:
+ * zeros) and the forward's lse and entropy (entropy may be null without
+ * entropy_grad):
+ *
+ *     dL/dz_j = logp_grad ([j = token] - p_j)
+ *               - entropy_grad p_j (log p_j + entropy)
+ *     logits_grad_j = scale dL/dz_j
+ *
+ * A row without a token (outside 0 .. V - 1) has no logp term; a row masked
+ * throughout has gradient 0.  logits_grad [N, V] contiguous, of type `dtype`;
+ * it may be logits itself (same address, logits_stride = V), else it may not
+ * overlap any input.  The top values carry no gradient.
+ * Errors: as kla_logprob_fwd.
+ */
+KLA_API kla_status kla_logprob_bwd(
+    const void* logits, long long logits_stride, const long long* tokens,
+    float scale, const float* lse, const float* entropy,
+    const float* logp_grad, const float* entropy_grad, void* logits_grad,
+    int N, int V, kla_dtype dtype, kla_stream_t stream);
 
 /*
  * kla_device_status -- synchronises `stream`, then reads and clears the

@@ -46,5 +46,24 @@ bool any_overlap(const Span (&ins)[NI], const Span (&outs)[NO]) {
     return false;
 }
 
+inline bool valid(kla_dtype t) { return t == KLA_F32 || t == KLA_BF16; }
+inline size_t size_of(kla_dtype t) { return t == KLA_BF16 ? 2 : 4; }
+
+// A pointer that may be null, aligned to its element.
+inline bool ok_or_null(const void* p, size_t n) { return !p || aligned(p, n); }
+inline bool given(const void* p, size_t n) { return p && aligned(p, n); }
+
+// Bytes from the first to the last element of `rows` rows of D, `stride`
+// apart (in elements of `elt` bytes).
+inline size_t row_bytes(int rows, int D, long long stride, size_t elt) {
+    return rows ? ((size_t)(rows - 1) * (size_t)stride + D) * elt : 0;
+}
+
+inline Span span(const void* p, size_t n) { return {p, p ? n : 0}; }
+
+// The kernels count columns, tokens and packed sequences in 32 bits; a thread
+// may step past the last one by a block's or a tile's worth.
+constexpr int kMaxCount = 0x7fffffff - 4096;
+
 }  // namespace api
 }  // namespace kla

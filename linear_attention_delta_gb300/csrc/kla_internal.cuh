@@ -191,6 +191,70 @@ struct GlrArgs {
     kla_dtype dtype, gdtype;
 };
 
+// A [B, T, H, d] tensor read through strides (elements), its last axis
+// adjacent.
+struct Heads {
+    const void* p;
+    long long sb, st, sh;
+};
+
+// One pass of decayed linear attention over B x H sequences of T tokens:
+//   o_r = sum_{s <= r} w^(r - s) (q_r k_s) v_s + w^(r + e) S0^T q_r,
+//   ST  = w^T S0 + sum_s w^(T - e - s) k_s v_s^T,       w = exp(log_decay[h]),
+// r, s counting tokens from the first (e = 1), or with `reverse` from the
+// last (e = 0).  The forward is one such pass, the backward is three.
+struct LinAttnJob {
+    Heads q, k, v;               // widths dk, dk, dv
+    void* o;                     // [B, T, H, dv] contiguous
+    const float* S0;             // null: zeros
+    float* ST;                   // null: not wanted; may be S0
+    int s_r, s_c;                // strides of the states' rows and columns
+    int dk, dv;
+    bool reverse;
+};
+struct LinAttnArgs {
+    LinAttnJob job[3];
+    int jobs;
+    const float* log_decay;      // [H]
+    int B, T, H;
+    kla_dtype dtype;
+};
+struct LinAttnStepArgs {
+    Heads q, k, v;               // sb: between sequences (st unused)
+    const float* log_decay;
+    float* S;                    // [N, H, dk, dv], in place
+    void* o;                     // [N, H, dv]
+    int N, H, dk, dv;
+    kla_dtype dtype;
+};
+
+struct LogprobArgs {
+    const void* logits;          // [N, V]
+    long long stride;            // elements between rows
+    const long long* tokens;     // [N]
+    float scale;
+    float* logp;                 // [N]
+    float* entropy;              // [N] or null
+    float* lse;                  // [N] or null
+    float* top_logp;             // [N, top] or null
+    long long* top_ids;          // [N, top] or null
+    int N, V, top;
+    kla_dtype dtype;
+};
+struct LogprobBwdArgs {
+    const void* logits;
+    long long stride;
+    const long long* tokens;
+    float scale;
+    const float* lse;
+    const float* entropy;        // null without entropy_grad
+    const float* logp_grad;      // or null
+    const float* entropy_grad;   // or null
+    void* logits_grad;           // [N, V] contiguous
+    int N, V;
+    kla_dtype dtype;
+};
+
 // Each returns cudaSuccess or the launch error.  Shapes are validated by the
 // caller (kla_api.cu); a launcher returning cudaErrorInvalidValue means the
 // shape has no instantiation.
@@ -271,6 +335,18 @@ cudaError_t launch_glr_step(const void* x, long long x_stride,
                             const void* la, long long la_stride, float* S,
                             void* o, int N, int D, kla_dtype dtype,
                             kla_dtype gdtype, cudaStream_t stream);
+// Linear attention with a decay for each head (B, H, T > 0), its workspace
+// (states between the parts of a sequence; 0 where none is cut) and one token
+// (N, H > 0).
+constexpr int kLinAttnMaxWidth = 256;
+size_t linattn_workspace_bytes(const LinAttnArgs& a);
+cudaError_t launch_linattn(const LinAttnArgs& a, void* workspace,
+                           cudaStream_t stream);
+cudaError_t launch_linattn_step(const LinAttnStepArgs& a, cudaStream_t stream);
+// Log probabilities of given tokens (N > 0).
+constexpr int kLogprobMaxTop = 128;
+cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream);
+cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, cudaStream_t stream);
 // SM count of the current device (cached per device).
 int device_sm_count();
 

@@ -9,29 +9,6 @@
 
 using namespace kla::api;
 
-namespace {
-
-bool valid(kla_dtype t) { return t == KLA_F32 || t == KLA_BF16; }
-size_t size_of(kla_dtype t) { return t == KLA_BF16 ? 2 : 4; }
-
-// A pointer that may be null, aligned to its element.
-bool ok_or_null(const void* p, size_t n) { return !p || aligned(p, n); }
-bool given(const void* p, size_t n) { return p && aligned(p, n); }
-
-// Bytes from the first to the last element of `rows` rows of D, `stride`
-// apart (in elements of `elt` bytes).
-size_t row_bytes(int rows, int D, long long stride, size_t elt) {
-    return rows ? ((size_t)(rows - 1) * (size_t)stride + D) * elt : 0;
-}
-
-Span span(const void* p, size_t n) { return {p, p ? n : 0}; }
-
-// The kernels count columns, tokens and packed sequences in 32 bits; a thread
-// may step past the last one by a block's or a tile's worth.
-constexpr int kMaxCount = 0x7fffffff - 4096;
-
-}  // namespace
-
 extern "C" kla_status kla_layernorm_fwd(
     const void* x, long long x_stride, const void* residual,
     long long residual_stride, const void* weight, const void* bias,

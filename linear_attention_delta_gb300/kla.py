@@ -89,6 +89,21 @@ SIGNATURES = {
                          _FP, _VP, _VP, _FP, _VP, _I, _I, _I, _I, _I, _VP]),
     "kla_glr_step": (_I, [_VP, _LL, _VP, _LL, _FP, _VP, _I, _I, _I, _I,
                           _VP]),
+    "kla_linattn_workspace_size": (
+        _I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "kla_linattn_fwd": (_I, [*3 * [_VP, _LL, _LL, _LL], _FP, _FP, _VP, _FP,
+                             _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
+                             _VP]),
+    "kla_linattn_bwd": (_I, [*3 * [_VP, _LL, _LL, _LL], _FP, _FP,
+                             _VP, _LL, _LL, _LL, _FP, _VP, _VP, _VP, _FP,
+                             _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
+                             _VP]),
+    "kla_linattn_step": (_I, [*3 * [_VP, _LL, _LL], _FP, _FP, _VP,
+                              _I, _I, _I, _I, _I, _VP]),
+    "kla_logprob_fwd": (_I, [_VP, _LL, _VP, _F, _FP, _FP, _FP, _FP, _VP,
+                             _I, _I, _I, _I, _VP]),
+    "kla_logprob_bwd": (_I, [_VP, _LL, _VP, _F, _FP, _FP, _FP, _FP, _VP,
+                             _I, _I, _I, _VP]),
     "kla_device_status": (_I, [_VP]),
     "kla_selftest_wait_timeout": (_I, [_VP]),
     "kla_selftest_glr_timeout": (_I, [_VP]),
@@ -914,6 +929,230 @@ def glr_step(x, log_alpha, S, o=None, stream=None):
     if st != KLA_OK:
         raise KlaError("kla_glr_step", st)
     return o
+
+
+def _head_inputs(names, tensors, shapes, device, dtype):
+    """Pointer and strides of each [..., H, d] input, checked."""
+    out = []
+    for name, t, shape in zip(names, tensors, shapes):
+        if not _plain(t, device, dtype, shape):
+            _check(name, t, device, (dtype,), shape)
+        out += [t.data_ptr(), *t.stride()[:-1]]
+    return out
+
+
+def _linattn_shape(q, v, ndim):
+    """(device, dtype, sizes before the width, dk, dv) of a call."""
+    dev = _device_of("q", q)
+    if q.ndim != ndim or not isinstance(v, torch.Tensor) or v.ndim != ndim:
+        raise ValueError("q, k and v must be "
+                         + ("[B, T, H, d]" if ndim == 4 else "[N, H, d]"))
+    dk, dv = q.shape[-1], v.shape[-1]
+    if dk < 1 or dv < 1:
+        raise ValueError("q, k and v must be at least one wide")
+    _counts(*q.shape, dv)
+    return dev, q.dtype, q.shape[:-1], dk, dv
+
+
+@functools.lru_cache(maxsize=256)
+def linattn_workspace_size(B: int, T: int, H: int, dk: int, dv: int, dtype,
+                           backward: bool = False) -> int:
+    """Bytes of device workspace ``linattn_fwd`` (or ``linattn_bwd``) needs."""
+    _counts(B, T, H, dk, dv)
+    n = ctypes.c_size_t(0)
+    st = load_library().kla_linattn_workspace_size(
+        B, T, H, dk, dv, DTYPES[dtype], int(backward), ctypes.byref(n))
+    if st != KLA_OK:
+        raise KlaError("kla_linattn_workspace_size", st)
+    return n.value
+
+
+def linattn_fwd(q, k, v, log_decay, h0=None, o=None, hT=None,
+                want_state: bool = True, workspace=None, stream=None):
+    """Linear attention with a decay for each head (``kla_linattn_fwd``): per
+    sequence and head S_t = exp(log_decay) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t.
+
+    q, k [B, T, H, dk], v [B, T, H, dv] (fp32 or bf16, one dtype; any strides
+    with the last axis adjacent, so slices of a fused projection and
+    transposed [B, H, T, d] tensors will do), log_decay [H] fp32, h0
+    [B, H, dk, dv] fp32 or None (zeros).  Returns (o, hT): o [B, T, H, dv]
+    contiguous, hT the last states (None unless ``want_state``).  ``o`` /
+    ``hT`` may be passed preallocated (``hT`` may be ``h0``).  ``workspace``:
+    a device uint8 tensor of at least ``linattn_workspace_size`` bytes,
+    allocated here when None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linattn_fwd(q, k, v, log_decay, h0, o, hT, want_state,
+                               workspace)
+    dev, dt, (B, T, H), dk, dv = _linattn_shape(q, v, 4)
+    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, (B, T, H, dv)),
+                       dev, dt)
+    _exact("log_decay", log_decay, dev, torch.float32, (H,))
+    if h0 is not None:
+        _exact("h0", h0, dev, torch.float32, (B, H, dk, dv))
+    if o is None:
+        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+    else:
+        _exact("o", o, dev, dt, (B, T, H, dv))
+    if hT is not None:
+        _exact("hT", hT, dev, torch.float32, (B, H, dk, dv))
+    elif want_state:
+        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    nbytes = linattn_workspace_size(B, T, H, dk, dv, dt)
+    if nbytes or workspace is not None:
+        workspace, nbytes = _workspace(workspace, nbytes, dev)
+    st = load_library().kla_linattn_fwd(
+        *ins, log_decay.data_ptr(), _addr(h0), o.data_ptr(), _addr(hT),
+        B, T, H, dk, dv, DTYPES[dt], _addr(workspace), nbytes,
+        _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_linattn_fwd", st)
+    return o, hT
+
+
+def linattn_bwd(q, k, v, log_decay, o_grad, hT_grad=None, h0=None,
+                want_h0_grad: bool = True, workspace=None, stream=None):
+    """Backward pass of ``linattn_fwd`` (``kla_linattn_bwd``): gradients given
+    dL/do (``o_grad``, like o, any strides) and dL/dhT (``hT_grad``, like h0,
+    or None); the other arguments are what the forward took.  Returns a dict
+    with q_grad, k_grad, v_grad (q's dtype, contiguous) and h0_grad (fp32;
+    None unless ``want_h0_grad``).  The decays have no gradient.
+    ``workspace``: as for the forward, sized with ``backward=True``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linattn_bwd(q, k, v, log_decay, o_grad, hT_grad, h0,
+                               want_h0_grad, workspace)
+    dev, dt, (B, T, H), dk, dv = _linattn_shape(q, v, 4)
+    vs = (B, T, H, dv)
+    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, vs), dev, dt)
+    do = _head_inputs(("o_grad",), (o_grad,), (vs,), dev, dt)
+    _exact("log_decay", log_decay, dev, torch.float32, (H,))
+    for name, t in (("h0", h0), ("hT_grad", hT_grad)):
+        if t is not None:
+            _exact(name, t, dev, torch.float32, (B, H, dk, dv))
+    dq = torch.empty((B, T, H, dk), dtype=dt, device=dev)
+    dkey = torch.empty_like(dq)
+    dval = torch.empty(vs, dtype=dt, device=dev)
+    dh0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) \
+        if want_h0_grad else None
+    nbytes = linattn_workspace_size(B, T, H, dk, dv, dt, True)
+    if nbytes or workspace is not None:
+        workspace, nbytes = _workspace(workspace, nbytes, dev)
+    st = load_library().kla_linattn_bwd(
+        *ins, log_decay.data_ptr(), _addr(h0), *do, _addr(hT_grad),
+        dq.data_ptr(), dkey.data_ptr(), dval.data_ptr(), _addr(dh0),
+        B, T, H, dk, dv, DTYPES[dt], _addr(workspace), nbytes,
+        _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_linattn_bwd", st)
+    return dict(q_grad=dq, k_grad=dkey, v_grad=dval, h0_grad=dh0)
+
+
+def linattn_step(q, k, v, log_decay, S, o=None, stream=None):
+    """One token of linear attention with a decay for each head for N
+    sequences (``kla_linattn_step``): S [N, H, dk, dv] fp32 becomes
+    exp(log_decay) S + k v^T in place; q, k [N, H, dk], v [N, H, dv] (fp32 or
+    bf16, one dtype, any strides with the last axis adjacent).  Returns
+    o [N, H, dv] = S^T q of the new states."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linattn_step(q, k, v, log_decay, S, o)
+    dev, dt, (N, H), dk, dv = _linattn_shape(q, v, 3)
+    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, (N, H, dv)), dev,
+                       dt)
+    _exact("log_decay", log_decay, dev, torch.float32, (H,))
+    _exact("S", S, dev, torch.float32, (N, H, dk, dv))
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=dt, device=dev)
+    else:
+        _exact("o", o, dev, dt, (N, H, dv))
+    st = load_library().kla_linattn_step(
+        *ins, log_decay.data_ptr(), S.data_ptr(), o.data_ptr(), N, H, dk, dv,
+        DTYPES[dt], _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_linattn_step", st)
+    return o
+
+
+def _logit_rows(logits):
+    """(device, elements between rows, leading shape, rows, V) of logits."""
+    dev = _device_of("logits", logits)
+    shape = logits.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("logits must have a last axis of at least one "
+                         "element")
+    stride = _input_rows("logits", logits, dev, logits.dtype, shape)
+    V = shape[-1]
+    N = logits.numel() // V
+    _counts(N, V)
+    return dev, stride, shape[:-1], N, V
+
+
+def logprob_fwd(logits, tokens, top: int = 0, scale: float = 1.0,
+                stream=None):
+    """Log probabilities of given tokens (``kla_logprob_fwd``) under
+    softmax(scale * logits), with the rows' entropies and the ``top`` likeliest
+    alternatives.
+
+    logits [..., V] (fp32 or bf16; rows evenly spaced, so a slice of a padded
+    tensor will do), tokens [...] int64; a token outside 0 .. V - 1 (padding)
+    has log probability 0.  Returns (logp, entropy, lse, top_logp, top_ids):
+    the first three [...] fp32 (lse: log of the sum of exp(scale * logits)),
+    the last two [..., top] fp32 and int64 (None with ``top`` 0), from the
+    likeliest down, equal ones by rising id."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return logprob_fwd(logits, tokens, top, scale)
+    dev, stride, lead, N, V = _logit_rows(logits)
+    _exact("tokens", tokens, dev, torch.int64, lead)
+    _counts(top)
+    out = torch.empty((3, *lead), dtype=torch.float32, device=dev)
+    logp, entropy, lse = out.unbind(0)
+    top_logp = top_ids = None
+    if top > 0:
+        top_logp = torch.empty((*lead, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((*lead, top), dtype=torch.int64, device=dev)
+    st = load_library().kla_logprob_fwd(
+        logits.data_ptr(), stride, tokens.data_ptr(), scale, logp.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), _addr(top_logp), _addr(top_ids),
+        N, V, top, DTYPES[logits.dtype], _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_logprob_fwd", st)
+    return logp, entropy, lse, top_logp, top_ids
+
+
+def logprob_bwd(logits, tokens, lse, entropy=None, logp_grad=None,
+                entropy_grad=None, scale: float = 1.0, out=None, stream=None):
+    """Gradient of the logits (``kla_logprob_bwd``) given those of logp and of
+    the entropy ([...] fp32, None: zeros); lse and entropy are what
+    ``logprob_fwd`` returned (entropy is needed only with ``entropy_grad``).
+    Returns the gradient in logits' dtype, contiguous; ``out`` may be passed
+    preallocated, and may be (contiguous) ``logits`` itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return logprob_bwd(logits, tokens, lse, entropy, logp_grad,
+                               entropy_grad, scale, out)
+    dev, stride, lead, N, V = _logit_rows(logits)
+    _exact("tokens", tokens, dev, torch.int64, lead)
+    _exact("lse", lse, dev, torch.float32, lead)
+    for name, t in (("entropy", entropy), ("logp_grad", logp_grad),
+                    ("entropy_grad", entropy_grad)):
+        if t is not None:
+            _exact(name, t, dev, torch.float32, lead)
+    if entropy_grad is not None and entropy is None:
+        raise ValueError("entropy_grad needs the forward's entropy")
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    else:
+        _exact("out", out, dev, logits.dtype, logits.shape)
+    st = load_library().kla_logprob_bwd(
+        logits.data_ptr(), stride, tokens.data_ptr(), scale, lse.data_ptr(),
+        _addr(entropy), _addr(logp_grad), _addr(entropy_grad),
+        out.data_ptr(), N, V, DTYPES[logits.dtype], _raw_stream(dev))
+    if st != KLA_OK:
+        raise KlaError("kla_logprob_bwd", st)
+    return out
 
 
 def device_status(stream=None) -> int:

@@ -1,4 +1,5 @@
-"""fp64 NumPy oracle of layer norm and the gated linear recurrence.
+"""fp64 NumPy oracle of layer norm, the gated linear recurrence, linear
+attention with a decay for each head and token log probabilities.
 
 Plain loops over tokens, no code shared with the CUDA library.  The
 ``*_bound`` functions run the same recurrences on absolute values and return
@@ -118,3 +119,79 @@ def glr_bwd_bound(o, log_alpha, o_grad, hT_grad=None, h0=None, cu=None, k=8):
     e, ea, e0 = glr_bwd(ab(o), log_alpha, k * U32 * mag + 1e-30, None,
                         ab(h0), cu)
     return e, ea + k * U32 * da, e0 + k * U32 * d0
+
+
+def la_fwd(q, k, v, log_decay, h0=None):
+    """(o, hT) of S_t = exp(a_h) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t; q, k
+    [B, T, H, dk], v [B, T, H, dv]."""
+    q, k, v, a = f64(q), f64(k), f64(v), f64(log_decay)
+    B, T, H, dk = q.shape
+    S = np.zeros((B, H, dk, v.shape[-1])) if h0 is None else f64(h0).copy()
+    o = np.zeros(v.shape)
+    decay = np.exp(a)[:, None, None]
+    for t in range(T):
+        S = decay * S + k[:, t, :, :, None] * v[:, t, :, None, :]
+        o[:, t] = np.einsum("bhd,bhde->bhe", q[:, t], S)
+    return o, S
+
+
+def la_bwd(q, k, v, log_decay, o_grad, hT_grad=None, h0=None):
+    """(dq, dk, dv, dh0)."""
+    q, k, v, a, g = (f64(x) for x in (q, k, v, log_decay, o_grad))
+    B, T, H, dk = q.shape
+    zero = np.zeros((B, H, dk, v.shape[-1]))
+    S = zero if h0 is None else f64(h0)
+    D = zero if hT_grad is None else f64(hT_grad)
+    dq, dkey, dval = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    decay = np.exp(a)[:, None, None]
+    for t in range(T):
+        S = decay * S + k[:, t, :, :, None] * v[:, t, :, None, :]
+        dq[:, t] = np.einsum("bhde,bhe->bhd", S, g[:, t])
+    for t in range(T - 1, -1, -1):
+        D = D + q[:, t, :, :, None] * g[:, t, :, None, :]
+        dkey[:, t] = np.einsum("bhde,bhe->bhd", D, v[:, t])
+        dval[:, t] = np.einsum("bhde,bhd->bhe", D, k[:, t])
+        D = decay * D
+    return dq, dkey, dval, D
+
+
+def lp_fwd(logits, tokens, top=0, scale=1.0):
+    """(logp, entropy, lse, top_logp, top_ids) of rows [N, V] without NaN or
+    +inf."""
+    x, tokens = f64(logits), np.asarray(tokens.cpu())
+    z = scale * x
+    N, V = z.shape
+    m = z.max(1, keepdims=True)
+    none = np.isneginf(m[:, 0])
+    with np.errstate(invalid="ignore", divide="ignore"):
+        lse = (m + np.log(np.exp(z - m).sum(1, keepdims=True)))[:, 0]
+        lse = np.where(none, -np.inf, lse)
+        lp = z - lse[:, None]
+        p = np.where(none[:, None], 0.0, np.exp(lp))
+        ent = -np.where(p > 0, p * lp, 0.0).sum(1)
+    lp = np.where(none[:, None], -np.inf, lp)
+    valid = (tokens >= 0) & (tokens < V)
+    logp = np.where(valid, lp[np.arange(N), np.where(valid, tokens, 0)], 0.0)
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :top]
+    return logp, ent, lse, np.take_along_axis(lp, ids, 1), ids
+
+
+def lp_bwd(logits, tokens, lse, entropy, logp_grad, entropy_grad=None,
+           scale=1.0):
+    """dL/dlogits with the given lse and entropy."""
+    z, lse, tokens = scale * f64(logits), f64(lse), np.asarray(tokens.cpu())
+    N, V = z.shape
+    none = np.isneginf(lse)
+    valid = (tokens >= 0) & (tokens < V) & ~none
+    with np.errstate(invalid="ignore"):
+        lp = z - lse[:, None]
+    p = np.where(none[:, None], 0.0, np.exp(lp))
+    g = np.zeros(N) if logp_grad is None else np.where(valid, f64(logp_grad),
+                                                       0.0)
+    d = -g[:, None] * p
+    d[np.arange(N)[valid], tokens[valid]] += g[valid]
+    if entropy_grad is not None:
+        with np.errstate(invalid="ignore"):
+            t = np.where(p > 0, p * (lp + f64(entropy)[:, None]), 0.0)
+        d = d - f64(entropy_grad)[:, None] * t
+    return scale * d

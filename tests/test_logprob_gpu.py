@@ -1,0 +1,280 @@
+"""Log probabilities of given tokens, entropies, alternatives and their
+gradient on the GPU against the fp64 oracle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_delta_gb300 import kla
+from oracle import mixer
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+U32, U16 = mixer.U32, mixer.U16
+
+
+def rows(N, V, dtype, seed=0, masked=0.0):
+    gen = torch.Generator().manual_seed(seed + V)
+    x = torch.randn(N, V, generator=gen) * 3 * torch.exp(
+        0.7 * torch.randn(N, 1, generator=gen)) + 2
+    if masked:
+        x[torch.rand(N, V, generator=gen) < masked] = -math.inf
+        x[:, V // 2] = 1.0
+    tokens = torch.randint(0, V, (N,), generator=gen)
+    return x.to(dtype).cuda(), tokens.cuda()
+
+
+def check_fwd(x, tokens, out, top=0, scale=1.0):
+    scale32 = float(np.float32(scale))
+    lp, ent, lse, tlp, ids = mixer.lp_fwd(x, tokens, top, scale32)
+    V = x.shape[1]
+    z = np.abs(scale32 * mixer.f64(x))
+    m = np.where(np.isfinite(z), z, 0).max(1)
+    # sums: a thread's terms and the joins; exp and its argument (a rounding
+    # of a difference of up to 104, after which exp is 0); every rounding of a
+    # logit or a logarithm of up to m + 12
+    s = (V / 128 + 64 + 104) * U32
+    base = s + 4 * U32 * (m + math.log(V) + 1)
+    logp, entropy, l, tl, ti = out
+    for got, want in ((logp, lp), (l, lse)):
+        got = mixer.f64(got)
+        inf = np.isinf(want)
+        assert (got[inf] == want[inf]).all()
+        with np.errstate(invalid="ignore"):
+            off = np.where(inf, 0, np.abs(got - want))
+            assert (off <= base + 4 * U32 * np.where(inf, 0, np.abs(want))
+                    ).all()
+    # the mean distance from the maximum, its relative error twice that of a sum
+    mean = np.abs(np.where(np.isinf(lse), 0, ent) + m + np.log(V))
+    assert (np.abs(mixer.f64(entropy) - ent) <=
+            2 * s * (1 + mean) + 4 * U32 * (m + 12)).all()
+    if top:
+        assert (ti.cpu().numpy() == ids).all()
+        got = mixer.f64(tl)
+        inf = np.isinf(tlp)
+        assert (got[inf] == tlp[inf]).all()
+        with np.errstate(invalid="ignore"):
+            off = np.where(inf, 0, np.abs(got - tlp))
+            assert (off <= base[:, None] + 4 * U32 * np.where(
+                inf, 0, np.abs(tlp))).all()
+    else:
+        assert tl is None and ti is None
+
+
+def check_bwd(x, tokens, lse, ent, g, ge, out, scale=1.0):
+    scale32 = float(np.float32(scale))
+    want = mixer.lp_bwd(x, tokens, lse, ent, g, ge, scale32)
+    z = scale32 * mixer.f64(x)
+    l64 = mixer.f64(lse)
+    with np.errstate(invalid="ignore"):
+        lp = z - l64[:, None]
+    p = np.where(np.isneginf(l64)[:, None] | np.isnan(lp), 0, np.exp(lp))
+    lp = np.where(p > 0, lp, 0)
+    gm = np.abs(mixer.f64(g))[:, None] if g is not None else 0.0
+    gem = np.abs(mixer.f64(ge))[:, None] if ge is not None else 0.0
+    H = np.abs(mixer.f64(ent))[:, None] if ent is not None else 0.0
+    # exp's argument (a difference of numbers up to |z| + |lse|) and exp; the
+    # factors' products and sums; the term of the token itself
+    arg = 2 * U32 * (np.where(p > 0, np.abs(z), 0) +
+                     np.where(np.isinf(l64), 0, np.abs(l64))[:, None]) + 6 * U32
+    size = p * (gm + gem * (np.abs(lp) + H))
+    bound = scale32 * ((arg + 8 * U32) * size + gem * p * arg +
+                       4 * U32 * gm * (p > 0)) + 1e-37
+    if x.dtype == BF16:
+        bound = bound + U16 * (np.abs(want) + bound)
+    got = mixer.f64(out)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound + 4 * U32 * np.abs(want)).all()
+
+
+SIZES = [(1, 1), (3, 2), (5, 31), (4, 257), (2, 1000), (7, 4097), (3, 32000),
+         (1, 50001), (2, 131072), (300, 640), (1000, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V", SIZES)
+def test_forward(N, V, dtype):
+    for scale, top in ((1.0, 0), (0.7, min(V, 20)), (1.25, 1)):
+        x, t = rows(N, V, dtype)
+        check_fwd(x, t, kla.logprob_fwd(x, t, top, scale), top, scale)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V", SIZES)
+def test_backward(N, V, dtype):
+    x, t = rows(N, V, dtype)
+    t[::3] = -1
+    gen = torch.Generator().manual_seed(1)
+    g = torch.randn(N, generator=gen).cuda()
+    ge = torch.randn(N, generator=gen).cuda()
+    for scale in (1.0, 0.7):
+        _, ent, lse, _, _ = kla.logprob_fwd(x, t, scale=scale)
+        for a, b in ((g, ge), (g, None), (None, ge)):
+            out = kla.logprob_bwd(x, t, lse, ent if b is not None else None,
+                                  a, b, scale)
+            check_bwd(x, t, lse, ent, a, b, out, scale)
+        assert (kla.logprob_bwd(x, t, lse, scale=scale) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [40, 5003, 40000])
+def test_masked_logits(V, dtype):
+    x, t = rows(9, V, dtype, masked=0.6)
+    low = torch.finfo(dtype).min
+    x[4] = -math.inf                      # nothing left
+    x[5, :] = low                         # all of the type's lowest value
+    x[6, 1:] = low
+    x[7, :-3] = -math.inf                 # fewer left than asked for
+    t[7] = V - 1
+    top = 12
+    out = kla.logprob_fwd(x, t, top)
+    check_fwd(x, t, out, top)
+    assert out[0][4] == -math.inf and out[2][4] == -math.inf
+    assert out[1][4] == 0 and out[4][4].tolist() == list(range(top))
+    g = torch.ones(9, device="cuda")
+    d = kla.logprob_bwd(x, t, out[2], out[1], g, g)
+    check_bwd(x, t, out[2], out[1], g, g, d)
+    assert (d[4] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [7, 3000, 70001])
+@pytest.mark.parametrize("values", [1, 2, 40])
+def test_ties_go_to_the_lowest_id(V, values, dtype):
+    gen = torch.Generator().manual_seed(V)
+    x = torch.randint(0, values, (6, V), generator=gen).to(dtype).cuda()
+    x[0] = torch.where(x[0] == 0, -0.0, x[0])     # -0 and 0 are equal
+    x[1] = torch.where(torch.arange(V, device="cuda") % 2 == 0, -0.0, 0.0)
+    t = torch.zeros(6, dtype=torch.int64, device="cuda")
+    top = min(V, 128)
+    check_fwd(x, t, kla.logprob_fwd(x, t, top), top)
+
+
+@pytest.mark.parametrize("order", ["up", "down"])
+def test_sorted_rows(order):
+    V, top = 20000, 50
+    x = torch.arange(V, device="cuda", dtype=F32).div(V).repeat(3, 1)
+    x = x if order == "up" else x.flip(1).contiguous()
+    t = torch.zeros(3, dtype=torch.int64, device="cuda")
+    check_fwd(x, t, kla.logprob_fwd(x, t, top), top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_not_finite_rows_leave_the_others(dtype):
+    x, t = rows(6, 3000, dtype)
+    want = kla.logprob_fwd(x, t, 5)
+    x[1, 17] = math.nan
+    x[3, 5] = math.inf
+    x[4, 9] = -math.nan
+    got = kla.logprob_fwd(x, t, 5)
+    for r in range(6):
+        for a, b in zip(got[:4], want[:4]):
+            if r in (1, 3, 4):
+                assert torch.isnan(a[r]).all()
+            else:
+                assert torch.equal(a[r], b[r])
+    assert [got[4][r, 0].item() for r in (1, 3, 4)] == [17, 5, 9]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("off,wide", [(0, 8), (1, 3), (5, 57)])
+def test_strided_rows(off, wide, dtype):
+    x, t = rows(9, 1003, dtype)
+    buf = torch.zeros(9, 1003 + wide + off, dtype=dtype, device="cuda")
+    y = buf[:, off:off + 1003]
+    y.copy_(x)
+    a, b = kla.logprob_fwd(y, t, 4), kla.logprob_fwd(x, t, 4)
+    check_fwd(x, t, a, 4)
+    assert torch.equal(a[4], b[4])
+    g = torch.rand(9, device="cuda")
+    check_bwd(x, t, a[2], a[1], g, g,
+              kla.logprob_bwd(y, t, a[2], a[1], g, g))
+    one = x[:1].expand(9, 1003)           # one row for all
+    check_fwd(one, t, kla.logprob_fwd(one, t, 4), 4)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_in_place(dtype):
+    x, t = rows(5, 2050, dtype)
+    _, ent, lse, _, _ = kla.logprob_fwd(x, t)
+    g = torch.rand(5, device="cuda")
+    want = kla.logprob_bwd(x, t, lse, ent, g, g)
+    assert kla.logprob_bwd(x, t, lse, ent, g, g, out=x) is x
+    assert torch.equal(x, want)
+
+
+def test_tokens_outside_the_vocabulary():
+    x, t = rows(6, 300, F32)
+    t[:5] = torch.tensor([-1, -100, 300, 2 ** 40, -2 ** 40])
+    logp = kla.logprob_fwd(x, t)[0]
+    assert (logp[:5] == 0).all() and logp[5] < 0
+    lse = kla.logprob_fwd(x, t)[2]
+    d = kla.logprob_bwd(x, t, lse, logp_grad=torch.ones(6, device="cuda"))
+    assert (d[:5] == 0).all() and (d[5] != 0).any()
+
+
+def test_shapes_streams_and_graphs():
+    x, t = rows(12, 5000, BF16)
+    x, t = x.view(3, 4, 5000), t.view(3, 4)
+    g = torch.rand(3, 4, device="cuda")
+
+    def run():
+        out = kla.logprob_fwd(x, t, 7)
+        return [*out, kla.logprob_bwd(x, t, out[2], out[1], g, g)]
+
+    want = run()
+    assert want[0].shape == (3, 4) and want[4].shape == (3, 4, 7)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = kla.logprob_fwd(x, t, 7, stream=s)
+    with torch.cuda.stream(s):
+        run()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for o in out:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    empty = kla.logprob_fwd(x[:0], t[:0], 2)
+    assert empty[0].shape == (0, 4) and empty[3].shape == (0, 4, 2)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^31 elements apart."""
+    V, far = 1000, 2 ** 31 + 40
+    buf = torch.empty(far + V, dtype=BF16, device="cuda")
+    x, t = rows(2, V, BF16)
+    y = buf.as_strided((2, V), (far, 1))
+    y.copy_(x)
+    out = kla.logprob_fwd(y, t, 3)
+    check_fwd(x, t, out, 3)
+    g = torch.ones(2, device="cuda")
+    check_bwd(x, t, out[2], out[1], g, None,
+              kla.logprob_bwd(y, t, out[2], None, g))
+
+
+def test_binding_refuses():
+    x, t = rows(4, 10, F32)
+    g = torch.ones(4, device="cuda")
+    with pytest.raises(ValueError):
+        kla.logprob_fwd(x, t[:3])
+    with pytest.raises(TypeError):
+        kla.logprob_fwd(x, t.int())
+    with pytest.raises(TypeError):
+        kla.logprob_fwd(x.half(), t)
+    with pytest.raises(kla.KlaError):
+        kla.logprob_fwd(x, t, top=11)
+    with pytest.raises(kla.KlaError):
+        kla.logprob_fwd(x, t, scale=0.0)
+    with pytest.raises(ValueError):
+        kla.logprob_bwd(x, t, g, None, g, g)
+    with pytest.raises(ValueError):
+        kla.logprob_bwd(x, t, g, out=torch.empty(4, 20, device="cuda")[:, ::2])
+    with pytest.raises(kla.KlaError):
+        kla.logprob_fwd(torch.zeros(2, 500, device="cuda"),
+                        t[:2], top=129)
