@@ -871,6 +871,13 @@ KLA_API kla_status kla_selftest_wait_timeout(kla_stream_t stream);
  */
 KLA_API kla_status kla_selftest_glr_timeout(kla_stream_t stream);
 
+/*
+ * kla_selftest_linattn_timeout -- the same for linear attention with a decay
+ * for each head: launches one block of its tensor-core pass on `stream` that
+ * copies nothing and whose waits give up after 1 ms.  Errors: KLA_ERR_CUDA.
+ */
+KLA_API kla_status kla_selftest_linattn_timeout(kla_stream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 KLA_API const char* kla_status_string(kla_status status);
 

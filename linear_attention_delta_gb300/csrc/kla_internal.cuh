@@ -299,6 +299,10 @@ cudaError_t read_and_clear_fault_glr(unsigned int* word);
 // runs out and it sets the fault word.
 cudaError_t launch_glr_selftest(cudaStream_t stream);
 cudaError_t read_and_clear_fault_ln(unsigned int* word);
+cudaError_t read_and_clear_fault_la(unsigned int* word);
+// One block of the tensor-core pass of linear attention that copies nothing
+// and waits 1 ms: its waits run out and it sets the fault word.
+cudaError_t launch_linattn_selftest(cudaStream_t stream);
 // One CTA of the state-pass kernel whose producer issues no copy and whose
 // waits give up after 1 ms: it takes the kernel's abort path and sets the
 // fault word.

@@ -9,21 +9,19 @@
 //   S   <- w^C S + sum_s w^(C - e - s) k_s v_s^T
 // so that the work per token is 2 C (dk + dv) / 2 + 4 dk dv products instead
 // of a state update per token, and the state leaves the chip never.
-#include "kla_internal.cuh"
+#include "kla_linattn.cuh"
 
 namespace kla {
 namespace {
 
+using la::kNV;
+using la::Part;
+using la::Plan;
+using la::power;
 using bf16 = __nv_bfloat16;
-
-// w^n (w^0 = 1, whatever w is).
-__device__ __forceinline__ float power(float a, int n) {
-    return n == 0 ? 1.f : expf(a * (float)n);
-}
 
 // ------------------------------------------------------------ chunked pass
 
-constexpr int kNV = 64;          // columns of v a block works on
 constexpr int kNT = 256;
 
 template <int DKP>
@@ -37,25 +35,11 @@ struct Shape {
 };
 
 struct PassParams {
-    LinAttnJob j;
+    Part part;
+    Plan plan;
     const float* log_decay;
-    float* ws;                   // [BH][parts][dk][dv], see kPart below
-    int T, H, slices, parts, len;   // tokens of a part: len, a multiple of C
+    int T, H;
 };
-
-// Sequences in parts.  With parts > 1 a first launch writes, for each part
-// but the last, the state that its own tokens leave (slot i + 1 of part i)
-// and a copy of S0 (slot 0, if there is one); the state before part p is
-// then sum over i <= p of w^(len (p - i)) slot_i.
-__device__ __forceinline__ float state_before(const PassParams& p, int part,
-                                              size_t bh, size_t at, float a) {
-    const size_t n = (size_t)p.j.dk * p.j.dv;
-    float s = 0.f;
-    for (int i = p.j.S0 ? 0 : 1; i <= part; ++i)
-        s = fmaf(power(a, (part - i) * p.len),
-                 p.ws[(bh * p.parts + i) * n + at], s);
-    return s;
-}
 
 // Rows r0 .. r0 + C - 1 (in the pass's order) of x into dst [C][ld], zeros
 // beyond `rows` and `width`; columns c0 .. c0 + W - 1.
@@ -76,6 +60,7 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
 template <typename T, int DKP, bool STATE_ONLY>
 __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     using Sh = Shape<DKP>;
+    const LinAttnJob& j = p.part.j;
     constexpr int C = Sh::C, LD = Sh::LD, LP = Sh::LP;
     constexpr int RI = C / 16;       // rows, and columns of P, of a thread
     constexpr int RD = DKP / 16;     // rows of the state of a thread
@@ -87,15 +72,15 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     float* S = Ps + C * LP;
     float* w = S + DKP * kNV;        // w^0 .. w^C
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int slice = blockIdx.x % p.slices, n0 = slice * kNV;
-    const size_t bh = blockIdx.x / p.slices;
+    const int slice = blockIdx.x % p.part.slices, n0 = slice * kNV;
+    const size_t bh = blockIdx.x / p.part.slices;
     const int b = bh / p.H, h = bh % p.H, part = blockIdx.y;
-    const int dk = p.j.dk, dv = p.j.dv, e = p.j.reverse ? 0 : 1;
+    const int dk = j.dk, dv = j.dv, e = j.reverse ? 0 : 1;
     const float a = p.log_decay[h];
-    const T* q = static_cast<const T*>(p.j.q.p) + b * p.j.q.sb + h * p.j.q.sh;
-    const T* k = static_cast<const T*>(p.j.k.p) + b * p.j.k.sb + h * p.j.k.sh;
-    const T* v = static_cast<const T*>(p.j.v.p) + b * p.j.v.sb + h * p.j.v.sh;
-    T* o = static_cast<T*>(p.j.o);
+    const T* q = static_cast<const T*>(j.q.p) + b * j.q.sb + h * j.q.sh;
+    const T* k = static_cast<const T*>(j.k.p) + b * j.k.sb + h * j.k.sh;
+    const T* v = static_cast<const T*>(j.v.p) + b * j.v.sb + h * j.v.sh;
+    T* o = static_cast<T*>(j.o);
     const size_t sn = (size_t)dk * dv;
 
     if (tid <= C) w[tid] = power(a, tid);
@@ -103,29 +88,28 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         const int r = i / kNV, c = n0 + i % kNV;
         float s = 0.f;
         if (r < dk && c < dv) {
-            const size_t at = (size_t)r * p.j.s_r + (size_t)c * p.j.s_c;
+            const size_t at = (size_t)r * j.s_r + (size_t)c * j.s_c;
             if (STATE_ONLY) {
-                if (part == 0 && p.j.S0)   // the main launch may replace S0
-                    p.ws[bh * p.parts * sn + at] = p.j.S0[bh * sn + at];
-            } else if (p.parts > 1) {
-                s = state_before(p, part, bh, at, a);
-            } else if (p.j.S0) {
-                s = p.j.S0[bh * sn + at];
+                if (part == 0 && j.S0)
+                    p.part.ws[bh * p.plan.parts * sn + at] =
+                        j.S0[bh * sn + at];
+            } else {
+                s = la::state_before(p.part, p.plan, part, bh, at, a);
             }
         }
         S[i] = s;
     }
 
-    const int first = part * p.len;
-    const int end = min(p.T, first + p.len);
-    const long long step = p.j.reverse ? -1 : 1;
+    const int first = part * p.plan.len;
+    const int end = min(p.T, first + p.plan.len);
+    const long long step = j.reverse ? -1 : 1;
     for (int r0 = first; r0 < end; r0 += C) {
         const int rows = min(C, end - r0);
-        const long long t0 = p.j.reverse ? p.T - 1 - r0 : r0;
+        const long long t0 = j.reverse ? p.T - 1 - r0 : r0;
         if (!STATE_ONLY)
-            load_rows<T, C, DKP>(Qs, LD, q, p.j.q.st, t0, step, rows, 0, dk);
-        load_rows<T, C, DKP>(Ks, LD, k, p.j.k.st, t0, step, rows, 0, dk);
-        load_rows<T, C, kNV>(Vs, kNV, v, p.j.v.st, t0, step, rows, n0, dv);
+            load_rows<T, C, DKP>(Qs, LD, q, j.q.st, t0, step, rows, 0, dk);
+        load_rows<T, C, DKP>(Ks, LD, k, j.k.st, t0, step, rows, 0, dk);
+        load_rows<T, C, kNV>(Vs, kNV, v, j.v.st, t0, step, rows, n0, dv);
         __syncthreads();
         if (!STATE_ONLY) {
             float s[RI][RI] = {};
@@ -247,21 +231,18 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         __syncthreads();
     }
 
-    if (!STATE_ONLY && (part + 1 < p.parts || !p.j.ST)) return;
-    float* dst = STATE_ONLY ? p.ws + (bh * p.parts + part + 1) * sn
-                            : p.j.ST + bh * sn;
+    if (!STATE_ONLY && (part + 1 < p.plan.parts || !j.ST)) return;
+    float* dst = STATE_ONLY ? p.part.ws + (bh * p.plan.parts + part + 1) * sn
+                            : j.ST + bh * sn;
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
         if (r < dk && c < dv)
-            dst[(size_t)r * p.j.s_r + (size_t)c * p.j.s_c] = S[i];
+            dst[(size_t)r * j.s_r + (size_t)c * j.s_c] = S[i];
     }
 }
 
 // Parts of a sequence: enough for about two blocks an SM, at least 256
 // tokens each.
-struct Plan {
-    int parts, len;
-};
 Plan plan(long long blocks, int T) {
     constexpr int kSMs = 152, kLeast = 256;
     long long parts = 2 * kSMs / blocks;
@@ -273,29 +254,38 @@ Plan plan(long long blocks, int T) {
     return {(T + len - 1) / len, len};
 }
 
-int slices_of(const LinAttnJob& j) { return (j.dv + kNV - 1) / kNV; }
-
 template <typename T, int DKP, bool STATE_ONLY>
-cudaError_t launch_pass(const PassParams& p, long long bh, int parts,
+cudaError_t launch_pass(const PassParams& p, long long bh,
                         cudaStream_t stream) {
     constexpr int bytes = Shape<DKP>::FLOATS * 4;
     auto kern = linattn_pass<T, DKP, STATE_ONLY>;
     cudaError_t e = cudaFuncSetAttribute(
         kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(bh * p.slices), parts), kNT, bytes, stream>>>(p);
+    const dim3 grid((unsigned)(bh * p.part.slices),
+                    p.plan.parts - (STATE_ONLY ? 1 : 0));
+    kern<<<grid, kNT, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int DKP>
 cudaError_t launch_job(const PassParams& p, long long bh,
                        cudaStream_t stream) {
-    if (p.parts > 1) {
-        cudaError_t e =
-            launch_pass<T, DKP, true>(p, bh, p.parts - 1, stream);
+    if (p.plan.parts > 1) {
+        cudaError_t e = launch_pass<T, DKP, true>(p, bh, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_pass<T, DKP, false>(p, bh, p.parts, stream);
+    return launch_pass<T, DKP, false>(p, bh, stream);
+}
+
+Plan plan_of(const LinAttnArgs& a, int job) {
+    return plan((long long)a.B * a.H * la::slices_of(a.job[job]), a.T);
+}
+
+// Floats of the part states of a job.
+size_t part_floats(const LinAttnArgs& a, int job, const Plan& pl) {
+    const LinAttnJob& j = a.job[job];
+    return pl.parts > 1 ? (size_t)a.B * a.H * pl.parts * j.dk * j.dv : 0;
 }
 
 template <typename T>
@@ -303,36 +293,35 @@ cudaError_t launch_all(const LinAttnArgs& a, float* ws, cudaStream_t stream) {
     const long long bh = (long long)a.B * a.H;
     for (int i = 0; i < a.jobs; ++i) {
         const LinAttnJob& j = a.job[i];
-        const int slices = slices_of(j);
-        const Plan pl = plan(bh * slices, a.T);
-        const PassParams p{j, a.log_decay, ws, a.T, a.H, slices, pl.parts,
-                           pl.len};
+        const Plan pl = plan_of(a, i);
+        const PassParams p{{j, ws, la::slices_of(j)}, pl, a.log_decay, a.T,
+                           a.H};
         const cudaError_t e =
             j.dk <= 64    ? launch_job<T, 64>(p, bh, stream)
             : j.dk <= 128 ? launch_job<T, 128>(p, bh, stream)
                           : launch_job<T, 256>(p, bh, stream);
         if (e != cudaSuccess) return e;
-        if (pl.parts > 1) ws += (size_t)bh * pl.parts * j.dk * j.dv;
+        if (pl.parts > 1) ws += part_floats(a, i, pl);
     }
     return cudaSuccess;
 }
 
 }  // namespace
 
+// By the sizes alone, whichever form the tensors' alignment allows.
 size_t linattn_workspace_bytes(const LinAttnArgs& a) {
-    const long long bh = (long long)a.B * a.H;
-    size_t n = 0;
+    size_t n = 0, tc = 0;
     for (int i = 0; i < a.jobs; ++i) {
-        const LinAttnJob& j = a.job[i];
-        const Plan pl = plan(bh * slices_of(j), a.T);
-        if (pl.parts > 1) n += (size_t)bh * pl.parts * j.dk * j.dv;
+        n += part_floats(a, i, plan_of(a, i));
+        if (linattn_tc_sizes(a)) tc += part_floats(a, i, linattn_tc_plan(a));
     }
-    return n * sizeof(float);
+    return (n > tc ? n : tc) * sizeof(float);
 }
 
 cudaError_t launch_linattn(const LinAttnArgs& a, void* workspace,
                            cudaStream_t stream) {
     float* ws = static_cast<float*>(workspace);
+    if (linattn_tc_eligible(a)) return launch_linattn_tc(a, ws, stream);
     return a.dtype == KLA_BF16 ? launch_all<bf16>(a, ws, stream)
                                : launch_all<float>(a, ws, stream);
 }

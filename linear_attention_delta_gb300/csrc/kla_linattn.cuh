@@ -1,0 +1,56 @@
+// What the two forms of the chunked pass of linear attention share.
+#pragma once
+
+#include "kla_internal.cuh"
+
+namespace kla {
+namespace la {
+
+constexpr int kNV = 64;          // columns of v (and of the state) a block has
+
+// w^n of w = exp(a) (w^0 = 1, whatever w is).
+__device__ __forceinline__ float power(float a, int n) {
+    return n == 0 ? 1.f : expf(a * (float)n);
+}
+
+// Sequences in parts of `len` tokens (a multiple of the chunk; the last part
+// the rest).  With parts > 1 a first launch writes, for each part but the
+// last, the state that its own tokens leave (slot i + 1 of part i) and a copy
+// of S0 (slot 0, if there is one; the main launch may replace S0); the state
+// before part p is then sum over i <= p of w^(len (p - i)) slot_i.
+struct Plan {
+    int parts, len;
+};
+
+struct Part {
+    LinAttnJob j;
+    float* ws;                   // [B H][parts][dk dv], null with one part
+    int slices;                  // blocks along dv
+};
+
+// Element `at` of the state before part `part` of sequence and head bh.
+__device__ __forceinline__ float state_before(const Part& p, const Plan& pl,
+                                              int part, size_t bh, size_t at,
+                                              float a) {
+    const size_t n = (size_t)p.j.dk * p.j.dv;
+    if (pl.parts == 1) return p.j.S0 ? p.j.S0[bh * n + at] : 0.f;
+    float s = 0.f;
+    for (int i = p.j.S0 ? 0 : 1; i <= part; ++i)
+        s = fmaf(power(a, (part - i) * pl.len),
+                 p.ws[(bh * pl.parts + i) * n + at], s);
+    return s;
+}
+
+inline int slices_of(const LinAttnJob& j) { return (j.dv + kNV - 1) / kNV; }
+
+}  // namespace la
+
+// The tensor-core form: bf16, q and k up to 128 wide, tensors that TMA can
+// describe.  linattn_tc_plan looks at sizes only.
+bool linattn_tc_sizes(const LinAttnArgs& a);
+bool linattn_tc_eligible(const LinAttnArgs& a);
+la::Plan linattn_tc_plan(const LinAttnArgs& a);
+cudaError_t launch_linattn_tc(const LinAttnArgs& a, float* ws,
+                              cudaStream_t stream);
+
+}  // namespace kla

@@ -266,3 +266,8 @@ extern "C" kla_status kla_logprob_bwd(
     return from_cuda(kla::launch_logprob_bwd(
         a, reinterpret_cast<cudaStream_t>(stream)));
 }
+
+extern "C" kla_status kla_selftest_linattn_timeout(kla_stream_t stream) {
+    return from_cuda(kla::launch_linattn_selftest(
+        reinterpret_cast<cudaStream_t>(stream)));
+}

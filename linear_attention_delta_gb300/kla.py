@@ -107,6 +107,7 @@ SIGNATURES = {
     "kla_device_status": (_I, [_VP]),
     "kla_selftest_wait_timeout": (_I, [_VP]),
     "kla_selftest_glr_timeout": (_I, [_VP]),
+    "kla_selftest_linattn_timeout": (_I, [_VP]),
     "kla_status_string": (ctypes.c_char_p, [_I]),
 }
 
@@ -1170,3 +1171,10 @@ def selftest_glr_timeout(stream=None) -> int:
     """``kla_selftest_glr_timeout``: one block of the recurrence's scan whose
     wait gives up after 1 ms; returns the launch status."""
     return int(load_library().kla_selftest_glr_timeout(_stream(stream)))
+
+
+def selftest_linattn_timeout(stream=None) -> int:
+    """``kla_selftest_linattn_timeout``: one block of linear attention's
+    tensor-core pass whose waits give up after 1 ms; returns the launch
+    status."""
+    return int(load_library().kla_selftest_linattn_timeout(_stream(stream)))

@@ -399,3 +399,12 @@ def test_binding_refuses():
     big = torch.zeros(1, 2, 1, 257, device="cuda")
     with pytest.raises(kla.KlaError):
         kla.linattn_fwd(big, big, big, torch.zeros(1, device="cuda"))
+
+
+def test_bounded_wait_runs_out_and_is_reported():
+    assert kla.device_status() == 0
+    assert kla.selftest_linattn_timeout() == 0
+    assert kla.device_status() == -4
+    assert kla.device_status() == 0
+    x, _ = make(1, 200, 2, 64, 64, BF16)
+    check_fwd(x, *kla.linattn_fwd(**x))
