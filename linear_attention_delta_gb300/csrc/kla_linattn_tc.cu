@@ -17,9 +17,10 @@
 // The weighted V of U is split into three bf16 parts (24 bits), so that the
 // state keeps the digits of fp32.
 //
-// Warps: 0 copies (TMA), 1 issues the products, 4-7 turn scores into P~
-// (thread = row), 8-11 weight V and hold the state (thread = row of S), 12-15
-// write the outputs (thread = row).  They hand over through mbarriers.
+// Warps: 0 copies (TMA), 1 issues the products, 4-7 hold the state (thread =
+// row of S), 8-15 weight V and turn scores into P~ (thread = row and half of
+// the columns), 16-19 write the outputs (thread = row).  They hand over
+// through mbarriers.
 //
 // In reverse the tiles lie in memory order all the same; r counts from the
 // tile's last row, masks and weights are mirrored.
@@ -33,6 +34,7 @@
 // and returns.
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "kla_linattn.cuh"
 #include "tc_primitives.cuh"
 
@@ -48,61 +50,71 @@ using bf16 = __nv_bfloat16;
 __device__ unsigned int g_fault_la = 0;
 
 constexpr int kC = 128;          // tokens a chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kBox = kC * 128;   // bytes of a TMA box: 128 rows of 64 bf16
 constexpr int kMaxJobs = 3;
 
-// Shared memory (bytes from a 1024-aligned base): the ring of stages (Q | K |
-// V, in boxes of 64 columns; without Q in the pass that forms part states),
-// the three parts of the weighted V, the bf16 copy of S, the weights.
+// Shared memory (bytes from a 1024-aligned base): the rings of Q, K and V
+// tiles (boxes of 64 columns; no Q in the pass that forms part states), the
+// three parts of the weighted V, the bf16 copy of S, the weights.
 template <int DK, bool STATE_ONLY>
 struct Smem {
     static constexpr int HALVES = DK / 64;
-    static constexpr int Q = 0;
-    static constexpr int K = STATE_ONLY ? 0 : HALVES * kBox;
-    static constexpr int V = K + HALVES * kBox;
-    static constexpr int STAGE = V + kBox;
     static constexpr int NS = STATE_ONLY ? (DK == 64 ? 5 : 3)
                                          : (DK == 64 ? 3 : 2);
-    static constexpr int VW = NS * STAGE;        // 3 boxes
+    static constexpr int TILE = HALVES * kBox;   // of Q or K
+    static constexpr int Q = 0;
+    static constexpr int K = Q + (STATE_ONLY ? 0 : NS * TILE);
+    static constexpr int V = K + NS * TILE;
+    static constexpr int VW = V + NS * kBox;     // 3 boxes
     static constexpr int S = VW + 3 * kBox;      // DK rows of 128 bytes
     static constexpr int W = S + DK * 128;       // w^0 .. w^128
-    static constexpr int BAD = W + 4 * 132;      // [2][4 warps][64]: see below
+    static constexpr int CW = W + 4 * 132;       // factors of 32 columns
+    static constexpr int DW = CW + 4 * 32;       // of a diagonal block
+    static constexpr int BAD = DW + 4 * 64;      // [2][4 warps][64]: see below
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
-    static constexpr int BARS = FLAG + 2 * 4 * 4;
-    static constexpr int NUM_BARS = 2 * NS + 11;
+    static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
+    static constexpr int BARS = DONE + 4 * 4;
+    static constexpr int NUM_BARS = 5 * NS + 11;
     static constexpr int MISC = BARS + 8 * NUM_BARS;   // abort, TMEM, issued
     static constexpr int BYTES = MISC + 16 + 1024;     // alignment
     static_assert(BYTES <= 232448, "shared memory");
     static_assert(BARS % 8 == 0 && W % 16 == 0, "alignment");
 };
 
-// mbarriers: a phase a chunk, or a phase every other chunk where there are two
+// mbarriers, a phase a chunk (of a ring: a phase a turn)
 template <int NS>
 struct Bars {
-    static constexpr int FULL = 0;               // NS: stage loaded
-    static constexpr int EMPTY = NS;             // NS: stage read by all
-    static constexpr int P_FULL = 2 * NS;        // 2: scores in TMEM
-    static constexpr int P_READY = 2 * NS + 2;   // 2: P~ in TMEM
-    static constexpr int V_READY = 2 * NS + 4;   // 2: weighted V in place, U
-                                                 // of the chunk before read
-    static constexpr int U_FULL = 2 * NS + 6;
-    static constexpr int S_READY = 2 * NS + 7;   // copy of S in place
-    static constexpr int S_FREE = 2 * NS + 8;    // Q S done
-    static constexpr int O_FULL = 2 * NS + 9;
-    static constexpr int O_FREE = 2 * NS + 10;   // outputs read
+    static constexpr int FULL = 0;               // NS: Q and K loaded
+    static constexpr int FULL_V = NS;            // NS
+    static constexpr int EMPTY_Q = 2 * NS;       // NS: read by all
+    static constexpr int EMPTY_K = 3 * NS;       // NS
+    static constexpr int EMPTY_V = 4 * NS;       // NS
+    static constexpr int SC_FULL = 5 * NS;       // scores in TMEM
+    static constexpr int SC_FREE = 5 * NS + 1;   // read
+    static constexpr int P_READY = 5 * NS + 2;   // P~ in TMEM
+    static constexpr int V_READY = 5 * NS + 3;   // weighted V in place
+    static constexpr int U_FULL = 5 * NS + 4;    // U in TMEM (V's parts read)
+    static constexpr int U_FREE = 5 * NS + 5;    // read
+    static constexpr int S_READY = 5 * NS + 6;   // copy of S in place
+    static constexpr int S_FREE = 5 * NS + 7;    // Q S done
+    static constexpr int O_FULL = 5 * NS + 8;    // outputs in TMEM (P~ read)
+    static constexpr int O_FREE = 5 * NS + 9;    // read
 };
 
-// TMEM columns
-constexpr uint32_t kColP = 0;        // 2 x 128: scores, then P~ (64 of them)
-constexpr uint32_t kColPV = 256;
-constexpr uint32_t kColQS = 320;
-constexpr uint32_t kColU = 384;
+// TMEM columns: all 512
+constexpr uint32_t kColSC = 0;       // 128: scores
+constexpr uint32_t kColP = 128;      // 64: P~, two bf16 a column
+constexpr uint32_t kColPV = 192;     // 64
+constexpr uint32_t kColQS = 256;     // 64
+constexpr uint32_t kColU = 320;      // 3 x 64: U from each part of V
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kIdQK = tc::idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdRow = tc::idesc_bf16(128, kNV, false, true);
-constexpr uint32_t kIdU = tc::idesc_bf16(128, kNV, true, true);
+// the parts of V side by side: K is read once for all three (three products
+// of 64 columns are bound by reading K from shared memory)
+constexpr uint32_t kIdU = tc::idesc_bf16(128, 3 * kNV, true, true);
 
 struct Maps {
     CUtensorMap q[kMaxJobs], k[kMaxJobs], v[kMaxJobs];
@@ -146,6 +158,16 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* u) {
         : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Whether the phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -159,10 +181,9 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Two floats less the two bf16 they were rounded to.
+// Two floats less the two bf16 they were rounded to (exact).
 __device__ __forceinline__ float2 rest(float2 x, uint32_t b) {
-    return make_float2(x.x - __uint_as_float(b << 16),
-                       x.y - __uint_as_float(b & 0xffff0000u));
+    return fma2(from_bf16x2(b), both(-1.f), x);
 }
 
 template <int DK, bool STATE_ONLY>
@@ -177,16 +198,21 @@ linattn_tc(const __grid_constant__ Maps maps,
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = tc::smem_u32(sm);
     float* w = reinterpret_cast<float*>(sm + Sm::W);
+    float* cw = reinterpret_cast<float*>(sm + Sm::CW);
+    float* dw = reinterpret_cast<float*>(sm + Sm::DW);
     // for each of two chunks, output warp and column: the first row (counted
     // as r) whose V is not finite, 255: none
     uint8_t* bad = sm + Sm::BAD;
     volatile int* flag = reinterpret_cast<int*>(sm + Sm::FLAG);
+    // chunks whose outputs each output warp has read
+    volatile int* done = reinterpret_cast<int*>(sm + Sm::DONE);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sm::BARS);
     int* abort_flag = reinterpret_cast<int*>(sm + Sm::MISC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sm::MISC + 4);
     int* issued = reinterpret_cast<int*>(sm + Sm::MISC + 8);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(~0u, tid >> 5, 0);   // uniform
     int job = 0;
     while (job + 1 < kMaxJobs && (int)blockIdx.x >= p.first[job + 1]) ++job;
     const Part& pt = p.part[job];
@@ -210,19 +236,31 @@ linattn_tc(const __grid_constant__ Maps maps,
     }
     if (tid == 32) {
         for (int i = 0; i < Sm::NUM_BARS; ++i) {
-            // the groups of four warps arrive once a warp
-            const bool group = i == B::P_READY || i == B::P_READY + 1 ||
-                               i == B::V_READY || i == B::V_READY + 1 ||
-                               i == B::S_READY || i == B::O_FREE;
-            tc::mbar_init(&bars[i], group ? 4 : 1);
+            // groups arrive once a warp; O_FULL by the products' end and by
+            // the thread that issued them
+            const int count =
+                i == B::SC_FREE || i == B::P_READY || i == B::V_READY ? 8
+                : i == B::U_FREE || i == B::S_READY || i == B::O_FREE ? 4
+                : i == B::O_FULL ? 2 : 1;
+            tc::mbar_init(&bars[i], count);
         }
         tc::fence_mbar_init();
         *abort_flag = 0;
         *issued = 0;
     }
     if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
+    // column m of a block of scores left of its row's own block: w^(31 - m) (in
+    // reverse w^m) times a factor of the row; on the diagonal entry 31 + lane
+    // - m is w^(lane - m) (w^(m - lane)), -1 what is masked
+    if (tid >= 256 && tid < 288)
+        cw[tid - 256] = power(a, rev ? tid - 256 : 287 - tid);
+    if (tid >= 288 && tid < 352) {
+        const int d = rev ? 319 - tid : tid - 319;
+        dw[tid - 288] = d >= 0 ? power(a, d) : -1.f;
+    }
     for (int i = tid; i < 2 * 4 * 64; i += kThreads) bad[i] = 255;
     if (tid < 8) flag[tid] = 0;
+    if (tid < 4) done[tid] = 0;
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -237,6 +275,11 @@ linattn_tc(const __grid_constant__ Maps maps,
     auto wait_warp = [&](int bar, int phase) {
         return __all_sync(~0u, wait(bar, phase));
     };
+    // one arrival of a warp whose lanes are done (each with its own fences)
+    auto arrive = [&](int bar) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[bar]);
+    };
     // the first token (in memory) of chunk c's tile; may be negative in
     // reverse
     auto tile_token = [&](int c) {
@@ -246,7 +289,6 @@ linattn_tc(const __grid_constant__ Maps maps,
     auto rows_of = [&](int c) { return min(kC, end - (first + c * kC)); };
 
     int last_bar = -1, last_phase = 0;   // the issuer's last commit
-    float S[kNV];                        // the state group's
 
     if (tid == 0 && !p.selftest) {
         // ------------------------------------------------------ copies
@@ -254,237 +296,284 @@ linattn_tc(const __grid_constant__ Maps maps,
         tc::prefetch_tmap(&maps.v[job]);
         if (!STATE_ONLY) tc::prefetch_tmap(&maps.q[job]);
         for (int c = 0; c < nchunks; ++c) {
-            const int s = c % NS;
-            if (c >= NS && !wait(B::EMPTY + s, c / NS - 1)) break;
-            uint8_t* st = sm + s * Sm::STAGE;
+            const int s = c % NS, turn = c / NS;
             uint64_t* full = &bars[B::FULL + s];
             const int t = tile_token(c);
-            tc::mbar_arrive_expect_tx(full, Sm::STAGE);
+            if (turn && !wait(B::EMPTY_K + s, turn - 1)) break;
+            tc::mbar_arrive_expect_tx(full,
+                                      (STATE_ONLY ? 1 : 2) * Sm::TILE);
 #pragma unroll
             for (int i = 0; i < HALVES; ++i)
-                tc::tma_load_4d(st + Sm::K + i * kBox, &maps.k[job], full,
-                                64 * i, h, t, b);
-            if (!STATE_ONLY)
+                tc::tma_load_4d(sm + Sm::K + s * Sm::TILE + i * kBox,
+                                &maps.k[job], full, 64 * i, h, t, b);
+            *reinterpret_cast<volatile int*>(issued) = c + 1;
+            if (!STATE_ONLY) {
+                if (turn && !wait(B::EMPTY_Q + s, turn - 1)) break;
 #pragma unroll
                 for (int i = 0; i < HALVES; ++i)
-                    tc::tma_load_4d(st + Sm::Q + i * kBox, &maps.q[job], full,
-                                    64 * i, h, t, b);
-            tc::tma_load_4d(st + Sm::V, &maps.v[job], full, n0, h, t, b);
-            *reinterpret_cast<volatile int*>(issued) = c + 1;
-        }
-    } else if (tid == 32) {
-        // ---------------------------------------------------- products
-        auto scores = [&](int c) {
-            const uint32_t st = sbase + c % NS * Sm::STAGE;
-            if (!wait(B::FULL + c % NS, c / NS)) return false;
-            tc::tc_fence_after();
-            // P~ V of chunk c - 2, which read this buffer, is ahead of this
-            // product in the queue
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * kBox + (ks & 3) * 32;
-                tc::mma_bf16(tmem + kColP + 128 * (c & 1),
-                             desc_k(st + Sm::Q + off),
-                             desc_k(st + Sm::K + off), kIdQK, ks > 0);
+                    tc::tma_load_4d(sm + Sm::Q + s * Sm::TILE + i * kBox,
+                                    &maps.q[job], full, 64 * i, h, t, b);
             }
-            tc::mma_commit(&bars[B::P_FULL + (c & 1)]);
-            last_bar = B::P_FULL + (c & 1), last_phase = c >> 1;
+            if (turn && !wait(B::EMPTY_V + s, turn - 1)) break;
+            tc::mbar_arrive_expect_tx(&bars[B::FULL_V + s], kBox);
+            tc::tma_load_4d(sm + Sm::V + s * kBox, &maps.v[job],
+                            &bars[B::FULL_V + s], n0, h, t, b);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- products
+        // The whole warp walks the chunks, one lane issues; what the products
+        // take is the same in all lanes, so it stays in uniform registers.
+        const bool issuer = elect_one();
+        // descriptors of the first stage's tiles; addresses count in 16 bytes
+        const uint64_t dQ = desc_k(sbase + Sm::Q), dK = desc_k(sbase + Sm::K);
+        const uint64_t dKt =       // 64 wide: rows 64 .. 127 of U repeat, unread
+            desc_mn(sbase + Sm::K, DK == 128 ? kBox : 0);
+        const uint64_t dVw = desc_mn(sbase + Sm::VW, kBox);
+        const uint64_t dS = desc_mn(sbase + Sm::S, 0);
+        const uint64_t dV = desc_mn(sbase + Sm::V, 0);
+        auto step_k = [](int ks) { return (ks >> 2) * (kBox >> 4) + (ks & 3) * 2; };
+        auto commit = [&](int bar, int phase) {
+            tc::mma_commit(&bars[bar]);
+            last_bar = bar, last_phase = phase;
+        };
+        auto scores = [&](int c) {
+            const uint32_t at = c % NS * (Sm::TILE >> 4);
+            if (!wait_warp(B::FULL + c % NS, c / NS)) return false;
+            if (c > 0 && !wait_warp(B::SC_FREE, c - 1)) return false;
+            tc::tc_fence_after();
+            if (issuer) {
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    tc::mma_bf16(tmem + kColSC, dQ + at + step_k(ks),
+                                 dK + at + step_k(ks), kIdQK, ks > 0);
+                commit(B::SC_FULL, c);
+            }
+            __syncwarp();
             return true;
         };
         int scored = 0;      // chunks whose scores are issued
         for (int c = 0; c < nchunks; ++c) {
-            const uint32_t st = sbase + c % NS * Sm::STAGE;
+            const int s = c % NS;
+            const uint32_t at = s * (Sm::TILE >> 4);
+            const bool again = c + NS < nchunks;   // the stage is loaded again
             if (!STATE_ONLY && scored == c) {
                 if (!scores(c)) break;
                 scored = c + 1;
             }
-            if (!wait(B::V_READY + (c & 1), c >> 1)) break;
+            if (!wait_warp(B::V_READY, c)) break;
+            if (STATE_ONLY && !wait_warp(B::FULL + s, c / NS)) break;
+            if (c > 0 && !wait_warp(B::U_FREE, c - 1)) break;
             tc::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
+            if (issuer) {
 #pragma unroll
                 for (int ks = 0; ks < kC / 16; ++ks)
-                    tc::mma_bf16(
-                        tmem + kColU,
-                        // 64 wide: rows 64 .. 127 of U repeat, unread
-                        desc_mn(st + Sm::K + ks * 2048, DK == 128 ? kBox : 0),
-                        desc_mn(sbase + Sm::VW + i * kBox + ks * 2048, 0),
-                        kIdU, i + ks > 0);
-            tc::mma_commit(&bars[B::U_FULL]);
-            last_bar = B::U_FULL, last_phase = c;
-            const bool again = c + NS < nchunks;   // the stage is loaded again
-            if (STATE_ONLY) {
-                if (again) tc::mma_commit(&bars[B::EMPTY + c % NS]);
-                continue;
+                    tc::mma_bf16(tmem + kColU, dKt + at + ks * 128,
+                                 dVw + ks * 128, kIdU, ks > 0);
+                commit(B::U_FULL, c);
+                if (again) tc::mma_commit(&bars[B::EMPTY_K + s]);
+                if (STATE_ONLY && again)
+                    tc::mma_commit(&bars[B::EMPTY_V + s]);
             }
-            if (!wait(B::S_READY, c)) break;
-            if (c > 0 && !wait(B::O_FREE, c - 1)) break;
+            __syncwarp();
+            if (STATE_ONLY) continue;
+            if (!wait_warp(B::S_READY, c)) break;
+            if (c > 0 && !wait_warp(B::O_FREE, c - 1)) break;
             tc::tc_fence_after();
+            if (issuer) {
 #pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)
-                tc::mma_bf16(tmem + kColQS,
-                             desc_k(st + Sm::Q + (ks >> 2) * kBox +
-                                    (ks & 3) * 32),
-                             desc_mn(sbase + Sm::S + ks * 2048, 0), kIdRow,
-                             ks > 0);
-            tc::mma_commit(&bars[B::S_FREE]);
-            last_bar = B::S_FREE, last_phase = c;
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    tc::mma_bf16(tmem + kColQS, dQ + at + step_k(ks),
+                                 dS + ks * 128, kIdRow, ks > 0);
+                commit(B::S_FREE, c);
+                if (again) tc::mma_commit(&bars[B::EMPTY_Q + s]);
+            }
+            __syncwarp();
             // the next scores, when their inputs are here: they are in the
             // works while this chunk's become P~
             if (scored == c + 1 && scored < nchunks &&
-                mbar_test(&bars[B::FULL + scored % NS], scored / NS & 1)) {
+                __all_sync(~0u, mbar_test(&bars[B::FULL + scored % NS],
+                                          scored / NS & 1) &&
+                                    mbar_test(&bars[B::SC_FREE], c & 1))) {
                 if (!scores(scored)) break;
                 ++scored;
             }
-            if (!wait(B::P_READY + (c & 1), c >> 1)) break;
+            if (!wait_warp(B::P_READY, c)) break;
             tc::tc_fence_after();
+            if (issuer) {
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                mma_bf16_ts(tmem + kColPV,
-                            tmem + kColP + 128 * (c & 1) + 8 * ks,
-                            desc_mn(st + Sm::V + ks * 2048, 0), kIdRow,
-                            ks > 0);
-            tc::mma_commit(&bars[B::O_FULL]);
-            last_bar = B::O_FULL, last_phase = c;
-            if (again) tc::mma_commit(&bars[B::EMPTY + c % NS]);
-        }
-    } else if (warp >= 4 && warp < 8 && !STATE_ONLY) {
-        // ------------------------------------------- scores to P~ (row i)
-        const int q = warp - 4, i = 32 * q + lane;
-        for (int c = 0; c < nchunks; ++c) {
-            if (!wait_warp(B::P_FULL + (c & 1), c >> 1)) break;
-            tc::tc_fence_after();
-            const uint32_t col =
-                tmem + ((uint32_t)(32 * q) << 16) + kColP + 128 * (c & 1);
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {      // 32 columns
-                float u[16];
-                uint32_t* pk = reinterpret_cast<uint32_t*>(u);
-                if (rev ? j < q : j > q) {
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) pk[n] = 0;
-                } else {
-                    float x[32];
-                    tc::tmem_ld32(col + 32 * j, x);
-                    tc::tmem_ld_wait();
-                    if (j == q) {
-                        // the diagonal: what is masked is not multiplied by 0
-#pragma unroll
-                        for (int n = 0; n < 32; ++n) {
-                            const int d = rev ? n - lane : lane - n;
-                            x[n] = d >= 0 ? x[n] * w[d < 0 ? 0 : d] : 0.f;
-                        }
-                    } else {
-                        // w^(r - s) as a factor of the row and one of the
-                        // column, neither exponent negative
-                        const float f =
-                            w[rev ? 32 * j - i : i - 32 * j - 31];
-#pragma unroll
-                        for (int n = 0; n < 32; n += 4) {
-                            const float4 g = *reinterpret_cast<const float4*>(
-                                &w[rev ? n : 28 - n]);
-                            x[n] *= f * (rev ? g.x : g.w);
-                            x[n + 1] *= f * (rev ? g.y : g.z);
-                            x[n + 2] *= f * (rev ? g.z : g.y);
-                            x[n + 3] *= f * (rev ? g.w : g.x);
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        pk[n] = tc::pack_bf16x2(x[2 * n], x[2 * n + 1]);
-                }
-                tc::tmem_st16(col + 16 * j, u);
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts(tmem + kColPV, tmem + kColP + 8 * ks,
+                                dV + s * (kBox >> 4) + ks * 128, kIdRow,
+                                ks > 0);
+                commit(B::O_FULL, c);
+                tc::mbar_arrive(&bars[B::O_FULL]);   // hands on what it saw
+                if (again) tc::mma_commit(&bars[B::EMPTY_V + s]);
             }
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[B::P_READY + (c & 1)]);
         }
-    } else if (warp >= 8 && warp < 12) {
-        // -------------------------------- weighted V, and the state (row d)
-        const int gt = tid - 256, d = gt;
+    } else if (warp >= 4 && warp < 8) {
+        // --------------------------------------------------- state (row d)
+        const int d = tid - 128;
         const bool mine = d < pt.j.dk;
         const size_t row = (size_t)d * pt.j.s_r;
         const size_t sn = (size_t)pt.j.dk * pt.j.dv;
+        float2 S[kNV / 2];
+        auto clear = [&] {
 #pragma unroll
-        for (int n = 0; n < kNV; ++n) {
-            S[n] = 0.f;
-            if (mine && n0 + n < pt.j.dv) {
-                const size_t at = row + (size_t)(n0 + n) * pt.j.s_c;
-                if (STATE_ONLY) {
-                    if (part == 0 && pt.j.S0)
-                        pt.ws[bh * p.plan.parts * sn + at] =
-                            pt.j.S0[bh * sn + at];
-                } else {
-                    S[n] = la::state_before(pt, p.plan, part, bh, at, a);
+            for (int n = 0; n < kNV / 2; ++n) S[n] = both(0.f);
+        };
+        clear();
+        // S += f x of a state in memory
+        auto add = [&](const float* x, float f) {
+            x += row + (size_t)n0 * pt.j.s_c;
+            if (pt.j.s_c == 1 && pt.j.dv % kNV == 0 &&
+                (reinterpret_cast<uintptr_t>(x) & 15) == 0) {
+#pragma unroll
+                for (int n = 0; n < kNV / 2; n += 2) {
+                    const float4 y =
+                        *reinterpret_cast<const float4*>(x + 2 * n);
+                    S[n] = fma2(both(f), make_float2(y.x, y.y), S[n]);
+                    S[n + 1] = fma2(both(f), make_float2(y.z, y.w), S[n + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < kNV; ++n) {
+                    float& s = n & 1 ? S[n / 2].y : S[n / 2].x;
+                    if (n0 + n < pt.j.dv)
+                        s = fmaf(f, x[(size_t)n * pt.j.s_c], s);
                 }
             }
+        };
+        auto store = [&](float* x) {
+            x += row + (size_t)n0 * pt.j.s_c;
+#pragma unroll
+            for (int n = 0; n < kNV; ++n)
+                if (n0 + n < pt.j.dv)
+                    x[(size_t)n * pt.j.s_c] = n & 1 ? S[n / 2].y : S[n / 2].x;
+        };
+        float* slots = pt.ws ? pt.ws + bh * p.plan.parts * sn : nullptr;
+        if (mine && STATE_ONLY) {
+            if (part == 0 && pt.j.S0) {
+                add(pt.j.S0 + bh * sn, 1.f);
+                store(slots);
+                clear();
+            }
+        } else if (mine && p.plan.parts == 1) {
+            if (pt.j.S0) add(pt.j.S0 + bh * sn, 1.f);
+        } else if (mine) {
+            for (int i = pt.j.S0 ? 0 : 1; i <= part; ++i)
+                add(slots + i * sn, power(a, (part - i) * p.plan.len));
         }
-        auto store_S = [&]() {     // the bf16 copy that Q S reads
+        auto copy_S = [&] {        // the bf16 copy that Q S reads
             if (d < DK) {
                 uint8_t* dst = sm + Sm::S + d * 128;
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     uint4 x;
-                    x.x = tc::pack_bf16x2(S[8 * n], S[8 * n + 1]);
-                    x.y = tc::pack_bf16x2(S[8 * n + 2], S[8 * n + 3]);
-                    x.z = tc::pack_bf16x2(S[8 * n + 4], S[8 * n + 5]);
-                    x.w = tc::pack_bf16x2(S[8 * n + 6], S[8 * n + 7]);
+                    x.x = tc::pack_bf16x2(S[4 * n].x, S[4 * n].y);
+                    x.y = tc::pack_bf16x2(S[4 * n + 1].x, S[4 * n + 1].y);
+                    x.z = tc::pack_bf16x2(S[4 * n + 2].x, S[4 * n + 2].y);
+                    x.w = tc::pack_bf16x2(S[4 * n + 3].x, S[4 * n + 3].y);
                     *reinterpret_cast<uint4*>(dst + ((n ^ (d & 7)) << 4)) = x;
                 }
             }
             tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[B::S_READY]);
+            arrive(B::S_READY);
         };
-        if (!STATE_ONLY) store_S();
+        if (!STATE_ONLY) copy_S();
         const uint32_t ucol =
-            tmem + ((uint32_t)(32 * (warp - 8)) << 16) + kColU;
+            tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kColU;
+        for (int c = 0; c < nchunks; ++c) {
+            // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
+            const float grow = expm1f(a * (float)rows_of(c));
+            if (!wait_warp(B::U_FULL, c)) break;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < kNV; m += 8) {
+                float u[3][8];
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    tc::tmem_ld8(ucol + kNV * k + m, u[k]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float2& x = S[m / 2 + k];
+                    const float2 y =
+                        add2(make_float2(u[0][2 * k], u[0][2 * k + 1]),
+                             add2(make_float2(u[1][2 * k], u[1][2 * k + 1]),
+                                  make_float2(u[2][2 * k], u[2][2 * k + 1])));
+                    x = add2(fma2(both(grow), x, x), y);
+                }
+            }
+            tc::tc_fence_before();
+            if (c + 1 < nchunks) {
+                arrive(B::U_FREE);
+                if (!STATE_ONLY) {
+                    if (!wait_warp(B::S_FREE, c)) break;
+                    copy_S();
+                }
+            }
+        }
+        float* dst = STATE_ONLY ? slots + (part + 1) * sn
+                     : part + 1 == parts && pt.j.ST ? pt.j.ST + bh * sn
+                                                    : nullptr;
+        if (*reinterpret_cast<volatile int*>(abort_flag) == 0 && mine && dst)
+            store(dst);
+    } else if (warp >= 8 && warp < 16) {
+        // ------------------------- weighted V, then scores to P~ (row i)
+        const int gt = tid - 256, q = warp & 3, i = 32 * q + lane;
+        const int j0 = (warp - 8) >> 2 << 1;   // its two blocks of 32 columns
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
         for (int c = 0; c < nchunks; ++c) {
             const int n = rows_of(c);
-            if (!wait_warp(B::FULL + c % NS, c / NS)) break;
-            uint8_t* v = sm + c % NS * Sm::STAGE + Sm::V;
+            if (!wait_warp(B::FULL_V + c % NS, c / NS)) break;
+            if (c > 0 && !wait_warp(B::U_FULL, c - 1)) break;
+            uint8_t* v = sm + Sm::V + c % NS * kBox;
             uint32_t seen = 0;
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {      // 8 of 1024 16-byte pieces
-                const int at = (gt + 128 * i) * 16, j = (gt >> 3) + 16 * i;
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {      // 4 of 1024 16-byte pieces
+                const int at = (gt + 256 * m) * 16, j = (gt >> 3) + 32 * m;
                 // rows beyond the sequence are zero: their weight is any
                 const float f = w[max(0, rev ? n - kC + 1 + j : n - 1 - j)];
                 const uint4 x = *reinterpret_cast<const uint4*>(v + at);
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[3][4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int k = 0; k < 4; ++k) {
                     asm("fma.rn.bf16x2 %0, %1, %2, %0;"
-                        : "+r"(seen) : "r"(xs[m]), "r"(0u));
-                    float2 y = make_float2(
-                        __uint_as_float(xs[m] << 16) * f,
-                        __uint_as_float(xs[m] & 0xffff0000u) * f);
-                    o[0][m] = tc::pack_bf16x2(y.x, y.y);
-                    y = rest(y, o[0][m]);
-                    o[1][m] = tc::pack_bf16x2(y.x, y.y);
-                    y = rest(y, o[1][m]);
-                    o[2][m] = tc::pack_bf16x2(y.x, y.y);
+                        : "+r"(seen) : "r"(xs[k]), "r"(0u));
+                    float2 y = mul2(from_bf16x2(xs[k]), both(f));
+                    o[0][k] = tc::pack_bf16x2(y.x, y.y);
+                    y = rest(y, o[0][k]);
+                    o[1][k] = tc::pack_bf16x2(y.x, y.y);
+                    y = rest(y, o[1][k]);
+                    o[2][k] = tc::pack_bf16x2(y.x, y.y);
                 }
 #pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    *reinterpret_cast<uint4*>(sm + Sm::VW + m * kBox + at) =
-                        make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint4*>(sm + Sm::VW + k * kBox + at) =
+                        make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
             }
             bool ok = true;
             if (!STATE_ONLY && (seen & 0x7fff7fffu)) {
-                // the outputs of chunk c - 2 have been read (those of c - 3
-                // had been before U of c - 1 was formed)
-                ok = c < 2 || wait(B::O_FREE, c - 2);
+                // the output warps are done with this slot's last chunk
+                const uint64_t t0 = tc::globaltimer_ns();
+                for (int o = 0; o < 4 && ok; ++o)
+                    while (ok && done[o] < c - 1)
+                        ok = *reinterpret_cast<volatile int*>(abort_flag) ==
+                                 0 &&
+                             tc::globaltimer_ns() - t0 < p.limit_ns;
+                if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+                __threadfence_block();
                 const int slot = c & 1;
-                for (int i = 0; i < 8 && ok; ++i) {
-                    const int piece = gt + 128 * i, j = piece >> 3;
+                for (int m = 0; m < 4 && ok; ++m) {
+                    const int piece = gt + 256 * m, j = piece >> 3;
                     uint16_t* x =
                         reinterpret_cast<uint16_t*>(v + piece * 16);
-                    for (int m = 0; m < 8; ++m) {
-                        if ((x[m] & 0x7f80) != 0x7f80) continue;
-                        x[m] = 0;
-                        const int col = ((piece & 7) ^ (j & 7)) * 8 + m;
+                    for (int k = 0; k < 8; ++k) {
+                        if ((x[k] & 0x7f80) != 0x7f80) continue;
+                        x[k] = 0;
+                        const int col = ((piece & 7) ^ (j & 7)) * 8 + k;
                         const int r = rev ? kC - 1 - j : j;
                         for (int o = 0; o < 4; ++o) {
                             // bytes: a compare-and-swap on their word
@@ -508,39 +597,68 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             tc::fence_proxy_async_smem();
             if (!__all_sync(~0u, ok)) break;
-            if (lane == 0) tc::mbar_arrive(&bars[B::V_READY + (c & 1)]);
-            if (!wait_warp(B::U_FULL, c)) break;
+            arrive(B::V_READY);
+            if (STATE_ONLY) continue;
+            if (!wait_warp(B::SC_FULL, c)) break;
+            if (c > 0 && !wait_warp(B::O_FULL, c - 1)) break;
             tc::tc_fence_after();
-            // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
-            const float grow = expm1f(a * (float)n);
+#pragma unroll 1
+            for (int jj = 0; jj < 2; ++jj) {
+                const int j = j0 + jj;
+                float u[16];
+                uint32_t* pk = reinterpret_cast<uint32_t*>(u);
+                float x[32];
+                const bool none = rev ? j < q : j > q;
+                if (!none) {
+                    tc::tmem_ld32(lanes + kColSC + 32 * j, x);
+                    tc::tmem_ld_wait();
+                }
+                if (jj == 1) {
+                    tc::tc_fence_before();
+                    arrive(B::SC_FREE);
+                }
+                if (none) {
 #pragma unroll
-            for (int m = 0; m < kNV; m += 32) {
-                float u[32];
-                tc::tmem_ld32(ucol + m, u);
-                tc::tmem_ld_wait();
+                    for (int m = 0; m < 16; ++m) pk[m] = 0;
+                } else {
+                    if (j == q) {
+                        // what is masked is not multiplied by 0
+                        const float* g = dw + 31 + lane;
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    S[m + k] = fmaf(grow, S[m + k], S[m + k]) + u[k];
+                        for (int m = 0; m < 32; ++m)
+                            x[m] = g[-m] >= 0.f ? x[m] * g[-m] : 0.f;
+                    } else {
+                        // w^(r - s) as a factor of the row and one of the
+                        // column, neither exponent negative
+                        const float2 f =
+                            both(w[rev ? 32 * j - i : i - 32 * j - 31]);
+#pragma unroll
+                        for (int m = 0; m < 32; m += 4) {
+                            const float4 g =
+                                *reinterpret_cast<const float4*>(&cw[m]);
+                            const float2 y =
+                                mul2(make_float2(x[m], x[m + 1]),
+                                     mul2(f, make_float2(g.x, g.y)));
+                            const float2 z =
+                                mul2(make_float2(x[m + 2], x[m + 3]),
+                                     mul2(f, make_float2(g.z, g.w)));
+                            x[m] = y.x, x[m + 1] = y.y;
+                            x[m + 2] = z.x, x[m + 3] = z.y;
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 16; ++m)
+                        pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
+                }
+                tc::tmem_st16(lanes + kColP + 16 * j, u);
             }
-            tc::tc_fence_before();     // U may be written again
-            if (!STATE_ONLY && c + 1 < nchunks) {
-                if (!wait_warp(B::S_FREE, c)) break;
-                store_S();
-            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            arrive(B::P_READY);
         }
-        const bool done = *reinterpret_cast<volatile int*>(abort_flag) == 0;
-        float* dst = STATE_ONLY
-            ? pt.ws + (bh * p.plan.parts + part + 1) * sn
-            : part + 1 == parts && pt.j.ST ? pt.j.ST + bh * sn : nullptr;
-        if (done && mine && dst) {
-#pragma unroll
-            for (int n = 0; n < kNV; ++n)
-                if (n0 + n < pt.j.dv)
-                    dst[row + (size_t)(n0 + n) * pt.j.s_c] = S[n];
-        }
-    } else if (warp >= 12 && !STATE_ONLY) {
+    } else if (warp >= 16 && !STATE_ONLY) {
         // ------------------------------------------------ outputs (row i)
-        const int q = warp - 12, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
+        const int q = warp - 16, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
         const float f = w[r + e];
         const int width = min(kNV, pt.j.dv - n0);
         const size_t dv = pt.j.dv;
@@ -548,59 +666,66 @@ linattn_tc(const __grid_constant__ Maps maps,
         bf16* out = static_cast<bf16*>(pt.j.o);
         const uintptr_t align = reinterpret_cast<uintptr_t>(out) | dv * 2;
         for (int c = 0; c < nchunks; ++c) {
-            // (the flags are set before V_READY; its phase after the next
-            // does not begin before these outputs are read)
-            if (!wait_warp(B::O_FULL, c) ||
-                !wait_warp(B::V_READY + (c & 1), c >> 1))
-                break;
+            if (!wait_warp(B::O_FULL, c)) break;
             tc::tc_fence_after();
-            uint32_t pk[kNV / 2];
             const bool any = flag[(c & 1) * 4 + q] != 0;
             uint8_t* own = bad + ((c & 1) * 4 + q) * 64;
-#pragma unroll
+            const bool some = r < rows_of(c);
+            bf16* dst = out + n0 +
+                (((size_t)b * p.T + (some ? tile_token(c) + i : 0)) * p.H +
+                 h) * dv;
+#pragma unroll 1
             for (int m = 0; m < kNV; m += 16) {
                 float x[16], y[16];
+                uint32_t pk[8];
+                __syncwarp();        // (rows beyond the sequence store nothing)
                 tc::tmem_ld16(lanes + kColPV + m, x);
                 tc::tmem_ld16(lanes + kColQS + m, y);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    x[n] = fmaf(f, y[n], x[n]);
-                    if (any && r >= own[m + n])
-                        x[n] = __uint_as_float(0x7fc00000u);
+                for (int n = 0; n < 16; n += 2) {
+                    const float2 z = fma2(both(f), make_float2(y[n], y[n + 1]),
+                                          make_float2(x[n], x[n + 1]));
+                    x[n] = z.x, x[n + 1] = z.y;
+                }
+                if (any) {
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        if (r >= own[m + n]) x[n] = __uint_as_float(0x7fc00000u);
+                }
+                if (m + 16 == kNV) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (any) {
+                        own[lane] = own[lane + 32] = 255;
+                        if (lane == 0) flag[(c & 1) * 4 + q] = 0;
+                        __threadfence_block();
+                        __syncwarp();
+                    }
+                    if (lane == 0) done[q] = c + 1;
+                    arrive(B::O_FREE);
                 }
 #pragma unroll
                 for (int n = 0; n < 8; ++n)
-                    pk[m / 2 + n] = tc::pack_bf16x2(x[2 * n], x[2 * n + 1]);
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (any) {
-                own[lane] = own[lane + 32] = 255;
-                if (lane == 0) flag[(c & 1) * 4 + q] = 0;
-                __syncwarp();
-            }
-            if (lane == 0) tc::mbar_arrive(&bars[B::O_FREE]);
-            if (r >= rows_of(c)) continue;
-            const size_t t = (size_t)(tile_token(c) + i);
-            bf16* dst = out + (((size_t)b * p.T + t) * p.H + h) * dv + n0;
-            if (align % 32 == 0) {
+                    pk[n] = tc::pack_bf16x2(x[2 * n], x[2 * n + 1]);
+                if (some && m < width) {
+                    if (align % 32 == 0) {
+                        st_global_32(dst + m, pk);
+                    } else if (align % 16 == 0) {
+                        *reinterpret_cast<uint4*>(dst + m) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        if (m + 8 < width)
+                            *reinterpret_cast<uint4*>(dst + m + 8) =
+                                make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    } else {
 #pragma unroll
-                for (int n = 0; n < kNV; n += 16)
-                    if (n < width) st_global_32(dst + n, pk + n / 2);
-            } else if (align % 16 == 0) {
-#pragma unroll
-                for (int n = 0; n < kNV; n += 8)
-                    if (n < width)
-                        *reinterpret_cast<uint4*>(dst + n) =
-                            make_uint4(pk[n / 2], pk[n / 2 + 1],
-                                       pk[n / 2 + 2], pk[n / 2 + 3]);
-            } else {
-#pragma unroll
-                for (int n = 0; n < kNV; ++n)
-                    if (n < width)
-                        reinterpret_cast<uint16_t*>(dst)[n] =
-                            (uint16_t)(n & 1 ? pk[n / 2] >> 16 : pk[n / 2]);
+                        for (int n = 0; n < 16; ++n)
+                            if (m + n < width)
+                                reinterpret_cast<uint16_t*>(dst)[m + n] =
+                                    (uint16_t)(n & 1 ? pk[n / 2] >> 16
+                                                     : pk[n / 2]);
+                    }
+                }
             }
         }
     }
@@ -609,13 +734,18 @@ linattn_tc(const __grid_constant__ Maps maps,
     __syncthreads();
     if (*reinterpret_cast<volatile int*>(abort_flag)) {
         constexpr uint64_t kDrain = 100000000ull;
-        if (tid == 32 && last_bar >= 0)
+        if (warp == 1 && last_bar >= 0)   // (the lane that issued)
             tc::mbar_wait(&bars[last_bar], last_phase & 1, kDrain);
         if (tid == 0) {
             atomicOr(&g_fault_la, 1u);
+            // copies in flight: at most the last turn of each ring (a barrier
+            // that a copy of the turn was never armed for runs out)
             const int n = *reinterpret_cast<volatile int*>(issued);
-            for (int c = n - NS < 0 ? 0 : n - NS; c < n; ++c)
+            for (int c = n - NS < 0 ? 0 : n - NS; c < n; ++c) {
                 tc::mbar_wait(&bars[B::FULL + c % NS], (c / NS) & 1, kDrain);
+                tc::mbar_wait(&bars[B::FULL_V + c % NS], (c / NS) & 1,
+                              kDrain);
+            }
         }
     }
     tc::tc_fence_before();
