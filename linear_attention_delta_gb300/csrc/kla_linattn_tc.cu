@@ -17,10 +17,12 @@
 // The weighted V of U is split into three bf16 parts (24 bits), so that the
 // state keeps the digits of fp32.
 //
-// Warps: 0 copies (TMA), 1 issues the products, 4-7 hold the state (thread =
-// row of S), 8-15 weight V and turn scores into P~ (thread = row and half of
-// the columns), 16-19 write the outputs (thread = row).  They hand over
-// through mbarriers.
+// Warps: 0-7 hold the state (thread = row of S and half of its columns), 8-15
+// weight V, 16-23 turn scores into P~ (thread = row and half of the columns),
+// 24-27 write the outputs (thread = row), 28 issues the products, 29 the
+// copies (TMA).  They hand over through mbarriers.  Many warps with few
+// registers, because what bounds a chunk is the latency of their instructions
+// (with 18 warps half of the issue slots stay empty).
 //
 // In reverse the tiles lie in memory order all the same; r counts from the
 // tile's last row, masks and weights are mirrored.
@@ -50,7 +52,8 @@ using bf16 = __nv_bfloat16;
 __device__ unsigned int g_fault_la = 0;
 
 constexpr int kC = 128;          // tokens a chunk
-constexpr int kThreads = 640;
+constexpr int kThreads = 960;    // 64 registers each
+constexpr int kIssuer = 28, kCopier = 29;   // warps
 constexpr int kBox = kC * 128;   // bytes of a TMA box: 128 rows of 64 bf16
 constexpr int kMaxJobs = 3;
 
@@ -70,8 +73,8 @@ struct Smem {
     static constexpr int S = VW + 3 * kBox;      // DK rows of 128 bytes
     static constexpr int W = S + DK * 128;       // w^0 .. w^128
     static constexpr int CW = W + 4 * 132;       // factors of 32 columns
-    static constexpr int DW = CW + 4 * 32;       // of a diagonal block
-    static constexpr int BAD = DW + 4 * 64;      // [2][4 warps][64]: see below
+    static constexpr int MASK = CW + 4 * 32;     // of a diagonal block
+    static constexpr int BAD = MASK + 4 * 64;    // [2][4 warps][64]: see below
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
     static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
     static constexpr int BARS = DONE + 4 * 4;
@@ -158,6 +161,17 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* u) {
         : "memory");
 }
 
+// 32 lanes x 8 consecutive 32-bit columns per warp.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr,
+                                         const uint32_t (&u)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]),
+        "r"(u[6]), "r"(u[7])
+        : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -166,6 +180,33 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
     return r != 0;
+}
+
+// The slow half of wait_phase: false, with *abort set, when `limit_ns` have
+// passed or another warp has given up.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity,
+                                       volatile int* abort,
+                                       uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        const uint64_t t = tc::globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) *abort = 1;
+    }
+}
+
+// Waits for the phase with the given parity; false when it gave up.  (The
+// clock is slow to read: not before some turns.)
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort,
+                                           uint64_t limit_ns) {
+    const uint32_t at = tc::smem_u32(bar);
+    if (tc::mbar_try_wait(at, parity)) return true;
+    return wait_long(at, parity, abort, limit_ns);
 }
 
 // Whether the phase has completed, without waiting.
@@ -199,7 +240,7 @@ linattn_tc(const __grid_constant__ Maps maps,
     const uint32_t sbase = tc::smem_u32(sm);
     float* w = reinterpret_cast<float*>(sm + Sm::W);
     float* cw = reinterpret_cast<float*>(sm + Sm::CW);
-    float* dw = reinterpret_cast<float*>(sm + Sm::DW);
+    uint32_t* mask = reinterpret_cast<uint32_t*>(sm + Sm::MASK);
     // for each of two chunks, output warp and column: the first row (counted
     // as r) whose V is not finite, 255: none
     uint8_t* bad = sm + Sm::BAD;
@@ -207,7 +248,7 @@ linattn_tc(const __grid_constant__ Maps maps,
     // chunks whose outputs each output warp has read
     volatile int* done = reinterpret_cast<int*>(sm + Sm::DONE);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sm::BARS);
-    int* abort_flag = reinterpret_cast<int*>(sm + Sm::MISC);
+    volatile int* abort = reinterpret_cast<int*>(sm + Sm::MISC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sm::MISC + 4);
     int* issued = reinterpret_cast<int*>(sm + Sm::MISC + 8);
 
@@ -239,24 +280,27 @@ linattn_tc(const __grid_constant__ Maps maps,
             // groups arrive once a warp; O_FULL by the products' end and by
             // the thread that issued them
             const int count =
-                i == B::SC_FREE || i == B::P_READY || i == B::V_READY ? 8
-                : i == B::U_FREE || i == B::S_READY || i == B::O_FREE ? 4
-                : i == B::O_FULL ? 2 : 1;
+                i == B::SC_FREE || i == B::P_READY || i == B::V_READY ||
+                        i == B::U_FREE || i == B::S_READY ? 8
+                : i == B::O_FREE ? 4 : i == B::O_FULL ? 2 : 1;
             tc::mbar_init(&bars[i], count);
         }
         tc::fence_mbar_init();
-        *abort_flag = 0;
+        *abort = 0;
         *issued = 0;
     }
     if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
-    // column m of a block of scores left of its row's own block: w^(31 - m) (in
-    // reverse w^m) times a factor of the row; on the diagonal entry 31 + lane
-    // - m is w^(lane - m) (w^(m - lane)), -1 what is masked
+    // column m of a block of 32 columns has the factor w^(31 - m) (in reverse
+    // w^m), next to one of the row; on the diagonal, columns m and m + 1 of row
+    // i keep what entry 31 + i - m leaves of their pair of bf16
     if (tid >= 256 && tid < 288)
         cw[tid - 256] = power(a, rev ? tid - 256 : 287 - tid);
     if (tid >= 288 && tid < 352) {
-        const int d = rev ? 319 - tid : tid - 319;
-        dw[tid - 288] = d >= 0 ? power(a, d) : -1.f;
+        const int d = tid - 288 - 31;        // i - m
+        mask[tid - 288] = rev ? (d <= 0 ? 0xffffu : 0u) |
+                                    (d <= 1 ? 0xffff0000u : 0u)
+                              : (d >= 0 ? 0xffffu : 0u) |
+                                    (d >= 1 ? 0xffff0000u : 0u);
     }
     for (int i = tid; i < 2 * 4 * 64; i += kThreads) bad[i] = 255;
     if (tid < 8) flag[tid] = 0;
@@ -267,14 +311,15 @@ linattn_tc(const __grid_constant__ Maps maps,
     const uint32_t tmem = *tmem_slot;
 
     auto wait = [&](int bar, int phase) {
-        const bool ok = tc::mbar_wait_or_abort(&bars[bar], phase & 1,
-                                               abort_flag, p.limit_ns);
-        if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
-        return ok;
+        return wait_phase(&bars[bar], phase & 1, abort, p.limit_ns);
     };
+    // For all lanes.  Where the wait gave up the warp goes on (with what is in
+    // place, in bounds all the same) and leaves at the end of its chunk.
     auto wait_warp = [&](int bar, int phase) {
-        return __all_sync(~0u, wait(bar, phase));
+        wait(bar, phase);
+        __syncwarp();
     };
+    auto gave_up = [&] { return __any_sync(~0u, *abort != 0); };
     // one arrival of a warp whose lanes are done (each with its own fences)
     auto arrive = [&](int bar) {
         __syncwarp();
@@ -290,12 +335,9 @@ linattn_tc(const __grid_constant__ Maps maps,
 
     int last_bar = -1, last_phase = 0;   // the issuer's last commit
 
-    if (tid == 0 && !p.selftest) {
+    if (tid == 32 * kCopier) {
         // ------------------------------------------------------ copies
-        tc::prefetch_tmap(&maps.k[job]);
-        tc::prefetch_tmap(&maps.v[job]);
-        if (!STATE_ONLY) tc::prefetch_tmap(&maps.q[job]);
-        for (int c = 0; c < nchunks; ++c) {
+        for (int c = 0; c < nchunks && !p.selftest; ++c) {
             const int s = c % NS, turn = c / NS;
             uint64_t* full = &bars[B::FULL + s];
             const int t = tile_token(c);
@@ -319,7 +361,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             tc::tma_load_4d(sm + Sm::V + s * kBox, &maps.v[job],
                             &bars[B::FULL_V + s], n0, h, t, b);
         }
-    } else if (warp == 1) {
+    } else if (warp == kIssuer) {
         // ---------------------------------------------------- products
         // The whole warp walks the chunks, one lane issues; what the products
         // take is the same in all lanes, so it stays in uniform registers.
@@ -338,8 +380,8 @@ linattn_tc(const __grid_constant__ Maps maps,
         };
         auto scores = [&](int c) {
             const uint32_t at = c % NS * (Sm::TILE >> 4);
-            if (!wait_warp(B::FULL + c % NS, c / NS)) return false;
-            if (c > 0 && !wait_warp(B::SC_FREE, c - 1)) return false;
+            wait_warp(B::FULL + c % NS, c / NS);
+            if (c > 0) wait_warp(B::SC_FREE, c - 1);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
@@ -349,20 +391,19 @@ linattn_tc(const __grid_constant__ Maps maps,
                 commit(B::SC_FULL, c);
             }
             __syncwarp();
-            return true;
         };
         int scored = 0;      // chunks whose scores are issued
-        for (int c = 0; c < nchunks; ++c) {
+        for (int c = 0; c < nchunks && !gave_up(); ++c) {
             const int s = c % NS;
             const uint32_t at = s * (Sm::TILE >> 4);
             const bool again = c + NS < nchunks;   // the stage is loaded again
             if (!STATE_ONLY && scored == c) {
-                if (!scores(c)) break;
+                scores(c);
                 scored = c + 1;
             }
-            if (!wait_warp(B::V_READY, c)) break;
-            if (STATE_ONLY && !wait_warp(B::FULL + s, c / NS)) break;
-            if (c > 0 && !wait_warp(B::U_FREE, c - 1)) break;
+            wait_warp(B::V_READY, c);
+            if (STATE_ONLY) wait_warp(B::FULL + s, c / NS);
+            if (c > 0) wait_warp(B::U_FREE, c - 1);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
@@ -376,8 +417,8 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             __syncwarp();
             if (STATE_ONLY) continue;
-            if (!wait_warp(B::S_READY, c)) break;
-            if (c > 0 && !wait_warp(B::O_FREE, c - 1)) break;
+            wait_warp(B::S_READY, c);
+            if (c > 0) wait_warp(B::O_FREE, c - 1);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
@@ -394,10 +435,9 @@ linattn_tc(const __grid_constant__ Maps maps,
                 __all_sync(~0u, mbar_test(&bars[B::FULL + scored % NS],
                                           scored / NS & 1) &&
                                     mbar_test(&bars[B::SC_FREE], c & 1))) {
-                if (!scores(scored)) break;
-                ++scored;
+                scores(scored++);
             }
-            if (!wait_warp(B::P_READY, c)) break;
+            wait_warp(B::P_READY, c);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
@@ -411,25 +451,26 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             __syncwarp();
         }
-    } else if (warp >= 4 && warp < 8) {
-        // --------------------------------------------------- state (row d)
-        const int d = tid - 128;
+    } else if (warp < 8) {
+        // ------------------------------ state (row d, columns c0 .. c0 + 31)
+        constexpr int W = kNV / 2;
+        const int d = tid & 127, c0 = n0 + (warp >> 2) * W;
         const bool mine = d < pt.j.dk;
         const size_t row = (size_t)d * pt.j.s_r;
         const size_t sn = (size_t)pt.j.dk * pt.j.dv;
-        float2 S[kNV / 2];
+        float2 S[W / 2];
         auto clear = [&] {
 #pragma unroll
-            for (int n = 0; n < kNV / 2; ++n) S[n] = both(0.f);
+            for (int n = 0; n < W / 2; ++n) S[n] = both(0.f);
         };
         clear();
         // S += f x of a state in memory
         auto add = [&](const float* x, float f) {
-            x += row + (size_t)n0 * pt.j.s_c;
-            if (pt.j.s_c == 1 && pt.j.dv % kNV == 0 &&
+            x += row + (size_t)c0 * pt.j.s_c;
+            if (pt.j.s_c == 1 && c0 + W <= pt.j.dv &&
                 (reinterpret_cast<uintptr_t>(x) & 15) == 0) {
 #pragma unroll
-                for (int n = 0; n < kNV / 2; n += 2) {
+                for (int n = 0; n < W / 2; n += 2) {
                     const float4 y =
                         *reinterpret_cast<const float4*>(x + 2 * n);
                     S[n] = fma2(both(f), make_float2(y.x, y.y), S[n]);
@@ -437,18 +478,18 @@ linattn_tc(const __grid_constant__ Maps maps,
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < kNV; ++n) {
+                for (int n = 0; n < W; ++n) {
                     float& s = n & 1 ? S[n / 2].y : S[n / 2].x;
-                    if (n0 + n < pt.j.dv)
+                    if (c0 + n < pt.j.dv)
                         s = fmaf(f, x[(size_t)n * pt.j.s_c], s);
                 }
             }
         };
         auto store = [&](float* x) {
-            x += row + (size_t)n0 * pt.j.s_c;
+            x += row + (size_t)c0 * pt.j.s_c;
 #pragma unroll
-            for (int n = 0; n < kNV; ++n)
-                if (n0 + n < pt.j.dv)
+            for (int n = 0; n < W; ++n)
+                if (c0 + n < pt.j.dv)
                     x[(size_t)n * pt.j.s_c] = n & 1 ? S[n / 2].y : S[n / 2].x;
         };
         float* slots = pt.ws ? pt.ws + bh * p.plan.parts * sn : nullptr;
@@ -468,13 +509,14 @@ linattn_tc(const __grid_constant__ Maps maps,
             if (d < DK) {
                 uint8_t* dst = sm + Sm::S + d * 128;
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
+                for (int n = 0; n < W / 8; ++n) {
                     uint4 x;
                     x.x = tc::pack_bf16x2(S[4 * n].x, S[4 * n].y);
                     x.y = tc::pack_bf16x2(S[4 * n + 1].x, S[4 * n + 1].y);
                     x.z = tc::pack_bf16x2(S[4 * n + 2].x, S[4 * n + 2].y);
                     x.w = tc::pack_bf16x2(S[4 * n + 3].x, S[4 * n + 3].y);
-                    *reinterpret_cast<uint4*>(dst + ((n ^ (d & 7)) << 4)) = x;
+                    const int at = (warp >> 2) * (W / 8) + n;   // of 8 in the row
+                    *reinterpret_cast<uint4*>(dst + ((at ^ (d & 7)) << 4)) = x;
                 }
             }
             tc::fence_proxy_async_smem();
@@ -482,14 +524,14 @@ linattn_tc(const __grid_constant__ Maps maps,
         };
         if (!STATE_ONLY) copy_S();
         const uint32_t ucol =
-            tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kColU;
-        for (int c = 0; c < nchunks; ++c) {
+            tmem + ((uint32_t)(d & 96) << 16) + kColU + (warp >> 2) * W;
+        for (int c = 0; c < nchunks && !gave_up(); ++c) {
             // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
             const float grow = expm1f(a * (float)rows_of(c));
-            if (!wait_warp(B::U_FULL, c)) break;
+            wait_warp(B::U_FULL, c);
             tc::tc_fence_after();
 #pragma unroll
-            for (int m = 0; m < kNV; m += 8) {
+            for (int m = 0; m < W; m += 8) {
                 float u[3][8];
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
@@ -509,7 +551,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             if (c + 1 < nchunks) {
                 arrive(B::U_FREE);
                 if (!STATE_ONLY) {
-                    if (!wait_warp(B::S_FREE, c)) break;
+                    wait_warp(B::S_FREE, c);
                     copy_S();
                 }
             }
@@ -517,17 +559,15 @@ linattn_tc(const __grid_constant__ Maps maps,
         float* dst = STATE_ONLY ? slots + (part + 1) * sn
                      : part + 1 == parts && pt.j.ST ? pt.j.ST + bh * sn
                                                     : nullptr;
-        if (*reinterpret_cast<volatile int*>(abort_flag) == 0 && mine && dst)
+        if (*abort == 0 && mine && dst)
             store(dst);
-    } else if (warp >= 8 && warp < 16) {
-        // ------------------------- weighted V, then scores to P~ (row i)
-        const int gt = tid - 256, q = warp & 3, i = 32 * q + lane;
-        const int j0 = (warp - 8) >> 2 << 1;   // its two blocks of 32 columns
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-        for (int c = 0; c < nchunks; ++c) {
+    } else if (warp < 16) {
+        // ------------------------------------------------------ weighted V
+        const int gt = tid - 256;
+        for (int c = 0; c < nchunks && !gave_up(); ++c) {
             const int n = rows_of(c);
-            if (!wait_warp(B::FULL_V + c % NS, c / NS)) break;
-            if (c > 0 && !wait_warp(B::U_FULL, c - 1)) break;
+            wait_warp(B::FULL_V + c % NS, c / NS);
+            if (c > 0) wait_warp(B::U_FULL, c - 1);
             uint8_t* v = sm + Sm::V + c % NS * kBox;
             uint32_t seen = 0;
 #pragma unroll 1
@@ -540,14 +580,13 @@ linattn_tc(const __grid_constant__ Maps maps,
                 uint32_t o[3][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    asm("fma.rn.bf16x2 %0, %1, %2, %0;"
-                        : "+r"(seen) : "r"(xs[k]), "r"(0u));
                     float2 y = mul2(from_bf16x2(xs[k]), both(f));
                     o[0][k] = tc::pack_bf16x2(y.x, y.y);
                     y = rest(y, o[0][k]);
                     o[1][k] = tc::pack_bf16x2(y.x, y.y);
                     y = rest(y, o[1][k]);
                     o[2][k] = tc::pack_bf16x2(y.x, y.y);
+                    seen |= o[2][k];
                 }
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
@@ -555,15 +594,17 @@ linattn_tc(const __grid_constant__ Maps maps,
                         make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
             }
             bool ok = true;
-            if (!STATE_ONLY && (seen & 0x7fff7fffu)) {
+            // the third part of what is not finite is NaN; those of others are
+            // below 2 unless the value is above 2^16: the exponent's top bit
+            // tells where to look
+            if (!STATE_ONLY && (seen & 0x40004000u)) {
                 // the output warps are done with this slot's last chunk
                 const uint64_t t0 = tc::globaltimer_ns();
                 for (int o = 0; o < 4 && ok; ++o)
                     while (ok && done[o] < c - 1)
-                        ok = *reinterpret_cast<volatile int*>(abort_flag) ==
-                                 0 &&
+                        ok = *abort == 0 &&
                              tc::globaltimer_ns() - t0 < p.limit_ns;
-                if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+                if (!ok) *abort = 1;
                 __threadfence_block();
                 const int slot = c & 1;
                 for (int m = 0; m < 4 && ok; ++m) {
@@ -596,69 +637,82 @@ linattn_tc(const __grid_constant__ Maps maps,
                 }
             }
             tc::fence_proxy_async_smem();
-            if (!__all_sync(~0u, ok)) break;
             arrive(B::V_READY);
-            if (STATE_ONLY) continue;
-            if (!wait_warp(B::SC_FULL, c)) break;
-            if (c > 0 && !wait_warp(B::O_FULL, c - 1)) break;
+        }
+    } else if (warp < 24 && !STATE_ONLY) {
+        // ------------------------------------------- scores to P~ (row i)
+        const int q = warp & 3, i = 32 * q + lane;
+        const int j0 = (warp - 16) >> 2 << 1;   // its two blocks of 32 columns
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+        // The row's factor on the diagonal, w^(lane - 31) (in reverse
+        // w^-lane), is above 1: for decays that keep it in range
+        const bool gentle = fabsf(a) * 31.f <= 80.f;
+        const float f0 = power(a, rev ? -lane : lane - 31);
+        for (int c = 0; c < nchunks && !gave_up(); ++c) {
+            wait_warp(B::SC_FULL, c);
+            if (c > 0) wait_warp(B::O_FULL, c - 1);
             tc::tc_fence_after();
 #pragma unroll 1
-            for (int jj = 0; jj < 2; ++jj) {
-                const int j = j0 + jj;
-                float u[16];
-                uint32_t* pk = reinterpret_cast<uint32_t*>(u);
-                float x[32];
+            for (int at = 32 * j0; at < 32 * j0 + 64; at += 16) {
+                const int j = at >> 5, m0 = at & 16;   // block, column in it
+                uint32_t pk[8];
+                float x[16];
                 const bool none = rev ? j < q : j > q;
                 if (!none) {
-                    tc::tmem_ld32(lanes + kColSC + 32 * j, x);
+                    tc::tmem_ld16(lanes + kColSC + at, x);
                     tc::tmem_ld_wait();
                 }
-                if (jj == 1) {
+                if (at == 32 * j0 + 48) {
                     tc::tc_fence_before();
                     arrive(B::SC_FREE);
                 }
                 if (none) {
 #pragma unroll
-                    for (int m = 0; m < 16; ++m) pk[m] = 0;
+                    for (int m = 0; m < 8; ++m) pk[m] = 0;
                 } else {
-                    if (j == q) {
-                        // what is masked is not multiplied by 0
-                        const float* g = dw + 31 + lane;
-#pragma unroll
-                        for (int m = 0; m < 32; ++m)
-                            x[m] = g[-m] >= 0.f ? x[m] * g[-m] : 0.f;
-                    } else {
+                    if (j < q || j > q || gentle) {
                         // w^(r - s) as a factor of the row and one of the
-                        // column, neither exponent negative
+                        // column
                         const float2 f =
-                            both(w[rev ? 32 * j - i : i - 32 * j - 31]);
+                            both(j == q ? f0 : w[rev ? 32 * j - i
+                                                     : i - 32 * j - 31]);
 #pragma unroll
-                        for (int m = 0; m < 32; m += 4) {
+                        for (int m = 0; m < 16; m += 4) {
                             const float4 g =
-                                *reinterpret_cast<const float4*>(&cw[m]);
+                                *reinterpret_cast<const float4*>(&cw[m0 + m]);
                             const float2 y =
                                 mul2(make_float2(x[m], x[m + 1]),
                                      mul2(f, make_float2(g.x, g.y)));
                             const float2 z =
                                 mul2(make_float2(x[m + 2], x[m + 3]),
                                      mul2(f, make_float2(g.z, g.w)));
-                            x[m] = y.x, x[m + 1] = y.y;
-                            x[m + 2] = z.x, x[m + 3] = z.y;
+                            pk[m / 2] = tc::pack_bf16x2(y.x, y.y);
+                            pk[m / 2 + 1] = tc::pack_bf16x2(z.x, z.y);
                         }
-                    }
+                    } else {
+                        const int d = rev ? m0 - lane : lane - m0;
 #pragma unroll
-                    for (int m = 0; m < 16; ++m)
-                        pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
+                        for (int m = 0; m < 16; ++m)
+                            x[m] *= w[max(0, rev ? d + m : d - m)];
+#pragma unroll
+                        for (int m = 0; m < 8; ++m)
+                            pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
+                    }
+                    if (j == q) {    // masked, not multiplied by 0
+                        const uint32_t* keep = mask + 31 + lane - m0;
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) pk[m] &= keep[-2 * m];
+                    }
                 }
-                tc::tmem_st16(lanes + kColP + 16 * j, u);
+                tmem_st8(lanes + kColP + at / 2, pk);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
             arrive(B::P_READY);
         }
-    } else if (warp >= 16 && !STATE_ONLY) {
+    } else if (warp < 28 && !STATE_ONLY) {
         // ------------------------------------------------ outputs (row i)
-        const int q = warp - 16, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
+        const int q = warp - 24, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
         const float f = w[r + e];
         const int width = min(kNV, pt.j.dv - n0);
         const size_t dv = pt.j.dv;
@@ -666,7 +720,8 @@ linattn_tc(const __grid_constant__ Maps maps,
         bf16* out = static_cast<bf16*>(pt.j.o);
         const uintptr_t align = reinterpret_cast<uintptr_t>(out) | dv * 2;
         for (int c = 0; c < nchunks; ++c) {
-            if (!wait_warp(B::O_FULL, c)) break;
+            wait_warp(B::O_FULL, c);
+            if (gave_up()) break;      // writes nothing
             tc::tc_fence_after();
             const bool any = flag[(c & 1) * 4 + q] != 0;
             uint8_t* own = bad + ((c & 1) * 4 + q) * 64;
@@ -732,9 +787,9 @@ linattn_tc(const __grid_constant__ Maps maps,
 
     __syncwarp();
     __syncthreads();
-    if (*reinterpret_cast<volatile int*>(abort_flag)) {
+    if (*abort) {
         constexpr uint64_t kDrain = 100000000ull;
-        if (warp == 1 && last_bar >= 0)   // (the lane that issued)
+        if (warp == kIssuer && last_bar >= 0)   // (the lane that issued)
             tc::mbar_wait(&bars[last_bar], last_phase & 1, kDrain);
         if (tid == 0) {
             atomicOr(&g_fault_la, 1u);
