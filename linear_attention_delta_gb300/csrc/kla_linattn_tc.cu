@@ -4,10 +4,15 @@
 // A block owns 64 columns of the state of one (pass, sequence, head, part)
 // and walks its chunks (S the state before a chunk, w = exp(log_decay)):
 //   P  = Q K^T                         128 x 128   scores, fp32 in TMEM
-//   P~ = P o w^(r - s), s <= r          in place    bf16, again in TMEM
-//   O  = P~ V + diag(w^(r + e)) Q S    two accumulators, joined on the way out
+//   P~ = P o w^(r - s), s <= r                      bf16, again in TMEM
+//   O  = diag(w^(r + e)) Q S + P~ V    128 x 64    one accumulator
 //   U  = K^T diag(w^(n - e - s)) V     128 x 64
 //   S <- w^n S + U                     fp32, in registers
+// For Q S and P~ V to share an accumulator, w^(r - 63) is taken out of a row
+// and multiplied in as it is written: P~ has the factor w^(63 - s) of its
+// column, and S that of w^(63 + e).  Decays whose powers would leave the range
+// (64 |log_decay| > 60) have their rows of Q S scaled in TMEM instead, and
+// every score its own factor.
 // U does not depend on S, so the only chain from chunk to chunk is one
 // multiply-add of the state, and everything else runs ahead of it.
 //
@@ -72,13 +77,13 @@ struct Smem {
     static constexpr int VW = V + NS * kBox;     // 3 boxes
     static constexpr int S = VW + 3 * kBox;      // DK rows of 128 bytes
     static constexpr int W = S + DK * 128;       // w^0 .. w^128
-    static constexpr int CW = W + 4 * 132;       // factors of 32 columns
-    static constexpr int MASK = CW + 4 * 32;     // of a diagonal block
+    static constexpr int CW = W + 4 * 132;       // factors of the columns
+    static constexpr int MASK = CW + 4 * kC;     // of a diagonal block
     static constexpr int BAD = MASK + 4 * 64;    // [2][4 warps][64]: see below
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
     static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
     static constexpr int BARS = DONE + 4 * 4;
-    static constexpr int NUM_BARS = 5 * NS + 11;
+    static constexpr int NUM_BARS = 5 * NS + 12;
     static constexpr int MISC = BARS + 8 * NUM_BARS;   // abort, TMEM, issued
     static constexpr int BYTES = MISC + 16 + 1024;     // alignment
     static_assert(BYTES <= 232448, "shared memory");
@@ -101,15 +106,14 @@ struct Bars {
     static constexpr int U_FREE = 5 * NS + 5;    // read
     static constexpr int S_READY = 5 * NS + 6;   // copy of S in place
     static constexpr int S_FREE = 5 * NS + 7;    // Q S done
-    static constexpr int O_FULL = 5 * NS + 8;    // outputs in TMEM (P~ read)
-    static constexpr int O_FREE = 5 * NS + 9;    // read
+    static constexpr int O_FULL = 5 * NS + 8;    // 2: outputs in TMEM (P~ read)
+    static constexpr int O_FREE = 5 * NS + 10;   // 2: read
 };
 
 // TMEM columns: all 512
 constexpr uint32_t kColSC = 0;       // 128: scores
 constexpr uint32_t kColP = 128;      // 64: P~, two bf16 a column
-constexpr uint32_t kColPV = 192;     // 64
-constexpr uint32_t kColQS = 256;     // 64
+constexpr uint32_t kColO = 192;      // 2 x 64: outputs of even and odd chunks
 constexpr uint32_t kColU = 320;      // 3 x 64: U from each part of V
 constexpr uint32_t kTmemCols = 512;
 
@@ -282,7 +286,8 @@ linattn_tc(const __grid_constant__ Maps maps,
             const int count =
                 i == B::SC_FREE || i == B::P_READY || i == B::V_READY ||
                         i == B::U_FREE || i == B::S_READY ? 8
-                : i == B::O_FREE ? 4 : i == B::O_FULL ? 2 : 1;
+                : i == B::O_FREE || i == B::O_FREE + 1 ? 4
+                : i == B::O_FULL || i == B::O_FULL + 1 ? 2 : 1;
             tc::mbar_init(&bars[i], count);
         }
         tc::fence_mbar_init();
@@ -290,11 +295,14 @@ linattn_tc(const __grid_constant__ Maps maps,
         *issued = 0;
     }
     if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
-    // column m of a block of 32 columns has the factor w^(31 - m) (in reverse
-    // w^m), next to one of the row; on the diagonal, columns m and m + 1 of row
-    // i keep what entry 31 + i - m leaves of their pair of bf16
-    if (tid >= 256 && tid < 288)
-        cw[tid - 256] = power(a, rev ? tid - 256 : 287 - tid);
+    // column j has the factor w^(63 - s); on the diagonal, columns m and m + 1
+    // of a block of 32 keep in row i what entry 31 + i - m leaves of their pair
+    // of bf16
+    const bool gentle = fabsf(a) * 64.f <= 60.f;
+    if (tid >= 352 && tid < 352 + kC) {
+        const int j = tid - 352;
+        cw[j] = power(a, 63 - (rev ? kC - 1 - j : j));
+    }
     if (tid >= 288 && tid < 352) {
         const int d = tid - 288 - 31;        // i - m
         mask[tid - 288] = rev ? (d <= 0 ? 0xffffu : 0u) |
@@ -417,14 +425,15 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             __syncwarp();
             if (STATE_ONLY) continue;
+            const uint32_t acc = tmem + kColO + kNV * (c & 1);
             wait_warp(B::S_READY, c);
-            if (c > 0) wait_warp(B::O_FREE, c - 1);
+            if (c > 1) wait_warp(B::O_FREE + (c & 1), (c >> 1) - 1);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks)
-                    tc::mma_bf16(tmem + kColQS, dQ + at + step_k(ks),
-                                 dS + ks * 128, kIdRow, ks > 0);
+                    tc::mma_bf16(acc, dQ + at + step_k(ks), dS + ks * 128,
+                                 kIdRow, ks > 0);
                 commit(B::S_FREE, c);
                 if (again) tc::mma_commit(&bars[B::EMPTY_Q + s]);
             }
@@ -433,20 +442,18 @@ linattn_tc(const __grid_constant__ Maps maps,
             // works while this chunk's become P~
             if (scored == c + 1 && scored < nchunks &&
                 __all_sync(~0u, mbar_test(&bars[B::FULL + scored % NS],
-                                          scored / NS & 1) &&
-                                    mbar_test(&bars[B::SC_FREE], c & 1))) {
+                                          scored / NS & 1)))
                 scores(scored++);
-            }
             wait_warp(B::P_READY, c);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll
                 for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts(tmem + kColPV, tmem + kColP + 8 * ks,
-                                dV + s * (kBox >> 4) + ks * 128, kIdRow,
-                                ks > 0);
-                commit(B::O_FULL, c);
-                tc::mbar_arrive(&bars[B::O_FULL]);   // hands on what it saw
+                    mma_bf16_ts(acc, tmem + kColP + 8 * ks,
+                                dV + s * (kBox >> 4) + ks * 128, kIdRow, true);
+                commit(B::O_FULL + (c & 1), c >> 1);
+                // hands on what it saw
+                tc::mbar_arrive(&bars[B::O_FULL + (c & 1)]);
                 if (again) tc::mma_commit(&bars[B::EMPTY_V + s]);
             }
             __syncwarp();
@@ -505,18 +512,21 @@ linattn_tc(const __grid_constant__ Maps maps,
             for (int i = pt.j.S0 ? 0 : 1; i <= part; ++i)
                 add(slots + i * sn, power(a, (part - i) * p.plan.len));
         }
+        const float2 fs = both(gentle ? power(a, 63 + e) : 1.f);
         auto copy_S = [&] {        // the bf16 copy that Q S reads
             if (d < DK) {
                 uint8_t* dst = sm + Sm::S + d * 128;
 #pragma unroll
                 for (int n = 0; n < W / 8; ++n) {
-                    uint4 x;
-                    x.x = tc::pack_bf16x2(S[4 * n].x, S[4 * n].y);
-                    x.y = tc::pack_bf16x2(S[4 * n + 1].x, S[4 * n + 1].y);
-                    x.z = tc::pack_bf16x2(S[4 * n + 2].x, S[4 * n + 2].y);
-                    x.w = tc::pack_bf16x2(S[4 * n + 3].x, S[4 * n + 3].y);
+                    uint32_t x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = mul2(fs, S[4 * n + k]);
+                        x[k] = tc::pack_bf16x2(y.x, y.y);
+                    }
                     const int at = (warp >> 2) * (W / 8) + n;   // of 8 in the row
-                    *reinterpret_cast<uint4*>(dst + ((at ^ (d & 7)) << 4)) = x;
+                    *reinterpret_cast<uint4*>(dst + ((at ^ (d & 7)) << 4)) =
+                        make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
             tc::fence_proxy_async_smem();
@@ -644,17 +654,33 @@ linattn_tc(const __grid_constant__ Maps maps,
         const int q = warp & 3, i = 32 * q + lane;
         const int j0 = (warp - 16) >> 2 << 1;   // its two blocks of 32 columns
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-        // The row's factor on the diagonal, w^(lane - 31) (in reverse
-        // w^-lane), is above 1: for decays that keep it in range
-        const bool gentle = fabsf(a) * 31.f <= 80.f;
-        const float f0 = power(a, rev ? -lane : lane - 31);
         for (int c = 0; c < nchunks && !gave_up(); ++c) {
+            if (!gentle) {       // rows of Q S, this warp's half of the columns
+                const float2 f = both(w[(rev ? kC - 1 - i : i) + e]);
+                const uint32_t acc = lanes + kColO + kNV * (c & 1) + 16 * j0;
+                wait_warp(B::S_FREE, c);
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int m = 0; m < kNV / 2; m += 8) {
+                    float x[8];
+                    uint32_t u[8];
+                    tc::tmem_ld8(acc + m, x);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 y = mul2(f, make_float2(x[k], x[k + 1]));
+                        u[k] = __float_as_uint(y.x);
+                        u[k + 1] = __float_as_uint(y.y);
+                    }
+                    tmem_st8(acc + m, u);
+                }
+            }
             wait_warp(B::SC_FULL, c);
-            if (c > 0) wait_warp(B::O_FULL, c - 1);
+            if (c > 0) wait_warp(B::O_FULL + ((c - 1) & 1), (c - 1) >> 1);
             tc::tc_fence_after();
 #pragma unroll 1
             for (int at = 32 * j0; at < 32 * j0 + 64; at += 16) {
-                const int j = at >> 5, m0 = at & 16;   // block, column in it
+                const int j = at >> 5;
                 uint32_t pk[8];
                 float x[16];
                 const bool none = rev ? j < q : j > q;
@@ -670,27 +696,21 @@ linattn_tc(const __grid_constant__ Maps maps,
 #pragma unroll
                     for (int m = 0; m < 8; ++m) pk[m] = 0;
                 } else {
-                    if (j < q || j > q || gentle) {
-                        // w^(r - s) as a factor of the row and one of the
-                        // column
-                        const float2 f =
-                            both(j == q ? f0 : w[rev ? 32 * j - i
-                                                     : i - 32 * j - 31]);
+                    if (gentle) {
 #pragma unroll
                         for (int m = 0; m < 16; m += 4) {
                             const float4 g =
-                                *reinterpret_cast<const float4*>(&cw[m0 + m]);
-                            const float2 y =
-                                mul2(make_float2(x[m], x[m + 1]),
-                                     mul2(f, make_float2(g.x, g.y)));
+                                *reinterpret_cast<const float4*>(&cw[at + m]);
+                            const float2 y = mul2(make_float2(x[m], x[m + 1]),
+                                                  make_float2(g.x, g.y));
                             const float2 z =
                                 mul2(make_float2(x[m + 2], x[m + 3]),
-                                     mul2(f, make_float2(g.z, g.w)));
+                                     make_float2(g.z, g.w));
                             pk[m / 2] = tc::pack_bf16x2(y.x, y.y);
                             pk[m / 2 + 1] = tc::pack_bf16x2(z.x, z.y);
                         }
                     } else {
-                        const int d = rev ? m0 - lane : lane - m0;
+                        const int d = rev ? at - i : i - at;
 #pragma unroll
                         for (int m = 0; m < 16; ++m)
                             x[m] *= w[max(0, rev ? d + m : d - m)];
@@ -699,7 +719,7 @@ linattn_tc(const __grid_constant__ Maps maps,
                             pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
                     }
                     if (j == q) {    // masked, not multiplied by 0
-                        const uint32_t* keep = mask + 31 + lane - m0;
+                        const uint32_t* keep = mask + 31 + lane - (at & 16);
 #pragma unroll
                         for (int m = 0; m < 8; ++m) pk[m] &= keep[-2 * m];
                     }
@@ -713,14 +733,14 @@ linattn_tc(const __grid_constant__ Maps maps,
     } else if (warp < 28 && !STATE_ONLY) {
         // ------------------------------------------------ outputs (row i)
         const int q = warp - 24, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
-        const float f = w[r + e];
+        const float2 f = both(gentle ? power(a, r - 63) : 1.f);
         const int width = min(kNV, pt.j.dv - n0);
         const size_t dv = pt.j.dv;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
         bf16* out = static_cast<bf16*>(pt.j.o);
         const uintptr_t align = reinterpret_cast<uintptr_t>(out) | dv * 2;
         for (int c = 0; c < nchunks; ++c) {
-            wait_warp(B::O_FULL, c);
+            wait_warp(B::O_FULL + (c & 1), c >> 1);
             if (gave_up()) break;      // writes nothing
             tc::tc_fence_after();
             const bool any = flag[(c & 1) * 4 + q] != 0;
@@ -731,17 +751,15 @@ linattn_tc(const __grid_constant__ Maps maps,
                  h) * dv;
 #pragma unroll 1
             for (int m = 0; m < kNV; m += 16) {
-                float x[16], y[16];
+                float x[16];
                 uint32_t pk[8];
                 __syncwarp();        // (rows beyond the sequence store nothing)
-                tc::tmem_ld16(lanes + kColPV + m, x);
-                tc::tmem_ld16(lanes + kColQS + m, y);
+                tc::tmem_ld16(lanes + kColO + kNV * (c & 1) + m, x);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int n = 0; n < 16; n += 2) {
-                    const float2 z = fma2(both(f), make_float2(y[n], y[n + 1]),
-                                          make_float2(x[n], x[n + 1]));
-                    x[n] = z.x, x[n + 1] = z.y;
+                    const float2 y = mul2(f, make_float2(x[n], x[n + 1]));
+                    x[n] = y.x, x[n + 1] = y.y;
                 }
                 if (any) {
 #pragma unroll
@@ -758,7 +776,7 @@ linattn_tc(const __grid_constant__ Maps maps,
                         __syncwarp();
                     }
                     if (lane == 0) done[q] = c + 1;
-                    arrive(B::O_FREE);
+                    arrive(B::O_FREE + (c & 1));
                 }
 #pragma unroll
                 for (int n = 0; n < 8; ++n)
