@@ -35,6 +35,7 @@ __device__ __forceinline__ float state_before(const Part& p, const Plan& pl,
     const size_t n = (size_t)p.j.dk * p.j.dv;
     if (pl.parts == 1) return p.j.S0 ? p.j.S0[bh * n + at] : 0.f;
     float s = 0.f;
+#pragma unroll 1
     for (int i = p.j.S0 ? 0 : 1; i <= part; ++i)
         s = fmaf(power(a, (part - i) * pl.len),
                  p.ws[(bh * pl.parts + i) * n + at], s);

@@ -51,16 +51,20 @@ namespace {
 using la::kNV;
 using la::Part;
 using la::Plan;
-using la::power;
 using bf16 = __nv_bfloat16;
 
 __device__ unsigned int g_fault_la = 0;
+
+// w^n of w = exp(a), out of line: the kernel's loops have to stay short for
+// the instruction caches, which hold the code of six kinds of warps.
+__device__ __noinline__ float power(float a, int n) { return la::power(a, n); }
 
 constexpr int kC = 128;          // tokens a chunk
 constexpr int kThreads = 960;    // 64 registers each
 constexpr int kIssuer = 28, kCopier = 29;   // warps
 constexpr int kBox = kC * 128;   // bytes of a TMA box: 128 rows of 64 bf16
 constexpr int kMaxJobs = 3;
+constexpr int kLdS = kNV + 1;    // row of the state's tile in shared memory
 
 // Shared memory (bytes from a 1024-aligned base): the rings of Q, K and V
 // tiles (boxes of 64 columns; no Q in the pass that forms part states), the
@@ -68,29 +72,30 @@ constexpr int kMaxJobs = 3;
 template <int DK, bool STATE_ONLY>
 struct Smem {
     static constexpr int HALVES = DK / 64;
-    static constexpr int NS = STATE_ONLY ? (DK == 64 ? 5 : 3)
-                                         : (DK == 64 ? 3 : 2);
+    static constexpr int NS = DK == 64 ? 3 : 2;
+    static constexpr int NVW = STATE_ONLY ? 2 : 1;   // weighted tiles
     static constexpr int TILE = HALVES * kBox;   // of Q or K
     static constexpr int Q = 0;
     static constexpr int K = Q + (STATE_ONLY ? 0 : NS * TILE);
     static constexpr int V = K + NS * TILE;
-    static constexpr int VW = V + NS * kBox;     // 3 boxes
-    static constexpr int S = VW + 3 * kBox;      // DK rows of 128 bytes
+    static constexpr int VW = V + NS * kBox;     // NVW x 3 boxes
+    static constexpr int S = VW + NVW * 3 * kBox;   // DK rows of 128 bytes
     static constexpr int W = S + DK * 128;       // w^0 .. w^128
-    static constexpr int CW = W + 4 * 132;       // factors of the columns
-    static constexpr int MASK = CW + 4 * kC;     // of a diagonal block
-    static constexpr int BAD = MASK + 4 * 64;    // [2][4 warps][64]: see below
+    static constexpr int BAD = W + 4 * 132;      // [2][4 warps][64]: see below
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
     static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
     static constexpr int BARS = DONE + 4 * 4;
-    static constexpr int NUM_BARS = 5 * NS + 12;
+    static constexpr int NUM_BARS = 5 * NS + 14;
     static constexpr int MISC = BARS + 8 * NUM_BARS;   // abort, TMEM, issued
     static constexpr int BYTES = MISC + 16 + 1024;     // alignment
     static_assert(BYTES <= 232448, "shared memory");
     static_assert(BARS % 8 == 0 && W % 16 == 0, "alignment");
 };
 
-// mbarriers, a phase a chunk (of a ring: a phase a turn)
+// mbarriers, a phase a chunk (of a ring: a phase a turn).  A wait tells a
+// phase from the one before or after it only, so none may complete two phases
+// ahead of one that waits; where nothing else rules that out there are two
+// barriers, for even and odd chunks.
 template <int NS>
 struct Bars {
     static constexpr int FULL = 0;               // NS: Q and K loaded
@@ -101,13 +106,13 @@ struct Bars {
     static constexpr int SC_FULL = 5 * NS;       // scores in TMEM
     static constexpr int SC_FREE = 5 * NS + 1;   // read
     static constexpr int P_READY = 5 * NS + 2;   // P~ in TMEM
-    static constexpr int V_READY = 5 * NS + 3;   // weighted V in place
-    static constexpr int U_FULL = 5 * NS + 4;    // U in TMEM (V's parts read)
-    static constexpr int U_FREE = 5 * NS + 5;    // read
-    static constexpr int S_READY = 5 * NS + 6;   // copy of S in place
-    static constexpr int S_FREE = 5 * NS + 7;    // Q S done
-    static constexpr int O_FULL = 5 * NS + 8;    // 2: outputs in TMEM (P~ read)
-    static constexpr int O_FREE = 5 * NS + 10;   // 2: read
+    static constexpr int V_READY = 5 * NS + 3;   // 2: weighted V in place
+    static constexpr int U_FULL = 5 * NS + 5;    // 2: U in TMEM (V's parts read)
+    static constexpr int U_FREE = 5 * NS + 7;    // read
+    static constexpr int S_READY = 5 * NS + 8;   // copy of S in place
+    static constexpr int S_FREE = 5 * NS + 9;    // Q S done
+    static constexpr int O_FULL = 5 * NS + 10;   // 2: outputs in TMEM (P~ read)
+    static constexpr int O_FREE = 5 * NS + 12;   // 2: read
 };
 
 // TMEM columns: all 512
@@ -231,6 +236,48 @@ __device__ __forceinline__ float2 rest(float2 x, uint32_t b) {
     return fma2(from_bf16x2(b), both(-1.f), x);
 }
 
+// Zeros in place of the values of this thread's pieces of a V tile that are
+// not finite, and for each output warp their columns' first such row in `bad`.
+__device__ __noinline__ void take_out(uint8_t* v, uint8_t* bad,
+                                      volatile int* flag, volatile int* done,
+                                      int c, int gt, bool rev,
+                                      volatile int* abort,
+                                      uint64_t limit_ns) {
+    // the output warps are done with what chunk c - 2 left there
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (int o = 0; o < 4; ++o)
+        while (done[o] < c - 1) {
+            if (tc::globaltimer_ns() - t0 > limit_ns) *abort = 1;
+            if (*abort) return;
+        }
+    __threadfence_block();
+    for (int m = 0; m < 4; ++m) {
+        const int piece = gt + 256 * m, j = piece >> 3;
+        uint16_t* x = reinterpret_cast<uint16_t*>(v + piece * 16);
+        for (int k = 0; k < 8; ++k) {
+            if ((x[k] & 0x7f80) != 0x7f80) continue;
+            x[k] = 0;
+            const int col = ((piece & 7) ^ (j & 7)) * 8 + k;
+            const int r = rev ? kC - 1 - j : j;
+            for (int o = 0; o < 4; ++o) {
+                // bytes: a compare-and-swap on their word
+                uint32_t* word =
+                    reinterpret_cast<uint32_t*>(bad + o * kNV + (col & ~3));
+                const int sh = (col & 3) * 8;
+                uint32_t old = *reinterpret_cast<volatile uint32_t*>(word);
+                uint32_t was;
+                do {
+                    was = old;
+                    if ((int)(was >> sh & 255) <= r) break;
+                    old = atomicCAS(word, was, (was & ~(255u << sh)) |
+                                                   (uint32_t)r << sh);
+                } while (old != was);
+                flag[o] = 1;
+            }
+        }
+    }
+}
+
 template <int DK, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ Maps maps,
@@ -243,8 +290,6 @@ linattn_tc(const __grid_constant__ Maps maps,
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = tc::smem_u32(sm);
     float* w = reinterpret_cast<float*>(sm + Sm::W);
-    float* cw = reinterpret_cast<float*>(sm + Sm::CW);
-    uint32_t* mask = reinterpret_cast<uint32_t*>(sm + Sm::MASK);
     // for each of two chunks, output warp and column: the first row (counted
     // as r) whose V is not finite, 255: none
     uint8_t* bad = sm + Sm::BAD;
@@ -285,7 +330,9 @@ linattn_tc(const __grid_constant__ Maps maps,
             // the thread that issued them
             const int count =
                 i == B::SC_FREE || i == B::P_READY || i == B::V_READY ||
-                        i == B::U_FREE || i == B::S_READY ? 8
+                        i == B::V_READY + 1 || i == B::U_FREE ||
+                        i == B::S_READY
+                    ? 8
                 : i == B::O_FREE || i == B::O_FREE + 1 ? 4
                 : i == B::O_FULL || i == B::O_FULL + 1 ? 2 : 1;
             tc::mbar_init(&bars[i], count);
@@ -295,21 +342,7 @@ linattn_tc(const __grid_constant__ Maps maps,
         *issued = 0;
     }
     if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
-    // column j has the factor w^(63 - s); on the diagonal, columns m and m + 1
-    // of a block of 32 keep in row i what entry 31 + i - m leaves of their pair
-    // of bf16
     const bool gentle = fabsf(a) * 64.f <= 60.f;
-    if (tid >= 352 && tid < 352 + kC) {
-        const int j = tid - 352;
-        cw[j] = power(a, 63 - (rev ? kC - 1 - j : j));
-    }
-    if (tid >= 288 && tid < 352) {
-        const int d = tid - 288 - 31;        // i - m
-        mask[tid - 288] = rev ? (d <= 0 ? 0xffffu : 0u) |
-                                    (d <= 1 ? 0xffff0000u : 0u)
-                              : (d >= 0 ? 0xffffu : 0u) |
-                                    (d >= 1 ? 0xffff0000u : 0u);
-    }
     for (int i = tid; i < 2 * 4 * 64; i += kThreads) bad[i] = 255;
     if (tid < 8) flag[tid] = 0;
     if (tid < 4) done[tid] = 0;
@@ -341,10 +374,36 @@ linattn_tc(const __grid_constant__ Maps maps,
     };
     auto rows_of = [&](int c) { return min(kC, end - (first + c * kC)); };
 
+    // The state's rows and columns of this block, one row kLdS floats, where
+    // the parts of V will be; by the first 512 threads.
+    float* tile = reinterpret_cast<float*>(sm + Sm::VW);
+    const size_t sn = (size_t)pt.j.dk * pt.j.dv;
+    float* slots = pt.ws ? pt.ws + bh * p.plan.parts * sn : nullptr;
+    if (warp < 16) {
+#pragma unroll 1
+        for (int i = tid; i < kC * kNV; i += 512) {
+            // along the axis whose elements are adjacent
+            const int r = pt.j.s_c == 1 ? i / kNV : i % kC;
+            const int n = pt.j.s_c == 1 ? i % kNV : i / kC;
+            float x = 0.f;
+            if (r < pt.j.dk && n0 + n < pt.j.dv) {
+                const size_t at =
+                    (size_t)r * pt.j.s_r + (size_t)(n0 + n) * pt.j.s_c;
+                if (!STATE_ONLY)
+                    x = la::state_before(pt, p.plan, part, bh, at, a);
+                else if (part == 0 && pt.j.S0)
+                    slots[at] = pt.j.S0[bh * sn + at];
+            }
+            tile[r * kLdS + n] = x;
+        }
+        tc::named_bar_sync(1, 512);
+    }
+
     int last_bar = -1, last_phase = 0;   // the issuer's last commit
 
     if (tid == 32 * kCopier) {
         // ------------------------------------------------------ copies
+#pragma unroll 1
         for (int c = 0; c < nchunks && !p.selftest; ++c) {
             const int s = c % NS, turn = c / NS;
             uint64_t* full = &bars[B::FULL + s];
@@ -392,7 +451,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             if (c > 0) wait_warp(B::SC_FREE, c - 1);
             tc::tc_fence_after();
             if (issuer) {
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < DK / 16; ++ks)
                     tc::mma_bf16(tmem + kColSC, dQ + at + step_k(ks),
                                  dK + at + step_k(ks), kIdQK, ks > 0);
@@ -401,6 +460,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             __syncwarp();
         };
         int scored = 0;      // chunks whose scores are issued
+#pragma unroll 1
         for (int c = 0; c < nchunks && !gave_up(); ++c) {
             const int s = c % NS;
             const uint32_t at = s * (Sm::TILE >> 4);
@@ -409,16 +469,17 @@ linattn_tc(const __grid_constant__ Maps maps,
                 scores(c);
                 scored = c + 1;
             }
-            wait_warp(B::V_READY, c);
+            wait_warp(B::V_READY + (c & 1), c >> 1);
             if (STATE_ONLY) wait_warp(B::FULL + s, c / NS);
             if (c > 0) wait_warp(B::U_FREE, c - 1);
             tc::tc_fence_after();
             if (issuer) {
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < kC / 16; ++ks)
                     tc::mma_bf16(tmem + kColU, dKt + at + ks * 128,
-                                 dVw + ks * 128, kIdU, ks > 0);
-                commit(B::U_FULL, c);
+                                 dVw + c % Sm::NVW * (3 * kBox >> 4) + ks * 128,
+                                 kIdU, ks > 0);
+                commit(B::U_FULL + (c & 1), c >> 1);
                 if (again) tc::mma_commit(&bars[B::EMPTY_K + s]);
                 if (STATE_ONLY && again)
                     tc::mma_commit(&bars[B::EMPTY_V + s]);
@@ -430,7 +491,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             if (c > 1) wait_warp(B::O_FREE + (c & 1), (c >> 1) - 1);
             tc::tc_fence_after();
             if (issuer) {
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < DK / 16; ++ks)
                     tc::mma_bf16(acc, dQ + at + step_k(ks), dS + ks * 128,
                                  kIdRow, ks > 0);
@@ -447,7 +508,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             wait_warp(B::P_READY, c);
             tc::tc_fence_after();
             if (issuer) {
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < kC / 16; ++ks)
                     mma_bf16_ts(acc, tmem + kColP + 8 * ks,
                                 dV + s * (kBox >> 4) + ks * 128, kIdRow, true);
@@ -461,57 +522,13 @@ linattn_tc(const __grid_constant__ Maps maps,
     } else if (warp < 8) {
         // ------------------------------ state (row d, columns c0 .. c0 + 31)
         constexpr int W = kNV / 2;
-        const int d = tid & 127, c0 = n0 + (warp >> 2) * W;
-        const bool mine = d < pt.j.dk;
-        const size_t row = (size_t)d * pt.j.s_r;
-        const size_t sn = (size_t)pt.j.dk * pt.j.dv;
+        const int d = tid & 127, c0 = (warp >> 2) * W;
         float2 S[W / 2];
-        auto clear = [&] {
 #pragma unroll
-            for (int n = 0; n < W / 2; ++n) S[n] = both(0.f);
-        };
-        clear();
-        // S += f x of a state in memory
-        auto add = [&](const float* x, float f) {
-            x += row + (size_t)c0 * pt.j.s_c;
-            if (pt.j.s_c == 1 && c0 + W <= pt.j.dv &&
-                (reinterpret_cast<uintptr_t>(x) & 15) == 0) {
-#pragma unroll
-                for (int n = 0; n < W / 2; n += 2) {
-                    const float4 y =
-                        *reinterpret_cast<const float4*>(x + 2 * n);
-                    S[n] = fma2(both(f), make_float2(y.x, y.y), S[n]);
-                    S[n + 1] = fma2(both(f), make_float2(y.z, y.w), S[n + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < W; ++n) {
-                    float& s = n & 1 ? S[n / 2].y : S[n / 2].x;
-                    if (c0 + n < pt.j.dv)
-                        s = fmaf(f, x[(size_t)n * pt.j.s_c], s);
-                }
-            }
-        };
-        auto store = [&](float* x) {
-            x += row + (size_t)c0 * pt.j.s_c;
-#pragma unroll
-            for (int n = 0; n < W; ++n)
-                if (c0 + n < pt.j.dv)
-                    x[(size_t)n * pt.j.s_c] = n & 1 ? S[n / 2].y : S[n / 2].x;
-        };
-        float* slots = pt.ws ? pt.ws + bh * p.plan.parts * sn : nullptr;
-        if (mine && STATE_ONLY) {
-            if (part == 0 && pt.j.S0) {
-                add(pt.j.S0 + bh * sn, 1.f);
-                store(slots);
-                clear();
-            }
-        } else if (mine && p.plan.parts == 1) {
-            if (pt.j.S0) add(pt.j.S0 + bh * sn, 1.f);
-        } else if (mine) {
-            for (int i = pt.j.S0 ? 0 : 1; i <= part; ++i)
-                add(slots + i * sn, power(a, (part - i) * p.plan.len));
-        }
+        for (int n = 0; n < W / 2; ++n)
+            S[n] = make_float2(tile[d * kLdS + c0 + 2 * n],
+                               tile[d * kLdS + c0 + 2 * n + 1]);
+        tc::named_bar_sync(2, 512);    // the tile may be written over
         const float2 fs = both(gentle ? power(a, 63 + e) : 1.f);
         auto copy_S = [&] {        // the bf16 copy that Q S reads
             if (d < DK) {
@@ -535,10 +552,12 @@ linattn_tc(const __grid_constant__ Maps maps,
         if (!STATE_ONLY) copy_S();
         const uint32_t ucol =
             tmem + ((uint32_t)(d & 96) << 16) + kColU + (warp >> 2) * W;
+        // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
+        float grow = expm1f(a * (float)kC);
+#pragma unroll 1
         for (int c = 0; c < nchunks && !gave_up(); ++c) {
-            // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
-            const float grow = expm1f(a * (float)rows_of(c));
-            wait_warp(B::U_FULL, c);
+            if (c + 1 == nchunks) grow = expm1f(a * (float)rows_of(c));
+            wait_warp(B::U_FULL + (c & 1), c >> 1);
             tc::tc_fence_after();
 #pragma unroll
             for (int m = 0; m < W; m += 8) {
@@ -566,25 +585,43 @@ linattn_tc(const __grid_constant__ Maps maps,
                 }
             }
         }
-        float* dst = STATE_ONLY ? slots + (part + 1) * sn
-                     : part + 1 == parts && pt.j.ST ? pt.j.ST + bh * sn
-                                                    : nullptr;
-        if (*abort == 0 && mine && dst)
-            store(dst);
+        // (U of the last chunk is formed: nobody reads V's parts any more)
+#pragma unroll
+        for (int n = 0; n < W / 2; ++n) {
+            tile[d * kLdS + c0 + 2 * n] = S[n].x;
+            tile[d * kLdS + c0 + 2 * n + 1] = S[n].y;
+        }
     } else if (warp < 16) {
         // ------------------------------------------------------ weighted V
+        tc::named_bar_sync(2, 512);    // the state has been taken out of there
         const int gt = tid - 256;
-        for (int c = 0; c < nchunks && !gave_up(); ++c) {
-            const int n = rows_of(c);
-            wait_warp(B::FULL_V + c % NS, c / NS);
-            if (c > 0) wait_warp(B::U_FULL, c - 1);
-            uint8_t* v = sm + Sm::V + c % NS * kBox;
-            uint32_t seen = 0;
-#pragma unroll 1
-            for (int m = 0; m < 4; ++m) {      // 4 of 1024 16-byte pieces
-                const int at = (gt + 256 * m) * 16, j = (gt >> 3) + 32 * m;
+        // weights of this thread's rows j0 + 32 m of a whole chunk (no table
+        // in shared memory: its bandwidth is what the products are bound by)
+        const int j0 = gt >> 3;
+        float wt[4];
+        auto weigh = [&](int n) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int j = j0 + 32 * m;
                 // rows beyond the sequence are zero: their weight is any
-                const float f = w[max(0, rev ? n - kC + 1 + j : n - 1 - j)];
+                wt[m] = power(a, max(0, rev ? n - kC + 1 + j : n - 1 - j));
+            }
+        };
+        weigh(kC);
+#pragma unroll 1
+        for (int c = 0; c < nchunks && !gave_up(); ++c) {
+            if (c + 1 == nchunks) weigh(rows_of(c));
+            wait_warp(B::FULL_V + c % NS, c / NS);
+            // the parts' last tile here has been read
+            if (c >= Sm::NVW)
+                wait_warp(B::U_FULL + ((c - Sm::NVW) & 1), (c - Sm::NVW) >> 1);
+            uint8_t* v = sm + Sm::V + c % NS * kBox;
+            uint8_t* vw = sm + Sm::VW + c % Sm::NVW * (3 * kBox);
+            uint32_t seen = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {      // 4 of 1024 16-byte pieces
+                const int at = (gt + 256 * m) * 16;
+                const float f = wt[m];
                 const uint4 x = *reinterpret_cast<const uint4*>(v + at);
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[3][4];
@@ -600,60 +637,33 @@ linattn_tc(const __grid_constant__ Maps maps,
                 }
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint4*>(sm + Sm::VW + k * kBox + at) =
+                    *reinterpret_cast<uint4*>(vw + k * kBox + at) =
                         make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
             }
-            bool ok = true;
             // the third part of what is not finite is NaN; those of others are
             // below 2 unless the value is above 2^16: the exponent's top bit
             // tells where to look
             if (!STATE_ONLY && (seen & 0x40004000u)) {
-                // the output warps are done with this slot's last chunk
-                const uint64_t t0 = tc::globaltimer_ns();
-                for (int o = 0; o < 4 && ok; ++o)
-                    while (ok && done[o] < c - 1)
-                        ok = *abort == 0 &&
-                             tc::globaltimer_ns() - t0 < p.limit_ns;
-                if (!ok) *abort = 1;
-                __threadfence_block();
-                const int slot = c & 1;
-                for (int m = 0; m < 4 && ok; ++m) {
-                    const int piece = gt + 256 * m, j = piece >> 3;
-                    uint16_t* x =
-                        reinterpret_cast<uint16_t*>(v + piece * 16);
-                    for (int k = 0; k < 8; ++k) {
-                        if ((x[k] & 0x7f80) != 0x7f80) continue;
-                        x[k] = 0;
-                        const int col = ((piece & 7) ^ (j & 7)) * 8 + k;
-                        const int r = rev ? kC - 1 - j : j;
-                        for (int o = 0; o < 4; ++o) {
-                            // bytes: a compare-and-swap on their word
-                            uint32_t* word = reinterpret_cast<uint32_t*>(
-                                bad + (slot * 4 + o) * 64 + (col & ~3));
-                            const int sh = (col & 3) * 8;
-                            uint32_t old =
-                                *reinterpret_cast<volatile uint32_t*>(word);
-                            uint32_t was;
-                            do {
-                                was = old;
-                                if ((int)(was >> sh & 255) <= r) break;
-                                old = atomicCAS(word, was,
-                                                (was & ~(255u << sh)) |
-                                                    (uint32_t)r << sh);
-                            } while (old != was);
-                            flag[slot * 4 + o] = 1;
-                        }
-                    }
-                }
+                take_out(v, bad + (c & 1) * 4 * kNV, flag + (c & 1) * 4, done,
+                         c, gt, rev, abort, p.limit_ns);
             }
             tc::fence_proxy_async_smem();
-            arrive(B::V_READY);
+            arrive(B::V_READY + (c & 1));
         }
     } else if (warp < 24 && !STATE_ONLY) {
         // ------------------------------------------- scores to P~ (row i)
         const int q = warp & 3, i = 32 * q + lane;
         const int j0 = (warp - 16) >> 2 << 1;   // its two blocks of 32 columns
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+        const float a2 = a * 1.4426950408889634f;
+        // the factor w^(63 - s) of column at + m: that of column `at` times
+        // w^-m (in reverse w^m); in registers, as the weights of V
+        float2 cw[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            cw[m] = make_float2(power(a, rev ? 2 * m : -2 * m),
+                                power(a, rev ? 2 * m + 1 : -2 * m - 1));
+#pragma unroll 1
         for (int c = 0; c < nchunks && !gave_up(); ++c) {
             if (!gentle) {       // rows of Q S, this warp's half of the columns
                 const float2 f = both(w[(rev ? kC - 1 - i : i) + e]);
@@ -697,32 +707,30 @@ linattn_tc(const __grid_constant__ Maps maps,
                     for (int m = 0; m < 8; ++m) pk[m] = 0;
                 } else {
                     if (gentle) {
+                        const float2 f = both(tc::ex2(
+                            a2 * (float)(rev ? at - (kC - 64) : 63 - at)));
 #pragma unroll
-                        for (int m = 0; m < 16; m += 4) {
-                            const float4 g =
-                                *reinterpret_cast<const float4*>(&cw[at + m]);
-                            const float2 y = mul2(make_float2(x[m], x[m + 1]),
-                                                  make_float2(g.x, g.y));
-                            const float2 z =
-                                mul2(make_float2(x[m + 2], x[m + 3]),
-                                     make_float2(g.z, g.w));
-                            pk[m / 2] = tc::pack_bf16x2(y.x, y.y);
-                            pk[m / 2 + 1] = tc::pack_bf16x2(z.x, z.y);
+                        for (int m = 0; m < 8; ++m) {
+                            const float2 y =
+                                mul2(make_float2(x[2 * m], x[2 * m + 1]),
+                                     mul2(f, cw[m]));
+                            x[2 * m] = y.x, x[2 * m + 1] = y.y;
                         }
                     } else {
                         const int d = rev ? at - i : i - at;
 #pragma unroll
                         for (int m = 0; m < 16; ++m)
                             x[m] *= w[max(0, rev ? d + m : d - m)];
-#pragma unroll
-                        for (int m = 0; m < 8; ++m)
-                            pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
                     }
                     if (j == q) {    // masked, not multiplied by 0
-                        const uint32_t* keep = mask + 31 + lane - (at & 16);
+                        const int d = lane - (at & 16);
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) pk[m] &= keep[-2 * m];
+                        for (int m = 0; m < 16; ++m)
+                            if (rev ? m < d : m > d) x[m] = 0.f;
                     }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m)
+                        pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
                 }
                 tmem_st8(lanes + kColP + at / 2, pk);
             }
@@ -739,6 +747,7 @@ linattn_tc(const __grid_constant__ Maps maps,
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
         bf16* out = static_cast<bf16*>(pt.j.o);
         const uintptr_t align = reinterpret_cast<uintptr_t>(out) | dv * 2;
+#pragma unroll 1
         for (int c = 0; c < nchunks; ++c) {
             wait_warp(B::O_FULL + (c & 1), c >> 1);
             if (gave_up()) break;      // writes nothing
@@ -821,6 +830,17 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
         }
     }
+    float* dst = STATE_ONLY ? slots + (part + 1) * sn
+                 : part + 1 == parts && pt.j.ST ? pt.j.ST + bh * sn : nullptr;
+    if (*abort == 0 && dst)
+#pragma unroll 1
+        for (int i = tid; i < kC * kNV; i += kThreads) {
+            const int r = pt.j.s_c == 1 ? i / kNV : i % kC;
+            const int n = pt.j.s_c == 1 ? i % kNV : i / kC;
+            if (r < pt.j.dk && n0 + n < pt.j.dv)
+                dst[(size_t)r * pt.j.s_r + (size_t)(n0 + n) * pt.j.s_c] =
+                    tile[r * kLdS + n];
+        }
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
