@@ -6,13 +6,32 @@
 //   lse = m + log s,     entropy = log s - t / s
 // and where two partial results meet, with m' = max(m1, m2), c = exp(m - m'):
 //   s' = sum c s,        t' = sum c (t + s (m - m')).
+// A row is read once; it belongs to one block, or, when there are fewer rows
+// than SMs, to a cluster of up to 8 that join their sums on chip.
+//
+// The largest: each thread keeps its own maximum.  The top-th largest of the
+// block's maxima is a lower bound of the row's top-th logit, and only the few
+// threads whose maximum reaches it read their part of the row again (from L2)
+// and hand in what is not below it.  Where ties make that more than fits, the
+// row is searched round by round instead.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "f32x2.cuh"
 #include "kla_internal.cuh"
 
 namespace kla {
 namespace {
 
+namespace cg = cooperative_groups;
 using bf16 = __nv_bfloat16;
-constexpr int kNT = 256;
+using u64 = unsigned long long;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCand = 1024;      // candidates a block can hold
+constexpr int kMaxParts = 8;     // blocks of a cluster
+static_assert(kMaxParts * kLogprobMaxTop <= kCand, "room for all parts");
 
 // Order of logits as whole numbers: larger values first, NaN above all.
 __device__ __forceinline__ unsigned order_of(float x) {
@@ -25,8 +44,8 @@ __device__ __forceinline__ float value_of(unsigned u) {
            : __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 // One key a logit: its order above, then the lower id.  0 is none.
-__device__ __forceinline__ unsigned long long key_of(float x, int id) {
-    return (unsigned long long)order_of(x) << 32 | (0xffffffffu - id);
+__device__ __forceinline__ u64 key_of(float x, int id) {
+    return (u64)order_of(x) << 32 | (0xffffffffu - id);
 }
 
 // The larger of two, NaN if one is.
@@ -35,118 +54,471 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 struct Sums {
     float m, s, t;
 };
-// exp(d) and d of a difference d <= 0 from the maximum; -200 in place of
-// what is far below has exp = 0, and 0 * -200 is no NaN.
+// -200 in place of a distance far below the maximum: exp of both is 0, and
+// 0 * -200 is no NaN where 0 * -inf is.
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
     const float m = max_nan(a.m, b.m);
     if (m == -INFINITY) return a;
     const float da = max_nan(a.m - m, -200.f), db = max_nan(b.m - m, -200.f);
-    const float ca = expf(da), cb = expf(db);
+    const float ca = ex2(da * kLog2e), cb = ex2(db * kLog2e);
     return {m, ca * a.s + cb * b.s,
             ca * fmaf(a.s, da, a.t) + cb * fmaf(b.s, db, b.t)};
 }
-__device__ __forceinline__ void add(Sums& x, float z) {
-    x = join(x, Sums{z, 1.f, 0.f});
+
+// N logits, the largest of them `top`, into a thread's sums.  The maximum
+// moves rarely; then what is summed so far is scaled.
+template <int N>
+__device__ __forceinline__ void add(Sums& a, const float (&v)[N], float top,
+                                    float scale) {
+    const float m = top * scale;
+    if (!(m <= a.m)) a = join(a, Sums{m, 0.f, 0.f});   // NaN too
+    if (m == -INFINITY) return;                        // all masked
+    float2 s = both(0.f), t = both(0.f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        float2 d = fma2(make_float2(v[i], i + 1 < N ? v[i + 1] : -INFINITY),
+                        both(scale), both(-a.m));
+        d.x = max_nan(d.x, -200.f);
+        d.y = max_nan(d.y, -200.f);
+        const float2 e = mul2(d, both(kLog2e));
+        const float2 p = make_float2(ex2(e.x), ex2(e.y));
+        s = add2(s, p);
+        t = fma2(p, d, t);
+    }
+    a.s += s.x + s.y;
+    a.t += t.x + t.y;
 }
 
+// 16 bytes of logits as floats.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float* p,
+                                                float (&x)[4]) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    }
+};
+template <int N>
+__device__ __forceinline__ float largest_of(const float (&v)[N]) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = max_nan(m, v[i]);
+    return m;
+}
+template <> struct Vec<bf16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const bf16* p,
+                                                float (&x)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const unsigned u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = from_bf16x2(u[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+};
+
+// Part of a row: [begin, end); its whole 16-byte pieces are [first, last).
+struct Range {
+    int begin, first, last, end;
+};
 template <typename T>
-__global__ void __launch_bounds__(kNT) logprob_fwd(LogprobArgs a) {
-    __shared__ Sums part[kNT / 32];
-    __shared__ unsigned long long keys[kNT / 32];
+__device__ __forceinline__ Range range_of(const T* x, int begin, int end) {
+    constexpr int N = Vec<T>::N;
+    const int off = (int)((reinterpret_cast<uintptr_t>(x + begin) & 15) /
+                          sizeof(T));
+    const int first = min(end, off ? begin + N - off : begin);
+    return {begin, first, first + (end - first) / N * N, end};
+}
+
+// f(id, values...) for each of this thread's pieces of the range; the same
+// split whenever it is called.
+template <typename T, int NT, typename F, typename G>
+__device__ __forceinline__ void for_each(const T* x, const Range& r, F piece,
+                                         G single) {
+    constexpr int N = Vec<T>::N;
+    const int tid = threadIdx.x;
+    // four pieces on their way at a time
+    int i = r.first + tid * N;
+    for (; r.last - i > 3 * NT * N; i += 4 * NT * N) {
+        float v[4][N];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) Vec<T>::load(x + i + k * NT * N, v[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) piece(i + k * NT * N, v[k]);
+    }
+    for (; i < r.last; i += NT * N) {
+        float v[N];
+        Vec<T>::load(x + i, v);
+        piece(i, v);
+    }
+    if (r.begin + tid < r.first)
+        single(r.begin + tid, to_f32(x[r.begin + tid]));
+    if (r.last + tid < r.end) single(r.last + tid, to_f32(x[r.last + tid]));
+}
+
+template <int NT>
+__device__ __forceinline__ u64 block_max(u64 k, u64* keys) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const u64 y = __shfl_xor_sync(~0u, k, o);
+        k = y > k ? y : k;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) keys[threadIdx.x >> 5] = k;
+    __syncthreads();
+    k = keys[0];
+    for (int w = 1; w < NT / 32; ++w) k = keys[w] > k ? keys[w] : k;
+    return k;
+}
+
+template <int NT> struct Shared {
+    Sums part[NT / 32];
+    Sums whole;                  // of this block's part
+    u64 keys[NT / 32];
+    u64 top[kLogprobMaxTop];     // this block's largest, sorted
+    u64 cand[kCand];
+    alignas(16) unsigned maxima[NT];
+    unsigned bound;
+    int count;
+};
+
+// The `top` largest of this block's part into sh.top, sorted (0: none).
+// own: the largest order among the thread's logits, 0 if it has none.
+template <typename T, int NT>
+__device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
+                                        const Range& r, int top,
+                                        unsigned own) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    // the maxima of groups of four threads do while there are far more of
+    // them than `top`
+    const int G = top <= NT / 8 ? 4 : 1, groups = NT / G;
+    unsigned gm = own;
+    if (G == 4) {
+        gm = max(gm, __shfl_xor_sync(~0u, gm, 1));
+        gm = max(gm, __shfl_xor_sync(~0u, gm, 2));
+    }
+    sh.maxima[tid / G] = gm;
+    if (tid == 0) sh.count = 0, sh.bound = 0;
+    __syncthreads();
+    // the top-th largest: each thread of a group compares with its share
+    {
+        int above = 0, level = 0;
+        const int share = groups / G, from = tid % G * share;
+        for (int i = from; i < from + share; i += 4) {
+            const uint4 m = *reinterpret_cast<const uint4*>(&sh.maxima[i]);
+            above += (m.x > gm) + (m.y > gm) + (m.z > gm) + (m.w > gm);
+            level += (m.x == gm) + (m.y == gm) + (m.z == gm) + (m.w == gm);
+        }
+        if (G == 4) {
+#pragma unroll
+            for (int o = 1; o < 4; o *= 2) {
+                above += __shfl_xor_sync(~0u, above, o);
+                level += __shfl_xor_sync(~0u, level, o);
+            }
+        }
+        if (above < top && above + level >= top) sh.bound = gm;
+    }
+    __syncthreads();
+    const unsigned bound = sh.bound;     // 0: fewer logits than `top`
+    // a warp reads the pieces of each of its threads that reach the bound
+    constexpr int N = Vec<T>::N;
+    unsigned found = __ballot_sync(~0u, own != 0 && own >= bound);
+    auto take = [&](int id, float v) {
+        if (order_of(v) < bound) return;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kCand) sh.cand[at] = key_of(v, id);
+    };
+    for (; found; found &= found - 1) {
+        const int t = (tid & ~31) + __ffs(found) - 1;
+        for (long long i = r.first + t * N + (long long)lane * NT * N;
+             i < r.last; i += 32ll * NT * N) {
+            float v[N];
+            Vec<T>::load(x + i, v);
+#pragma unroll
+            for (int k = 0; k < N; ++k) take((int)i + k, v[k]);
+        }
+        if (lane == 0 && r.begin + t < r.first)
+            take(r.begin + t, to_f32(x[r.begin + t]));
+        if (lane == 1 && r.last + t < r.end)
+            take(r.last + t, to_f32(x[r.last + t]));
+    }
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kCand) {
+        // its rank is the number of larger keys (no two are equal)
+        for (int i = tid; i < n; i += NT) {
+            const u64 k = sh.cand[i];
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += sh.cand[j] > k;
+            if (rank < top) sh.top[rank] = k;
+        }
+        for (int i = n + tid; i < top; i += NT) sh.top[i] = 0;
+        __syncthreads();
+        return;
+    }
+    u64 last = ~0ull;
+    for (int i = 0; i < top; ++i) {
+        u64 best = 0;
+        auto look = [&](int id, float v) {
+            const u64 k = key_of(v, id);
+            if (k < last && k > best) best = k;
+        };
+        for_each<T, NT>(
+            x, r,
+            [&](int id, const float (&v)[Vec<T>::N]) {
+#pragma unroll
+                for (int k = 0; k < Vec<T>::N; ++k) look(id + k, v[k]);
+            },
+            look);
+        last = block_max<NT>(best, sh.keys);
+        if (tid == 0) sh.top[i] = last;
+    }
+    __syncthreads();
+}
+
+// grid: rows x parts (a cluster each where parts > 1).
+template <typename T, int NT, bool TOP>
+__global__ void __launch_bounds__(NT) logprob_fwd(LogprobArgs a, int parts) {
+    __shared__ Shared<NT> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const size_t row = blockIdx.x;
+    const size_t row = blockIdx.x / parts;
+    const int part = blockIdx.x % parts;
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+    const int len = (a.V + parts - 1) / parts;
+    const int begin = (int)min((long long)a.V, (long long)part * len);
+    const Range r = range_of(x, begin, min(a.V, begin + len));
+    await_grid_before();
+    release_grid_after();
     Sums acc{-INFINITY, 0.f, 0.f};
-    for (int i = tid; i < a.V; i += kNT) add(acc, to_f32(x[i]) * a.scale);
+    unsigned own = 0;
+    for_each<T, NT>(
+        x, r,
+        [&](int, const float (&v)[Vec<T>::N]) {
+            const float m = largest_of(v);
+            add(acc, v, m, a.scale);
+            if (TOP) own = max(own, order_of(m));
+        },
+        [&](int, float v) {
+            const float one[1] = {v};
+            add(acc, one, v, a.scale);
+            if (TOP) own = max(own, order_of(v));
+        });
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
                              __shfl_xor_sync(~0u, acc.s, o),
                              __shfl_xor_sync(~0u, acc.t, o)});
-    if (lane == 0) part[warp] = acc;
+    if (lane == 0) sh.part[warp] = acc;
     __syncthreads();
-    acc = part[0];
-    for (int w = 1; w < kNT / 32; ++w) acc = join(acc, part[w]);
-    const bool none = acc.m == -INFINITY;
-    const float ls = logf(acc.s), lse = none ? -INFINITY : acc.m + ls;
-    if (tid == 0) {
-        const long long t = a.tokens[row];
-        float lp = 0.f;
-        if (t >= 0 && t < a.V)
-            lp = none ? -INFINITY : to_f32(x[t]) * a.scale - lse;
-        a.logp[row] = lp;
-        if (a.entropy) a.entropy[row] = none ? 0.f : ls - acc.t / acc.s;
-        if (a.lse) a.lse[row] = lse;
-    }
-    unsigned long long last = ~0ull;
-    for (int n = 0; n < a.top; ++n) {
-        unsigned long long best = 0;
-        for (int i = tid; i < a.V; i += kNT) {
-            const unsigned long long k = key_of(to_f32(x[i]), i);
-            if (k < last && k > best) best = k;
-        }
+    if (warp == 0) {
+        acc = lane < NT / 32 ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f};
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const unsigned long long k = __shfl_xor_sync(~0u, best, o);
-            best = k > best ? k : best;
+        for (int o = NT / 64; o; o >>= 1)
+            acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
+                                 __shfl_xor_sync(~0u, acc.s, o),
+                                 __shfl_xor_sync(~0u, acc.t, o)});
+        if (lane == 0) sh.whole = acc;
+    }
+    if (TOP) largest<T, NT>(sh, x, r, a.top, own);
+    else __syncthreads();
+
+    // one block of the row writes; the others' sums and largest come over
+    // the cluster's shared memory, in the order of the parts
+    if (parts > 1) cg::this_cluster().sync();
+    if (part == 0) {
+        if (parts > 1) {
+            if (warp == 0) {
+                Sums all{-INFINITY, 0.f, 0.f};
+                if (lane < parts)
+                    all = *cg::this_cluster().map_shared_rank(&sh.whole, lane);
+#pragma unroll
+                for (int o = kMaxParts / 2; o; o >>= 1)
+                    all = join(all, Sums{__shfl_xor_sync(~0u, all.m, o),
+                                         __shfl_xor_sync(~0u, all.s, o),
+                                         __shfl_xor_sync(~0u, all.t, o)});
+                if (lane == 0) sh.part[0] = all;
+            }
+            if (TOP) {
+                for (int i = tid; i < parts * a.top; i += NT)
+                    sh.cand[i] = cg::this_cluster().map_shared_rank(
+                        sh.top, i / a.top)[i % a.top];
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (lane == 0) keys[warp] = best;
-        __syncthreads();
-        for (int w = 0; w < kNT / 32; ++w)
-            best = keys[w] > best ? keys[w] : best;
-        last = best;
+        const Sums all = parts > 1 ? sh.part[0] : sh.whole;
+        const bool none = all.m == -INFINITY;
+        const float ls = logf(all.s);
+        const float lse = none ? -INFINITY : all.m + ls;
         if (tid == 0) {
-            const size_t at = row * a.top + n;
-            const float z = value_of((unsigned)(best >> 32)) * a.scale;
-            a.top_logp[at] = none ? -INFINITY : z - lse;
-            a.top_ids[at] = 0xffffffffu - (unsigned)best;
+            const long long t = a.tokens[row];
+            float lp = 0.f;
+            if (t >= 0 && t < a.V)
+                lp = none ? -INFINITY : fmaf(to_f32(x[t]), a.scale, -lse);
+            a.logp[row] = lp;
+            if (a.entropy) a.entropy[row] = none ? 0.f : ls - all.t / all.s;
+            if (a.lse) a.lse[row] = lse;
+        }
+        if (TOP) {
+            const u64* keys = parts > 1 ? sh.cand : sh.top;
+            const int n = parts * a.top;
+            for (int i = tid; i < n; i += NT) {
+                const u64 k = keys[i];
+                if (k == 0) continue;
+                // its place: the number of larger keys
+                int rank = parts > 1 ? 0 : i;
+                if (parts > 1)
+                    for (int j = 0; j < n; ++j) rank += keys[j] > k;
+                if (rank >= a.top) continue;
+                const size_t out = row * a.top + rank;
+                const float v = value_of((unsigned)(k >> 32));
+                a.top_logp[out] = none ? -INFINITY : fmaf(v, a.scale, -lse);
+                a.top_ids[out] = 0xffffffffu - (unsigned)k;
+            }
         }
     }
+    if (parts > 1) cg::this_cluster().sync();    // its shared memory is read
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kNT) logprob_bwd(LogprobBwdArgs a) {
-    const size_t row = blockIdx.x;
+// ---------------------------------------------------------------- gradient
+
+// d_j = -p_j (g + ge (log p_j + H)), + g at the token, times scale.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
+                                                  int parts) {
+    constexpr int N = Vec<T>::N;
+    const size_t row = blockIdx.x / parts;
+    const int part = blockIdx.x % parts;
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
     T* y = static_cast<T*>(a.logits_grad) + row * a.V;
+    const int len = (a.V + parts - 1) / parts;
+    const int begin = (int)min((long long)a.V, (long long)part * len);
+    const int end = min(a.V, begin + len);
+    await_grid_before();
+    release_grid_after();
     const float lse = a.lse[row];
     const long long t = a.tokens[row];
     const bool some = t >= 0 && t < a.V && lse != -INFINITY;
     const float g = a.logp_grad && some ? a.logp_grad[row] : 0.f;
     const float ge = a.entropy_grad ? a.entropy_grad[row] : 0.f;
     const float H = a.entropy_grad ? a.entropy[row] : 0.f;
-    for (int i = threadIdx.x; i < a.V; i += kNT) {
-        // log p; -200 in place of what is far below (p = 0)
-        const float lp = lse == -INFINITY ? -200.f
-            : max_nan(fmaf(to_f32(x[i]), a.scale, -lse), -200.f);
+    const int at = g != 0.f ? (int)t : -1;
+    // -200 in place of a log p far below: p is 0, and 0 * -200 is no NaN
+    auto grad = [&](int id, float v) {
+        const float lp = lse == -INFINITY
+                             ? -200.f
+                             : max_nan(fmaf(v, a.scale, -lse), -200.f);
         const float p = expf(lp);
         float d = -p * fmaf(ge, lp + H, g);
-        if (i == t) d += g;
-        y[i] = from_f32<T>(d * a.scale);
+        if (id == at) d += g;
+        return d * a.scale;
+    };
+    const Range r = range_of(x, begin, end);
+    if (((reinterpret_cast<uintptr_t>(x + r.first) |
+          reinterpret_cast<uintptr_t>(y + r.first)) & 15) == 0) {
+        auto piece = [&](int id, const float (&v)[N]) {
+            float d[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) d[k] = grad(id + k, v[k]);
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(y + id) =
+                    make_float4(d[0], d[1], d[2], d[3]);
+            } else {
+                __nv_bfloat162 o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = __floats2bfloat162_rn(d[2 * k], d[2 * k + 1]);
+                *reinterpret_cast<uint4*>(y + id) =
+                    *reinterpret_cast<const uint4*>(o);
+            }
+        };
+        for_each<T, NT>(x, r, piece, [&](int id, float v) {
+            y[id] = from_f32<T>(grad(id, v));
+        });
+    } else {
+        // logits and gradient rows that do not line up
+        int i = begin + threadIdx.x;
+        for (; end - i > 3 * NT; i += 4 * NT) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = to_f32(x[i + k * NT]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[i + k * NT] = from_f32<T>(grad(i + k * NT, v[k]));
+        }
+        for (; i < end; i += NT) y[i] = from_f32<T>(grad(i, to_f32(x[i])));
     }
+}
+
+// ---------------------------------------------------------------- launch
+
+constexpr int kSMs = 152;
+
+// Blocks of a row: up to four for every SM, of at least 4096 logits.
+int parts_of(int N, int V, int most) {
+    int parts = 1;
+    while (parts < most && (long long)N * parts * 2 <= 4 * kSMs &&
+           V / (parts * 2) >= 4096)
+        parts *= 2;
+    return parts;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_rows(void (*kernel)(P...), long long rows, int parts,
+                        int threads, bool cluster, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * parts));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster && parts > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args..., parts);
+}
+
+template <typename T>
+cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
+    constexpr int NT = 512;
+    const int parts = parts_of(a.N, a.V, kMaxParts);
+    return a.top ? launch_rows(logprob_fwd<T, NT, true>, a.N, parts, NT, true,
+                               s, a)
+                 : launch_rows(logprob_fwd<T, NT, false>, a.N, parts, NT,
+                               true, s, a);
+}
+
+template <typename T>
+cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
+    constexpr int NT = 512;
+    const int parts = parts_of(a.N, a.V, 64);
+    return launch_rows(logprob_bwd<T, NT>, a.N, parts, NT, false, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream) {
-    if (a.dtype == KLA_BF16)
-        logprob_fwd<bf16><<<a.N, kNT, 0, stream>>>(a);
-    else
-        logprob_fwd<float><<<a.N, kNT, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.dtype == KLA_BF16 ? launch_fwd<bf16>(a, stream)
+                               : launch_fwd<float>(a, stream);
 }
 
 cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, cudaStream_t stream) {
-    if (a.dtype == KLA_BF16)
-        logprob_bwd<bf16><<<a.N, kNT, 0, stream>>>(a);
-    else
-        logprob_bwd<float><<<a.N, kNT, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.dtype == KLA_BF16 ? launch_bwd<bf16>(a, stream)
+                               : launch_bwd<float>(a, stream);
 }
 
 }  // namespace kla
