@@ -4,6 +4,7 @@
 // Forward, one pass over a row with a running maximum m (z = scale x):
 //   s = sum exp(z - m),  t = sum exp(z - m) (z - m)
 //   lse = m + log s,     entropy = log s - t / s
+// (for any m near the maximum),
 // and where two partial results meet, with m' = max(m1, m2), c = exp(m - m'):
 //   s' = sum c s,        t' = sum c (t + s (m - m')).
 // A row is read once; it belongs to one block, or, when there are fewer rows
@@ -74,14 +75,19 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
             ca * fmaf(a.s, da, a.t) + cb * fmaf(b.s, db, b.t)};
 }
 
-// N logits, the largest of them `top`, into a thread's sums.  The maximum
-// moves rarely; then what is summed so far is scaled.
+// How far a logit may be above the m that a thread's sums are relative to:
+// they need no maximum, only exponentials in range, so m moves hardly ever.
+constexpr float kAbove = 40.f;
+
+// m for logits of which `top` (scaled) is the largest.
+__device__ __forceinline__ void refer(Sums& a, float top) {
+    if (!(top - a.m <= kAbove)) a = join(a, Sums{top, 0.f, 0.f});   // NaN too
+}
+// N logits into a thread's sums.
 template <int N>
-__device__ __forceinline__ void add(Sums& a, const float (&v)[N], float top,
+__device__ __forceinline__ void add(Sums& a, const float (&v)[N],
                                     float scale) {
-    const float m = top * scale;
-    if (!(m <= a.m)) a = join(a, Sums{m, 0.f, 0.f});   // NaN too
-    if (m == -INFINITY) return;                        // all masked
+    if (a.m == -INFINITY) return;                      // all masked so far
     float2 s = both(0.f), t = both(0.f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -98,28 +104,36 @@ __device__ __forceinline__ void add(Sums& a, const float (&v)[N], float top,
     a.t += t.x + t.y;
 }
 
-// 16 bytes of logits as floats.
+// 16 bytes of logits: as loaded, as floats, and the largest of K such.
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float* p,
-                                                float (&x)[4]) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
+    using Raw = float4;
+    static __device__ __forceinline__ Raw none() {
+        return make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+    static __device__ __forceinline__ void floats(const Raw& v,
+                                                  float (&x)[4]) {
         x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
     }
-};
-template <int N>
-__device__ __forceinline__ float largest_of(const float (&v)[N]) {
-    float m = v[0];
+    template <int K>
+    static __device__ __forceinline__ float largest(const Raw (&v)[K]) {
+        float m = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < N; ++i) m = max_nan(m, v[i]);
-    return m;
-}
+        for (int k = 0; k < K; ++k)
+            m = max_nan(m, max_nan(max_nan(v[k].x, v[k].y),
+                                   max_nan(v[k].z, v[k].w)));
+        return m;
+    }
+};
 template <> struct Vec<bf16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const bf16* p,
-                                                float (&x)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw none() {
+        return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    }
+    static __device__ __forceinline__ void floats(const Raw& v,
+                                                  float (&x)[8]) {
         const unsigned u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -127,7 +141,25 @@ template <> struct Vec<bf16> {
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     }
+    static __device__ __forceinline__ unsigned two(unsigned a, unsigned b) {
+        unsigned r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    template <int K>
+    static __device__ __forceinline__ float largest(const Raw (&v)[K]) {
+        unsigned m = 0xff80ff80u;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            m = two(m, two(two(v[k].x, v[k].y), two(v[k].z, v[k].w)));
+        const float2 f = from_bf16x2(m);
+        return max_nan(f.x, f.y);
+    }
 };
+template <typename T>
+__device__ __forceinline__ typename Vec<T>::Raw load(const T* x) {
+    return *reinterpret_cast<const typename Vec<T>::Raw*>(x);
+}
 
 // Part of a row: [begin, end); its whole 16-byte pieces are [first, last).
 struct Range {
@@ -142,31 +174,53 @@ __device__ __forceinline__ Range range_of(const T* x, int begin, int end) {
     return {begin, first, first + (end - first) / N * N, end};
 }
 
-// f(id, values...) for each of this thread's pieces of the range; the same
-// split whenever it is called.
-template <typename T, int NT, typename F, typename G>
-__device__ __forceinline__ void for_each(const T* x, const Range& r, F piece,
-                                         G single) {
+// piece(id, values) for each of this thread's pieces
+// of the range, after ready(the pieces as loaded, up to four at a time);
+// single(id, value) for what is before and behind them.  The same split whenever called.
+template <typename T, int NT, typename R, typename F, typename G>
+__device__ __forceinline__ void for_each(const T* x, const Range& r, R ready,
+                                         F piece, G single) {
     constexpr int N = Vec<T>::N;
+    using Raw = typename Vec<T>::Raw;
     const int tid = threadIdx.x;
-    // four pieces on their way at a time
+    // (distances from r.last: an id past it may pass 2^31)
     int i = r.first + tid * N;
     for (; r.last - i > 3 * NT * N; i += 4 * NT * N) {
-        float v[4][N];
+        Raw v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) Vec<T>::load(x + i + k * NT * N, v[k]);
+        for (int k = 0; k < 4; ++k) v[k] = load(x + i + k * NT * N);
+        ready(v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) piece(i + k * NT * N, v[k]);
+        for (int k = 0; k < 4; ++k) {
+            float f[N];
+            Vec<T>::floats(v[k], f);
+            piece(i + k * NT * N, f);
+        }
     }
-    for (; i < r.last; i += NT * N) {
-        float v[N];
-        Vec<T>::load(x + i, v);
-        piece(i, v);
+    // the up to three pieces left, on their way together too
+    if (r.last - i > 0) {
+        Raw v[3];
+        v[0] = load(x + i);
+#pragma unroll
+        for (int k = 1; k < 3; ++k)
+            v[k] = r.last - i > k * NT * N ? load(x + i + k * NT * N)
+                                           : Vec<T>::none();
+        ready(v);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (r.last - i <= k * NT * N) break;
+            float f[N];
+            Vec<T>::floats(v[k], f);
+            piece(i + k * NT * N, f);
+        }
     }
     if (r.begin + tid < r.first)
         single(r.begin + tid, to_f32(x[r.begin + tid]));
     if (r.last + tid < r.end) single(r.last + tid, to_f32(x[r.last + tid]));
 }
+struct Nothing {
+    template <typename V> __device__ void operator()(const V&) const {}
+};
 
 template <int NT>
 __device__ __forceinline__ u64 block_max(u64 k, u64* keys) {
@@ -195,7 +249,7 @@ template <int NT> struct Shared {
 };
 
 // The `top` largest of this block's part into sh.top, sorted (0: none).
-// own: the largest order among the thread's logits, 0 if it has none.
+// own: the largest order among the thread's logits (-inf's if it has none).
 template <typename T, int NT>
 __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
                                         const Range& r, int top,
@@ -231,10 +285,10 @@ __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
         if (above < top && above + level >= top) sh.bound = gm;
     }
     __syncthreads();
-    const unsigned bound = sh.bound;     // 0: fewer logits than `top`
+    const unsigned bound = sh.bound;
     // a warp reads the pieces of each of its threads that reach the bound
     constexpr int N = Vec<T>::N;
-    unsigned found = __ballot_sync(~0u, own != 0 && own >= bound);
+    unsigned found = __ballot_sync(~0u, own >= bound);
     auto take = [&](int id, float v) {
         if (order_of(v) < bound) return;
         const int at = atomicAdd(&sh.count, 1);
@@ -245,7 +299,7 @@ __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
         for (long long i = r.first + t * N + (long long)lane * NT * N;
              i < r.last; i += 32ll * NT * N) {
             float v[N];
-            Vec<T>::load(x + i, v);
+            Vec<T>::floats(load(x + i), v);
 #pragma unroll
             for (int k = 0; k < N; ++k) take((int)i + k, v[k]);
         }
@@ -276,7 +330,7 @@ __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
             if (k < last && k > best) best = k;
         };
         for_each<T, NT>(
-            x, r,
+            x, r, Nothing(),
             [&](int id, const float (&v)[Vec<T>::N]) {
 #pragma unroll
                 for (int k = 0; k < Vec<T>::N; ++k) look(id + k, v[k]);
@@ -290,7 +344,8 @@ __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
 
 // grid: rows x parts (a cluster each where parts > 1).
 template <typename T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT) logprob_fwd(LogprobArgs a, int parts) {
+__global__ void __launch_bounds__(NT, 1536 / NT)
+logprob_fwd(LogprobArgs a, int parts) {
     __shared__ Shared<NT> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const size_t row = blockIdx.x / parts;
@@ -302,18 +357,20 @@ __global__ void __launch_bounds__(NT) logprob_fwd(LogprobArgs a, int parts) {
     await_grid_before();
     release_grid_after();
     Sums acc{-INFINITY, 0.f, 0.f};
-    unsigned own = 0;
+    float own = -INFINITY;
     for_each<T, NT>(
         x, r,
-        [&](int, const float (&v)[Vec<T>::N]) {
-            const float m = largest_of(v);
-            add(acc, v, m, a.scale);
-            if (TOP) own = max(own, order_of(m));
+        [&](const auto& v) {
+            const float m = Vec<T>::largest(v);
+            refer(acc, m * a.scale);
+            if (TOP) own = max_nan(own, m);
         },
+        [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, a.scale); },
         [&](int, float v) {
             const float one[1] = {v};
-            add(acc, one, v, a.scale);
-            if (TOP) own = max(own, order_of(v));
+            refer(acc, v * a.scale);
+            add(acc, one, a.scale);
+            if (TOP) own = max_nan(own, v);
         });
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -331,7 +388,7 @@ __global__ void __launch_bounds__(NT) logprob_fwd(LogprobArgs a, int parts) {
                                  __shfl_xor_sync(~0u, acc.t, o)});
         if (lane == 0) sh.whole = acc;
     }
-    if (TOP) largest<T, NT>(sh, x, r, a.top, own);
+    if (TOP) largest<T, NT>(sh, x, r, a.top, order_of(own));
     else __syncthreads();
 
     // one block of the row writes; the others' sums and largest come over
@@ -443,7 +500,7 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
                     *reinterpret_cast<const uint4*>(o);
             }
         };
-        for_each<T, NT>(x, r, piece, [&](int id, float v) {
+        for_each<T, NT>(x, r, Nothing(), piece, [&](int id, float v) {
             y[id] = from_f32<T>(grad(id, v));
         });
     } else {
@@ -464,6 +521,7 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
 // ---------------------------------------------------------------- launch
 
 constexpr int kSMs = 152;
+constexpr int kShort = 8192;     // logits up to which 128 threads have a row
 
 // Blocks of a row: up to four for every SM, of at least 4096 logits.
 int parts_of(int N, int V, int most) {
@@ -492,21 +550,27 @@ cudaError_t launch_rows(void (*kernel)(P...), long long rows, int parts,
     return cudaLaunchKernelEx(&cfg, kernel, args..., parts);
 }
 
-template <typename T>
-cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
-    constexpr int NT = 512;
-    const int parts = parts_of(a.N, a.V, kMaxParts);
+template <typename T, int NT>
+cudaError_t launch_fwd_of(const LogprobArgs& a, int parts, cudaStream_t s) {
     return a.top ? launch_rows(logprob_fwd<T, NT, true>, a.N, parts, NT, true,
                                s, a)
                  : launch_rows(logprob_fwd<T, NT, false>, a.N, parts, NT,
                                true, s, a);
 }
+template <typename T>
+cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
+    const int parts = parts_of(a.N, a.V, kMaxParts);
+    return a.V / parts <= kShort ? launch_fwd_of<T, 128>(a, parts, s)
+                                 : launch_fwd_of<T, 256>(a, parts, s);
+}
 
 template <typename T>
 cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
-    constexpr int NT = 512;
     const int parts = parts_of(a.N, a.V, 64);
-    return launch_rows(logprob_bwd<T, NT>, a.N, parts, NT, false, s, a);
+    return a.V / parts <= kShort
+               ? launch_rows(logprob_bwd<T, 128>, a.N, parts, 128, false, s, a)
+               : launch_rows(logprob_bwd<T, 512>, a.N, parts, 512, false, s,
+                             a);
 }
 
 }  // namespace
