@@ -294,19 +294,38 @@ __device__ __forceinline__ void largest(Shared<NT>& sh, const T* x,
         const int at = atomicAdd(&sh.count, 1);
         if (at < kCand) sh.cand[at] = key_of(v, id);
     };
-    for (; found; found &= found - 1) {
-        const int t = (tid & ~31) + __ffs(found) - 1;
-        for (long long i = r.first + t * N + (long long)lane * NT * N;
-             i < r.last; i += 32ll * NT * N) {
+    while (found) {
+        // two at a time: both threads' pieces are on their way together
+        const int t0 = (tid & ~31) + __ffs(found) - 1;
+        found &= found - 1;
+        const int t1 = found ? (tid & ~31) + __ffs(found) - 1 : -1;
+        found &= found - 1;
+        // (a piece's distance from r.first, in 64 bits)
+        for (long long at = (long long)lane * NT * N; at < r.last - r.first;
+             at += 32ll * NT * N) {
+            const long long i0 = r.first + at + t0 * N;
+            const long long i1 = r.first + at + t1 * N;
+            const bool in0 = i0 < r.last, in1 = t1 >= 0 && i1 < r.last;
+            typename Vec<T>::Raw w0 = Vec<T>::none(), w1 = w0;
+            if (in0) w0 = load(x + i0);
+            if (in1) w1 = load(x + i1);
             float v[N];
-            Vec<T>::floats(load(x + i), v);
+            if (in0) {
+                Vec<T>::floats(w0, v);
 #pragma unroll
-            for (int k = 0; k < N; ++k) take((int)i + k, v[k]);
+                for (int k = 0; k < N; ++k) take((int)i0 + k, v[k]);
+            }
+            if (in1) {
+                Vec<T>::floats(w1, v);
+#pragma unroll
+                for (int k = 0; k < N; ++k) take((int)i1 + k, v[k]);
+            }
         }
-        if (lane == 0 && r.begin + t < r.first)
-            take(r.begin + t, to_f32(x[r.begin + t]));
-        if (lane == 1 && r.last + t < r.end)
-            take(r.last + t, to_f32(x[r.last + t]));
+        const int t = lane < 2 ? t0 : t1;
+        if (t >= 0 && lane < 4) {
+            const int i = lane & 1 ? r.last + t : r.begin + t;
+            if (i < (lane & 1 ? r.end : r.first)) take(i, to_f32(x[i]));
+        }
     }
     __syncthreads();
     const int n = sh.count;
@@ -521,7 +540,7 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
 // ---------------------------------------------------------------- launch
 
 constexpr int kSMs = 152;
-constexpr int kShort = 8192;     // logits up to which 128 threads have a row
+constexpr int kShort = 4096;     // logits up to which 128 threads have a row
 
 // Blocks of a row: up to four for every SM, of at least 4096 logits.
 int parts_of(int N, int V, int most) {
