@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const size_t sn = (size_t)dk * dv;
 
     if (tid <= C) w[tid] = power(a, tid);
+    const float* before =
+        STATE_ONLY ? nullptr : la::state_before(p.part, p.plan, part, bh);
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
         float s = 0.f;
@@ -93,8 +95,8 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 if (part == 0 && j.S0)
                     p.part.ws[bh * p.plan.parts * sn + at] =
                         j.S0[bh * sn + at];
-            } else {
-                s = la::state_before(p.part, p.plan, part, bh, at, a);
+            } else if (before) {
+                s = before[at];
             }
         }
         S[i] = s;
@@ -241,6 +243,30 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     }
 }
 
+// A thread has one element of the states of one sequence and head.
+__global__ void __launch_bounds__(256)
+linattn_join(float* ws, const float* log_decay, int parts, int len, int H,
+             int n, int blocks, bool first) {
+    const size_t bh = blockIdx.x / blocks;
+    const int at = blockIdx.x % blocks * 256 + threadIdx.x;
+    if (at >= n) return;
+    const float f = power(log_decay[bh % H], len);
+    float* x = ws + bh * parts * n + at;
+    float s = first ? x[0] : 0.f;
+    for (int i = 1; i < parts; i += 8) {     // eight on their way at a time
+        float u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i + k < parts) u[k] = x[(size_t)(i + k) * n];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (i + k >= parts) break;
+            s = fmaf(f, s, u[k]);
+            x[(size_t)(i + k) * n] = s;
+        }
+    }
+}
+
 // Parts of a sequence: enough for about two blocks an SM, at least 256
 // tokens each.
 Plan plan(long long blocks, int T) {
@@ -273,6 +299,8 @@ cudaError_t launch_job(const PassParams& p, long long bh,
                        cudaStream_t stream) {
     if (p.plan.parts > 1) {
         cudaError_t e = launch_pass<T, DKP, true>(p, bh, stream);
+        if (e == cudaSuccess)
+            e = la::join_parts(p.part, p.plan, p.log_decay, bh, p.H, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_pass<T, DKP, false>(p, bh, stream);
@@ -307,6 +335,15 @@ cudaError_t launch_all(const LinAttnArgs& a, float* ws, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t la::join_parts(const Part& p, const Plan& pl,
+                           const float* log_decay, long long bh, int H,
+                           cudaStream_t stream) {
+    const int n = p.j.dk * p.j.dv, blocks = (n + 255) / 256;
+    linattn_join<<<(unsigned)(bh * blocks), 256, 0, stream>>>(
+        p.ws, log_decay, pl.parts, pl.len, H, n, blocks, p.j.S0 != nullptr);
+    return cudaGetLastError();
+}
 
 // By the sizes alone, whichever form the tensors' alignment allows.
 size_t linattn_workspace_bytes(const LinAttnArgs& a) {

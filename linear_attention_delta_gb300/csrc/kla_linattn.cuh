@@ -16,8 +16,11 @@ __device__ __forceinline__ float power(float a, int n) {
 // Sequences in parts of `len` tokens (a multiple of the chunk; the last part
 // the rest).  With parts > 1 a first launch writes, for each part but the
 // last, the state that its own tokens leave (slot i + 1 of part i) and a copy
-// of S0 (slot 0, if there is one; the main launch may replace S0); the state
-// before part p is then sum over i <= p of w^(len (p - i)) slot_i.
+// of S0 (slot 0, if there is one; the main launch may replace S0).  A second
+// turns them into the states before the parts,
+//   slot_i = w^len slot_{i - 1} + slot_i,
+// so that a block of the main launch reads one state, however many parts come
+// before its own.
 struct Plan {
     int parts, len;
 };
@@ -28,21 +31,20 @@ struct Part {
     int slices;                  // blocks along dv
 };
 
-// Element `at` of the state before part `part` of sequence and head bh.
-__device__ __forceinline__ float state_before(const Part& p, const Plan& pl,
-                                              int part, size_t bh, size_t at,
-                                              float a) {
+// The state before part `part` of sequence and head bh; null: zeros.
+__device__ __forceinline__ const float* state_before(const Part& p,
+                                                     const Plan& pl, int part,
+                                                     size_t bh) {
     const size_t n = (size_t)p.j.dk * p.j.dv;
-    if (pl.parts == 1) return p.j.S0 ? p.j.S0[bh * n + at] : 0.f;
-    float s = 0.f;
-#pragma unroll 1
-    for (int i = p.j.S0 ? 0 : 1; i <= part; ++i)
-        s = fmaf(power(a, (part - i) * pl.len),
-                 p.ws[(bh * pl.parts + i) * n + at], s);
-    return s;
+    if (pl.parts == 1) return p.j.S0 ? p.j.S0 + bh * n : nullptr;
+    return part || p.j.S0 ? p.ws + (bh * pl.parts + part) * n : nullptr;
 }
 
 inline int slices_of(const LinAttnJob& j) { return (j.dv + kNV - 1) / kNV; }
+
+// The second launch above for one pass over B x H sequences and heads.
+cudaError_t join_parts(const Part& p, const Plan& pl, const float* log_decay,
+                       long long bh, int H, cudaStream_t stream);
 
 }  // namespace la
 

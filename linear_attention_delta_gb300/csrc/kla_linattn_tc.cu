@@ -380,22 +380,38 @@ linattn_tc(const __grid_constant__ Maps maps,
     const size_t sn = (size_t)pt.j.dk * pt.j.dv;
     float* slots = pt.ws ? pt.ws + bh * p.plan.parts * sn : nullptr;
     if (warp < 16) {
-#pragma unroll 1
-        for (int i = tid; i < kC * kNV; i += 512) {
-            // along the axis whose elements are adjacent
-            const int r = pt.j.s_c == 1 ? i / kNV : i % kC;
-            const int n = pt.j.s_c == 1 ? i % kNV : i / kC;
-            float x = 0.f;
-            if (r < pt.j.dk && n0 + n < pt.j.dv) {
-                const size_t at =
-                    (size_t)r * pt.j.s_r + (size_t)(n0 + n) * pt.j.s_c;
-                if (!STATE_ONLY)
-                    x = la::state_before(pt, p.plan, part, bh, at, a);
-                else if (part == 0 && pt.j.S0)
-                    slots[at] = pt.j.S0[bh * sn + at];
+        // 16 elements a thread, along the axis whose elements are adjacent;
+        // those of one state are on their way together
+        constexpr int E = kC * kNV / 512;
+        const bool rows = pt.j.s_c == 1;
+        const int r = rows ? tid / kNV : tid % kC;
+        const int n = rows ? tid % kNV : tid / kC;
+        const int dr = rows ? 512 / kNV : 0, dn = rows ? 0 : 512 / kC;
+        const size_t at = (size_t)r * pt.j.s_r + (size_t)(n0 + n) * pt.j.s_c;
+        const size_t step = (size_t)dr * pt.j.s_r + (size_t)dn * pt.j.s_c;
+        float x[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) x[k] = 0.f;
+        auto in = [&](int k) {
+            return r + k * dr < pt.j.dk && n0 + n + k * dn < pt.j.dv;
+        };
+        if (STATE_ONLY) {
+            if (part == 0 && pt.j.S0)
+                for (int k = 0; k < E; ++k)
+                    if (in(k))
+                        slots[at + k * step] =
+                            pt.j.S0[bh * sn + at + k * step];
+        } else {
+            const float* from = la::state_before(pt, p.plan, part, bh);
+            if (from) {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (in(k)) x[k] = from[at + k * step];
             }
-            tile[r * kLdS + n] = x;
         }
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            tile[(r + k * dr) * kLdS + n + k * dn] = x[k];
         tc::named_bar_sync(1, 512);
     }
 
@@ -928,17 +944,31 @@ bool linattn_tc_eligible(const LinAttnArgs& a) {
     return true;
 }
 
+// Parts of a sequence.  A block has an SM to itself, so a launch takes as many
+// turns as its blocks fill the SMs; measured, a chunk takes a block 2.2 us, or
+// 1.1 us where only the state is formed, and a block takes 4 us besides.  More
+// parts fill the last turn better and cost a pass over k and v more.
 la::Plan linattn_tc_plan(const LinAttnArgs& a) {
-    constexpr int kSMs = 152, kLeast = 512;
+    constexpr int kSMs = 152, kMost = 32;
     long long blocks = 0;
     for (int i = 0; i < a.jobs; ++i)
         blocks += (long long)a.B * a.H * la::slices_of(a.job[i]);
-    long long parts = kSMs / blocks;
-    if (parts > a.T / kLeast) parts = a.T / kLeast;
-    if (parts < 2) return {1, a.T};
-    int len = (int)((a.T + parts - 1) / parts);
-    len = (len + kC - 1) / kC * kC;
-    return {(a.T + len - 1) / len, len};
+    const int chunks = (a.T + kC - 1) / kC;
+    Plan best{1, a.T};
+    auto turns = [&](long long n) { return (n + kSMs - 1) / kSMs; };
+    double least = turns(blocks) * (2.2 * chunks + 4.0);
+    for (int p = 2; p <= kMost && p <= chunks; ++p) {
+        const int len = (chunks + p - 1) / p;           // chunks
+        const int parts = (chunks + len - 1) / len;
+        const double t =
+            turns(blocks * parts) * (2.2 * len + 4.0 + 0.4 * parts) +
+            turns(blocks * (parts - 1)) * (1.1 * len + 4.0) + 3.0;
+        if (t < 0.97 * least) {
+            least = t;
+            best = {parts, len * kC};
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_linattn_tc(const LinAttnArgs& a, float* ws,
@@ -961,9 +991,12 @@ cudaError_t launch_linattn_tc(const LinAttnArgs& a, float* ws,
     }
     const bool narrow = widest_key(a) <= 64;
     if (p.plan.parts > 1) {
-        const cudaError_t e =
+        cudaError_t e =
             narrow ? launch<64, true>(maps, p, a.jobs, bh, stream)
                    : launch<128, true>(maps, p, a.jobs, bh, stream);
+        for (int i = 0; i < a.jobs && e == cudaSuccess; ++i)
+            e = la::join_parts(p.part[i], p.plan, a.log_decay, bh, a.H,
+                               stream);
         if (e != cudaSuccess) return e;
     }
     return narrow ? launch<64, false>(maps, p, a.jobs, bh, stream)
