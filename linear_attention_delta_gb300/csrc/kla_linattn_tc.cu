@@ -85,7 +85,7 @@ struct Smem {
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
     static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
     static constexpr int BARS = DONE + 4 * 4;
-    static constexpr int NUM_BARS = 5 * NS + 14;
+    static constexpr int NUM_BARS = 5 * NS + 15;
     static constexpr int MISC = BARS + 8 * NUM_BARS;   // abort, TMEM, issued
     static constexpr int BYTES = MISC + 16 + 1024;     // alignment
     static_assert(BYTES <= 232448, "shared memory");
@@ -108,18 +108,20 @@ struct Bars {
     static constexpr int P_READY = 5 * NS + 2;   // P~ in TMEM
     static constexpr int V_READY = 5 * NS + 3;   // 2: weighted V in place
     static constexpr int U_FULL = 5 * NS + 5;    // 2: U in TMEM (V's parts read)
-    static constexpr int U_FREE = 5 * NS + 7;    // read
-    static constexpr int S_READY = 5 * NS + 8;   // copy of S in place
-    static constexpr int S_FREE = 5 * NS + 9;    // Q S done
-    static constexpr int O_FULL = 5 * NS + 10;   // 2: outputs in TMEM (P~ read)
-    static constexpr int O_FREE = 5 * NS + 12;   // 2: read
+    static constexpr int U_FREE = 5 * NS + 7;    // 2: read
+    static constexpr int S_READY = 5 * NS + 9;   // copy of S in place
+    static constexpr int S_FREE = 5 * NS + 10;   // Q S done
+    static constexpr int O_FULL = 5 * NS + 11;   // 2: outputs in TMEM (P~ read)
+    static constexpr int O_FREE = 5 * NS + 13;   // 2: read
 };
 
 // TMEM columns: all 512
 constexpr uint32_t kColSC = 0;       // 128: scores
 constexpr uint32_t kColP = 128;      // 64: P~, two bf16 a column
 constexpr uint32_t kColO = 192;      // 2 x 64: outputs of even and odd chunks
-constexpr uint32_t kColU = 320;      // 3 x 64: U from each part of V
+constexpr uint32_t kColU = 320;      // 3 x 64: U from each part of V (two of
+                                     // them, from 128 on, where only the
+                                     // state is formed)
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kIdQK = tc::idesc_bf16(128, 128, false, false);
@@ -231,9 +233,16 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Two floats less the two bf16 they were rounded to (exact).
-__device__ __forceinline__ float2 rest(float2 x, uint32_t b) {
-    return fma2(from_bf16x2(b), both(-1.f), x);
+// The upper halves of two floats, as two bf16: their first 8 bits.  What is
+// left has the other 16, so that three parts hold a float whole.
+__device__ __forceinline__ uint32_t upper(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ float2 rest(float2 x) {
+    return fma2(make_float2(
+                    __uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                    __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
+                both(-1.f), x);
 }
 
 // Zeros in place of the values of this thread's pieces of a V tile that are
@@ -331,7 +340,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             const int count =
                 i == B::SC_FREE || i == B::P_READY || i == B::V_READY ||
                         i == B::V_READY + 1 || i == B::U_FREE ||
-                        i == B::S_READY
+                        i == B::U_FREE + 1 || i == B::S_READY
                     ? 8
                 : i == B::O_FREE || i == B::O_FREE + 1 ? 4
                 : i == B::O_FULL || i == B::O_FULL + 1 ? 2 : 1;
@@ -371,6 +380,9 @@ linattn_tc(const __grid_constant__ Maps maps,
     auto tile_token = [&](int c) {
         const int r0 = first + c * kC;
         return rev ? p.T - r0 - kC : r0;
+    };
+    auto u_col = [](int c) -> uint32_t {
+        return STATE_ONLY ? kColU - 3 * kNV * (c & 1) : kColU;
     };
     auto rows_of = [&](int c) { return min(kC, end - (first + c * kC)); };
 
@@ -487,12 +499,13 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             wait_warp(B::V_READY + (c & 1), c >> 1);
             if (STATE_ONLY) wait_warp(B::FULL + s, c / NS);
-            if (c > 0) wait_warp(B::U_FREE, c - 1);
+            if (c >= Sm::NVW)
+                wait_warp(B::U_FREE + ((c - Sm::NVW) & 1), (c - Sm::NVW) >> 1);
             tc::tc_fence_after();
             if (issuer) {
 #pragma unroll 2
                 for (int ks = 0; ks < kC / 16; ++ks)
-                    tc::mma_bf16(tmem + kColU, dKt + at + ks * 128,
+                    tc::mma_bf16(tmem + u_col(c), dKt + at + ks * 128,
                                  dVw + c % Sm::NVW * (3 * kBox >> 4) + ks * 128,
                                  kIdU, ks > 0);
                 commit(B::U_FULL + (c & 1), c >> 1);
@@ -567,7 +580,7 @@ linattn_tc(const __grid_constant__ Maps maps,
         };
         if (!STATE_ONLY) copy_S();
         const uint32_t ucol =
-            tmem + ((uint32_t)(d & 96) << 16) + kColU + (warp >> 2) * W;
+            tmem + ((uint32_t)(d & 96) << 16) + (warp >> 2) * W;
         // w^n S as S + (w^n - 1) S: a decay close to 1 keeps its digits
         float grow = expm1f(a * (float)kC);
 #pragma unroll 1
@@ -580,7 +593,7 @@ linattn_tc(const __grid_constant__ Maps maps,
                 float u[3][8];
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
-                    tc::tmem_ld8(ucol + kNV * k + m, u[k]);
+                    tc::tmem_ld8(ucol + u_col(c) + kNV * k + m, u[k]);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -594,7 +607,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             }
             tc::tc_fence_before();
             if (c + 1 < nchunks) {
-                arrive(B::U_FREE);
+                arrive(B::U_FREE + (c & 1));
                 if (!STATE_ONLY) {
                     wait_warp(B::S_FREE, c);
                     copy_S();
@@ -644,11 +657,10 @@ linattn_tc(const __grid_constant__ Maps maps,
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float2 y = mul2(from_bf16x2(xs[k]), both(f));
-                    o[0][k] = tc::pack_bf16x2(y.x, y.y);
-                    y = rest(y, o[0][k]);
-                    o[1][k] = tc::pack_bf16x2(y.x, y.y);
-                    y = rest(y, o[1][k]);
-                    o[2][k] = tc::pack_bf16x2(y.x, y.y);
+                    o[0][k] = upper(y);
+                    y = rest(y);
+                    o[1][k] = upper(y);
+                    o[2][k] = upper(rest(y));
                     seen |= o[2][k];
                 }
 #pragma unroll
