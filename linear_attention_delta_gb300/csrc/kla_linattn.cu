@@ -1,5 +1,6 @@
-// Linear attention with a decay for each head: the chunked pass on the CUDA
-// cores (any width up to 256, fp32 or bf16, any strides) and one token.
+// Linear attention with a decay for each head: the chunked pass for fp32 and
+// for what the bf16 form on tcgen05 does not take (wide or odd heads, rows off
+// their 16 bytes), and one token.
 //
 // A pass (see LinAttnJob) counts its tokens r from the first or, in reverse,
 // from the last.  Over a chunk of C tokens, with S the state before it and
@@ -9,7 +10,15 @@
 //   S   <- w^C S + sum_s w^(C - e - s) k_s v_s^T
 // so that the work per token is 2 C (dk + dv) / 2 + 4 dk dv products instead
 // of a state update per token, and the state leaves the chip never.
+//
+// The products are warp-level ones of tf32 (mma.sync): a number of fp32 is two
+// of tf32, x = hi + lo up to 2^-23, and x y = hi hi' + hi lo' + lo hi' up to
+// 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
+// operands from shared memory as they are; three times the tiles of fp32 would
+// not fit there.)
+#include "f32x2.cuh"
 #include "kla_linattn.cuh"
+#include "tc_primitives.cuh"
 
 namespace kla {
 namespace {
@@ -22,17 +31,58 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------ chunked pass
 
-constexpr int kNT = 256;
+constexpr int kNT = 512;
 
 template <int DKP>
 struct Shape {
     static constexpr int C = DKP == 256 ? 32 : 64;   // tokens a chunk
-    static constexpr int LD = DKP + 4;   // row of q or k: 16 rows that lie
-                                         // 16 apart start in 8 bank groups
+    // rows of q, k and P lie 4 banks apart, those of v and S 8: a warp's
+    // fragments come from 32 different banks
+    static constexpr int LD = DKP + 4;
     static constexpr int LP = C + 4;
-    static constexpr int FLOATS =
-        2 * C * LD + C * kNV + C * LP + DKP * kNV + C + 4;
+    static constexpr int LV = kNV + 8;
+    static constexpr int FLOATS = 2 * C * LD + C * LV + C * LP + DKP * LV +
+                                  C + 4 + kNV;
 };
+
+// A number as one or two of tf32 (11 bits; the products look at no lower
+// ones), the first rounded by adding half a step to its bits (the conversion
+// instruction has a quarter of the rate), the second cut off: 2^-22 of x.
+template <bool EXACT>
+struct Split {
+    uint32_t hi, lo;
+    __device__ __forceinline__ explicit Split(float x) {
+        hi = __float_as_uint(x);
+        lo = 0;
+        if (!EXACT) {
+            hi = (hi + 0x1000u) & 0xffffe000u;
+            // what is not finite: NaN here, whatever hi is
+            lo = __float_as_uint(x - __uint_as_float(hi));
+        }
+    }
+};
+template <bool EXACT>
+struct FragA {
+    uint32_t hi[4], lo[4];
+    // elements (row g or g + 8, step t or t + 4)
+    __device__ __forceinline__ FragA(float x0, float x1, float x2, float x3) {
+        const float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Split<EXACT> s(x[i]);
+            hi[i] = s.hi, lo[i] = s.lo;
+        }
+    }
+};
+// d += a b (16 x 8 x 8) to the precision above.
+template <bool XA, bool XB>
+__device__ __forceinline__ void mma(float (&d)[4], const FragA<XA>& a,
+                                    float b0, float b1) {
+    const Split<XB> x(b0), y(b1);
+    if (!XA) tc::mma_m16n8k8_tf32(d, a.lo, x.hi, y.hi);
+    if (!XB) tc::mma_m16n8k8_tf32(d, a.hi, x.lo, y.lo);
+    tc::mma_m16n8k8_tf32(d, a.hi, x.hi, y.hi);
+}
 
 struct PassParams {
     Part part;
@@ -42,14 +92,49 @@ struct PassParams {
 };
 
 // Rows r0 .. r0 + C - 1 (in the pass's order) of x into dst [C][ld], zeros
-// beyond `rows` and `width`; columns c0 .. c0 + W - 1.
+// beyond `rows` and `width`; columns c0 .. c0 + W - 1, the first `most` of
+// them.
+// Four adjacent elements at a time where they line up (`by4`), eight such on
+// their way at a time.
 template <typename T, int C, int W>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
                                           long long st, long long first,
                                           long long step, int rows, int c0,
-                                          int width) {
+                                          int width, int most, bool by4) {
+    if (by4) {
+        constexpr int N = C * W / 4 / kNT > 0 ? C * W / 4 / kNT : 1;
+        constexpr int K = N < 8 ? N : 8;
+        for (int i0 = threadIdx.x; i0 < C * W / 4; i0 += K * kNT) {
+            float4 v[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int i = i0 + k * kNT, r = i / (W / 4), c = i % (W / 4) * 4;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < C * W / 4 && r < rows && c0 + c < width) {
+                    const T* from = x + (first + step * r) * st + c0 + c;
+                    if constexpr (sizeof(T) == 4) {
+                        v[k] = *reinterpret_cast<const float4*>(from);
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(from);
+                        const float2 y = from_bf16x2(u.x);
+                        const float2 z = from_bf16x2(u.y);
+                        v[k] = make_float4(y.x, y.y, z.x, z.y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int i = i0 + k * kNT, r = i / (W / 4), c = i % (W / 4) * 4;
+                if (i < C * W / 4 && c < most)
+                    *reinterpret_cast<float4*>(&dst[r * ld + c]) = v[k];
+            }
+        }
+        return;
+    }
+#pragma unroll 8
     for (int i = threadIdx.x; i < C * W; i += kNT) {
         const int r = i / W, c = i % W;
+        if (c >= most) continue;
         float v = 0.f;
         if (r < rows && c0 + c < width)
             v = to_f32(x[(first + step * r) * st + c0 + c]);
@@ -57,21 +142,45 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
     }
 }
 
+// The same rows on their way into L2, a line a thread.
+template <typename T, int C>
+__device__ __forceinline__ void prefetch_rows(const T* x, long long st,
+                                              long long first, long long step,
+                                              int rows, int c0, int width) {
+    const int lines = (width * (int)sizeof(T) + 127) / 128;
+    for (int i = threadIdx.x; i < rows * lines; i += kNT) {
+        const T* at = x + (first + step * (i / lines)) * st + c0 +
+                      i % lines * (128 / (int)sizeof(T));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+}
+
+// Whether rows of x can be read four elements at a time.
+template <typename T>
+__device__ __forceinline__ bool in_fours(const T* x, long long st, int width) {
+    return (reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T))) == 0 &&
+           st % 4 == 0 && width % 4 == 0;
+}
+
 template <typename T, int DKP, bool STATE_ONLY>
 __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     using Sh = Shape<DKP>;
+    constexpr int C = Sh::C, LD = Sh::LD, LP = Sh::LP, LV = Sh::LV;
+    constexpr bool X = sizeof(T) == 2;      // inputs are one of tf32 each
+    // 16 warps: tiles of 16 rows, NG groups of 8-column tiles
+    constexpr int MT = C / 16, NG = 16 / MT, NO = kNV / 8 / NG;
+    constexpr int UT = DKP / 16, UG = 16 / UT, NU = kNV / 8 / UG;
     const LinAttnJob& j = p.part.j;
-    constexpr int C = Sh::C, LD = Sh::LD, LP = Sh::LP;
-    constexpr int RI = C / 16;       // rows, and columns of P, of a thread
-    constexpr int RD = DKP / 16;     // rows of the state of a thread
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
     float* Ks = Qs + C * LD;
     float* Vs = Ks + C * LD;
-    float* Ps = Vs + C * kNV;
+    float* Ps = Vs + C * LV;
     float* S = Ps + C * LP;
-    float* w = S + DKP * kNV;        // w^0 .. w^C
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    float* w = S + DKP * LV;         // w^0 .. w^C
+    int* bad = reinterpret_cast<int*>(w + C + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
     const int slice = blockIdx.x % p.part.slices, n0 = slice * kNV;
     const size_t bh = blockIdx.x / p.part.slices;
     const int b = bh / p.H, h = bh % p.H, part = blockIdx.y;
@@ -82,10 +191,12 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const T* v = static_cast<const T*>(j.v.p) + b * j.v.sb + h * j.v.sh;
     T* o = static_cast<T*>(j.o);
     const size_t sn = (size_t)dk * dv;
+    const int dk8 = (dk + 7) / 8 * 8;     // columns of q and k that are looked at
 
     if (tid <= C) w[tid] = power(a, tid);
     const float* before =
         STATE_ONLY ? nullptr : la::state_before(p.part, p.plan, part, bh);
+#pragma unroll 4
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
         float s = 0.f;
@@ -99,9 +210,11 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 s = before[at];
             }
         }
-        S[i] = s;
+        S[r * LV + i % kNV] = s;
     }
 
+    const bool q4 = in_fours(q, j.q.st, dk), k4 = in_fours(k, j.k.st, dk);
+    const bool v4 = in_fours(v, j.v.st, dv);
     const int first = part * p.plan.len;
     const int end = min(p.T, first + p.plan.len);
     const long long step = j.reverse ? -1 : 1;
@@ -109,137 +222,164 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         const int rows = min(C, end - r0);
         const long long t0 = j.reverse ? p.T - 1 - r0 : r0;
         if (!STATE_ONLY)
-            load_rows<T, C, DKP>(Qs, LD, q, j.q.st, t0, step, rows, 0, dk);
-        load_rows<T, C, DKP>(Ks, LD, k, j.k.st, t0, step, rows, 0, dk);
-        load_rows<T, C, kNV>(Vs, kNV, v, j.v.st, t0, step, rows, n0, dv);
+            load_rows<T, C, DKP>(Qs, LD, q, j.q.st, t0, step, rows, 0, dk, dk8,
+                                 q4);
+        load_rows<T, C, DKP>(Ks, LD, k, j.k.st, t0, step, rows, 0, dk, dk8,
+                             k4);
+        load_rows<T, C, kNV>(Vs, LV, v, j.v.st, t0, step, rows, n0, dv, kNV,
+                             v4);
+        if (r0 + C < end) {
+            const int more = min(C, end - r0 - C);
+            const long long t1 = t0 + step * C;
+            if (!STATE_ONLY)
+                prefetch_rows<T, C>(q, j.q.st, t1, step, more, 0, dk);
+            prefetch_rows<T, C>(k, j.k.st, t1, step, more, 0, dk);
+            prefetch_rows<T, C>(v, j.v.st, t1, step, more, n0,
+                                min(kNV, dv - n0));
+        }
+        if (tid < kNV) bad[tid] = C;
         __syncthreads();
+        // What is not finite in v is taken out, as in P v it would meet the
+        // zeros of earlier rows; its column's later outputs and state get NaN.
+#pragma unroll 4
+        for (int i = tid; i < C * kNV; i += kNT) {
+            float* x = &Vs[i / kNV * LV + i % kNV];
+            if ((__float_as_uint(*x) & 0x7f800000u) == 0x7f800000u) {
+                *x = 0.f;
+                atomicMin(&bad[i % kNV], i / kNV);
+            }
+        }
+        const int m = warp % MT, ng = warp / MT;
+        float acc[NO][4];
         if (!STATE_ONLY) {
-            float s[RI][RI] = {};
-#pragma unroll 2
-            for (int d = 0; d < DKP; d += 4) {
-                float4 x[RI], y[RI];
+            // scores, 16 rows x NO 8-column tiles a warp
+            if (ng * NO * 8 < C) {
 #pragma unroll
-                for (int i = 0; i < RI; ++i) {
-                    x[i] = *reinterpret_cast<const float4*>(
-                        &Qs[(ty + 16 * i) * LD + d]);
-                    y[i] = *reinterpret_cast<const float4*>(
-                        &Ks[(tx + 16 * i) * LD + d]);
+                for (int n = 0; n < NO; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                const float* x = &Qs[(16 * m + g) * LD + t];
+                const float* y = &Ks[(ng * NO * 8 + g) * LD + t];
+                // columns all above the diagonal stay 0
+                const int last = 16 * m + 15 < ng * NO * 8 ? 0 : dk8;
+#pragma unroll 2
+                for (int d = 0; d < last; d += 8) {
+                    const FragA<X> f(x[d], x[8 * LD + d], x[d + 4],
+                                     x[8 * LD + d + 4]);
+#pragma unroll
+                    for (int n = 0; n < NO; ++n)
+                        mma<X, X>(acc[n], f, y[8 * n * LD + d],
+                                  y[8 * n * LD + d + 4]);
                 }
 #pragma unroll
-                for (int i = 0; i < RI; ++i)
+                for (int n = 0; n < NO; ++n)
 #pragma unroll
-                    for (int j = 0; j < RI; ++j)
-                        s[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z,
-                                  fmaf(x[i].y, y[j].y,
-                                       fmaf(x[i].x, y[j].x, s[i][j]))));
-            }
-#pragma unroll
-            for (int i = 0; i < RI; ++i)
-#pragma unroll
-                for (int j = 0; j < RI; ++j) {
-                    const int r = ty + 16 * i, c = tx + 16 * j;
-                    Ps[r * LP + c] = c <= r ? s[i][j] * w[r - c] : 0.f;
-                }
-            __syncthreads();
-
-            float acc[RI][4] = {};
-#pragma unroll 2
-            for (int d = 0; d < DKP; d += 4) {
-                float4 x[RI], y[4];
-#pragma unroll
-                for (int i = 0; i < RI; ++i)
-                    x[i] = *reinterpret_cast<const float4*>(
-                        &Qs[(ty + 16 * i) * LD + d]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    y[j] = *reinterpret_cast<const float4*>(
-                        &S[(d + j) * kNV + 4 * tx]);
-#pragma unroll
-                for (int i = 0; i < RI; ++i) {
-                    const float z[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][0] = fmaf(z[j], y[j].x, acc[i][0]);
-                        acc[i][1] = fmaf(z[j], y[j].y, acc[i][1]);
-                        acc[i][2] = fmaf(z[j], y[j].z, acc[i][2]);
-                        acc[i][3] = fmaf(z[j], y[j].w, acc[i][3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * m + g + (i >> 1) * 8;
+                        const int c = (ng * NO + n) * 8 + 2 * t + (i & 1);
+                        Ps[r * LP + c] =
+                            c <= r ? acc[n][i] * w[r - c] : 0.f;
                     }
-                }
             }
 #pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                const float u = w[ty + 16 * i + e];
+            for (int n = 0; n < NO; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) acc[i][n] *= u;
-            }
-            // later rows are skipped, not multiplied by 0: what is not finite
-            // in them may not reach this one
+                for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+            // Q S, its rows times w^(r + e)
+            {
+                const float* x = &Qs[(16 * m + g) * LD + t];
+                const float* y = &S[t * LV + ng * NO * 8 + g];
 #pragma unroll 2
-            for (int c = 0; c < C; ++c) {
-                const float4 y =
-                    *reinterpret_cast<const float4*>(&Vs[c * kNV + 4 * tx]);
+                for (int d = 0; d < dk8; d += 8) {
+                    const FragA<X> f(x[d], x[8 * LD + d], x[d + 4],
+                                     x[8 * LD + d + 4]);
 #pragma unroll
-                for (int i = 0; i < RI; ++i) {
-                    const int r = ty + 16 * i;
-                    if (c <= r) {
-                        const float x = Ps[r * LP + c];
-                        acc[i][0] = fmaf(x, y.x, acc[i][0]);
-                        acc[i][1] = fmaf(x, y.y, acc[i][1]);
-                        acc[i][2] = fmaf(x, y.z, acc[i][2]);
-                        acc[i][3] = fmaf(x, y.w, acc[i][3]);
-                    }
+                    for (int n = 0; n < NO; ++n)
+                        mma<X, false>(acc[n], f, y[d * LV + 8 * n],
+                                      y[(d + 4) * LV + 8 * n]);
                 }
+                const float u0 = w[16 * m + g + e], u1 = w[16 * m + g + 8 + e];
+#pragma unroll
+                for (int n = 0; n < NO; ++n)
+                    acc[n][0] *= u0, acc[n][1] *= u0, acc[n][2] *= u1,
+                        acc[n][3] *= u1;
+            }
+        }
+        __syncthreads();             // P in place; S read
+        if (!STATE_ONLY) {
+            const float* x = &Ps[(16 * m + g) * LP + t];
+            const float* y = &Vs[t * LV + ng * NO * 8 + g];
+#pragma unroll 2
+            for (int c = 0; c < 16 * m + 16; c += 8) {
+                const FragA<false> f(x[c], x[8 * LP + c], x[c + 4],
+                                     x[8 * LP + c + 4]);
+#pragma unroll
+                for (int n = 0; n < NO; ++n)
+                    mma<false, X>(acc[n], f, y[c * LV + 8 * n],
+                                  y[(c + 4) * LV + 8 * n]);
             }
 #pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                const int r = ty + 16 * i;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * m + g + (i >> 1) * 8;
                 if (r >= rows) continue;
-                const size_t t = (size_t)(t0 + step * r);
-                T* dst = o + (((size_t)b * p.T + t) * p.H + h) * dv;
+                const size_t at = (size_t)(t0 + step * r);
+                T* dst = o + (((size_t)b * p.T + at) * p.H + h) * dv + n0;
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    if (n0 + 4 * tx + n < dv)
-                        dst[n0 + 4 * tx + n] = from_f32<T>(acc[i][n]);
-            }
-            __syncthreads();
-        }
-        // w^n S as S + (w^n - 1) S: n * log_decay close to 0 keeps its digits
-        const float grow = expm1f(a * (float)rows);
-        float4 u[RD] = {};
-        for (int c = 0; c < rows; ++c) {
-            const float x = w[rows - e - c];
-            float4 y = *reinterpret_cast<const float4*>(&Vs[c * kNV + 4 * tx]);
-            y.x *= x, y.y *= x, y.z *= x, y.w *= x;
-            const float* kr = &Ks[c * LD + ty * RD];
-#pragma unroll
-            for (int d = 0; d < RD; ++d) {
-                u[d].x = fmaf(kr[d], y.x, u[d].x);
-                u[d].y = fmaf(kr[d], y.y, u[d].y);
-                u[d].z = fmaf(kr[d], y.z, u[d].z);
-                u[d].w = fmaf(kr[d], y.w, u[d].w);
+                for (int n = 0; n < NO; ++n) {
+                    const int c = (ng * NO + n) * 8 + 2 * t + (i & 1);
+                    if (n0 + c < dv)
+                        dst[c] = from_f32<T>(r < bad[c]
+                                                 ? acc[n][i]
+                                                 : __uint_as_float(0x7fc00000u));
+                }
             }
         }
+        // U: 16 rows of the state x NU 8-column tiles a warp
+        const int um = warp % UT, ug = warp / UT;
+        if (16 * um < dk) {
+            float u[NU][4];
 #pragma unroll
-        for (int d = 0; d < RD; ++d) {
-            float4* s = reinterpret_cast<float4*>(
-                &S[(ty * RD + d) * kNV + 4 * tx]);
-            float4 x = *s;
-            x.x = fmaf(grow, x.x, x.x) + u[d].x;
-            x.y = fmaf(grow, x.y, x.y) + u[d].y;
-            x.z = fmaf(grow, x.z, x.z) + u[d].z;
-            x.w = fmaf(grow, x.w, x.w) + u[d].w;
-            *s = x;
+            for (int n = 0; n < NU; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[n][i] = 0.f;
+            const float* x = &Ks[t * LD + 16 * um + g];
+            const float* y = &Vs[t * LV + ug * NU * 8 + g];
+#pragma unroll 2
+            for (int c = 0; c < rows; c += 8) {
+                const FragA<X> f(x[c * LD], x[c * LD + 8], x[(c + 4) * LD],
+                                 x[(c + 4) * LD + 8]);
+                // rows beyond the sequence are zero: their weight is any
+                const float w0 = w[max(0, rows - e - c - t)];
+                const float w1 = w[max(0, rows - e - c - t - 4)];
+#pragma unroll
+                for (int n = 0; n < NU; ++n)
+                    mma<X, false>(u[n], f, w0 * y[c * LV + 8 * n],
+                                  w1 * y[(c + 4) * LV + 8 * n]);
+            }
+            // w^n S as S + (w^n - 1) S: n * log_decay close to 0 keeps its
+            // digits
+            const float grow = expm1f(a * (float)rows);
+#pragma unroll
+            for (int n = 0; n < NU; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = (ug * NU + n) * 8 + 2 * t + (i & 1);
+                    float* s = &S[(16 * um + g + (i >> 1) * 8) * LV + c];
+                    *s = bad[c] < C ? __uint_as_float(0x7fc00000u)
+                                    : fmaf(grow, *s, *s) + u[n][i];
+                }
         }
         __syncthreads();
     }
 
     if (!STATE_ONLY && (part + 1 < p.plan.parts || !j.ST)) return;
-    float* dst = STATE_ONLY ? p.part.ws + (bh * p.plan.parts + part + 1) * sn
-                            : j.ST + bh * sn;
+    float* dst = STATE_ONLY
+                     ? p.part.ws + (bh * p.plan.parts + part + 1) * sn
+                     : j.ST + bh * sn;
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
         if (r < dk && c < dv)
-            dst[(size_t)r * j.s_r + (size_t)c * j.s_c] = S[i];
+            dst[(size_t)r * j.s_r + (size_t)c * j.s_c] = S[r * LV + i % kNV];
     }
 }
 
@@ -267,17 +407,27 @@ linattn_join(float* ws, const float* log_decay, int parts, int len, int H,
     }
 }
 
-// Parts of a sequence: enough for about two blocks an SM, at least 256
-// tokens each.
-Plan plan(long long blocks, int T) {
-    constexpr int kSMs = 152, kLeast = 256;
-    long long parts = 2 * kSMs / blocks;
-    if (parts > T / kLeast) parts = T / kLeast;
-    if (parts > 32) parts = 32;
-    if (parts < 2) return {1, T};
-    int len = (int)((T + parts - 1) / parts);
-    len = (len + 63) / 64 * 64;
-    return {(T + len - 1) / len, len};
+// Parts of a sequence.  A launch takes as many turns as its blocks, one an
+// SM, fill the SMs.  Counted in chunks: a
+// block takes about half a chunk's time besides its own, a chunk of the pass
+// that forms the state 0.35, and the two launches more about one.
+Plan plan(long long blocks, int dk, int T) {
+    const int C = dk > 128 ? 32 : 64, slots = 152;
+    const int chunks = (T + C - 1) / C;
+    auto turns = [&](long long n) { return (double)((n + slots - 1) / slots); };
+    Plan best{1, T};
+    double least = turns(blocks) * (chunks + 0.5);
+    for (int p = 2; p <= 32 && p <= chunks; ++p) {
+        const int len = (chunks + p - 1) / p;
+        const int parts = (chunks + len - 1) / len;
+        const double t = turns(blocks * parts) * (len + 0.5) +
+                         turns(blocks * (parts - 1)) * (0.35 * len + 0.5) + 1;
+        if (t < 0.97 * least) {
+            least = t;
+            best = {parts, len * C};
+        }
+    }
+    return best;
 }
 
 template <typename T, int DKP, bool STATE_ONLY>
@@ -307,7 +457,8 @@ cudaError_t launch_job(const PassParams& p, long long bh,
 }
 
 Plan plan_of(const LinAttnArgs& a, int job) {
-    return plan((long long)a.B * a.H * la::slices_of(a.job[job]), a.T);
+    const LinAttnJob& j = a.job[job];
+    return plan((long long)a.B * a.H * la::slices_of(j), j.dk, a.T);
 }
 
 // Floats of the part states of a job.

@@ -576,6 +576,8 @@ def decode_step_kw(q, k, k_write, v, log_alpha, eta, S, eps: float = 1e-6,
 
 _F32, _IO = (torch.float32,), tuple(DTYPES)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_Tensor = torch.Tensor
 
 
 def _addr(t):
@@ -613,7 +615,7 @@ def _device_of(name, t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (no CPU fallback)")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current "
                          f"device")
     if t.dtype not in DTYPES:
@@ -936,23 +938,29 @@ def _head_inputs(names, tensors, shapes, device, dtype):
     """Pointer and strides of each [..., H, d] input, checked."""
     out = []
     for name, t, shape in zip(names, tensors, shapes):
-        if not _plain(t, device, dtype, shape):
+        if not (isinstance(t, _Tensor) and t.dtype is dtype
+                and t.get_device() == device and t.shape == shape
+                and t.stride(-1) == 1):
             _check(name, t, device, (dtype,), shape)
-        out += [t.data_ptr(), *t.stride()[:-1]]
+        out.append(t.data_ptr())
+        out.extend(t.stride()[:-1])
     return out
 
 
 def _linattn_shape(q, v, ndim):
-    """(device, dtype, sizes before the width, dk, dv) of a call."""
+    """(device, dtype, q's shape, v's shape) of a call."""
     dev = _device_of("q", q)
-    if q.ndim != ndim or not isinstance(v, torch.Tensor) or v.ndim != ndim:
+    qs, vs = q.shape, getattr(v, "shape", ())
+    if len(qs) != ndim or len(vs) != ndim:
         raise ValueError("q, k and v must be "
                          + ("[B, T, H, d]" if ndim == 4 else "[N, H, d]"))
-    dk, dv = q.shape[-1], v.shape[-1]
-    if dk < 1 or dv < 1:
+    if qs[-1] < 1 or vs[-1] < 1:
         raise ValueError("q, k and v must be at least one wide")
-    _counts(*q.shape, dv)
-    return dev, q.dtype, q.shape[:-1], dk, dv
+    if qs[:-1] != vs[:-1]:
+        raise ValueError(f"v must have shape {tuple(qs[:-1])} before its "
+                         f"width, got {tuple(vs)}")
+    _counts(*qs, vs[-1])
+    return dev, q.dtype, qs, vs
 
 
 @functools.lru_cache(maxsize=256)
@@ -986,16 +994,16 @@ def linattn_fwd(q, k, v, log_decay, h0=None, o=None, hT=None,
         with torch.cuda.stream(stream):
             return linattn_fwd(q, k, v, log_decay, h0, o, hT, want_state,
                                workspace)
-    dev, dt, (B, T, H), dk, dv = _linattn_shape(q, v, 4)
-    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, (B, T, H, dv)),
-                       dev, dt)
+    dev, dt, qs, vs = _linattn_shape(q, v, 4)
+    (B, T, H, dk), dv = qs, vs[3]
+    ins = _head_inputs("qkv", (q, k, v), (qs, qs, vs), dev, dt)
     _exact("log_decay", log_decay, dev, torch.float32, (H,))
     if h0 is not None:
         _exact("h0", h0, dev, torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = torch.empty(vs, dtype=dt, device=dev)
     else:
-        _exact("o", o, dev, dt, (B, T, H, dv))
+        _exact("o", o, dev, dt, vs)
     if hT is not None:
         _exact("hT", hT, dev, torch.float32, (B, H, dk, dv))
     elif want_state:
@@ -1024,16 +1032,16 @@ def linattn_bwd(q, k, v, log_decay, o_grad, hT_grad=None, h0=None,
         with torch.cuda.stream(stream):
             return linattn_bwd(q, k, v, log_decay, o_grad, hT_grad, h0,
                                want_h0_grad, workspace)
-    dev, dt, (B, T, H), dk, dv = _linattn_shape(q, v, 4)
-    vs = (B, T, H, dv)
-    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, vs), dev, dt)
+    dev, dt, qs, vs = _linattn_shape(q, v, 4)
+    (B, T, H, dk), dv = qs, vs[3]
+    ins = _head_inputs("qkv", (q, k, v), (qs, qs, vs), dev, dt)
     do = _head_inputs(("o_grad",), (o_grad,), (vs,), dev, dt)
     _exact("log_decay", log_decay, dev, torch.float32, (H,))
     for name, t in (("h0", h0), ("hT_grad", hT_grad)):
         if t is not None:
             _exact(name, t, dev, torch.float32, (B, H, dk, dv))
-    dq = torch.empty((B, T, H, dk), dtype=dt, device=dev)
-    dkey = torch.empty_like(dq)
+    dq = torch.empty(qs, dtype=dt, device=dev)
+    dkey = torch.empty(qs, dtype=dt, device=dev)
     dval = torch.empty(vs, dtype=dt, device=dev)
     dh0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) \
         if want_h0_grad else None
@@ -1059,15 +1067,15 @@ def linattn_step(q, k, v, log_decay, S, o=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return linattn_step(q, k, v, log_decay, S, o)
-    dev, dt, (N, H), dk, dv = _linattn_shape(q, v, 3)
-    ins = _head_inputs("qkv", (q, k, v), (q.shape, q.shape, (N, H, dv)), dev,
-                       dt)
+    dev, dt, qs, vs = _linattn_shape(q, v, 3)
+    (N, H, dk), dv = qs, vs[2]
+    ins = _head_inputs("qkv", (q, k, v), (qs, qs, vs), dev, dt)
     _exact("log_decay", log_decay, dev, torch.float32, (H,))
     _exact("S", S, dev, torch.float32, (N, H, dk, dv))
     if o is None:
-        o = torch.empty((N, H, dv), dtype=dt, device=dev)
+        o = torch.empty(vs, dtype=dt, device=dev)
     else:
-        _exact("o", o, dev, dt, (N, H, dv))
+        _exact("o", o, dev, dt, vs)
     st = load_library().kla_linattn_step(
         *ins, log_decay.data_ptr(), S.data_ptr(), o.data_ptr(), N, H, dk, dv,
         DTYPES[dt], _raw_stream(dev))

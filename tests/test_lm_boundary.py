@@ -138,7 +138,8 @@ def test_linattn_workspace(lib):
     size = kla.linattn_workspace_size
     for back in (False, True):
         assert size(64, 4096, 16, 128, 128, torch.bfloat16, back) == 0
-        assert size(1, 255, 1, 64, 64, torch.float32, back) == 0
+        assert size(1, 64, 1, 64, 64, torch.float32, back) == 0
+        assert size(1, 128, 1, 64, 64, torch.bfloat16, back) <= 3 * 4 * 64 * 64 * 4
         n = size(1, 65536, 4, 128, 64, torch.bfloat16, back)
         assert 0 < n <= (3 if back else 1) * 64 * 4 * 128 * 64 * 4
 
