@@ -5,9 +5,9 @@ sequences and then run token by token.
 
 Every norm takes the residual add in front of it (``kla.layernorm_fwd`` with
 ``residual``), the mixer's recurrence is ``kla.glr_fwd`` over packed sequences
-of different lengths, both with their backward passes; decoding carries one
-state per block with ``kla.glr_step``.  The projections are plain matrix
-products.  The task: repeat, in every position, the token seen `lag` positions
+of different lengths, the loss comes from ``kla.logprob_fwd``, all with their
+backward passes; decoding carries one state per block with ``kla.glr_step``.
+The projections are plain matrix products.  The task: repeat, in every position, the token seen `lag` positions
 before, which takes memory.
 
     python examples/recurrent_lm.py [--steps 200]
@@ -60,6 +60,24 @@ class Recurrence(torch.autograd.Function):
         g = kla.glr_bwd(o, log_alpha, do.contiguous(), dhT, cu_seqlens=cu,
                         want_h0_grad=False)
         return g["x_grad"], g["log_alpha_grad"], None
+
+
+class TokenLoss(torch.autograd.Function):
+    """Minus the mean log probability of the targets that are there (a target
+    below 0 is none)."""
+
+    @staticmethod
+    def forward(ctx, logits, target):
+        logp, _, lse, _, _ = kla.logprob_fwd(logits, target)
+        count = (target >= 0).sum().clamp(min=1)
+        ctx.save_for_backward(logits, target, lse, count)
+        return -logp.sum() / count
+
+    @staticmethod
+    def backward(ctx, g):
+        logits, target, lse, count = ctx.saved_tensors
+        weight = (-g / count).expand(target.shape).contiguous()
+        return kla.logprob_bwd(logits, target, lse, logp_grad=weight), None
 
 
 class Model(torch.nn.Module):
@@ -140,7 +158,7 @@ def main(steps=200, lag=2, vocab=32, seed=0):
     for i in range(steps):
         tokens, target, cu = batch(lens, vocab, lag, gen)
         logits, _ = model(tokens, cu)
-        loss = F.cross_entropy(logits.float(), target, ignore_index=-1)
+        loss = TokenLoss.apply(logits, target)
         opt.zero_grad()
         loss.backward()
         opt.step()

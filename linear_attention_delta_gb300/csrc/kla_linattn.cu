@@ -74,14 +74,19 @@ struct FragA {
         }
     }
 };
-// d += a b (16 x 8 x 8) to the precision above.
+// d += a b (16 x 8 x 8) to the precision above.  The sum over k is d's own, in
+// fp32: the product instruction cuts off what it adds up, which over a row of
+// 72 ended 4 times as far from the exact sum.
 template <bool XA, bool XB>
 __device__ __forceinline__ void mma(float (&d)[4], const FragA<XA>& a,
                                     float b0, float b1) {
     const Split<XB> x(b0), y(b1);
-    if (!XA) tc::mma_m16n8k8_tf32(d, a.lo, x.hi, y.hi);
-    if (!XB) tc::mma_m16n8k8_tf32(d, a.hi, x.lo, y.lo);
-    tc::mma_m16n8k8_tf32(d, a.hi, x.hi, y.hi);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!XA) tc::mma_m16n8k8_tf32(s, a.lo, x.hi, y.hi);
+    if (!XB) tc::mma_m16n8k8_tf32(s, a.hi, x.lo, y.lo);
+    tc::mma_m16n8k8_tf32(s, a.hi, x.hi, y.hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += s[i];
 }
 
 struct PassParams {
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const bool q4 = in_fours(q, j.q.st, dk), k4 = in_fours(k, j.k.st, dk);
     const bool v4 = in_fours(v, j.v.st, dv);
     const int first = part * p.plan.len;
-    const int end = min(p.T, first + p.plan.len);
+    const int end = first + min(p.T - first, p.plan.len);
     const long long step = j.reverse ? -1 : 1;
     for (int r0 = first; r0 < end; r0 += C) {
         const int rows = min(C, end - r0);

@@ -326,7 +326,7 @@ linattn_tc(const __grid_constant__ Maps maps,
     const int e = rev ? 0 : 1;
     const float a = p.log_decay[h];
     const int first = part * p.plan.len;
-    const int end = min(p.T, first + p.plan.len);
+    const int end = first + min(p.T - first, p.plan.len);
     const int nchunks = (end - first + kC - 1) / kC;
 
     if (warp == 0) {
