@@ -41,8 +41,10 @@ struct Shape {
     static constexpr int LD = DKP + 4;
     static constexpr int LP = C + 4;
     static constexpr int LV = kNV + 8;
-    static constexpr int FLOATS = 2 * C * LD + C * LV + C * LP + DKP * LV +
-                                  C + 4 + kNV;
+    static constexpr int STAGE = 2 * C * LD + C * LV;   // q, k and v
+    static constexpr int FLOATS =
+        2 * STAGE + C * LP + DKP * LV + C + 4 + kNV;
+    static_assert(FLOATS * 4 <= 232448, "shared memory");
 };
 
 // A number as one or two of tf32 (11 bits; the products look at no lower
@@ -99,39 +101,33 @@ struct PassParams {
 // Rows r0 .. r0 + C - 1 (in the pass's order) of x into dst [C][ld], zeros
 // beyond `rows` and `width`; columns c0 .. c0 + W - 1, the first `most` of
 // them.
-// Four adjacent elements at a time where they line up (`by4`), eight such on
-// their way at a time.
+// Four adjacent elements at a time where they line up (`by4`): fp32 straight to
+// shared memory (complete after wait_copies), bf16 eight such at a time.
 template <typename T, int C, int W>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
                                           long long st, long long first,
                                           long long step, int rows, int c0,
                                           int width, int most, bool by4) {
     if (by4) {
-        constexpr int N = C * W / 4 / kNT > 0 ? C * W / 4 / kNT : 1;
-        constexpr int K = N < 8 ? N : 8;
-        for (int i0 = threadIdx.x; i0 < C * W / 4; i0 += K * kNT) {
-            float4 v[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int i = i0 + k * kNT, r = i / (W / 4), c = i % (W / 4) * 4;
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < C * W / 4 && r < rows && c0 + c < width) {
-                    const T* from = x + (first + step * r) * st + c0 + c;
-                    if constexpr (sizeof(T) == 4) {
-                        v[k] = *reinterpret_cast<const float4*>(from);
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(from);
-                        const float2 y = from_bf16x2(u.x);
-                        const float2 z = from_bf16x2(u.y);
-                        v[k] = make_float4(y.x, y.y, z.x, z.y);
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int i = i0 + k * kNT, r = i / (W / 4), c = i % (W / 4) * 4;
-                if (i < C * W / 4 && c < most)
-                    *reinterpret_cast<float4*>(&dst[r * ld + c]) = v[k];
+#pragma unroll 8
+        for (int i = threadIdx.x; i < C * W / 4; i += kNT) {
+            const int r = i / (W / 4), c = i % (W / 4) * 4;
+            if (c >= most) continue;
+            const bool in = r < rows && c0 + c < width;
+            const T* from = in ? x + (first + step * r) * st + c0 + c : x;
+            float* to = &dst[r * ld + c];
+            if constexpr (sizeof(T) == 4) {
+                // 16 bytes, or none of them (zeros)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::
+                                 "r"(tc::smem_u32(to)),
+                             "l"(from), "r"(in ? 16 : 0)
+                             : "memory");
+            } else {
+                const uint2 u = in ? *reinterpret_cast<const uint2*>(from)
+                                   : make_uint2(0u, 0u);
+                const float2 y = from_bf16x2(u.x), z = from_bf16x2(u.y);
+                *reinterpret_cast<float4*>(to) =
+                    make_float4(y.x, y.y, z.x, z.y);
             }
         }
         return;
@@ -146,18 +142,9 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
         dst[r * ld + c] = v;
     }
 }
-
-// The same rows on their way into L2, a line a thread.
-template <typename T, int C>
-__device__ __forceinline__ void prefetch_rows(const T* x, long long st,
-                                              long long first, long long step,
-                                              int rows, int c0, int width) {
-    const int lines = (width * (int)sizeof(T) + 127) / 128;
-    for (int i = threadIdx.x; i < rows * lines; i += kNT) {
-        const T* at = x + (first + step * (i / lines)) * st + c0 +
-                      i % lines * (128 / (int)sizeof(T));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-    }
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" :::
+                     "memory");
 }
 
 // Whether rows of x can be read four elements at a time.
@@ -177,10 +164,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     constexpr int UT = DKP / 16, UG = 16 / UT, NU = kNV / 8 / UG;
     const LinAttnJob& j = p.part.j;
     extern __shared__ __align__(16) float smem[];
-    float* Qs = smem;
-    float* Ks = Qs + C * LD;
-    float* Vs = Ks + C * LD;
-    float* Ps = Vs + C * LV;
+    float* Ps = smem + 2 * Sh::STAGE;
     float* S = Ps + C * LP;
     float* w = S + DKP * LV;         // w^0 .. w^C
     int* bad = reinterpret_cast<int*>(w + C + 4);
@@ -223,27 +207,31 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const int first = part * p.plan.len;
     const int end = first + min(p.T - first, p.plan.len);
     const long long step = j.reverse ? -1 : 1;
-    for (int r0 = first; r0 < end; r0 += C) {
+    // chunks alternate between two stages: one is loaded while the other is
+    // worked on
+    auto load = [&](int r0) {
+        float* Qs = smem + ((r0 - first) / C & 1) * Sh::STAGE;
         const int rows = min(C, end - r0);
         const long long t0 = j.reverse ? p.T - 1 - r0 : r0;
         if (!STATE_ONLY)
             load_rows<T, C, DKP>(Qs, LD, q, j.q.st, t0, step, rows, 0, dk, dk8,
                                  q4);
-        load_rows<T, C, DKP>(Ks, LD, k, j.k.st, t0, step, rows, 0, dk, dk8,
-                             k4);
-        load_rows<T, C, kNV>(Vs, LV, v, j.v.st, t0, step, rows, n0, dv, kNV,
-                             v4);
-        if (r0 + C < end) {
-            const int more = min(C, end - r0 - C);
-            const long long t1 = t0 + step * C;
-            if (!STATE_ONLY)
-                prefetch_rows<T, C>(q, j.q.st, t1, step, more, 0, dk);
-            prefetch_rows<T, C>(k, j.k.st, t1, step, more, 0, dk);
-            prefetch_rows<T, C>(v, j.v.st, t1, step, more, n0,
-                                min(kNV, dv - n0));
-        }
+        load_rows<T, C, DKP>(Qs + C * LD, LD, k, j.k.st, t0, step, rows, 0, dk,
+                             dk8, k4);
+        load_rows<T, C, kNV>(Qs + 2 * C * LD, LV, v, j.v.st, t0, step, rows,
+                             n0, dv, kNV, v4);
+    };
+    load(first);
+    for (int r0 = first; r0 < end; r0 += C) {
+        float* Qs = smem + ((r0 - first) / C & 1) * Sh::STAGE;
+        float* Ks = Qs + C * LD;
+        float* Vs = Ks + C * LD;
+        const int rows = min(C, end - r0);
+        const long long t0 = j.reverse ? p.T - 1 - r0 : r0;
         if (tid < kNV) bad[tid] = C;
+        wait_copies();
         __syncthreads();
+        if (end - r0 > C) load(r0 + C);
         // What is not finite in v is taken out, as in P v it would meet the
         // zeros of earlier rows; its column's later outputs and state get NaN.
 #pragma unroll 4
