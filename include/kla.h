@@ -734,10 +734,10 @@ KLA_API kla_status kla_glr_step(const void* x, long long x_stride,
  * ones, then it may be null), 16-byte aligned: the states between the parts
  * of long sequences.  Its contents on entry do not matter.  Results are the
  * same bits on every run.
- * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, a null or
- * misaligned pointer, overlapping buffers, a workspace too small),
- * KLA_ERR_UNSUPPORTED_SHAPE (dk or dv outside the range, T > 2^31 - 4097,
- * B H > 2^24), KLA_ERR_CUDA.
+ * Errors: KLA_ERR_INVALID_ARG (negative sizes or strides, dk or dv < 1, a
+ * null or misaligned pointer, overlapping buffers, a workspace too small),
+ * KLA_ERR_UNSUPPORTED_SHAPE (dk or dv > 256, T > 2^31 - 4097, B H > 2^24),
+ * KLA_ERR_CUDA.
  */
 KLA_API kla_status kla_linattn_workspace_size(int B, int T, int H, int dk,
                                               int dv, kla_dtype dtype,

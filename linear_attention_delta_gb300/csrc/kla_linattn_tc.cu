@@ -10,9 +10,10 @@
 //   S <- w^n S + U                     fp32, in registers
 // For Q S and P~ V to share an accumulator, w^(r - 63) is taken out of a row
 // and multiplied in as it is written: P~ has the factor w^(63 - s) of its
-// column, and S that of w^(63 + e).  Decays whose powers would leave the range
-// (64 |log_decay| > 60) have their rows of Q S scaled in TMEM instead, and
-// every score its own factor.
+// column, and S that of w^(63 + e).  These factors stay within e^48, which
+// leaves bf16 its digits for scores up to 4e17 and states down to 1e-17;
+// stronger decays (64 |log_decay| > 48: a memory of a token or two) have their
+// rows of Q S scaled in TMEM instead, and every score its own factor.
 // U does not depend on S, so the only chain from chunk to chunk is one
 // multiply-add of the state, and everything else runs ahead of it.
 //
@@ -351,7 +352,7 @@ linattn_tc(const __grid_constant__ Maps maps,
         *issued = 0;
     }
     if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
-    const bool gentle = fabsf(a) * 64.f <= 60.f;
+    const bool gentle = fabsf(a) * 64.f <= 48.f;
     for (int i = tid; i < 2 * 4 * 64; i += kThreads) bad[i] = 255;
     if (tid < 8) flag[tid] = 0;
     if (tid < 4) done[tid] = 0;

@@ -175,6 +175,24 @@ def test_extreme_decays(T, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("a", [-0.65, -0.74, -0.76, -0.92, -1.5])
+@pytest.mark.parametrize("scale,name", [(1e-14, "v"), (1e8, "qk")])
+def test_range_of_the_decays_factors(scale, name, a, dtype):
+    """Small values and states, large scores: a chunk's decays reach e^190,
+    and no factor of theirs may take a 16-bit number out of its digits (the
+    bounds are relative to the values)."""
+    for d in (64, 128):
+        x, y = make(1, 260, 2, d, d, dtype)
+        x["log_decay"] = torch.full((2,), a).cuda()
+        if name == "v":
+            x["v"], x["h0"] = x["v"] * scale, x["h0"] * scale
+        else:
+            x["q"], x["k"] = x["q"] * scale, x["k"] * scale
+        check_fwd(x, *kla.linattn_fwd(**x))
+        check_bwd(x, y, kla.linattn_bwd(**x, **y))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T", [100, 4200])
 def test_state_replaced_in_place(T, dtype):
     x, _ = make(1, T, 2, 128, 128, dtype)
@@ -356,6 +374,26 @@ def test_same_bits_and_graph_replay():
     torch.cuda.synchronize()
     for out in outs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_streams_at_once(dtype):
+    """Calls in flight beside one another, each with parts of its own."""
+    xs = [make(1, 2500, 2, 64, 64, dtype, seed=i) for i in range(2)]
+    alone = [(kla.linattn_fwd(**x), kla.linattn_bwd(**x, **y)) for x, y in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (x, y) in enumerate(xs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append((kla.linattn_fwd(**x),
+                               kla.linattn_bwd(**x, **y)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for fwd, bwd in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(fwd, alone[i][0]))
+            assert all(torch.equal(bwd[n], alone[i][1][n]) for n in bwd)
 
 
 @pytest.mark.parametrize("d,dtype", [(64, BF16), (20, F32)])
