@@ -598,8 +598,10 @@ cudaError_t launch_step(const LinAttnStepArgs& a, cudaStream_t stream) {
                      (reinterpret_cast<uintptr_t>(a.S) & 15) == 0;
     const int v = vec ? 4 : 1;
     // a row of a tile is at least a 128-byte line (32 fp32), at most 128
-    // columns; narrower tiles where the heads alone do not fill the SMs
-    int cg = vec ? (heads >= 304 ? 5 : 3) : 5;
+    // columns; the narrower where there are fewer heads than SMs (measured,
+    // dk = dv = 128, us with tiles of 32 and of 128 columns: 16 heads 2.4 and
+    // 3.3, 64 heads 4.1 and 5.4, 256 heads 9.3 and 8.4, 4096 heads 102 and 81)
+    int cg = vec ? (heads >= 128 ? 5 : 3) : 5;
     while (cg > 3 && (v << (cg - 1)) >= a.dv) --cg;
     const int tiles = (a.dv + (v << cg) - 1) / (v << cg);
     const dim3 grid((unsigned)(heads * tiles));

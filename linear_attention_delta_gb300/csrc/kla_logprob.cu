@@ -17,7 +17,7 @@
 // row is searched round by round instead.
 #include <cooperative_groups.h>
 
-#include <atomic>
+#include <algorithm>
 
 #include "f32x2.cuh"
 #include "kla_internal.cuh"
@@ -540,16 +540,6 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
 // ---------------------------------------------------------------- launch
 
 constexpr int kSMs = 152;
-constexpr int kShort = 4096;     // logits up to which 128 threads have a row
-
-// Blocks of a row: up to four for every SM, of at least 4096 logits.
-int parts_of(int N, int V, int most) {
-    int parts = 1;
-    while (parts < most && (long long)N * parts * 2 <= 4 * kSMs &&
-           V / (parts * 2) >= 4096)
-        parts *= 2;
-    return parts;
-}
 
 template <typename... P, typename... A>
 cudaError_t launch_rows(void (*kernel)(P...), long long rows, int parts,
@@ -576,20 +566,31 @@ cudaError_t launch_fwd_of(const LogprobArgs& a, int parts, cudaStream_t s) {
                  : launch_rows(logprob_fwd<T, NT, false>, a.N, parts, NT,
                                true, s, a);
 }
+// Blocks of a row: up to four for every SM, of at least 16384 logits
+// (measured, us with a row in one block and over a cluster: 1 x 32000 7.4 and
+// 8.4, 64 x 32000 with 20 alternatives 11.3 and 12.8, 8 x 131072 about 8 and
+// 4.4).  128 threads for short rows (4096 x 1000: 20 and 30 with 256) and for
+// more rows than fit the SMs twice at that size: blocks then start and end
+// more evenly (8192 x 32000: 81 and 85; 1023 x 50257: 28 and 24).
 template <typename T>
 cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
-    const int parts = parts_of(a.N, a.V, kMaxParts);
-    return a.V / parts <= kShort ? launch_fwd_of<T, 128>(a, parts, s)
-                                 : launch_fwd_of<T, 256>(a, parts, s);
+    int parts = 1;
+    while (parts < kMaxParts && (long long)a.N * parts * 2 <= 4 * kSMs &&
+           a.V / (parts * 2) >= 16384)
+        parts *= 2;
+    return a.V / parts <= 4096 || a.N >= 24 * kSMs
+               ? launch_fwd_of<T, 128>(a, parts, s)
+               : launch_fwd_of<T, 256>(a, parts, s);
 }
 
+// Many small blocks: up to 32 an SM, of at least 4096 logits (measured, us:
+// 8192 x 32000 in 1, 2 and 8 blocks a row 164, 174, 195; 256 x 131072 in 8, 16
+// and 32 27.8, 25.7, 27.2; 512 x 32000 in 4 and 7 17.2, 14.9).
 template <typename T>
 cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
-    const int parts = parts_of(a.N, a.V, 64);
-    return a.V / parts <= kShort
-               ? launch_rows(logprob_bwd<T, 128>, a.N, parts, 128, false, s, a)
-               : launch_rows(logprob_bwd<T, 512>, a.N, parts, 512, false, s,
-                             a);
+    const int parts =
+        std::max(1, std::min({32 * kSMs / a.N, a.V / 4096, 64}));
+    return launch_rows(logprob_bwd<T, 128>, a.N, parts, 128, false, s, a);
 }
 
 }  // namespace
