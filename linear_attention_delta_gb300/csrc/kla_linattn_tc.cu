@@ -41,6 +41,7 @@
 // then sets the fault word, lets its copies and products finish, frees TMEM
 // and returns.
 #include <atomic>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "kla_linattn.cuh"
@@ -69,7 +70,7 @@ constexpr int kLdS = kNV + 1;    // row of the state's tile in shared memory
 
 // Shared memory (bytes from a 1024-aligned base): the rings of Q, K and V
 // tiles (boxes of 64 columns; no Q in the pass that forms part states), the
-// three parts of the weighted V, the bf16 copy of S, the weights.
+// three parts of the weighted V, the bf16 copy of S.
 template <int DK, bool STATE_ONLY>
 struct Smem {
     static constexpr int HALVES = DK / 64;
@@ -81,8 +82,7 @@ struct Smem {
     static constexpr int V = K + NS * TILE;
     static constexpr int VW = V + NS * kBox;     // NVW x 3 boxes
     static constexpr int S = VW + NVW * 3 * kBox;   // DK rows of 128 bytes
-    static constexpr int W = S + DK * 128;       // w^0 .. w^128
-    static constexpr int BAD = W + 4 * 132;      // [2][4 warps][64]: see below
+    static constexpr int BAD = S + DK * 128;     // [2][4 warps][64]: see below
     static constexpr int FLAG = BAD + 2 * 4 * 64;   // [2][4 warps]
     static constexpr int DONE = FLAG + 2 * 4 * 4;   // [4 warps]
     static constexpr int BARS = DONE + 4 * 4;
@@ -90,7 +90,7 @@ struct Smem {
     static constexpr int MISC = BARS + 8 * NUM_BARS;   // abort, TMEM, issued
     static constexpr int BYTES = MISC + 16 + 1024;     // alignment
     static_assert(BYTES <= 232448, "shared memory");
-    static_assert(BARS % 8 == 0 && W % 16 == 0, "alignment");
+    static_assert(BARS % 8 == 0, "alignment");
 };
 
 // mbarriers, a phase a chunk (of a ring: a phase a turn).  A wait tells a
@@ -299,7 +299,6 @@ linattn_tc(const __grid_constant__ Maps maps,
     uint8_t* sm = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = tc::smem_u32(sm);
-    float* w = reinterpret_cast<float*>(sm + Sm::W);
     // for each of two chunks, output warp and column: the first row (counted
     // as r) whose V is not finite, 255: none
     uint8_t* bad = sm + Sm::BAD;
@@ -351,7 +350,6 @@ linattn_tc(const __grid_constant__ Maps maps,
         *abort = 0;
         *issued = 0;
     }
-    if (tid >= 64 && tid < 64 + kC + 1) w[tid - 64] = power(a, tid - 64);
     const bool gentle = fabsf(a) * 64.f <= 48.f;
     for (int i = tid; i < 2 * 4 * 64; i += kThreads) bad[i] = 255;
     if (tid < 8) flag[tid] = 0;
@@ -684,7 +682,9 @@ linattn_tc(const __grid_constant__ Maps maps,
         const int q = warp & 3, i = 32 * q + lane;
         const int j0 = (warp - 16) >> 2 << 1;   // its two blocks of 32 columns
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-        const float a2 = a * 1.4426950408889634f;
+        // (a decay of 0 stays out of 0 * inf)
+        const float a2 = (a < -1e4f ? -1e4f : a) * 1.4426950408889634f;
+        const float2 row = both(power(a, (rev ? kC - 1 - i : i) + e));
         // the factor w^(63 - s) of column at + m: that of column `at` times
         // w^-m (in reverse w^m); in registers, as the weights of V
         float2 cw[8];
@@ -692,81 +692,90 @@ linattn_tc(const __grid_constant__ Maps maps,
         for (int m = 0; m < 8; ++m)
             cw[m] = make_float2(power(a, rev ? 2 * m : -2 * m),
                                 power(a, rev ? 2 * m + 1 : -2 * m - 1));
+        // (a loop for each kind, as short as it can be)
+        auto walk = [&](auto kind, auto order) {
+            constexpr bool GENTLE = decltype(kind)::value;
+            constexpr bool REV = decltype(order)::value;
 #pragma unroll 1
-        for (int c = 0; c < nchunks && !gave_up(); ++c) {
-            if (!gentle) {       // rows of Q S, this warp's half of the columns
-                const float2 f = both(w[(rev ? kC - 1 - i : i) + e]);
-                const uint32_t acc = lanes + kColO + kNV * (c & 1) + 16 * j0;
-                wait_warp(B::S_FREE, c);
+            for (int c = 0; c < nchunks && !gave_up(); ++c) {
+                wait_warp(B::SC_FULL, c);
+                if (c > 0) wait_warp(B::O_FULL + ((c - 1) & 1), (c - 1) >> 1);
                 tc::tc_fence_after();
 #pragma unroll 1
-                for (int m = 0; m < kNV / 2; m += 8) {
-                    float x[8];
-                    uint32_t u[8];
-                    tc::tmem_ld8(acc + m, x);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const float2 y = mul2(f, make_float2(x[k], x[k + 1]));
-                        u[k] = __float_as_uint(y.x);
-                        u[k + 1] = __float_as_uint(y.y);
+                for (int at = 32 * j0; at < 32 * j0 + 64; at += 16) {
+                    const int j = at >> 5;
+                    uint32_t pk[8];
+                    float x[16];
+                    const bool none = REV ? j < q : j > q;
+                    if (!none) {
+                        tc::tmem_ld16(lanes + kColSC + at, x);
+                        tc::tmem_ld_wait();
                     }
-                    tmem_st8(acc + m, u);
-                }
-            }
-            wait_warp(B::SC_FULL, c);
-            if (c > 0) wait_warp(B::O_FULL + ((c - 1) & 1), (c - 1) >> 1);
-            tc::tc_fence_after();
-#pragma unroll 1
-            for (int at = 32 * j0; at < 32 * j0 + 64; at += 16) {
-                const int j = at >> 5;
-                uint32_t pk[8];
-                float x[16];
-                const bool none = rev ? j < q : j > q;
-                if (!none) {
-                    tc::tmem_ld16(lanes + kColSC + at, x);
-                    tc::tmem_ld_wait();
-                }
-                if (at == 32 * j0 + 48) {
-                    tc::tc_fence_before();
-                    arrive(B::SC_FREE);
-                }
-                if (none) {
+                    if (at == 32 * j0 + 48) {
+                        tc::tc_fence_before();
+                        arrive(B::SC_FREE);
+                    }
+                    if (none) {
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) pk[m] = 0;
-                } else {
-                    if (gentle) {
-                        const float2 f = both(tc::ex2(
-                            a2 * (float)(rev ? at - (kC - 64) : 63 - at)));
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            const float2 y =
-                                mul2(make_float2(x[2 * m], x[2 * m + 1]),
-                                     mul2(f, cw[m]));
-                            x[2 * m] = y.x, x[2 * m + 1] = y.y;
-                        }
+                        for (int m = 0; m < 8; ++m) pk[m] = 0;
                     } else {
-                        const int d = rev ? at - i : i - at;
+                        if (GENTLE) {
+                            const float2 f = both(tc::ex2(
+                                a2 * (float)(REV ? at - (kC - 64) : 63 - at)));
 #pragma unroll
-                        for (int m = 0; m < 16; ++m)
-                            x[m] *= w[max(0, rev ? d + m : d - m)];
+                            for (int m = 0; m < 8; ++m) {
+                                const float2 y =
+                                    mul2(make_float2(x[2 * m], x[2 * m + 1]),
+                                         mul2(f, cw[m]));
+                                x[2 * m] = y.x, x[2 * m + 1] = y.y;
+                            }
+                        } else {
+                            const int d = REV ? at - i : i - at;
+#pragma unroll
+                            for (int m = 0; m < 16; ++m)
+                                x[m] *= tc::ex2(a2 * (float)max(0, REV ? d + m
+                                                                      : d - m));
+                        }
+                        if (j == q) {    // masked, not multiplied by 0
+                            const int d = lane - (at & 16);
+#pragma unroll
+                            for (int m = 0; m < 16; ++m)
+                                if (REV ? m < d : m > d) x[m] = 0.f;
+                        }
+#pragma unroll
+                        for (int m = 0; m < 8; ++m)
+                            pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
                     }
-                    if (j == q) {    // masked, not multiplied by 0
-                        const int d = lane - (at & 16);
-#pragma unroll
-                        for (int m = 0; m < 16; ++m)
-                            if (rev ? m < d : m > d) x[m] = 0.f;
-                    }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m)
-                        pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
+                    tmem_st8(lanes + kColP + at / 2, pk);
                 }
-                tmem_st8(lanes + kColP + at / 2, pk);
+                if (!GENTLE) {       // rows of Q S, this warp's half of the columns
+                    const uint32_t acc = lanes + kColO + kNV * (c & 1) + 16 * j0;
+                    wait_warp(B::S_FREE, c);
+                    tc::tc_fence_after();
+#pragma unroll 1
+                    for (int m = 0; m < kNV / 2; m += 8) {
+                        float x[8];
+                        uint32_t u[8];
+                        tc::tmem_ld8(acc + m, x);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 y = mul2(row, make_float2(x[k], x[k + 1]));
+                            u[k] = __float_as_uint(y.x);
+                            u[k + 1] = __float_as_uint(y.y);
+                        }
+                        tmem_st8(acc + m, u);
+                    }
+                }
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                arrive(B::P_READY);
             }
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            arrive(B::P_READY);
-        }
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (gentle) rev ? walk(yes, yes) : walk(yes, no);
+        else rev ? walk(no, yes) : walk(no, no);
     } else if (warp < 28 && !STATE_ONLY) {
         // ------------------------------------------------ outputs (row i)
         const int q = warp - 24, i = 32 * q + lane, r = rev ? kC - 1 - i : i;
