@@ -13,7 +13,8 @@
 // column, and S that of w^(63 + e).  These factors stay within e^48, which
 // leaves bf16 its digits for scores up to 4e17 and states down to 1e-17;
 // stronger decays (64 |log_decay| > 48: a memory of a token or two) have their
-// rows of Q S scaled in TMEM instead, and every score its own factor.
+// rows of Q S scaled in TMEM instead, and every score its own factor (88 us
+// where the others take 71, if all 16 heads of B4 T4096 d128 are such).
 // U does not depend on S, so the only chain from chunk to chunk is one
 // multiply-add of the state, and everything else runs ahead of it.
 //
@@ -26,9 +27,19 @@
 // Warps: 0-7 hold the state (thread = row of S and half of its columns), 8-15
 // weight V, 16-23 turn scores into P~ (thread = row and half of the columns),
 // 24-27 write the outputs (thread = row), 28 issues the products, 29 the
-// copies (TMA).  They hand over through mbarriers.  Many warps with few
-// registers, because what bounds a chunk is the latency of their instructions
-// (with 18 warps half of the issue slots stay empty).
+// copies (TMA).  They hand over through mbarriers.
+//
+// What bounds it, at B4 T4096 H16 d128 (71 us; HBM would take 40, and the
+// tensor cores are busy 29 % of the time): a chunk takes a block 2.1 us, about
+// 4000 cycles, in which 368 KB pass through shared memory (2900 cycles) and
+// some 11000 warp instructions are issued (61 % of the slots, 79 % on the
+// busiest SMs); the hand-overs and products without the element-wise work took
+// 59 us, the hand-overs alone 44.  Hence many warps with few registers (18
+// larger ones: 87 us), short loops, and weights in registers.  Measured and
+// left out: a second issuing thread 81 us, scores twice buffered with separate
+// products for the parts of V 78, or with one accumulator of outputs and P~ in
+// the scores' place 74, waits for the next product before the last two of this
+// one 74.
 //
 // In reverse the tiles lie in memory order all the same; r counts from the
 // tile's last row, masks and weights are mirrored.
@@ -692,7 +703,9 @@ linattn_tc(const __grid_constant__ Maps maps,
         for (int m = 0; m < 8; ++m)
             cw[m] = make_float2(power(a, rev ? 2 * m : -2 * m),
                                 power(a, rev ? 2 * m + 1 : -2 * m - 1));
-        // (a loop for each kind, as short as it can be)
+        // (a loop for each kind and order, as short as it can be: one loop
+        // with the cases inside took 252 us where this takes 222, at B8 T8192
+        // H32 d64)
         auto walk = [&](auto kind, auto order) {
             constexpr bool GENTLE = decltype(kind)::value;
             constexpr bool REV = decltype(order)::value;
@@ -969,7 +982,9 @@ bool linattn_tc_eligible(const LinAttnArgs& a) {
 // Parts of a sequence.  A block has an SM to itself, so a launch takes as many
 // turns as its blocks fill the SMs; measured, a chunk takes a block 2.2 us, or
 // 1.1 us where only the state is formed, and a block takes 4 us besides.  More
-// parts fill the last turn better and cost a pass over k and v more.
+// parts fill the last turn better and cost a pass over k and v more (d128, in
+// one part and by this rule: B1 T65536 H16 983 and 400 us, B1 T8192 H16 131 and
+// 76; B2 T2049 H12 d64 41 and 32; B4 T4096 H16 stays in one).
 la::Plan linattn_tc_plan(const LinAttnArgs& a) {
     constexpr int kSMs = 152, kMost = 32;
     long long blocks = 0;
