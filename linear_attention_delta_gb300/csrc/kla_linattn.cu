@@ -16,10 +16,12 @@
 // 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
 // operands from shared memory as they are; three times the tiles of fp32 would
 // not fit there.)  Chunks of 64 tokens by 64 columns of the state a block, 16
-// warps, two stages: 808 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 12.6
-// us a chunk.  It is bound by the instructions around the products: fragments
-// from shared memory taken apart, issue in 54 % of the slots, the tensor pipe
-// busy 36 %.  One stage: 878 us.
+// warps, two stages: 752 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 11.7
+// us a chunk.  Of it the products take about 410 (with one of the three
+// products: 476), taking the fragments apart most of the rest (without any
+// products and fragments: 221); Q S and the scores 290, U 167, P V 62, the
+// copies 62 (by leaving each out).  One stage: 878 us; a loop of its own for
+// the scores, fragments by single loads: 808.
 #include "f32x2.cuh"
 #include "kla_linattn.cuh"
 #include "tc_primitives.cuh"
@@ -80,19 +82,61 @@ struct FragA {
         }
     }
 };
-// d += a b (16 x 8 x 8) to the precision above.  The sum over k is d's own, in
-// fp32: the product instruction cuts off what it adds up, which over a row of
-// 72 ended 4 times as far from the exact sum.
-template <bool XA, bool XB>
-__device__ __forceinline__ void mma(float (&d)[4], const FragA<XA>& a,
-                                    float b0, float b1) {
-    const Split<XB> x(b0), y(b1);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (!XA) tc::mma_m16n8k8_tf32(s, a.lo, x.hi, y.hi);
-    if (!XB) tc::mma_m16n8k8_tf32(s, a.hi, x.lo, y.lo);
-    tc::mma_m16n8k8_tf32(s, a.hi, x.hi, y.hi);
+// d[n] += a b[n] (16 x 8 x 8, N tiles) to the precision above.  The sum over k
+// is d's own, in fp32: the product instruction cuts off what it adds up, which
+// over a row of 72 ended 4 times as far from the exact sum.  The tiles'
+// products alternate: those of one tile wait for one another.
+template <bool XA, bool XB, int N>
+__device__ __forceinline__ void mma(float (&d)[N][4], const FragA<XA>& a,
+                                    const float (&b)[N][2]) {
+    float s[N][4] = {};
+    uint32_t hi[N][2], lo[N][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] += s[i];
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Split<XB> x(b[n][i]);
+            hi[n][i] = x.hi, lo[n][i] = x.lo;
+        }
+    if (!XA)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            tc::mma_m16n8k8_tf32(s[n], a.lo, hi[n][0], hi[n][1]);
+    if (!XB)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            tc::mma_m16n8k8_tf32(s[n], a.hi, lo[n][0], lo[n][1]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        tc::mma_m16n8k8_tf32(s[n], a.hi, hi[n][0], hi[n][1]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const float2 x = add2(make_float2(d[n][i], d[n][i + 1]),
+                                  make_float2(s[n][i], s[n][i + 1]));
+            d[n][i] = x.x, d[n][i + 1] = x.y;
+        }
+}
+// 8 x 4 blocks of fp32 (rows of 16 bytes at the addresses of 8 lanes each);
+// lane 4 g + t gets element (g, t) of each: fragments of the products, where
+// rows lie along the sum's axis (written before the last block barrier).
+__device__ __forceinline__ void load_blocks(float& a, float& b, float& c,
+                                            float& d, const float* row) {
+    asm volatile(
+        "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+        : "r"(tc::smem_u32(row)));
+}
+__device__ __forceinline__ void load_blocks(float (&x)[2][2],
+                                            const float* row) {
+    load_blocks(x[0][0], x[0][1], x[1][0], x[1][1], row);
+}
+__device__ __forceinline__ void load_blocks(float (&x)[1][2],
+                                            const float* row) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
+                 : "=f"(x[0][0]), "=f"(x[0][1])
+                 : "r"(tc::smem_u32(row)));
 }
 
 struct PassParams {
@@ -178,6 +222,9 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const size_t bh = blockIdx.x / p.part.slices;
     const int b = bh / p.H, h = bh % p.H, part = blockIdx.y;
     const int dk = j.dk, dv = j.dv, e = j.reverse ? 0 : 1;
+    // (with parts the join came before, which itself waited: what is not of the
+    // workspace is there)
+    if (STATE_ONLY || p.plan.parts == 1) await_grid_before();
     const float a = p.log_decay[h];
     const T* q = static_cast<const T*>(j.q.p) + b * j.q.sb + h * j.q.sh;
     const T* k = static_cast<const T*>(j.k.p) + b * j.k.sb + h * j.k.sh;
@@ -187,25 +234,6 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const int dk8 = (dk + 7) / 8 * 8;     // columns of q and k that are looked at
 
     if (tid <= C) w[tid] = power(a, tid);
-    const float* before =
-        STATE_ONLY ? nullptr : la::state_before(p.part, p.plan, part, bh);
-#pragma unroll 4
-    for (int i = tid; i < DKP * kNV; i += kNT) {
-        const int r = i / kNV, c = n0 + i % kNV;
-        float s = 0.f;
-        if (r < dk && c < dv) {
-            const size_t at = (size_t)r * j.s_r + (size_t)c * j.s_c;
-            if (STATE_ONLY) {
-                if (part == 0 && j.S0)
-                    p.part.ws[bh * p.plan.parts * sn + at] =
-                        j.S0[bh * sn + at];
-            } else if (before) {
-                s = before[at];
-            }
-        }
-        S[r * LV + i % kNV] = s;
-    }
-
     const bool q4 = in_fours(q, j.q.st, dk), k4 = in_fours(k, j.k.st, dk);
     const bool v4 = in_fours(v, j.v.st, dv);
     const int first = part * p.plan.len;
@@ -226,6 +254,25 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                              n0, dv, kNV, v4);
     };
     load(first);
+    await_grid_before();
+    const float* before =
+        STATE_ONLY ? nullptr : la::state_before(p.part, p.plan, part, bh);
+#pragma unroll 4
+    for (int i = tid; i < DKP * kNV; i += kNT) {
+        const int r = i / kNV, c = n0 + i % kNV;
+        float s = 0.f;
+        if (r < dk && c < dv) {
+            const size_t at = (size_t)r * j.s_r + (size_t)c * j.s_c;
+            if (STATE_ONLY) {
+                if (part == 0 && j.S0)
+                    p.part.ws[bh * p.plan.parts * sn + at] =
+                        j.S0[bh * sn + at];
+            } else if (before) {
+                s = before[at];
+            }
+        }
+        S[r * LV + i % kNV] = s;
+    }
     for (int r0 = first; r0 < end; r0 += C) {
         float* Qs = smem + ((r0 - first) / C & 1) * Sh::STAGE;
         float* Ks = Qs + C * LD;
@@ -248,72 +295,71 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         }
         const int m = warp % MT, ng = warp / MT;
         float acc[NO][4];
+        // this lane's row of the blocks of an A fragment (16 x 8)
+        const int arow = 16 * m + (lane & 15), acol = (lane >> 4) * 4;
         if (!STATE_ONLY) {
-            // scores, 16 rows x NO 8-column tiles a warp
-            if (ng * NO * 8 < C) {
+            // scores and Q S together, 16 rows x NO 8-column tiles a warp
+            float sc[NO][4];
+#pragma unroll
+            for (int n = 0; n < NO; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] = sc[n][i] = 0.f;
+            const int s0 = ng * NO * 8;
+            // columns all above the diagonal stay 0
+            const bool below = s0 < C && s0 <= 16 * m + 15;
+            const float* x = &Qs[arow * LD + acol];
+            // (NO tiles; the lanes beyond 8 NO rows repeat addresses in use)
+            const float* y =
+                &Ks[((below ? s0 : 0) + (lane & 7) + (NO > 1 ? lane >> 4 << 3 : 0)) *
+                        LD + (lane >> 3 & 1) * 4];
+            const float* z = &S[t * LV + s0 + g];
+#pragma unroll 4
+            for (int d = 0; d < dk8; d += 8) {
+                float v[4];
+                load_blocks(v[0], v[1], v[2], v[3], x + d);
+                const FragA<X> f(v[0], v[1], v[2], v[3]);
+                if (below) {
+                    float u[NO][2];
+                    load_blocks(u, y + d);
+                    mma<X, X>(sc, f, u);
+                }
+                float u[NO][2];
 #pragma unroll
                 for (int n = 0; n < NO; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-                const float* x = &Qs[(16 * m + g) * LD + t];
-                const float* y = &Ks[(ng * NO * 8 + g) * LD + t];
-                // columns all above the diagonal stay 0
-                const int last = 16 * m + 15 < ng * NO * 8 ? 0 : dk8;
-#pragma unroll 2
-                for (int d = 0; d < last; d += 8) {
-                    const FragA<X> f(x[d], x[8 * LD + d], x[d + 4],
-                                     x[8 * LD + d + 4]);
-#pragma unroll
-                    for (int n = 0; n < NO; ++n)
-                        mma<X, X>(acc[n], f, y[8 * n * LD + d],
-                                  y[8 * n * LD + d + 4]);
-                }
+                    u[n][0] = z[d * LV + 8 * n], u[n][1] = z[(d + 4) * LV + 8 * n];
+                mma<X, false>(acc, f, u);
+            }
+            if (s0 < C) {
 #pragma unroll
                 for (int n = 0; n < NO; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 16 * m + g + (i >> 1) * 8;
-                        const int c = (ng * NO + n) * 8 + 2 * t + (i & 1);
-                        Ps[r * LP + c] =
-                            c <= r ? acc[n][i] * w[r - c] : 0.f;
+                        const int c = s0 + 8 * n + 2 * t + (i & 1);
+                        Ps[r * LP + c] = c <= r ? sc[n][i] * w[r - c] : 0.f;
                     }
             }
+            // rows of Q S times w^(r + e)
+            const float u0 = w[16 * m + g + e], u1 = w[16 * m + g + 8 + e];
 #pragma unroll
             for (int n = 0; n < NO; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-            // Q S, its rows times w^(r + e)
-            {
-                const float* x = &Qs[(16 * m + g) * LD + t];
-                const float* y = &S[t * LV + ng * NO * 8 + g];
-#pragma unroll 2
-                for (int d = 0; d < dk8; d += 8) {
-                    const FragA<X> f(x[d], x[8 * LD + d], x[d + 4],
-                                     x[8 * LD + d + 4]);
-#pragma unroll
-                    for (int n = 0; n < NO; ++n)
-                        mma<X, false>(acc[n], f, y[d * LV + 8 * n],
-                                      y[(d + 4) * LV + 8 * n]);
-                }
-                const float u0 = w[16 * m + g + e], u1 = w[16 * m + g + 8 + e];
-#pragma unroll
-                for (int n = 0; n < NO; ++n)
-                    acc[n][0] *= u0, acc[n][1] *= u0, acc[n][2] *= u1,
-                        acc[n][3] *= u1;
-            }
+                acc[n][0] *= u0, acc[n][1] *= u0, acc[n][2] *= u1,
+                    acc[n][3] *= u1;
         }
         __syncthreads();             // P in place; S read
         if (!STATE_ONLY) {
-            const float* x = &Ps[(16 * m + g) * LP + t];
+            const float* x = &Ps[arow * LP + acol];
             const float* y = &Vs[t * LV + ng * NO * 8 + g];
 #pragma unroll 2
             for (int c = 0; c < 16 * m + 16; c += 8) {
-                const FragA<false> f(x[c], x[8 * LP + c], x[c + 4],
-                                     x[8 * LP + c + 4]);
+                float v[4];
+                load_blocks(v[0], v[1], v[2], v[3], x + c);
+                const FragA<false> f(v[0], v[1], v[2], v[3]);
+                float u[NO][2];
 #pragma unroll
                 for (int n = 0; n < NO; ++n)
-                    mma<false, X>(acc[n], f, y[c * LV + 8 * n],
-                                  y[(c + 4) * LV + 8 * n]);
+                    u[n][0] = y[c * LV + 8 * n], u[n][1] = y[(c + 4) * LV + 8 * n];
+                mma<false, X>(acc, f, u);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -341,17 +387,19 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 for (int i = 0; i < 4; ++i) u[n][i] = 0.f;
             const float* x = &Ks[t * LD + 16 * um + g];
             const float* y = &Vs[t * LV + ug * NU * 8 + g];
-#pragma unroll 2
+#pragma unroll 1
             for (int c = 0; c < rows; c += 8) {
-                const FragA<X> f(x[c * LD], x[c * LD + 8], x[(c + 4) * LD],
-                                 x[(c + 4) * LD + 8]);
                 // rows beyond the sequence are zero: their weight is any
                 const float w0 = w[max(0, rows - e - c - t)];
                 const float w1 = w[max(0, rows - e - c - t - 4)];
+                const FragA<false> f(w0 * x[c * LD], w0 * x[c * LD + 8],
+                                     w1 * x[(c + 4) * LD],
+                                     w1 * x[(c + 4) * LD + 8]);
+                float v[NU][2];
 #pragma unroll
                 for (int n = 0; n < NU; ++n)
-                    mma<X, false>(u[n], f, w0 * y[c * LV + 8 * n],
-                                  w1 * y[(c + 4) * LV + 8 * n]);
+                    v[n][0] = y[c * LV + 8 * n], v[n][1] = y[(c + 4) * LV + 8 * n];
+                mma<false, X>(u, f, v);
             }
             // w^n S as S + (w^n - 1) S: n * log_decay close to 0 keeps its
             // digits
@@ -386,6 +434,10 @@ linattn_join(float* ws, const float* log_decay, int parts, int len, int H,
              int n, int blocks, bool first) {
     const size_t bh = blockIdx.x / blocks;
     const int at = blockIdx.x % blocks * 256 + threadIdx.x;
+    // the passes read what came before the first of them at once: not before
+    // it is all there
+    await_grid_before();
+    release_grid_after();
     if (at >= n) return;
     const float f = power(log_decay[bh % H], len);
     float* x = ws + bh * parts * n + at;
@@ -432,14 +484,12 @@ template <typename T, int DKP, bool STATE_ONLY>
 cudaError_t launch_pass(const PassParams& p, long long bh,
                         cudaStream_t stream) {
     constexpr int bytes = Shape<DKP>::FLOATS * 4;
-    auto kern = linattn_pass<T, DKP, STATE_ONLY>;
-    cudaError_t e = cudaFuncSetAttribute(
-        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = la::allow_smem<linattn_pass<T, DKP, STATE_ONLY>>(bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(bh * p.part.slices),
                     p.plan.parts - (STATE_ONLY ? 1 : 0));
-    kern<<<grid, kNT, bytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(linattn_pass<T, DKP, STATE_ONLY>, grid, kNT, stream,
+                            bytes, p);
 }
 
 template <typename T, int DKP>
@@ -489,9 +539,9 @@ cudaError_t la::join_parts(const Part& p, const Plan& pl,
                            const float* log_decay, long long bh, int H,
                            cudaStream_t stream) {
     const int n = p.j.dk * p.j.dv, blocks = (n + 255) / 256;
-    linattn_join<<<(unsigned)(bh * blocks), 256, 0, stream>>>(
-        p.ws, log_decay, pl.parts, pl.len, H, n, blocks, p.j.S0 != nullptr);
-    return cudaGetLastError();
+    return launch_dependent(linattn_join, dim3((unsigned)(bh * blocks)), 256,
+                            stream, 0, p.ws, log_decay, pl.parts, pl.len, H, n,
+                            blocks, p.j.S0 != nullptr);
 }
 
 // By the sizes alone, whichever form the tensors' alignment allows.

@@ -1,6 +1,8 @@
 // What the two forms of the chunked pass of linear attention share.
 #pragma once
 
+#include <atomic>
+
 #include "kla_internal.cuh"
 
 namespace kla {
@@ -38,6 +40,21 @@ __device__ __forceinline__ const float* state_before(const Part& p,
     const size_t n = (size_t)p.j.dk * p.j.dv;
     if (pl.parts == 1) return p.j.S0 ? p.j.S0 + bh * n : nullptr;
     return part || p.j.S0 ? p.ws + (bh * pl.parts + part) * n : nullptr;
+}
+
+// The opt-in to more shared memory, once a kernel and device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (bit && (done.load() & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(
+        KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 inline int slices_of(const LinAttnJob& j) { return (j.dv + kNV - 1) / kNV; }

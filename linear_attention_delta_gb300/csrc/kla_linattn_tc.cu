@@ -51,7 +51,6 @@
 // Every wait is bounded (2 s) and gives up when another warp has: the block
 // then sets the fault word, lets its copies and products finish, frees TMEM
 // and returns.
-#include <atomic>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -335,6 +334,9 @@ linattn_tc(const __grid_constant__ Maps maps,
     const int b = bh / p.H, h = bh % p.H;
     const bool rev = pt.j.reverse;
     const int e = rev ? 0 : 1;
+    // (with parts the join came before, which itself waited: what is not of the
+    // workspace is there)
+    if (STATE_ONLY || p.plan.parts == 1) await_grid_before();
     const float a = p.log_decay[h];
     const int first = part * p.plan.len;
     const int end = first + min(p.T - first, p.plan.len);
@@ -424,6 +426,7 @@ linattn_tc(const __grid_constant__ Maps maps,
                         slots[at + k * step] =
                             pt.j.S0[bh * sn + at + k * step];
         } else {
+            await_grid_before();
             const float* from = la::state_before(pt, p.plan, part, bh);
             if (from) {
 #pragma unroll
@@ -933,27 +936,16 @@ template <int DK, bool STATE_ONLY>
 cudaError_t launch(const Maps& maps, TcParams& p, int jobs, long long bh,
                    cudaStream_t stream) {
     using Sm = Smem<DK, STATE_ONLY>;
-    auto kern = linattn_tc<DK, STATE_ONLY>;
-    // the shared-memory opt-in, once a device
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = la::allow_smem<linattn_tc<DK, STATE_ONLY>>(Sm::BYTES);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (!bit || !(done.load() & bit)) {
-        e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::BYTES);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit);
-    }
     const long long parts = p.plan.parts - (STATE_ONLY ? 1 : 0);
     long long n = 0;
     for (int i = 0; i <= kMaxJobs; ++i) {
         p.first[i] = (int)n;
         if (i < jobs) n += bh * parts * p.part[i].slices;
     }
-    kern<<<(unsigned)n, kThreads, Sm::BYTES, stream>>>(maps, p);
-    return cudaGetLastError();
+    return launch_dependent(linattn_tc<DK, STATE_ONLY>, dim3((unsigned)n),
+                            kThreads, stream, Sm::BYTES, maps, p);
 }
 
 int widest_key(const LinAttnArgs& a) {
