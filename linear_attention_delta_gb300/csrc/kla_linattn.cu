@@ -29,6 +29,7 @@
 namespace kla {
 namespace {
 
+using la::kMaxJobs;
 using la::kNV;
 using la::Part;
 using la::Plan;
@@ -140,8 +141,9 @@ __device__ __forceinline__ void load_blocks(float (&x)[1][2],
 }
 
 struct PassParams {
-    Part part;
-    Plan plan;
+    Part part[kMaxJobs];
+    int first[kMaxJobs + 1];     // first block of each pass
+    Plan plan;                   // the same for all passes
     const float* log_decay;
     int T, H;
 };
@@ -210,7 +212,10 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     // 16 warps: tiles of 16 rows, NG groups of 8-column tiles
     constexpr int MT = C / 16, NG = 16 / MT, NO = kNV / 8 / NG;
     constexpr int UT = DKP / 16, UG = 16 / UT, NU = kNV / 8 / UG;
-    const LinAttnJob& j = p.part.j;
+    int job = 0;
+    while (job + 1 < kMaxJobs && (int)blockIdx.x >= p.first[job + 1]) ++job;
+    const Part& pt = p.part[job];
+    const LinAttnJob& j = pt.j;
     extern __shared__ __align__(16) float smem[];
     float* Ps = smem + 2 * Sh::STAGE;
     float* S = Ps + C * LP;
@@ -218,9 +223,13 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     int* bad = reinterpret_cast<int*>(w + C + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int slice = blockIdx.x % p.part.slices, n0 = slice * kNV;
-    const size_t bh = blockIdx.x / p.part.slices;
-    const int b = bh / p.H, h = bh % p.H, part = blockIdx.y;
+    const int parts = STATE_ONLY ? p.plan.parts - 1 : p.plan.parts;
+    int item = blockIdx.x - p.first[job];
+    const int n0 = item % pt.slices * kNV;
+    item /= pt.slices;
+    const int part = item % parts;
+    const size_t bh = item / parts;
+    const int b = bh / p.H, h = bh % p.H;
     const int dk = j.dk, dv = j.dv, e = j.reverse ? 0 : 1;
     // (with parts the join came before, which itself waited: what is not of the
     // workspace is there)
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     load(first);
     await_grid_before();
     const float* before =
-        STATE_ONLY ? nullptr : la::state_before(p.part, p.plan, part, bh);
+        STATE_ONLY ? nullptr : la::state_before(pt, p.plan, part, bh);
 #pragma unroll 4
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
@@ -265,8 +274,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
             const size_t at = (size_t)r * j.s_r + (size_t)c * j.s_c;
             if (STATE_ONLY) {
                 if (part == 0 && j.S0)
-                    p.part.ws[bh * p.plan.parts * sn + at] =
-                        j.S0[bh * sn + at];
+                    pt.ws[bh * p.plan.parts * sn + at] = j.S0[bh * sn + at];
             } else if (before) {
                 s = before[at];
             }
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
 
     if (!STATE_ONLY && (part + 1 < p.plan.parts || !j.ST)) return;
     float* dst = STATE_ONLY
-                     ? p.part.ws + (bh * p.plan.parts + part + 1) * sn
+                     ? pt.ws + (bh * p.plan.parts + part + 1) * sn
                      : j.ST + bh * sn;
     for (int i = tid; i < DKP * kNV; i += kNT) {
         const int r = i / kNV, c = n0 + i % kNV;
@@ -428,20 +436,33 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     }
 }
 
+struct JoinParams {
+    Part part[kMaxJobs];
+    int first[kMaxJobs + 1];     // first block of each pass
+    Plan plan;
+    const float* log_decay;
+    int H;
+};
+
+constexpr int kJoin = 256;       // elements a block has
+
 // A thread has one element of the states of one sequence and head.
-__global__ void __launch_bounds__(256)
-linattn_join(float* ws, const float* log_decay, int parts, int len, int H,
-             int n, int blocks, bool first) {
-    const size_t bh = blockIdx.x / blocks;
-    const int at = blockIdx.x % blocks * 256 + threadIdx.x;
+__global__ void __launch_bounds__(kJoin) linattn_join(JoinParams p) {
+    int job = 0;
+    while (job + 1 < kMaxJobs && (int)blockIdx.x >= p.first[job + 1]) ++job;
+    const Part& pt = p.part[job];
+    const int n = pt.j.dk * pt.j.dv, blocks = (n + kJoin - 1) / kJoin;
+    const int item = blockIdx.x - p.first[job], parts = p.plan.parts;
+    const size_t bh = item / blocks;
+    const int at = item % blocks * kJoin + threadIdx.x;
     // the passes read what came before the first of them at once: not before
     // it is all there
     await_grid_before();
     release_grid_after();
     if (at >= n) return;
-    const float f = power(log_decay[bh % H], len);
-    float* x = ws + bh * parts * n + at;
-    float s = first ? x[0] : 0.f;
+    const float f = power(p.log_decay[bh % p.H], p.plan.len);
+    float* x = pt.ws + bh * parts * n + at;
+    float s = pt.j.S0 ? x[0] : 0.f;
     for (int i = 1; i < parts; i += 8) {     // eight on their way at a time
         float u[8];
 #pragma unroll
@@ -481,32 +502,26 @@ Plan plan(long long blocks, int dk, int T) {
 }
 
 template <typename T, int DKP, bool STATE_ONLY>
-cudaError_t launch_pass(const PassParams& p, long long bh,
+cudaError_t launch_pass(PassParams& p, int jobs, long long bh,
                         cudaStream_t stream) {
     constexpr int bytes = Shape<DKP>::FLOATS * 4;
     const cudaError_t e = la::allow_smem<linattn_pass<T, DKP, STATE_ONLY>>(bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(bh * p.part.slices),
-                    p.plan.parts - (STATE_ONLY ? 1 : 0));
-    return launch_dependent(linattn_pass<T, DKP, STATE_ONLY>, grid, kNT, stream,
-                            bytes, p);
-}
-
-template <typename T, int DKP>
-cudaError_t launch_job(const PassParams& p, long long bh,
-                       cudaStream_t stream) {
-    if (p.plan.parts > 1) {
-        cudaError_t e = launch_pass<T, DKP, true>(p, bh, stream);
-        if (e == cudaSuccess)
-            e = la::join_parts(p.part, p.plan, p.log_decay, bh, p.H, stream);
-        if (e != cudaSuccess) return e;
+    const long long parts = p.plan.parts - (STATE_ONLY ? 1 : 0);
+    long long n = 0;
+    for (int i = 0; i <= kMaxJobs; ++i) {
+        p.first[i] = (int)n;
+        if (i < jobs) n += bh * parts * p.part[i].slices;
     }
-    return launch_pass<T, DKP, false>(p, bh, stream);
+    return launch_dependent(linattn_pass<T, DKP, STATE_ONLY>,
+                            dim3((unsigned)n), kNT, stream, bytes, p);
 }
 
-Plan plan_of(const LinAttnArgs& a, int job) {
-    const LinAttnJob& j = a.job[job];
-    return plan((long long)a.B * a.H * la::slices_of(j), j.dk, a.T);
+Plan plan_of(const LinAttnArgs& a) {
+    long long blocks = 0;
+    for (int i = 0; i < a.jobs; ++i)
+        blocks += (long long)a.B * a.H * la::slices_of(a.job[i]);
+    return plan(blocks, la::widest_key(a), a.T);
 }
 
 // Floats of the part states of a job.
@@ -515,40 +530,61 @@ size_t part_floats(const LinAttnArgs& a, int job, const Plan& pl) {
     return pl.parts > 1 ? (size_t)a.B * a.H * pl.parts * j.dk * j.dv : 0;
 }
 
+template <typename T, int DKP>
+cudaError_t launch_passes(const LinAttnArgs& a, float* ws,
+                          cudaStream_t stream) {
+    const long long bh = (long long)a.B * a.H;
+    PassParams p{};
+    p.plan = plan_of(a);
+    p.log_decay = a.log_decay;
+    p.T = a.T, p.H = a.H;
+    for (int i = 0; i < a.jobs; ++i) {
+        p.part[i] = {a.job[i], ws, la::slices_of(a.job[i])};
+        if (p.plan.parts > 1) ws += part_floats(a, i, p.plan);
+    }
+    if (p.plan.parts > 1) {
+        cudaError_t e = launch_pass<T, DKP, true>(p, a.jobs, bh, stream);
+        if (e == cudaSuccess)
+            e = la::join_parts(p.part, a.jobs, p.plan, a.log_decay, bh, a.H,
+                               stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pass<T, DKP, false>(p, a.jobs, bh, stream);
+}
+
 template <typename T>
 cudaError_t launch_all(const LinAttnArgs& a, float* ws, cudaStream_t stream) {
-    const long long bh = (long long)a.B * a.H;
-    for (int i = 0; i < a.jobs; ++i) {
-        const LinAttnJob& j = a.job[i];
-        const Plan pl = plan_of(a, i);
-        const PassParams p{{j, ws, la::slices_of(j)}, pl, a.log_decay, a.T,
-                           a.H};
-        const cudaError_t e =
-            j.dk <= 64    ? launch_job<T, 64>(p, bh, stream)
-            : j.dk <= 128 ? launch_job<T, 128>(p, bh, stream)
-                          : launch_job<T, 256>(p, bh, stream);
-        if (e != cudaSuccess) return e;
-        if (pl.parts > 1) ws += part_floats(a, i, pl);
-    }
-    return cudaSuccess;
+    const int dk = la::widest_key(a);
+    return dk <= 64    ? launch_passes<T, 64>(a, ws, stream)
+           : dk <= 128 ? launch_passes<T, 128>(a, ws, stream)
+                       : launch_passes<T, 256>(a, ws, stream);
 }
 
 }  // namespace
 
-cudaError_t la::join_parts(const Part& p, const Plan& pl,
+cudaError_t la::join_parts(const Part* part, int jobs, const Plan& pl,
                            const float* log_decay, long long bh, int H,
                            cudaStream_t stream) {
-    const int n = p.j.dk * p.j.dv, blocks = (n + 255) / 256;
-    return launch_dependent(linattn_join, dim3((unsigned)(bh * blocks)), 256,
-                            stream, 0, p.ws, log_decay, pl.parts, pl.len, H, n,
-                            blocks, p.j.S0 != nullptr);
+    JoinParams p{};
+    p.plan = pl;
+    p.log_decay = log_decay;
+    p.H = H;
+    long long n = 0;
+    for (int i = 0; i <= kMaxJobs; ++i) {
+        p.first[i] = (int)n;
+        if (i >= jobs) continue;
+        p.part[i] = part[i];
+        n += bh * ((part[i].j.dk * part[i].j.dv + kJoin - 1) / kJoin);
+    }
+    return launch_dependent(linattn_join, dim3((unsigned)n), kJoin, stream, 0,
+                            p);
 }
 
 // By the sizes alone, whichever form the tensors' alignment allows.
 size_t linattn_workspace_bytes(const LinAttnArgs& a) {
     size_t n = 0, tc = 0;
     for (int i = 0; i < a.jobs; ++i) {
-        n += part_floats(a, i, plan_of(a, i));
+        n += part_floats(a, i, plan_of(a));
         if (linattn_tc_sizes(a)) tc += part_floats(a, i, linattn_tc_plan(a));
     }
     return (n > tc ? n : tc) * sizeof(float);

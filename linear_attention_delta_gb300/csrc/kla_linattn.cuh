@@ -9,6 +9,7 @@ namespace kla {
 namespace la {
 
 constexpr int kNV = 64;          // columns of v (and of the state) a block has
+constexpr int kMaxJobs = 3;      // passes of a call, all in the same launches
 
 // w^n of w = exp(a) (w^0 = 1, whatever w is).
 __device__ __forceinline__ float power(float a, int n) {
@@ -59,9 +60,16 @@ cudaError_t allow_smem(int bytes) {
 
 inline int slices_of(const LinAttnJob& j) { return (j.dv + kNV - 1) / kNV; }
 
-// The second launch above for one pass over B x H sequences and heads.
-cudaError_t join_parts(const Part& p, const Plan& pl, const float* log_decay,
-                       long long bh, int H, cudaStream_t stream);
+inline int widest_key(const LinAttnArgs& a) {
+    int n = 0;
+    for (int i = 0; i < a.jobs; ++i) n = a.job[i].dk > n ? a.job[i].dk : n;
+    return n;
+}
+
+// The second launch above for the passes over B x H sequences and heads.
+cudaError_t join_parts(const Part* p, int jobs, const Plan& pl,
+                       const float* log_decay, long long bh, int H,
+                       cudaStream_t stream);
 
 }  // namespace la
 

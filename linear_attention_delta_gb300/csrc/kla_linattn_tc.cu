@@ -60,9 +60,11 @@
 namespace kla {
 namespace {
 
+using la::kMaxJobs;
 using la::kNV;
 using la::Part;
 using la::Plan;
+using la::widest_key;
 using bf16 = __nv_bfloat16;
 
 __device__ unsigned int g_fault_la = 0;
@@ -75,7 +77,6 @@ constexpr int kC = 128;          // tokens a chunk
 constexpr int kThreads = 960;    // 64 registers each
 constexpr int kIssuer = 28, kCopier = 29;   // warps
 constexpr int kBox = kC * 128;   // bytes of a TMA box: 128 rows of 64 bf16
-constexpr int kMaxJobs = 3;
 constexpr int kLdS = kNV + 1;    // row of the state's tile in shared memory
 
 // Shared memory (bytes from a 1024-aligned base): the rings of Q, K and V
@@ -948,12 +949,6 @@ cudaError_t launch(const Maps& maps, TcParams& p, int jobs, long long bh,
                             kThreads, stream, Sm::BYTES, maps, p);
 }
 
-int widest_key(const LinAttnArgs& a) {
-    int n = 0;
-    for (int i = 0; i < a.jobs; ++i) n = a.job[i].dk > n ? a.job[i].dk : n;
-    return n;
-}
-
 }  // namespace
 
 bool linattn_tc_sizes(const LinAttnArgs& a) {
@@ -1023,8 +1018,8 @@ cudaError_t launch_linattn_tc(const LinAttnArgs& a, float* ws,
         cudaError_t e =
             narrow ? launch<64, true>(maps, p, a.jobs, bh, stream)
                    : launch<128, true>(maps, p, a.jobs, bh, stream);
-        for (int i = 0; i < a.jobs && e == cudaSuccess; ++i)
-            e = la::join_parts(p.part[i], p.plan, a.log_decay, bh, a.H,
+        if (e == cudaSuccess)
+            e = la::join_parts(p.part, a.jobs, p.plan, a.log_decay, bh, a.H,
                                stream);
         if (e != cudaSuccess) return e;
     }
