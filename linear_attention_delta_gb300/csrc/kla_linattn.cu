@@ -16,7 +16,7 @@
 // 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
 // operands from shared memory as they are; three times the tiles of fp32 would
 // not fit there.)  Chunks of 64 tokens by 64 columns of the state a block, 16
-// warps, two stages: 752 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 11.7
+// warps, two stages: 745 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 11.6
 // us a chunk.  Of it the products take about 410 (with one of the three
 // products: 476), taking the fragments apart most of the rest (without any
 // products and fragments: 221); Q S and the scores 290, U 167, P V 62, the
