@@ -16,12 +16,13 @@
 // 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
 // operands from shared memory as they are; three times the tiles of fp32 would
 // not fit there.)  Chunks of 64 tokens by 64 columns of the state a block, 16
-// warps, two stages: 745 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 11.6
-// us a chunk.  Of it the products take about 410 (with one of the three
-// products: 476), taking the fragments apart most of the rest (without any
-// products and fragments: 221); Q S and the scores 290, U 167, P V 62, the
-// copies 62 (by leaving each out).  One stage: 878 us; a loop of its own for
-// the scores, fragments by single loads: 808.
+// warps, two stages: 690 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 10.8
+// us a chunk.  The warp-level products bound it: without two of the three of a
+// pair 275 us less; without them and the fragments taken apart for them 530
+// less (Q S and the scores 290, U 167, P V 62).  On the way: one stage 878 us; a
+// loop of its own for the scores, fragments by single loads 808; a place's
+// address and bounds formed anew for every copy, single elements of P, S and o
+// 745.
 #include "f32x2.cuh"
 #include "kla_linattn.cuh"
 #include "tc_primitives.cuh"
@@ -140,6 +141,13 @@ __device__ __forceinline__ void load_blocks(float (&x)[1][2],
                  : "r"(tc::smem_u32(row)));
 }
 
+__device__ __forceinline__ void store_two(float* p, float a, float b) {
+    *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void store_two(bf16* p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
 struct PassParams {
     Part part[kMaxJobs];
     int first[kMaxJobs + 1];     // first block of each pass
@@ -152,25 +160,29 @@ struct PassParams {
 // beyond `rows` and `width`; columns c0 .. c0 + W - 1, the first `most` of
 // them.
 // Four adjacent elements at a time where they line up (`by4`): fp32 straight to
-// shared memory (complete after wait_copies), bf16 eight such at a time.
+// shared memory (complete after wait_copies).
 template <typename T, int C, int W>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
                                           long long st, long long first,
                                           long long step, int rows, int c0,
                                           int width, int most, bool by4) {
     if (by4) {
-#pragma unroll 8
-        for (int i = threadIdx.x; i < C * W / 4; i += kNT) {
-            const int r = i / (W / 4), c = i % (W / 4) * 4;
-            if (c >= most) continue;
-            const bool in = r < rows && c0 + c < width;
-            const T* from = in ? x + (first + step * r) * st + c0 + c : x;
-            float* to = &dst[r * ld + c];
+        // a thread has one place of every RS-th row
+        constexpr int RS = kNT / (W / 4);
+        const int r0 = threadIdx.x / (W / 4), c = threadIdx.x % (W / 4) * 4;
+        if (c >= most) return;
+        const bool inside = c0 + c < width;
+        const T* from = x + (first + step * r0) * st + c0 + c;
+        const long long next = step * RS * st;
+        float* to = &dst[r0 * ld + c];
+#pragma unroll
+        for (int r = 0; r < C; r += RS, to += RS * ld) {
+            const bool in = inside && r0 + r < rows;
             if constexpr (sizeof(T) == 4) {
                 // 16 bytes, or none of them (zeros)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::
                                  "r"(tc::smem_u32(to)),
-                             "l"(from), "r"(in ? 16 : 0)
+                             "l"(in ? from : x), "r"(in ? 16 : 0)
                              : "memory");
             } else {
                 const uint2 u = in ? *reinterpret_cast<const uint2*>(from)
@@ -179,6 +191,7 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* x,
                 *reinterpret_cast<float4*>(to) =
                     make_float4(y.x, y.y, z.x, z.y);
             }
+            from += next;
         }
         return;
     }
@@ -243,6 +256,13 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
     const int dk8 = (dk + 7) / 8 * 8;     // columns of q and k that are looked at
 
     if (tid <= C) w[tid] = power(a, tid);
+    // the state's elements in the order in which they lie in memory
+    const bool by_row = j.s_c == 1;
+    auto r_of = [&](int i) { return by_row ? i / kNV : i % DKP; };
+    auto n_of = [&](int i) { return by_row ? i % kNV : i / DKP; };
+    // two outputs at a time
+    const bool o2 = dv % 2 == 0 &&
+                    reinterpret_cast<uintptr_t>(o) % (2 * sizeof(T)) == 0;
     const bool q4 = in_fours(q, j.q.st, dk), k4 = in_fours(k, j.k.st, dk);
     const bool v4 = in_fours(v, j.v.st, dv);
     const int first = part * p.plan.len;
@@ -268,7 +288,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         STATE_ONLY ? nullptr : la::state_before(pt, p.plan, part, bh);
 #pragma unroll 4
     for (int i = tid; i < DKP * kNV; i += kNT) {
-        const int r = i / kNV, c = n0 + i % kNV;
+        const int r = r_of(i), n = n_of(i), c = n0 + n;
         float s = 0.f;
         if (r < dk && c < dv) {
             const size_t at = (size_t)r * j.s_r + (size_t)c * j.s_c;
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 s = before[at];
             }
         }
-        S[r * LV + i % kNV] = s;
+        S[r * LV + n] = s;
     }
     for (int r0 = first; r0 < end; r0 += C) {
         float* Qs = smem + ((r0 - first) / C & 1) * Sh::STAGE;
@@ -293,13 +313,21 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
         if (end - r0 > C) load(r0 + C);
         // What is not finite in v is taken out, as in P v it would meet the
         // zeros of earlier rows; its column's later outputs and state get NaN.
-#pragma unroll 4
-        for (int i = tid; i < C * kNV; i += kNT) {
-            float* x = &Vs[i / kNV * LV + i % kNV];
-            if ((__float_as_uint(*x) & 0x7f800000u) == 0x7f800000u) {
-                *x = 0.f;
-                atomicMin(&bad[i % kNV], i / kNV);
-            }
+        bool found = false;
+#pragma unroll
+        for (int i = tid; i < C * kNV / 4; i += kNT) {
+            const int r = i / (kNV / 4), c = i % (kNV / 4) * 4;
+            float* x = &Vs[r * LV + c];
+            const float4 y = *reinterpret_cast<const float4*>(x);
+            // x - x is 0 of a finite x, else NaN
+            if ((y.x - y.x) + (y.y - y.y) + (y.z - y.z) + (y.w - y.w) == 0.f)
+                continue;
+            found = true;
+            for (int k = 0; k < 4; ++k)
+                if ((__float_as_uint(x[k]) & 0x7f800000u) == 0x7f800000u) {
+                    x[k] = 0.f;
+                    atomicMin(&bad[c + k], r);
+                }
         }
         const int m = warp % MT, ng = warp / MT;
         float acc[NO][4];
@@ -321,7 +349,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 &Ks[((below ? s0 : 0) + (lane & 7) + (NO > 1 ? lane >> 4 << 3 : 0)) *
                         LD + (lane >> 3 & 1) * 4];
             const float* z = &S[t * LV + s0 + g];
-#pragma unroll 4
+#pragma unroll 2
             for (int d = 0; d < dk8; d += 8) {
                 float v[4];
                 load_blocks(v[0], v[1], v[2], v[3], x + d);
@@ -341,10 +369,13 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
 #pragma unroll
                 for (int n = 0; n < NO; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 16 * m + g + (i >> 1) * 8;
-                        const int c = s0 + 8 * n + 2 * t + (i & 1);
-                        Ps[r * LP + c] = c <= r ? sc[n][i] * w[r - c] : 0.f;
+                    for (int i = 0; i < 4; i += 2) {
+                        const int r = 16 * m + g + i * 4;
+                        const int c = s0 + 8 * n + 2 * t;
+                        *reinterpret_cast<float2*>(&Ps[r * LP + c]) =
+                            make_float2(
+                                c <= r ? sc[n][i] * w[r - c] : 0.f,
+                                c < r ? sc[n][i + 1] * w[r - c - 1] : 0.f);
                     }
             }
             // rows of Q S times w^(r + e)
@@ -354,7 +385,8 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 acc[n][0] *= u0, acc[n][1] *= u0, acc[n][2] *= u1,
                     acc[n][3] *= u1;
         }
-        __syncthreads();             // P in place; S read
+        // P in place; S read
+        const bool any = __syncthreads_or(found);
         if (!STATE_ONLY) {
             const float* x = &Ps[arow * LP + acol];
             const float* y = &Vs[t * LV + ng * NO * 8 + g];
@@ -370,18 +402,26 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                 mma<false, X>(acc, f, u);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * m + g + (i >> 1) * 8;
+            for (int i = 0; i < 4; i += 2) {
+                const int r = 16 * m + g + i * 4;
                 if (r >= rows) continue;
                 const size_t at = (size_t)(t0 + step * r);
                 T* dst = o + (((size_t)b * p.T + at) * p.H + h) * dv + n0;
 #pragma unroll
                 for (int n = 0; n < NO; ++n) {
-                    const int c = (ng * NO + n) * 8 + 2 * t + (i & 1);
-                    if (n0 + c < dv)
-                        dst[c] = from_f32<T>(r < bad[c]
-                                                 ? acc[n][i]
-                                                 : __uint_as_float(0x7fc00000u));
+                    const int c = (ng * NO + n) * 8 + 2 * t;
+                    float u0 = acc[n][i], u1 = acc[n][i + 1];
+                    if (any) {
+                        const float nan = __uint_as_float(0x7fc00000u);
+                        if (r >= bad[c]) u0 = nan;
+                        if (r >= bad[c + 1]) u1 = nan;
+                    }
+                    if (o2) {        // dv is even
+                        if (n0 + c < dv) store_two(dst + c, u0, u1);
+                    } else {
+                        if (n0 + c < dv) dst[c] = from_f32<T>(u0);
+                        if (n0 + c + 1 < dv) dst[c + 1] = from_f32<T>(u1);
+                    }
                 }
             }
         }
@@ -415,11 +455,19 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
 #pragma unroll
             for (int n = 0; n < NU; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (ug * NU + n) * 8 + 2 * t + (i & 1);
-                    float* s = &S[(16 * um + g + (i >> 1) * 8) * LV + c];
-                    *s = bad[c] < C ? __uint_as_float(0x7fc00000u)
-                                    : fmaf(grow, *s, *s) + u[n][i];
+                for (int i = 0; i < 4; i += 2) {
+                    const int c = (ug * NU + n) * 8 + 2 * t;
+                    float2* s = reinterpret_cast<float2*>(
+                        &S[(16 * um + g + i * 4) * LV + c]);
+                    float2 y = *s;
+                    y = add2(fma2(both(grow), y, y),
+                             make_float2(u[n][i], u[n][i + 1]));
+                    if (any) {
+                        const float nan = __uint_as_float(0x7fc00000u);
+                        if (bad[c] < C) y.x = nan;
+                        if (bad[c + 1] < C) y.y = nan;
+                    }
+                    *s = y;
                 }
         }
         __syncthreads();
@@ -430,9 +478,9 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                      ? pt.ws + (bh * p.plan.parts + part + 1) * sn
                      : j.ST + bh * sn;
     for (int i = tid; i < DKP * kNV; i += kNT) {
-        const int r = i / kNV, c = n0 + i % kNV;
+        const int r = r_of(i), n = n_of(i), c = n0 + n;
         if (r < dk && c < dv)
-            dst[(size_t)r * j.s_r + (size_t)c * j.s_c] = S[r * LV + i % kNV];
+            dst[(size_t)r * j.s_r + (size_t)c * j.s_c] = S[r * LV + n];
     }
 }
 
