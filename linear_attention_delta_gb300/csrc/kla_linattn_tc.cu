@@ -29,17 +29,16 @@
 // 24-27 write the outputs (thread = row), 28 issues the products, 29 the
 // copies (TMA).  They hand over through mbarriers.
 //
-// What bounds it, at B4 T4096 H16 d128 (71 us; HBM would take 40, and the
-// tensor cores are busy 29 % of the time): a chunk takes a block 2.1 us, about
-// 4000 cycles, in which 368 KB pass through shared memory (2900 cycles) and
-// some 11000 warp instructions are issued (61 % of the slots, 79 % on the
-// busiest SMs); the hand-overs and products without the element-wise work took
-// 59 us, the hand-overs alone 44.  Hence many warps with few registers (18
-// larger ones: 87 us), short loops, and weights in registers.  Measured and
+// What bounds it, at B4 T4096 H16 d128 (68 us; HBM would take 40, and the
+// tensor cores are busy in 42 % of the cycles): a chunk takes a block 2.0 us,
+// about 3900 cycles, in which 368 KB pass through shared memory (2900 cycles)
+// and some 10000 warp instructions are issued (58 % of the slots); before the
+// last steps, at 72 us, the hand-overs and products without the element-wise
+// work took 59 us, the hand-overs alone 44.  Hence many warps with few registers
+// (18 larger ones: 87 us), short loops, and weights in registers.  Measured and
 // left out: a second issuing thread 81 us, scores twice buffered with separate
 // products for the parts of V 78, or with one accumulator of outputs and P~ in
-// the scores' place 74, waits for the next product before the last two of this
-// one 74.
+// the scores' place 71, weighted V by halves 67 (but 59 for 58 with d64).
 //
 // In reverse the tiles lie in memory order all the same; r counts from the
 // tile's last row, masks and weights are mirrored.
