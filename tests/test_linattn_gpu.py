@@ -377,6 +377,20 @@ def test_same_bits_and_graph_replay():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 72, 200, 33])
+def test_outputs_at_any_alignment(d, dtype):
+    """o one element off every wider piece it is written in."""
+    x, _ = make(2, 130, 2, d, d, dtype)
+    room = torch.full((2 * 130 * 2 * d + 2,), 7.0, dtype=dtype).cuda()
+    o = room[1:-1].view(2, 130, 2, d)
+    got, hT = kla.linattn_fwd(**x, o=o)
+    assert got is o
+    check_fwd(x, o, hT)
+    assert room[0] == 7 and room[-1] == 7
+    assert torch.equal(o, kla.linattn_fwd(**x)[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_two_streams_at_once(dtype):
     """Calls in flight beside one another, each with parts of its own."""
     xs = [make(1, 2500, 2, 64, 64, dtype, seed=i) for i in range(2)]
