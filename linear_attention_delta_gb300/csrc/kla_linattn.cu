@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
                     atomicMin(&bad[c + k], r);
                 }
         }
-        const int m = warp % MT, ng = warp / MT;
+        // (warps of one scheduler, those equal modulo 4, have different rows, and
+        // with 4 x 4 tiles of scores two or three of the lower triangle's ten)
+        const int m = (warp ^ warp >> 2) & (MT - 1), ng = warp / MT;
         float acc[NO][4];
         // this lane's row of the blocks of an A fragment (16 x 8)
         const int arow = 16 * m + (lane & 15), acol = (lane >> 4) * 4;
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
             for (int n = 0; n < NO; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[n][i] = sc[n][i] = 0.f;
-            const int s0 = ng * NO * 8;
+            const int s0 = (MT == 4 ? (warp + 2 * ng) & 3 : ng) * NO * 8;
             // columns all above the diagonal stay 0
             const bool below = s0 < C && s0 <= 16 * m + 15;
             const float* x = &Qs[arow * LD + acol];
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
             const float* y =
                 &Ks[((below ? s0 : 0) + (lane & 7) + (NO > 1 ? lane >> 4 << 3 : 0)) *
                         LD + (lane >> 3 & 1) * 4];
-            const float* z = &S[t * LV + s0 + g];
+            const float* z = &S[t * LV + ng * NO * 8 + g];
 #pragma unroll 2
             for (int d = 0; d < dk8; d += 8) {
                 float v[4];
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kNT, 1) linattn_pass(PassParams p) {
             }
         }
         // U: 16 rows of the state x NU 8-column tiles a warp
-        const int um = warp % UT, ug = warp / UT;
+        const int ug = warp / UT, um = (warp + ug) % UT;
         if (16 * um < dk) {
             float u[NU][4];
 #pragma unroll
