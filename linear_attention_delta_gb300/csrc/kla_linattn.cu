@@ -16,13 +16,13 @@
 // 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
 // operands from shared memory as they are; three times the tiles of fp32 would
 // not fit there.)  Chunks of 64 tokens by 64 columns of the state a block, 16
-// warps, two stages: 690 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 10.8
-// us a chunk.  The warp-level products bound it: without two of the three of a
-// pair 275 us less; without them and the fragments taken apart for them 530
+// warps, two stages: 640 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 10 us
+// a chunk.  The warp-level products bound it: at 750 us, without two of the three
+// of a pair 275 less; without them and the fragments taken apart for them 530
 // less (Q S and the scores 290, U 167, P V 62).  On the way: one stage 878 us; a
 // loop of its own for the scores, fragments by single loads 808; a place's
 // address and bounds formed anew for every copy, single elements of P, S and o
-// 745.
+// 745; the lower triangle's work uneven among the schedulers 692.
 #include "f32x2.cuh"
 #include "kla_linattn.cuh"
 #include "tc_primitives.cuh"
@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(kJoin) linattn_join(JoinParams p) {
 // Parts of a sequence.  A launch takes as many turns as its blocks, one an
 // SM, fill the SMs.  Counted in chunks: a block takes about half a chunk's time
 // besides its own, a chunk of the pass that forms the state 0.35, and the two
-// launches more about one (fp32, in one part and by this rule: B1 T20000 H4 d64
-// 2590 and 134 us, B3 T1001 H5 d72 156 and 77, B1 T4096 H4 d256 1600 and 291).
+// launches more about one (measured at an earlier step, fp32, in one part and by
+// this rule: B1 T20000 H4 d64 2590 and 134 us, B3 T1001 H5 d72 156 and 77, B1
+// T4096 H4 d256 1600 and 291).
 Plan plan(long long blocks, int dk, int T) {
     const int C = dk > 128 ? 32 : 64, slots = 152;
     const int chunks = (T + C - 1) / C;
