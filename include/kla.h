@@ -801,9 +801,13 @@ KLA_API kla_status kla_linattn_step(
  * lse [N] fp32 or null; top_logp [N, top] fp32 and top_ids [N, top] int64
  * (null with top = 0).  A token outside 0 .. V - 1 (padding, by custom -1 or
  * -100) has logp 0.  scale (1 / temperature): finite and > 0.  -inf masks a
- * logit (its p is 0); a row masked throughout has lse and logp -inf, entropy
- * 0, and its top ids are 0, 1, ...  NaN or +inf in a row makes its lse, logp
- * and entropy NaN (NaN ranks above +inf among the top).  All sums in fp32.
+ * logit (its p is 0), and so does a z below the range of fp32; a row masked
+ * throughout has lse and logp -inf, entropy 0, and its top ids are the lowest
+ * of the largest logits.  NaN or +inf in a row (or a z above the range) makes
+ * its lse, logp and entropy NaN (NaN ranks above +inf among the top).
+ * All sums in fp32, of distances from the row's largest z: logp and entropy
+ * keep their digits near 0 and in rows far from 0, logp is never above 0 and
+ * entropy never below; lse is never below the row's largest z.
  * The outputs may not overlap logits, tokens or each other.
  * Errors: KLA_ERR_INVALID_ARG (N < 0, V < 1, top < 0 or > V, a negative
  * stride, a bad scale, a null or misaligned pointer, overlapping buffers),
@@ -826,6 +830,8 @@ KLA_API kla_status kla_logprob_fwd(
  *               - entropy_grad p_j (log p_j + entropy)
  *     logits_grad_j = scale dL/dz_j
  *
+ * p_j is exp(z_j - lse): what lse was rounded by, up to 2^-24 |lse|, is a
+ * relative error of p_j.
  * A row without a token (outside 0 .. V - 1) has no logp term; a row masked
  * throughout has gradient 0.  logits_grad [N, V] contiguous, of type `dtype`;
  * it may be logits itself (same address, logits_stride = V), else it may not

@@ -3,8 +3,10 @@
 //
 // Forward, one pass over a row with a running maximum m (z = scale x):
 //   s = sum exp(z - m),  t = sum exp(z - m) (z - m)
-//   lse = m + log s,     entropy = log s - t / s
-// (for any m near the maximum),
+//   lse = m + log s,     entropy = log s - t / s,    logp = (z - m) - log s
+// (with m the maximum both terms of the entropy are of one sign and nothing
+// cancels: relative to a number up to 40 below it, entropies under 1 came out
+// up to 1e-5 off and below 0),
 // and where two partial results meet, with m' = max(m1, m2), c = exp(m - m'):
 //   s' = sum c s,        t' = sum c (t + s (m - m')).
 // A row is read once; it belongs to one block, or, when there are few long
@@ -79,13 +81,17 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
             ca * fmaf(a.s, da, a.t) + cb * fmaf(b.s, db, b.t)};
 }
 
-// How far a logit may be above the m that a thread's sums are relative to:
-// they need no maximum, only exponentials in range, so m moves hardly ever.
-constexpr float kAbove = 40.f;
-
-// m for logits of which `top` (scaled) is the largest.
-__device__ __forceinline__ void refer(Sums& a, float top) {
-    if (!(top - a.m <= kAbove)) a = join(a, Sums{top, 0.f, 0.f});   // NaN too
+// Moves the sums to logits of which `top` is the largest, if it is the largest
+// so far.  m is rounded up: no scaled logit is above it, so that all terms of t
+// have one sign and the entropy keeps its digits however small it is.
+__device__ __forceinline__ void refer(Sums& a, float top, float scale) {
+    const float m = __fmul_ru(top, scale);
+    if (m <= a.m) return;                              // (NaN goes on)
+    const float to = max_nan(a.m, m);
+    const float d = max_nan(a.m - to, -200.f), c = ex2(d * kLog2e);
+    a.t = c * fmaf(a.s, d, a.t);
+    a.s *= c;
+    a.m = to;
 }
 // N logits into a thread's sums.
 template <int N>
@@ -385,13 +391,13 @@ logprob_fwd(LogprobArgs a, int parts) {
         x, r,
         [&](const auto& v) {
             const float m = Vec<T>::largest(v);
-            refer(acc, m * a.scale);
+            refer(acc, m, a.scale);
             if (TOP) own = max_nan(own, m);
         },
         [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, a.scale); },
         [&](int, float v) {
             const float one[1] = {v};
-            refer(acc, v * a.scale);
+            refer(acc, v, a.scale);
             add(acc, one, a.scale);
             if (TOP) own = max_nan(own, v);
         });
@@ -438,16 +444,27 @@ logprob_fwd(LogprobArgs a, int parts) {
             __syncthreads();
         }
         const Sums all = parts > 1 ? sh.part[0] : sh.whole;
-        const bool none = all.m == -INFINITY;
+        // (of a row whose scaled logits are all out of range downwards m is
+        // the lowest number and s is 0)
+        const bool none = all.s == 0.f;
         const float ls = logf(all.s);
-        const float lse = none ? -INFINITY : all.m + ls;
+        // Where m was rounded up s may be below 1: the true lse is not below
+        // the largest logit for all that.
+        const float lse = none ? -INFINITY : all.m + max_nan(ls, 0.f);
+        // from m and log s apart: their sum would lose the digits of rows far
+        // from 0; no log probability is above 0
+        auto logp = [&](float v) {
+            const float lp = fmaf(v, a.scale, -all.m) - ls;
+            return none ? -INFINITY : lp > 0.f ? 0.f : lp;      // (NaN stays)
+        };
         if (tid == 0) {
             const long long t = a.tokens[row];
             float lp = 0.f;
             if (t >= 0 && t < a.V)
-                lp = none ? -INFINITY : fmaf(to_f32(x[t]), a.scale, -lse);
+                lp = logp(to_f32(x[t]));
             a.logp[row] = lp;
-            if (a.entropy) a.entropy[row] = none ? 0.f : ls - all.t / all.s;
+            const float ent = ls - all.t / all.s;
+            if (a.entropy) a.entropy[row] = none || ent < 0.f ? 0.f : ent;
             if (a.lse) a.lse[row] = lse;
         }
         if (TOP) {
@@ -463,7 +480,7 @@ logprob_fwd(LogprobArgs a, int parts) {
                 if (rank >= a.top) continue;
                 const size_t out = row * a.top + rank;
                 const float v = value_of((unsigned)(k >> 32));
-                a.top_logp[out] = none ? -INFINITY : fmaf(v, a.scale, -lse);
+                a.top_logp[out] = logp(v);
                 a.top_ids[out] = 0xffffffffu - (unsigned)k;
             }
         }

@@ -278,3 +278,86 @@ def test_binding_refuses():
     with pytest.raises(kla.KlaError):
         kla.logprob_fwd(torch.zeros(2, 500, device="cuda"),
                         t[:2], top=129)
+
+
+def peaked(V, dtype, peaks, seed=0):
+    """Rows around 0 with one logit far above the others, early and late."""
+    gen = torch.Generator().manual_seed(seed + V)
+    n = len(peaks)
+    x = torch.randn(n, V, generator=gen)
+    at = torch.tensor([0, V // 3, V - 1 - V // 50, V - 1, V // 2]).repeat(
+        n)[:n]
+    x[torch.arange(n), at] = torch.tensor(peaks, dtype=F32)
+    return x.to(dtype).cuda(), at.cuda()
+
+
+PEAKS = [12.0, 13.5, 15.0, 17.0, 18.0, 20.0, 22.5, 25.0, 27.0, 30.0, 32.0,
+         35.0, 37.0, 39.0]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1000, 32000, 131072])
+@pytest.mark.parametrize("scale", [1.0, 0.8, 1.3])
+def test_confident_rows_keep_their_digits(V, scale, dtype):
+    """Entropies and log probabilities near 0, and their signs."""
+    x, t = peaked(V, dtype, PEAKS)
+    scale32, top = float(np.float32(scale)), 4
+    want = mixer.lp_fwd(x, t, top, scale32)
+    out = kla.logprob_fwd(x, t, top, scale)
+    logp, ent, lse, tlp = (mixer.f64(o) for o in out[:4])
+    # Relative to the largest logit all terms of a sum have one sign.  A row's
+    # sum meets some 100 roundings of half a step, 2^-24, at most: they add up
+    # to 32 of them where their signs are any (more than three times the square
+    # root of their number).  The quotient, the logarithm and the last sum are
+    # roundings of what is returned.
+    step = 32 * U32
+    assert (np.abs(ent - want[1]) <= step + 4 * U32 * want[1]).all()
+    assert (np.abs(logp - want[0]) <= step + 4 * U32 * np.abs(want[0])).all()
+    assert (np.abs(lse - want[2]) <= step + 2 * U32 * np.abs(want[2])).all()
+    assert (np.abs(tlp - want[3]) <= step + 4 * U32 * np.abs(want[3])).all()
+    assert (out[4].cpu().numpy() == want[4]).all()
+    # what no rounding may turn round
+    assert (ent >= 0).all() and (logp <= 0).all() and (tlp <= 0).all()
+    assert (lse >= scale32 * mixer.f64(x).max(1)).all()
+    g = torch.ones(len(PEAKS), device="cuda")
+    d = mixer.f64(kla.logprob_bwd(x, t, out[2], logp_grad=g, scale=scale))
+    own = d[np.arange(len(PEAKS)), t.cpu().numpy()]
+    assert (own >= 0).all()
+    assert (np.delete(d, t.cpu().numpy(), 1).max() <= 0)
+    # 1 - p, of an lse rounded once more, and rounded to logits' type
+    exact = -np.expm1(want[0]) * scale32
+    bound = scale32 * (step + 4 * U32 * (1 + np.abs(want[2])))
+    if dtype == BF16:
+        bound = bound + U16 * (exact + bound)
+    assert (np.abs(own - exact) <= bound).all()
+
+
+@pytest.mark.parametrize("V", [700, 32000, 131072])
+def test_a_shift_of_all_logits_changes_lse_alone(V):
+    gen = torch.Generator().manual_seed(V)
+    # multiples of 2^-10 below 2^13: exact with the shift
+    x = (torch.randn(5, V, generator=gen) * 4096).round().div(1024)
+    x[2, V - 3] = 30.0
+    x, t = x.cuda(), torch.randint(0, V, (5,), generator=gen).cuda()
+    a, b = kla.logprob_fwd(x, t, 6), kla.logprob_fwd(x + 4096, t, 6)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(a[i], b[i])
+    assert ((b[2] - 4096 - a[2]).abs() <= 2 * U32 * 4200).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scaled_logits_below_the_range_are_masked(dtype):
+    x = torch.full((3, 2000), torch.finfo(dtype).min, dtype=dtype,
+                   device="cuda")
+    x[1, 7] = 1.0
+    x[2, :1999] = -math.inf
+    t = torch.full((3,), 7, dtype=torch.int64, device="cuda")
+    logp, ent, lse, tlp, ids = kla.logprob_fwd(x, t, 2, scale=2.0)
+    inf = math.inf
+    assert logp.tolist() == [-inf, 0, -inf] and ent.tolist() == [0, 0, 0]
+    assert lse.tolist() == [-inf, 2, -inf]
+    assert tlp.tolist() == [[-inf, -inf], [0, -inf], [-inf, -inf]]
+    assert ids.tolist() == [[0, 1], [7, 0], [1999, 0]]
+    d = kla.logprob_bwd(x, t, lse, ent, torch.ones_like(lse),
+                        torch.ones_like(lse), scale=2.0)
+    assert (d == 0).all()
