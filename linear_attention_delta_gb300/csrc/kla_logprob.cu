@@ -50,9 +50,13 @@ __device__ __forceinline__ float value_of(unsigned u) {
     return u == 0xffffffffu ? __uint_as_float(0x7fc00000u)
            : __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
-// One key a logit: its order above, then the lower id.  0 is none.
+// One key a logit: its order above, then the lower id.  0 is none, and ~0 is
+// above all of them (NaN at id 0 too).
 __device__ __forceinline__ u64 key_of(float x, int id) {
-    return (u64)order_of(x) << 32 | (0xffffffffu - id);
+    return (u64)order_of(x) << 32 | (0xfffffffeu - id);
+}
+__device__ __forceinline__ unsigned id_of(u64 key) {
+    return 0xfffffffeu - (unsigned)key;
 }
 
 // The larger of two, NaN if one is.
@@ -481,7 +485,7 @@ logprob_fwd(LogprobArgs a, int parts) {
                 const size_t out = row * a.top + rank;
                 const float v = value_of((unsigned)(k >> 32));
                 a.top_logp[out] = logp(v);
-                a.top_ids[out] = 0xffffffffu - (unsigned)k;
+                a.top_ids[out] = id_of(k);
             }
         }
     }

@@ -361,3 +361,22 @@ def test_scaled_logits_below_the_range_are_masked(dtype):
     d = kla.logprob_bwd(x, t, lse, ent, torch.ones_like(lse),
                         torch.ones_like(lse), scale=2.0)
     assert (d == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1000, 3000, 70001])
+def test_nan_at_the_first_id(V, dtype):
+    """NaN ranks first, equal logits by rising id, whichever way the row is
+    searched (more candidates than a block holds: round by round)."""
+    x = torch.zeros(5, V, dtype=dtype, device="cuda")
+    x[0] = math.nan
+    x[1, 0] = math.nan                       # above V - 1 equal logits
+    x[2] = -math.inf
+    x[2, 0] = math.nan                       # the only one not masked
+    x[3, V - 1] = math.nan
+    t = torch.ones(5, dtype=torch.int64, device="cuda")
+    _, _, _, tlp, ids = kla.logprob_fwd(x, t, 6)
+    first = list(range(6))
+    assert [r.tolist() for r in ids] == [first, first, first,
+                                         [V - 1] + first[:5], first]
+    assert torch.isnan(tlp[:4]).all() and torch.isfinite(tlp[4]).all()
