@@ -23,7 +23,7 @@ import torch
 import torch.nn.functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from examples.recurrent_lm import AddNorm, TokenLoss  # noqa: E402
+from examples.recurrent_lm import AddNorm, TokenLoss, first_order  # noqa: E402
 from linear_attention_delta_gb300 import kla  # noqa: E402
 
 
@@ -37,6 +37,7 @@ class Attention(torch.autograd.Function):
         return o, hT
 
     @staticmethod
+    @first_order
     def backward(ctx, do, dhT):
         q, k, v, log_decay = ctx.saved_tensors
         g = kla.linattn_bwd(q, k, v, log_decay, do.contiguous(), hT_grad=dhT,

@@ -15,6 +15,7 @@ before, which takes memory.
 from __future__ import annotations
 
 import argparse
+import functools
 import os
 import sys
 
@@ -23,6 +24,19 @@ import torch.nn.functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from linear_attention_delta_gb300 import kla  # noqa: E402
+
+
+def first_order(backward):
+    """For a backward pass that is not differentiable itself: an error where a
+    graph of it is asked for (create_graph), as what autograd would record of
+    it is not its derivative."""
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        if torch.is_grad_enabled():
+            raise RuntimeError("there is no second derivative of this "
+                               "operator (create_graph)")
+        return backward(ctx, *grads)
+    return wrapped
 
 
 class AddNorm(torch.autograd.Function):
@@ -37,6 +51,7 @@ class AddNorm(torch.autograd.Function):
         return y, s.view_as(s)
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, ds):
         s, w, mean, rstd = ctx.saved_tensors
         g = kla.layernorm_bwd(dy.contiguous(), s, w, mean, rstd,
@@ -55,6 +70,7 @@ class Recurrence(torch.autograd.Function):
         return o, hT
 
     @staticmethod
+    @first_order
     def backward(ctx, do, dhT):
         o, log_alpha, cu = ctx.saved_tensors
         g = kla.glr_bwd(o, log_alpha, do.contiguous(), dhT, cu_seqlens=cu,
@@ -74,6 +90,7 @@ class TokenLoss(torch.autograd.Function):
         return -logp.sum() / count
 
     @staticmethod
+    @first_order
     def backward(ctx, g):
         logits, target, lse, count = ctx.saved_tensors
         weight = (-g / count).expand(target.shape).contiguous()

@@ -101,3 +101,25 @@ def test_training_step_in_a_graph():
     torch.cuda.synchronize()
     for x, y in zip(out, want):
         assert torch.equal(x, y)
+
+
+def test_second_derivatives_are_refused():
+    """The backward passes are not differentiable themselves: asked for, that
+    is an error and no wrong gradient."""
+    from examples import linattn_lm, recurrent_lm
+    B, T, H, d = 1, 12, 2, 16
+    x = torch.randn(B, T, H, d, device="cuda", requires_grad=True)
+    one = torch.ones(d, device="cuda", requires_grad=True)
+    zero = torch.zeros(d, device="cuda", requires_grad=True)
+    target = torch.zeros(B, T, H, dtype=torch.int64, device="cuda")
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    a = torch.full((H,), -0.1, device="cuda")
+    for f in (lambda: linattn_lm.Attention.apply(x, x * x, x, a)[0],
+              lambda: recurrent_lm.TokenLoss.apply(x * x, target),
+              lambda: recurrent_lm.AddNorm.apply(x * x, None, one, zero)[0],
+              lambda: recurrent_lm.Recurrence.apply(
+                  x[0].flatten(1), -x[0].flatten(1).square(), cu)[0]):
+        for g in (lambda y: y.sum(), lambda y: y.square().sum()):
+            with pytest.raises(RuntimeError, match="second derivative"):
+                dx, = torch.autograd.grad(g(f()), x, create_graph=True)
+                torch.autograd.grad(dx.square().sum(), x)
