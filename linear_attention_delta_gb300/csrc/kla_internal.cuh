@@ -353,6 +353,10 @@ cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream);
 cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, cudaStream_t stream);
 // SM count of the current device (cached per device).
 int device_sm_count();
+// SMs that the rules for cutting sequences into parts and rows over blocks
+// count with, those of a GB300: on purpose no property of the device, so that
+// workspace sizes and the bits of results are the same everywhere.
+constexpr int kPlanSMs = 152;
 
 // cuTensorMapEncodeTiled from the driver (looked up once); false if absent.
 bool get_encoder();

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kJoin) linattn_join(JoinParams p) {
 // this rule: B1 T20000 H4 d64 2590 and 134 us, B3 T1001 H5 d72 156 and 77, B1
 // T4096 H4 d256 1600 and 291).
 Plan plan(long long blocks, int dk, int T) {
-    const int C = dk > 128 ? 32 : 64, slots = 152;
+    const int C = dk > 128 ? 32 : 64, slots = kPlanSMs;
     const int chunks = (T + C - 1) / C;
     auto turns = [&](long long n) { return (double)((n + slots - 1) / slots); };
     Plan best{1, T};

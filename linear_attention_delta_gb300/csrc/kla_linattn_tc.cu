@@ -972,13 +972,13 @@ bool linattn_tc_eligible(const LinAttnArgs& a) {
 // one part and by this rule: B1 T65536 H16 983 and 400 us, B1 T8192 H16 131 and
 // 76; B2 T2049 H12 d64 41 and 32; B4 T4096 H16 stays in one).
 la::Plan linattn_tc_plan(const LinAttnArgs& a) {
-    constexpr int kSMs = 152, kMost = 32;
+    constexpr int kMost = 32;
     long long blocks = 0;
     for (int i = 0; i < a.jobs; ++i)
         blocks += (long long)a.B * a.H * la::slices_of(a.job[i]);
     const int chunks = (a.T + kC - 1) / kC;
     Plan best{1, a.T};
-    auto turns = [&](long long n) { return (n + kSMs - 1) / kSMs; };
+    auto turns = [&](long long n) { return (n + kPlanSMs - 1) / kPlanSMs; };
     double least = turns(blocks) * (2.2 * chunks + 4.0);
     for (int p = 2; p <= kMost && p <= chunks; ++p) {
         const int len = (chunks + p - 1) / p;           // chunks

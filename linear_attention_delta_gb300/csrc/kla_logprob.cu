@@ -564,8 +564,6 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
 
 // ---------------------------------------------------------------- launch
 
-constexpr int kSMs = 152;
-
 template <typename... P, typename... A>
 cudaError_t launch_rows(void (*kernel)(P...), long long rows, int parts,
                         int threads, bool cluster, cudaStream_t s, A... args) {
@@ -600,10 +598,10 @@ cudaError_t launch_fwd_of(const LogprobArgs& a, int parts, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
     int parts = 1;
-    while (parts < kMaxParts && (long long)a.N * parts * 2 <= 4 * kSMs &&
+    while (parts < kMaxParts && (long long)a.N * parts * 2 <= 4 * kPlanSMs &&
            a.V / (parts * 2) >= 16384)
         parts *= 2;
-    return a.V / parts <= 4096 || a.N >= 24 * kSMs
+    return a.V / parts <= 4096 || a.N >= 24 * kPlanSMs
                ? launch_fwd_of<T, 128>(a, parts, s)
                : launch_fwd_of<T, 256>(a, parts, s);
 }
@@ -614,7 +612,7 @@ cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
     const int parts =
-        std::max(1, std::min({32 * kSMs / a.N, a.V / 4096, 64}));
+        std::max(1, std::min({32 * kPlanSMs / a.N, a.V / 4096, 64}));
     return launch_rows(logprob_bwd<T, 128>, a.N, parts, 128, false, s, a);
 }
 
