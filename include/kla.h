@@ -727,7 +727,16 @@ KLA_API kla_status kla_glr_step(const void* x, long long x_stride,
  * linear attention without decay, positive values grow as written while
  * they stay in range.  The decays are constants of the model: there is no
  * gradient for them.  1 <= dk, dv <= 256.
- * Sums and states are held in fp32.  A value that is not finite makes its own
+ * Sums and states are held in fp32.  bf16 with q and k up to 128 wide, tensors
+ * that start and step by 16 bytes, takes the tensor cores: there the weighted
+ * scores exp((t - s) log_decay) (q_t k_s) and the copy of the state that o reads
+ * are rounded to bf16 once each (o is 1.4 times as far from the exact one as if
+ * rounded once; hT is not rounded).  Inside a chunk of 128 tokens both carry
+ * factors of up to exp(64 |log_decay|), for |log_decay| <= 0.75 only: near 0.75
+ * scores, and scores times values, above 4e17 overflow, and scores, states and
+ * outputs below 1e-17 lose digits; at 0.1 that is 5e35 and 1e-35.  Wider heads,
+ * other tensors and fp32 have neither.
+ * A value that is not finite makes its own
  * token's and later outputs not finite (which of inf and NaN is not fixed)
  * and reaches no earlier token, sequence or head.
  * workspace: kla_linattn_workspace_size bytes (0 for many sequences or short
@@ -759,7 +768,10 @@ KLA_API kla_status kla_linattn_fwd(
  *     q_grad_t = S_t o_grad_t,  k_grad_t = D_t v_t,  v_grad_t = D_t^T k_t,
  *     h0_grad = exp(log_decay_h) D_1                    (T = 0: hT_grad)
  *
- * The states are formed again from k, v and h0.  q_grad, k_grad, v_grad are
+ * The states are formed again from k, v and h0; the gradients are passes of the
+ * forward with (o_grad, v, k), (v, o_grad, q) and (k, q, o_grad) in place of
+ * (q, k, v), with its roundings and ranges (tensor cores where all widths are up
+ * to 128).  q_grad, k_grad, v_grad are
  * contiguous and of type `dtype`; h0_grad [B, H, dk, dv] fp32 or null.  The
  * outputs may not overlap any input nor each other.  workspace:
  * kla_linattn_workspace_size bytes with backward = 1.
