@@ -13,9 +13,11 @@
 //
 // The products are warp-level ones of tf32 (mma.sync): a number of fp32 is two
 // of tf32, x = hi + lo up to 2^-23, and x y = hi hi' + hi lo' + lo hi' up to
-// 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 takes its
-// operands from shared memory as they are; three times the tiles of fp32 would
-// not fit there.)  Chunks of 64 tokens by 64 columns of the state a block, 16
+// 2^-22; bf16 inputs are one of tf32 and need no lo.  (tcgen05 adds up inside
+// the instruction, which cuts off what it adds: with sums there, and not outside
+// as here, outputs were 7 times as far from the exact ones.  And it takes its
+// operands from shared memory, where two tiles in place of each would leave no
+// room for a second stage of 128-wide heads.)  Chunks of 64 tokens by 64 columns of the state a block, 16
 // warps, two stages: 640 us at B4 T4096 H16 d128 fp32 (HBM would take 79), 10 us
 // a chunk.  The warp-level products bound it: at 750 us, without two of the three
 // of a pair 275 less; without them and the fragments taken apart for them 530
@@ -530,9 +532,10 @@ __global__ void __launch_bounds__(kJoin) linattn_join(JoinParams p) {
 // Parts of a sequence.  A launch takes as many turns as its blocks, one an
 // SM, fill the SMs.  Counted in chunks: a block takes about half a chunk's time
 // besides its own, a chunk of the pass that forms the state 0.35, and the two
-// launches more about one (measured at an earlier step, fp32, in one part and by
-// this rule: B1 T20000 H4 d64 2590 and 134 us, B3 T1001 H5 d72 156 and 77, B1
-// T4096 H4 d256 1600 and 291).
+// launches more about one (shares of an earlier step, whose chunks took a fifth
+// longer; us on the GPU now, fp32, in one part and by this rule: B1 T20000 H4 d64
+// 2008 and 98, B3 T1001 H5 d72 119 and 51, B1 T4096 H4 d256 1294 and 228, B1 T4096
+// H16 d128 638 and 234).
 Plan plan(long long blocks, int dk, int T) {
     const int C = dk > 128 ? 32 : 64, slots = kPlanSMs;
     const int chunks = (T + C - 1) / C;

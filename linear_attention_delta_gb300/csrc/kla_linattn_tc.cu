@@ -13,8 +13,9 @@
 // column, and S that of w^(63 + e).  These factors stay within e^48, which
 // leaves bf16 its digits for scores up to 4e17 and states down to 1e-17;
 // stronger decays (64 |log_decay| > 48: a memory of a token or two) have their
-// rows of Q S scaled in TMEM instead, and every score its own factor (88 us
-// where the others take 71, if all 16 heads of B4 T4096 d128 are such).
+// rows of Q S scaled in TMEM instead, and every score its own factor (if all
+// heads are such: 69 us where the others take 66 at B4 T4096 H16 d128, 61 and 56
+// with d64, 256 and 217 at B8 T8192 H32 d64).
 // U does not depend on S, so the only chain from chunk to chunk is one
 // multiply-add of the state, and everything else runs ahead of it.
 //
@@ -29,16 +30,19 @@
 // 24-27 write the outputs (thread = row), 28 issues the products, 29 the
 // copies (TMA).  They hand over through mbarriers.
 //
-// What bounds it, at B4 T4096 H16 d128 (68 us; HBM would take 40, and the
-// tensor cores are busy in 42 % of the cycles): a chunk takes a block 2.0 us,
-// about 3900 cycles, in which 368 KB pass through shared memory (2900 cycles)
-// and some 10000 warp instructions are issued (58 % of the slots); before the
-// last steps, at 72 us, the hand-overs and products without the element-wise
-// work took 59 us, the hand-overs alone 44.  Hence many warps with few registers
-// (18 larger ones: 87 us), short loops, and weights in registers.  Measured and
-// left out: a second issuing thread 81 us, scores twice buffered with separate
-// products for the parts of V 78, or with one accumulator of outputs and P~ in
-// the scores' place 71, weighted V by halves 67 (but 59 for 58 with d64).
+// What bounds it, at B4 T4096 H16 d128 (66 us on the GPU, as all times here
+// unless they are said to be of an earlier step; HBM would take 40): a chunk
+// takes a block 2.0 us, about 4100 cycles, in which 368 KB pass through shared
+// memory (2900 cycles) and some 10000 warp instructions are issued.  Captured at
+// B4 T2048 H16 d128 (37 us) the SMs at work use 58 % of their issue slots, and
+// the tensor cores are busy in 42 % of the cycles.  At an earlier step, at 72 us,
+// the hand-overs and products without the element-wise work took 59 us, the
+// hand-overs alone 44.  Hence many warps with few registers, short loops, and
+// weights in registers.  Measured and left out: weighted V by halves 65 us (but
+// 57.5 for 56 with d64), scores twice buffered with one accumulator of outputs
+// and P~ in the scores' place 69 (57.6 with d64); at earlier steps, at 72 to 80
+// us, 18 larger warps 87, a second issuing thread 81, scores twice buffered with
+// separate products for the parts of V 78.
 //
 // In reverse the tiles lie in memory order all the same; r counts from the
 // tile's last row, masks and weights are mirrored.
@@ -707,7 +711,7 @@ linattn_tc(const __grid_constant__ Maps maps,
             cw[m] = make_float2(power(a, rev ? 2 * m : -2 * m),
                                 power(a, rev ? 2 * m + 1 : -2 * m - 1));
         // (a loop for each kind and order, as short as it can be: one loop
-        // with the cases inside took 252 us where this takes 222, at B8 T8192
+        // with the cases inside took 252 us where these took 222, at B8 T8192
         // H32 d64)
         auto walk = [&](auto kind, auto order) {
             constexpr bool GENTLE = decltype(kind)::value;
@@ -966,11 +970,13 @@ bool linattn_tc_eligible(const LinAttnArgs& a) {
 }
 
 // Parts of a sequence.  A block has an SM to itself, so a launch takes as many
-// turns as its blocks fill the SMs; measured, a chunk takes a block 2.2 us, or
-// 1.1 us where only the state is formed, and a block takes 4 us besides.  More
-// parts fill the last turn better and cost a pass over k and v more (d128, in
-// one part and by this rule: B1 T65536 H16 983 and 400 us, B1 T8192 H16 131 and
-// 76; B2 T2049 H12 d64 41 and 32; B4 T4096 H16 stays in one).
+// turns as its blocks fill the SMs; counted with 2.2 us for a chunk, 1.1 us where
+// only the state is formed, and 4 us for a block besides (figures of an earlier
+// step; a chunk takes 1.7 to 2.0 us now).  More parts fill the last turn better
+// and cost a pass over k and v more (us on the GPU, in one part and by this rule:
+// d128 B1 T65536 H16 895 and 387, B1 T8192 H16 118 and 67; d64 B1 T16384 H16 227
+// and 55, B2 T2049 H12 33 and 22, B4 T4096 H16, in two parts, 57 and 57; B4 T4096
+// H16 d128 stays in one).
 la::Plan linattn_tc_plan(const LinAttnArgs& a) {
     constexpr int kMost = 32;
     long long blocks = 0;

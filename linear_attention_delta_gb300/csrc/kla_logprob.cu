@@ -590,11 +590,13 @@ cudaError_t launch_fwd_of(const LogprobArgs& a, int parts, cudaStream_t s) {
                                true, s, a);
 }
 // Blocks of a row: up to four for every SM, of at least 16384 logits
-// (measured, us with a row in one block and over a cluster: 1 x 32000 7.4 and
-// 8.4, 64 x 32000 with 20 alternatives 11.3 and 12.8, 8 x 131072 about 8 and
-// 4.4).  128 threads for short rows (4096 x 1000: 20 and 30 with 256) and for
-// more rows than fit the SMs twice at that size: blocks then start and end
-// more evenly (8192 x 32000: 81 and 85; 1023 x 50257: 28 and 24).
+// (measured, us with a row in one block and over a cluster: 1 x 32000 with 8
+// alternatives 7.3 and 8.1, 64 x 32000 with 20 11.4 and 12.8, 8 x 131072 10.7 and
+// 4.4, 256 x 131072 20.1 and 20.2, with 20 alternatives 32.2 and 30.3).  128
+// threads for short rows (4096 x 1000 8.1 and 12.1 with 256, with 8 alternatives
+// 23.5 and 34.5) and for more rows than fit the SMs twice at that size: blocks
+// then start and end more evenly (8192 x 32000 81 and 85; but 1023 x 50257 28 and
+// 24).
 template <typename T>
 cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
     int parts = 1;
@@ -607,8 +609,8 @@ cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
 }
 
 // Many small blocks: up to 32 an SM, of at least 4096 logits (measured, us:
-// 8192 x 32000 in 1, 2 and 8 blocks a row 164, 174, 195; 256 x 131072 in 8, 16
-// and 32 27.8, 25.7, 27.2; 512 x 32000 in 4 and 7 17.2, 14.9).
+// 8192 x 32000 in 1, 2 and 8 blocks a row 164, 173, 224; 256 x 131072 in 8, 16
+// and, by this rule, 19 27.5, 25.9, 26.9; 512 x 32000 in 4 and 7 16.5, 14.9).
 template <typename T>
 cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
     const int parts =
