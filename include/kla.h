@@ -813,12 +813,13 @@ KLA_API kla_status kla_linattn_step(
  * lse [N] fp32 or null; top_logp [N, top] fp32 and top_ids [N, top] int64
  * (null with top = 0).  A token outside 0 .. V - 1 (padding, by custom -1 or
  * -100) has logp 0.  scale (1 / temperature): finite and > 0.  -inf masks a
- * logit (its p is 0), and so does a z below the range of fp32; a row masked
- * throughout has lse and logp -inf, entropy 0, and its top ids are the lowest
+ * logit (its p is 0); a row masked throughout, or whose z are all below the
+ * range of fp32, has lse and logp -inf, entropy 0, and its top ids are the lowest
  * of the largest logits.  NaN or +inf in a row (or a z above the range) makes
  * its lse, logp and entropy NaN (NaN ranks above +inf among the top).
- * All sums in fp32, of distances from the row's largest z: logp and entropy
- * keep their digits near 0 and in rows far from 0, logp is never above 0 and
+ * All sums in fp32, of distances from the row's largest logit: logp and entropy
+ * keep their digits near 0 and in rows however far from 0 (a row that has the
+ * type's lowest value throughout is a uniform one), logp is never above 0 and
  * entropy never below; lse is never below the row's largest z.
  * The outputs may not overlap logits, tokens or each other.
  * Errors: KLA_ERR_INVALID_ARG (N < 0, V < 1, top < 0 or > V, a negative

@@ -1,14 +1,16 @@
 // Log probabilities of given tokens, with entropy and the largest
 // alternatives, and their gradient.
 //
-// Forward, one pass over a row with a running maximum m (z = scale x):
-//   s = sum exp(z - m),  t = sum exp(z - m) (z - m)
-//   lse = m + log s,     entropy = log s - t / s,    logp = (z - m) - log s
+// Forward, one pass over a row x with its running maximum m, in powers of two:
+//   e = scale log2(e) (x - m),  s = sum 2^e,  t = sum 2^e e
+//   lse = scale m + log s,      entropy = log s - t log(2) / s,
+//   logp = scale (x - m) - log s
 // (with m the maximum both terms of the entropy are of one sign and nothing
 // cancels: relative to a number up to 40 below it, entropies under 1 came out
-// up to 1e-5 off and below 0),
-// and where two partial results meet, with m' = max(m1, m2), c = exp(m - m'):
-//   s' = sum c s,        t' = sum c (t + s (m - m')).
+// up to 1e-5 off and below 0; and a difference of logits has the digits that
+// one of scaled logits has lost where rows are far from 0),
+// and where two partial results meet, with m' = max(m1, m2) and e of m - m':
+//   s' = sum 2^e s,             t' = sum 2^e (t + s e).
 // A row is read once; it belongs to one block, or, when there are few long
 // rows, to a cluster of up to 8 that join their sums on chip.  Bound by HBM
 // where there are many rows (8192 x 32000 bf16: 80 us, 0.96 of it; gradient 165
@@ -35,7 +37,7 @@ namespace cg = cooperative_groups;
 using bf16 = __nv_bfloat16;
 using u64 = unsigned long long;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kCand = 1024;      // candidates a block can hold
 constexpr int kMaxParts = 8;     // blocks of a cluster
 static_assert(kMaxParts * kLogprobMaxTop <= kCand, "room for all parts");
@@ -74,45 +76,44 @@ __device__ __forceinline__ float ex2(float x) {
 struct Sums {
     float m, s, t;
 };
-// -200 in place of a distance far below the maximum: exp of both is 0, and
-// 0 * -200 is no NaN where 0 * -inf is.
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+// -300 in place of an e far below: 2^e of both is 0, and 0 * -300 is no NaN
+// where 0 * -inf is.  (k: scale log2(e))
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float k) {
     const float m = max_nan(a.m, b.m);
     if (m == -INFINITY) return a;
-    const float da = max_nan(a.m - m, -200.f), db = max_nan(b.m - m, -200.f);
-    const float ca = ex2(da * kLog2e), cb = ex2(db * kLog2e);
+    const float ea = max_nan((a.m - m) * k, -300.f);
+    const float eb = max_nan((b.m - m) * k, -300.f);
+    const float ca = ex2(ea), cb = ex2(eb);
     return {m, ca * a.s + cb * b.s,
-            ca * fmaf(a.s, da, a.t) + cb * fmaf(b.s, db, b.t)};
+            ca * fmaf(a.s, ea, a.t) + cb * fmaf(b.s, eb, b.t)};
 }
 
 // Moves the sums to logits of which `top` is the largest, if it is the largest
-// so far.  m is rounded up: no scaled logit is above it, so that all terms of t
-// have one sign and the entropy keeps its digits however small it is.
-__device__ __forceinline__ void refer(Sums& a, float top, float scale) {
-    const float m = __fmul_ru(top, scale);
-    if (m <= a.m) return;                              // (NaN goes on)
-    const float to = max_nan(a.m, m);
-    const float d = max_nan(a.m - to, -200.f), c = ex2(d * kLog2e);
-    a.t = c * fmaf(a.s, d, a.t);
+// so far.
+__device__ __forceinline__ void refer(Sums& a, float top, float k) {
+    if (top <= a.m) return;                            // (NaN goes on)
+    const float m = max_nan(a.m, top);
+    const float e = max_nan((a.m - m) * k, -300.f), c = ex2(e);
+    a.t = c * fmaf(a.s, e, a.t);
     a.s *= c;
-    a.m = to;
+    a.m = m;
 }
 // N logits into a thread's sums.
 template <int N>
-__device__ __forceinline__ void add(Sums& a, const float (&v)[N],
-                                    float scale) {
+__device__ __forceinline__ void add(Sums& a, const float (&v)[N], float k) {
     if (a.m == -INFINITY) return;                      // all masked so far
     float2 s = both(0.f), t = both(0.f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        float2 d = fma2(make_float2(v[i], i + 1 < N ? v[i + 1] : -INFINITY),
-                        both(scale), both(-a.m));
-        d.x = max_nan(d.x, -200.f);
-        d.y = max_nan(d.y, -200.f);
-        const float2 e = mul2(d, both(kLog2e));
+        const float2 d =
+            add2(make_float2(v[i], i + 1 < N ? v[i + 1] : -INFINITY),
+                 both(-a.m));
+        float2 e = mul2(d, both(k));
+        e.x = max_nan(e.x, -300.f);
+        e.y = max_nan(e.y, -300.f);
         const float2 p = make_float2(ex2(e.x), ex2(e.y));
         s = add2(s, p);
-        t = fma2(p, d, t);
+        t = fma2(p, e, t);
     }
     a.s += s.x + s.y;
     a.t += t.x + t.y;
@@ -389,27 +390,23 @@ logprob_fwd(LogprobArgs a, int parts) {
     const Range r = range_of(x, begin, min(a.V, begin + len));
     await_grid_before();
     release_grid_after();
+    const float k = fminf(a.scale * kLog2e, 3.4e38f);  // (0 k is no NaN)
     Sums acc{-INFINITY, 0.f, 0.f};
-    float own = -INFINITY;
     for_each<T, NT>(
         x, r,
-        [&](const auto& v) {
-            const float m = Vec<T>::largest(v);
-            refer(acc, m, a.scale);
-            if (TOP) own = max_nan(own, m);
-        },
-        [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, a.scale); },
+        [&](const auto& v) { refer(acc, Vec<T>::largest(v), k); },
+        [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, k); },
         [&](int, float v) {
             const float one[1] = {v};
-            refer(acc, v, a.scale);
-            add(acc, one, a.scale);
-            if (TOP) own = max_nan(own, v);
+            refer(acc, v, k);
+            add(acc, one, k);
         });
+    const float own = acc.m;     // the largest of this thread's
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
                              __shfl_xor_sync(~0u, acc.s, o),
-                             __shfl_xor_sync(~0u, acc.t, o)});
+                             __shfl_xor_sync(~0u, acc.t, o)}, k);
     if (lane == 0) sh.part[warp] = acc;
     __syncthreads();
     if (warp == 0) {
@@ -418,7 +415,7 @@ logprob_fwd(LogprobArgs a, int parts) {
         for (int o = NT / 64; o; o >>= 1)
             acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
                                  __shfl_xor_sync(~0u, acc.s, o),
-                                 __shfl_xor_sync(~0u, acc.t, o)});
+                                 __shfl_xor_sync(~0u, acc.t, o)}, k);
         if (lane == 0) sh.whole = acc;
     }
     if (TOP) largest<T, NT>(sh, x, r, a.top, order_of(own));
@@ -437,7 +434,7 @@ logprob_fwd(LogprobArgs a, int parts) {
                 for (int o = kMaxParts / 2; o; o >>= 1)
                     all = join(all, Sums{__shfl_xor_sync(~0u, all.m, o),
                                          __shfl_xor_sync(~0u, all.s, o),
-                                         __shfl_xor_sync(~0u, all.t, o)});
+                                         __shfl_xor_sync(~0u, all.t, o)}, k);
                 if (lane == 0) sh.part[0] = all;
             }
             if (TOP) {
@@ -448,18 +445,17 @@ logprob_fwd(LogprobArgs a, int parts) {
             __syncthreads();
         }
         const Sums all = parts > 1 ? sh.part[0] : sh.whole;
-        // (of a row whose scaled logits are all out of range downwards m is
-        // the lowest number and s is 0)
-        const bool none = all.s == 0.f;
-        const float ls = logf(all.s);
-        // Where m was rounded up s may be below 1: the true lse is not below
-        // the largest logit for all that.
-        const float lse = none ? -INFINITY : all.m + max_nan(ls, 0.f);
-        // from m and log s apart: their sum would lose the digits of rows far
-        // from 0; no log probability is above 0
+        // the largest z; below the range of fp32 it is masked, above it NaN
+        const float top = a.scale * all.m;
+        const bool none = top == -INFINITY;
+        const float ls =
+            top == INFINITY ? __uint_as_float(0x7fc00000u) : logf(all.s);
+        // not below the largest z, whatever is rounded
+        const float lse = none ? -INFINITY
+                               : max_nan(fmaf(a.scale, all.m, ls),
+                                         __fmul_ru(a.scale, all.m));
         auto logp = [&](float v) {
-            const float lp = fmaf(v, a.scale, -all.m) - ls;
-            return none ? -INFINITY : lp > 0.f ? 0.f : lp;      // (NaN stays)
+            return none ? -INFINITY : fmaf(v - all.m, a.scale, -ls);
         };
         if (tid == 0) {
             const long long t = a.tokens[row];
@@ -467,8 +463,8 @@ logprob_fwd(LogprobArgs a, int parts) {
             if (t >= 0 && t < a.V)
                 lp = logp(to_f32(x[t]));
             a.logp[row] = lp;
-            const float ent = ls - all.t / all.s;
-            if (a.entropy) a.entropy[row] = none || ent < 0.f ? 0.f : ent;
+            if (a.entropy)
+                a.entropy[row] = none ? 0.f : fmaf(-kLn2, all.t / all.s, ls);
             if (a.lse) a.lse[row] = lse;
         }
         if (TOP) {

@@ -380,3 +380,88 @@ def test_nan_at_the_first_id(V, dtype):
     assert [r.tolist() for r in ids] == [first, first, first,
                                          [V - 1] + first[:5], first]
     assert torch.isnan(tlp[:4]).all() and torch.isfinite(tlp[4]).all()
+
+
+def far_rows(V, dtype, seed=0):
+    """Rows far from 0: some neighbouring numbers of the type each, from one to
+    the next the same step; the last ones all of the type's lowest value."""
+    gen = torch.Generator().manual_seed(seed + V)
+    bits = 23 if dtype == F32 else 7
+    at, rows = [300.0, -900.0, 5000.0, -70000.0, 3e9, -2e20, -1e38], []
+    for x in at:
+        step = 2.0 ** (math.floor(math.log2(abs(x))) - bits)
+        base = round(x / step) * step
+        n = max(1.0, round(0.5 / step)) if step < 1 else 1.0
+        j = torch.randint(-8, 9, (V,), generator=gen).double()
+        rows.append(base + step * n * j)
+    low = torch.full((2, V), torch.finfo(dtype).min, dtype=torch.float64)
+    x = torch.cat([torch.stack(rows), low])
+    out = x.to(dtype)
+    assert torch.equal(out.double(), x)
+    return out.cuda(), torch.randint(0, V, (len(x),), generator=gen).cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1, 2, 700, 5003, 40000])
+@pytest.mark.parametrize("scale", [1.0, 0.6, 0.9])
+def test_rows_far_from_zero(V, scale, dtype):
+    x, t = far_rows(V, dtype)
+    top = min(V, 5)
+    logp, ent, lse, tlp, ids = kla.logprob_fwd(x, t, top, scale)
+    # 64 bits hold the differences from the largest logit
+    scale32 = float(np.float32(scale))
+    x64 = mixer.f64(x)
+    m = x64.max(1, keepdims=True)
+    z = scale32 * (x64 - m)
+    ls = np.log(np.exp(z).sum(1, keepdims=True))
+    p = np.exp(z - ls)
+    n = np.arange(len(x64))
+    want = (z - ls)[n, t.cpu().numpy()]
+    H = ls[:, 0] - (p * z).sum(1)
+    # 32 roundings of a sum's own (see above); each e is off by three half
+    # steps (of the difference, the factor and the product), which moves ls by
+    # the mean of |z|, and the entropy by that of z^2, of as many
+    far = 32 * U32 + 3 * U32 * ((p * np.abs(z)).sum(1) + (p * z * z).sum(1))
+    assert (np.abs(mixer.f64(logp) - want) <= far + 4 * U32 * np.abs(want)
+            ).all()
+    assert (np.abs(mixer.f64(ent) - H) <= far + 4 * U32 * H).all()
+    l64 = scale32 * m[:, 0] + ls[:, 0]
+    assert (np.abs(mixer.f64(lse) - l64) <= far + 2 * U32 * np.abs(l64)).all()
+    assert (mixer.f64(lse) >= scale32 * m[:, 0]).all()
+    order = np.argsort(-x64, axis=1, kind="stable")[:, :top]
+    assert (ids.cpu().numpy() == order).all()
+    want = np.take_along_axis(z - ls, order, 1)
+    assert (np.abs(mixer.f64(tlp) - want) <= far[:, None] +
+            4 * U32 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.3])
+def test_a_shift_of_all_logits_at_other_scales(scale):
+    gen = torch.Generator().manual_seed(5)
+    x = (torch.randn(5, 9000, generator=gen) * 4096).round().div(1024).cuda()
+    x[1, ::2] = -math.inf
+    t = torch.randint(0, 9000, (5,), generator=gen).cuda()
+    a, b = kla.logprob_fwd(x, t, 6, scale), kla.logprob_fwd(x + 4096, t, 6,
+                                                            scale)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(a[i], b[i])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_extreme_scales(dtype):
+    x = torch.full((3, 900), -1.0, dtype=dtype, device="cuda")
+    x[0, 300:302] = -0.5                  # two of the same
+    x[1, 500:] = -math.inf                # 500 of the same
+    x[2, 7] = -0.5
+    t = torch.full((3,), 300, dtype=torch.int64, device="cuda")
+    logp, ent, lse, tlp, ids = kla.logprob_fwd(x, t, 2, 3e38)
+    ln2, ln500 = math.log(2), math.log(500)
+    assert (ent.cpu() - torch.tensor([ln2, ln500, 0.0])).abs().max() <= 1e-6
+    assert (logp[:2].cpu() + torch.tensor([ln2, ln500])).abs().max() <= 1e-6
+    assert logp[2] == torch.tensor(-0.5 * 3e38) and lse[2] == logp[2]
+    assert ids.tolist() == [[300, 301], [0, 1], [7, 0]]
+    logp, ent, lse, tlp, ids = kla.logprob_fwd(x, t, 2, 1e-38)
+    ln = torch.tensor([900.0, 500.0, 900.0]).log()
+    for got in (ent, -logp, lse, -tlp[:, 0], -tlp[:, 1]):
+        # (a sum of 900 equal terms, and the roundings above)
+        assert (got.cpu() - ln).abs().max() <= (32 + 8 * 7) * U32
