@@ -814,8 +814,8 @@ KLA_API kla_status kla_linattn_step(
  * (null with top = 0).  A token outside 0 .. V - 1 (padding, by custom -1 or
  * -100) has logp 0.  scale (1 / temperature): finite and > 0.  -inf masks a
  * logit (its p is 0); a row masked throughout, or whose z are all below the
- * range of fp32, has lse and logp -inf, entropy 0, and its top ids are the lowest
- * of the largest logits.  NaN or +inf in a row (or a z above the range) makes
+ * range of fp32, has lse and logp -inf and entropy 0 (and top ids like any row:
+ * masked throughout 0, 1, ...).  NaN or +inf in a row (or a z above the range) makes
  * its lse, logp and entropy NaN (NaN ranks above +inf among the top).
  * All sums in fp32, of distances from the row's largest logit: logp and entropy
  * keep their digits near 0 and in rows however far from 0 (a row that has the
@@ -844,7 +844,9 @@ KLA_API kla_status kla_logprob_fwd(
  *     logits_grad_j = scale dL/dz_j
  *
  * p_j is exp(z_j - lse): what lse was rounded by, up to 2^-24 |lse|, is a
- * relative error of p_j.
+ * relative error of p_j.  From |lse| = 1024 on it is not: a lse that the logits
+ * given round to is formed again from them.  (One that they do not, such as that
+ * of a whole vocabulary with a part of it, is taken as given.)
  * A row without a token (outside 0 .. V - 1) has no logp term; a row masked
  * throughout has gradient 0.  logits_grad [N, V] contiguous, of type `dtype`;
  * it may be logits itself (same address, logits_stride = V), else it may not

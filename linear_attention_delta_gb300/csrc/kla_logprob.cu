@@ -13,8 +13,8 @@
 //   s' = sum 2^e s,             t' = sum 2^e (t + s e).
 // A row is read once; it belongs to one block, or, when there are few long
 // rows, to a cluster of up to 8 that join their sums on chip.  Bound by HBM
-// where there are many rows (8192 x 32000 bf16: 80 us, 0.96 of it; gradient 165
-// us, 0.94); few rows are bound by the launch and its ramp (256 x 131072: 20 us,
+// where there are many rows (8192 x 32000 bf16: 82 us, 0.94 of it; gradient 166
+// us, 0.93); few rows are bound by the launch and its ramp (256 x 131072: 20 us,
 // of which the bytes take 10).
 //
 // The largest: each thread keeps its own maximum.  The top-th largest of the
@@ -97,6 +97,16 @@ __device__ __forceinline__ void refer(Sums& a, float top, float k) {
     a.t = c * fmaf(a.s, e, a.t);
     a.s *= c;
     a.m = m;
+}
+// The sums of LANES adjacent lanes.
+template <int LANES>
+__device__ __forceinline__ Sums join_lanes(Sums a, float k) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1)
+        a = join(a, Sums{__shfl_xor_sync(~0u, a.m, o),
+                         __shfl_xor_sync(~0u, a.s, o),
+                         __shfl_xor_sync(~0u, a.t, o)}, k);
+    return a;
 }
 // N logits into a thread's sums.
 template <int N>
@@ -236,6 +246,28 @@ __device__ __forceinline__ void for_each(const T* x, const Range& r, R ready,
 struct Nothing {
     template <typename V> __device__ void operator()(const V&) const {}
 };
+
+// This thread's sums over its share of a range.
+template <typename T, int NT>
+__device__ __forceinline__ Sums sums_of(const T* x, const Range& r, float k) {
+    Sums acc{-INFINITY, 0.f, 0.f};
+    for_each<T, NT>(
+        x, r, [&](const auto& v) { refer(acc, Vec<T>::largest(v), k); },
+        [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, k); },
+        [&](int, float v) {
+            const float one[1] = {v};
+            refer(acc, v, k);
+            add(acc, one, k);
+        });
+    return acc;
+}
+__device__ __forceinline__ float in_twos(float scale) {
+    return fminf(scale * kLog2e, 3.4e38f);      // (0 times it is no NaN)
+}
+// scale m + ls, not below scale m whatever is rounded.
+__device__ __forceinline__ float lse_of(float scale, float m, float ls) {
+    return max_nan(fmaf(scale, m, ls), __fmul_ru(scale, m));
+}
 
 template <int NT>
 __device__ __forceinline__ u64 block_max(u64 k, u64* keys) {
@@ -390,32 +422,15 @@ logprob_fwd(LogprobArgs a, int parts) {
     const Range r = range_of(x, begin, min(a.V, begin + len));
     await_grid_before();
     release_grid_after();
-    const float k = fminf(a.scale * kLog2e, 3.4e38f);  // (0 k is no NaN)
-    Sums acc{-INFINITY, 0.f, 0.f};
-    for_each<T, NT>(
-        x, r,
-        [&](const auto& v) { refer(acc, Vec<T>::largest(v), k); },
-        [&](int, const float (&v)[Vec<T>::N]) { add(acc, v, k); },
-        [&](int, float v) {
-            const float one[1] = {v};
-            refer(acc, v, k);
-            add(acc, one, k);
-        });
+    const float k = in_twos(a.scale);
+    Sums acc = sums_of<T, NT>(x, r, k);
     const float own = acc.m;     // the largest of this thread's
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
-                             __shfl_xor_sync(~0u, acc.s, o),
-                             __shfl_xor_sync(~0u, acc.t, o)}, k);
+    acc = join_lanes<32>(acc, k);
     if (lane == 0) sh.part[warp] = acc;
     __syncthreads();
     if (warp == 0) {
         acc = lane < NT / 32 ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int o = NT / 64; o; o >>= 1)
-            acc = join(acc, Sums{__shfl_xor_sync(~0u, acc.m, o),
-                                 __shfl_xor_sync(~0u, acc.s, o),
-                                 __shfl_xor_sync(~0u, acc.t, o)}, k);
+        acc = join_lanes<NT / 32>(acc, k);
         if (lane == 0) sh.whole = acc;
     }
     if (TOP) largest<T, NT>(sh, x, r, a.top, order_of(own));
@@ -430,11 +445,7 @@ logprob_fwd(LogprobArgs a, int parts) {
                 Sums all{-INFINITY, 0.f, 0.f};
                 if (lane < parts)
                     all = *cg::this_cluster().map_shared_rank(&sh.whole, lane);
-#pragma unroll
-                for (int o = kMaxParts / 2; o; o >>= 1)
-                    all = join(all, Sums{__shfl_xor_sync(~0u, all.m, o),
-                                         __shfl_xor_sync(~0u, all.s, o),
-                                         __shfl_xor_sync(~0u, all.t, o)}, k);
+                all = join_lanes<kMaxParts>(all, k);
                 if (lane == 0) sh.part[0] = all;
             }
             if (TOP) {
@@ -450,10 +461,7 @@ logprob_fwd(LogprobArgs a, int parts) {
         const bool none = top == -INFINITY;
         const float ls =
             top == INFINITY ? __uint_as_float(0x7fc00000u) : logf(all.s);
-        // not below the largest z, whatever is rounded
-        const float lse = none ? -INFINITY
-                               : max_nan(fmaf(a.scale, all.m, ls),
-                                         __fmul_ru(a.scale, all.m));
+        const float lse = none ? -INFINITY : lse_of(a.scale, all.m, ls);
         auto logp = [&](float v) {
             return none ? -INFINITY : fmaf(v - all.m, a.scale, -ls);
         };
@@ -491,20 +499,47 @@ logprob_fwd(LogprobArgs a, int parts) {
 // ---------------------------------------------------------------- gradient
 
 // d_j = -p_j (g + ge (log p_j + H)), + g at the token, times scale.
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
-                                                  int parts) {
+//
+// log p_j = z_j - lse has lost what lse was rounded by, 2^-24 |lse| at most and
+// the same relative to p (in a row of the type's lowest value p would be 1
+// throughout).  From |lse| = 1024 on (2^-14) m and log s are formed again, and
+// take the place of lse where they round to it; of part of a vocabulary with the
+// whole's lse they do not, and lse is taken as it is.  Each block of such a row
+// reads all of it, or, in place, the first one has it to itself (us if all rows
+// are such: 8192 x 32000 bf16 246 for 166, 256 x 131072 160 for 27).  In 32
+// registers: unbound it takes 40 and 45, and other rows 186 us for 166.
+constexpr float kFar = 1024.f;
+template <typename T, int NT, bool IN_PLACE>
+__global__ void __launch_bounds__(NT, 2048 / NT)
+logprob_bwd(LogprobBwdArgs a, int parts) {
     constexpr int N = Vec<T>::N;
     const size_t row = blockIdx.x / parts;
     const int part = blockIdx.x % parts;
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
     T* y = static_cast<T*>(a.logits_grad) + row * a.V;
     const int len = (a.V + parts - 1) / parts;
-    const int begin = (int)min((long long)a.V, (long long)part * len);
-    const int end = min(a.V, begin + len);
+    int begin = (int)min((long long)a.V, (long long)part * len);
+    int end = min(a.V, begin + len);
     await_grid_before();
     release_grid_after();
     const float lse = a.lse[row];
+    float x0 = 0.f, z0 = lse;    // log p = scale (x - x0) - z0
+    if (fabsf(lse) >= kFar && fabsf(lse) < INFINITY) {
+        if (IN_PLACE) {
+            if (part > 0) return;
+            begin = 0, end = a.V;
+        }
+        __shared__ Sums of_warp[NT / 32];
+        const float k = in_twos(a.scale);
+        Sums all = join_lanes<32>(sums_of<T, NT>(x, range_of(x, 0, a.V), k), k);
+        if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = all;
+        __syncthreads();
+        all = of_warp[0];
+        for (int w = 1; w < NT / 32; ++w) all = join(all, of_warp[w], k);
+        const float ls = logf(all.s);
+        if (fabsf(lse_of(a.scale, all.m, ls) - lse) <= 0x1p-22f * fabsf(lse))
+            x0 = all.m, z0 = ls;
+    }
     const long long t = a.tokens[row];
     const bool some = t >= 0 && t < a.V && lse != -INFINITY;
     const float g = a.logp_grad && some ? a.logp_grad[row] : 0.f;
@@ -515,7 +550,7 @@ __global__ void __launch_bounds__(NT) logprob_bwd(LogprobBwdArgs a,
     auto grad = [&](int id, float v) {
         const float lp = lse == -INFINITY
                              ? -200.f
-                             : max_nan(fmaf(v, a.scale, -lse), -200.f);
+                             : max_nan(fmaf(v - x0, a.scale, -z0), -200.f);
         const float p = expf(lp);
         float d = -p * fmaf(ge, lp + H, g);
         if (id == at) d += g;
@@ -605,13 +640,15 @@ cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t s) {
 }
 
 // Many small blocks: up to 32 an SM, of at least 4096 logits (measured, us:
-// 8192 x 32000 in 1, 2 and 8 blocks a row 164, 173, 224; 256 x 131072 in 8, 16
+// 8192 x 32000 in 1, 2 and 8 blocks a row 166, 173, 224; 256 x 131072 in 8, 16
 // and, by this rule, 19 27.5, 25.9, 26.9; 512 x 32000 in 4 and 7 16.5, 14.9).
 template <typename T>
 cudaError_t launch_bwd(const LogprobBwdArgs& a, cudaStream_t s) {
     const int parts =
         std::max(1, std::min({32 * kPlanSMs / a.N, a.V / 4096, 64}));
-    return launch_rows(logprob_bwd<T, 128>, a.N, parts, 128, false, s, a);
+    return launch_rows(a.logits == a.logits_grad ? logprob_bwd<T, 128, true>
+                                                 : logprob_bwd<T, 128, false>,
+                       a.N, parts, 128, false, s, a);
 }
 
 }  // namespace

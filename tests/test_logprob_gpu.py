@@ -465,3 +465,60 @@ def test_extreme_scales(dtype):
     for got in (ent, -logp, lse, -tlp[:, 0], -tlp[:, 1]):
         # (a sum of 900 equal terms, and the roundings above)
         assert (got.cpu() - ln).abs().max() <= (32 + 8 * 7) * U32
+
+
+def exact_gradient(x, t, g, ge, scale32):
+    """(gradient, p, z, log p, H, mean |z|, mean z^2) in 64 bits, from
+    differences of logits; z: scaled distances from the largest."""
+    x64 = mixer.f64(x)
+    z = scale32 * (x64 - x64.max(1, keepdims=True))
+    lp = z - np.log(np.exp(z).sum(1, keepdims=True))
+    p = np.exp(lp)
+    H = -(p * lp).sum(1, keepdims=True)
+    g, ge = (mixer.f64(a)[:, None] for a in (g, ge))
+    d = -p * (g + ge * (lp + H))
+    n = np.arange(len(x64))
+    d[n, t.cpu().numpy()] += g[:, 0]
+    mean = [(p * y).sum(1, keepdims=True) for y in (np.abs(z), z * z)]
+    return scale32 * d, p, z, lp, H, *mean
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1, 2, 700, 5003, 40000])
+@pytest.mark.parametrize("scale", [1.0, 0.6])
+def test_gradient_of_rows_far_from_zero(V, scale, dtype):
+    x, t = far_rows(V, dtype)
+    gen = torch.Generator().manual_seed(3)
+    g, ge = (torch.randn(len(x), generator=gen).cuda() for _ in range(2))
+    _, ent, lse, _, _ = kla.logprob_fwd(x, t, scale=scale)
+    got = kla.logprob_bwd(x, t, lse, ent, g, ge, scale)
+    scale32 = float(np.float32(scale))
+    want, p, z, lp, H, d1, d2 = exact_gradient(x, t, g, ge, scale32)
+    # log p: three half steps of z, those of log s (as in the forward), and,
+    # where it is small enough to be used, of lse; then exp and the products
+    small = np.abs(mixer.f64(lse))[:, None]
+    small = np.where(small < 1024, small, 0)
+    e = 3 * U32 * np.abs(z) + (32 + 3 * d1 + 3 * d2 + small) * U32
+    gm, gem = (np.abs(mixer.f64(a))[:, None] for a in (g, ge))
+    bound = scale32 * (p * (gm + gem * (np.abs(lp) + H)) * (e + 8 * U32) +
+                       gem * p * (2 * e + 4 * U32 * (np.abs(lp) + H)) +
+                       4 * U32 * gm * (p > 0)) + 1e-37
+    if dtype == BF16:
+        bound = bound + U16 * (np.abs(want) + bound)
+    off = np.abs(mixer.f64(got) - want)
+    assert (off <= bound + 4 * U32 * np.abs(want)).all()
+    y = x.clone()
+    kla.logprob_bwd(y, t, lse, ent, g, ge, scale, out=y)
+    assert torch.equal(y, got)
+
+
+def test_gradient_of_part_of_a_vocabulary():
+    """The whole's lse with a part's logits, far from 0: taken as given."""
+    gen = torch.Generator().manual_seed(8)
+    x = (torch.randn(6, 9000, generator=gen) * 2 + 5000).cuda()
+    t = torch.randint(0, 4000, (6,), generator=gen).cuda()
+    _, ent, lse, _, _ = kla.logprob_fwd(x, t)
+    g = torch.ones(6, device="cuda")
+    part = x[:, :4000]
+    check_bwd(part, t, lse, ent, g, g,
+              kla.logprob_bwd(part, t, lse, ent, g, g))
